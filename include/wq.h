@@ -373,6 +373,189 @@ int wq_stream_read(const void* src, size_t bytes, void* sink, size_t sink_words,
 int wq_mfma_rate(const void* operands, int iters, float* sink, size_t sink_floats,
                  double* flops_out, void* stream);
 
+/* ---- the decode step around the quantized products -------------------------------------
+ *
+ * RMS norm with the residual add, rotary positions with the paged cache write, attention of
+ * one new token over that cache, and the mixture-of-experts layer of a few tokens.  The
+ * conventions above hold: calls enqueue on `stream` and never allocate, free or synchronize
+ * (all four may be captured into a graph), validation precedes any launch, and flags select
+ * the element type (fp16, or bf16 with WQ_FLAG_BF16).  abi_version, struct_size and a zero
+ * `reserved` are checked as in the other structs.  Strides count elements.
+ */
+
+typedef struct wq_norm_args {
+  uint32_t abi_version;     /* WQ_ABI_VERSION                                          */
+  uint32_t struct_size;     /* sizeof(wq_norm_args)                                    */
+  const void* x;            /* device fp16 (bf16) [rows][ldx], 16-byte aligned rows      */
+  const void* delta;        /* device [rows][ldd], added to x, or NULL                   */
+  const void* weight;       /* device [n], 16-byte aligned                              */
+  void* sum_out;            /* device [rows][lds]: x + delta rounded once, or NULL; needs
+                               delta.  May be x or delta itself (same row stride)       */
+  void* y;                  /* device [rows][ldy]; may be x or delta itself (same row
+                               stride), but not sum_out                                 */
+  void* stream;
+  int32_t rows, n;          /* rows >= 1; n a multiple of 8, at most 65536               */
+  int32_t ldx, ldd, lds, ldy; /* row strides, >= n, multiples of 8 (ldd, lds: 0 if unused) */
+  float eps;                /* >= 0                                                    */
+  uint32_t flags;           /* 0 or WQ_FLAG_BF16                                       */
+  int32_t reserved;
+} wq_norm_args;
+
+/*
+ * RMS norm with the residual add: s = x + delta (x alone without delta), and for each row
+ * y = s / sqrt(mean(s^2) + eps) * weight.  The sum stays in fp32 for the norm: y and
+ * sum_out are each rounded once.
+ */
+int wq_add_rms_norm(const wq_norm_args* args);
+
+/* A paged KV cache: position j of a sequence lies in slot j % page_size of the page its
+ * block table names at j / page_size.  K and V have the same shape and strides: element
+ * (page, slot, head, i) at page*page_stride + slot*slot_stride + head*head_stride + i, so
+ * head-major and slot-major pages are both taken.  Elements are fp16 (bf16 with
+ * WQ_FLAG_BF16), or E4M3 with WQ_FLAG_FP8: the stored value is then value / scale of its KV
+ * head, rounded to nearest even and clamped to +-448 (NaN stays NaN). */
+typedef struct wq_kv_cache {
+  void* k;                  /* device, 16-byte aligned (E4M3: 8-byte)                    */
+  void* v;
+  const float* k_scale;     /* device fp32 [kv_heads] (E4M3 only), or NULL: 1            */
+  const float* v_scale;
+  int64_t page_stride, slot_stride, head_stride; /* multiples of 8, >= 0                 */
+  int32_t num_pages, page_size;                  /* each >= 1                            */
+  int32_t kv_heads, head_dim; /* head_dim a multiple of 8, 16 to 256                     */
+} wq_kv_cache;
+
+#define WQ_MAX_ROPE_AXES 4
+typedef struct wq_rope_args {
+  uint32_t abi_version;     /* WQ_ABI_VERSION                                          */
+  uint32_t struct_size;     /* sizeof(wq_rope_args)                                    */
+  wq_kv_cache cache;
+  const void* q;            /* device [tokens][ldq], heads contiguous in a row; may be NULL
+                               with q_heads 0                                          */
+  const void* k;            /* device [tokens][ldk]                                     */
+  const void* v;            /* device [tokens][ldv]                                     */
+  void* q_out;              /* device [tokens][ldqo], the rotated q; may be q itself (same
+                               row stride)                                             */
+  const int64_t* slots;     /* device [tokens]: page * page_size + slot of each token; a
+                               value outside the cache (-1: padding) writes nothing     */
+  const int32_t* positions; /* device [axes][tokens]; NULL with rot_dim 0                */
+  const float* inv_freq;    /* device fp32 [rot_dim / 2]; NULL with rot_dim 0            */
+  void* stream;
+  int32_t tokens, q_heads;
+  int32_t ldq, ldk, ldv, ldqo; /* row strides, multiples of 8                            */
+  int32_t rot_dim;          /* rotated leading elements of a head: a multiple of 8, 0 to
+                               head_dim                                                */
+  int32_t axes;             /* 1 to WQ_MAX_ROPE_AXES                                    */
+  int32_t sections[WQ_MAX_ROPE_AXES]; /* frequency pairs of each axis, in order; their sum
+                               is rot_dim / 2 (ignored past `axes`)                     */
+  int32_t interleaved;      /* pair (2i, 2i+1) of a head, else (i, i + rot_dim/2)         */
+  uint32_t flags;           /* WQ_FLAG_BF16: q, k, v; WQ_FLAG_FP8: an E4M3 cache         */
+  int32_t reserved;
+} wq_rope_args;
+
+/*
+ * Rotary positions and the cache write of new tokens: pair i of every q and k head turns by
+ * positions[axis(i)][token] * inv_freq[i] (the angle formed and reduced in fp64, so far
+ * positions keep their phase), q goes to q_out, k and v to their cache slots, each rounded
+ * once.  Tokens of one call must name distinct slots.
+ */
+int wq_rope_append(const wq_rope_args* args);
+
+typedef struct wq_attn_args {
+  uint32_t abi_version;     /* WQ_ABI_VERSION                                          */
+  uint32_t struct_size;     /* sizeof(wq_attn_args)                                    */
+  wq_kv_cache cache;
+  const void* q;            /* device [batch][ldq], q_heads x head_dim contiguous         */
+  void* out;                /* device [batch][ldo], as q                                */
+  float* lse;               /* device fp32 [batch][q_heads], or NULL                    */
+  const int32_t* block_table; /* device [batch][table_stride] page numbers              */
+  const int32_t* lens;      /* device [batch]: positions of each sequence, taken into
+                               0..max_len                                             */
+  const uint8_t* keep;      /* device [batch][keep_stride], 0 = position left out; or NULL */
+  void* workspace;          /* device, 16-byte aligned; wq_paged_attention_workspace_bytes */
+  size_t workspace_bytes;
+  void* stream;
+  int32_t batch, q_heads;   /* q_heads a multiple of cache.kv_heads: query head h reads KV
+                               head h / (q_heads / kv_heads)                           */
+  int32_t max_len;          /* 1 to 2^30; at most table_stride * page_size               */
+  int32_t table_stride, keep_stride;
+  int32_t ldq, ldo;         /* row strides, multiples of 8, >= q_heads * head_dim         */
+  float scale;              /* of the scores                                           */
+  float softcap;            /* c > 0: scores become c * tanh(score / c); 0: none         */
+  int32_t window;           /* w > 0: only the last w positions; 0: all                  */
+  uint32_t flags;           /* WQ_FLAG_BF16: q and out; WQ_FLAG_FP8: an E4M3 cache       */
+  int32_t reserved;
+} wq_attn_args;
+
+/* Workspace bytes of wq_paged_attention (0 when one work-group covers every sequence).
+ * Contents need no initialization; calls that share one must not run concurrently. */
+int wq_paged_attention_workspace_bytes(int batch, int q_heads, int kv_heads, int head_dim,
+                                       int max_len, int window, size_t* bytes_out);
+
+/*
+ * Attention of one new token per sequence over the paged cache: out = sum_j p_j v_j with p
+ * the softmax over the sequence's live positions j (j < len, inside the window, kept, and on
+ * a page number inside the cache: other entries are never followed) of scale * q . k_j.
+ * Statistics and sums are fp32.  A sequence without live positions gives 0, and lse -inf
+ * (lse: log of the sum of exp of the scores).  Values outside the live positions are never
+ * used, NaN and infinities among them.  Splits of a long sequence are joined in order, so
+ * results do not depend on scheduling.
+ */
+int wq_paged_attention(const wq_attn_args* args);
+
+typedef struct wq_expert_bank {
+  const void* b;            /* expert e's library-layout weights at b + e*b_stride_bytes */
+  const void* s;            /* scales, likewise                                        */
+  const void* zp;           /* zero points, or NULL (u4b8, E4M3)                         */
+  size_t b_stride_bytes, s_stride_bytes, zp_stride_bytes; /* multiples of 16             */
+  int32_t group_size;
+  int32_t reserved;
+} wq_expert_bank;
+
+#define WQ_MOE_MAX_TOKENS 16
+#define WQ_MOE_MAX_EXPERTS 256
+#define WQ_MOE_MAX_TOPK 16
+typedef struct wq_moe_args {
+  uint32_t abi_version;     /* WQ_ABI_VERSION                                          */
+  uint32_t struct_size;     /* sizeof(wq_moe_args)                                     */
+  const void* x;            /* device fp16 (bf16) [tokens][ldx]                         */
+  const void* router;       /* device fp16 (bf16) [n_expert][hidden], 16-byte aligned     */
+  wq_expert_bank gate_up;   /* k = hidden, n = 2 * inter, gate and up paired by
+                               wq_interleave_gate_up before the repack                  */
+  wq_expert_bank down;      /* k = inter, n = hidden                                    */
+  const void* residual;     /* device [tokens][ldr], added to the output, or NULL         */
+  void* y;                  /* device [tokens][ldy]; may be residual or x itself (same row
+                               stride)                                                 */
+  int32_t* ids;             /* device [tokens][top_k] chosen experts, best first, or NULL */
+  float* weights;           /* device fp32 [tokens][top_k] their routing weights, or NULL */
+  void* workspace;          /* device, 16-byte aligned; wq_moe_layer_workspace_bytes      */
+  size_t workspace_bytes;
+  void* stream;
+  int32_t tokens;           /* 1 to WQ_MOE_MAX_TOKENS                                   */
+  int32_t n_expert, top_k;  /* <= WQ_MOE_MAX_EXPERTS; top_k <= n_expert, WQ_MOE_MAX_TOPK  */
+  int32_t hidden, inter;    /* hidden % 256 == 0, inter % 128 == 0                       */
+  int32_t ldx, ldr, ldy;    /* row strides, >= hidden, multiples of 8                    */
+  float routed_scale;       /* multiplies every routing weight                          */
+  int32_t renormalize;      /* weights divided by the sum of the chosen ones             */
+  uint32_t flags;           /* WQ_FLAG_BF16, WQ_FLAG_FP8 (E4M3 banks), WQ_FLAG_HAS_ZP (both
+                               banks have zero points)                                 */
+  int32_t reserved;
+} wq_moe_args;
+
+/* Workspace bytes of wq_moe_layer.  Contents need no initialization; calls that share one
+ * must not run concurrently. */
+int wq_moe_layer_workspace_bytes(int tokens, int n_expert, int top_k, int hidden, int inter,
+                                 size_t* bytes_out);
+
+/*
+ * A whole mixture-of-experts layer of a few tokens, routing included and nothing on the host:
+ *   p = softmax(x router^T); the top_k largest (equal ones: lowest expert first);
+ *   w = routed_scale * p (divided by the chosen ones' sum with `renormalize`);
+ *   y = residual + sum over the chosen e of w_e * down_e(silu(x gate_e) * (x up_e)).
+ * Sums are fp32 (the router's fp64); the activation between the two products is rounded to
+ * the element type, y once.  A NaN logit makes its token's weights, and so its row, NaN.
+ */
+int wq_moe_layer(const wq_moe_args* args);
+
 #ifdef __cplusplus
 }
 #endif

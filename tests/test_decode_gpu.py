@@ -1,0 +1,519 @@
+"""The decode-step operators on the GPU against their 64-bit forms (oracle/decode.py).
+
+Tolerances: half a step of the output type relative to the value (finfo.eps / 2), plus the
+bound the oracle derives for fp32 sums, plus half of fp16's smallest step."""
+
+import math
+
+import numpy as np
+import pytest
+
+from oracle import decode as ref
+
+torch = pytest.importorskip("torch")
+wq = pytest.importorskip("weight_only_quantized_gemm_amd")
+from weight_only_quantized_gemm_amd import decode, torch_ops  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+E4M3 = torch.float8_e4m3fn
+F16, BF16 = torch.float16, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def dev():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    return torch.device("cuda:0")
+
+
+def np64(t):
+    return t.double().cpu().numpy()
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def check(got, want, err, label):
+    """|got - want| within one rounding of got's type and err; infinities and NaN in place."""
+    half = half_step(got.dtype)
+    got = np64(got)
+    assert np.array_equal(np.isnan(got), np.isnan(want)), label
+    inf = np.isinf(want)
+    assert np.array_equal(got[inf], want[inf]), label
+    fine = np.isfinite(want)
+    tol = np.abs(want) * half * 1.01 + np.broadcast_to(err, want.shape) * 1.01 + 2.0 ** -25
+    off = np.where(fine, np.abs(got - want), 0) - np.where(fine, tol, 0)
+    assert off.max(initial=0) <= 0, (label, float(off.max()))
+
+
+def rng_of(dev, seed):
+    return torch.Generator(device=dev).manual_seed(seed)
+
+
+def normal(g, shape, dtype, sd=1.0):
+    return (torch.randn(shape, generator=g, device=g.device) * sd).to(dtype)
+
+
+# ---- RMS norm ------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("rows,n", [(1, 8), (3, 512), (1, 520), (5, 2048), (2, 4096), (7, 4104),
+                                    (1, 8192), (3, 8200), (2, 16384), (1, 16392), (2, 32768),
+                                    (1, 32776), (1, 65536), (300, 4096), (1000, 136)])
+def test_add_rms_norm(dev, dtype, rows, n):
+    g = rng_of(dev, n + rows)
+    x, d = normal(g, (rows, n), dtype, 3.0), normal(g, (rows, n), dtype)
+    w = normal(g, (n,), dtype)
+    eps = 1e-5
+    for delta in (None, d):
+        y, s = decode.add_rms_norm(x, w, eps, delta=delta)
+        want_y, want_s = ref.add_rms_norm(np64(x), None if delta is None else np64(d), np64(w), eps)
+        check(s, want_s, np.abs(want_s) * 2 * ref.E32, "sum")
+        check(y, want_y, np.abs(want_y) * 128 * ref.E32, "norm")
+
+
+def test_add_rms_norm_strides_and_aliases(dev):
+    g = rng_of(dev, 5)
+    wide = normal(g, (9, 3 * 640), F16)
+    x, d = wide[:, 640:1280], wide[:, 1280:]
+    w = normal(g, (640,), F16)
+    y0, s0 = decode.add_rms_norm(x.contiguous(), w, delta=d.contiguous())
+    out = torch.full((9, 1280), 7.0, dtype=F16, device=dev)
+    y1, _ = decode.add_rms_norm(x, w, delta=d, sum_out=x, out=out[:, 640:])  # sum over x
+    assert torch.equal(y1, y0) and torch.equal(wide[:, 640:1280], s0)
+    assert bool((out[:, :640] == 7).all())
+    y2, s2 = decode.add_rms_norm(s0, w, out=d)  # norm over another operand's rows
+    assert s2 is s0 and torch.equal(wide[:, 1280:], y2)
+
+
+def test_add_rms_norm_extremes(dev):
+    x = torch.zeros((4, 64), dtype=BF16, device=dev)
+    x[1] = 3e38          # its square overflows fp32: the norm is 0, as in the formula's fp32
+    x[2, 5] = float("nan")
+    x[3] = 1e-30
+    w = torch.ones(64, dtype=BF16, device=dev)
+    y, _ = decode.add_rms_norm(x, w, 1e-6)
+    assert bool((y[0] == 0).all()) and bool(y[2].isnan().all())
+    assert bool(y[3].isfinite().all())
+
+
+# ---- rotary positions and the cache write -----------------------------------------------------
+
+def paged(dev, pages, page, heads, d, dtype, order, scales=None, g=None):
+    """A cache of the given storage order, filled with random values."""
+    shape = (pages, heads, page, d) if order == "hnd" else (pages, page, heads, d)
+    g = g or rng_of(dev, 1)
+    kv = [torch.randn(shape, generator=g, device=dev) for _ in range(2)]
+    kv = [(x * (60 if dtype is E4M3 else 1)).to(dtype) for x in kv]
+    kv = [x.transpose(1, 2) if order == "hnd" else x for x in kv]
+    return decode.PagedCache(kv[0], kv[1], *(scales or (None, None)))
+
+
+@pytest.mark.parametrize("case", [
+    # tokens, q heads, kv heads, d, rot, page, axes, interleaved, cache, order, type
+    (1, 4, 2, 128, 128, 16, 1, False, "same", "hnd", F16),
+    (1, 0, 1, 64, 64, 16, 1, True, "same", "nhd", BF16),
+    (37, 7, 1, 80, 40, 24, 2, False, "e4m3", "hnd", F16),
+    (37, 7, 1, 80, 40, 24, 2, True, "e4m3", "nhd", BF16),
+    (5, 3, 3, 16, 8, 1, 1, False, "same", "nhd", BF16),
+    (130, 8, 2, 256, 256, 7, 3, False, "e4m3", "nhd", BF16),
+    (130, 8, 2, 256, 128, 7, 4, True, "same", "hnd", F16),
+    (9, 2, 2, 72, 0, 8, 1, False, "e4m3", "hnd", BF16),
+    (4200, 1, 1, 64, 64, 64, 1, False, "same", "hnd", F16),
+])
+def test_rope_append(dev, case):
+    t, hq, hkv, d, rot, page, axes, inter, kind, order, dtype = case
+    g = rng_of(dev, 11 + t + d)
+    qkv = normal(g, (t, (hq + 2 * hkv) * d), dtype)
+    q, k, v = (x.unflatten(1, (-1, d)) if x.shape[1] else None
+               for x in qkv.split([hq * d, hkv * d, hkv * d], dim=1))
+    scales = None
+    if kind == "e4m3":
+        scales = [torch.rand(hkv, generator=g, device=dev) * 0.02 + 0.004 for _ in range(2)]
+    pages = -(-t // page) + 2
+    cache = paged(dev, pages, page, hkv, d, E4M3 if kind == "e4m3" else dtype, order, scales, g)
+    slots = torch.randperm(pages * page, generator=g, device=dev)[:t]
+    if t > 4:
+        slots[1], slots[3] = -1, pages * page  # padding, and a slot past the cache
+    before = np64(cache.k), np64(cache.v)
+    half = rot // 2
+    inv = (10000.0 ** (-torch.arange(half, device=dev).double() / max(1, half))).float()
+    pos = torch.randint(0, 1 << 20, (axes, t), generator=g, device=dev).to(torch.int32)
+    cut = [half * i // axes for i in range(axes + 1)]
+    sections = [cut[i + 1] - cut[i] for i in range(axes)]
+    got = decode.rope_append(q, k, v, cache, slots, positions=pos if half else None,
+                             inv_freq=inv, sections=sections, interleaved=inter)
+    posn, invn = pos.cpu().numpy(), inv.cpu().numpy()
+    if q is not None:
+        want, err = ref.rotate(np64(q), posn, invn, sections, inter)
+        check(got, want, err, "q")
+    kw, kerr = ref.rotate(np64(k), posn, invn, sections, inter)
+    vw, verr = np64(v), np.zeros_like(np64(v))
+    for name, tensor, was, want, err, sc in (
+            ("k", cache.k, before[0], kw, kerr, 0), ("v", cache.v, before[1], vw, verr, 1)):
+        full, full_err = was.copy(), np.zeros_like(was)
+        if scales is not None:
+            s = np64(scales[sc])[:, None]
+            # the quotient is fp32; E4M3's smallest half step is 2^-10
+            want = np.clip(want / s, -448, 448)
+            err = err / s + np.abs(want) * 2 * ref.E32 + 2.0 ** -10
+        for i, slot in enumerate(slots.tolist()):
+            if 0 <= slot < pages * page:
+                full[slot // page, slot % page] = want[i]
+                full_err[slot // page, slot % page] = err[i]
+        check(tensor, full, full_err, name)
+
+
+def test_rope_append_in_place_and_special_values(dev):
+    """q may be rotated over itself; NaN and infinities reach an E4M3 cache as NaN and 448."""
+    g = rng_of(dev, 3)
+    q = normal(g, (6, 4, 64), F16)
+    k, v = normal(g, (6, 1, 64), F16), normal(g, (6, 1, 64), F16)
+    v[0, 0, :4] = torch.tensor([float("nan"), float("inf"), -float("inf"), 449.0])
+    cache = paged(dev, 2, 4, 1, 64, E4M3, "hnd")
+    slots = torch.arange(6, device=dev)
+    pos = torch.arange(6, device=dev, dtype=torch.int32)
+    inv = torch.rand(32, generator=g, device=dev)
+    want = decode.rope_append(q, k, v, cache, slots, positions=pos, inv_freq=inv)
+    got = decode.rope_append(q, k, v, cache, slots, positions=pos, inv_freq=inv, q_out=q)
+    assert got is q and torch.equal(got, want)
+    head = cache.v[0, 0, 0, :4].float()
+    assert bool(head[0].isnan()) and head[1:].tolist() == [448.0, -448.0, 448.0]
+
+
+# ---- attention ------------------------------------------------------------------------------
+
+def attn_case(dev, lens, hq, hkv, d, page, dtype, kind="same", order="hnd", window=0, softcap=0.0,
+              keep=False, max_len=None, seed=0, spare=3, poison=True):
+    g = rng_of(dev, seed + 31 * d + hq)
+    b = len(lens)
+    top = max_len or max(1, max(lens))
+    per = -(-top // page)
+    scales = None
+    if kind == "e4m3":
+        scales = [torch.rand(hkv, generator=g, device=dev) * 0.02 + 0.005 for _ in range(2)]
+    cache = paged(dev, b * per + spare, page, hkv, d, E4M3 if kind == "e4m3" else dtype, order,
+                  scales, g)
+    order_ = torch.randperm(b * per + spare, generator=g, device=dev)[: b * per]
+    table = order_.view(b, per).to(torch.int32).contiguous()
+    lens_t = torch.tensor(lens, dtype=torch.int32, device=dev)
+    q = normal(g, (b, hq, d), dtype)
+    mask = None
+    if keep:
+        mask = (torch.rand((b, top + 5), generator=g, device=dev) > 0.4).to(torch.uint8)
+        mask[0] = 0
+    if poison:  # NaN wherever no live position lies
+        live = torch.zeros(cache.k.shape[:2], dtype=torch.bool, device=dev)
+        for i, n in enumerate(lens):
+            j = torch.arange(max(0, n - window) if window else 0, n, device=dev)
+            if mask is not None:
+                j = j[mask[i, j] != 0]
+            live[table[i, j // page].long(), j % page] = True
+        dead = (~live)[:, :, None, None]
+        for x in (cache.k, cache.v):
+            if kind == "e4m3":
+                x.view(torch.uint8).masked_fill_(dead, 0x7F)
+            else:
+                x.masked_fill_(dead, float("nan"))
+    return dict(cache=cache, table=table, lens=lens_t, q=q, keep=mask, top=top, window=window,
+                softcap=softcap, hq=hq, dtype=dtype, scale=1 / math.sqrt(d))
+
+
+def attn_run(c, **kw):
+    plan = decode.PagedAttention(c["cache"], len(c["lens"]), c["hq"], c["top"], dtype=c["dtype"],
+                                 scale=c["scale"], window=c["window"], softcap=c["softcap"])
+    return plan(c["q"], c["table"], c["lens"], keep=c["keep"], lse=True, **kw)
+
+
+def attn_check(c, out, lse, label=""):
+    cache = c["cache"]
+    k, v = np64(cache.k), np64(cache.v)
+    if cache.k_scale is not None:
+        k, v = k * np64(cache.k_scale)[:, None], v * np64(cache.v_scale)[:, None]
+    want, want_lse, err, lse_err = ref.paged_attention(
+        np64(c["q"]), k, v, c["table"].cpu().numpy(), c["lens"].cpu().numpy(), c["scale"],
+        c["window"], c["softcap"], None if c["keep"] is None else c["keep"].cpu().numpy())
+    check(out, want, err, label + " out")
+    check(lse, want_lse, lse_err, label + " lse")
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("kind", ["same", "e4m3"])
+@pytest.mark.parametrize("d,hq,hkv,page,order", [
+    (16, 1, 1, 1, "hnd"), (64, 4, 4, 16, "nhd"), (72, 6, 2, 5, "hnd"), (80, 3, 3, 24, "nhd"),
+    (96, 20, 1, 16, "hnd"), (128, 8, 1, 16, "hnd"), (128, 40, 2, 64, "nhd"), (136, 2, 1, 32, "hnd"),
+    (192, 16, 1, 7, "nhd"), (256, 5, 1, 16, "hnd")])
+def test_attention_heads(dev, dtype, kind, d, hq, hkv, page, order):
+    c = attn_case(dev, [0, 1, 15, 31, 32, 33, 127, 300], hq, hkv, d, page, dtype, kind, order)
+    attn_check(c, *attn_run(c))
+
+
+@pytest.mark.parametrize("lens,kw", [
+    ([1], {}), ([0], {}), ([2, 0, 0], {}),
+    ([255, 256, 257, 129], dict(max_len=1000)),
+    ([5000, 17], {}), ([12345], dict(hkv=1, hq=2)), ([4097] * 3, dict(window=100)),
+    ([700, 33, 1], dict(window=1)), ([700, 33, 1], dict(window=32)), ([700, 33], dict(window=4000)),
+    ([513, 64], dict(softcap=20.0)), ([900, 300, 40], dict(keep=True)),
+    ([3000, 1], dict(keep=True, window=1500, softcap=5.0)),
+])
+@pytest.mark.parametrize("kind", ["same", "e4m3"])
+def test_attention_lengths_and_masks(dev, lens, kw, kind):
+    kw = dict(dict(hq=8, hkv=2), **kw)
+    c = attn_case(dev, lens, d=64, page=16, dtype=BF16, kind=kind, seed=sum(lens), **kw)
+    attn_check(c, *attn_run(c))
+
+
+def test_attention_empty_rows_are_zero(dev):
+    c = attn_case(dev, [600, 0, 40], 4, 2, 128, 16, F16, keep=True)
+    c["keep"][2] = 0
+    out, lse = attn_run(c)
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all())  # keep[0] is all zero
+
+
+def test_attention_page_numbers_outside_the_cache_are_left_out(dev):
+    c = attn_case(dev, [200, 64, 40], 4, 2, 64, 16, BF16, poison=False)
+    c["table"][0, 3], c["table"][0, 7] = -1, c["cache"].num_pages
+    c["table"][1, :] = 2 ** 31 - 1
+    c["table"][2, 0] = -2 ** 31
+    attn_check(c, *attn_run(c))
+
+
+def test_attention_lens_are_taken_into_range(dev):
+    c = attn_case(dev, [100, 100], 2, 1, 64, 16, F16)
+    want = attn_run(c)
+    c["lens"] = torch.tensor([1000000, -5], dtype=torch.int32, device=dev)
+    out, lse = attn_run(c)
+    assert torch.equal(out[0], want[0][0]) and bool((out[1] == 0).all())
+    assert lse[1].tolist() == [-math.inf] * 2
+
+
+def test_attention_extreme_scores(dev):
+    """Equal huge scores, one dominating score, and scores that fp16 p could not hold."""
+    c = attn_case(dev, [400], 2, 1, 64, 16, F16, poison=False)
+    c["cache"].k.fill_(20.0)
+    c["q"].fill_(30.0)
+    attn_check(c, *attn_run(c), "huge")
+    c["cache"].k.zero_()
+    c["cache"].k[c["table"][0, 0].long(), 3] = 1.0
+    c["q"].fill_(2.0)  # position 3 leads by 16: the rest are exp(-16) of it
+    attn_check(c, *attn_run(c), "tail")
+
+
+def test_attention_small_tail_counts_in_fp16(dev):
+    """40000 positions at 2^-25.2 of the largest hold 1/1000 of the sum: V is 1000 there."""
+    c = attn_case(dev, [40000], 1, 1, 64, 64, F16, poison=False)
+    c["cache"].k.zero_()
+    c["cache"].v.fill_(1000.0)
+    first = c["table"][0, 0].long()
+    c["cache"].k[first, 0] = 1.0
+    c["cache"].v[first, 0] = 0.0
+    c["q"].fill_(17.5 / 8)  # 64 * q * scale = 17.5
+    attn_check(c, *attn_run(c))
+
+
+def test_attention_strided_rows_and_given_outputs(dev):
+    c = attn_case(dev, [77, 300], 4, 2, 64, 16, BF16)
+    want, want_lse = attn_run(c)
+    wide = torch.zeros((2, 10 * 64), dtype=BF16, device=dev)
+    wide[:, 128:384] = c["q"].flatten(1)
+    c["q"] = wide[:, 128:384].unflatten(1, (4, 64))
+    dest = torch.full((2, 6, 64), 9.0, dtype=BF16, device=dev)
+    lse = torch.zeros((2, 4), device=dev)
+    plan = decode.PagedAttention(c["cache"], 2, 4, c["top"], dtype=BF16)
+    got = plan(c["q"], c["table"], c["lens"], out=dest[:, 1:5], lse=lse)
+    assert torch.equal(got[0], want) and torch.equal(lse, want_lse)
+    assert bool((dest[:, 0] == 9).all()) and bool((dest[:, 5] == 9).all())
+    assert torch.equal(plan(c["q"], c["table"], c["lens"]), want)
+
+
+def test_attention_offsets_past_32_bits(dev):
+    """Pages beyond 4 GiB of an E4M3 cache: element and byte offsets need 64 bits."""
+    pages, page, hkv, d = (1 << 20) + 64, 16, 2, 128  # 4096 bytes a page
+    kv = [torch.empty((pages, hkv, page, d), dtype=torch.uint8, device=dev) for _ in range(2)]
+    g = rng_of(dev, 9)
+    table = torch.tensor([[pages - 1, 3, pages - 40, (1 << 19) + 5]], dtype=torch.int32, device=dev)
+    small = [(torch.randn((4, hkv, page, d), generator=g, device=dev) * 50).to(E4M3)
+             for _ in range(2)]
+    for x, s in zip(kv, small):
+        x[table[0].long()] = s.view(torch.uint8)
+    far = decode.PagedCache(*(x.view(E4M3).transpose(1, 2) for x in kv))
+    near = decode.PagedCache(*(x.transpose(1, 2) for x in small))
+    q, lens = normal(g, (1, 4, d), BF16, 0.02), torch.tensor([61], dtype=torch.int32, device=dev)
+    a = decode.PagedAttention(far, 1, 4, 64, dtype=BF16)(q, table, lens)
+    order = torch.arange(4, dtype=torch.int32, device=dev)[None]
+    assert torch.equal(a, decode.PagedAttention(near, 1, 4, 64, dtype=BF16)(q, order, lens))
+    k = normal(g, (1, hkv, d), BF16)
+    slot = torch.tensor([pages * page - 3], device=dev)
+    decode.rope_append(None, k, k, far, slot)
+    assert torch.equal(far.k[pages - 1, 13].float(), k[0].to(E4M3).float())
+
+
+def test_attention_is_deterministic(dev):
+    c = attn_case(dev, [9000, 100, 4000], 8, 2, 128, 16, BF16)
+    first = attn_run(c)
+    for _ in range(3):
+        again = attn_run(c)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+# ---- the mixture-of-experts layer ---------------------------------------------------------------
+
+def moe_case(dev, tokens, experts, top_k, hidden, inter, dtype, kind="u4b8", group=128, seed=0,
+             **kw):
+    g = rng_of(dev, seed + 7 * tokens + experts + inter)
+
+    def bank(k, n):
+        per = 4 if kind == "e4m3" else 8
+        words = torch.randint(-2 ** 31, 2 ** 31, (experts, k // per, n), generator=g, device=dev,
+                              dtype=torch.int64).to(torch.int32)
+        if kind == "e4m3":
+            words &= ~0x08080808
+        rows = 1 if group == -1 else k // group
+        s = torch.rand((experts, rows, n), generator=g, device=dev)
+        s = (s * 5e-4 + 1e-4 if kind == "e4m3" else s * 0.015 + 0.005).to(dtype)
+        z = None
+        if kind == "u4":
+            z = torch.randint(-2 ** 31, 2 ** 31, (experts, rows, n // 8), generator=g, device=dev,
+                              dtype=torch.int64).to(torch.int32)
+        return dict(words=words, s=s, z=z)
+
+    gate, up, down = bank(hidden, inter), bank(hidden, inter), bank(inter, hidden)
+
+    def one(b, e):
+        return dict(qweight=b["words"][e], scales=b["s"][e],
+                    zeros=None if b["z"] is None else b["z"][e], group_size=group)
+
+    pairs = [dict(gate=one(gate, e), up=one(up, e), group_size=group) for e in range(experts)]
+    banks = [torch_ops.ExpertBank(x, device=dev, bf16=dtype is BF16, fp8=kind == "e4m3")
+             for x in (pairs, [one(down, e) for e in range(experts)])]
+    router = normal(g, (experts, hidden), dtype, 1.5 / math.sqrt(hidden))
+    x = normal(g, (tokens, hidden), dtype)
+    return dict(banks=banks, router=router, x=x, raw=(gate, up, down), kind=kind, group=group,
+                top_k=top_k, dtype=dtype, g=g, **kw)
+
+
+def dequant(b, kind, group):
+    w = b["words"].cpu().numpy()
+    e, r, n = w.shape
+    per, bits = (4, 8) if kind == "e4m3" else (8, 4)
+    code = np.stack([(w >> (bits * i)) & (2 ** bits - 1) for i in range(per)], 2).reshape(e, r * per, n)
+    rows = r * per if group == -1 else group
+    if kind == "e4m3":
+        v = np64(torch.from_numpy(code.astype(np.uint8)).view(E4M3))
+    else:
+        zero = np.full((e, r * per // rows, n), 8.0)
+        if b["z"] is not None:
+            zw = b["z"].cpu().numpy()
+            zero = np.stack([(zw >> (4 * i)) & 15 for i in range(8)], 3).reshape(e, -1, n)
+        v = code - np.repeat(zero, rows, 1)
+    return v * np.repeat(np64(b["s"]), rows, 1)
+
+
+def moe_check(c, residual=None, renormalize=True, scale=1.0, **kw):
+    layer = decode.MoELayer(*c["banks"], c["router"], c["top_k"], renormalize=renormalize,
+                            routed_scale=scale)
+    x = c["x"]
+    y = layer(x, residual=residual, **kw)
+    n = x.shape[0]
+    w = [dequant(b, c["kind"], c["group"]) for b in c["raw"]]
+    want, ids, weights, err = ref.moe_layer(np64(x), np64(c["router"]), *w, c["top_k"], renormalize,
+                                            scale, None if residual is None else np64(residual),
+                                            half_step(c["dtype"]))
+    assert np.array_equal(layer.ids[:n].cpu().numpy(), ids)
+    check(layer.weights[:n], weights, weights * 32 * ref.E32, "weights")
+    # the routing weights' own error is relative to every term
+    check(y, want, err * (1 + 64 * ref.E32) + np.abs(want) * 64 * ref.E32, "y")
+    return layer, y
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("kind,group", [("u4b8", 128), ("u4b8", 64), ("u4b8", 32), ("u4b8", 16),
+                                        ("u4b8", -1), ("u4", 128), ("u4", 64), ("u4", 32),
+                                        ("u4", 16), ("e4m3", 128), ("e4m3", -1)])
+def test_moe_weights(dev, dtype, kind, group):
+    c = moe_case(dev, 5, 6, 2, 512, 384, dtype, kind, group)
+    moe_check(c, residual=normal(c["g"], (5, 512), dtype))
+
+
+@pytest.mark.parametrize("tokens,experts,top_k,hidden,inter,renorm", [
+    (1, 1, 1, 256, 128, True), (1, 8, 2, 512, 256, False), (2, 8, 2, 256, 1408, True),
+    (16, 4, 4, 256, 128, False), (16, 64, 8, 256, 128, True), (7, 256, 16, 256, 128, False),
+    (13, 65, 3, 768, 128, True), (16, 1, 1, 1280, 640, True), (3, 100, 1, 256, 256, False),
+])
+def test_moe_shapes(dev, tokens, experts, top_k, hidden, inter, renorm):
+    c = moe_case(dev, tokens, experts, top_k, hidden, inter, BF16)
+    moe_check(c, renormalize=renorm, scale=2.5)
+
+
+def test_moe_ties_take_the_lowest_expert(dev):
+    c = moe_case(dev, 4, 70, 5, 256, 128, F16)
+    c["router"][:] = 0
+    c["router"][[3, 40, 68]] = c["router"].new_ones(256) * 0.5  # equal logits, either sign
+    layer, _ = moe_check(c)
+    for t in range(4):
+        up = float(c["x"][t].double().sum()) > 0
+        assert layer.ids[t].tolist() == ([3, 40, 68, 0, 1] if up else [0, 1, 2, 4, 5])
+
+
+def test_moe_strides_aliases_and_nan_rows(dev):
+    c = moe_case(dev, 6, 8, 2, 512, 256, BF16)
+    _, want = moe_check(c, residual=c["x"])
+    layer = decode.MoELayer(*c["banks"], c["router"], 2)
+    wide = torch.zeros((6, 2048), dtype=BF16, device=dev)
+    wide[:, 512:1024] = c["x"]
+    view = wide[:, 512:1024]
+    got = layer(view, residual=view, out=view)  # over its own input
+    assert torch.equal(got, want) and bool((wide[:, :512] == 0).all())
+    x = c["x"].clone()
+    x[2, 7] = float("nan")
+    y = layer(x, residual=x)
+    rest = [0, 1, 3, 4, 5]
+    assert torch.equal(y[rest], want[rest]) and bool(y[2].isnan().all())
+    assert bool(layer.weights[2].isnan().all())
+
+
+# ---- streams and graphs ---------------------------------------------------------------------------
+
+def test_a_decode_step_on_another_stream_and_in_a_graph(dev):
+    """All four on a side stream, then captured and replayed on changed inputs: the replays
+    give what eager calls give."""
+    c = attn_case(dev, [100, 37], 4, 2, 128, 16, BF16, poison=False, max_len=400)
+    m = moe_case(dev, 2, 4, 2, 512, 256, BF16)
+    layer = decode.MoELayer(*m["banks"], m["router"], 2)
+    plan = decode.PagedAttention(c["cache"], 2, 4, 400, dtype=BF16)
+    norm_w = normal(m["g"], (512,), BF16)
+    inv = torch.rand(64, device=dev)
+    x, delta = normal(m["g"], (2, 512), BF16), normal(m["g"], (2, 512), BF16)
+    q, k, v = (normal(m["g"], (2, h, 128), BF16) for h in (4, 2, 2))
+    slots = c["table"][:, 6].long() * 16 + 4
+    pos = torch.tensor([100, 100], dtype=torch.int32, device=dev)
+    lens = torch.tensor([101, 101], dtype=torch.int32, device=dev)
+
+    def step():
+        y, s = decode.add_rms_norm(x, norm_w, delta=delta)
+        qr = decode.rope_append(q, k, v, c["cache"], slots, positions=pos, inv_freq=inv)
+        o = plan(qr, c["table"], lens)
+        z = layer((y + o.flatten(1)), residual=s)
+        return y, s, qr, o, z
+
+    eager = step()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = step()
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(eager, other))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for i in range(3):
+        x.copy_(normal(m["g"], (2, 512), BF16))
+        q.copy_(normal(m["g"], (2, 4, 128), BF16))
+        lens.fill_(101 + 40 * i)
+        eager = [t.clone() for t in step()]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(eager, held)), i

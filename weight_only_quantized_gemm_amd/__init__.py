@@ -38,9 +38,14 @@ EXPORTED = (
     "wq_csr_from_routes", "wq_grouped_workspace_bytes", "wq_grouped_gemm",
     "wq_stream_read_sink_words", "wq_stream_read", "wq_interleave_gate_up", "wq_repack_fp8",
     "wq_repack_fp8_rows", "wq_fp8_block_scales", "wq_mfma_rate", "wq_gemm_plan",
-    "wq_gemm_noalloc",
+    "wq_gemm_noalloc", "wq_add_rms_norm", "wq_rope_append",
+    "wq_paged_attention_workspace_bytes", "wq_paged_attention",
+    "wq_moe_layer_workspace_bytes", "wq_moe_layer",
 )
 WQ_NOALLOC_SCRATCH_BYTES = 32 << 20
+
+WQ_MAX_ROPE_AXES = 4
+WQ_MOE_MAX_TOKENS, WQ_MOE_MAX_EXPERTS, WQ_MOE_MAX_TOPK = 16, 256, 16
 
 WQ_KERNEL_SMALL_M, WQ_KERNEL_TILE_256, WQ_KERNEL_TILE_128 = 1, 2, 3
 KERNEL_NAMES = {WQ_KERNEL_SMALL_M: "small-M (16-column blocks)",
@@ -89,6 +94,80 @@ class wq_grouped_args(ctypes.Structure):
     ]
 
 
+class wq_norm_args(ctypes.Structure):
+    _fields_ = [
+        ("abi_version", ctypes.c_uint32), ("struct_size", ctypes.c_uint32),
+        ("x", ctypes.c_void_p), ("delta", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+        ("sum_out", ctypes.c_void_p), ("y", ctypes.c_void_p), ("stream", ctypes.c_void_p),
+        ("rows", ctypes.c_int32), ("n", ctypes.c_int32), ("ldx", ctypes.c_int32),
+        ("ldd", ctypes.c_int32), ("lds", ctypes.c_int32), ("ldy", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("flags", ctypes.c_uint32), ("reserved", ctypes.c_int32),
+    ]
+
+
+class wq_kv_cache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+        ("slot_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+        ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+    ]
+
+
+class wq_rope_args(ctypes.Structure):
+    _fields_ = [
+        ("abi_version", ctypes.c_uint32), ("struct_size", ctypes.c_uint32),
+        ("cache", wq_kv_cache), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
+        ("stream", ctypes.c_void_p), ("tokens", ctypes.c_int32), ("q_heads", ctypes.c_int32),
+        ("ldq", ctypes.c_int32), ("ldk", ctypes.c_int32), ("ldv", ctypes.c_int32),
+        ("ldqo", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("axes", ctypes.c_int32),
+        ("sections", ctypes.c_int32 * WQ_MAX_ROPE_AXES), ("interleaved", ctypes.c_int32),
+        ("flags", ctypes.c_uint32), ("reserved", ctypes.c_int32),
+    ]
+
+
+class wq_attn_args(ctypes.Structure):
+    _fields_ = [
+        ("abi_version", ctypes.c_uint32), ("struct_size", ctypes.c_uint32),
+        ("cache", wq_kv_cache), ("q", ctypes.c_void_p), ("out", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+        ("keep", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t), ("stream", ctypes.c_void_p),
+        ("batch", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("max_len", ctypes.c_int32),
+        ("table_stride", ctypes.c_int32), ("keep_stride", ctypes.c_int32),
+        ("ldq", ctypes.c_int32), ("ldo", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("flags", ctypes.c_uint32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class wq_expert_bank(ctypes.Structure):
+    _fields_ = [
+        ("b", ctypes.c_void_p), ("s", ctypes.c_void_p), ("zp", ctypes.c_void_p),
+        ("b_stride_bytes", ctypes.c_size_t), ("s_stride_bytes", ctypes.c_size_t),
+        ("zp_stride_bytes", ctypes.c_size_t), ("group_size", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class wq_moe_args(ctypes.Structure):
+    _fields_ = [
+        ("abi_version", ctypes.c_uint32), ("struct_size", ctypes.c_uint32),
+        ("x", ctypes.c_void_p), ("router", ctypes.c_void_p), ("gate_up", wq_expert_bank),
+        ("down", wq_expert_bank), ("residual", ctypes.c_void_p), ("y", ctypes.c_void_p),
+        ("ids", ctypes.c_void_p), ("weights", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+        ("stream", ctypes.c_void_p), ("tokens", ctypes.c_int32), ("n_expert", ctypes.c_int32),
+        ("top_k", ctypes.c_int32), ("hidden", ctypes.c_int32), ("inter", ctypes.c_int32),
+        ("ldx", ctypes.c_int32), ("ldr", ctypes.c_int32), ("ldy", ctypes.c_int32),
+        ("routed_scale", ctypes.c_float), ("renormalize", ctypes.c_int32),
+        ("flags", ctypes.c_uint32), ("reserved", ctypes.c_int32),
+    ]
+
+
 _LIB = None
 
 
@@ -127,6 +206,14 @@ def lib() -> ctypes.CDLL:
             "wq_mfma_rate": (ctypes.c_int, [vp, i32, vp, sz, ctypes.POINTER(ctypes.c_double),
                                             vp]),
             "wq_interleave_gate_up": (ctypes.c_int, [vp, vp, vp, i32, i32, i32, vp]),
+            "wq_add_rms_norm": (ctypes.c_int, [ctypes.POINTER(wq_norm_args)]),
+            "wq_rope_append": (ctypes.c_int, [ctypes.POINTER(wq_rope_args)]),
+            "wq_paged_attention_workspace_bytes": (ctypes.c_int, [i32, i32, i32, i32, i32, i32,
+                                                                  ctypes.POINTER(sz)]),
+            "wq_paged_attention": (ctypes.c_int, [ctypes.POINTER(wq_attn_args)]),
+            "wq_moe_layer_workspace_bytes": (ctypes.c_int, [i32, i32, i32, i32, i32,
+                                                            ctypes.POINTER(sz)]),
+            "wq_moe_layer": (ctypes.c_int, [ctypes.POINTER(wq_moe_args)]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -335,3 +422,43 @@ def wq_interleave_gate_up(gate, up, out, rows: int, cols: int, bits_per_column: 
     """Pair gate/up columns in 16-column blocks for WQ_FLAG_SWIGLU (see include/wq.h)."""
     _check(lib().wq_interleave_gate_up(_ptr(gate), _ptr(up), _ptr(out), rows, cols,
                                        bits_per_column, _stream(stream, out)))
+
+
+def versioned(cls, **fields):
+    """An argument struct of the decode-step calls with its version and size filled in."""
+    return cls(abi_version=WQ_ABI_VERSION, struct_size=ctypes.sizeof(cls), **fields)
+
+
+# The decode-step calls take their argument struct as it is (weight_only_quantized_gemm_amd
+# .decode fills them from tensors): they run once per layer and token, and a call that is to
+# cost a few microseconds cannot spend as long on marshalling.
+def wq_add_rms_norm(args: wq_norm_args) -> None:
+    _check(lib().wq_add_rms_norm(ctypes.byref(args)))
+
+
+def wq_rope_append(args: wq_rope_args) -> None:
+    _check(lib().wq_rope_append(ctypes.byref(args)))
+
+
+def wq_paged_attention_workspace_bytes(batch: int, q_heads: int, kv_heads: int, head_dim: int,
+                                       max_len: int, window: int = 0) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().wq_paged_attention_workspace_bytes(batch, q_heads, kv_heads, head_dim, max_len,
+                                                    window, ctypes.byref(out)))
+    return int(out.value)
+
+
+def wq_paged_attention(args: wq_attn_args) -> None:
+    _check(lib().wq_paged_attention(ctypes.byref(args)))
+
+
+def wq_moe_layer_workspace_bytes(tokens: int, n_expert: int, top_k: int, hidden: int,
+                                 inter: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().wq_moe_layer_workspace_bytes(tokens, n_expert, top_k, hidden, inter,
+                                              ctypes.byref(out)))
+    return int(out.value)
+
+
+def wq_moe_layer(args: wq_moe_args) -> None:
+    _check(lib().wq_moe_layer(ctypes.byref(args)))

@@ -223,6 +223,7 @@ def attn_case(dev, lens, hq, hkv, d, page, dtype, kind="same", order="hnd", wind
 def attn_run(c, **kw):
     plan = decode.PagedAttention(c["cache"], len(c["lens"]), c["hq"], c["top"], dtype=c["dtype"],
                                  scale=c["scale"], window=c["window"], softcap=c["softcap"])
+    plan.workspace.fill_(0xFF)  # its contents need no initialization
     return plan(c["q"], c["table"], c["lens"], keep=c["keep"], lse=True, **kw)
 
 
@@ -414,6 +415,7 @@ def moe_check(c, residual=None, renormalize=True, scale=1.0, **kw):
     layer = decode.MoELayer(*c["banks"], c["router"], c["top_k"], renormalize=renormalize,
                             routed_scale=scale)
     x = c["x"]
+    layer.workspace.fill_(0xFF)  # its contents need no initialization
     y = layer(x, residual=residual, **kw)
     n = x.shape[0]
     w = [dequant(b, c["kind"], c["group"]) for b in c["raw"]]

@@ -2,17 +2,19 @@
 // experts' gate/up projections with SwiGLU, their down projections and the weighted sum.
 //
 // The layer reads every chosen expert's weights once and does 2 * (rows per expert) products
-// per weight, so it is bound by the weight stream.  Four kernels, each needing the whole
-// result of the one before it:
+// per weight, so it is bound by the weight stream.  Five launches, each needing the whole
+// result of the one before it, and nothing on the host:
 //  1. router_kernel: the logits x router^T.
-//  2. route_kernel (one work-group): top-k and weights per token, then the experts that were
-//     chosen at all ("slots"), which tokens each has, and where its rows of the activation
-//     buffer start.  Nothing returns to the host: the next grids are sized for the most slots
-//     there can be, and work-groups past the last slot end at once.
-//  3. gate_up_kernel: one work-group per pair of 16-column blocks and slot.
-//  4. down_kernel: one work-group per 16 output columns walks all slots, so the weighted sum
-//     over a token's experts is formed in registers, in a fixed order, and no pair rows or
-//     atomics are needed.
+//  2. route_kernel, one work-group: the tokens' top-k, and for each expert that any token
+//     chose (a "slot") its rows.  (Taken in every work-group of the next kernel instead, the
+//     routing cost 4 to 30 us more than this launch.)
+//  3. product_kernel on the gate/up bank: a work-group per slot and pair of 16-column blocks,
+//     a gate and an up block, ends in the activation silu(g) * u.  The grid has room for the
+//     most slots there can be; work-groups past the last one end at once.
+//  4. product_kernel on the down bank: the same over two neighbouring blocks, ends in fp32
+//     rows, one for each (token, choice).
+//  5. combine_kernel: each token's rows times their routing weights, in the order of choice
+//     (no atomics), and the residual.
 // Products are 16x16x32 MFMAs on codes dequantized in registers (wq_device.h); each scale
 // unit's partial is scaled in fp32.
 #include "wq_decode.h"
@@ -24,14 +26,15 @@ namespace {
 constexpr int kMaxT = WQ_MOE_MAX_TOKENS;
 constexpr int kMaxE = WQ_MOE_MAX_EXPERTS;
 
-// The routing of a call, in the workspace.
+// The routing of a call, in the workspace.  A slot's row is a (token, choice) pair: its number
+// token * top_k + choice in the low half, the token in the high half.
+struct RouteSlot {
+  int32_t expert, rows;  // ascending experts; no rows: past the last chosen expert
+  uint32_t pair[kMaxT];
+};
 struct Route {
-  int32_t n_active;
-  int32_t pad[3];
-  int32_t expert[kMaxE];   // of each slot, ascending
-  uint32_t mask[kMaxE];    // its tokens
-  int32_t off[kMaxE];      // its first row of the activation buffer
-  float w[kMaxE][kMaxT];   // routing weight of each token (0 where not routed)
+  RouteSlot slot[kMaxE];
+  float w[kMaxT * WQ_MOE_MAX_TOPK];  // routing weight of each pair
 };
 
 struct Bank {
@@ -45,195 +48,250 @@ size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 // ---- routing ---------------------------------------------------------------------------
 
-// Logits of one expert and four tokens per wave.  Eight products at a time are summed in
-// fp32, the sums in fp64: the order of nearly equal logits decides which experts run.
+constexpr int kRouterThreads = 256;
+
+// Logits of one expert and four tokens per work-group, whose threads share the hidden size
+// (one CU reading a whole router of 64 KiB takes 2 us longer, one of 256 KiB 10 us).  Eight
+// products at a time are summed in fp32, the sums in fp64 and rounded once: the order of
+// nearly equal logits decides which experts run.
 template <bool BF16>
-__global__ __launch_bounds__(256) void router_kernel(const uint16_t* __restrict__ x, int ldx,
-                                                     const uint16_t* __restrict__ router,
-                                                     int tokens, int n_expert, int hidden,
-                                                     double* __restrict__ logits) {
+__global__ __launch_bounds__(kRouterThreads) void router_kernel(
+    const uint16_t* __restrict__ x, int ldx, const uint16_t* __restrict__ router, int tokens,
+    int n_expert, int hidden, float* __restrict__ logits) {
   using A = Act<BF16>;
-  const int lane = threadIdx.x & 63;
-  const int e = blockIdx.x * 4 + (threadIdx.x >> 6);
+  __shared__ double red[kRouterThreads / 64][4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int e = blockIdx.x;
   const int t0 = blockIdx.y * 4;
-  if (e >= n_expert) return;
   const uint16_t* rp = router + (long)e * hidden;
   double acc[4] = {0., 0., 0., 0.};
 #pragma unroll 2
-  for (int k = lane * 8; k < hidden; k += 512) {
+  for (int k = tid * 8; k < hidden; k += kRouterThreads * 8) {
     const u32x4 r = *reinterpret_cast<const u32x4*>(rp + k);
-    float rf[8];
+    u32x4 xv[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) rf[i] = A::value((uint16_t)(r[i / 2] >> (16 * (i % 2))));
+    for (int j = 0; j < 4; ++j)
+      xv[j] = *reinterpret_cast<const u32x4*>(x + (long)min(t0 + j, tokens - 1) * ldx + k);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int t = t0 + j < tokens ? t0 + j : tokens - 1;
-      const u32x4 xv = *reinterpret_cast<const u32x4*>(x + (long)t * ldx + k);
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        sum = __builtin_fmaf(rf[i], A::value((uint16_t)(xv[i / 2] >> (16 * (i % 2)))), sum);
+        sum = __builtin_fmaf(A::value((uint16_t)(r[i / 2] >> (16 * (i % 2)))),
+                             A::value((uint16_t)(xv[j][i / 2] >> (16 * (i % 2)))), sum);
       acc[j] += (double)sum;
     }
   }
+  // Each exchange halves the tokens a lane carries, then adds over the lanes left.
+  const bool up = lane & 32, odd = lane & 16;
+  const double a0 = (up ? acc[2] : acc[0]) + __shfl_xor(up ? acc[0] : acc[2], 32);
+  const double a1 = (up ? acc[3] : acc[1]) + __shfl_xor(up ? acc[1] : acc[3], 32);
+  double v = (odd ? a1 : a0) + __shfl_xor(odd ? a0 : a1, 16);
 #pragma unroll
-  for (int d = 32; d >= 1; d /= 2)
+  for (int d = 8; d >= 1; d /= 2) v += __shfl_xor(v, d);
+  if ((lane & 15) == 0) red[wave][lane >> 4] = v;  // token 2 * up + odd
+  __syncthreads();
+  if (tid < 4 && t0 + tid < tokens) {
+    double sum = red[0][tid];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] += __shfl_xor(acc[j], d);
-  if (lane < 4 && t0 + lane < tokens) {
-    double v = acc[0];
-#pragma unroll
-    for (int j = 1; j < 4; ++j) v = lane == j ? acc[j] : v;
-    logits[(t0 + lane) * n_expert + e] = v;
+    for (int w = 1; w < kRouterThreads / 64; ++w) sum += red[w][tid];
+    logits[(t0 + tid) * n_expert + e] = (float)sum;
   }
 }
 
 template <int CTRL>
-__device__ __forceinline__ double dpp_max(double x) {
-  const long long bits = __builtin_bit_cast(long long, x);
-  const int lo = __builtin_amdgcn_update_dpp((int)bits, (int)bits, CTRL, 0xf, 0xf, false);
-  const int hi = __builtin_amdgcn_update_dpp((int)(bits >> 32), (int)(bits >> 32), CTRL, 0xf,
-                                             0xf, false);
-  const double other =
-      __builtin_bit_cast(double, ((long long)hi << 32) | (long long)(unsigned)lo);
+__device__ __forceinline__ uint32_t dpp_max(uint32_t x) {
+  const uint32_t other = __builtin_amdgcn_update_dpp((int)x, (int)x, CTRL, 0xf, 0xf, false);
   return other > x ? other : x;
 }
 
-// Maximum over the wave, in every lane.
-__device__ __forceinline__ double wave_max(double x) {
+// Maximum over the wave, as a scalar.
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
   x = dpp_max<0x111>(x);  // row_shr 1, 2, 4, 8: lane 15 of each row of 16 has its maximum
   x = dpp_max<0x112>(x);
   x = dpp_max<0x114>(x);
   x = dpp_max<0x118>(x);
   x = dpp_max<0x142>(x);  // row_bcast 15 and 31: lane 63 has the wave's
   x = dpp_max<0x143>(x);
-  const long long bits = __builtin_bit_cast(long long, x);
-  const unsigned lo = __builtin_amdgcn_readlane((int)bits, 63);
-  const int hi = __builtin_amdgcn_readlane((int)(bits >> 32), 63);
-  return __builtin_bit_cast(double, ((long long)hi << 32) | (long long)lo);
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
 }
 
-// Wave t takes token t's top-k.  Each logit's lowest 8 mantissa bits give way to its expert
-// number, coded so that of equal logits the lower expert is the larger key.
-__global__ __launch_bounds__(kMaxT * 64) void route_kernel(const double* __restrict__ logits,
-                                                          int tokens, int n_expert, int top_k,
-                                                          int renormalize, float routed_scale,
-                                                          int32_t* __restrict__ ids,
-                                                          float* __restrict__ weights,
-                                                          Route* __restrict__ route) {
-  constexpr int PER = kMaxE / 64;
-  __shared__ uint32_t mask_lds[kMaxE];
-  __shared__ float w_lds[kMaxE][kMaxT];
-  __shared__ int total_lds[PER][2];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int t = __builtin_amdgcn_readfirstlane(tid >> 6);
-  for (int i = tid; i < kMaxE; i += kMaxT * 64) mask_lds[i] = 0;
-  for (int i = tid; i < n_expert * kMaxT; i += kMaxT * 64) w_lds[i / kMaxT][i % kMaxT] = 0.f;
-  __syncthreads();
-  if (t < tokens) {
-    double l[PER], key[PER];
-    bool bad = false;
+// One token's top-k by its wave: lane j ends with the j-th best expert and its weight.  Equal
+// logits go to the lower expert, NaN below everything; PER experts a lane.
+template <int PER>
+__device__ __forceinline__ void token_top_k(const float* logits, int n_expert, int top_k,
+                                            bool renormalize, float routed_scale, int lane,
+                                            int& my_id, float& my_w) {
+  float l[PER];
+  uint32_t key[PER];  // ordered as the logits are; 0 is below every expert's
+  bool bad = false;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = lane + 64 * i;
-      l[i] = e < n_expert ? logits[t * n_expert + e] : -INFINITY;
-      bad |= l[i] != l[i] || l[i] == INFINITY;
-      const double big = 1e300;
-      double c = l[i] > -big ? (l[i] < big ? l[i] : big) : -big;  // NaN: lowest
-      if (l[i] == INFINITY) c = big;
-      c += 0.0;  // -0 and 0 are equal
-      unsigned long long bits = __builtin_bit_cast(unsigned long long, c);
-      bits = (bits & ~255ull) | (unsigned long long)((bits >> 63) ? e : 255 - e);
-      key[i] = e < n_expert ? __builtin_bit_cast(double, bits) : -INFINITY;
+  for (int i = 0; i < PER; ++i) {
+    const int e = lane + 64 * i;
+    l[i] = e < n_expert ? logits[e] : -INFINITY;
+    bad |= l[i] != l[i] || l[i] == INFINITY;
+    const uint32_t bits = __builtin_bit_cast(uint32_t, l[i] + 0.f);  // -0 and 0 are equal
+    key[i] = (bits >> 31) ? ~bits : bits | 0x80000000u;
+    if (l[i] != l[i]) key[i] = 1u;
+    if (e >= n_expert) key[i] = 0u;
+  }
+  const bool nan_row = __ballot(bad) != 0;
+  uint32_t my_key = 0, top_key = 0;
+  if constexpr (PER == 1) {
+    // An expert's place is the number of experts before it: larger keys, and equal ones of
+    // lower number.  (No round waits for the one before: 8 choices of 64 experts for 16
+    // tokens in well under a microsecond.)
+    int place = 0;
+    for (int e0 = 0; e0 < n_expert; e0 += 8) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int e = e0 + k;  // past n_expert the keys are 0
+        const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)key[0], e);
+        place += other > key[0] || (other == key[0] && e < lane);
+      }
     }
-    const bool nan_row = __ballot(bad) != 0;
-    double top = 0.;
-    float chosen = 0.f, mine = 0.f;
-    int my_id = 0;
+    // lane j fetches the key and number of the expert in place j
+    const bool in = lane < n_expert && place < top_k;
+    const int dest = in ? place : 63;
+    my_key = (uint32_t)__builtin_amdgcn_ds_permute(4 * dest, (int)(in ? key[0] : 0u));
+    my_id = __builtin_amdgcn_ds_permute(4 * dest, in ? lane : 0);
+    top_key = (uint32_t)__builtin_amdgcn_readlane((int)my_key, 0);
+  } else {
     for (int j = 0; j < top_k; ++j) {
-      double best = key[0];
+      uint32_t best = key[0];
 #pragma unroll
-      for (int i = 1; i < PER; ++i) best = key[i] > best ? key[i] : best;
+      for (int i = 1; i < PER; ++i) best = max(best, key[i]);
       best = wave_max(best);
-      if (j == 0) top = best;
+      int id = -1;  // lowest expert with this key
 #pragma unroll
-      for (int i = 0; i < PER; ++i) key[i] = key[i] == best ? -INFINITY : key[i];
-      const unsigned long long bits = __builtin_bit_cast(unsigned long long, best);
-      const int code = (int)(bits & 255ull);
-      const float w = expf((float)(best - top));
-      chosen += w;
+      for (int i = PER - 1; i >= 0; --i) {
+        const unsigned long long has = __ballot(key[i] == best);
+        if (has) id = 64 * i + __builtin_ctzll(has);
+      }
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (id == lane + 64 * i) key[i] = 0u;
+      if (j == 0) top_key = best;
       if (lane == j) {
-        mine = w;
-        my_id = (bits >> 63) ? code : 255 - code;
+        my_key = best;
+        my_id = id;
       }
     }
-    float all = 0.f;
+  }
+  const auto value = [](uint32_t k) {
+    return __builtin_bit_cast(float, (k >> 31) ? k & 0x7fffffffu : ~k);
+  };
+  const float top = value(top_key);
+  const float mine = lane < top_k ? expf(value(my_key) - top) : 0.f;
+  float sum = mine;
+  if (!renormalize) {
+    sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) all += expf((float)(l[i] - top));
+    for (int i = 0; i < PER; ++i) sum += expf(l[i] - top);
+  }
 #pragma unroll
-    for (int d = 32; d >= 1; d /= 2) all += __shfl_xor(all, d);
-    const float sum = renormalize ? chosen : all;
-    // a row without a finite logit has no softmax
-    float w = nan_row || !(all > 0.f) ? __builtin_nanf("") : mine / sum;
-    if (lane < top_k) {
-      if (ids != nullptr) ids[t * top_k + lane] = my_id;
-      w *= routed_scale;
-      if (weights != nullptr) weights[t * top_k + lane] = w;
-      w_lds[my_id][t] = w;
-      atomicOr(&mask_lds[my_id], 1u << t);
+  for (int d = 32; d >= 1; d /= 2) sum += __shfl_xor(sum, d);
+  // no softmax of a row with NaN, or without a logit above -inf
+  my_w = nan_row || !(sum > 0.f) ? __builtin_nanf("") : mine / sum * routed_scale;
+}
+
+struct RouteArgs {
+  const float* logits;
+  Route* route;
+  int32_t* ids;
+  float* weights;
+  int tokens, n_expert, top_k, renormalize, slots;  // slots: of the next kernels' grids
+  float routed_scale;
+};
+
+// One work-group, a wave per token.  PER: 64 experts for each lane of a wave, 1 or 4.
+template <int PER>
+__global__ __launch_bounds__(kMaxT * 64) void route_kernel(RouteArgs p) {
+  __shared__ uint32_t mask_lds[kMaxE];
+  __shared__ uint8_t slot_of[kMaxE];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  for (int i = tid; i < kMaxE; i += blockDim.x) mask_lds[i] = 0;
+  __syncthreads();
+  int id = 0;  // lane j of wave t: token t's j-th choice
+  const bool mine = wave < p.tokens && lane < p.top_k;
+  const int pair = wave * p.top_k + lane;
+  if (wave < p.tokens) {
+    float w = 0.f;
+    token_top_k<PER>(p.logits + wave * p.n_expert, p.n_expert, p.top_k, p.renormalize, p.routed_scale, lane, id, w);
+    if (mine) {
+      atomicOr(&mask_lds[id], 1u << wave);
+      p.route->w[pair] = w;
+      if (p.ids != nullptr) p.ids[pair] = id;
+      if (p.weights != nullptr) p.weights[pair] = w;
     }
   }
   __syncthreads();
-  // Thread e of the first waves: expert e's slot and first row, counted over lower experts.
-  uint32_t m = 0;
-  int slot = 0, off = 0;
-  if (tid < kMaxE) {
-    m = mask_lds[tid];
-    const unsigned long long below = (1ull << lane) - 1;
-    const unsigned long long act = __ballot(m != 0);
-    slot = __popcll(act & below);
-    int rows = 0;
-#pragma unroll
-    for (int i = 0; i < kMaxT; ++i) {
-      const unsigned long long has = __ballot((m >> i) & 1u);
-      off += __popcll(has & below);
-      rows += __popcll(has);
-    }
-    if (lane == 0) {
-      total_lds[t][0] = __popcll(act);
-      total_lds[t][1] = rows;
-    }
-  }
-  __syncthreads();
-  if (tid < kMaxE) {
-    int active = 0;
+  if (wave == 0) {
+    int slots = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      if (i < t) {
-        slot += total_lds[i][0];
-        off += total_lds[i][1];
+      const uint32_t m = mask_lds[64 * i + lane];
+      const unsigned long long act = __ballot(m != 0);
+      const int slot = slots + __popcll(act & ((1ull << lane) - 1));
+      slots += __popcll(act);
+      if (m != 0) {
+        slot_of[64 * i + lane] = (uint8_t)slot;
+        p.route->slot[slot].expert = 64 * i + lane;
+        p.route->slot[slot].rows = __popc(m);
       }
-      active += total_lds[i][0];
     }
-    if (tid == 0) route->n_active = active;
-    if (m != 0) {
-      route->expert[slot] = tid;
-      route->mask[slot] = m;
-      route->off[slot] = off;
-#pragma unroll
-      for (int i = 0; i < kMaxT; i += 4)
-        *reinterpret_cast<f32x4*>(&route->w[slot][i]) =
-            *reinterpret_cast<const f32x4*>(&w_lds[tid][i]);
-    }
+    for (int i = slots + lane; i < p.slots; i += 64) p.route->slot[i].rows = 0;
   }
+  __syncthreads();
+  if (mine)  // the expert's rows lie in token order
+    p.route->slot[slot_of[id]].pair[__popc(mask_lds[id] & ((1u << wave) - 1))] =
+        (uint32_t)pair | (uint32_t)wave << 16;
 }
 
 // ---- the quantized products ------------------------------------------------------------
+
+// bf16 has no packed subtract, so its codes enter the products as 128 + q (one mask-and-or a
+// pair) and (128 + z) times the rows' sums is taken off each unit's partial; the sums are a
+// product with ones, on a matrix unit that has the time.  fp16 codes are made exact.
+template <bool BF16, bool W8>
+constexpr bool kBiased = BF16 && !W8;
+
+// The sums of a 128-row chunk of activations over each scale unit, as the products lay them.
+template <bool BF16, bool W8, int GPC>
+struct RowSums {
+  f32x4 v[kBiased<BF16, W8> ? GPC : 1];
+
+  __device__ __forceinline__ void form(const f16x8* a, int lane) {
+    if constexpr (kBiased<BF16, W8>) {
+      using A = Act<true>;
+      const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+      const u32x4 one_bits = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+      const bf16x8 ones = __builtin_bit_cast(bf16x8, one_bits), none{};
+      if constexpr (GPC <= 4) {
+#pragma unroll
+        for (int u = 0; u < GPC; ++u) {
+          v[u] = zero;
+#pragma unroll
+          for (int j = 4 / GPC * u; j < 4 / GPC * (u + 1); ++j) v[u] = A::mfma16(a[j], ones, v[u]);
+        }
+      } else {
+        const bool second = lane >= 32;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[2 * j] = A::mfma16(a[j], second ? none : ones, zero);
+          v[2 * j + 1] = A::mfma16(a[j], second ? ones : none, zero);
+        }
+      }
+    }
+  }
+};
 
 // One 128-row chunk of a 16-column block as its wave holds it: codes, scales, zero points.
 template <bool BF16, bool W8, bool ZP, int GPC>
 struct Chunk {
   using A = Act<BF16>;
+  using Sums = RowSums<BF16, W8, GPC>;
   u32x4 w[W8 ? 2 : 1];
   uint16_t s[GPC];
   u32x2 z[ZP ? GPC : 1];
@@ -253,180 +311,164 @@ struct Chunk {
   }
 
   // acc += (16 rows of A, four 32-row steps) x chunk
-  __device__ __forceinline__ void multiply(const f16x8* a, int lane, f32x4& acc) const {
+  __device__ __forceinline__ void multiply(const f16x8* a, const Sums& sums, int lane,
+                                           f32x4& acc) const {
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-    const auto add = [&](uint16_t scale, f32x4 part) {
-      const float f = A::value(scale);
+    const auto code = [&](int u) { return ZP ? zero_code(z[ZP ? u : 0], lane & 15) : 8; };
+    const auto add = [&](int u, f32x4 part) {
+      const float f = A::value(s[u]);
+      if constexpr (kBiased<BF16, W8>) {
+        const float excess = (float)(128 + code(u));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) part[e] = __builtin_fmaf(-excess, sums.v[u][e], part[e]);
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(f, part[e], acc[e]);
     };
-    const auto offsets = [&](int u) { return A::zero(ZP ? zero_code(z[ZP ? u : 0], lane & 15) : 8); };
     if constexpr (W8) {
       f32x4 p = zero;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         p = A::mfma16(a[j], A::fp8(w[j / 2][2 * (j % 2)], w[j / 2][2 * (j % 2) + 1]), p);
-      add(s[0], p);
-    } else if constexpr (GPC <= 4) {
-      const auto mr = A::magic();
-      constexpr int JQ = 4 / GPC;
-#pragma unroll
-      for (int u = 0; u < GPC; ++u) {
-        const auto zo = offsets(u);
-        f32x4 p = zero;
-#pragma unroll
-        for (int j = JQ * u; j < JQ * (u + 1); ++j)
-          p = A::mfma16(a[j], A::dequant(w[0][j], zo, mr), p);
-        add(s[u], p);
-      }
+      add(0, p);
     } else {
-      // 16-row units: lanes 0-31 hold a step's first unit, lanes 32-63 its second; each unit
-      // has its product, the other half's weights set to zero
-      const auto mr = A::magic();
-      const bool second = lane >= 32;
-      const typename A::W8 none{};
+      // the weights of step j, as unit u's zero point makes them
+      const auto weights = [&](int j, int u) -> typename A::W8 {
+        if constexpr (BF16)
+          return dequant8_bf_biased(w[0][j], magic_reg_bf128());
+        else
+          return A::dequant(w[0][j], A::zero(code(u)), A::magic());
+      };
+      if constexpr (GPC <= 4) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const auto z0 = offsets(2 * j), z1 = offsets(2 * j + 1);
-        const typename A::W8 q = second ? A::dequant(w[0][j], z1, mr) : A::dequant(w[0][j], z0, mr);
-        add(s[2 * j], A::mfma16(a[j], second ? none : q, zero));
-        add(s[2 * j + 1], A::mfma16(a[j], second ? q : none, zero));
+        for (int u = 0; u < GPC; ++u) {
+          f32x4 p = zero;
+#pragma unroll
+          for (int j = 4 / GPC * u; j < 4 / GPC * (u + 1); ++j)
+            p = A::mfma16(a[j], weights(j, u), p);
+          add(u, p);
+        }
+      } else {
+        // 16-row units: lanes 0-31 hold a step's first unit, lanes 32-63 its second; each
+        // unit has its product, the other half's weights set to zero
+        const bool second = lane >= 32;
+        const typename A::W8 none{};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const typename A::W8 q0 = weights(j, 2 * j), q1 = weights(j, 2 * j + 1);
+          add(2 * j, A::mfma16(a[j], second ? none : q0, zero));
+          add(2 * j + 1, A::mfma16(a[j], second ? q1 : none, zero));
+        }
       }
     }
   }
 };
 
-__device__ __forceinline__ void load_rows(const uint16_t* row_at, int g, f16x8* a) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    a[j] = *reinterpret_cast<const f16x8*>(row_at + (long)g * kGroup + 32 * j);
-}
+struct ProductArgs {
+  const uint16_t* a;  // x, rows by token; or the activation, rows by pair
+  Bank bank;
+  const Route* route;
+  uint16_t* h;   // GATE_UP: the activation [pair][inter]
+  float* part;   // else: fp32 rows [pair][hidden]
+  long lda;
+  int groups, n;  // n: columns of a row of the output
+};
 
-constexpr int kGuWaves = 8;
-constexpr int kGuUnroll = 2;
-
-template <bool BF16, bool W8, bool ZP, int GPC>
-__global__ __launch_bounds__(kGuWaves * 64) void gate_up_kernel(
-    const uint16_t* __restrict__ x, int ldx, Bank bank, const Route* __restrict__ route,
-    int groups, int inter, uint16_t* __restrict__ h) {
+// Two neighbouring 16-column blocks of a slot's expert.  The waves take 128-row groups in
+// turn; a lane's activation rows serve both blocks (as loads they would take as long as the
+// weights do for one).
+template <bool GATE_UP, bool BF16, bool W8, bool ZP, int GPC, int WAVES, int U>
+__global__ __launch_bounds__(WAVES * 64) void product_kernel(ProductArgs p) {
   using A = Act<BF16>;
   using C = Chunk<BF16, W8, ZP, GPC>;
-  __shared__ f32x4 red[2][kGuWaves][64];
-  const int slot = blockIdx.y;
-  if (slot >= route->n_active) return;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const long expert = route->expert[slot];
-  const uint32_t mask = route->mask[slot];
-  const int off = route->off[slot];
-  const int rows = __popc(mask);
-  const u32x4* b = bank.b + expert * bank.b_stride;
-  const uint16_t* s = bank.s + expert * bank.s_stride;
-  const u32x2* z = ZP ? bank.z + expert * bank.z_stride : nullptr;
-
-  // Row r of the block is the slot's r-th token; rows past the last repeat the first.
-  uint32_t rest = mask;
-  for (int i = 0; i < (lane & 15) && (lane & 15) < rows; ++i) rest &= rest - 1;
-  const int token = __ffs(rest) - 1;
-  const uint16_t* xp = x + (long)token * ldx + 8 * (lane >> 4);
-
-  const long gate0 = 2L * blockIdx.x * groups, up0 = gate0 + groups;
-  f32x4 gate = {0.f, 0.f, 0.f, 0.f}, up = gate;
-  for (int g0 = wave; g0 < groups; g0 += kGuWaves * kGuUnroll) {
-    C cg[kGuUnroll], cu[kGuUnroll];
-    f16x8 a[kGuUnroll][4];
-#pragma unroll
-    for (int i = 0; i < kGuUnroll; ++i) {
-      const int g = min(g0 + i * kGuWaves, groups - 1);
-      cg[i].load(b, s, z, gate0 + g, lane);
-      cu[i].load(b, s, z, up0 + g, lane);
-      load_rows(xp, g, a[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < kGuUnroll; ++i) {
-      if (g0 + i * kGuWaves >= groups) continue;
-      cg[i].multiply(a[i], lane, gate);
-      cu[i].multiply(a[i], lane, up);
-    }
-  }
-  red[0][wave][lane] = gate;
-  red[1][wave][lane] = up;
-  __syncthreads();
-  if (wave >= 4) return;
-  // wave e sums element e of the lane's block, in wave order
-  const int e = wave, r = 4 * (lane >> 4) + e;
-  float gs = 0.f, us = 0.f;
-#pragma unroll
-  for (int w = 0; w < kGuWaves; ++w) {
-    gs += reinterpret_cast<const float*>(&red[0][w][lane])[e];
-    us += reinterpret_cast<const float*>(&red[1][w][lane])[e];
-  }
-  if (r < rows) h[(long)(off + r) * inter + 16 * blockIdx.x + (lane & 15)] = A::round(silu_times(gs, us));
-}
-
-constexpr int kDnWaves = 16;
-constexpr int kDnUnroll = 4;
-
-template <bool BF16, bool W8, bool ZP, int GPC>
-__global__ __launch_bounds__(kDnWaves * 64) void down_kernel(
-    const uint16_t* __restrict__ h, Bank bank, const Route* __restrict__ route, int groups,
-    int inter, const uint16_t* residual, int ldr, uint16_t* y, int ldy, int tokens) {
-  using A = Act<BF16>;
-  using C = Chunk<BF16, W8, ZP, GPC>;
-  __shared__ f32x4 red[kDnWaves][64];
+  __shared__ f32x4 red[2][WAVES][64];
+  const RouteSlot& slot = p.route->slot[blockIdx.y];
+  const int expert = slot.expert, rows = slot.rows;
+  if (rows == 0) return;  // past the last chosen expert
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row = lane & 15, qd = lane >> 4;
-  const long block0 = (long)blockIdx.x * groups;
+  const uint32_t row_pair = slot.pair[row];  // (not written past the slot's rows)
+  // rows past the last repeat the first (and are not stored)
+  // (read from the first lane by the whole wave, not inside the choice between the two)
+  const uint32_t first_pair = (uint32_t)__builtin_amdgcn_readfirstlane((int)row_pair);
+  const uint32_t pair = row < rows ? row_pair : first_pair;
+  const uint16_t* ap = p.a + (GATE_UP ? pair >> 16 : pair & 0xffffu) * p.lda + 8 * qd;
+  const u32x4* b = p.bank.b + expert * p.bank.b_stride;
+  const uint16_t* s = p.bank.s + expert * p.bank.s_stride;
+  const u32x2* z = ZP ? p.bank.z + expert * p.bank.z_stride : nullptr;
 
-  // (slot, group) items in slot order; each wave takes a run of them
-  const int items = route->n_active * groups;
-  int i = (int)((long)items * wave / kDnWaves);
-  const int last = (int)((long)items * (wave + 1) / kDnWaves);
-  f32x4 total = {0.f, 0.f, 0.f, 0.f};
-  while (i < last) {
-    const int slot = i / groups;
-    const int g1 = min(last - slot * groups, groups);
-    const long expert = route->expert[slot];
-    const uint32_t mask = route->mask[slot];
-    const f32x4 w = *reinterpret_cast<const f32x4*>(&route->w[slot][4 * qd]);
-    const u32x4* b = bank.b + expert * bank.b_stride;
-    const uint16_t* s = bank.s + expert * bank.s_stride;
-    const u32x2* z = ZP ? bank.z + expert * bank.z_stride : nullptr;
-    // Row t of the block is token t; a token without this expert reads the slot's first row
-    // (its sums are left out below).
-    const int r = (mask >> row) & 1u ? __popc(mask & ((1u << row) - 1)) : 0;
-    const uint16_t* hp = h + (long)(route->off[slot] + r) * inter + 8 * qd;
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    for (int g0 = i - slot * groups; g0 < g1; g0 += kDnUnroll) {
-      C c[kDnUnroll];
-      f16x8 a[kDnUnroll][4];
+  const long block0 = 2L * blockIdx.x * p.groups, block1 = block0 + p.groups;
+  f32x4 acc0 = {0.f, 0.f, 0.f, 0.f}, acc1 = acc0;
+  for (int g0 = wave; g0 < p.groups; g0 += WAVES * U) {
+    C c0[U], c1[U];
+    f16x8 a[U][4];
 #pragma unroll
-      for (int k = 0; k < kDnUnroll; ++k) {
-        const int g = min(g0 + k, g1 - 1);
-        c[k].load(b, s, z, block0 + g, lane);
-        load_rows(hp, g, a[k]);
-      }
+    for (int i = 0; i < U; ++i) {
+      const int g = min(g0 + i * WAVES, p.groups - 1);
+      c0[i].load(b, s, z, block0 + g, lane);
+      c1[i].load(b, s, z, block1 + g, lane);
 #pragma unroll
-      for (int k = 0; k < kDnUnroll; ++k)
-        if (g0 + k < g1) c[k].multiply(a[k], lane, acc);
+      for (int j = 0; j < 4; ++j)
+        a[i][j] = *reinterpret_cast<const f16x8*>(ap + (long)g * kGroup + 32 * j);
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      total[e] = (mask >> (4 * qd + e)) & 1u ? __builtin_fmaf(w[e], acc[e], total[e]) : total[e];
-    i = slot * groups + g1;
+    for (int i = 0; i < U; ++i) {
+      if (g0 + i * WAVES >= p.groups) continue;
+      typename C::Sums sums;
+      sums.form(a[i], lane);
+      c0[i].multiply(a[i], sums, lane, acc0);
+      c1[i].multiply(a[i], sums, lane, acc1);
+    }
   }
-  red[wave][lane] = total;
+  red[0][wave][lane] = acc0;
+  red[1][wave][lane] = acc1;
   __syncthreads();
   if (wave >= 4) return;
-  const int e = wave, t = 4 * qd + e;
-  if (t >= tokens) return;
-  float sum = 0.f;
+  // wave e sums element e of the lane's two blocks, in wave order
+  const int r = 4 * qd + wave;
+  float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-  for (int k = 0; k < kDnWaves; ++k) sum += reinterpret_cast<const float*>(&red[k][lane])[e];
-  const long col = 16L * blockIdx.x + row;
-  if (residual != nullptr) sum += A::value(residual[(long)t * ldr + col]);
-  y[(long)t * ldy + col] = A::round(sum);
+  for (int w = 0; w < WAVES; ++w) {
+    s0 += reinterpret_cast<const float*>(&red[0][w][lane])[wave];
+    s1 += reinterpret_cast<const float*>(&red[1][w][lane])[wave];
+  }
+  const long out = (long)(__shfl(pair, r) & 0xffffu) * p.n;
+  if (r >= rows) return;
+  if constexpr (GATE_UP) {
+    p.h[out + 16 * blockIdx.x + row] = A::round(silu_times(s0, s1));
+  } else {
+    p.part[out + 32 * blockIdx.x + row] = s0;
+    p.part[out + 32 * blockIdx.x + 16 + row] = s1;
+  }
+}
+
+// y[t] = residual[t] + sum over the token's choices j of w_j part[t][j], 4 columns a thread.
+template <bool BF16>
+__global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ part,
+                                                      const Route* __restrict__ route, int top_k,
+                                                      int hidden, const uint16_t* residual,
+                                                      int ldr, uint16_t* y, int ldy) {
+  using A = Act<BF16>;
+  const int col = 4 * (blockIdx.x * 256 + threadIdx.x);
+  const int t = blockIdx.y;
+  if (col >= hidden) return;
+  u32x2 res = {0u, 0u};
+  if (residual != nullptr) res = *reinterpret_cast<const u32x2*>(residual + (long)t * ldr + col);
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int j = 0; j < top_k; ++j) {
+    const float w = route->w[t * top_k + j];
+    const f32x4 v = *reinterpret_cast<const f32x4*>(part + (long)(t * top_k + j) * hidden + col);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(w, v[e], sum[e]);
+  }
+  uint32_t out[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    out[e] = A::round(sum[e] + A::value((uint16_t)(res[e / 2] >> (16 * (e % 2)))));
+  *reinterpret_cast<u32x2*>(y + (long)t * ldy + col) =
+      u32x2{out[0] | out[1] << 16, out[2] | out[3] << 16};
 }
 
 int max_slots(int tokens, int n_expert, int top_k) {
@@ -440,56 +482,61 @@ Bank bank_of(const wq_expert_bank& b) {
 }
 
 struct MoeScratch {
-  double* logits;
+  float* logits;
   Route* route;
   uint16_t* h;
+  float* part;
   size_t bytes;
 };
 
-MoeScratch scratch_of(void* base, int tokens, int n_expert, int top_k, int inter) {
-  const size_t logits = round256((size_t)tokens * n_expert * sizeof(double));
+MoeScratch scratch_of(void* base, int tokens, int n_expert, int top_k, int hidden, int inter) {
+  const size_t logits = round256((size_t)tokens * n_expert * sizeof(float));
   const size_t route = round256(sizeof(Route));
+  const size_t h = round256((size_t)tokens * top_k * inter * 2);
   char* p = static_cast<char*>(base);
-  return MoeScratch{reinterpret_cast<double*>(p), reinterpret_cast<Route*>(p + logits),
+  return MoeScratch{reinterpret_cast<float*>(p), reinterpret_cast<Route*>(p + logits),
                     reinterpret_cast<uint16_t*>(p + logits + route),
-                    logits + route + round256((size_t)tokens * top_k * inter * 2)};
+                    reinterpret_cast<float*>(p + logits + route + h),
+                    logits + route + h + (size_t)tokens * top_k * hidden * sizeof(float)};
 }
 
-template <bool BF16, bool W8, bool ZP, int GPC>
-hipError_t launch_gate_up(const wq_moe_args& a, const MoeScratch& m, hipStream_t stream) {
-  const dim3 grid(a.inter / 16, max_slots(a.tokens, a.n_expert, a.top_k));
-  hipLaunchKernelGGL((gate_up_kernel<BF16, W8, ZP, GPC>), grid, dim3(kGuWaves * 64), 0, stream,
-                     static_cast<const uint16_t*>(a.x), a.ldx, bank_of(a.gate_up), m.route,
-                     a.hidden / kGroup, a.inter, m.h);
+template <bool GATE_UP, bool BF16, bool W8, bool ZP, int GPC>
+hipError_t launch_product(const wq_moe_args& a, const MoeScratch& m, hipStream_t stream) {
+  ProductArgs p{};
+  p.a = GATE_UP ? static_cast<const uint16_t*>(a.x) : m.h;
+  p.bank = bank_of(GATE_UP ? a.gate_up : a.down);
+  p.route = m.route;
+  p.h = m.h;
+  p.part = m.part;
+  p.lda = GATE_UP ? a.ldx : a.inter;
+  p.groups = (GATE_UP ? a.hidden : a.inter) / kGroup;
+  p.n = GATE_UP ? a.inter : a.hidden;
+  const dim3 grid(GATE_UP ? a.inter / 16 : a.hidden / 32,
+                  max_slots(a.tokens, a.n_expert, a.top_k));
+  constexpr int U = GPC >= 4 ? 1 : 2;  // small units' scales and zero points take the registers
+#define WQ_MOE_PRODUCT(W)                                                                      \
+  hipLaunchKernelGGL((product_kernel<GATE_UP, BF16, W8, ZP, GPC, W, U>), grid, dim3(W * 64), 0, \
+                     stream, p)
+  if (p.groups <= 8)
+    WQ_MOE_PRODUCT(4);
+  else if (p.groups <= 64)
+    WQ_MOE_PRODUCT(8);
+  else
+    WQ_MOE_PRODUCT(16);
+#undef WQ_MOE_PRODUCT
   return hipGetLastError();
 }
 
-template <bool BF16, bool W8, bool ZP, int GPC>
-hipError_t launch_down(const wq_moe_args& a, const MoeScratch& m, hipStream_t stream) {
-  hipLaunchKernelGGL((down_kernel<BF16, W8, ZP, GPC>), dim3(a.hidden / 16), dim3(kDnWaves * 64),
-                     0, stream, m.h, bank_of(a.down), m.route, a.inter / kGroup, a.inter,
-                     static_cast<const uint16_t*>(a.residual), a.ldr,
-                     static_cast<uint16_t*>(a.y), a.ldy, a.tokens);
-  return hipGetLastError();
-}
-
-template <bool BF16, bool W8, bool ZP, int GPC>
-hipError_t launch_product(bool down, const wq_moe_args& a, const MoeScratch& m,
-                          hipStream_t stream) {
-  return down ? launch_down<BF16, W8, ZP, GPC>(a, m, stream)
-              : launch_gate_up<BF16, W8, ZP, GPC>(a, m, stream);
-}
-
-template <bool BF16>
-hipError_t launch_product_type(bool down, int gpc, const wq_moe_args& a, const MoeScratch& m,
+template <bool GATE_UP, bool BF16>
+hipError_t launch_product_type(int gpc, const wq_moe_args& a, const MoeScratch& m,
                                hipStream_t stream) {
-  if (a.flags & WQ_FLAG_FP8) return launch_product<BF16, true, false, 1>(down, a, m, stream);
+  if (a.flags & WQ_FLAG_FP8) return launch_product<GATE_UP, BF16, true, false, 1>(a, m, stream);
   const bool zp = (a.flags & WQ_FLAG_HAS_ZP) != 0;
   switch (gpc) {
-#define WQ_MOE_GPC(G)                                                            \
-  case G:                                                                        \
-    return zp ? launch_product<BF16, false, true, G>(down, a, m, stream)         \
-              : launch_product<BF16, false, false, G>(down, a, m, stream)
+#define WQ_MOE_GPC(G)                                                             \
+  case G:                                                                         \
+    return zp ? launch_product<GATE_UP, BF16, false, true, G>(a, m, stream)       \
+              : launch_product<GATE_UP, BF16, false, false, G>(a, m, stream)
     WQ_MOE_GPC(1);
     WQ_MOE_GPC(2);
     WQ_MOE_GPC(4);
@@ -499,38 +546,53 @@ hipError_t launch_product_type(bool down, int gpc, const wq_moe_args& a, const M
   }
 }
 
+template <bool BF16>
+hipError_t launch_route(const wq_moe_args& a, const MoeScratch& m, hipStream_t stream) {
+  hipLaunchKernelGGL((router_kernel<BF16>), dim3(a.n_expert, (a.tokens + 3) / 4),
+                     dim3(kRouterThreads), 0, stream, static_cast<const uint16_t*>(a.x), a.ldx,
+                     static_cast<const uint16_t*>(a.router), a.tokens, a.n_expert, a.hidden,
+                     m.logits);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const RouteArgs p{m.logits,   m.route, a.ids,         a.weights,
+                    a.tokens,   a.n_expert, a.top_k,    a.renormalize,
+                    max_slots(a.tokens, a.n_expert, a.top_k), a.routed_scale};
+  const dim3 block(64 * a.tokens);
+  if (a.n_expert <= 64)
+    hipLaunchKernelGGL((route_kernel<1>), dim3(1), block, 0, stream, p);
+  else
+    hipLaunchKernelGGL((route_kernel<kMaxE / 64>), dim3(1), block, 0, stream, p);
+  return hipGetLastError();
+}
+
+template <bool BF16>
+hipError_t launch_moe_type(const wq_moe_args& a, int gate_up_gpc, int down_gpc,
+                           hipStream_t stream) {
+  const MoeScratch m =
+      scratch_of(a.workspace, a.tokens, a.n_expert, a.top_k, a.hidden, a.inter);
+  hipError_t e = launch_route<BF16>(a, m, stream);
+  if (e != hipSuccess) return e;
+  e = launch_product_type<true, BF16>(gate_up_gpc, a, m, stream);
+  if (e != hipSuccess) return e;
+  e = launch_product_type<false, BF16>(down_gpc, a, m, stream);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((combine_kernel<BF16>), dim3((a.hidden + 1023) / 1024, a.tokens), dim3(256),
+                     0, stream, m.part, m.route, a.top_k, a.hidden,
+                     static_cast<const uint16_t*>(a.residual), a.ldr,
+                     static_cast<uint16_t*>(a.y), a.ldy);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 size_t moe_workspace_bytes(int tokens, int n_expert, int top_k, int hidden, int inter) {
-  (void)hidden;
-  return scratch_of(nullptr, tokens, n_expert, top_k, inter).bytes;
+  return scratch_of(nullptr, tokens, n_expert, top_k, hidden, inter).bytes;
 }
 
 hipError_t launch_moe_layer(const wq_moe_args& a, int gate_up_gpc, int down_gpc,
                             hipStream_t stream) {
-  const MoeScratch m = scratch_of(a.workspace, a.tokens, a.n_expert, a.top_k, a.inter);
-  const bool bf16 = (a.flags & WQ_FLAG_BF16) != 0;
-  const dim3 grid((a.n_expert + 3) / 4, (a.tokens + 3) / 4);
-  const uint16_t* x = static_cast<const uint16_t*>(a.x);
-  const uint16_t* r = static_cast<const uint16_t*>(a.router);
-  if (bf16)
-    hipLaunchKernelGGL((router_kernel<true>), grid, dim3(256), 0, stream, x, a.ldx, r, a.tokens,
-                       a.n_expert, a.hidden, m.logits);
-  else
-    hipLaunchKernelGGL((router_kernel<false>), grid, dim3(256), 0, stream, x, a.ldx, r, a.tokens,
-                       a.n_expert, a.hidden, m.logits);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(route_kernel, dim3(1), dim3(kMaxT * 64), 0, stream, m.logits, a.tokens,
-                     a.n_expert, a.top_k, a.renormalize, a.routed_scale, a.ids, a.weights,
-                     m.route);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  e = bf16 ? launch_product_type<true>(false, gate_up_gpc, a, m, stream)
-           : launch_product_type<false>(false, gate_up_gpc, a, m, stream);
-  if (e != hipSuccess) return e;
-  return bf16 ? launch_product_type<true>(true, down_gpc, a, m, stream)
-              : launch_product_type<false>(true, down_gpc, a, m, stream);
+  return (a.flags & WQ_FLAG_BF16) ? launch_moe_type<true>(a, gate_up_gpc, down_gpc, stream)
+                                  : launch_moe_type<false>(a, gate_up_gpc, down_gpc, stream);
 }
 
 }  // namespace wq

@@ -5,78 +5,101 @@ new token over that cache, and the mixture-of-experts layer of a few tokens.  Py
 allocates device buffers and supplies the stream; every operation is a libwq kernel.
 
 Calls run on the current stream of their tensors' device, enqueue and return; none
-synchronizes, so all of them may be captured into a graph (pass the outputs then, or keep
-what the call returns).  A plan (PagedAttention, MoELayer) owns a workspace: its calls must
-not overlap on different streams.
+synchronizes, so all of them may be captured into a graph.  A plan (PagedAttention, MoELayer)
+owns a workspace: its calls must not overlap on different streams.
+
+The arguments of a call are packed as the bytes of its C struct and checked here only where
+the library cannot see them (types, devices, shapes, strides): a call of a few microseconds on
+the GPU should not take longer than that to make.
 """
 
 from __future__ import annotations
 
+import ctypes
 import math
+import struct
 
 import torch
 
-from . import (WQ_FLAG_BF16, WQ_FLAG_FP8, WQ_FLAG_HAS_ZP, WQ_MOE_MAX_TOKENS, versioned,
-               wq_add_rms_norm, wq_attn_args, wq_expert_bank, wq_kv_cache, wq_moe_args,
-               wq_moe_layer, wq_moe_layer_workspace_bytes, wq_norm_args, wq_paged_attention,
-               wq_paged_attention_workspace_bytes, wq_rope_append, wq_rope_args)
+from . import (WQ_ABI_VERSION, WQ_FLAG_BF16, WQ_FLAG_FP8, WQ_FLAG_HAS_ZP, WQ_MAX_ROPE_AXES,
+               WQ_MOE_MAX_TOKENS, wq_add_rms_norm, wq_attn_args, wq_expert_bank, wq_kv_cache,
+               wq_moe_args, wq_moe_layer, wq_moe_layer_workspace_bytes, wq_norm_args,
+               wq_paged_attention, wq_paged_attention_workspace_bytes, wq_rope_append,
+               wq_rope_args)
 
-_FLOATS = (torch.float16, torch.bfloat16)
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(
-    torch._C, "_cuda_getCurrentRawStream") else None
-
-
-def _enqueue(call, args, device: torch.device) -> None:
-    """call(args) on the device's current stream, with that device current."""
-    index = device.index
-    if _raw_stream is None:
-        raise RuntimeError("this PyTorch build has no GPU support")
-    args.stream = _raw_stream(index)
-    if index == torch.cuda.current_device():
-        call(args)
-    else:
-        with torch.cuda.device(index):
-            call(args)
+_TYPE_FLAGS = {torch.float16: 0, torch.bfloat16: WQ_FLAG_BF16}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
-def _flag(dtype: torch.dtype) -> int:
-    if dtype is torch.float16:
-        return 0
-    if dtype is torch.bfloat16:
-        return WQ_FLAG_BF16
-    raise TypeError(f"fp16 or bf16 expected, got {dtype}")
+def _layout(cls, fields: str) -> struct.Struct:
+    """The native layout of a C argument struct after its version and size."""
+    s = struct.Struct("@II" + fields + "0P")
+    assert s.size == ctypes.sizeof(cls), cls
+    return s
 
 
-def _rows(t: torch.Tensor, name: str, dtype, device, cols: int, rows: int | None = None) -> int:
-    """The row stride of a [rows][cols] tensor, checked."""
-    if t.dtype is not dtype or t.device != device:
-        raise TypeError(f"{name}: {dtype} on {device} expected, got {t.dtype} on {t.device}")
-    shape = t.shape
-    if len(shape) != 2 or shape[1] != cols or (rows is not None and shape[0] != rows):
-        raise ValueError(f"{name}: [{rows or 'rows'}][{cols}] expected, got {tuple(shape)}")
+_CACHE = f"{ctypes.sizeof(wq_kv_cache)}s"
+_BANK = f"{ctypes.sizeof(wq_expert_bank)}s"
+_NORM = _layout(wq_norm_args, "6P6ifIi")
+_ROPE = _layout(wq_rope_args, _CACHE + "8P8i" + f"{WQ_MAX_ROPE_AXES}iiIi")
+_ATTN = _layout(wq_attn_args, _CACHE + "7PNP7iffiIi")
+_MOE = _layout(wq_moe_args, "2P" + 2 * _BANK + "5PNP8ifiIi")
+
+
+def _stream(dev: int) -> int:
+    """The current stream of GPU `dev`, which has to be the current device."""
+    if dev < 0:
+        raise TypeError("GPU tensors expected")
+    if _current_device() != dev:
+        raise ValueError(f"the tensors are on GPU {dev}, the current device is "
+                         f"{_current_device()}: call under torch.cuda.device({dev})")
+    return _raw_stream(dev)
+
+
+def _type_flag(dtype: torch.dtype) -> int:
+    flag = _TYPE_FLAGS.get(dtype)
+    if flag is None:
+        raise TypeError(f"fp16 or bf16 expected, got {dtype}")
+    return flag
+
+
+def _check_type(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int) -> None:
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise TypeError(f"{name}: {dtype} on device {dev} expected, got {t.dtype} on "
+                        f"{t.get_device()}")
+
+
+def _rows(t: torch.Tensor, name: str, dtype, dev: int, rows: int, cols: int) -> int:
+    """The row stride of a [rows][cols] tensor."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        _check_type(t, name, dtype, dev)
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name}: [{rows}][{cols}] expected, got {tuple(t.shape)}")
     ld, one = t.stride()
     if one != 1 and cols > 1:
         raise ValueError(f"{name}: its last dimension must be contiguous")
-    return ld if shape[0] > 1 else max(ld, cols)
+    return ld if rows > 1 else cols
 
 
-def _heads(t: torch.Tensor, name: str, dtype, device, rows: int, heads: int, d: int) -> int:
+def _heads(t: torch.Tensor, name: str, dtype, dev: int, rows: int, heads: int, d: int) -> int:
     """The row stride of a [rows][heads][d] tensor whose heads lie one after another."""
-    if t.dtype is not dtype or t.device != device:
-        raise TypeError(f"{name}: {dtype} on {device} expected, got {t.dtype} on {t.device}")
+    if t.dtype is not dtype or t.get_device() != dev:
+        _check_type(t, name, dtype, dev)
     if t.shape != (rows, heads, d):
         raise ValueError(f"{name}: {(rows, heads, d)} expected, got {tuple(t.shape)}")
     ld, head, one = t.stride()
-    if one != 1 or (heads > 1 and head != d):
+    if one != 1 or (head != d and heads > 1):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return ld if rows > 1 else max(ld, heads * d)
+    return ld if rows > 1 else heads * d
 
 
-def _index(t: torch.Tensor, name: str, dtype, device, shape) -> int:
-    if t.dtype is not dtype or t.device != device:
-        raise TypeError(f"{name}: {dtype} on {device} expected, got {t.dtype} on {t.device}")
+def _dense(t: torch.Tensor, name: str, dtype, dev: int, shape: tuple) -> int:
+    """The address of a contiguous tensor of this shape."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        _check_type(t, name, dtype, dev)
     if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: contiguous {tuple(shape)} expected, got {tuple(t.shape)}")
+        raise ValueError(f"{name}: contiguous {shape} expected, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
@@ -86,31 +109,35 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *,
     """(y, s) of [rows][n] tensors: s = x + delta, y = s / sqrt(mean(s^2) + eps) * weight.
     Without delta, s is x itself.  sum_out may be x or delta (the residual stream kept in
     place), out likewise, but not both the same."""
-    if x.dtype not in _FLOATS:
-        raise TypeError(f"fp16 or bf16 expected, got {x.dtype}")
-    if x.dim() != 2:
-        raise ValueError(f"x: two dimensions expected, got {tuple(x.shape)}")
-    rows, n = x.shape
-    dtype, device = x.dtype, x.device
+    dtype, dev = x.dtype, x.get_device()
+    flags = _type_flag(dtype)
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x: two dimensions expected, got {tuple(shape)}")
+    rows, n = shape
+    ldx = _rows(x, "x", dtype, dev, rows, n)
+    w = _dense(weight, "weight", dtype, dev, (n,))
+    ldy = n
     if out is None:
-        out = torch.empty((rows, n), dtype=dtype, device=device)
-    args = versioned(wq_norm_args, x=x.data_ptr(), y=out.data_ptr(),
-                     weight=_index(weight, "weight", dtype, device, (n,)), rows=rows, n=n,
-                     ldx=_rows(x, "x", dtype, device, n), eps=eps, flags=_flag(dtype),
-                     ldy=_rows(out, "out", dtype, device, n, rows))
+        out = torch.empty_like(x)
+    else:
+        ldy = _rows(out, "out", dtype, dev, rows, n)
+    dp = sp = ldd = lds = 0
+    s = x
     if delta is not None:
+        dp, ldd, lds = delta.data_ptr(), _rows(delta, "delta", dtype, dev, rows, n), n
         if sum_out is None:
-            sum_out = torch.empty((rows, n), dtype=dtype, device=device)
-        args.delta, args.ldd = delta.data_ptr(), _rows(delta, "delta", dtype, device, n, rows)
-        args.sum_out, args.lds = (sum_out.data_ptr(),
-                                  _rows(sum_out, "sum_out", dtype, device, n, rows))
+            s = torch.empty_like(x)
+        else:
+            s, lds = sum_out, _rows(sum_out, "sum_out", dtype, dev, rows, n)
+        sp = s.data_ptr()
     elif sum_out is not None:
         raise ValueError("sum_out needs delta")
-    else:
-        sum_out = x
     if rows:
-        _enqueue(wq_add_rms_norm, args, device)
-    return out, sum_out
+        wq_add_rms_norm(_NORM.pack(WQ_ABI_VERSION, _NORM.size, x.data_ptr(), dp, w, sp,
+                                   out.data_ptr(), _stream(dev), rows, n, ldx, ldd, lds, ldy, eps,
+                                   flags, 0))
+    return out, s
 
 
 class PagedCache:
@@ -126,25 +153,25 @@ class PagedCache:
         if k.dtype != v.dtype or k.device != v.device:
             raise TypeError("K and V differ in type or device")
         self.fp8 = k.dtype is torch.float8_e4m3fn
-        if not self.fp8 and k.dtype not in _FLOATS:
-            raise TypeError(f"fp16, bf16 or float8_e4m3fn expected, got {k.dtype}")
+        if not self.fp8:
+            _type_flag(k.dtype)
         if k.stride(3) != 1:
             raise ValueError("the elements of a head must be contiguous")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.dtype, self.device = k.dtype, k.device
+        self.dtype, self.device, self.dev = k.dtype, k.device, k.get_device()
         self.num_pages, self.page_size, self.kv_heads, self.head_dim = k.shape
         for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
             if s is not None:
                 if not self.fp8:
                     raise ValueError(f"{name}: only an E4M3 cache has scales")
-                _index(s, name, torch.float32, self.device, (self.kv_heads,))
+                _dense(s, name, torch.float32, self.dev, (self.kv_heads,))
         strides = [k.stride(i) if k.shape[i] > 1 else 0 for i in range(3)]
-        self.args = wq_kv_cache(
+        self.packed = bytes(wq_kv_cache(
             k=k.data_ptr(), v=v.data_ptr(),
             k_scale=None if k_scale is None else k_scale.data_ptr(),
             v_scale=None if v_scale is None else v_scale.data_ptr(), page_stride=strides[0],
             slot_stride=strides[1], head_stride=strides[2], num_pages=self.num_pages,
-            page_size=self.page_size, kv_heads=self.kv_heads, head_dim=self.head_dim)
+            page_size=self.page_size, kv_heads=self.kv_heads, head_dim=self.head_dim))
 
     @classmethod
     def empty(cls, num_pages: int, page_size: int, kv_heads: int, head_dim: int,
@@ -154,11 +181,13 @@ class PagedCache:
                             device=device).transpose(1, 2) for _ in range(2))
         return cls(k, v, k_scale, v_scale)
 
-    def check_type(self, dtype: torch.dtype) -> int:
+    def flags(self, dtype: torch.dtype) -> int:
         """The flags of a call whose q (or k and v) have this type."""
-        if not self.fp8 and dtype is not self.dtype:
+        if self.fp8:
+            return _type_flag(dtype) | WQ_FLAG_FP8
+        if dtype is not self.dtype:
             raise TypeError(f"the cache holds {self.dtype}, the call's tensors are {dtype}")
-        return _flag(dtype) | (WQ_FLAG_FP8 if self.fp8 else 0)
+        return _type_flag(dtype)
 
 
 def rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: PagedCache,
@@ -170,50 +199,52 @@ def rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache:
     positions[axis(i)][token] * inv_freq[i]: positions int32 [axes][tokens] (or [tokens]),
     inv_freq fp32 [rot / 2] (None or empty: no rotation), sections the number of pairs of each
     axis.  Returns the rotated q (q_out, which may be q; a new tensor by default)."""
+    dtype, dev, d, kv_heads = k.dtype, cache.dev, cache.head_dim, cache.kv_heads
+    flags = cache.flags(dtype)
     tokens = k.shape[0]
-    dtype, device, d = k.dtype, k.device, cache.head_dim
-    if device != cache.device:
-        raise TypeError(f"the cache is on {cache.device}, k on {device}")
-    args = versioned(wq_rope_args, cache=cache.args, k=k.data_ptr(), v=v.data_ptr(),
-                     ldk=_heads(k, "k", dtype, device, tokens, cache.kv_heads, d),
-                     ldv=_heads(v, "v", dtype, device, tokens, cache.kv_heads, d),
-                     slots=_index(slots, "slots", torch.int64, device, (tokens,)),
-                     tokens=tokens, axes=1, interleaved=int(interleaved),
-                     flags=cache.check_type(dtype))
+    ldk = _heads(k, "k", dtype, dev, tokens, kv_heads, d)
+    ldv = _heads(v, "v", dtype, dev, tokens, kv_heads, d)
+    sl = _dense(slots, "slots", torch.int64, dev, (tokens,))
+    qp = qo = heads = ldq = ldqo = 0
     if q is not None:
         heads = q.shape[1]
+        ldq = _heads(q, "q", dtype, dev, tokens, heads, d)
         if q_out is None:
-            q_out = torch.empty((tokens, heads, d), dtype=dtype, device=device)
-        args.q, args.q_out, args.q_heads = q.data_ptr(), q_out.data_ptr(), heads
-        args.ldq = _heads(q, "q", dtype, device, tokens, heads, d)
-        args.ldqo = _heads(q_out, "q_out", dtype, device, tokens, heads, d)
+            q_out = torch.empty_like(q)
+        ldqo = _heads(q_out, "q_out", dtype, dev, tokens, heads, d)
+        qp, qo = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    if inv_freq is not None and inv_freq.numel():
+    half = pp = fp = 0
+    axes, pairs = 1, [0, 0, 0, 0]
+    if inv_freq is not None:
         half = inv_freq.numel()
+    if half:
         if positions is None:
             raise ValueError("inv_freq needs positions")
-        axes = 1 if positions.dim() == 1 else positions.shape[0]
+        shape = positions.shape
+        axes = 1 if len(shape) == 1 else shape[0]
         if sections is None:
             if axes != 1:
                 raise ValueError("several axes need sections")
             sections = (half,)
-        if len(sections) != axes or axes > len(args.sections):
+        if len(sections) != axes or axes > WQ_MAX_ROPE_AXES:
             raise ValueError(f"{axes} axes of positions, {len(sections)} sections")
-        args.rot_dim, args.axes = 2 * half, axes
-        for i, pairs in enumerate(sections):
-            args.sections[i] = pairs
-        args.inv_freq = _index(inv_freq, "inv_freq", torch.float32, device, (half,))
-        args.positions = _index(positions, "positions", torch.int32, device,
-                                (tokens,) if positions.dim() == 1 else (axes, tokens))
+        pairs[:axes] = sections
+        fp = _dense(inv_freq, "inv_freq", torch.float32, dev, (half,))
+        pp = _dense(positions, "positions", torch.int32, dev,
+                    (tokens,) if len(shape) == 1 else (axes, tokens))
     if tokens:
-        _enqueue(wq_rope_append, args, device)
+        wq_rope_append(_ROPE.pack(WQ_ABI_VERSION, _ROPE.size, cache.packed, qp, k.data_ptr(),
+                                  v.data_ptr(), qo, sl, pp, fp, _stream(dev), tokens, heads, ldq,
+                                  ldk, ldv, ldqo, 2 * half, axes, *pairs, int(interleaved), flags,
+                                  0))
     return q_out
 
 
 class PagedAttention:
-    """Attention of one new token for up to `batch` sequences of up to `max_len` positions
-    over a paged cache: the plan of a call and its workspace.  window: only the last that many
+    """Attention of one new token for `batch` sequences of up to `max_len` positions over a
+    paged cache: the plan of a call and its workspace.  window: only the last that many
     positions; softcap: scores become softcap * tanh(score / softcap); scale: 1/sqrt(head_dim)
     by default.  One of its calls must not overlap another on a different stream."""
 
@@ -224,14 +255,11 @@ class PagedAttention:
         self.dtype, self.device = dtype, cache.device
         nbytes = wq_paged_attention_workspace_bytes(batch, q_heads, cache.kv_heads,
                                                     cache.head_dim, max_len, window)
-        self.workspace = (torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-                          if nbytes else None)
-        self._args = versioned(
-            wq_attn_args, cache=cache.args, q_heads=q_heads, max_len=max_len, window=window,
-            softcap=softcap, flags=cache.check_type(dtype),
-            scale=1.0 / math.sqrt(cache.head_dim) if scale is None else scale,
-            workspace=None if self.workspace is None else self.workspace.data_ptr(),
-            workspace_bytes=nbytes)
+        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        self._space = (self.workspace.data_ptr(), nbytes)
+        self._lse = torch.empty((batch, q_heads), dtype=torch.float32, device=self.device)
+        scale = 1.0 / math.sqrt(cache.head_dim) if scale is None else scale
+        self._last = (scale, softcap, window, cache.flags(dtype), 0)
 
     def __call__(self, q: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor, *,
                  keep: torch.Tensor | None = None, out: torch.Tensor | None = None,
@@ -239,35 +267,36 @@ class PagedAttention:
         """q [batch][q_heads][d]; block_table int32 [batch][pages]; lens int32 [batch]; keep
         uint8 [batch][>= max_len] (0: position left out).  Returns out, or (out, lse) when lse
         is True or a fp32 [batch][q_heads] tensor to write."""
-        b, d, device = self.batch, self.cache.head_dim, self.device
-        args = wq_attn_args.from_buffer_copy(self._args)
+        cache, b, heads, dtype = self.cache, self.batch, self.q_heads, self.dtype
+        dev, d = cache.dev, cache.head_dim
+        ldq = _heads(q, "q", dtype, dev, b, heads, d)
         if out is None:
-            out = torch.empty((b, self.q_heads, d), dtype=self.dtype, device=device)
-        if lse is True:
-            lse = torch.empty((b, self.q_heads), dtype=torch.float32, device=device)
-        args.batch = b
-        args.q, args.out = q.data_ptr(), out.data_ptr()
-        args.ldq = _heads(q, "q", self.dtype, device, b, self.q_heads, d)
-        args.ldo = _heads(out, "out", self.dtype, device, b, self.q_heads, d)
-        args.table_stride = block_table.shape[-1]
-        args.block_table = _index(block_table, "block_table", torch.int32, device,
-                                  (b, block_table.shape[-1]))
-        args.lens = _index(lens, "lens", torch.int32, device, (b,))
+            out = torch.empty_like(q)
+        ldo = _heads(out, "out", dtype, dev, b, heads, d)
+        pages = block_table.shape[-1]
+        table = _dense(block_table, "block_table", torch.int32, dev, (b, pages))
+        n = _dense(lens, "lens", torch.int32, dev, (b,))
+        kp = lp = keep_stride = 0
         if keep is not None:
-            args.keep_stride = keep.shape[-1]
-            args.keep = _index(keep, "keep", torch.uint8, device, (b, keep.shape[-1]))
+            keep_stride = keep.shape[-1]
+            kp = _dense(keep, "keep", torch.uint8, dev, (b, keep_stride))
         if lse is not False:
-            args.lse = _index(lse, "lse", torch.float32, device, (b, self.q_heads))
-        _enqueue(wq_paged_attention, args, device)
+            if lse is True:
+                lse = torch.empty_like(self._lse)
+            lp = _dense(lse, "lse", torch.float32, dev, (b, heads))
+        wq_paged_attention(_ATTN.pack(WQ_ABI_VERSION, _ATTN.size, cache.packed, q.data_ptr(),
+                                      out.data_ptr(), lp, table, n, kp, *self._space,
+                                      _stream(dev), b, heads, self.max_len, pages, keep_stride,
+                                      ldq, ldo, *self._last))
         return out if lse is False else (out, lse)
 
 
-def _bank(bank) -> wq_expert_bank:
+def _bank(bank) -> bytes:
     """The C view of a torch_ops.ExpertBank."""
-    return wq_expert_bank(b=bank.b.data_ptr(), s=bank.s.data_ptr(),
-                          zp=None if bank.z is None else bank.z.data_ptr(),
-                          b_stride_bytes=bank.b_stride, s_stride_bytes=bank.s_stride,
-                          zp_stride_bytes=bank.z_stride, group_size=bank.group_size)
+    return bytes(wq_expert_bank(b=bank.b.data_ptr(), s=bank.s.data_ptr(),
+                                zp=None if bank.z is None else bank.z.data_ptr(),
+                                b_stride_bytes=bank.b_stride, s_stride_bytes=bank.s_stride,
+                                zp_stride_bytes=bank.z_stride, group_size=bank.group_size))
 
 
 class MoELayer:
@@ -289,7 +318,7 @@ class MoELayer:
         if (gate_up.bf16, gate_up.fp8, gate_up.z is None) != (down.bf16, down.fp8, down.z is None):
             raise TypeError("the two banks differ in type")
         self.dtype = torch.bfloat16 if gate_up.bf16 else torch.float16
-        self.device = gate_up.b.device
+        self.device, self.dev = gate_up.b.device, gate_up.b.get_device()
         self.gate_up, self.down, self.router, self.top_k = gate_up, down, router, top_k
         nbytes = wq_moe_layer_workspace_bytes(max_tokens, self.n_expert, top_k, self.hidden,
                                               self.inter)
@@ -297,31 +326,31 @@ class MoELayer:
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         self.ids = torch.empty((max_tokens, top_k), dtype=torch.int32, device=self.device)
         self.weights = torch.empty((max_tokens, top_k), dtype=torch.float32, device=self.device)
-        self._args = versioned(
-            wq_moe_args, gate_up=_bank(gate_up), down=_bank(down),
-            router=_index(router, "router", self.dtype, self.device,
-                          (self.n_expert, self.hidden)),
-            ids=self.ids.data_ptr(), weights=self.weights.data_ptr(),
-            workspace=self.workspace.data_ptr(), workspace_bytes=nbytes,
-            n_expert=self.n_expert, top_k=top_k, hidden=self.hidden, inter=self.inter,
-            routed_scale=routed_scale, renormalize=int(renormalize),
-            flags=_flag(self.dtype) | (WQ_FLAG_FP8 if gate_up.fp8 else 0)
-            | (WQ_FLAG_HAS_ZP if gate_up.z is not None else 0))
+        r = _dense(router, "router", self.dtype, self.dev, (self.n_expert, self.hidden))
+        self._banks = (r, _bank(gate_up), _bank(down))
+        self._space = (self.ids.data_ptr(), self.weights.data_ptr(), self.workspace.data_ptr(),
+                       nbytes)
+        self._last = (routed_scale, int(renormalize),
+                      _type_flag(self.dtype) | (WQ_FLAG_FP8 if gate_up.fp8 else 0)
+                      | (WQ_FLAG_HAS_ZP if gate_up.z is not None else 0), 0)
 
     def __call__(self, x: torch.Tensor, *, residual: torch.Tensor | None = None,
                  out: torch.Tensor | None = None) -> torch.Tensor:
         """residual + the layer's output for x [tokens][hidden] (out may be residual or x)."""
-        tokens, device = x.shape[0], self.device
+        tokens, hidden, dtype, dev = x.shape[0], self.hidden, self.dtype, self.dev
         if not 0 < tokens <= self.max_tokens:
             raise ValueError(f"1 to {self.max_tokens} tokens expected, got {tokens}")
-        args = wq_moe_args.from_buffer_copy(self._args)
+        ldx = _rows(x, "x", dtype, dev, tokens, hidden)
+        ldy = hidden
         if out is None:
-            out = torch.empty((tokens, self.hidden), dtype=self.dtype, device=device)
-        args.tokens, args.x, args.y = tokens, x.data_ptr(), out.data_ptr()
-        args.ldx = _rows(x, "x", self.dtype, device, self.hidden)
-        args.ldy = _rows(out, "out", self.dtype, device, self.hidden, tokens)
+            out = torch.empty_like(x)
+        else:
+            ldy = _rows(out, "out", dtype, dev, tokens, hidden)
+        rp = ldr = 0
         if residual is not None:
-            args.residual = residual.data_ptr()
-            args.ldr = _rows(residual, "residual", self.dtype, device, self.hidden, tokens)
-        _enqueue(wq_moe_layer, args, device)
+            rp, ldr = residual.data_ptr(), _rows(residual, "residual", dtype, dev, tokens, hidden)
+        router, gate_up, down = self._banks
+        wq_moe_layer(_MOE.pack(WQ_ABI_VERSION, _MOE.size, x.data_ptr(), router, gate_up, down, rp,
+                               out.data_ptr(), *self._space, _stream(dev), tokens, self.n_expert,
+                               self.top_k, hidden, self.inter, ldx, ldr, ldy, *self._last))
         return out

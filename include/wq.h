@@ -486,10 +486,11 @@ typedef struct wq_attn_args {
   int32_t reserved;
 } wq_attn_args;
 
-/* Workspace bytes of wq_paged_attention (0 when one work-group covers every sequence).
- * Contents need no initialization; calls that share one must not run concurrently. */
+/* Workspace bytes of wq_paged_attention (0 when one work-group covers every sequence); flags
+ * as in its arguments.  Contents need no initialization; calls that share one must not run concurrently. */
 int wq_paged_attention_workspace_bytes(int batch, int q_heads, int kv_heads, int head_dim,
-                                       int max_len, int window, size_t* bytes_out);
+                                       int max_len, int window, uint32_t flags,
+                                       size_t* bytes_out);
 
 /*
  * Attention of one new token per sequence over the paged cache: out = sum_j p_j v_j with p

@@ -115,11 +115,17 @@ def test_attention_refusals(changes, want):
 
 def test_attention_workspace():
     f = wq.wq_paged_attention_workspace_bytes
-    assert f(1, 8, 2, 64, 1) == 0                     # one work-group covers it
-    long = f(1, 8, 2, 64, 1 << 20)
-    assert long > 0 and long % (8 * 66 * 4) == 0      # [q_heads][splits][head_dim + 2] floats
-    assert f(1, 8, 2, 64, 1 << 20, 1000) < long       # a window bounds the positions
-    assert f(65535, 8, 2, 64, 128) == 0
+    assert f(1, 8, 2, 64, 1) == 0 == f(65535, 8, 2, 64, 128)  # no sequence is split
+    # partials [384 splits][2 KV heads][4 query heads] of head_dim + 2 floats, 8 bytes a
+    # sequence
+    assert f(3, 8, 2, 64, 129) == f(3, 8, 2, 64, 1 << 20) == 384 * 8 * 66 * 4 + 3 * 8
+    assert f(1, 8, 2, 64, 1 << 20, 90) == 0                   # a window that one work-group covers
+    assert f(1, 8, 2, 64, 1 << 20, 0, wq.WQ_FLAG_FP8) > f(1, 8, 2, 64, 1 << 20)
+    with pytest.raises(wq.WQError):
+        f(1, 8, 2, 64, 1, 0, wq.WQ_FLAG_SWIGLU)
+    with pytest.raises(wq.WQError) as e:
+        f(65535, 512, 512, 64, 128)                           # work-groups of one launch
+    assert e.value.code == wq.WQ_ERR_OVERFLOW
     for bad in ((0, 8, 2, 64, 1), (1, 7, 2, 64, 1), (1, 8, 0, 64, 1), (1, 8, 2, 20, 1)):
         with pytest.raises(wq.WQError):
             f(*bad)

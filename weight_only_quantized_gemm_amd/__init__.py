@@ -208,7 +208,7 @@ def lib() -> ctypes.CDLL:
             "wq_interleave_gate_up": (ctypes.c_int, [vp, vp, vp, i32, i32, i32, vp]),
             "wq_add_rms_norm": (ctypes.c_int, [vp]),
             "wq_rope_append": (ctypes.c_int, [vp]),
-            "wq_paged_attention_workspace_bytes": (ctypes.c_int, [i32, i32, i32, i32, i32, i32,
+            "wq_paged_attention_workspace_bytes": (ctypes.c_int, [i32, i32, i32, i32, i32, i32, u32,
                                                                   ctypes.POINTER(sz)]),
             "wq_paged_attention": (ctypes.c_int, [vp]),
             "wq_moe_layer_workspace_bytes": (ctypes.c_int, [i32, i32, i32, i32, i32,
@@ -447,10 +447,10 @@ def wq_rope_append(args: wq_rope_args | bytes) -> None:
 
 
 def wq_paged_attention_workspace_bytes(batch: int, q_heads: int, kv_heads: int, head_dim: int,
-                                       max_len: int, window: int = 0) -> int:
+                                       max_len: int, window: int = 0, flags: int = 0) -> int:
     out = ctypes.c_size_t(0)
     _check(lib().wq_paged_attention_workspace_bytes(batch, q_heads, kv_heads, head_dim, max_len,
-                                                    window, ctypes.byref(out)))
+                                                    window, flags, ctypes.byref(out)))
     return int(out.value)
 
 

@@ -33,6 +33,7 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kTile = 32;  // positions of a wave's step
+constexpr int kStep = kWaves * kTile;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -48,11 +49,19 @@ struct AttnArgs {
   const float *k_scale, *v_scale;
   const int32_t *table, *lens;
   const uint8_t* keep;
-  float* part_o;   // [batch][q_heads][splits][d], not divided by the sum
-  float* part_ml;  // [batch][q_heads][splits][2]: maximum (times log2 e) and sum
+  // Partials of the split sequences' work-groups: [part][16 or fewer query heads].
+  float* part_o;   // [d], not divided by the sum
+  float* part_ml;  // [2]: maximum (times log2 e) and sum
+  int32_t* parts;  // [batch][2]: splits of each sequence and its first partial
   int64_t page_stride, slot_stride, head_stride;
   int num_pages, page_size, kv_heads, q_heads, d, group, head_blocks, max_len;
-  int table_stride, keep_stride, ldq, ldo, window, splits, chunk;
+  int table_stride, keep_stride, ldq, ldo, window, batch;
+  int units;       // work-groups of a sequence's split: KV heads times head blocks
+  int part_rows;   // query heads of a partial: 16, or the group where it is smaller
+  int target;      // most splits of all sequences; 0: none is split
+  int round;       // splits that the CUs take at once
+  uint32_t page_mul;  // position / page_size = umulhi(2 * position, page_mul) >> page_shift
+  int page_shift;
   float scale, softcap;
 };
 
@@ -65,6 +74,11 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// 1 - 2 / (e^2x + 1): off by some 2^-23, which is all that a capped score needs.
+__device__ __forceinline__ float fast_tanh(float x) {
+  return 1.f - 2.f * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(2.f * kLog2e * x) + 1.f);
+}
+
 template <bool BF16>
 __device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
   return Act<BF16>::mfma16(a, __builtin_bit_cast(typename Act<BF16>::W8, b), c);
@@ -75,8 +89,100 @@ __device__ __forceinline__ f16x8 from_e4m3(uint32_t lo, uint32_t hi) {
   return __builtin_bit_cast(f16x8, Act<BF16>::fp8(lo, hi));
 }
 
-// DP: head_dim rounded up to 64, 128 or 256.
-template <bool BF16, bool KV8, int DP>
+__device__ __forceinline__ int wave_max(int x) {  // of values >= 0
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false));
+  return __builtin_amdgcn_readlane(x, 63);
+}
+
+// What a work-group does: granules [first, last) of kStep positions of sequence b, as one of
+// `splits` splits; part: its partial (splits > 1).
+struct Piece {
+  int b, len, splits, part, first, last;
+};
+
+// Positions of a sequence that may be live start in the tile of the window's first one.
+__device__ __forceinline__ int window_start(const AttnArgs& p, int len) {
+  return p.window > 0 ? max(0, len - p.window) & ~(kTile - 1) : 0;
+}
+__device__ __forceinline__ int granules_of(const AttnArgs& p, int len) {
+  return (len - window_start(p, len) + kStep - 1) / kStep;
+}
+
+// Inclusive sum over the wave's lanes.
+__device__ __forceinline__ int wave_scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);  // row_shr 1, 2, 4, 8: each
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);  // row of 16 lanes
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);  // row_bcast 15 to rows 1, 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);  // row_bcast 31 to rows 2, 3
+  return x;
+}
+
+// The index-th split of the batch; false past the last.  The sequences' lengths are known
+// only here, so every wave divides them alike, each lane counting a run of sequences: the
+// smallest chunks (to an eighth) that give no more than `target` splits over all sequences.
+// (Cut by the longest length alone, as the host could, half the work-groups of a ragged batch
+// were empty and the rest uneven: 64 sequences of up to 8192 positions, E4M3, 114 against
+// 81 us.)
+__device__ __forceinline__ bool find_piece(const AttnArgs& p, int index, int lane, Piece& out) {
+  const int run = (p.batch + 63) / 64;
+  const int b0 = lane * run, b1 = min(p.batch, b0 + run);
+  const auto length = [&](int b) { return max(0, min(p.lens[b], p.max_len)); };
+  int sum = 0, longest = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int n = granules_of(p, length(b));
+    sum += n;
+    longest = max(longest, n);
+  }
+  sum = __builtin_amdgcn_readlane(wave_scan(sum), 63);
+  longest = wave_max(longest);
+  int chunk = max(1, (sum + p.target - 1) / p.target);
+  // sequences that are even enough for one round of work-groups are left whole
+  if ((int64_t)longest * 4 * p.round <= (int64_t)sum * 5) chunk = max(1, longest);
+  while (chunk < longest) {
+    int n = 0;
+    for (int b = b0; b < b1; ++b) n += max(1, (granules_of(p, length(b)) + chunk - 1) / chunk);
+    if (__builtin_amdgcn_readlane(wave_scan(n), 63) <= p.target) break;
+    chunk += (chunk + 7) / 8;
+  }
+  // splits in the low 18 bits (at most batch or target), partials above (at most target)
+  const auto counts = [&](int n) {
+    const int splits = max(1, (n + chunk - 1) / chunk);
+    return splits | (splits > 1 ? splits << 18 : 0);
+  };
+  constexpr int kLow = (1 << 18) - 1;
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) mine += counts(granules_of(p, length(b)));
+  int at = wave_scan(mine);
+  const unsigned long long above = __ballot(index < (at & kLow));
+  if (above == 0) return false;
+  const int owner = __builtin_ctzll(above);
+  // the owner's run, on every lane
+  at = __builtin_amdgcn_readlane(at - mine, owner);
+  for (int b = owner * run;; ++b) {
+    const int len = length(b), n = granules_of(p, len), c = counts(n);
+    if (index < ((at + c) & kLow)) {
+      const int splits = c & kLow, split = index - (at & kLow);
+      out.b = b;
+      out.len = len;
+      out.splits = splits;
+      out.part = (at >> 18) + split;
+      out.first = (int)((int64_t)n * split / splits);
+      out.last = (int)((int64_t)n * (split + 1) / splits);
+      return true;
+    }
+    at += c;
+  }
+}
+
+// DP: head_dim rounded up to 64, 128 or 256; FULL: head_dim is DP.
+template <bool BF16, bool KV8, int DP, bool FULL>
 __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
   using A = Act<BF16>;
   constexpr int NS = DP / 32;            // MFMA steps along the head
@@ -96,29 +202,30 @@ __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row = lane & 15, qd = lane >> 4;
-  const int split = blockIdx.x, b = blockIdx.z;
-  const int kvh = blockIdx.y / p.head_blocks, hb = blockIdx.y - kvh * p.head_blocks;
+  const int index = blockIdx.x / p.units, unit = blockIdx.x - index * p.units;
+  Piece pc{index, 0, 1, 0, 0, 0};
+  if (p.target > 0) {
+    if (!find_piece(p, index, lane, pc)) return;
+  } else {
+    pc.len = max(0, min(p.lens[index], p.max_len));
+  }
+  const int b = pc.b, len = pc.len, splits = pc.splits, part = pc.part;
+  const int lo = p.window > 0 ? max(0, len - p.window) : 0;  // first live position
+  int t0 = window_start(p, len), t1 = len;
+  // Page numbers are read for positions below t_pages: without splits or a window they need
+  // not wait for the length.
+  const int t_pages = p.target > 0 || p.window > 0 ? len : p.max_len;
+  if (p.target > 0) {
+    t1 = min(len, t0 + pc.last * kStep);
+    t0 += pc.first * kStep;
+    if (unit == 0 && pc.first == 0 && threadIdx.x == 0) {
+      p.parts[2 * b] = splits;
+      p.parts[2 * b + 1] = part;
+    }
+  }
+  const int kvh = unit / p.head_blocks, hb = unit - kvh * p.head_blocks;
   const int h0 = kvh * p.group + 16 * hb;         // first query head
   const int rows = min(16, p.group - 16 * hb);
-  const int len = max(0, min(p.lens[b], p.max_len));
-  const int lo = p.window > 0 ? max(0, len - p.window) : 0;  // first live position
-  const int t0 = (lo & ~(kTile - 1)) + split * p.chunk;
-  const int t1 = min(len, t0 + p.chunk);
-  if (t0 >= t1) {  // nothing in this split
-    for (int i = threadIdx.x; i < rows; i += kWaves * 64) {
-      const int64_t h = (int64_t)b * p.q_heads + h0 + i;
-      if (p.splits > 1) {
-        p.part_ml[(h * p.splits + split) * 2] = -INFINITY;
-        p.part_ml[(h * p.splits + split) * 2 + 1] = 0.f;
-      } else if (p.lse != nullptr) {
-        p.lse[h] = -INFINITY;
-      }
-    }
-    if (p.splits == 1)
-      for (int i = threadIdx.x; i < rows * p.d; i += kWaves * 64)
-        p.out[(int64_t)b * p.ldo + (int64_t)h0 * p.d + i] = 0;
-    return;
-  }
 
   // Q as the B operand; query heads past the last repeat the first (never stored).
   f16x8 qf[NS];
@@ -128,7 +235,7 @@ __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
     for (int s = 0; s < NS; ++s) {
       const int e = KV8 ? 64 * (s / 2) + 16 * qd + 8 * (s % 2) : 32 * s + 8 * qd;
       qf[s] = f16x8{};
-      if (e < p.d) qf[s] = *reinterpret_cast<const f16x8*>(qp + e);
+      if (FULL || e < p.d) qf[s] = *reinterpret_cast<const f16x8*>(qp + e);
     }
   }
 
@@ -140,30 +247,36 @@ __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
   // A vector that lies past the head's end is read from its start and not used; an E4M3
   // vector that passes the end half way (head_dim % 16 == 8) is read 8 bytes earlier and
   // shifted.
-  const auto vec_at = [&](int e) { return e + CE <= p.d ? e : (e < p.d ? p.d - CE : 0); };
+  const auto vec_at = [&](int e) {
+    return FULL || e + CE <= p.d ? e : (e < p.d ? p.d - CE : 0);
+  };
   const auto vec_fix = [&](u32x4 w, int e) {
+    if (FULL) return w;
     if (KV8 && e < p.d && e + CE > p.d) w = u32x4{w[2], w[3], 0u, 0u};
     return e < p.d ? w : u32x4{0u, 0u, 0u, 0u};
   };
 
   // Page numbers (and keep bytes) of the tile at t, one position per lane and half-wave.
-  int page_next = -1;
+  int page_next = -1, pos_next = 0, slot_next = 0;
+  uint8_t keep_next = 1;
   const auto read_pages = [&](int t) {
     const int pos = t + (lane & (kTile - 1));
+    const int at = (int)(__umulhi(2u * (unsigned)pos, p.page_mul) >> p.page_shift);
+    pos_next = pos;
+    slot_next = pos - at * p.page_size;
     page_next = -1;
-    if (pos >= lo && pos < t1) {
-      page_next = table[pos / p.page_size];
-      if (keep != nullptr && keep[pos] == 0) page_next = -1;
+    if (pos < t_pages) {
+      page_next = table[at];
+      if (keep != nullptr) keep_next = keep[pos];
     }
   };
-  // Cache offsets of the tile at t, from page_next; returns the mask of live positions.  A
+  // Cache offsets of the tile whose pages were read; returns the mask of live positions.  A
   // position that is not live reads the cache's first slot, and is not used.
-  const auto place = [&](int t) -> uint32_t {
-    const int pos = t + (lane & (kTile - 1));
-    const bool live = (unsigned)page_next < (unsigned)p.num_pages;
-    const int slot = pos - pos / p.page_size * p.page_size;
+  const auto place = [&]() -> uint32_t {
+    const bool live = (unsigned)page_next < (unsigned)p.num_pages && keep_next != 0 &&
+                      pos_next >= lo && pos_next < t1;
     off_lds[wave][lane & (kTile - 1)] =
-        live ? page_next * p.page_stride + slot * p.slot_stride : 0;
+        live ? page_next * p.page_stride + slot_next * p.slot_stride : 0;
     return (uint32_t)__ballot(live);
   };
   u32x4 kr[2][NK], vr[NV];
@@ -188,23 +301,21 @@ __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
   uint16_t* const v_lds = reinterpret_cast<uint16_t*>(lds) + wave * kTile * VS;
   const float kscale = KV8 && p.k_scale != nullptr ? p.k_scale[kvh] : 1.f;
   const float sc = p.scale * kscale;
+  const float sc2 = p.softcap > 0.f ? kLog2e : sc * kLog2e;
+  const float cap = sc / p.softcap;
   float m = -INFINITY, l = 0.f;
   f32x4 o[NB];
 #pragma unroll
   for (int i = 0; i < NB; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  constexpr int kStep = kWaves * kTile;
   int t = t0 + wave * kTile;
-  uint32_t live = 0;
-  if (t < t1) {
-    read_pages(t);
-    wave_lds_fence();
-    live = place(t);
-    wave_lds_fence();
-    read_pages(t + kStep);
-    load_k();
-    load_v();
-  }
+  read_pages(t);  // (a wave without a tile reads the cache's first slot, and ends)
+  wave_lds_fence();
+  uint32_t live = place();
+  wave_lds_fence();
+  read_pages(t + kStep);
+  load_k();
+  load_v();
   for (; t < t1; t += kStep) {
     // scores
     f32x4 s[2];
@@ -226,32 +337,48 @@ __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
     const uint32_t now = live;
     // the next tile's K (positions past the range are not live and read the first slot)
     wave_lds_fence();
-    live = place(t + kStep);
+    live = place();
     wave_lds_fence();
     read_pages(t + 2 * kStep);
     load_k();
 
     // running maximum and sum, in base 2
     float mx = -INFINITY;
+    if (p.softcap > 0.f) {
+#pragma unroll
+      for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[blk][e] = p.softcap * fast_tanh(s[blk][e] * cap);
+    }
 #pragma unroll
     for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float x = s[blk][e] * sc;
-        if (p.softcap > 0.f) x = p.softcap * tanhf(x / p.softcap);
-        x *= kLog2e;
-        x = (now >> (16 * blk + 4 * qd + e)) & 1u ? x : -INFINITY;
-        s[blk][e] = x;
-        mx = fmaxf(mx, x);
-      }
+      for (int e = 0; e < 4; ++e) s[blk][e] *= sc2;
+    if (now != 0xFFFFFFFFu) {
+#pragma unroll
+      for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          s[blk][e] = (now >> (16 * blk + 4 * qd + e)) & 1u ? s[blk][e] : -INFINITY;
+    }
+#pragma unroll
+    for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mx = fmaxf(mx, s[blk][e]);
     mx = fmaxf(mx, __shfl_xor(mx, 16));
     mx = fmaxf(mx, __shfl_xor(mx, 32));
     const float m_new = fmaxf(m, mx);
     const float top = m_new == -INFINITY ? 0.f : m_new;  // nothing live so far
     const float ref = top - kPShift<BF16>;
     const float alpha = __builtin_amdgcn_exp2f(m - top);
+    if (__ballot(m_new > m)) {  // some head's maximum moved
+      l *= alpha;
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] *= alpha;
+    }
     m = m_new;
-    l *= alpha;
     uint16_t hi[8], lw[8];
 #pragma unroll
     for (int blk = 0; blk < 2; ++blk)
@@ -291,8 +418,6 @@ __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
       f16x8 vf;
       __builtin_memcpy(&vf, &a0, 8);
       __builtin_memcpy(reinterpret_cast<char*>(&vf) + 8, &a1, 8);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] *= alpha;
       o[i] = mfma<BF16>(vf, ph, o[i]);
       o[i] = mfma<BF16>(vf, pl, o[i]);
     }
@@ -331,11 +456,12 @@ __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
       for (int c = 0; c < 4; ++c) acc[c] = __builtin_fmaf(x[c], f, acc[c]);
     }
     const int64_t h = (int64_t)b * p.q_heads + h0 + r;
-    if (p.splits > 1) {
-      *reinterpret_cast<f32x4*>(p.part_o + (h * p.splits + split) * p.d + e) = acc;
+    if (splits > 1) {
+      const int64_t at = ((int64_t)part * p.units + unit) * p.part_rows + r;
+      *reinterpret_cast<f32x4*>(p.part_o + at * p.d + e) = acc;
       if (e == 0) {
-        p.part_ml[(h * p.splits + split) * 2] = top;
-        p.part_ml[(h * p.splits + split) * 2 + 1] = sum;
+        p.part_ml[at * 2] = top;
+        p.part_ml[at * 2 + 1] = sum;
       }
     } else {
       const float f = sum == 0.f ? 0.f : vscale / sum;
@@ -357,45 +483,54 @@ template <bool BF16>
 __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs p) {
   using A = Act<BF16>;
   __shared__ f32x4 acc_lds[kJoinThreads];
-  __shared__ float sum_lds[kJoinThreads];
+  __shared__ float sum_lds[kJoinThreads], top_lds[kJoinThreads];
   const int head = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  const int splits = p.parts[2 * b];
+  if (splits < 2) return;  // the output is there
   const int64_t h = (int64_t)b * p.q_heads + head;
   const int per_row = p.d / 4;  // at most 64
   const int groups = kJoinThreads / per_row;
   const int g = tid / per_row, e = 4 * (tid - g * per_row);
-  const float* ml = p.part_ml + h * p.splits * 2;
-  const float* po = p.part_o + h * p.splits * p.d;
+  const int kvh = head / p.group, in_group = head - kvh * p.group;
+  const int unit = kvh * p.head_blocks + in_group / 16;
+  // partial of split s: row r0 + s * step
+  const int64_t step = (int64_t)p.units * p.part_rows;
+  const int64_t r0 = p.parts[2 * b + 1] * step + unit * p.part_rows + in_group % 16;
+  const float* ml = p.part_ml + r0 * 2;
+  const float* po = p.part_o + r0 * p.d;
 
-  float top = -INFINITY;
-  for (int s = tid; s < p.splits; s += kJoinThreads) top = fmaxf(top, ml[2 * s]);
-#pragma unroll
-  for (int d = 32; d >= 1; d /= 2) top = fmaxf(top, __shfl_xor(top, d));
-  if ((tid & 63) == 0) sum_lds[tid >> 6] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(sum_lds[0], sum_lds[1]), fmaxf(sum_lds[2], sum_lds[3]));
-  __syncthreads();
-  const float ref = top == -INFINITY ? 0.f : top;
-
-  float sum = 0.f;
+  // each group of threads keeps its own maximum, so that no load waits for another split
+  float top = -INFINITY, sum = 0.f;
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   if (g < groups) {
-    for (int s = g; s < p.splits; s += groups) {
-      const float ms = ml[2 * s], ls = ml[2 * s + 1];
-      if (ms == -INFINITY && ls == 0.f) continue;  // an empty split wrote no sums
-      const float f = __builtin_amdgcn_exp2f(ms - ref);
-      sum = __builtin_fmaf(ls, f, sum);
-      const f32x4 x = *reinterpret_cast<const f32x4*>(po + (int64_t)s * p.d + e);
+#pragma unroll 4
+    for (int s = g; s < splits; s += groups) {
+      const float ms = ml[2 * step * s], ls = ml[2 * step * s + 1];
+      const f32x4 x = *reinterpret_cast<const f32x4*>(po + step * s * p.d + e);
+      const float high = fmaxf(top, ms);
+      const float ref = high == -INFINITY ? 0.f : high;
+      const float fa = __builtin_amdgcn_exp2f(top - ref), fx = __builtin_amdgcn_exp2f(ms - ref);
+      top = high;
+      sum = sum * fa + ls * fx;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) acc[c] = __builtin_fmaf(x[c], f, acc[c]);
+      for (int c = 0; c < 4; ++c) acc[c] = acc[c] * fa + x[c] * fx;
     }
   }
   acc_lds[tid] = acc;
   sum_lds[tid] = sum;
+  top_lds[tid] = top;
   __syncthreads();
   if (g != 0) return;
-  for (int k = 1; k < groups; ++k) {
-    sum += sum_lds[tid + k * per_row];
-    acc += acc_lds[tid + k * per_row];
+  for (int k = 1; k < groups; ++k) top = fmaxf(top, top_lds[tid + k * per_row]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  sum = 0.f;
+  acc = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int k = 0; k < groups; ++k) {
+    const int at = tid + k * per_row;
+    const float f = __builtin_amdgcn_exp2f(top_lds[at] - ref);
+    sum = __builtin_fmaf(sum_lds[at], f, sum);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[c] = __builtin_fmaf(acc_lds[at][c], f, acc[c]);
   }
   const float vscale = p.v_scale != nullptr ? p.v_scale[head / p.group] : 1.f;
   const float f = sum == 0.f ? 0.f : vscale / sum;
@@ -409,25 +544,38 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs p) {
 
 }  // namespace
 
-AttnPlan attn_plan(int batch, int q_heads, int kv_heads, int head_dim, int max_len, int window) {
+// Work-groups of a round.  A single sequence is cut evenly, so as many as hold the bytes in
+// flight that the memory needs, 64 KiB on each CU (bf16, head_dim 128, 131072 positions: 256
+// work-groups 99.7 us, 512 102.8, 1024 105.9).  Sequences of different lengths are cut finer,
+// into as many as the CUs hold at once by their registers (16 sequences of up to 4096: 256
+// work-groups 37.9 us, 512 35.6, 768 42.2; E4M3, 64 of up to 8192: 512 118, 768 92.7, 1024
+// 103 us).
+int attn_groups(int batch, int head_dim, bool kv8) {
+  if (batch == 1) return (head_dim <= 64 ? 512 : 256) * (kv8 && head_dim <= 128 ? 2 : 1);
+  return 256 * (head_dim <= 64 ? (kv8 ? 4 : 3) : head_dim <= 128 ? (kv8 ? 3 : 2) : 1);
+}
+
+AttnPlan attn_plan(int batch, int q_heads, int kv_heads, int head_dim, int max_len, int window,
+                   bool kv8) {
   AttnPlan plan{};
   plan.head_blocks = (q_heads / kv_heads + 15) / 16;
+  plan.units = kv_heads * plan.head_blocks;
   // positions a sequence may need, from the tile that holds the window's first
   const long span = window > 0 && window < max_len - kTile ? window + kTile - 1 : max_len;
-  const long units = (long)batch * kv_heads * plan.head_blocks;
-  constexpr long kStep = kWaves * kTile;
-  long chunk = span * units / 1024;
-  if (chunk < 2 * kStep) chunk = 2 * kStep;
-  chunk = (chunk + kStep - 1) / kStep * kStep;
-  (void)head_dim;
-  plan.chunk = (int)chunk;
-  plan.splits = (int)((span + chunk - 1) / chunk);
+  if (span <= kStep) return plan;
+  plan.round = (attn_groups(batch, head_dim, kv8) + plan.units - 1) / plan.units;
+  // whole rounds, with half a split more than one for each sequence
+  const int least = batch == 1 ? 1 : batch + batch / 2;
+  plan.target = (least + plan.round - 1) / plan.round * plan.round;
   return plan;
 }
 
-size_t attn_workspace_bytes(const AttnPlan& plan, int batch, int q_heads, int head_dim) {
-  if (plan.splits <= 1) return 0;
-  return (size_t)batch * q_heads * plan.splits * (head_dim + 2) * sizeof(float);
+size_t attn_workspace_bytes(const AttnPlan& plan, int batch, int q_heads, int kv_heads,
+                            int head_dim) {
+  if (plan.target == 0) return 0;
+  const int group = q_heads / kv_heads;
+  const size_t rows = (size_t)plan.target * plan.units * (group < 16 ? group : 16);
+  return rows * (head_dim + 2) * sizeof(float) + 2 * (size_t)batch * sizeof(int32_t);
 }
 
 hipError_t launch_paged_attention(const wq_attn_args& a, const AttnPlan& plan,
@@ -459,24 +607,36 @@ hipError_t launch_paged_attention(const wq_attn_args& a, const AttnPlan& plan,
   p.ldq = a.ldq;
   p.ldo = a.ldo;
   p.window = a.window;
-  p.splits = plan.splits;
-  p.chunk = plan.chunk;
+  p.batch = a.batch;
+  p.units = plan.units;
+  p.part_rows = p.group < 16 ? p.group : 16;
+  p.target = plan.target;
+  p.round = plan.round;
   p.scale = a.scale;
   p.softcap = a.softcap;
-  if (plan.splits > 1) {
+  // exact for positions below 2^30: the multiplier is 2^(31 + shift) / page_size rounded up,
+  // with page_size <= 2^shift
+  while ((1ll << p.page_shift) < p.page_size) ++p.page_shift;
+  p.page_mul = (uint32_t)(((1ull << (31 + p.page_shift)) + p.page_size - 1) / p.page_size);
+  if (plan.target > 0) {
+    const size_t rows = (size_t)plan.target * plan.units * p.part_rows;
     p.part_o = static_cast<float*>(a.workspace);
-    p.part_ml = p.part_o + (size_t)a.batch * a.q_heads * plan.splits * p.d;
+    p.part_ml = p.part_o + rows * p.d;
+    p.parts = reinterpret_cast<int32_t*>(p.part_ml + rows * 2);
   }
   const bool bf16 = (a.flags & WQ_FLAG_BF16) != 0, kv8 = (a.flags & WQ_FLAG_FP8) != 0;
-  const dim3 grid((unsigned)plan.splits, (unsigned)(p.kv_heads * plan.head_blocks),
-                  (unsigned)a.batch);
-#define WQ_ATTN(B, F, D)                                                                      \
-  hipLaunchKernelGGL((attn_kernel<B, F, D>), grid, dim3(kWaves * 64), 0, stream, p)
+  const int splits = plan.target > a.batch ? plan.target : a.batch;
+  const dim3 grid((unsigned)((size_t)splits * plan.units));
+#define WQ_ATTN(B, F, D, FULL)                                                                \
+  hipLaunchKernelGGL((attn_kernel<B, F, D, FULL>), grid, dim3(kWaves * 64), 0, stream, p)
 #define WQ_ATTN_D(B, F)                                                                       \
   do {                                                                                        \
-    if (p.d <= 64) WQ_ATTN(B, F, 64);                                                         \
-    else if (p.d <= 128) WQ_ATTN(B, F, 128);                                                  \
-    else WQ_ATTN(B, F, 256);                                                                  \
+    if (p.d == 64) WQ_ATTN(B, F, 64, true);                                                   \
+    else if (p.d < 64) WQ_ATTN(B, F, 64, false);                                              \
+    else if (p.d == 128) WQ_ATTN(B, F, 128, true);                                            \
+    else if (p.d < 128) WQ_ATTN(B, F, 128, false);                                            \
+    else if (p.d == 256) WQ_ATTN(B, F, 256, true);                                            \
+    else WQ_ATTN(B, F, 256, false);                                                           \
   } while (0)
   if (bf16) {
     if (kv8) WQ_ATTN_D(true, true); else WQ_ATTN_D(true, false);
@@ -486,7 +646,7 @@ hipError_t launch_paged_attention(const wq_attn_args& a, const AttnPlan& plan,
 #undef WQ_ATTN_D
 #undef WQ_ATTN
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || plan.splits == 1) return e;
+  if (e != hipSuccess || plan.target == 0) return e;
   const dim3 join((unsigned)a.q_heads, (unsigned)a.batch);
   if (bf16)
     hipLaunchKernelGGL((attn_join_kernel<true>), join, dim3(kJoinThreads), 0, stream, p);

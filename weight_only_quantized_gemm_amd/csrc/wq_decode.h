@@ -14,16 +14,20 @@ hipError_t launch_add_rms_norm(const wq_norm_args& a, hipStream_t stream);
 
 hipError_t launch_rope_append(const wq_rope_args& a, hipStream_t stream);
 
-// How a call's positions are cut: `splits` work-groups per (sequence, KV head, 16 query
-// heads), each over `chunk` consecutive positions (a multiple of 128); more than one split
-// leaves fp32 partials that a second kernel joins.
+// How a call's positions are cut: at most `target` splits of about equal length over all
+// sequences (0: none is split), each taken by `units` work-groups, one per KV head and block
+// of 16 of its query heads; the CUs take `round` splits at once.  Split sequences leave fp32
+// partials that a second kernel joins.
 struct AttnPlan {
-  int splits;
-  int chunk;
+  int target;
+  int round;
+  int units;
   int head_blocks;  // blocks of 16 query heads per KV head
 };
-AttnPlan attn_plan(int batch, int q_heads, int kv_heads, int head_dim, int max_len, int window);
-size_t attn_workspace_bytes(const AttnPlan& plan, int batch, int q_heads, int head_dim);
+AttnPlan attn_plan(int batch, int q_heads, int kv_heads, int head_dim, int max_len, int window,
+                   bool kv8);
+size_t attn_workspace_bytes(const AttnPlan& plan, int batch, int q_heads, int kv_heads,
+                            int head_dim);
 hipError_t launch_paged_attention(const wq_attn_args& a, const AttnPlan& plan,
                                   hipStream_t stream);
 

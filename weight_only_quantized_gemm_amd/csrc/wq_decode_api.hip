@@ -113,14 +113,20 @@ int wq_rope_append(const wq_rope_args* args) {
 }
 
 int wq_paged_attention_workspace_bytes(int batch, int q_heads, int kv_heads, int head_dim,
-                                       int max_len, int window, size_t* bytes_out) {
+                                       int max_len, int window, uint32_t flags,
+                                       size_t* bytes_out) {
   if (bytes_out == nullptr) return fail(WQ_STAGE_ARGS, WQ_ERR_NULL);
+  if (flags & ~(uint32_t)(WQ_FLAG_BF16 | WQ_FLAG_FP8)) return flags_error();
   if (batch < 1 || batch > kMaxHeads || kv_heads < 1 || q_heads < kv_heads ||
       q_heads > kMaxHeads || q_heads % kv_heads != 0 || head_dim < 16 || head_dim > 256 ||
       head_dim % 8 != 0 || max_len < 1 || max_len > (1 << 30) || window < 0)
     return shape_error();
-  const wq::AttnPlan plan = wq::attn_plan(batch, q_heads, kv_heads, head_dim, max_len, window);
-  *bytes_out = wq::attn_workspace_bytes(plan, batch, q_heads, head_dim);
+  const wq::AttnPlan plan = wq::attn_plan(batch, q_heads, kv_heads, head_dim, max_len, window,
+                                          (flags & WQ_FLAG_FP8) != 0);
+  const int64_t splits = plan.target > batch ? plan.target : batch;
+  if (splits * plan.units > (1 << 23) || splits >= 1 << 18)  // work-groups of one launch
+    return fail(WQ_STAGE_SHAPE, WQ_ERR_OVERFLOW);
+  *bytes_out = wq::attn_workspace_bytes(plan, batch, q_heads, kv_heads, head_dim);
   return 0;
 }
 
@@ -132,7 +138,7 @@ int wq_paged_attention(const wq_attn_args* args) {
   if ((st = check_cache(a.cache, a.flags))) return st;
   size_t need = 0;
   if ((st = wq_paged_attention_workspace_bytes(a.batch, a.q_heads, a.cache.kv_heads,
-                                               a.cache.head_dim, a.max_len, a.window, &need)))
+                                               a.cache.head_dim, a.max_len, a.window, a.flags, &need)))
     return st;
   const int64_t row = (int64_t)a.q_heads * a.cache.head_dim;
   if (!row_stride_ok(a.ldq, row) || !row_stride_ok(a.ldo, row) || a.table_stride < 1 ||
@@ -151,7 +157,7 @@ int wq_paged_attention(const wq_attn_args* args) {
     if (!aligned(a.workspace, 16)) return fail(WQ_STAGE_ARGS, WQ_ERR_ALIGN);
   }
   const wq::AttnPlan plan = wq::attn_plan(a.batch, a.q_heads, a.cache.kv_heads, a.cache.head_dim,
-                                          a.max_len, a.window);
+                                          a.max_len, a.window, (a.flags & WQ_FLAG_FP8) != 0);
   return launched(wq::launch_paged_attention(a, plan, as_stream(a.stream)));
 }
 

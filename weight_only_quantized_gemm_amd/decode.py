@@ -254,7 +254,8 @@ class PagedAttention:
         self.cache, self.batch, self.q_heads, self.max_len = cache, batch, q_heads, max_len
         self.dtype, self.device = dtype, cache.device
         nbytes = wq_paged_attention_workspace_bytes(batch, q_heads, cache.kv_heads,
-                                                    cache.head_dim, max_len, window)
+                                                    cache.head_dim, max_len, window,
+                                                    cache.flags(dtype))
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         self._space = (self.workspace.data_ptr(), nbytes)
         self._lse = torch.empty((batch, q_heads), dtype=torch.float32, device=self.device)

@@ -40,7 +40,7 @@ struct Route {
 struct Bank {
   const u32x4* b;
   const uint16_t* s;
-  const u32x2* z;
+  const uint32_t* z;
   long b_stride, s_stride, z_stride;  // in elements of the above
 };
 
@@ -249,6 +249,12 @@ __global__ __launch_bounds__(kMaxT * 64) void route_kernel(RouteArgs p) {
         (uint32_t)pair | (uint32_t)wave << 16;
 }
 
+// Orders a wave's own LDS accesses (they execute in order; this keeps the compiler to it).
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // ---- the quantized products ------------------------------------------------------------
 
 // bf16 has no packed subtract, so its codes enter the products as 128 + q (one mask-and-or a
@@ -294,10 +300,10 @@ struct Chunk {
   using Sums = RowSums<BF16, W8, GPC>;
   u32x4 w[W8 ? 2 : 1];
   uint16_t s[GPC];
-  u32x2 z[ZP ? GPC : 1];
+  uint32_t z[ZP ? GPC : 1];  // the lane's half of the unit's codes
 
   // at: chunk index of the expert's layout (block * groups + group)
-  __device__ __forceinline__ void load(const u32x4* b, const uint16_t* sp, const u32x2* zp,
+  __device__ __forceinline__ void load(const u32x4* b, const uint16_t* sp, const uint32_t* zp,
                                        long at, int lane) {
 #pragma unroll
     for (int v = 0; v < (W8 ? 2 : 1); ++v)
@@ -306,7 +312,7 @@ struct Chunk {
     for (int u = 0; u < GPC; ++u) s[u] = sp[(at * GPC + u) * 16 + (lane & 15)];
     if constexpr (ZP) {
 #pragma unroll
-      for (int u = 0; u < GPC; ++u) z[u] = zp[at * GPC + u];
+      for (int u = 0; u < GPC; ++u) z[u] = zp[(at * GPC + u) * 2 + ((lane >> 3) & 1)];
     }
   }
 
@@ -314,7 +320,9 @@ struct Chunk {
   __device__ __forceinline__ void multiply(const f16x8* a, const Sums& sums, int lane,
                                            f32x4& acc) const {
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-    const auto code = [&](int u) { return ZP ? zero_code(z[ZP ? u : 0], lane & 15) : 8; };
+    const auto code = [&](int u) {
+      return ZP ? (int)((z[ZP ? u : 0] >> (4 * (lane & 7))) & 0xFu) : 8;
+    };
     const auto add = [&](int u, f32x4 part) {
       const float f = A::value(s[u]);
       if constexpr (kBiased<BF16, W8>) {
@@ -374,14 +382,30 @@ struct ProductArgs {
   int groups, n;  // n: columns of a row of the output
 };
 
-// Two neighbouring 16-column blocks of a slot's expert.  The waves take 128-row groups in
-// turn; a lane's activation rows serve both blocks (as loads they would take as long as the
-// weights do for one).
-template <bool GATE_UP, bool BF16, bool W8, bool ZP, int GPC, int WAVES, int U>
+// Two neighbouring 16-column blocks of a slot's expert.  Each wave takes a run of 128-row
+// groups, GW at a time, with all of their weights requested at once.  A lane's activations
+// serve both blocks; of up to kStagedRows rows the wave first brings its run into LDS, in
+// whole rows (16 rows read as MFMA operands are as many loads as the weights of both blocks,
+// and operands held in registers leave none for weights in flight).
+constexpr int kStagedRows = 4;
+
+// Groups in flight, by the registers of a chunk (codes, scales, zero points) and of a wave.
+template <bool W8, bool ZP, int GPC, int WAVES>
+constexpr int kInFlight = [] {
+  const int regs = (W8 ? 8 : 4) + GPC + (ZP ? GPC : 0);
+  if (regs <= 6 || W8) return 4;
+  if (regs <= 8) return WAVES == 16 ? 2 : 4;
+  return WAVES == 16 ? 1 : 2;
+}();
+
+template <bool GATE_UP, bool BF16, bool W8, bool ZP, int GPC, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void product_kernel(ProductArgs p) {
   using A = Act<BF16>;
   using C = Chunk<BF16, W8, ZP, GPC>;
-  __shared__ f32x4 red[2][WAVES][64];
+  constexpr int GW = kInFlight<W8, ZP, GPC, WAVES>;
+  constexpr int LR = GW * 16 + 1;  // granules of a staged row, one of padding
+  constexpr int kStage = WAVES * kStagedRows * LR * 16, kRed = 2 * WAVES * 64 * 16;
+  __shared__ __align__(16) uint8_t lds[kStage > kRed ? kStage : kRed];
   const RouteSlot& slot = p.route->slot[blockIdx.y];
   const int expert = slot.expert, rows = slot.rows;
   if (rows == 0) return;  // past the last chosen expert
@@ -393,34 +417,89 @@ __global__ __launch_bounds__(WAVES * 64) void product_kernel(ProductArgs p) {
   // (read from the first lane by the whole wave, not inside the choice between the two)
   const uint32_t first_pair = (uint32_t)__builtin_amdgcn_readfirstlane((int)row_pair);
   const uint32_t pair = row < rows ? row_pair : first_pair;
-  const uint16_t* ap = p.a + (GATE_UP ? pair >> 16 : pair & 0xffffu) * p.lda + 8 * qd;
+  const auto row_at = [&](uint32_t pr) {
+    return p.a + (long)(GATE_UP ? pr >> 16 : pr & 0xffffu) * p.lda;
+  };
   const u32x4* b = p.bank.b + expert * p.bank.b_stride;
   const uint16_t* s = p.bank.s + expert * p.bank.s_stride;
-  const u32x2* z = ZP ? p.bank.z + expert * p.bank.z_stride : nullptr;
+  const uint32_t* z = ZP ? p.bank.z + expert * p.bank.z_stride : nullptr;
 
   const long block0 = 2L * blockIdx.x * p.groups, block1 = block0 + p.groups;
   f32x4 acc0 = {0.f, 0.f, 0.f, 0.f}, acc1 = acc0;
-  for (int g0 = wave; g0 < p.groups; g0 += WAVES * U) {
-    C c0[U], c1[U];
-    f16x8 a[U][4];
+  const int last = p.groups * (wave + 1) / WAVES;
+  int g0 = p.groups * wave / WAVES;
+  if (rows <= kStagedRows) {
+    u32x4* const own = reinterpret_cast<u32x4*>(lds) + wave * kStagedRows * LR;
+    const u32x4* ap = own + (row < rows ? row : 0) * LR + qd;
+    for (; g0 < last; g0 += GW) {
+      const int n = min(GW, last - g0);
+      u32x4 stage[GW];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int g = min(g0 + i * WAVES, p.groups - 1);
-      c0[i].load(b, s, z, block0 + g, lane);
-      c1[i].load(b, s, z, block1 + g, lane);
+      for (int u = 0; u < GW; ++u) {  // 64 granules of the rows' GW * 16 each
+        if (u * 64 < rows * GW * 16) {
+          const int i = u * 64 + lane, r = i / (GW * 16), c = i % (GW * 16);
+          const uint32_t pr = __shfl(pair, min(r, rows - 1));
+          stage[u] = reinterpret_cast<const u32x4*>(row_at(pr) + (long)g0 * kGroup)[
+              min(c, n * 16 - 1)];
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);  // the rows are requested before any weight
+      C c0[GW], c1[GW];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        a[i][j] = *reinterpret_cast<const f16x8*>(ap + (long)g * kGroup + 32 * j);
+      for (int i = 0; i < GW; ++i) {
+        const int g = g0 + min(i, n - 1);
+        c0[i].load(b, s, z, block0 + g, lane);
+        c1[i].load(b, s, z, block1 + g, lane);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int u = 0; u < GW; ++u) {
+        if (u * 64 < rows * GW * 16) {
+          const int i = u * 64 + lane;
+          own[i / (GW * 16) * LR + i % (GW * 16)] = stage[u];
+        }
+      }
+      wave_lds_fence();
+#pragma unroll
+      for (int i = 0; i < GW; ++i) {
+        if (i >= n) continue;
+        f16x8 a[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[j] = __builtin_bit_cast(f16x8, ap[16 * i + 4 * j]);
+        typename C::Sums sums;
+        sums.form(a, lane);
+        c0[i].multiply(a, sums, lane, acc0);
+        c1[i].multiply(a, sums, lane, acc1);
+      }
+      wave_lds_fence();
     }
+  } else {
+    constexpr int U = GW >= 2 ? 2 : 1;
+    const uint16_t* ap = row_at(pair) + 8 * qd;
+    for (; g0 < last; g0 += U) {
+      C c0[U], c1[U];
+      f16x8 a[U][4];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      if (g0 + i * WAVES >= p.groups) continue;
-      typename C::Sums sums;
-      sums.form(a[i], lane);
-      c0[i].multiply(a[i], sums, lane, acc0);
-      c1[i].multiply(a[i], sums, lane, acc1);
+      for (int i = 0; i < U; ++i) {
+        const int g = min(g0 + i, last - 1);
+        c0[i].load(b, s, z, block0 + g, lane);
+        c1[i].load(b, s, z, block1 + g, lane);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          a[i][j] = *reinterpret_cast<const f16x8*>(ap + (long)g * kGroup + 32 * j);
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (g0 + i >= last) continue;
+        typename C::Sums sums;
+        sums.form(a[i], lane);
+        c0[i].multiply(a[i], sums, lane, acc0);
+        c1[i].multiply(a[i], sums, lane, acc1);
+      }
     }
   }
+  __syncthreads();  // the staged rows are no longer read
+  f32x4(*const red)[WAVES][64] = reinterpret_cast<f32x4(*)[WAVES][64]>(lds);
   red[0][wave][lane] = acc0;
   red[1][wave][lane] = acc1;
   __syncthreads();
@@ -477,8 +556,8 @@ int max_slots(int tokens, int n_expert, int top_k) {
 
 Bank bank_of(const wq_expert_bank& b) {
   return Bank{static_cast<const u32x4*>(b.b), static_cast<const uint16_t*>(b.s),
-              static_cast<const u32x2*>(b.zp), (long)(b.b_stride_bytes / 16),
-              (long)(b.s_stride_bytes / 2), (long)(b.zp_stride_bytes / 8)};
+              static_cast<const uint32_t*>(b.zp), (long)(b.b_stride_bytes / 16),
+              (long)(b.s_stride_bytes / 2), (long)(b.zp_stride_bytes / 4)};
 }
 
 struct MoeScratch {
@@ -513,11 +592,10 @@ hipError_t launch_product(const wq_moe_args& a, const MoeScratch& m, hipStream_t
   p.n = GATE_UP ? a.inter : a.hidden;
   const dim3 grid(GATE_UP ? a.inter / 16 : a.hidden / 32,
                   max_slots(a.tokens, a.n_expert, a.top_k));
-  constexpr int U = GPC >= 4 ? 1 : 2;  // small units' scales and zero points take the registers
 #define WQ_MOE_PRODUCT(W)                                                                      \
-  hipLaunchKernelGGL((product_kernel<GATE_UP, BF16, W8, ZP, GPC, W, U>), grid, dim3(W * 64), 0, \
+  hipLaunchKernelGGL((product_kernel<GATE_UP, BF16, W8, ZP, GPC, W>), grid, dim3(W * 64), 0,   \
                      stream, p)
-  if (p.groups <= 8)
+  if (p.groups <= 16)
     WQ_MOE_PRODUCT(4);
   else if (p.groups <= 64)
     WQ_MOE_PRODUCT(8);

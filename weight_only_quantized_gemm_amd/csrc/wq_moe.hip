@@ -142,12 +142,13 @@ __device__ __forceinline__ void token_top_k(const float* logits, int n_expert, i
     // lower number.  (No round waits for the one before: 8 choices of 64 experts for 16
     // tokens in well under a microsecond.)
     int place = 0;
+    const uint64_t full = (uint64_t)key[0] << 32 | (uint32_t)(63 - lane);
     for (int e0 = 0; e0 < n_expert; e0 += 8) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int e = e0 + k;  // past n_expert the keys are 0
         const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)key[0], e);
-        place += other > key[0] || (other == key[0] && e < lane);
+        place += ((uint64_t)other << 32 | (uint32_t)(63 - e)) > full;
       }
     }
     // lane j fetches the key and number of the expert in place j
@@ -390,19 +391,17 @@ struct ProductArgs {
 constexpr int kStagedRows = 4;
 
 // Groups in flight, by the registers of a chunk (codes, scales, zero points) and of a wave.
-template <bool W8, bool ZP, int GPC, int WAVES>
+template <bool W8, bool ZP, int GPC>
 constexpr int kInFlight = [] {
   const int regs = (W8 ? 8 : 4) + GPC + (ZP ? GPC : 0);
-  if (regs <= 6 || W8) return 4;
-  if (regs <= 8) return WAVES == 16 ? 2 : 4;
-  return WAVES == 16 ? 1 : 2;
+  return regs <= 8 || W8 ? 4 : 2;
 }();
 
 template <bool GATE_UP, bool BF16, bool W8, bool ZP, int GPC, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void product_kernel(ProductArgs p) {
   using A = Act<BF16>;
   using C = Chunk<BF16, W8, ZP, GPC>;
-  constexpr int GW = kInFlight<W8, ZP, GPC, WAVES>;
+  constexpr int GW = kInFlight<W8, ZP, GPC>;
   constexpr int LR = GW * 16 + 1;  // granules of a staged row, one of padding
   constexpr int kStage = WAVES * kStagedRows * LR * 16, kRed = 2 * WAVES * 64 * 16;
   __shared__ __align__(16) uint8_t lds[kStage > kRed ? kStage : kRed];
@@ -503,22 +502,25 @@ __global__ __launch_bounds__(WAVES * 64) void product_kernel(ProductArgs p) {
   red[0][wave][lane] = acc0;
   red[1][wave][lane] = acc1;
   __syncthreads();
-  if (wave >= 4) return;
-  // wave e sums element e of the lane's two blocks, in wave order
-  const int r = 4 * qd + wave;
-  float s0 = 0.f, s1 = 0.f;
+  // the lane's four elements of the two blocks are summed by different waves, in wave order
 #pragma unroll
-  for (int w = 0; w < WAVES; ++w) {
-    s0 += reinterpret_cast<const float*>(&red[0][w][lane])[wave];
-    s1 += reinterpret_cast<const float*>(&red[1][w][lane])[wave];
-  }
-  const long out = (long)(__shfl(pair, r) & 0xffffu) * p.n;
-  if (r >= rows) return;
-  if constexpr (GATE_UP) {
-    p.h[out + 16 * blockIdx.x + row] = A::round(silu_times(s0, s1));
-  } else {
-    p.part[out + 32 * blockIdx.x + row] = s0;
-    p.part[out + 32 * blockIdx.x + 16 + row] = s1;
+  for (int e = wave; e < 4; e += WAVES) {
+    const int r = 4 * qd + e;
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      s0 += reinterpret_cast<const float*>(&red[0][w][lane])[e];
+      s1 += reinterpret_cast<const float*>(&red[1][w][lane])[e];
+    }
+    const long out = (long)(__shfl(pair, r) & 0xffffu) * p.n;
+    if (r < rows) {
+      if constexpr (GATE_UP) {
+        p.h[out + 16 * blockIdx.x + row] = A::round(silu_times(s0, s1));
+      } else {
+        p.part[out + 32 * blockIdx.x + row] = s0;
+        p.part[out + 32 * blockIdx.x + 16 + row] = s1;
+      }
+    }
   }
 }
 
@@ -595,12 +597,13 @@ hipError_t launch_product(const wq_moe_args& a, const MoeScratch& m, hipStream_t
 #define WQ_MOE_PRODUCT(W)                                                                      \
   hipLaunchKernelGGL((product_kernel<GATE_UP, BF16, W8, ZP, GPC, W>), grid, dim3(W * 64), 0,   \
                      stream, p)
-  if (p.groups <= 16)
+  // Four waves; eight where each would have a long run and there are few work-groups (down
+  // projection of 112 groups, 1 token: 45.9 -> 42.8 us for the layer; 64 groups and fewer are
+  // slower with eight: 16 tokens of 64 experts, 50.4 -> 61.9 us).
+  if (p.groups <= 64)
     WQ_MOE_PRODUCT(4);
-  else if (p.groups <= 64)
-    WQ_MOE_PRODUCT(8);
   else
-    WQ_MOE_PRODUCT(16);
+    WQ_MOE_PRODUCT(8);
 #undef WQ_MOE_PRODUCT
   return hipGetLastError();
 }

@@ -537,12 +537,21 @@ __global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ 
   u32x2 res = {0u, 0u};
   if (residual != nullptr) res = *reinterpret_cast<const u32x2*>(residual + (long)t * ldr + col);
   f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int j = 0; j < top_k; ++j) {
-    const float w = route->w[t * top_k + j];
-    const f32x4 v = *reinterpret_cast<const f32x4*>(part + (long)(t * top_k + j) * hidden + col);
+  for (int j0 = 0; j0 < top_k; j0 += 4) {  // four rows requested together
+    float w[4];
+    f32x4 v[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(w, v[e], sum[e]);
+    for (int i = 0; i < 4; ++i) {
+      const int pair = t * top_k + min(j0 + i, top_k - 1);
+      w[i] = route->w[pair];
+      v[i] = *reinterpret_cast<const f32x4*>(part + (long)pair * hidden + col);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (j0 + i >= top_k) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(w[i], v[i][e], sum[e]);
+    }
   }
   uint32_t out[4];
 #pragma unroll
@@ -600,7 +609,11 @@ hipError_t launch_product(const wq_moe_args& a, const MoeScratch& m, hipStream_t
   // Four waves; eight where each would have a long run and there are few work-groups (down
   // projection of 112 groups, 1 token: 45.9 -> 42.8 us for the layer; 64 groups and fewer are
   // slower with eight: 16 tokens of 64 experts, 50.4 -> 61.9 us).
-  if (p.groups <= 64)
+  // Two for a short K when there are many work-groups (8 groups, 64 slots: 50.4 -> 48.5 us; 8
+  // slots: 18.1 -> 18.8).
+  if (p.groups <= 8 && grid.y > 8)
+    WQ_MOE_PRODUCT(2);
+  else if (p.groups <= 64)
     WQ_MOE_PRODUCT(4);
   else
     WQ_MOE_PRODUCT(8);

@@ -70,7 +70,7 @@ __device__ __forceinline__ void store4(void* base, int64_t at, const float* f, f
 
 template <bool BF16, bool FP8, bool INTERLEAVED>
 __global__ __launch_bounds__(kThreads) void rope_append_kernel(RopeArgs p) {
-  __shared__ float cs[kMaxPairs], sn[kMaxPairs];
+  __shared__ __align__(16) float cs[kMaxPairs], sn[kMaxPairs];
   const int token = blockIdx.x;
   const int tid = threadIdx.x;
   if (tid < p.half) {
@@ -79,9 +79,7 @@ __global__ __launch_bounds__(kThreads) void rope_append_kernel(RopeArgs p) {
     const double angle =
         (double)p.positions[(long)axis * p.tokens + token] * (double)p.inv_freq[tid];
     const double turns = angle * 0.15915494309189533577;  // 1 / (2 pi)
-    const float r = (float)((turns - rint(turns)) * 6.283185307179586477);
-    cs[tid] = cosf(r);
-    sn[tid] = sinf(r);
+    sincospif(2.f * (float)(turns - rint(turns)), &sn[tid], &cs[tid]);
   }
   const int64_t slot = p.slots[token];
   const bool real = slot >= 0 && slot < p.total_slots;
@@ -115,8 +113,8 @@ __global__ __launch_bounds__(kThreads) void rope_append_kernel(RopeArgs p) {
     unpack4<BF16>(*reinterpret_cast<const u32x2*>(src + e0), a);
     unpack4<BF16>(*reinterpret_cast<const u32x2*>(src + e1), b);
     if (turn) {
-      const float* c = cs + 4 * e;
-      const float* s = sn + 4 * e;
+      const f32x4 c = *reinterpret_cast<const f32x4*>(cs + 4 * e);
+      const f32x4 s = *reinterpret_cast<const f32x4*>(sn + 4 * e);
       if constexpr (INTERLEAVED) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {

@@ -429,21 +429,15 @@ def versioned(cls, **fields):
     return cls(abi_version=WQ_ABI_VERSION, struct_size=ctypes.sizeof(cls), **fields)
 
 
-# The decode-step calls take their argument struct as it is, or as its bytes: they run once
-# per layer and token, and filling a ctypes struct field by field costs more than the launch
-# (weight_only_quantized_gemm_amd.decode packs the bytes from tensors).
-def _call_packed(name: str, args) -> None:
-    status = getattr(lib(), name)(args if type(args) is bytes else ctypes.byref(args))
-    if status:
-        _check(status)
+# The decode-step calls take their argument struct (weight_only_quantized_gemm_amd.decode packs
+# its bytes from tensors instead: filling a ctypes struct field by field costs more than the
+# launch of a call that runs once per layer and token).
+def wq_add_rms_norm(args: wq_norm_args) -> None:
+    _check(lib().wq_add_rms_norm(ctypes.byref(args)))
 
 
-def wq_add_rms_norm(args: wq_norm_args | bytes) -> None:
-    _call_packed("wq_add_rms_norm", args)
-
-
-def wq_rope_append(args: wq_rope_args | bytes) -> None:
-    _call_packed("wq_rope_append", args)
+def wq_rope_append(args: wq_rope_args) -> None:
+    _check(lib().wq_rope_append(ctypes.byref(args)))
 
 
 def wq_paged_attention_workspace_bytes(batch: int, q_heads: int, kv_heads: int, head_dim: int,
@@ -454,8 +448,8 @@ def wq_paged_attention_workspace_bytes(batch: int, q_heads: int, kv_heads: int, 
     return int(out.value)
 
 
-def wq_paged_attention(args: wq_attn_args | bytes) -> None:
-    _call_packed("wq_paged_attention", args)
+def wq_paged_attention(args: wq_attn_args) -> None:
+    _check(lib().wq_paged_attention(ctypes.byref(args)))
 
 
 def wq_moe_layer_workspace_bytes(tokens: int, n_expert: int, top_k: int, hidden: int,
@@ -466,5 +460,5 @@ def wq_moe_layer_workspace_bytes(tokens: int, n_expert: int, top_k: int, hidden:
     return int(out.value)
 
 
-def wq_moe_layer(args: wq_moe_args | bytes) -> None:
-    _call_packed("wq_moe_layer", args)
+def wq_moe_layer(args: wq_moe_args) -> None:
+    _check(lib().wq_moe_layer(ctypes.byref(args)))

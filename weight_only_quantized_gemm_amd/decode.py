@@ -22,10 +22,9 @@ import struct
 import torch
 
 from . import (WQ_ABI_VERSION, WQ_FLAG_BF16, WQ_FLAG_FP8, WQ_FLAG_HAS_ZP, WQ_MAX_ROPE_AXES,
-               WQ_MOE_MAX_TOKENS, wq_add_rms_norm, wq_attn_args, wq_expert_bank, wq_kv_cache,
-               wq_moe_args, wq_moe_layer, wq_moe_layer_workspace_bytes, wq_norm_args,
-               wq_paged_attention, wq_paged_attention_workspace_bytes, wq_rope_append,
-               wq_rope_args)
+               WQ_MOE_MAX_TOKENS, _check, lib, wq_attn_args, wq_expert_bank, wq_kv_cache,
+               wq_moe_args, wq_moe_layer_workspace_bytes, wq_norm_args,
+               wq_paged_attention_workspace_bytes, wq_rope_args)
 
 _TYPE_FLAGS = {torch.float16: 0, torch.bfloat16: WQ_FLAG_BF16}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -57,6 +56,24 @@ def _stream(dev: int) -> int:
     return _raw_stream(dev)
 
 
+class _Call:
+    """A library call that takes the bytes of its argument struct."""
+
+    def __init__(self, name: str):
+        self.name, self.fn = name, None
+
+    def __call__(self, packed: bytes) -> None:
+        if self.fn is None:
+            self.fn = getattr(lib(), self.name)
+        status = self.fn(packed)
+        if status:
+            _check(status)
+
+
+_norm_call, _rope_call = _Call("wq_add_rms_norm"), _Call("wq_rope_append")
+_attn_call, _moe_call = _Call("wq_paged_attention"), _Call("wq_moe_layer")
+
+
 def _type_flag(dtype: torch.dtype) -> int:
     flag = _TYPE_FLAGS.get(dtype)
     if flag is None:
@@ -70,16 +87,16 @@ def _check_type(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int) -> Non
                         f"{t.get_device()}")
 
 
-def _rows(t: torch.Tensor, name: str, dtype, dev: int, rows: int, cols: int) -> int:
-    """The row stride of a [rows][cols] tensor."""
+def _rows(t: torch.Tensor, name: str, dtype, dev: int, shape) -> int:
+    """The row stride of a [rows][cols] tensor of this shape."""
     if t.dtype is not dtype or t.get_device() != dev:
         _check_type(t, name, dtype, dev)
-    if t.shape != (rows, cols):
-        raise ValueError(f"{name}: [{rows}][{cols}] expected, got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: {tuple(shape)} expected, got {tuple(t.shape)}")
     ld, one = t.stride()
-    if one != 1 and cols > 1:
+    if one != 1 and shape[1] > 1:
         raise ValueError(f"{name}: its last dimension must be contiguous")
-    return ld if rows > 1 else cols
+    return ld if shape[0] > 1 else shape[1]
 
 
 def _heads(t: torch.Tensor, name: str, dtype, dev: int, rows: int, heads: int, d: int) -> int:
@@ -109,34 +126,32 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *,
     """(y, s) of [rows][n] tensors: s = x + delta, y = s / sqrt(mean(s^2) + eps) * weight.
     Without delta, s is x itself.  sum_out may be x or delta (the residual stream kept in
     place), out likewise, but not both the same."""
-    dtype, dev = x.dtype, x.get_device()
+    dtype, dev, shape = x.dtype, x.get_device(), x.shape
     flags = _type_flag(dtype)
-    shape = x.shape
     if len(shape) != 2:
         raise ValueError(f"x: two dimensions expected, got {tuple(shape)}")
     rows, n = shape
-    ldx = _rows(x, "x", dtype, dev, rows, n)
+    ldx = _rows(x, "x", dtype, dev, shape)
     w = _dense(weight, "weight", dtype, dev, (n,))
     ldy = n
     if out is None:
         out = torch.empty_like(x)
     else:
-        ldy = _rows(out, "out", dtype, dev, rows, n)
+        ldy = _rows(out, "out", dtype, dev, shape)
     dp = sp = ldd = lds = 0
     s = x
     if delta is not None:
-        dp, ldd, lds = delta.data_ptr(), _rows(delta, "delta", dtype, dev, rows, n), n
+        dp, ldd, lds = delta.data_ptr(), _rows(delta, "delta", dtype, dev, shape), n
         if sum_out is None:
             s = torch.empty_like(x)
         else:
-            s, lds = sum_out, _rows(sum_out, "sum_out", dtype, dev, rows, n)
+            s, lds = sum_out, _rows(sum_out, "sum_out", dtype, dev, shape)
         sp = s.data_ptr()
     elif sum_out is not None:
         raise ValueError("sum_out needs delta")
     if rows:
-        wq_add_rms_norm(_NORM.pack(WQ_ABI_VERSION, _NORM.size, x.data_ptr(), dp, w, sp,
-                                   out.data_ptr(), _stream(dev), rows, n, ldx, ldd, lds, ldy, eps,
-                                   flags, 0))
+        _norm_call(_NORM.pack(WQ_ABI_VERSION, _NORM.size, x.data_ptr(), dp, w, sp, out.data_ptr(),
+                              _stream(dev), rows, n, ldx, ldd, lds, ldy, eps, flags, 0))
     return out, s
 
 
@@ -209,9 +224,11 @@ def rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache:
     if q is not None:
         heads = q.shape[1]
         ldq = _heads(q, "q", dtype, dev, tokens, heads, d)
+        ldqo = heads * d
         if q_out is None:
             q_out = torch.empty_like(q)
-        ldqo = _heads(q_out, "q_out", dtype, dev, tokens, heads, d)
+        else:
+            ldqo = _heads(q_out, "q_out", dtype, dev, tokens, heads, d)
         qp, qo = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out needs q")
@@ -235,10 +252,9 @@ def rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache:
         pp = _dense(positions, "positions", torch.int32, dev,
                     (tokens,) if len(shape) == 1 else (axes, tokens))
     if tokens:
-        wq_rope_append(_ROPE.pack(WQ_ABI_VERSION, _ROPE.size, cache.packed, qp, k.data_ptr(),
-                                  v.data_ptr(), qo, sl, pp, fp, _stream(dev), tokens, heads, ldq,
-                                  ldk, ldv, ldqo, 2 * half, axes, *pairs, int(interleaved), flags,
-                                  0))
+        _rope_call(_ROPE.pack(WQ_ABI_VERSION, _ROPE.size, cache.packed, qp, k.data_ptr(),
+                              v.data_ptr(), qo, sl, pp, fp, _stream(dev), tokens, heads, ldq, ldk,
+                              ldv, ldqo, 2 * half, axes, *pairs, interleaved, flags, 0))
     return q_out
 
 
@@ -271,9 +287,11 @@ class PagedAttention:
         cache, b, heads, dtype = self.cache, self.batch, self.q_heads, self.dtype
         dev, d = cache.dev, cache.head_dim
         ldq = _heads(q, "q", dtype, dev, b, heads, d)
+        ldo = heads * d
         if out is None:
             out = torch.empty_like(q)
-        ldo = _heads(out, "out", dtype, dev, b, heads, d)
+        else:
+            ldo = _heads(out, "out", dtype, dev, b, heads, d)
         pages = block_table.shape[-1]
         table = _dense(block_table, "block_table", torch.int32, dev, (b, pages))
         n = _dense(lens, "lens", torch.int32, dev, (b,))
@@ -284,11 +302,12 @@ class PagedAttention:
         if lse is not False:
             if lse is True:
                 lse = torch.empty_like(self._lse)
-            lp = _dense(lse, "lse", torch.float32, dev, (b, heads))
-        wq_paged_attention(_ATTN.pack(WQ_ABI_VERSION, _ATTN.size, cache.packed, q.data_ptr(),
-                                      out.data_ptr(), lp, table, n, kp, *self._space,
-                                      _stream(dev), b, heads, self.max_len, pages, keep_stride,
-                                      ldq, ldo, *self._last))
+                lp = lse.data_ptr()
+            else:
+                lp = _dense(lse, "lse", torch.float32, dev, (b, heads))
+        _attn_call(_ATTN.pack(WQ_ABI_VERSION, _ATTN.size, cache.packed, q.data_ptr(),
+                              out.data_ptr(), lp, table, n, kp, *self._space, _stream(dev), b,
+                              heads, self.max_len, pages, keep_stride, ldq, ldo, *self._last))
         return out if lse is False else (out, lse)
 
 
@@ -338,20 +357,21 @@ class MoELayer:
     def __call__(self, x: torch.Tensor, *, residual: torch.Tensor | None = None,
                  out: torch.Tensor | None = None) -> torch.Tensor:
         """residual + the layer's output for x [tokens][hidden] (out may be residual or x)."""
-        tokens, hidden, dtype, dev = x.shape[0], self.hidden, self.dtype, self.dev
-        if not 0 < tokens <= self.max_tokens:
-            raise ValueError(f"1 to {self.max_tokens} tokens expected, got {tokens}")
-        ldx = _rows(x, "x", dtype, dev, tokens, hidden)
+        hidden, dtype, dev, shape = self.hidden, self.dtype, self.dev, x.shape
+        tokens = shape[0]
+        if not 0 < tokens <= self.max_tokens or shape[1:] != (hidden,):
+            raise ValueError(f"x: [1 to {self.max_tokens}][{hidden}] expected, got {tuple(shape)}")
+        ldx = _rows(x, "x", dtype, dev, shape)
         ldy = hidden
         if out is None:
             out = torch.empty_like(x)
         else:
-            ldy = _rows(out, "out", dtype, dev, tokens, hidden)
+            ldy = _rows(out, "out", dtype, dev, shape)
         rp = ldr = 0
         if residual is not None:
-            rp, ldr = residual.data_ptr(), _rows(residual, "residual", dtype, dev, tokens, hidden)
+            rp, ldr = residual.data_ptr(), _rows(residual, "residual", dtype, dev, shape)
         router, gate_up, down = self._banks
-        wq_moe_layer(_MOE.pack(WQ_ABI_VERSION, _MOE.size, x.data_ptr(), router, gate_up, down, rp,
-                               out.data_ptr(), *self._space, _stream(dev), tokens, self.n_expert,
-                               self.top_k, hidden, self.inter, ldx, ldr, ldy, *self._last))
+        _moe_call(_MOE.pack(WQ_ABI_VERSION, _MOE.size, x.data_ptr(), router, gate_up, down, rp,
+                            out.data_ptr(), *self._space, _stream(dev), tokens, self.n_expert,
+                            self.top_k, hidden, self.inter, ldx, ldr, ldy, *self._last))
         return out

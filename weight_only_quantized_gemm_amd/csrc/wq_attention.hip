@@ -181,6 +181,32 @@ __device__ __forceinline__ bool find_piece(const AttnArgs& p, int index, int lan
   }
 }
 
+// Eight values >= 0 as high + low 16-bit parts.
+template <bool BF16>
+__device__ __forceinline__ void split_p(const float* p, f16x8& high, f16x8& low) {
+  uint32_t hi[4], lo[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float x = p[2 * i], y = p[2 * i + 1];
+    if constexpr (BF16) {
+      const uint32_t xb = __builtin_bit_cast(uint32_t, x) & 0xffff0000u;
+      const uint32_t yb = __builtin_bit_cast(uint32_t, y) & 0xffff0000u;
+      hi[i] = xb >> 16 | yb;
+      const float xl = fmaxf(x - __builtin_bit_cast(float, xb), 0x1p-100f);
+      const float yl = fmaxf(y - __builtin_bit_cast(float, yb), 0x1p-100f);
+      lo[i] = (uint32_t)Act<true>::round(xl) | (uint32_t)Act<true>::round(yl) << 16;
+    } else {
+      const auto h = __builtin_amdgcn_cvt_pkrtz(x, y);
+      hi[i] = __builtin_bit_cast(uint32_t, h);
+      const auto r = __builtin_amdgcn_cvt_pkrtz(fmaxf(x - (float)h[0], 0x1p-24f),
+                                                fmaxf(y - (float)h[1], 0x1p-24f));
+      lo[i] = __builtin_bit_cast(uint32_t, r);
+    }
+  }
+  __builtin_memcpy(&high, hi, 16);
+  __builtin_memcpy(&low, lo, 16);
+}
+
 // DP: head_dim rounded up to 64, 128 or 256; FULL: head_dim is DP.
 template <bool BF16, bool KV8, int DP, bool FULL>
 __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
@@ -379,20 +405,17 @@ __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
         for (int e = 0; e < 4; ++e) o[i][e] *= alpha;
     }
     m = m_new;
-    uint16_t hi[8], lw[8];
-#pragma unroll
-    for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float x = __builtin_amdgcn_exp2f(s[blk][e] - ref);
-        l += x;
-        const uint16_t h = A::round(x);
-        hi[4 * blk + e] = h;
-        lw[4 * blk + e] = A::round(x - A::value(h));
-      }
+    // high + low: the high part is cut off, not rounded, so that the low part is never
+    // negative, and it is kept above 0 (by 2^-39 of the largest p at most): an infinite value
+    // of V then stays infinite
     f16x8 ph, pl;
-    __builtin_memcpy(&ph, hi, 16);
-    __builtin_memcpy(&pl, lw, 16);
+    float ps[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      ps[i] = __builtin_amdgcn_exp2f(s[i / 4][i % 4] - ref);
+      l += ps[i];
+    }
+    split_p<BF16>(ps, ph, pl);
 
     // V to LDS as 16-bit rows, zero where a position is not live
 #pragma unroll

@@ -1,11 +1,11 @@
 // Attention of one new token per sequence over a paged KV cache (wq_paged_attention).
 //
 // Each live K and V element is read once and takes part in 2 * (query heads per KV head)
-// products, so the kernel is bound by the cache reads.  A work-group handles one sequence, one KV head and up to 16
-// of its query heads over a range of positions (a split); its waves take tiles of 32
-// positions in turn and keep their own running maximum, sum and output, joined at the end
-// through LDS.  Splits of long sequences leave fp32 partials that attn_join_kernel adds in
-// split order.
+// products, so the kernel is bound by the cache reads.  The batch's positions are cut into
+// equal ranges; a work-group takes a range for one KV head and up to 16 of its query heads.
+// Its waves take tiles of 32 or 64 positions in turn and keep their own running maximum, sum
+// and output, joined at the end of each sequence through LDS.  Sequences that lie in several
+// ranges leave fp32 partials that attn_join_kernel adds in their order.
 //
 // Both products run on 16x16x32 MFMAs with the positions as rows:
 //  - S^T = K Q^T: the A operand is K straight from memory (a lane holds 8 consecutive
@@ -32,8 +32,12 @@ namespace wq {
 namespace {
 
 constexpr int kWaves = 4;
-constexpr int kTile = 32;  // positions of a wave's step
-constexpr int kStep = kWaves * kTile;
+
+// Positions of a wave's step (dp: head_dim rounded up to 64, 128 or 256).  64 rows of an E4M3
+// head of 128 keep 16 KiB requested, as 32 of a 16-bit one do (16 sequences of 4096 positions:
+// 36.4 us with 32, 34.7 with 64; one of 65536: 35.3 and 32.7).  16-bit heads of 64 are faster
+// with 32, whose registers leave room for a third work-group on the CU.
+constexpr int tile_of(int dp, bool kv8) { return kv8 && dp <= 128 ? 64 : 32; }
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -49,17 +53,16 @@ struct AttnArgs {
   const float *k_scale, *v_scale;
   const int32_t *table, *lens;
   const uint8_t* keep;
-  // Partials of the split sequences' work-groups: [part][16 or fewer query heads].
+  // Partials of sequences that no range holds whole: [2 ranges][units][part_rows].
   float* part_o;   // [d], not divided by the sum
   float* part_ml;  // [2]: maximum (times log2 e) and sum
-  int32_t* parts;  // [batch][2]: splits of each sequence and its first partial
+  int32_t* parts;  // [batch][2]: the ranges that hold a part of each sequence: first, count
   int64_t page_stride, slot_stride, head_stride;
   int num_pages, page_size, kv_heads, q_heads, d, group, head_blocks, max_len;
   int table_stride, keep_stride, ldq, ldo, window, batch;
-  int units;       // work-groups of a sequence's split: KV heads times head blocks
+  int units;       // work-groups of a range: KV heads times head blocks
   int part_rows;   // query heads of a partial: 16, or the group where it is smaller
-  int target;      // most splits of all sequences; 0: none is split
-  int round;       // splits that the CUs take at once
+  int ranges;      // most ranges that the batch is cut into; 0: one for each sequence
   uint32_t page_mul;  // position / page_size = umulhi(2 * position, page_mul) >> page_shift
   int page_shift;
   float scale, softcap;
@@ -89,28 +92,15 @@ __device__ __forceinline__ f16x8 from_e4m3(uint32_t lo, uint32_t hi) {
   return __builtin_bit_cast(f16x8, Act<BF16>::fp8(lo, hi));
 }
 
-__device__ __forceinline__ int wave_max(int x) {  // of values >= 0
-  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false));
-  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false));
-  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false));
-  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false));
-  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false));
-  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false));
-  return __builtin_amdgcn_readlane(x, 63);
-}
-
-// What a work-group does: granules [first, last) of kStep positions of sequence b, as one of
-// `splits` splits; part: its partial (splits > 1).
-struct Piece {
-  int b, len, splits, part, first, last;
-};
-
-// Positions of a sequence that may be live start in the tile of the window's first one.
+// Positions of a sequence that may be live start in the tile of the window's first one; they
+// are dealt out in granules of a tile for each wave.
+template <int TILE>
 __device__ __forceinline__ int window_start(const AttnArgs& p, int len) {
-  return p.window > 0 ? max(0, len - p.window) & ~(kTile - 1) : 0;
+  return p.window > 0 ? max(0, len - p.window) & ~(TILE - 1) : 0;
 }
+template <int TILE>
 __device__ __forceinline__ int granules_of(const AttnArgs& p, int len) {
-  return (len - window_start(p, len) + kStep - 1) / kStep;
+  return (len - window_start<TILE>(p, len) + kWaves * TILE - 1) / (kWaves * TILE);
 }
 
 // Inclusive sum over the wave's lanes.
@@ -124,61 +114,53 @@ __device__ __forceinline__ int wave_scan(int x) {
   return x;
 }
 
-// The index-th split of the batch; false past the last.  The sequences' lengths are known
-// only here, so every wave divides them alike, each lane counting a run of sequences: the
-// smallest chunks (to an eighth) that give no more than `target` splits over all sequences.
-// (Cut by the longest length alone, as the host could, half the work-groups of a ragged batch
-// were empty and the rest uneven: 64 sequences of up to 8192 positions, E4M3, 114 against
-// 81 us.)
-__device__ __forceinline__ bool find_piece(const AttnArgs& p, int index, int lane, Piece& out) {
+// A range's first sequence, the first of its granules there, and how many granules it has,
+// over this and the next sequences.
+struct Range {
+  int b, first, left;
+};
+
+// The index-th range; false past the last.  All sequences' granules, one sequence after the
+// other, are cut into `ranges` equal ranges.  The lengths are known only here, so every wave
+// counts them, each lane a run of sequences.  (64 sequences of up to 8192 positions, E4M3: cut
+// by the host by the longest length 135 us, in equal splits of each sequence 93.7, as here
+// 88.8; unmasked 121.7 in equal splits, 112.5 here.)
+template <int TILE>
+__device__ __forceinline__ bool find_range(const AttnArgs& p, int index, bool publish, int lane,
+                                           Range& out) {
   const int run = (p.batch + 63) / 64;
   const int b0 = lane * run, b1 = min(p.batch, b0 + run);
-  const auto length = [&](int b) { return max(0, min(p.lens[b], p.max_len)); };
-  int sum = 0, longest = 0;
-  for (int b = b0; b < b1; ++b) {
-    const int n = granules_of(p, length(b));
-    sum += n;
-    longest = max(longest, n);
-  }
-  sum = __builtin_amdgcn_readlane(wave_scan(sum), 63);
-  longest = wave_max(longest);
-  int chunk = max(1, (sum + p.target - 1) / p.target);
-  // sequences that are even enough for one round of work-groups are left whole
-  if ((int64_t)longest * 4 * p.round <= (int64_t)sum * 5) chunk = max(1, longest);
-  while (chunk < longest) {
-    int n = 0;
-    for (int b = b0; b < b1; ++b) n += max(1, (granules_of(p, length(b)) + chunk - 1) / chunk);
-    if (__builtin_amdgcn_readlane(wave_scan(n), 63) <= p.target) break;
-    chunk += (chunk + 7) / 8;
-  }
-  // splits in the low 18 bits (at most batch or target), partials above (at most target)
-  const auto counts = [&](int n) {
-    const int splits = max(1, (n + chunk - 1) / chunk);
-    return splits | (splits > 1 ? splits << 18 : 0);
+  const auto granules = [&](int b) {
+    return granules_of<TILE>(p, max(0, min(p.lens[b], p.max_len)));
   };
-  constexpr int kLow = (1 << 18) - 1;
   int mine = 0;
-  for (int b = b0; b < b1; ++b) mine += counts(granules_of(p, length(b)));
-  int at = wave_scan(mine);
-  const unsigned long long above = __ballot(index < (at & kLow));
-  if (above == 0) return false;
-  const int owner = __builtin_ctzll(above);
-  // the owner's run, on every lane
-  at = __builtin_amdgcn_readlane(at - mine, owner);
-  for (int b = owner * run;; ++b) {
-    const int len = length(b), n = granules_of(p, len), c = counts(n);
-    if (index < ((at + c) & kLow)) {
-      const int splits = c & kLow, split = index - (at & kLow);
-      out.b = b;
-      out.len = len;
-      out.splits = splits;
-      out.part = (at >> 18) + split;
-      out.first = (int)((int64_t)n * split / splits);
-      out.last = (int)((int64_t)n * (split + 1) / splits);
-      return true;
+  for (int b = b0; b < b1; ++b) mine += granules(b);
+  const int end = wave_scan(mine);
+  const int total = __builtin_amdgcn_readlane(end, 63);
+  const int chunk = max(1, (total + p.ranges - 1) / p.ranges);
+  if (publish) {  // where the join finds each sequence's parts
+    int at = end - mine;
+    for (int b = b0; b < b1; ++b) {
+      const int n = granules(b);
+      p.parts[2 * b] = at / chunk;
+      p.parts[2 * b + 1] = n == 0 ? 0 : (at + n - 1) / chunk - at / chunk + 1;
+      at += n;
     }
-    at += c;
   }
+  const int g0 = index * chunk;
+  if (g0 >= total) return false;
+  const int owner = __builtin_ctzll(__ballot(g0 < end));
+  int at = __builtin_amdgcn_readlane(end - mine, owner);
+  int b = owner * run;
+  for (;; ++b) {
+    const int n = granules(b);
+    if (g0 < at + n) break;
+    at += n;
+  }
+  out.b = b;
+  out.first = g0 - at;
+  out.left = min(chunk, total - g0);
+  return true;
 }
 
 // Eight values >= 0 as high + low 16-bit parts.
@@ -211,295 +193,314 @@ __device__ __forceinline__ void split_p(const float* p, f16x8& high, f16x8& low)
 template <bool BF16, bool KV8, int DP, bool FULL>
 __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
   using A = Act<BF16>;
+  constexpr int TILE = tile_of(DP, KV8), kStep = kWaves * TILE;
+  constexpr int NT = TILE / 16;          // 16-position blocks of a tile
   constexpr int NS = DP / 32;            // MFMA steps along the head
   constexpr int NK = KV8 ? NS / 2 : NS;  // 16-byte K vectors per lane and position block
   constexpr int CE = KV8 ? 16 : 8;       // elements of a 16-byte vector
   constexpr int CPR = DP / CE;           // vectors of a V row
   constexpr int RPI = 64 / CPR;          // V rows of one load
-  constexpr int NV = kTile / RPI;
+  constexpr int NV = TILE / RPI;
   constexpr int NB = DP / 16;            // 16-element blocks of the output
   constexpr int VS = DP + 16;            // LDS row of V: rows start 8 banks apart
   constexpr int OS = DP + 4;             // LDS row of the joined outputs
-  constexpr int kVBytes = kWaves * kTile * VS * 2, kOBytes = kWaves * 16 * OS * 4;
+  constexpr int kVBytes = kWaves * TILE * VS * 2, kOBytes = kWaves * 16 * OS * 4;
   __shared__ __align__(16) uint8_t lds[kVBytes > kOBytes ? kVBytes : kOBytes];
-  __shared__ int64_t off_lds[kWaves][kTile];
+  __shared__ int64_t off_lds[kWaves][TILE];
   __shared__ float ml_lds[kWaves][16][2];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row = lane & 15, qd = lane >> 4;
   const int index = blockIdx.x / p.units, unit = blockIdx.x - index * p.units;
-  Piece pc{index, 0, 1, 0, 0, 0};
-  if (p.target > 0) {
-    if (!find_piece(p, index, lane, pc)) return;
-  } else {
-    pc.len = max(0, min(p.lens[index], p.max_len));
-  }
-  const int b = pc.b, len = pc.len, splits = pc.splits, part = pc.part;
-  const int lo = p.window > 0 ? max(0, len - p.window) : 0;  // first live position
-  int t0 = window_start(p, len), t1 = len;
-  // Page numbers are read for positions below t_pages: without splits or a window they need
-  // not wait for the length.
-  const int t_pages = p.target > 0 || p.window > 0 ? len : p.max_len;
-  if (p.target > 0) {
-    t1 = min(len, t0 + pc.last * kStep);
-    t0 += pc.first * kStep;
-    if (unit == 0 && pc.first == 0 && threadIdx.x == 0) {
-      p.parts[2 * b] = splits;
-      p.parts[2 * b + 1] = part;
-    }
-  }
+  Range rg{index, 0, 0};
+  if (p.ranges > 0 && !find_range<TILE>(p, index, blockIdx.x == 0 && wave == 0, lane, rg)) return;
   const int kvh = unit / p.head_blocks, hb = unit - kvh * p.head_blocks;
   const int h0 = kvh * p.group + 16 * hb;         // first query head
   const int rows = min(16, p.group - 16 * hb);
 
-  // Q as the B operand; query heads past the last repeat the first (never stored).
-  f16x8 qf[NS];
-  {
-    const uint16_t* qp = p.q + (int64_t)b * p.ldq + (int64_t)(h0 + (row < rows ? row : 0)) * p.d;
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      const int e = KV8 ? 64 * (s / 2) + 16 * qd + 8 * (s % 2) : 32 * s + 8 * qd;
-      qf[s] = f16x8{};
-      if (FULL || e < p.d) qf[s] = *reinterpret_cast<const f16x8*>(qp + e);
+  for (;;) {  // the range's sequences
+    const int b = rg.b;
+    const int len = max(0, min(p.lens[b], p.max_len));
+    const int lo = p.window > 0 ? max(0, len - p.window) : 0;  // first live position
+    const int granules = granules_of<TILE>(p, len);
+    int t0 = window_start<TILE>(p, len), t1 = len;
+    // Page numbers are read for positions below t_pages: without ranges or a window they need
+    // not wait for the length.
+    const int t_pages = p.ranges > 0 || p.window > 0 ? len : p.max_len;
+    int count = granules;
+    if (p.ranges > 0) {
+      count = min(granules - rg.first, rg.left);
+      t1 = min(len, t0 + (rg.first + count) * kStep);
+      t0 += rg.first * kStep;
     }
-  }
 
-  const uint8_t* kbase = p.k + kvh * p.head_stride * (KV8 ? 1 : 2);
-  const uint8_t* vbase = p.v + kvh * p.head_stride * (KV8 ? 1 : 2);
-  const int32_t* table = p.table + (int64_t)b * p.table_stride;
-  const uint8_t* keep = p.keep != nullptr ? p.keep + (int64_t)b * p.keep_stride : nullptr;
-
-  // A vector that lies past the head's end is read from its start and not used; an E4M3
-  // vector that passes the end half way (head_dim % 16 == 8) is read 8 bytes earlier and
-  // shifted.
-  const auto vec_at = [&](int e) {
-    return FULL || e + CE <= p.d ? e : (e < p.d ? p.d - CE : 0);
-  };
-  const auto vec_fix = [&](u32x4 w, int e) {
-    if (FULL) return w;
-    if (KV8 && e < p.d && e + CE > p.d) w = u32x4{w[2], w[3], 0u, 0u};
-    return e < p.d ? w : u32x4{0u, 0u, 0u, 0u};
-  };
-
-  // Page numbers (and keep bytes) of the tile at t, one position per lane and half-wave.
-  int page_next = -1, pos_next = 0, slot_next = 0;
-  uint8_t keep_next = 1;
-  const auto read_pages = [&](int t) {
-    const int pos = t + (lane & (kTile - 1));
-    const int at = (int)(__umulhi(2u * (unsigned)pos, p.page_mul) >> p.page_shift);
-    pos_next = pos;
-    slot_next = pos - at * p.page_size;
-    page_next = -1;
-    if (pos < t_pages) {
-      page_next = table[at];
-      if (keep != nullptr) keep_next = keep[pos];
-    }
-  };
-  // Cache offsets of the tile whose pages were read; returns the mask of live positions.  A
-  // position that is not live reads the cache's first slot, and is not used.
-  const auto place = [&]() -> uint32_t {
-    const bool live = (unsigned)page_next < (unsigned)p.num_pages && keep_next != 0 &&
-                      pos_next >= lo && pos_next < t1;
-    off_lds[wave][lane & (kTile - 1)] =
-        live ? page_next * p.page_stride + slot_next * p.slot_stride : 0;
-    return (uint32_t)__ballot(live);
-  };
-  u32x4 kr[2][NK], vr[NV];
-  const auto load_k = [&] {
+    // Q as the B operand; query heads past the last repeat the first (never stored).
+    f16x8 qf[NS];
+    {
+      const uint16_t* qp = p.q + (int64_t)b * p.ldq + (int64_t)(h0 + (row < rows ? row : 0)) * p.d;
 #pragma unroll
-    for (int blk = 0; blk < 2; ++blk) {
-      const uint8_t* kp = kbase + off_lds[wave][16 * blk + row] * (KV8 ? 1 : 2);
-#pragma unroll
-      for (int s = 0; s < NK; ++s)
-        kr[blk][s] = *reinterpret_cast<const u32x4*>(
-            kp + vec_at(4 * CE * s + CE * qd) * (KV8 ? 1 : 2));
-    }
-  };
-  const int vcol = CE * (lane % CPR);
-  const auto load_v = [&] {
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      vr[j] = *reinterpret_cast<const u32x4*>(
-          vbase + (off_lds[wave][j * RPI + lane / CPR] + vec_at(vcol)) * (KV8 ? 1 : 2));
-  };
-
-  uint16_t* const v_lds = reinterpret_cast<uint16_t*>(lds) + wave * kTile * VS;
-  const float kscale = KV8 && p.k_scale != nullptr ? p.k_scale[kvh] : 1.f;
-  const float sc = p.scale * kscale;
-  const float sc2 = p.softcap > 0.f ? kLog2e : sc * kLog2e;
-  const float cap = sc / p.softcap;
-  float m = -INFINITY, l = 0.f;
-  f32x4 o[NB];
-#pragma unroll
-  for (int i = 0; i < NB; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  int t = t0 + wave * kTile;
-  read_pages(t);  // (a wave without a tile reads the cache's first slot, and ends)
-  wave_lds_fence();
-  uint32_t live = place();
-  wave_lds_fence();
-  read_pages(t + kStep);
-  load_k();
-  load_v();
-  for (; t < t1; t += kStep) {
-    // scores
-    f32x4 s[2];
-#pragma unroll
-    for (int blk = 0; blk < 2; ++blk) {
-      s[blk] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        f16x8 kf;
-        if constexpr (KV8) {
-          const u32x4 w = vec_fix(kr[blk][i / 2], 64 * (i / 2) + 16 * qd);
-          kf = from_e4m3<BF16>(w[2 * (i % 2)], w[2 * (i % 2) + 1]);
-        } else {
-          kf = __builtin_bit_cast(f16x8, vec_fix(kr[blk][i], 32 * i + 8 * qd));
-        }
-        s[blk] = mfma<BF16>(kf, qf[i], s[blk]);
+      for (int s = 0; s < NS; ++s) {
+        const int e = KV8 ? 64 * (s / 2) + 16 * qd + 8 * (s % 2) : 32 * s + 8 * qd;
+        qf[s] = f16x8{};
+        if (FULL || e < p.d) qf[s] = *reinterpret_cast<const f16x8*>(qp + e);
       }
     }
-    const uint32_t now = live;
-    // the next tile's K (positions past the range are not live and read the first slot)
+
+    const uint8_t* kbase = p.k + kvh * p.head_stride * (KV8 ? 1 : 2);
+    const uint8_t* vbase = p.v + kvh * p.head_stride * (KV8 ? 1 : 2);
+    const int32_t* table = p.table + (int64_t)b * p.table_stride;
+    const uint8_t* keep = p.keep != nullptr ? p.keep + (int64_t)b * p.keep_stride : nullptr;
+
+    // A vector that lies past the head's end is read from its start and not used; an E4M3
+    // vector that passes the end half way (head_dim % 16 == 8) is read 8 bytes earlier and
+    // shifted.
+    const auto vec_at = [&](int e) {
+      return FULL || e + CE <= p.d ? e : (e < p.d ? p.d - CE : 0);
+    };
+    const auto vec_fix = [&](u32x4 w, int e) {
+      if (FULL) return w;
+      if (KV8 && e < p.d && e + CE > p.d) w = u32x4{w[2], w[3], 0u, 0u};
+      return e < p.d ? w : u32x4{0u, 0u, 0u, 0u};
+    };
+
+    // Page numbers (and keep bytes) of the tile at t, one position per lane and half-wave.
+    int page_next = -1, pos_next = 0, slot_next = 0;
+    uint8_t keep_next = 1;
+    const auto read_pages = [&](int t) {
+      const int pos = t + (lane & (TILE - 1));
+      const int at = (int)(__umulhi(2u * (unsigned)pos, p.page_mul) >> p.page_shift);
+      pos_next = pos;
+      slot_next = pos - at * p.page_size;
+      page_next = -1;
+      if (pos < t_pages) {
+        page_next = table[at];
+        if (keep != nullptr) keep_next = keep[pos];
+      }
+    };
+    // Cache offsets of the tile whose pages were read; returns the mask of live positions.  A
+    // position that is not live reads the cache's first slot, and is not used.
+    const auto place = [&]() -> uint64_t {
+      const bool live = (unsigned)page_next < (unsigned)p.num_pages && keep_next != 0 &&
+                        pos_next >= lo && pos_next < t1;
+      off_lds[wave][lane & (TILE - 1)] =
+          live ? page_next * p.page_stride + slot_next * p.slot_stride : 0;
+      return __ballot(live);
+    };
+    u32x4 kr[NT][NK], vr[NV];
+    const auto load_k = [&] {
+#pragma unroll
+      for (int blk = 0; blk < NT; ++blk) {
+        const uint8_t* kp = kbase + off_lds[wave][16 * blk + row] * (KV8 ? 1 : 2);
+#pragma unroll
+        for (int s = 0; s < NK; ++s)
+          kr[blk][s] = *reinterpret_cast<const u32x4*>(
+              kp + vec_at(4 * CE * s + CE * qd) * (KV8 ? 1 : 2));
+      }
+    };
+    const int vcol = CE * (lane % CPR);
+    const auto load_v = [&] {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        vr[j] = *reinterpret_cast<const u32x4*>(
+            vbase + (off_lds[wave][j * RPI + lane / CPR] + vec_at(vcol)) * (KV8 ? 1 : 2));
+    };
+
+    uint16_t* const v_lds = reinterpret_cast<uint16_t*>(lds) + wave * TILE * VS;
+    const float kscale = KV8 && p.k_scale != nullptr ? p.k_scale[kvh] : 1.f;
+    const float sc = p.scale * kscale;
+    const float sc2 = p.softcap > 0.f ? kLog2e : sc * kLog2e;
+    const float cap = sc / p.softcap;
+    float m = -INFINITY, l = 0.f;
+    f32x4 o[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    int t = t0 + wave * TILE;
+    read_pages(t);  // (a wave without a tile reads the cache's first slot, and ends)
     wave_lds_fence();
-    live = place();
+    uint64_t live = place();
     wave_lds_fence();
-    read_pages(t + 2 * kStep);
+    read_pages(t + kStep);
     load_k();
-
-    // running maximum and sum, in base 2
-    float mx = -INFINITY;
-    if (p.softcap > 0.f) {
-#pragma unroll
-      for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[blk][e] = p.softcap * fast_tanh(s[blk][e] * cap);
-    }
-#pragma unroll
-    for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[blk][e] *= sc2;
-    if (now != 0xFFFFFFFFu) {
-#pragma unroll
-      for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          s[blk][e] = (now >> (16 * blk + 4 * qd + e)) & 1u ? s[blk][e] : -INFINITY;
-    }
-#pragma unroll
-    for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) mx = fmaxf(mx, s[blk][e]);
-    mx = fmaxf(mx, __shfl_xor(mx, 16));
-    mx = fmaxf(mx, __shfl_xor(mx, 32));
-    const float m_new = fmaxf(m, mx);
-    const float top = m_new == -INFINITY ? 0.f : m_new;  // nothing live so far
-    const float ref = top - kPShift<BF16>;
-    const float alpha = __builtin_amdgcn_exp2f(m - top);
-    if (__ballot(m_new > m)) {  // some head's maximum moved
-      l *= alpha;
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][e] *= alpha;
-    }
-    m = m_new;
-    // high + low: the high part is cut off, not rounded, so that the low part is never
-    // negative, and it is kept above 0 (by 2^-39 of the largest p at most): an infinite value
-    // of V then stays infinite
-    f16x8 ph, pl;
-    float ps[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      ps[i] = __builtin_amdgcn_exp2f(s[i / 4][i % 4] - ref);
-      l += ps[i];
-    }
-    split_p<BF16>(ps, ph, pl);
-
-    // V to LDS as 16-bit rows, zero where a position is not live
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int r = j * RPI + lane / CPR;
-      u32x4 w = vec_fix(vr[j], vcol);
-      if (now != 0xFFFFFFFFu && !((now >> r) & 1u)) w = u32x4{0u, 0u, 0u, 0u};
-      if constexpr (KV8) {
-        *reinterpret_cast<f16x8*>(v_lds + r * VS + vcol) = from_e4m3<BF16>(w[0], w[1]);
-        *reinterpret_cast<f16x8*>(v_lds + r * VS + vcol + 8) = from_e4m3<BF16>(w[2], w[3]);
-      } else {
-        *reinterpret_cast<u32x4*>(v_lds + r * VS + vcol) = w;
-      }
-    }
-    wave_lds_fence();
     load_v();
-
+    for (; t < t1; t += kStep) {
+      // scores
+      f32x4 s[NT];
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const uint16_t* src = v_lds + (4 * qd + (row >> 2)) * VS + 16 * i + 4 * (row & 3);
-      const s16x4 a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)src);
-      const s16x4 a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(src + 16 * VS));
-      f16x8 vf;
-      __builtin_memcpy(&vf, &a0, 8);
-      __builtin_memcpy(reinterpret_cast<char*>(&vf) + 8, &a1, 8);
-      o[i] = mfma<BF16>(vf, ph, o[i]);
-      o[i] = mfma<BF16>(vf, pl, o[i]);
-    }
-    wave_lds_fence();
-  }
-
-  // Join the waves, in wave order.
-  l += __shfl_xor(l, 16);
-  l += __shfl_xor(l, 32);
-  __syncthreads();  // every wave is done with its V rows
-  float* const o_lds = reinterpret_cast<float*>(lds);
-  if (qd == 0) {
-    ml_lds[wave][row][0] = m - kPShift<BF16>;
-    ml_lds[wave][row][1] = l;
-  }
+      for (int blk = 0; blk < NT; ++blk) {
+        s[blk] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < NB; ++i)
-    *reinterpret_cast<f32x4*>(o_lds + (wave * 16 + row) * OS + 16 * i + 4 * qd) = o[i];
-  __syncthreads();
-  const int per_row = p.d / 4;
-  const float vscale = KV8 && p.v_scale != nullptr ? p.v_scale[kvh] : 1.f;
-  for (int i = threadIdx.x; i < rows * per_row; i += kWaves * 64) {
-    const int r = i / per_row, e = 4 * (i - r * per_row);
-    float top = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, ml_lds[w][r][0]);
-    const float ref = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const float f = __builtin_amdgcn_exp2f(ml_lds[w][r][0] - ref);
-      sum = __builtin_fmaf(ml_lds[w][r][1], f, sum);
-      const f32x4 x = *reinterpret_cast<const f32x4*>(o_lds + (w * 16 + r) * OS + e);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[c] = __builtin_fmaf(x[c], f, acc[c]);
-    }
-    const int64_t h = (int64_t)b * p.q_heads + h0 + r;
-    if (splits > 1) {
-      const int64_t at = ((int64_t)part * p.units + unit) * p.part_rows + r;
-      *reinterpret_cast<f32x4*>(p.part_o + at * p.d + e) = acc;
-      if (e == 0) {
-        p.part_ml[at * 2] = top;
-        p.part_ml[at * 2 + 1] = sum;
+        for (int i = 0; i < NS; ++i) {
+          f16x8 kf;
+          if constexpr (KV8) {
+            const u32x4 w = vec_fix(kr[blk][i / 2], 64 * (i / 2) + 16 * qd);
+            kf = from_e4m3<BF16>(w[2 * (i % 2)], w[2 * (i % 2) + 1]);
+          } else {
+            kf = __builtin_bit_cast(f16x8, vec_fix(kr[blk][i], 32 * i + 8 * qd));
+          }
+          s[blk] = mfma<BF16>(kf, qf[i], s[blk]);
+        }
       }
-    } else {
-      const float f = sum == 0.f ? 0.f : vscale / sum;
-      uint16_t* dst = p.out + (int64_t)b * p.ldo + (int64_t)(h0 + r) * p.d + e;
-      *reinterpret_cast<u32x2*>(dst) =
-          u32x2{(uint32_t)A::round(acc[0] * f) | ((uint32_t)A::round(acc[1] * f) << 16),
-                (uint32_t)A::round(acc[2] * f) | ((uint32_t)A::round(acc[3] * f) << 16)};
-      if (e == 0 && p.lse != nullptr)
-        p.lse[h] = sum == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+      const uint64_t now = live;
+      // the next tile's K (positions past the range are not live and read the first slot)
+      wave_lds_fence();
+      live = place();
+      wave_lds_fence();
+      read_pages(t + 2 * kStep);
+      load_k();
+
+      // running maximum and sum, in base 2
+      float mx = -INFINITY;
+      if (p.softcap > 0.f) {
+#pragma unroll
+        for (int blk = 0; blk < NT; ++blk)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[blk][e] = p.softcap * fast_tanh(s[blk][e] * cap);
+      }
+#pragma unroll
+      for (int blk = 0; blk < NT; ++blk)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[blk][e] *= sc2;
+      if (now != ~0ull) {
+#pragma unroll
+        for (int blk = 0; blk < NT; ++blk)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            s[blk][e] = (now >> (16 * blk + 4 * qd + e)) & 1 ? s[blk][e] : -INFINITY;
+      }
+#pragma unroll
+      for (int blk = 0; blk < NT; ++blk)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx = fmaxf(mx, s[blk][e]);
+      mx = fmaxf(mx, __shfl_xor(mx, 16));
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      const float m_new = fmaxf(m, mx);
+      const float top = m_new == -INFINITY ? 0.f : m_new;  // nothing live so far
+      const float ref = top - kPShift<BF16>;
+      const float alpha = __builtin_amdgcn_exp2f(m - top);
+      if (__ballot(m_new > m)) {  // some head's maximum moved
+        l *= alpha;
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][e] *= alpha;
+      }
+      m = m_new;
+      // high + low: the high part is cut off, not rounded, so that the low part is never
+      // negative, and it is kept above 0 (by 2^-39 of the largest p at most): an infinite value
+      // of V then stays infinite
+      f16x8 ph[NT / 2], pl[NT / 2];
+#pragma unroll
+      for (int k = 0; k < NT / 2; ++k) {
+        float ps[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          ps[i] = __builtin_amdgcn_exp2f(s[2 * k + i / 4][i % 4] - ref);
+          l += ps[i];
+        }
+        split_p<BF16>(ps, ph[k], pl[k]);
+      }
+
+      // V to LDS as 16-bit rows, zero where a position is not live
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int r = j * RPI + lane / CPR;
+        u32x4 w = vec_fix(vr[j], vcol);
+        if (now != ~0ull && !((now >> r) & 1)) w = u32x4{0u, 0u, 0u, 0u};
+        if constexpr (KV8) {
+          *reinterpret_cast<f16x8*>(v_lds + r * VS + vcol) = from_e4m3<BF16>(w[0], w[1]);
+          *reinterpret_cast<f16x8*>(v_lds + r * VS + vcol + 8) = from_e4m3<BF16>(w[2], w[3]);
+        } else {
+          *reinterpret_cast<u32x4*>(v_lds + r * VS + vcol) = w;
+        }
+      }
+      wave_lds_fence();
+      load_v();
+
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const uint16_t* src = v_lds + (4 * qd + (row >> 2)) * VS + 16 * i + 4 * (row & 3);
+#pragma unroll
+        for (int k = 0; k < NT / 2; ++k) {
+          const s16x4 a0 =
+              __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(src + 32 * k * VS));
+          const s16x4 a1 =
+              __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(src + (32 * k + 16) * VS));
+          f16x8 vf;
+          __builtin_memcpy(&vf, &a0, 8);
+          __builtin_memcpy(reinterpret_cast<char*>(&vf) + 8, &a1, 8);
+          o[i] = mfma<BF16>(vf, ph[k], o[i]);
+          o[i] = mfma<BF16>(vf, pl[k], o[i]);
+        }
+      }
+      wave_lds_fence();
     }
+
+    // Join the waves, in wave order.
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    __syncthreads();  // every wave is done with its V rows
+    float* const o_lds = reinterpret_cast<float*>(lds);
+    if (qd == 0) {
+      ml_lds[wave][row][0] = m - kPShift<BF16>;
+      ml_lds[wave][row][1] = l;
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+      *reinterpret_cast<f32x4*>(o_lds + (wave * 16 + row) * OS + 16 * i + 4 * qd) = o[i];
+    __syncthreads();
+    const int per_row = p.d / 4;
+    const float vscale = KV8 && p.v_scale != nullptr ? p.v_scale[kvh] : 1.f;
+    for (int i = threadIdx.x; i < rows * per_row; i += kWaves * 64) {
+      const int r = i / per_row, e = 4 * (i - r * per_row);
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) top = fmaxf(top, ml_lds[w][r][0]);
+      const float ref = top == -INFINITY ? 0.f : top;
+      float sum = 0.f;
+      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float f = __builtin_amdgcn_exp2f(ml_lds[w][r][0] - ref);
+        sum = __builtin_fmaf(ml_lds[w][r][1], f, sum);
+        const f32x4 x = *reinterpret_cast<const f32x4*>(o_lds + (w * 16 + r) * OS + e);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[c] = __builtin_fmaf(x[c], f, acc[c]);
+      }
+      const int64_t h = (int64_t)b * p.q_heads + h0 + r;
+      if (count < granules) {
+        // a sequence that began in an earlier range leaves the range's first partial, one that
+        // goes on in the next its second
+        const int64_t part = 2 * index + (rg.first == 0);
+        const int64_t at = (part * p.units + unit) * p.part_rows + r;
+        *reinterpret_cast<f32x4*>(p.part_o + at * p.d + e) = acc;
+        if (e == 0) {
+          p.part_ml[at * 2] = top;
+          p.part_ml[at * 2 + 1] = sum;
+        }
+      } else {
+        const float f = sum == 0.f ? 0.f : vscale / sum;
+        uint16_t* dst = p.out + (int64_t)b * p.ldo + (int64_t)(h0 + r) * p.d + e;
+        *reinterpret_cast<u32x2*>(dst) =
+            u32x2{(uint32_t)A::round(acc[0] * f) | ((uint32_t)A::round(acc[1] * f) << 16),
+                  (uint32_t)A::round(acc[2] * f) | ((uint32_t)A::round(acc[3] * f) << 16)};
+        if (e == 0 && p.lse != nullptr)
+          p.lse[h] = sum == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+      }
+    }
+    rg.left -= count;
+    if (rg.left <= 0) return;
+    rg.first = 0;
+    do {  // (granules are left, so a sequence with some follows)
+      ++rg.b;
+    } while (granules_of<TILE>(p, max(0, min(p.lens[rg.b], p.max_len))) == 0);
+    __syncthreads();  // the joined outputs are no longer read
   }
 }
 
-// Joins the splits of one query head: groups of threads, each d / 4 wide, take splits in
-// turn and are added in group order.
+// Joins the parts of one query head: groups of threads, each d / 4 wide, take parts in turn
+// and are added in group order.  Sequences of one part are done; empty ones become 0.
 constexpr int kJoinThreads = 256;
 
 template <bool BF16>
@@ -508,28 +509,26 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs p) {
   __shared__ f32x4 acc_lds[kJoinThreads];
   __shared__ float sum_lds[kJoinThreads], top_lds[kJoinThreads];
   const int head = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
-  const int splits = p.parts[2 * b];
-  if (splits < 2) return;  // the output is there
+  const int first = p.parts[2 * b], parts = p.parts[2 * b + 1];
+  if (parts == 1) return;  // the output is there
   const int64_t h = (int64_t)b * p.q_heads + head;
   const int per_row = p.d / 4;  // at most 64
   const int groups = kJoinThreads / per_row;
   const int g = tid / per_row, e = 4 * (tid - g * per_row);
   const int kvh = head / p.group, in_group = head - kvh * p.group;
   const int unit = kvh * p.head_blocks + in_group / 16;
-  // partial of split s: row r0 + s * step
-  const int64_t step = (int64_t)p.units * p.part_rows;
-  const int64_t r0 = p.parts[2 * b + 1] * step + unit * p.part_rows + in_group % 16;
-  const float* ml = p.part_ml + r0 * 2;
-  const float* po = p.part_o + r0 * p.d;
+  const int64_t at = unit * p.part_rows + in_group % 16;
 
   // each group of threads keeps its own maximum, so that no load waits for another split
   float top = -INFINITY, sum = 0.f;
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   if (g < groups) {
 #pragma unroll 4
-    for (int s = g; s < splits; s += groups) {
-      const float ms = ml[2 * step * s], ls = ml[2 * step * s + 1];
-      const f32x4 x = *reinterpret_cast<const f32x4*>(po + step * s * p.d + e);
+    for (int s = g; s < parts; s += groups) {
+      // the second partial of the first range, then the first ones of the others
+      const int64_t r = (2 * (int64_t)(first + s) + (s == 0)) * p.units * p.part_rows + at;
+      const float ms = p.part_ml[2 * r], ls = p.part_ml[2 * r + 1];
+      const f32x4 x = *reinterpret_cast<const f32x4*>(p.part_o + r * p.d + e);
       const float high = fmaxf(top, ms);
       const float ref = high == -INFINITY ? 0.f : high;
       const float fa = __builtin_amdgcn_exp2f(top - ref), fx = __builtin_amdgcn_exp2f(ms - ref);
@@ -567,15 +566,15 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs p) {
 
 }  // namespace
 
-// Work-groups of a round.  A single sequence is cut evenly, so as many as hold the bytes in
-// flight that the memory needs, 64 KiB on each CU (bf16, head_dim 128, 131072 positions: 256
-// work-groups 99.7 us, 512 102.8, 1024 105.9).  Sequences of different lengths are cut finer,
-// into as many as the CUs hold at once by their registers (16 sequences of up to 4096: 256
-// work-groups 37.9 us, 512 35.6, 768 42.2; E4M3, 64 of up to 8192: 512 118, 768 92.7, 1024
-// 103 us).
-int attn_groups(int batch, int head_dim, bool kv8) {
-  if (batch == 1) return (head_dim <= 64 ? 512 : 256) * (kv8 && head_dim <= 128 ? 2 : 1);
-  return 256 * (head_dim <= 64 ? (kv8 ? 4 : 3) : head_dim <= 128 ? (kv8 ? 3 : 2) : 1);
+// Work-groups to cut the batch for.  A single sequence is cut evenly, into as many as hold the
+// bytes in flight that the memory needs, 64 KiB on each CU (bf16, head_dim 128, 131072
+// positions: 256 work-groups 99.2 us, 512 103.4, 1024 105.7).  Several sequences' ranges begin
+// and end inside sequences, so there are as many as the CUs hold at once by their registers
+// (16 sequences of up to 4096: 256 work-groups 36.4 us, 512 34.2, 768 39.5; E4M3, 64 of up to
+// 8192, masked: 256 109.0, 512 88.8, 768 104.5).
+int attn_groups(int batch, int head_dim) {
+  if (batch == 1) return head_dim <= 64 ? 512 : 256;
+  return head_dim <= 64 ? 768 : head_dim <= 128 ? 512 : 256;
 }
 
 AttnPlan attn_plan(int batch, int q_heads, int kv_heads, int head_dim, int max_len, int window,
@@ -584,20 +583,20 @@ AttnPlan attn_plan(int batch, int q_heads, int kv_heads, int head_dim, int max_l
   plan.head_blocks = (q_heads / kv_heads + 15) / 16;
   plan.units = kv_heads * plan.head_blocks;
   // positions a sequence may need, from the tile that holds the window's first
-  const long span = window > 0 && window < max_len - kTile ? window + kTile - 1 : max_len;
-  if (span <= kStep) return plan;
-  plan.round = (attn_groups(batch, head_dim, kv8) + plan.units - 1) / plan.units;
-  // whole rounds, with half a split more than one for each sequence
-  const int least = batch == 1 ? 1 : batch + batch / 2;
-  plan.target = (least + plan.round - 1) / plan.round * plan.round;
+  const int tile = tile_of(head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256, kv8);
+  const long span = window > 0 && window < max_len - tile ? window + tile - 1 : max_len;
+  if (span > kWaves * tile) {
+    const int groups = attn_groups(batch, head_dim);
+    plan.ranges = groups / plan.units > 0 ? groups / plan.units : 1;
+  }
   return plan;
 }
 
 size_t attn_workspace_bytes(const AttnPlan& plan, int batch, int q_heads, int kv_heads,
                             int head_dim) {
-  if (plan.target == 0) return 0;
+  if (plan.ranges == 0) return 0;
   const int group = q_heads / kv_heads;
-  const size_t rows = (size_t)plan.target * plan.units * (group < 16 ? group : 16);
+  const size_t rows = 2 * (size_t)plan.ranges * plan.units * (group < 16 ? group : 16);
   return rows * (head_dim + 2) * sizeof(float) + 2 * (size_t)batch * sizeof(int32_t);
 }
 
@@ -633,23 +632,21 @@ hipError_t launch_paged_attention(const wq_attn_args& a, const AttnPlan& plan,
   p.batch = a.batch;
   p.units = plan.units;
   p.part_rows = p.group < 16 ? p.group : 16;
-  p.target = plan.target;
-  p.round = plan.round;
+  p.ranges = plan.ranges;
   p.scale = a.scale;
   p.softcap = a.softcap;
   // exact for positions below 2^30: the multiplier is 2^(31 + shift) / page_size rounded up,
   // with page_size <= 2^shift
   while ((1ll << p.page_shift) < p.page_size) ++p.page_shift;
   p.page_mul = (uint32_t)(((1ull << (31 + p.page_shift)) + p.page_size - 1) / p.page_size);
-  if (plan.target > 0) {
-    const size_t rows = (size_t)plan.target * plan.units * p.part_rows;
+  if (plan.ranges > 0) {
+    const size_t rows = 2 * (size_t)plan.ranges * plan.units * p.part_rows;
     p.part_o = static_cast<float*>(a.workspace);
     p.part_ml = p.part_o + rows * p.d;
     p.parts = reinterpret_cast<int32_t*>(p.part_ml + rows * 2);
   }
   const bool bf16 = (a.flags & WQ_FLAG_BF16) != 0, kv8 = (a.flags & WQ_FLAG_FP8) != 0;
-  const int splits = plan.target > a.batch ? plan.target : a.batch;
-  const dim3 grid((unsigned)((size_t)splits * plan.units));
+  const dim3 grid((unsigned)((size_t)(plan.ranges > 0 ? plan.ranges : a.batch) * plan.units));
 #define WQ_ATTN(B, F, D, FULL)                                                                \
   hipLaunchKernelGGL((attn_kernel<B, F, D, FULL>), grid, dim3(kWaves * 64), 0, stream, p)
 #define WQ_ATTN_D(B, F)                                                                       \
@@ -669,7 +666,7 @@ hipError_t launch_paged_attention(const wq_attn_args& a, const AttnPlan& plan,
 #undef WQ_ATTN_D
 #undef WQ_ATTN
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || plan.target == 0) return e;
+  if (e != hipSuccess || plan.ranges == 0) return e;
   const dim3 join((unsigned)a.q_heads, (unsigned)a.batch);
   if (bf16)
     hipLaunchKernelGGL((attn_join_kernel<true>), join, dim3(kJoinThreads), 0, stream, p);

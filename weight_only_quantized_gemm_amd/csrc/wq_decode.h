@@ -14,13 +14,12 @@ hipError_t launch_add_rms_norm(const wq_norm_args& a, hipStream_t stream);
 
 hipError_t launch_rope_append(const wq_rope_args& a, hipStream_t stream);
 
-// How a call's positions are cut: at most `target` splits of about equal length over all
-// sequences (0: none is split), each taken by `units` work-groups, one per KV head and block
-// of 16 of its query heads; the CUs take `round` splits at once.  Split sequences leave fp32
-// partials that a second kernel joins.
+// How a call's positions are cut: at most `ranges` ranges of equal length over all sequences
+// (0: one range for each sequence), each taken by `units` work-groups, one per KV head and
+// block of 16 of its query heads.  Sequences that no range holds whole leave fp32 partials
+// that a second kernel joins.
 struct AttnPlan {
-  int target;
-  int round;
+  int ranges;
   int units;
   int head_blocks;  // blocks of 16 query heads per KV head
 };

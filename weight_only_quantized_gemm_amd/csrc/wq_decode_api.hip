@@ -123,8 +123,7 @@ int wq_paged_attention_workspace_bytes(int batch, int q_heads, int kv_heads, int
     return shape_error();
   const wq::AttnPlan plan = wq::attn_plan(batch, q_heads, kv_heads, head_dim, max_len, window,
                                           (flags & WQ_FLAG_FP8) != 0);
-  const int64_t splits = plan.target > batch ? plan.target : batch;
-  if (splits * plan.units > (1 << 23) || splits >= 1 << 18)  // work-groups of one launch
+  if ((int64_t)(plan.ranges > 0 ? plan.ranges : batch) * plan.units > (1 << 23))  // work-groups of one launch
     return fail(WQ_STAGE_SHAPE, WQ_ERR_OVERFLOW);
   *bytes_out = wq::attn_workspace_bytes(plan, batch, q_heads, kv_heads, head_dim);
   return 0;

@@ -394,7 +394,7 @@ typedef struct wq_norm_args {
   void* y;                  /* device [rows][ldy]; may be x or delta itself (same row
                                stride), but not sum_out                                 */
   void* stream;
-  int32_t rows, n;          /* rows >= 1; n a multiple of 8, at most 65536               */
+  int32_t rows, n;          /* rows 1 to 2^22 - 1; n a multiple of 8, at most 65536        */
   int32_t ldx, ldd, lds, ldy; /* row strides, >= n, multiples of 8 (ldd, lds: 0 if unused) */
   float eps;                /* >= 0                                                    */
   uint32_t flags;           /* 0 or WQ_FLAG_BF16                                       */
@@ -440,7 +440,7 @@ typedef struct wq_rope_args {
   const int32_t* positions; /* device [axes][tokens]; NULL with rot_dim 0                */
   const float* inv_freq;    /* device fp32 [rot_dim / 2]; NULL with rot_dim 0            */
   void* stream;
-  int32_t tokens, q_heads;
+  int32_t tokens, q_heads;  /* tokens 1 to 2^24 - 1                                     */
   int32_t ldq, ldk, ldv, ldqo; /* row strides, multiples of 8                            */
   int32_t rot_dim;          /* rotated leading elements of a head: a multiple of 8, 0 to
                                head_dim                                                */
@@ -486,8 +486,8 @@ typedef struct wq_attn_args {
   int32_t reserved;
 } wq_attn_args;
 
-/* Workspace bytes of wq_paged_attention (0 when one work-group covers every sequence); flags
- * as in its arguments.  Contents need no initialization; calls that share one must not run concurrently. */
+/* Workspace bytes of wq_paged_attention (0 where no sequence is split); flags as in its
+ * arguments.  Contents need no initialization; calls that share one must not run concurrently. */
 int wq_paged_attention_workspace_bytes(int batch, int q_heads, int kv_heads, int head_dim,
                                        int max_len, int window, uint32_t flags,
                                        size_t* bytes_out);

@@ -41,7 +41,8 @@ def norm_args():
     (dict(abi_version=2), ABI), (dict(struct_size=8), ABI), (dict(reserved=1), ABI),
     (dict(x=None), NULL), (dict(weight=None), NULL), (dict(y=None), NULL),
     (dict(x=P + 8), ALIGN), (dict(delta=P + 2), ALIGN), (dict(sum_out=P + 2), ALIGN),
-    (dict(rows=0), BAD), (dict(n=0), BAD), (dict(n=60), BAD), (dict(n=65544, ldx=65544), BAD),
+    (dict(rows=0), BAD), (dict(rows=1 << 22), BAD), (dict(n=0), BAD), (dict(n=60), BAD),
+    (dict(n=65544, ldx=65544), BAD),
     (dict(ldx=56), BAD), (dict(ldy=68), BAD), (dict(ldd=8), BAD), (dict(lds=60), BAD),
     (dict(eps=-1.0), BAD), (dict(eps=math.nan), BAD), (dict(delta=None), FLAGS),
     (dict(sum_out=3 * P), FLAGS), (dict(flags=wq.WQ_FLAG_FP8), FLAGS),
@@ -76,7 +77,8 @@ def rope_args():
 
 
 @pytest.mark.parametrize("changes,want", CACHE_REFUSALS + [
-    (dict(tokens=0), BAD), (dict(q_heads=-1), BAD), (dict(ldq=248), BAD), (dict(ldk=120), BAD),
+    (dict(tokens=0), BAD), (dict(tokens=1 << 24), BAD), (dict(q_heads=-1), BAD), (dict(ldq=248), BAD),
+    (dict(ldk=120), BAD),
     (dict(ldv=132), BAD), (dict(ldqo=0), BAD), (dict(rot_dim=4), BAD), (dict(rot_dim=72), BAD),
     (dict(rot_dim=56), BAD), (dict(axes=0), BAD), (dict(axes=5), BAD), (dict(axes=1), BAD),
     (dict(interleaved=2), FLAGS), (dict(q=None), NULL), (dict(k=None), NULL),
@@ -116,15 +118,22 @@ def test_attention_refusals(changes, want):
 def test_attention_workspace():
     f = wq.wq_paged_attention_workspace_bytes
     assert f(1, 8, 2, 64, 1) == 0 == f(65535, 8, 2, 64, 128)  # no sequence is split
-    # two partials for each of 384 ranges, [2 KV heads][4 query heads] of head_dim + 2 floats, 8 bytes a
-    # sequence
-    assert f(3, 8, 2, 64, 129) == f(3, 8, 2, 64, 1 << 20) == 2 * 384 * 8 * 66 * 4 + 24
-    assert f(1, 8, 2, 64, 1 << 20, 90) == 0                   # a window that one work-group covers
-    assert f(1, 8, 2, 128, 200, 0, wq.WQ_FLAG_FP8) == 0 < f(1, 8, 2, 128, 200)
+    # two partials for each of 384 ranges, [2 KV heads][4 query heads] of head_dim + 2 floats,
+    # 8 bytes a sequence
+    assert f(3, 8, 2, 64, 769) == f(3, 8, 2, 64, 1 << 20) == 2 * 384 * 8 * 66 * 4 + 24
+    # whole sequences up to a KiB of keys for each work-group, between 96 and 256
+    assert f(3, 8, 2, 64, 768) == 0 == f(100, 8, 2, 64, 1600) < f(100, 8, 2, 64, 1601)
+    assert f(4096, 8, 2, 64, 2048) == 0 < f(4096, 8, 2, 64, 2049)
+    assert f(1, 8, 2, 64, 1 << 20, 700) == 0                  # a window that one work-group covers
+    assert f(1, 8, 2, 128, 500, 0, wq.WQ_FLAG_FP8) == 0 < f(1, 8, 2, 128, 500)
     with pytest.raises(wq.WQError):
         f(1, 8, 2, 64, 1, 0, wq.WQ_FLAG_SWIGLU)
     with pytest.raises(wq.WQError) as e:
         f(65535, 512, 512, 64, 128)                           # work-groups of one launch
+    assert e.value.code == wq.WQ_ERR_OVERFLOW
+    assert f(65535, 8, 2, 64, 1 << 20) > 0 == f(65535, 8, 2, 64, 1 << 30, 100)
+    with pytest.raises(wq.WQError) as e:
+        f(65535, 8, 2, 64, 1 << 30)                           # steps of all sequences
     assert e.value.code == wq.WQ_ERR_OVERFLOW
     for bad in ((0, 8, 2, 64, 1), (1, 7, 2, 64, 1), (1, 8, 0, 64, 1), (1, 8, 2, 20, 1)):
         with pytest.raises(wq.WQError):

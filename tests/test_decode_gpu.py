@@ -220,9 +220,19 @@ def attn_case(dev, lens, hq, hkv, d, page, dtype, kind="same", order="hnd", wind
                 softcap=softcap, hq=hq, dtype=dtype, scale=1 / math.sqrt(d))
 
 
-def attn_run(c, **kw):
+def attn_run(c, cut=False, **kw):
+    """cut: planned for sequences far longer than the table's pages (the rest are no pages of the
+    cache), so that they are cut into ranges."""
+    if cut:
+        c = dict(c, top=c["top"] + (1 << 18) // c["cache"].head_dim)
+        pages = -(-c["top"] // c["cache"].page_size)
+        c["table"] = torch.nn.functional.pad(c["table"], (0, pages - c["table"].shape[1]), value=-1)
+        if c["keep"] is not None:
+            c["keep"] = torch.nn.functional.pad(c["keep"], (0, c["top"] - c["keep"].shape[1]),
+                                                value=1)
     plan = decode.PagedAttention(c["cache"], len(c["lens"]), c["hq"], c["top"], dtype=c["dtype"],
                                  scale=c["scale"], window=c["window"], softcap=c["softcap"])
+    assert not cut or c["window"] or plan.workspace.numel()
     plan.workspace.fill_(0xFF)  # its contents need no initialization
     return plan(c["q"], c["table"], c["lens"], keep=c["keep"], lse=True, **kw)
 
@@ -247,7 +257,8 @@ def attn_check(c, out, lse, label=""):
     (192, 16, 1, 7, "nhd"), (256, 5, 1, 16, "hnd")])
 def test_attention_heads(dev, dtype, kind, d, hq, hkv, page, order):
     c = attn_case(dev, [0, 1, 15, 31, 32, 33, 127, 300], hq, hkv, d, page, dtype, kind, order)
-    attn_check(c, *attn_run(c))
+    for cut in (False, True):
+        attn_check(c, *attn_run(c, cut), f"cut {cut}")
 
 
 @pytest.mark.parametrize("lens,kw", [
@@ -257,12 +268,14 @@ def test_attention_heads(dev, dtype, kind, d, hq, hkv, page, order):
     ([700, 33, 1], dict(window=1)), ([700, 33, 1], dict(window=32)), ([700, 33], dict(window=4000)),
     ([513, 64], dict(softcap=20.0)), ([900, 300, 40], dict(keep=True)),
     ([3000, 1], dict(keep=True, window=1500, softcap=5.0)),
+    ([9000, 40, 6000], dict(window=5000)), ([7000, 1], dict(keep=True, window=6500, softcap=5.0)),
 ])
 @pytest.mark.parametrize("kind", ["same", "e4m3"])
 def test_attention_lengths_and_masks(dev, lens, kw, kind):
     kw = dict(dict(hq=8, hkv=2), **kw)
     c = attn_case(dev, lens, d=64, page=16, dtype=BF16, kind=kind, seed=sum(lens), **kw)
-    attn_check(c, *attn_run(c))
+    for cut in (False, True):
+        attn_check(c, *attn_run(c, cut), f"cut {cut}")
 
 
 @pytest.mark.parametrize("batch,longest,hq,hkv", [(65, 700, 2, 1), (130, 3000, 2, 1),
@@ -273,10 +286,10 @@ def test_attention_many_sequences(dev, batch, longest, hq, hkv):
     lens = g.integers(0, 60, batch)
     lens[batch // 2] = longest
     lens[-1] = longest // 2
-    c = attn_case(dev, lens.tolist(), hq, hkv, 64, 16, BF16, seed=batch)
-    attn_check(c, *attn_run(c))
-    c = attn_case(dev, [130] * batch, hq, hkv, 64, 16, BF16, max_len=longest, seed=batch)
-    attn_check(c, *attn_run(c))
+    for n in (lens.tolist(), [130] * batch):
+        c = attn_case(dev, n, hq, hkv, 64, 16, BF16, max_len=longest, seed=batch)
+        for cut in (False, True):
+            attn_check(c, *attn_run(c, cut), f"cut {cut}")
 
 
 def test_attention_a_split_without_kept_positions(dev):
@@ -294,10 +307,11 @@ def test_attention_live_infinities_and_nan(dev):
     at = [(c["table"][i, 5].long(), 3) for i in range(3)]
     c["cache"].v[at[0][0], at[0][1], 0, 7] = float("inf")
     c["cache"].k[at[1][0], at[1][1], 0, 0] = float("nan")
-    out, lse = attn_run(c)
-    assert bool(out[0, :, 7].isinf().all()) and int(out[0].isinf().sum()) == 2
-    assert bool(out[1].isnan().all()) and bool(lse[1].isnan().all())
-    assert bool(out[2].isfinite().all()) and bool(lse[0].isfinite().all())
+    for cut in (False, True):
+        out, lse = attn_run(c, cut)
+        assert bool(out[0, :, 7].isinf().all()) and int(out[0].isinf().sum()) == 2
+        assert bool(out[1].isnan().all()) and bool(lse[1].isnan().all())
+        assert bool(out[2].isfinite().all()) and bool(lse[0].isfinite().all())
 
 
 def test_an_e4m3_cache_without_scales(dev):
@@ -316,8 +330,9 @@ def test_an_e4m3_cache_without_scales(dev):
 def test_attention_empty_rows_are_zero(dev):
     c = attn_case(dev, [600, 0, 40], 4, 2, 128, 16, F16, keep=True)
     c["keep"][2] = 0
-    out, lse = attn_run(c)
-    assert bool((out == 0).all()) and bool((lse == -math.inf).all())  # keep[0] is all zero
+    for cut in (False, True):  # keep[0] is all zero
+        out, lse = attn_run(c, cut)
+        assert bool((out == 0).all()) and bool((lse == -math.inf).all())
 
 
 def test_attention_page_numbers_outside_the_cache_are_left_out(dev):
@@ -325,7 +340,8 @@ def test_attention_page_numbers_outside_the_cache_are_left_out(dev):
     c["table"][0, 3], c["table"][0, 7] = -1, c["cache"].num_pages
     c["table"][1, :] = 2 ** 31 - 1
     c["table"][2, 0] = -2 ** 31
-    attn_check(c, *attn_run(c))
+    for cut in (False, True):
+        attn_check(c, *attn_run(c, cut), f"cut {cut}")
 
 
 def test_attention_lens_are_taken_into_range(dev):

@@ -25,6 +25,8 @@
 // One register set serves the loads: K of the next tile is requested when this tile's scores
 // are formed, V when this tile's V has gone to LDS, so each wave keeps about a tile in
 // flight.  Page numbers are read a tile further ahead.
+#include <algorithm>
+
 #include "wq_decode.h"
 #include "wq_device.h"
 
@@ -585,7 +587,14 @@ AttnPlan attn_plan(int batch, int q_heads, int kv_heads, int head_dim, int max_l
   // positions a sequence may need, from the tile that holds the window's first
   const int tile = tile_of(head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256, kv8);
   const long span = window > 0 && window < max_len - tile ? window + tile - 1 : max_len;
-  if (span > kWaves * tile) {
+  // Short sequences stay whole, which spares the partials and the join.  A work-group takes
+  // about 1.2 us for 32 KiB of keys, so the longest there may be is bounded: a KiB of keys for
+  // each work-group of the launch, between 96 and 256 (head_dim 128, 16-bit: 8 work-groups, 384
+  // positions 9.4 us cut, 7.9 whole, 768 positions 9.4 and 11.5; 192 and 768: 20.9, 15.4; 512
+  // and 1024: 52.0, 49.5; 8192 and 150: 194, 150).
+  const long keys = span * head_dim * (kv8 ? 1 : 2);
+  const long whole = std::min(256l, std::max(96l, (long)batch * plan.units)) * 1024;
+  if (span > kWaves * tile && keys > whole) {
     const int groups = attn_groups(batch, head_dim);
     plan.ranges = groups / plan.units > 0 ? groups / plan.units : 1;
   }

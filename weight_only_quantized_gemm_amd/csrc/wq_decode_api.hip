@@ -1,4 +1,5 @@
 // C ABI of the decode-step operators: argument validation and launches (see include/wq.h).
+#include <algorithm>
 #include <limits>
 
 #include "wq.h"
@@ -37,6 +38,8 @@ bool row_stride_ok(int ld, int64_t least) { return ld >= least && ld % 8 == 0; }
 hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
 constexpr int kMaxHeads = 65535;  // heads of one kind: grid axes and 32-bit row offsets
+constexpr int kMaxRows = (1 << 22) - 1;     // 1024 threads each, below 2^32 in a launch
+constexpr int kMaxTokens = (1 << 24) - 1;   // 256 threads each
 
 int check_cache(const wq_kv_cache& c, uint32_t flags) {
   const bool fp8 = (flags & WQ_FLAG_FP8) != 0;
@@ -71,8 +74,8 @@ int wq_add_rms_norm(const wq_norm_args* args) {
   if (st) return st;
   const wq_norm_args& a = *args;
   if (a.flags & ~(uint32_t)WQ_FLAG_BF16) return flags_error();
-  if (a.rows < 1 || a.n < 8 || a.n > 65536 || a.n % 8 != 0 || !(a.eps >= 0.f) ||
-      !row_stride_ok(a.ldx, a.n) || !row_stride_ok(a.ldy, a.n) ||
+  if (a.rows < 1 || a.rows > kMaxRows || a.n < 8 || a.n > 65536 || a.n % 8 != 0 ||
+      !(a.eps >= 0.f) || !row_stride_ok(a.ldx, a.n) || !row_stride_ok(a.ldy, a.n) ||
       (a.delta != nullptr && !row_stride_ok(a.ldd, a.n)) ||
       (a.sum_out != nullptr && !row_stride_ok(a.lds, a.n)))
     return shape_error();
@@ -92,11 +95,12 @@ int wq_rope_append(const wq_rope_args* args) {
   if (a.interleaved != 0 && a.interleaved != 1) return flags_error();
   if ((st = check_cache(a.cache, a.flags))) return st;
   const int64_t d = a.cache.head_dim;
-  if (a.tokens < 1 || a.q_heads < 0 || a.q_heads > kMaxHeads || a.rot_dim < 0 ||
-      a.rot_dim > d || a.rot_dim % 8 != 0 || a.axes < 1 || a.axes > WQ_MAX_ROPE_AXES)
+  if (a.tokens < 1 || a.tokens > kMaxTokens || a.q_heads < 0 || a.q_heads > kMaxHeads ||
+      a.rot_dim < 0 || a.rot_dim > d || a.rot_dim % 8 != 0 || a.axes < 1 || a.axes > WQ_MAX_ROPE_AXES)
     return shape_error();
   if (!row_stride_ok(a.ldk, a.cache.kv_heads * d) || !row_stride_ok(a.ldv, a.cache.kv_heads * d) ||
-      (a.q_heads > 0 && (!row_stride_ok(a.ldq, a.q_heads * d) || !row_stride_ok(a.ldqo, a.q_heads * d))))
+      (a.q_heads > 0 &&
+       (!row_stride_ok(a.ldq, a.q_heads * d) || !row_stride_ok(a.ldqo, a.q_heads * d))))
     return shape_error();
   int64_t pairs = 0;
   for (int i = 0; i < a.axes; ++i) {
@@ -123,7 +127,10 @@ int wq_paged_attention_workspace_bytes(int batch, int q_heads, int kv_heads, int
     return shape_error();
   const wq::AttnPlan plan = wq::attn_plan(batch, q_heads, kv_heads, head_dim, max_len, window,
                                           (flags & WQ_FLAG_FP8) != 0);
-  if ((int64_t)(plan.ranges > 0 ? plan.ranges : batch) * plan.units > (1 << 23))  // work-groups of one launch
+  // work-groups of one launch; steps of 128 positions over all sequences, counted in 32 bits
+  const int64_t steps = (window > 0 ? std::min(window, max_len) : max_len) / 128 + 2;
+  if ((int64_t)(plan.ranges > 0 ? plan.ranges : batch) * plan.units > (1 << 23) ||
+      batch * steps > (1 << 30))
     return fail(WQ_STAGE_SHAPE, WQ_ERR_OVERFLOW);
   *bytes_out = wq::attn_workspace_bytes(plan, batch, q_heads, kv_heads, head_dim);
   return 0;
@@ -137,7 +144,8 @@ int wq_paged_attention(const wq_attn_args* args) {
   if ((st = check_cache(a.cache, a.flags))) return st;
   size_t need = 0;
   if ((st = wq_paged_attention_workspace_bytes(a.batch, a.q_heads, a.cache.kv_heads,
-                                               a.cache.head_dim, a.max_len, a.window, a.flags, &need)))
+                                               a.cache.head_dim, a.max_len, a.window, a.flags,
+                                               &need)))
     return st;
   const int64_t row = (int64_t)a.q_heads * a.cache.head_dim;
   if (!row_stride_ok(a.ldq, row) || !row_stride_ok(a.ldo, row) || a.table_stride < 1 ||

@@ -219,7 +219,8 @@ __global__ __launch_bounds__(kMaxT * 64) void route_kernel(RouteArgs p) {
   const int pair = wave * p.top_k + lane;
   if (wave < p.tokens) {
     float w = 0.f;
-    token_top_k<PER>(p.logits + wave * p.n_expert, p.n_expert, p.top_k, p.renormalize, p.routed_scale, lane, id, w);
+    token_top_k<PER>(p.logits + wave * p.n_expert, p.n_expert, p.top_k, p.renormalize,
+                     p.routed_scale, lane, id, w);
     if (mine) {
       atomicOr(&mask_lds[id], 1u << wave);
       p.route->w[pair] = w;

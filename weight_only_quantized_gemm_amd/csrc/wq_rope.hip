@@ -84,7 +84,8 @@ __global__ __launch_bounds__(kThreads) void rope_append_kernel(RopeArgs p) {
   const int64_t slot = p.slots[token];
   const bool real = slot >= 0 && slot < p.total_slots;
   const int64_t page = real ? slot / p.page_size : 0;
-  const int64_t cache_at = page * p.page_stride + (real ? slot - page * p.page_size : 0) * p.slot_stride;
+  const int64_t cache_at =
+      page * p.page_stride + (real ? slot - page * p.page_size : 0) * p.slot_stride;
   __syncthreads();
 
   // Units of a token: per q and k head, rot/8 rotated units of four pairs and (d - rot)/8

@@ -6,7 +6,9 @@ allocates device buffers and supplies the stream; every operation is a libwq ker
 
 Calls run on the current stream of their tensors' device, enqueue and return; none
 synchronizes, so all of them may be captured into a graph.  A plan (PagedAttention, MoELayer)
-owns a workspace: its calls must not overlap on different streams.
+owns a workspace: its calls must not overlap on different streams.  Tensors that a call is given
+follow PyTorch's rules for streams other than their own; a plan's own memory is not reused before
+the calls made on any stream are done.
 
 The arguments of a call are packed as the bytes of its C struct and checked here only where
 the library cannot see them (types, devices, shapes, strides): a call of a few microseconds on
@@ -54,6 +56,21 @@ def _stream(dev: int) -> int:
         raise ValueError(f"the tensors are on GPU {dev}, the current device is "
                          f"{_current_device()}: call under torch.cuda.device({dev})")
     return _raw_stream(dev)
+
+
+class _PlanMemory:
+    """A plan's own tensors, and the stream they were allocated on."""
+
+    def __init__(self, dev: int, *tensors: torch.Tensor):
+        self.tensors, self.home = tensors, _raw_stream(dev) if dev >= 0 else None
+
+    def stream(self, dev: int) -> int:
+        """The current stream, for a call that uses the memory there."""
+        stream = _stream(dev)
+        if stream != self.home:
+            for t in self.tensors:
+                t.record_stream(torch.cuda.current_stream(dev))
+        return stream
 
 
 class _Call:
@@ -275,6 +292,7 @@ class PagedAttention:
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         self._space = (self.workspace.data_ptr(), nbytes)
         self._lse = torch.empty((batch, q_heads), dtype=torch.float32, device=self.device)
+        self._memory = _PlanMemory(cache.dev, self.workspace)
         scale = 1.0 / math.sqrt(cache.head_dim) if scale is None else scale
         self._last = (scale, softcap, window, cache.flags(dtype), 0)
 
@@ -306,8 +324,8 @@ class PagedAttention:
             else:
                 lp = _dense(lse, "lse", torch.float32, dev, (b, heads))
         _attn_call(_ATTN.pack(WQ_ABI_VERSION, _ATTN.size, cache.packed, q.data_ptr(),
-                              out.data_ptr(), lp, table, n, kp, *self._space, _stream(dev), b,
-                              heads, self.max_len, pages, keep_stride, ldq, ldo, *self._last))
+                              out.data_ptr(), lp, table, n, kp, *self._space,
+                              self._memory.stream(dev), b, heads, self.max_len, pages, keep_stride, ldq, ldo, *self._last))
         return out if lse is False else (out, lse)
 
 
@@ -346,6 +364,7 @@ class MoELayer:
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         self.ids = torch.empty((max_tokens, top_k), dtype=torch.int32, device=self.device)
         self.weights = torch.empty((max_tokens, top_k), dtype=torch.float32, device=self.device)
+        self._memory = _PlanMemory(self.dev, self.workspace, self.ids, self.weights)
         r = _dense(router, "router", self.dtype, self.dev, (self.n_expert, self.hidden))
         self._banks = (r, _bank(gate_up), _bank(down))
         self._space = (self.ids.data_ptr(), self.weights.data_ptr(), self.workspace.data_ptr(),
@@ -372,6 +391,6 @@ class MoELayer:
             rp, ldr = residual.data_ptr(), _rows(residual, "residual", dtype, dev, shape)
         router, gate_up, down = self._banks
         _moe_call(_MOE.pack(WQ_ABI_VERSION, _MOE.size, x.data_ptr(), router, gate_up, down, rp,
-                            out.data_ptr(), *self._space, _stream(dev), tokens, self.n_expert,
-                            self.top_k, hidden, self.inter, ldx, ldr, ldy, *self._last))
+                            out.data_ptr(), *self._space, self._memory.stream(dev), tokens,
+                            self.n_expert, self.top_k, hidden, self.inter, ldx, ldr, ldy, *self._last))
         return out

@@ -121,6 +121,8 @@ def paged(dev, pages, page, heads, d, dtype, order, scales=None, g=None):
     (130, 8, 2, 256, 128, 7, 4, True, "same", "hnd", F16),
     (9, 2, 2, 72, 0, 8, 1, False, "e4m3", "hnd", BF16),
     (4200, 1, 1, 64, 64, 64, 1, False, "same", "hnd", F16),
+    (600, 32, 8, 128, 128, 16, 3, False, "e4m3", "hnd", BF16),
+    (1100, 24, 8, 128, 64, 16, 1, True, "same", "nhd", F16),
 ])
 def test_rope_append(dev, case):
     t, hq, hkv, d, rot, page, axes, inter, kind, order, dtype = case

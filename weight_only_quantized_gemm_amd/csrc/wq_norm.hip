@@ -1,8 +1,9 @@
 // RMS norm with the residual add: s = x + delta, y = s / sqrt(mean(s^2) + eps) * w.
 //
 // Two rows read, two written, a few operations per element: bound by memory for many rows
-// and by latency for few.  A row stays in registers as fp32 between its one read and its two
-// writes, so nothing is read twice and the norm sees the unrounded sum.
+// (bf16, 8192 rows of 8192: 92 us, 5.8 TB/s of the four rows) and by its launch and one trip to
+// memory for few (fp16, one row of 4096: 2.7 us).  A row stays in registers as fp32 between its
+// one read and its two writes, so nothing is read twice and the norm sees the unrounded sum.
 #include "wq_decode.h"
 #include "wq_device.h"
 
@@ -89,11 +90,17 @@ hipError_t launch_norm_t(const wq_norm_args& a, hipStream_t stream) {
 
 template <bool BF16>
 hipError_t launch_norm_type(const wq_norm_args& a, hipStream_t stream) {
+  // One granule a thread as far as a work-group goes: a row's loads then leave together (us,
+  // one row and 8192 rows, bf16: n 4096, 256 threads of two 2.93 and 48.2, 512 of one 2.69 and
+  // 48.5; n 8192, 256 of four 3.50 and 96.2, 1024 of one 3.16 and 91.9; n 32768 and 2048 rows,
+  // 256 of sixteen 6.65 and 106.9, 1024 of four 5.49 and 103.8).  A single wave needs no exchange
+  // through LDS (n 512: 2.32 and 7.52, 256 threads 2.43 and 9.05), but two granules a thread
+  // cost a lone row more than that (n 1024: 2.71 and 2.44).
   const int granules = a.n / 8;
   if (granules <= 64) return launch_norm_t<BF16, 64, 1>(a, stream);
   if (granules <= 256) return launch_norm_t<BF16, 256, 1>(a, stream);
-  if (granules <= 512) return launch_norm_t<BF16, 256, 2>(a, stream);
-  if (granules <= 1024) return launch_norm_t<BF16, 256, 4>(a, stream);
+  if (granules <= 512) return launch_norm_t<BF16, 512, 1>(a, stream);
+  if (granules <= 1024) return launch_norm_t<BF16, 1024, 1>(a, stream);
   if (granules <= 2048) return launch_norm_t<BF16, 1024, 2>(a, stream);
   if (granules <= 4096) return launch_norm_t<BF16, 1024, 4>(a, stream);
   return launch_norm_t<BF16, 1024, 8>(a, stream);

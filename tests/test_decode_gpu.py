@@ -511,15 +511,18 @@ def moe_check(c, residual=None, renormalize=True, scale=1.0, **kw):
 @pytest.mark.parametrize("kind,group", [("u4b8", 128), ("u4b8", 64), ("u4b8", 32), ("u4b8", 16),
                                         ("u4b8", -1), ("u4", 128), ("u4", 64), ("u4", 32),
                                         ("u4", 16), ("e4m3", 128), ("e4m3", -1)])
-def test_moe_weights(dev, dtype, kind, group):
-    c = moe_case(dev, 5, 6, 2, 512, 384, dtype, kind, group)
-    moe_check(c, residual=normal(c["g"], (5, 512), dtype))
+@pytest.mark.parametrize("hidden,inter", [(512, 384), (1024, 896)])  # few launches, and more
+def test_moe_weights(dev, dtype, kind, group, hidden, inter):
+    c = moe_case(dev, 5, 6, 2, hidden, inter, dtype, kind, group)
+    moe_check(c, residual=normal(c["g"], (5, hidden), dtype))
 
 
 @pytest.mark.parametrize("tokens,experts,top_k,hidden,inter,renorm", [
     (1, 1, 1, 256, 128, True), (1, 8, 2, 512, 256, False), (2, 8, 2, 256, 1408, True),
     (16, 4, 4, 256, 128, False), (16, 64, 8, 256, 128, True), (7, 256, 16, 256, 128, False),
     (13, 65, 3, 768, 128, True), (16, 1, 1, 1280, 640, True), (3, 100, 1, 256, 256, False),
+    (9, 5, 3, 512, 768, True), (1, 16, 4, 512, 1024, True), (4, 3, 2, 2560, 256, False),
+    (16, 2, 1, 1024, 2048, True), (1, 1, 1, 8192, 128, True), (2, 20, 16, 256, 256, True),
 ])
 def test_moe_shapes(dev, tokens, experts, top_k, hidden, inter, renorm):
     c = moe_case(dev, tokens, experts, top_k, hidden, inter, BF16)
@@ -553,7 +556,21 @@ def test_moe_strides_aliases_and_nan_rows(dev):
     assert bool(layer.weights[2].isnan().all())
 
 
-# ---- streams and graphs ---------------------------------------------------------------------------
+@pytest.mark.parametrize("inter", [256, 1280])
+@pytest.mark.parametrize("kind", ["u4b8", "e4m3"])
+def test_moe_an_expert_s_values_reach_only_its_own_tokens(dev, inter, kind):
+    """Infinite scales of one expert: the other tokens' rows stay what they were."""
+    c = moe_case(dev, 16, 6, 2, 512, inter, F16, kind)
+    layer, clean = moe_check(c)
+    hit = (layer.ids[:16] == 4).any(1)
+    assert 0 < int(hit.sum()) < 16
+    for bank in c["banks"]:
+        bank.s[4] = float("inf")
+    y = layer(c["x"])
+    assert torch.equal(y[~hit], clean[~hit]) and not bool(y[hit].isfinite().any())
+
+
+# ---- streams and graphs -----------------------------------------------------------------------
 
 def test_a_decode_step_on_another_stream_and_in_a_graph(dev):
     """All four on a side stream, then captured and replayed on changed inputs: the replays

@@ -2,12 +2,12 @@
 // experts' gate/up projections with SwiGLU, their down projections and the weighted sum.
 //
 // The layer reads every chosen expert's weights once and does 2 * (rows per expert) products
-// per weight, so it is bound by the weight stream.  Five launches, each needing the whole
-// result of the one before it, and nothing on the host:
+// per weight, so a large one is bound by the weight stream and a small one by its launches,
+// each of which needs the whole result of the one before it.  Nothing is done on the host:
 //  1. router_kernel: the logits x router^T.
 //  2. route_kernel, one work-group: the tokens' top-k, and for each expert that any token
 //     chose (a "slot") its rows.  (Taken in every work-group of the next kernel instead, the
-//     routing cost 4 to 30 us more than this launch.)
+//     routing cost 4 to 30 us more than this launch.)  It forms a small router's logits too.
 //  3. product_kernel on the gate/up bank: a work-group per slot and pair of 16-column blocks,
 //     a gate and an up block, ends in the activation silu(g) * u.  The grid has room for the
 //     most slots there can be; work-groups past the last one end at once.
@@ -15,8 +15,16 @@
 //     rows, one for each (token, choice).
 //  5. combine_kernel: each token's rows times their routing weights, in the order of choice
 //     (no atomics), and the residual.
+// Where there are few weights down_all_kernel does 4 and 5 in one launch.
 // Products are 16x16x32 MFMAs on codes dequantized in registers (wq_device.h); each scale
-// unit's partial is scaled in fp32.
+// unit's partial is scaled in fp32.  The activation is rounded to the element type between the
+// two products, whose matrix units take it so; that is the layer's one rounding beside y's.
+//
+// Measured as a graph, 128-row groups, K x N of an expert 4096 x 2 * 14336 and 14336 x 4096: one
+// token of two experts, fp16, 43 us, 4.2 TB/s (products 24.0 us at 5.1 TB/s and 13.5 at 4.5 in a
+// kernel trace, the others 2 to 4 each); four tokens of five to six experts, bf16 with zero points,
+// 95 us, 5.2 TB/s (56.6 us at 5.9, 34.5 at 4.9).  16 tokens over 56 of 64 experts of 2048 x 2 * 1024,
+// 64-row groups, 47 us, 4.0 TB/s (24.0 us at 5.2, 14.3 at 4.5).
 #include "wq_decode.h"
 #include "wq_device.h"
 
@@ -31,8 +39,12 @@ constexpr int kMaxE = WQ_MOE_MAX_EXPERTS;
 struct RouteSlot {
   int32_t expert, rows;  // ascending experts; no rows: past the last chosen expert
   uint32_t pair[kMaxT];
+  // by token, for down_all_kernel: its pair here (-1: it has none) and that pair's weight
+  int32_t token_pair[kMaxT];
+  float token_w[kMaxT];
 };
 struct Route {
+  int32_t used, pad[3];  // slots with rows
   RouteSlot slot[kMaxE];
   float w[kMaxT * WQ_MOE_MAX_TOPK];  // routing weight of each pair
 };
@@ -50,23 +62,18 @@ size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 constexpr int kRouterThreads = 256;
 
-// Logits of one expert and four tokens per work-group, whose threads share the hidden size
-// (one CU reading a whole router of 64 KiB takes 2 us longer, one of 256 KiB 10 us).  Eight
-// products at a time are summed in fp32, the sums in fp64 and rounded once: the order of
-// nearly equal logits decides which experts run.
-template <bool BF16>
-__global__ __launch_bounds__(kRouterThreads) void router_kernel(
-    const uint16_t* __restrict__ x, int ldx, const uint16_t* __restrict__ router, int tokens,
-    int n_expert, int hidden, float* __restrict__ logits) {
+// Products of one expert's router row with four tokens (past the last: the last one), over k0,
+// k0 + step, ... of the hidden size, 8 elements each; lanes 16 j, ... of the wave return token
+// t0 + j's sum over the wave.  Eight products at a time are summed in fp32, the sums in fp64 and
+// rounded once: the order of nearly equal logits decides which experts run.
+template <bool BF16, int UNROLL>
+__device__ __forceinline__ double wave_logits(const uint16_t* x, int ldx, const uint16_t* rp,
+                                              int tokens, int t0, int k0, int step, int end,
+                                              int lane) {
   using A = Act<BF16>;
-  __shared__ double red[kRouterThreads / 64][4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int e = blockIdx.x;
-  const int t0 = blockIdx.y * 4;
-  const uint16_t* rp = router + (long)e * hidden;
   double acc[4] = {0., 0., 0., 0.};
-#pragma unroll 2
-  for (int k = tid * 8; k < hidden; k += kRouterThreads * 8) {
+#pragma unroll UNROLL
+  for (int k = k0; k < end; k += step) {
     const u32x4 r = *reinterpret_cast<const u32x4*>(rp + k);
     u32x4 xv[4];
 #pragma unroll
@@ -89,7 +96,21 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(
   double v = (odd ? a1 : a0) + __shfl_xor(odd ? a0 : a1, 16);
 #pragma unroll
   for (int d = 8; d >= 1; d /= 2) v += __shfl_xor(v, d);
-  if ((lane & 15) == 0) red[wave][lane >> 4] = v;  // token 2 * up + odd
+  return v;  // token 2 * up + odd
+}
+
+// Logits of one expert and four tokens per work-group, whose threads share the hidden size.
+template <bool BF16>
+__global__ __launch_bounds__(kRouterThreads) void router_kernel(
+    const uint16_t* __restrict__ x, int ldx, const uint16_t* __restrict__ router, int tokens,
+    int n_expert, int hidden, float* __restrict__ logits) {
+  __shared__ double red[kRouterThreads / 64][4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int e = blockIdx.x;
+  const int t0 = blockIdx.y * 4;
+  const double v = wave_logits<BF16, 2>(x, ldx, router + (long)e * hidden, tokens, t0, tid * 8,
+                                        kRouterThreads * 8, hidden, lane);
+  if ((lane & 15) == 0) red[wave][lane >> 4] = v;
   __syncthreads();
   if (tid < 4 && t0 + tid < tokens) {
     double sum = red[0][tid];
@@ -203,23 +224,50 @@ struct RouteArgs {
   float* weights;
   int tokens, n_expert, top_k, renormalize, slots;  // slots: of the next kernels' grids
   float routed_scale;
+  int by_token;  // the slots' token_pair and token_w are needed
+  // with the logits formed here:
+  const uint16_t *x, *router;
+  int ldx, hidden;
 };
 
-// One work-group, a wave per token.  PER: 64 experts for each lane of a wave, 1 or 4.
-template <int PER>
+// One work-group, a wave per token.  PER: 64 experts for each lane of a wave, 1 or 4.  ROUTER: 16
+// waves form the logits here too, first, (1: fp16, 2: bf16): an expert and four tokens for each,
+// or with fewer of these a part of the hidden size.
+template <int PER, int ROUTER>
 __global__ __launch_bounds__(kMaxT * 64) void route_kernel(RouteArgs p) {
   __shared__ uint32_t mask_lds[kMaxE];
   __shared__ uint8_t slot_of[kMaxE];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   for (int i = tid; i < kMaxE; i += blockDim.x) mask_lds[i] = 0;
+  const float* logits = p.logits;
+  if constexpr (ROUTER != 0) {
+    __shared__ double part_lds[kMaxT][4];
+    __shared__ float logit_lds[kMaxT * 4];
+    const int quads = (p.tokens + 3) / 4, items = p.n_expert * quads, segs = kMaxT / items;
+    if (wave < items * segs) {
+      const int item = wave / segs, e = item / quads, t0 = 4 * (item - e * quads);
+      const int k0 = (wave - item * segs) * 512 + lane * 8;
+      const double v = wave_logits<ROUTER == 2, 4>(p.x, p.ldx, p.router + (long)e * p.hidden,
+                                                   p.tokens, t0, k0, segs * 512, p.hidden, lane);
+      if ((lane & 15) == 0) part_lds[wave][lane >> 4] = v;
+    }
+    __syncthreads();
+    if (tid < 4 * items) {
+      const int item = tid / 4, e = item / quads, t = 4 * (item - e * quads) + tid % 4;
+      double sum = 0.;
+      for (int k = 0; k < segs; ++k) sum += part_lds[item * segs + k][tid % 4];
+      if (t < p.tokens) logit_lds[t * p.n_expert + e] = (float)sum;
+    }
+    logits = logit_lds;
+  }
   __syncthreads();
   int id = 0;  // lane j of wave t: token t's j-th choice
+  float w = 0.f;
   const bool mine = wave < p.tokens && lane < p.top_k;
   const int pair = wave * p.top_k + lane;
   if (wave < p.tokens) {
-    float w = 0.f;
-    token_top_k<PER>(p.logits + wave * p.n_expert, p.n_expert, p.top_k, p.renormalize,
+    token_top_k<PER>(logits + wave * p.n_expert, p.n_expert, p.top_k, p.renormalize,
                      p.routed_scale, lane, id, w);
     if (mine) {
       atomicOr(&mask_lds[id], 1u << wave);
@@ -244,11 +292,21 @@ __global__ __launch_bounds__(kMaxT * 64) void route_kernel(RouteArgs p) {
       }
     }
     for (int i = slots + lane; i < p.slots; i += 64) p.route->slot[i].rows = 0;
+    if (lane == 0) p.route->used = slots;
+  }
+  if (p.by_token) {  // no pairs first (p.slots are at least as many as the slots with rows)
+    for (int i = tid; i < p.slots * kMaxT; i += blockDim.x)
+      p.route->slot[i / kMaxT].token_pair[i % kMaxT] = -1;
   }
   __syncthreads();
-  if (mine)  // the expert's rows lie in token order
-    p.route->slot[slot_of[id]].pair[__popc(mask_lds[id] & ((1u << wave) - 1))] =
-        (uint32_t)pair | (uint32_t)wave << 16;
+  if (mine) {  // the expert's rows lie in token order
+    RouteSlot& slot = p.route->slot[slot_of[id]];
+    slot.pair[__popc(mask_lds[id] & ((1u << wave) - 1))] = (uint32_t)pair | (uint32_t)wave << 16;
+    if (p.by_token) {
+      slot.token_pair[wave] = pair;
+      slot.token_w[wave] = w;
+    }
+  }
 }
 
 // Orders a wave's own LDS accesses (they execute in order; this keeps the compiler to it).
@@ -524,6 +582,79 @@ __global__ __launch_bounds__(WAVES * 64) void product_kernel(ProductArgs p) {
   }
 }
 
+struct DownArgs {
+  const uint16_t* h;  // the activation [pair][inter]
+  Bank bank;
+  const Route* route;
+  const uint16_t* residual;
+  uint16_t* y;
+  int inter, groups, tokens, ldr, ldy;
+};
+
+// The down projections of a small layer with the weighted sum: a work-group per 16-column block
+// of the output, whose waves share all slots' 128-row groups.  The rows are the tokens; one that
+// did not choose a slot's expert has zeros there, and its products (of a zero, and of whatever
+// that expert's weights are) are left out.  Bound by three trips to memory one after the other:
+// the slot, its rows and weights, the store.  Two groups in flight, fewer waves, or the slots'
+// rows brought to LDS first were no faster.
+constexpr int kDownWaves = 16;
+
+template <bool BF16, bool W8, bool ZP, int GPC>
+__global__ __launch_bounds__(kDownWaves * 64) void down_all_kernel(DownArgs p) {
+  using A = Act<BF16>;
+  using C = Chunk<BF16, W8, ZP, GPC>;
+  __shared__ f32x4 red[kDownWaves][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int row = lane & 15, qd = lane >> 4;
+  const int items = p.route->used * p.groups;
+  const int last = items * (wave + 1) / kDownWaves;
+  const long block = (long)blockIdx.x * p.groups;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  for (int i = items * wave / kDownWaves; i < last; ++i) {
+    const int s = i / p.groups, g = i - s * p.groups;
+    const RouteSlot& slot = p.route->slot[s];
+    const long e = slot.expert;
+    C c;
+    c.load(p.bank.b + e * p.bank.b_stride, p.bank.s + e * p.bank.s_stride,
+           ZP ? p.bank.z + e * p.bank.z_stride : nullptr, block + g, lane);
+    const int pair = slot.token_pair[row];
+    const uint16_t* ap = p.h + (long)max(pair, 0) * p.inter + (long)g * kGroup + 8 * qd;
+    f16x8 a[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      a[j] = *reinterpret_cast<const f16x8*>(ap + 32 * j);
+      if (pair < 0) a[j] = f16x8{};
+    }
+    int member[4];
+    float w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      member[k] = slot.token_pair[4 * qd + k];
+      w[k] = slot.token_w[4 * qd + k];  // (not written where it has no pair)
+    }
+    typename C::Sums sums;
+    sums.form(a, lane);
+    f32x4 part = {0.f, 0.f, 0.f, 0.f};
+    c.multiply(a, sums, lane, part);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      acc[k] = member[k] >= 0 ? __builtin_fmaf(w[k], part[k], acc[k]) : acc[k];
+  }
+  red[wave][lane] = acc;
+  __syncthreads();
+  // the block's 16 rows of 16 columns, in wave order
+  const int t = tid >> 4, col = tid & 15;
+  if (t >= p.tokens) return;
+  const long at = 16 * blockIdx.x + col;
+  float sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < kDownWaves; ++k)
+    sum += reinterpret_cast<const float*>(&red[k][16 * (t >> 2) + col])[t & 3];
+  if (p.residual != nullptr) sum += A::value(p.residual[(long)t * p.ldr + at]);
+  p.y[(long)t * p.ldy + at] = A::round(sum);
+}
+
 // y[t] = residual[t] + sum over the token's choices j of w_j part[t][j], 4 columns a thread.
 template <bool BF16>
 __global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ part,
@@ -621,16 +752,43 @@ hipError_t launch_product(const wq_moe_args& a, const MoeScratch& m, hipStream_t
   return hipGetLastError();
 }
 
-template <bool GATE_UP, bool BF16>
-hipError_t launch_product_type(int gpc, const wq_moe_args& a, const MoeScratch& m,
-                               hipStream_t stream) {
-  if (a.flags & WQ_FLAG_FP8) return launch_product<GATE_UP, BF16, true, false, 1>(a, m, stream);
+template <bool BF16, bool W8, bool ZP, int GPC>
+hipError_t launch_down_all(const wq_moe_args& a, const MoeScratch& m, hipStream_t stream) {
+  const DownArgs p{m.h,
+                   bank_of(a.down),
+                   m.route,
+                   static_cast<const uint16_t*>(a.residual),
+                   static_cast<uint16_t*>(a.y),
+                   a.inter,
+                   a.inter / kGroup,
+                   a.tokens,
+                   a.ldr,
+                   a.ldy};
+  hipLaunchKernelGGL((down_all_kernel<BF16, W8, ZP, GPC>), dim3(a.hidden / 16),
+                     dim3(kDownWaves * 64), 0, stream, p);
+  return hipGetLastError();
+}
+
+// DOWN_ALL: down_all_kernel, else product_kernel.
+template <bool GATE_UP, bool DOWN_ALL, bool BF16, bool W8, bool ZP, int GPC>
+hipError_t launch_bank(const wq_moe_args& a, const MoeScratch& m, hipStream_t stream) {
+  if constexpr (DOWN_ALL)
+    return launch_down_all<BF16, W8, ZP, GPC>(a, m, stream);
+  else
+    return launch_product<GATE_UP, BF16, W8, ZP, GPC>(a, m, stream);
+}
+
+template <bool GATE_UP, bool DOWN_ALL, bool BF16>
+hipError_t launch_bank_type(int gpc, const wq_moe_args& a, const MoeScratch& m,
+                            hipStream_t stream) {
+  if (a.flags & WQ_FLAG_FP8)
+    return launch_bank<GATE_UP, DOWN_ALL, BF16, true, false, 1>(a, m, stream);
   const bool zp = (a.flags & WQ_FLAG_HAS_ZP) != 0;
   switch (gpc) {
-#define WQ_MOE_GPC(G)                                                             \
-  case G:                                                                         \
-    return zp ? launch_product<GATE_UP, BF16, false, true, G>(a, m, stream)       \
-              : launch_product<GATE_UP, BF16, false, false, G>(a, m, stream)
+#define WQ_MOE_GPC(G)                                                                    \
+  case G:                                                                                \
+    return zp ? launch_bank<GATE_UP, DOWN_ALL, BF16, false, true, G>(a, m, stream)       \
+              : launch_bank<GATE_UP, DOWN_ALL, BF16, false, false, G>(a, m, stream)
     WQ_MOE_GPC(1);
     WQ_MOE_GPC(2);
     WQ_MOE_GPC(4);
@@ -641,21 +799,42 @@ hipError_t launch_product_type(int gpc, const wq_moe_args& a, const MoeScratch& 
 }
 
 template <bool BF16>
-hipError_t launch_route(const wq_moe_args& a, const MoeScratch& m, hipStream_t stream) {
+hipError_t launch_route(const wq_moe_args& a, const MoeScratch& m, bool by_token,
+                        hipStream_t stream) {
+  RouteArgs p{};
+  p.logits = m.logits;
+  p.route = m.route;
+  p.ids = a.ids;
+  p.weights = a.weights;
+  p.tokens = a.tokens;
+  p.n_expert = a.n_expert;
+  p.top_k = a.top_k;
+  p.renormalize = a.renormalize;
+  p.slots = max_slots(a.tokens, a.n_expert, a.top_k);
+  p.routed_scale = a.routed_scale;
+  p.by_token = by_token;
+  p.x = static_cast<const uint16_t*>(a.x);
+  p.router = static_cast<const uint16_t*>(a.router);
+  p.ldx = a.ldx;
+  p.hidden = a.hidden;
+  // The routing's one work-group forms the logits of a small router as well, one item of work a
+  // wave: a launch less (us for the layer: 4096 products of a router element and a group of
+  // tokens 14.9 -> 13.3, 8192 15.8 -> 15.0; 10240 14.4 -> 14.6, 65536 16.6 -> 20.0).
+  const int items = a.n_expert * ((a.tokens + 3) / 4);
+  if (items <= kMaxT && items * a.hidden <= 8192) {
+    hipLaunchKernelGGL((route_kernel<1, BF16 ? 2 : 1>), dim3(1), dim3(kMaxT * 64), 0, stream, p);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL((router_kernel<BF16>), dim3(a.n_expert, (a.tokens + 3) / 4),
-                     dim3(kRouterThreads), 0, stream, static_cast<const uint16_t*>(a.x), a.ldx,
-                     static_cast<const uint16_t*>(a.router), a.tokens, a.n_expert, a.hidden,
-                     m.logits);
+                     dim3(kRouterThreads), 0, stream, p.x, a.ldx, p.router, a.tokens, a.n_expert,
+                     a.hidden, m.logits);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const RouteArgs p{m.logits,   m.route, a.ids,         a.weights,
-                    a.tokens,   a.n_expert, a.top_k,    a.renormalize,
-                    max_slots(a.tokens, a.n_expert, a.top_k), a.routed_scale};
   const dim3 block(64 * a.tokens);
   if (a.n_expert <= 64)
-    hipLaunchKernelGGL((route_kernel<1>), dim3(1), block, 0, stream, p);
+    hipLaunchKernelGGL((route_kernel<1, 0>), dim3(1), block, 0, stream, p);
   else
-    hipLaunchKernelGGL((route_kernel<kMaxE / 64>), dim3(1), block, 0, stream, p);
+    hipLaunchKernelGGL((route_kernel<kMaxE / 64, 0>), dim3(1), block, 0, stream, p);
   return hipGetLastError();
 }
 
@@ -664,11 +843,16 @@ hipError_t launch_moe_type(const wq_moe_args& a, int gate_up_gpc, int down_gpc,
                            hipStream_t stream) {
   const MoeScratch m =
       scratch_of(a.workspace, a.tokens, a.n_expert, a.top_k, a.hidden, a.inter);
-  hipError_t e = launch_route<BF16>(a, m, stream);
+  // A work-group takes all slots' groups of a column block while that is two for each wave: two
+  // launches become one (us, product and combine / down_all: 16 groups 14.6, 14.0; 30 19.6, 18.9;
+  // 48 14.9, 16.6; 64 16.5, 20.6).
+  const bool down_all = max_slots(a.tokens, a.n_expert, a.top_k) * (a.inter / kGroup) <= 32;
+  hipError_t e = launch_route<BF16>(a, m, down_all, stream);
   if (e != hipSuccess) return e;
-  e = launch_product_type<true, BF16>(gate_up_gpc, a, m, stream);
+  e = launch_bank_type<true, false, BF16>(gate_up_gpc, a, m, stream);
   if (e != hipSuccess) return e;
-  e = launch_product_type<false, BF16>(down_gpc, a, m, stream);
+  if (down_all) return launch_bank_type<false, true, BF16>(down_gpc, a, m, stream);
+  e = launch_bank_type<false, false, BF16>(down_gpc, a, m, stream);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((combine_kernel<BF16>), dim3((a.hidden + 1023) / 1024, a.tokens), dim3(256),
                      0, stream, m.part, m.route, a.top_k, a.hidden,

@@ -2,10 +2,11 @@
 //
 // Each live K and V element is read once and takes part in 2 * (query heads per KV head)
 // products, so the kernel is bound by the cache reads.  The batch's positions are cut into
-// equal ranges; a work-group takes a range for one KV head and up to 16 of its query heads.
-// Its waves take tiles of 32 or 64 positions in turn and keep their own running maximum, sum
-// and output, joined at the end of each sequence through LDS.  Sequences that lie in several
-// ranges leave fp32 partials that attn_join_kernel adds in their order.
+// equal ranges (a range a sequence where these are short); a work-group takes a range for one KV
+// head and up to 16 of its query heads.  Its waves take tiles of 32 or 64 positions in turn and
+// keep their own running maximum, sum and output, joined at the end of each sequence through
+// LDS.  Sequences that lie in several ranges leave fp32 partials that attn_join_kernel adds in
+// their order.
 //
 // Both products run on 16x16x32 MFMAs with the positions as rows:
 //  - S^T = K Q^T: the A operand is K straight from memory (a lane holds 8 consecutive
@@ -25,6 +26,14 @@
 // One register set serves the loads: K of the next tile is requested when this tile's scores
 // are formed, V when this tile's V has gone to LDS, so each wave keeps about a tile in
 // flight.  Page numbers are read a tile further ahead.
+//
+// Measured as a graph, and in a kernel trace, 8 KV heads of 128: one sequence of 131072 positions,
+// bf16, 91 us, 5.9 TB/s (88.5 us and the join's 4.9; the matrix units are busy 6% of the time);
+// 16 sequences of up to 4096, 30 us, 4.5 TB/s (27.3, and 4.5); 64 of up to 8192, E4M3,
+// 70% of the positions kept, 87 us, 4.3 TB/s of the kept rows (82.6, and 5.8; matrix units 15%,
+// dropped rows and conversions between); one sequence of 128: 5.5 us, the launch and the trips to
+// memory for the page, K and V.  No byte is fetched twice: the counters show the kept rows' bytes
+// and the table's.
 #include <algorithm>
 
 #include "wq_decode.h"
@@ -301,11 +310,16 @@ __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
       }
     };
     const int vcol = CE * (lane % CPR);
+    // V is read once and by whole rows, so it need not stay in the caches (16 sequences of up to
+    // 4096: 34.1 us, 30.0 so; 64 of 8192, 373 and 337; only heads that share their lines with other
+    // heads are slower, 112 sequences of slot-major heads of 96, 154 and 158).  A 64-byte piece
+    // of K's rows is followed by the rest of its line, which has to be there still (one sequence
+    // of 131072 slot-major positions: 99.0 us, V read so 91.0, both 100.8).
     const auto load_v = [&] {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        vr[j] = *reinterpret_cast<const u32x4*>(
-            vbase + (off_lds[wave][j * RPI + lane / CPR] + vec_at(vcol)) * (KV8 ? 1 : 2));
+        vr[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(
+            vbase + (off_lds[wave][j * RPI + lane / CPR] + vec_at(vcol)) * (KV8 ? 1 : 2)));
     };
 
     uint16_t* const v_lds = reinterpret_cast<uint16_t*>(lds) + wave * TILE * VS;
@@ -502,7 +516,9 @@ __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
 }
 
 // Joins the parts of one query head: groups of threads, each d / 4 wide, take parts in turn
-// and are added in group order.  Sequences of one part are done; empty ones become 0.
+// and are added in group order.  Sequences of one part are done; empty ones become 0.  Bound by
+// its launch and two trips to memory, the part numbers and the parts: 4.5 us for 16 sequences of
+// 32 heads.
 constexpr int kJoinThreads = 256;
 
 template <bool BF16>
@@ -570,13 +586,14 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs p) {
 
 // Work-groups to cut the batch for.  A single sequence is cut evenly, into as many as hold the
 // bytes in flight that the memory needs, 64 KiB on each CU (bf16, head_dim 128, 131072
-// positions: 256 work-groups 99.2 us, 512 103.4, 1024 105.7).  Several sequences' ranges begin
-// and end inside sequences, so there are as many as the CUs hold at once by their registers
-// (16 sequences of up to 4096: 256 work-groups 36.4 us, 512 34.2, 768 39.5; E4M3, 64 of up to
-// 8192, masked: 256 109.0, 512 88.8, 768 104.5).
-int attn_groups(int batch, int head_dim) {
+// positions: 256 work-groups 91.0 us, 512 95.2, 1024 97.9; head_dim 64 54.6, 49.7, 55.9).  Several
+// sequences' ranges begin and end inside sequences, so there are as many as the CUs hold at once
+// by their registers (16 sequences of up to 4096: 256 work-groups 32.4 us, 512 30.1, 768 35.6;
+// E4M3, 64 of up to 8192, masked: 256 109.1, 512 87.4, 768 103.2; head_dim 256: 57.9, 61.1, 70.3,
+// E4M3 62.2, 58.5, 65.5; head_dim 64: 65.8, 54.8, 54.7).
+int attn_groups(int batch, int head_dim, bool kv8) {
   if (batch == 1) return head_dim <= 64 ? 512 : 256;
-  return head_dim <= 64 ? 768 : head_dim <= 128 ? 512 : 256;
+  return head_dim <= 64 ? 768 : head_dim <= 128 || kv8 ? 512 : 256;
 }
 
 AttnPlan attn_plan(int batch, int q_heads, int kv_heads, int head_dim, int max_len, int window,
@@ -595,7 +612,7 @@ AttnPlan attn_plan(int batch, int q_heads, int kv_heads, int head_dim, int max_l
   const long keys = span * head_dim * (kv8 ? 1 : 2);
   const long whole = std::min(256l, std::max(96l, (long)batch * plan.units)) * 1024;
   if (span > kWaves * tile && keys > whole) {
-    const int groups = attn_groups(batch, head_dim);
+    const int groups = attn_groups(batch, head_dim, kv8);
     plan.ranges = groups / plan.units > 0 ? groups / plan.units : 1;
   }
   return plan;

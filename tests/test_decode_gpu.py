@@ -270,6 +270,7 @@ def test_attention_heads(dev, dtype, kind, d, hq, hkv, page, order):
     ([700, 33, 1], dict(window=1)), ([700, 33, 1], dict(window=32)), ([700, 33], dict(window=4000)),
     ([513, 64], dict(softcap=20.0)), ([900, 300, 40], dict(keep=True)),
     ([3000, 1], dict(keep=True, window=1500, softcap=5.0)),
+    ([700, 33, 1], dict(hq=40, hkv=2)), ([0, 3, 64, 129] * 5, dict(hq=34)),
     ([9000, 40, 6000], dict(window=5000)), ([7000, 1], dict(keep=True, window=6500, softcap=5.0)),
 ])
 @pytest.mark.parametrize("kind", ["same", "e4m3"])

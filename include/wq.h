@@ -403,8 +403,8 @@ typedef struct wq_norm_args {
 
 /*
  * RMS norm with the residual add: s = x + delta (x alone without delta), and for each row
- * y = s / sqrt(mean(s^2) + eps) * weight.  The sum stays in fp32 for the norm: y and
- * sum_out are each rounded once.
+ * y = s / sqrt(mean(s^2) + eps) * weight.  The sum and its squares stay in fp32 for the norm: y
+ * and sum_out are each rounded once, and a row whose squares pass fp32 gives 0.
  */
 int wq_add_rms_norm(const wq_norm_args* args);
 
@@ -496,10 +496,10 @@ int wq_paged_attention_workspace_bytes(int batch, int q_heads, int kv_heads, int
  * Attention of one new token per sequence over the paged cache: out = sum_j p_j v_j with p
  * the softmax over the sequence's live positions j (j < len, inside the window, kept, and on
  * a page number inside the cache: other entries are never followed) of scale * q . k_j.
- * Statistics and sums are fp32.  A sequence without live positions gives 0, and lse -inf
- * (lse: log of the sum of exp of the scores).  Values outside the live positions are never
- * used, NaN and infinities among them.  Splits of a long sequence are joined in order, so
- * results do not depend on scheduling.
+ * Statistics and sums are fp32.  A sequence without live positions, or whose scores are all
+ * -inf, gives 0, and lse -inf (lse: log of the sum of exp of the scores).  Values outside the
+ * live positions are never used, NaN and infinities among them.  Splits of a long sequence are
+ * joined in order, so results do not depend on scheduling.
  */
 int wq_paged_attention(const wq_attn_args* args);
 
@@ -553,7 +553,8 @@ int wq_moe_layer_workspace_bytes(int tokens, int n_expert, int top_k, int hidden
  *   w = routed_scale * p (divided by the chosen ones' sum with `renormalize`);
  *   y = residual + sum over the chosen e of w_e * down_e(silu(x gate_e) * (x up_e)).
  * Sums are fp32 (the router's fp64); the activation between the two products is rounded to
- * the element type, y once.  A NaN logit makes its token's weights, and so its row, NaN.
+ * the element type, y once.  A NaN logit, or a largest one
+ * that is infinite, makes its token's weights, and so its row, NaN.
  */
 int wq_moe_layer(const wq_moe_args* args);
 

@@ -317,6 +317,25 @@ def test_attention_live_infinities_and_nan(dev):
         assert bool(out[2].isfinite().all()) and bool(lse[0].isfinite().all())
 
 
+def test_attention_scores_of_minus_infinity(dev):
+    """They count for nothing, beside others and alone."""
+    c = attn_case(dev, [300, 40], 2, 1, 64, 16, BF16, poison=False)
+    c["q"].abs_()
+    cut_off = c["table"][0, 2:9].long()
+    c["cache"].k[cut_off] = 0
+    c["cache"].k[cut_off, :, 0, 0] = float("-inf")
+    c["cache"].k[c["table"][1, :3].long()] = 0
+    c["cache"].k[c["table"][1, :3].long(), :, 0, 0] = float("-inf")
+    kept = dict(c, keep=torch.ones((2, 300), dtype=torch.uint8, device=dev))
+    kept["keep"][0, 32:144] = 0
+    kept["keep"][1] = 0
+    for cut in (False, True):
+        out, lse = attn_run(c, cut)
+        want, want_lse = attn_run(kept, cut)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+        assert bool((out[1] == 0).all()) and bool((lse[1] == -math.inf).all())
+
+
 def test_an_e4m3_cache_without_scales(dev):
     g = rng_of(dev, 21)
     cache = decode.PagedCache.empty(8, 16, 2, 64, E4M3, dev)
@@ -530,14 +549,16 @@ def test_moe_shapes(dev, tokens, experts, top_k, hidden, inter, renorm):
     moe_check(c, renormalize=renorm, scale=2.5)
 
 
-def test_moe_ties_take_the_lowest_expert(dev):
-    c = moe_case(dev, 4, 70, 5, 256, 128, F16)
+@pytest.mark.parametrize("experts", [12, 40, 70])
+def test_moe_ties_take_the_lowest_expert(dev, experts):
+    c = moe_case(dev, 4, experts, 5, 256, 128, F16)
     c["router"][:] = 0
-    c["router"][[3, 40, 68]] = c["router"].new_ones(256) * 0.5  # equal logits, either sign
+    equal = [3, experts // 2 + 1, experts - 2]
+    c["router"][equal] = c["router"].new_ones(256) * 0.5  # equal logits, either sign
     layer, _ = moe_check(c)
     for t in range(4):
         up = float(c["x"][t].double().sum()) > 0
-        assert layer.ids[t].tolist() == ([3, 40, 68, 0, 1] if up else [0, 1, 2, 4, 5])
+        assert layer.ids[t].tolist() == (equal + [0, 1] if up else [0, 1, 2, 4, 5])
 
 
 def test_moe_strides_aliases_and_nan_rows(dev):

@@ -542,7 +542,8 @@ def test_moe_weights(dev, dtype, kind, group, hidden, inter):
     (16, 4, 4, 256, 128, False), (16, 64, 8, 256, 128, True), (7, 256, 16, 256, 128, False),
     (13, 65, 3, 768, 128, True), (16, 1, 1, 1280, 640, True), (3, 100, 1, 256, 256, False),
     (9, 5, 3, 512, 768, True), (1, 16, 4, 512, 1024, True), (4, 3, 2, 2560, 256, False),
-    (16, 2, 1, 1024, 2048, True), (1, 1, 1, 8192, 128, True), (2, 20, 16, 256, 256, True),
+    (16, 2, 1, 1024, 2048, True), (1, 1, 1, 8192, 128, True), (1, 3, 2, 1280, 512, True),
+    (1, 16, 16, 2048, 128, False), (1, 17, 2, 256, 256, True), (1, 8, 2, 4352, 128, True), (2, 20, 16, 256, 256, True),
 ])
 def test_moe_shapes(dev, tokens, experts, top_k, hidden, inter, renorm):
     c = moe_case(dev, tokens, experts, top_k, hidden, inter, BF16)

@@ -62,25 +62,25 @@ size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 constexpr int kRouterThreads = 256;
 
-// Products of one expert's router row with four tokens (past the last: the last one), over k0,
-// k0 + step, ... of the hidden size, 8 elements each; lanes 16 j, ... of the wave return token
-// t0 + j's sum over the wave.  Eight products at a time are summed in fp32, the sums in fp64 and
-// rounded once: the order of nearly equal logits decides which experts run.
-template <bool BF16, int UNROLL>
+// Products of one expert's router row with T = 1 or 4 tokens (past the last: the last one), over
+// k0, k0 + step, ... of the hidden size, 8 elements each; lanes 64 / T * j, ... of the wave return
+// token t0 + j's sum over the wave.  Eight products at a time are summed in fp32, the sums in
+// fp64 and rounded once: the order of nearly equal logits decides which experts run.
+template <bool BF16, int T, int UNROLL>
 __device__ __forceinline__ double wave_logits(const uint16_t* x, int ldx, const uint16_t* rp,
                                               int tokens, int t0, int k0, int step, int end,
                                               int lane) {
   using A = Act<BF16>;
-  double acc[4] = {0., 0., 0., 0.};
+  double acc[T] = {};
 #pragma unroll UNROLL
   for (int k = k0; k < end; k += step) {
     const u32x4 r = *reinterpret_cast<const u32x4*>(rp + k);
-    u32x4 xv[4];
+    u32x4 xv[T];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < T; ++j)
       xv[j] = *reinterpret_cast<const u32x4*>(x + (long)min(t0 + j, tokens - 1) * ldx + k);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < T; ++j) {
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -89,14 +89,17 @@ __device__ __forceinline__ double wave_logits(const uint16_t* x, int ldx, const 
       acc[j] += (double)sum;
     }
   }
-  // Each exchange halves the tokens a lane carries, then adds over the lanes left.
-  const bool up = lane & 32, odd = lane & 16;
-  const double a0 = (up ? acc[2] : acc[0]) + __shfl_xor(up ? acc[0] : acc[2], 32);
-  const double a1 = (up ? acc[3] : acc[1]) + __shfl_xor(up ? acc[1] : acc[3], 32);
-  double v = (odd ? a1 : a0) + __shfl_xor(odd ? a0 : a1, 16);
+  double v = acc[0];
+  if constexpr (T == 4) {
+    // Each exchange halves the tokens a lane carries: token 2 * up + odd is left.
+    const bool up = lane & 32, odd = lane & 16;
+    const double a0 = (up ? acc[2] : acc[0]) + __shfl_xor(up ? acc[0] : acc[2], 32);
+    const double a1 = (up ? acc[3] : acc[1]) + __shfl_xor(up ? acc[1] : acc[3], 32);
+    v = (odd ? a1 : a0) + __shfl_xor(odd ? a0 : a1, 16);
+  }
 #pragma unroll
-  for (int d = 8; d >= 1; d /= 2) v += __shfl_xor(v, d);
-  return v;  // token 2 * up + odd
+  for (int d = 32 / T; d >= 1; d /= 2) v += __shfl_xor(v, d);
+  return v;
 }
 
 // Logits of one expert and four tokens per work-group, whose threads share the hidden size: 2 us,
@@ -110,7 +113,7 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int e = blockIdx.x;
   const int t0 = blockIdx.y * 4;
-  const double v = wave_logits<BF16, 2>(x, ldx, router + (long)e * hidden, tokens, t0, tid * 8,
+  const double v = wave_logits<BF16, 4, 2>(x, ldx, router + (long)e * hidden, tokens, t0, tid * 8,
                                         kRouterThreads * 8, hidden, lane);
   if ((lane & 15) == 0) red[wave][lane >> 4] = v;
   __syncthreads();
@@ -236,9 +239,9 @@ struct RouteArgs {
 
 // One work-group, a wave per token; 2.0 us for one token of 8 experts, 4.6 for 16 of 64, a chain
 // of three trips to memory and LDS.  PER: 64 experts for each lane of a wave, 1 or 4.  ROUTER: 16
-// waves form the logits here too, first, (1: fp16, 2: bf16): an expert and four tokens for each,
-// or with fewer of these a part of the hidden size.
-template <int PER, int ROUTER>
+// waves form the logits here too, first, (1: fp16, 2: bf16): an expert and T tokens for each, or
+// with fewer of these a part of the hidden size.
+template <int PER, int ROUTER, int T>
 __global__ __launch_bounds__(kMaxT * 64) void route_kernel(RouteArgs p) {
   __shared__ uint32_t mask_lds[kMaxE];
   __shared__ uint8_t slot_of[kMaxE];
@@ -247,21 +250,21 @@ __global__ __launch_bounds__(kMaxT * 64) void route_kernel(RouteArgs p) {
   for (int i = tid; i < kMaxE; i += blockDim.x) mask_lds[i] = 0;
   const float* logits = p.logits;
   if constexpr (ROUTER != 0) {
-    __shared__ double part_lds[kMaxT][4];
-    __shared__ float logit_lds[kMaxT * 4];
-    const int quads = (p.tokens + 3) / 4, items = p.n_expert * quads, segs = kMaxT / items;
+    __shared__ double part_lds[kMaxT][T];
+    __shared__ float logit_lds[kMaxT * T];
+    const int parts = (p.tokens + T - 1) / T, items = p.n_expert * parts, segs = kMaxT / items;
     if (wave < items * segs) {
-      const int item = wave / segs, e = item / quads, t0 = 4 * (item - e * quads);
+      const int item = wave / segs, e = item / parts, t0 = T * (item - e * parts);
       const int k0 = (wave - item * segs) * 512 + lane * 8;
-      const double v = wave_logits<ROUTER == 2, 4>(p.x, p.ldx, p.router + (long)e * p.hidden,
-                                                   p.tokens, t0, k0, segs * 512, p.hidden, lane);
-      if ((lane & 15) == 0) part_lds[wave][lane >> 4] = v;
+      const double v = wave_logits<ROUTER == 2, T, 4>(p.x, p.ldx, p.router + (long)e * p.hidden,
+                                                      p.tokens, t0, k0, segs * 512, p.hidden, lane);
+      if (lane % (64 / T) == 0) part_lds[wave][lane / (64 / T)] = v;
     }
     __syncthreads();
-    if (tid < 4 * items) {
-      const int item = tid / 4, e = item / quads, t = 4 * (item - e * quads) + tid % 4;
+    if (tid < T * items) {
+      const int item = tid / T, e = item / parts, t = T * (item - e * parts) + tid % T;
       double sum = 0.;
-      for (int k = 0; k < segs; ++k) sum += part_lds[item * segs + k][tid % 4];
+      for (int k = 0; k < segs; ++k) sum += part_lds[item * segs + k][tid % T];
       if (t < p.tokens) logit_lds[t * p.n_expert + e] = (float)sum;
     }
     logits = logit_lds;
@@ -825,11 +828,16 @@ hipError_t launch_route(const wq_moe_args& a, const MoeScratch& m, bool by_token
   p.ldx = a.ldx;
   p.hidden = a.hidden;
   // The routing's one work-group forms the logits of a small router as well, one item of work a
-  // wave: a launch less (us for the layer: 4096 products of a router element and a group of
-  // tokens 14.9 -> 13.3, 8192 15.8 -> 15.0; 10240 14.4 -> 14.6, 65536 16.6 -> 20.0).
+  // wave: a launch less (us for the layer: 4096 products of a router element and four tokens
+  // 14.9 -> 13.3, 8192 15.8 -> 15.0; 10240 14.4 -> 14.6, 65536 16.6 -> 20.0; of one token 8192
+  // 11.7 -> 10.9, 32768 43.0 -> 42.2, 65536 14.6 -> 14.3 or 15.1, 131072 18.3 -> 19.7).
   const int items = a.n_expert * ((a.tokens + 3) / 4);
-  if (items <= kMaxT && items * a.hidden <= 8192) {
-    hipLaunchKernelGGL((route_kernel<1, BF16 ? 2 : 1>), dim3(1), dim3(kMaxT * 64), 0, stream, p);
+  if (items <= kMaxT && items * a.hidden <= (a.tokens == 1 ? 32768 : 8192)) {
+    constexpr int R = BF16 ? 2 : 1;
+    if (a.tokens == 1)
+      hipLaunchKernelGGL((route_kernel<1, R, 1>), dim3(1), dim3(kMaxT * 64), 0, stream, p);
+    else
+      hipLaunchKernelGGL((route_kernel<1, R, 4>), dim3(1), dim3(kMaxT * 64), 0, stream, p);
     return hipGetLastError();
   }
   hipLaunchKernelGGL((router_kernel<BF16>), dim3(a.n_expert, (a.tokens + 3) / 4),
@@ -839,9 +847,9 @@ hipError_t launch_route(const wq_moe_args& a, const MoeScratch& m, bool by_token
   if (e != hipSuccess) return e;
   const dim3 block(64 * a.tokens);
   if (a.n_expert <= 64)
-    hipLaunchKernelGGL((route_kernel<1, 0>), dim3(1), block, 0, stream, p);
+    hipLaunchKernelGGL((route_kernel<1, 0, 1>), dim3(1), block, 0, stream, p);
   else
-    hipLaunchKernelGGL((route_kernel<kMaxE / 64, 0>), dim3(1), block, 0, stream, p);
+    hipLaunchKernelGGL((route_kernel<kMaxE / 64, 0, 1>), dim3(1), block, 0, stream, p);
   return hipGetLastError();
 }
 

@@ -256,7 +256,8 @@ def attn_check(c, out, lse, label=""):
 @pytest.mark.parametrize("d,hq,hkv,page,order", [
     (16, 1, 1, 1, "hnd"), (64, 4, 4, 16, "nhd"), (72, 6, 2, 5, "hnd"), (80, 3, 3, 24, "nhd"),
     (96, 20, 1, 16, "hnd"), (128, 8, 1, 16, "hnd"), (128, 40, 2, 64, "nhd"), (136, 2, 1, 32, "hnd"),
-    (192, 16, 1, 7, "nhd"), (256, 5, 1, 16, "hnd")])
+    (160, 4, 2, 16, "hnd"), (184, 2, 1, 16, "nhd"), (192, 16, 1, 7, "nhd"), (200, 3, 1, 9, "hnd"),
+    (256, 5, 1, 16, "hnd")])
 def test_attention_heads(dev, dtype, kind, d, hq, hkv, page, order):
     c = attn_case(dev, [0, 1, 15, 31, 32, 33, 127, 300], hq, hkv, d, page, dtype, kind, order)
     for cut in (False, True):

@@ -35,6 +35,7 @@
 // memory for the page, K and V.  No byte is fetched twice: the counters show the kept rows' bytes
 // and the table's.
 #include <algorithm>
+#include <type_traits>
 
 #include "wq_decode.h"
 #include "wq_device.h"
@@ -44,7 +45,7 @@ namespace {
 
 constexpr int kWaves = 4;
 
-// Positions of a wave's step (dp: head_dim rounded up to 64, 128 or 256).  64 rows of an E4M3
+// Positions of a wave's step (dp: head_dim rounded up to 64, 128 or more).  64 rows of an E4M3
 // head of 128 keep 16 KiB requested, as 32 of a 16-bit one do (16 sequences of 4096 positions:
 // 36.4 us with 32, 34.7 with 64; one of 65536: 35.3 and 32.7).  16-bit heads of 64 are faster
 // with 32, whose registers leave room for a third work-group on the CU.
@@ -201,7 +202,7 @@ __device__ __forceinline__ void split_p(const float* p, f16x8& high, f16x8& low)
   __builtin_memcpy(&low, lo, 16);
 }
 
-// DP: head_dim rounded up to 64, 128 or 256; FULL: head_dim is DP.
+// DP: head_dim rounded up (launch_attn); FULL: head_dim is DP.
 template <bool BF16, bool KV8, int DP, bool FULL>
 __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
   using A = Act<BF16>;
@@ -211,10 +212,9 @@ __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
   constexpr int NK = KV8 ? NS / 2 : NS;  // 16-byte K vectors per lane and position block
   constexpr int CE = KV8 ? 16 : 8;       // elements of a 16-byte vector
   constexpr int CPR = DP / CE;           // vectors of a V row
-  constexpr int RPI = 64 / CPR;          // V rows of one load
-  constexpr int NV = TILE / RPI;
+  constexpr int NV = TILE * CPR / 64;    // V vectors per lane
   constexpr int NB = DP / 16;            // 16-element blocks of the output
-  constexpr int VS = DP + 16;            // LDS row of V: rows start 8 banks apart
+  constexpr int VS = DP + 16;            // LDS row of V: rows start 8 banks apart, or more
   constexpr int OS = DP + 4;             // LDS row of the joined outputs
   constexpr int kVBytes = kWaves * TILE * VS * 2, kOBytes = kWaves * 16 * OS * 4;
   __shared__ __align__(16) uint8_t lds[kVBytes > kOBytes ? kVBytes : kOBytes];
@@ -316,7 +316,6 @@ __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
               kp + vec_at(4 * CE * s + CE * qd) * (KV8 ? 1 : 2));
       }
     };
-    const int vcol = CE * (lane % CPR);
     // V is read once and by whole rows, so it need not stay in the caches (16 sequences of up to
     // 4096: 34.1 us, 30.0 so; 64 of 8192, 373 and 337).  A 64-byte piece
     // of K's rows is followed by the rest of its line, which has to be there still (one sequence
@@ -325,7 +324,8 @@ __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
         vr[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(
-            vbase + (off_lds[wave][j * RPI + lane / CPR] + vec_at(vcol)) * (KV8 ? 1 : 2)));
+            vbase + (off_lds[wave][(64 * j + lane) / CPR] + vec_at(CE * ((64 * j + lane) % CPR))) *
+                        (KV8 ? 1 : 2)));
     };
 
     uint16_t* const v_lds = reinterpret_cast<uint16_t*>(lds) + wave * TILE * VS;
@@ -427,7 +427,7 @@ __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
       // V to LDS as 16-bit rows, zero where a position is not live
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int r = j * RPI + lane / CPR;
+        const int r = (64 * j + lane) / CPR, vcol = CE * ((64 * j + lane) % CPR);
         u32x4 w = vec_fix(vr[j], vcol);
         if (now != ~0ull && !((now >> r) & 1)) w = u32x4{0u, 0u, 0u, 0u};
         if constexpr (KV8) {
@@ -519,6 +519,29 @@ __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
     } while (granules_of<TILE>(p, max(0, min(p.lens[rg.b], p.max_len))) == 0);
     __syncthreads();  // the joined outputs are no longer read
   }
+}
+
+// The instance for a head_dim.  Rounded up to 64 and to powers of two from there; 96 and 192 as
+// well, where the rest of the next power of two costs registers, LDS and loads (16 sequences of up
+// to 4096, us with 128 or 256 and so: heads of 80 26.0, 25.0; 96 27.5, 25.2; 192 52.3, 46.2, E4M3
+// 32.5, 28.6; 160 46.7, 47.4).  A step of the head is 64 elements of an E4M3 row: no 96 there.
+template <bool BF16, bool KV8>
+void launch_attn(const AttnArgs& p, dim3 grid, hipStream_t stream) {
+  const auto run = [&](auto dp) {
+    constexpr int DP = decltype(dp)::value;
+    const dim3 block(kWaves * 64);
+    if (p.d == DP)
+      hipLaunchKernelGGL((attn_kernel<BF16, KV8, DP, true>), grid, block, 0, stream, p);
+    else
+      hipLaunchKernelGGL((attn_kernel<BF16, KV8, DP, false>), grid, block, 0, stream, p);
+  };
+  if (p.d <= 64) return run(std::integral_constant<int, 64>());
+  if constexpr (!KV8) {
+    if (p.d <= 96) return run(std::integral_constant<int, 96>());
+  }
+  if (p.d <= 128) return run(std::integral_constant<int, 128>());
+  if (p.d <= 192) return run(std::integral_constant<int, 192>());
+  run(std::integral_constant<int, 256>());
 }
 
 // Joins the parts of one query head: groups of threads, each d / 4 wide, take parts in turn
@@ -689,24 +712,10 @@ hipError_t launch_paged_attention(const wq_attn_args& a, const AttnPlan& plan,
   size_t rows = plan.ranges > 0 ? plan.ranges : a.batch;
   if (p.near_units) rows = (rows + 7) / 8 * 8;
   const dim3 grid((unsigned)(rows * plan.units));
-#define WQ_ATTN(B, F, D, FULL)                                                                \
-  hipLaunchKernelGGL((attn_kernel<B, F, D, FULL>), grid, dim3(kWaves * 64), 0, stream, p)
-#define WQ_ATTN_D(B, F)                                                                       \
-  do {                                                                                        \
-    if (p.d == 64) WQ_ATTN(B, F, 64, true);                                                   \
-    else if (p.d < 64) WQ_ATTN(B, F, 64, false);                                              \
-    else if (p.d == 128) WQ_ATTN(B, F, 128, true);                                            \
-    else if (p.d < 128) WQ_ATTN(B, F, 128, false);                                            \
-    else if (p.d == 256) WQ_ATTN(B, F, 256, true);                                            \
-    else WQ_ATTN(B, F, 256, false);                                                           \
-  } while (0)
-  if (bf16) {
-    if (kv8) WQ_ATTN_D(true, true); else WQ_ATTN_D(true, false);
-  } else {
-    if (kv8) WQ_ATTN_D(false, true); else WQ_ATTN_D(false, false);
-  }
-#undef WQ_ATTN_D
-#undef WQ_ATTN
+  if (bf16)
+    kv8 ? launch_attn<true, true>(p, grid, stream) : launch_attn<true, false>(p, grid, stream);
+  else
+    kv8 ? launch_attn<false, true>(p, grid, stream) : launch_attn<false, false>(p, grid, stream);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || plan.ranges == 0) return e;
   const dim3 join((unsigned)a.q_heads, (unsigned)a.batch);

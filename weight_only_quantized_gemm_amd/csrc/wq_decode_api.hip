@@ -96,7 +96,8 @@ int wq_rope_append(const wq_rope_args* args) {
   if ((st = check_cache(a.cache, a.flags))) return st;
   const int64_t d = a.cache.head_dim;
   if (a.tokens < 1 || a.tokens > kMaxTokens || a.q_heads < 0 || a.q_heads > kMaxHeads ||
-      a.rot_dim < 0 || a.rot_dim > d || a.rot_dim % 8 != 0 || a.axes < 1 || a.axes > WQ_MAX_ROPE_AXES)
+      a.rot_dim < 0 || a.rot_dim > d || a.rot_dim % 8 != 0 || a.axes < 1 ||
+      a.axes > WQ_MAX_ROPE_AXES)
     return shape_error();
   if (!row_stride_ok(a.ldk, a.cache.kv_heads * d) || !row_stride_ok(a.ldv, a.cache.kv_heads * d) ||
       (a.q_heads > 0 &&

@@ -22,8 +22,8 @@
 //
 // Measured as a graph, 128-row groups, K x N of an expert 4096 x 2 * 14336 and 14336 x 4096: one
 // token of two experts, fp16, 43 us, 4.2 TB/s (products 23.5 us at 5.2 TB/s and 13.5 at 4.5 in a
-// kernel trace, routing 4.6, combine 3.4); four tokens of five to six experts, bf16 with zero points,
-// 95 us, 5.2 TB/s (56.4 us at 6.0, 33.9 at 5.0).  16 tokens over 56 of 64 experts of
+// kernel trace, routing 4.6, combine 3.4); four tokens of five to six experts, bf16 with zero
+// points, 95 us, 5.2 TB/s (56.4 us at 6.0, 33.9 at 5.0).  16 tokens over 56 of 64 experts of
 // 2048 x 2 * 1024, 64-row groups, 47 us, 4.0 TB/s (24.1 us at 5.2, 14.4 at 4.5).
 #include "wq_decode.h"
 #include "wq_device.h"
@@ -238,9 +238,9 @@ struct RouteArgs {
 };
 
 // One work-group, a wave per token; 2.4 us for one token of 8 experts (4.6 with the logits of
-// 4096 elements), 4.1 for 16 of 64: a chain of trips to memory and LDS.  PER: 64 experts for each lane of a wave, 1 or 4.  ROUTER: 16
-// waves form the logits here too, first, (1: fp16, 2: bf16): an expert and T tokens for each, or
-// with fewer of these a part of the hidden size.
+// 4096 elements), 4.1 for 16 of 64: a chain of trips to memory and LDS.  PER: 64 experts for each
+// lane of a wave, 1 or 4.  ROUTER: 16 waves form the logits here too, first (1: fp16, 2: bf16): an
+// expert and T tokens for each, or with fewer of these a part of the hidden size.
 template <int PER, int ROUTER, int T>
 __global__ __launch_bounds__(kMaxT * 64) void route_kernel(RouteArgs p) {
   __shared__ uint32_t mask_lds[kMaxE];

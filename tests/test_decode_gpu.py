@@ -296,6 +296,16 @@ def test_attention_many_sequences(dev, batch, longest, hq, hkv):
             attn_check(c, *attn_run(c, cut), f"cut {cut}")
 
 
+@pytest.mark.parametrize("kw", [{}, dict(kind="e4m3"), dict(keep=True)])
+def test_attention_several_short_sequences_in_a_range(dev, kw):
+    """Waves with no, one, two and more tiles of a sequence, in every order."""
+    g = np.random.default_rng(7)
+    sizes = np.array([0, 1, 31, 32, 33, 64, 96, 127, 128, 129, 160, 200, 256, 257, 300, 390])
+    lens = sizes[g.integers(0, len(sizes), 260)]
+    c = attn_case(dev, lens.tolist(), 8, 8, 64, 16, F16, **kw)
+    attn_check(c, *attn_run(c, True))
+
+
 def test_attention_a_split_without_kept_positions(dev):
     """Whole splits masked away, the first and one between others."""
     c = attn_case(dev, [6000, 5000], 4, 1, 64, 16, F16, keep=True, poison=False)

@@ -237,116 +237,147 @@ __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
   const int h0 = kvh * p.group + 16 * hb;         // first query head
   const int rows = min(16, p.group - 16 * hb);
 
-  for (;;) {  // the range's sequences
-    const int b = rg.b;
+  // Part of a sequence that this range holds.
+  struct Part {
+    int b, lo, t0, t1;           // sequence, first live position, positions [t0, t1)
+    int t_pages;                 // page numbers are read for positions below it
+    int first, count, granules;  // granules of the sequence: first one here, how many, in all
+  };
+  const auto part_of = [&](int b, int first, int left) {
+    Part s;
     const int len = max(0, min(p.lens[b], p.max_len));
-    const int lo = p.window > 0 ? max(0, len - p.window) : 0;  // first live position
-    const int granules = granules_of<TILE>(p, len);
-    int t0 = window_start<TILE>(p, len), t1 = len;
-    // Page numbers are read for positions below t_pages: without ranges or a window they need
-    // not wait for the length.
-    const int t_pages = p.ranges > 0 || p.window > 0 ? len : p.max_len;
-    int count = granules;
-    if (p.ranges > 0) {
-      count = min(granules - rg.first, rg.left);
-      t1 = min(len, t0 + (rg.first + count) * kStep);
-      t0 += rg.first * kStep;
+    s.b = b;
+    s.lo = p.window > 0 ? max(0, len - p.window) : 0;
+    s.first = first;
+    s.granules = granules_of<TILE>(p, len);
+    s.count = p.ranges > 0 ? min(s.granules - first, left) : s.granules;
+    const int start = window_start<TILE>(p, len);
+    s.t0 = start + first * kStep;
+    s.t1 = p.ranges > 0 ? min(len, start + (first + s.count) * kStep) : len;
+    // without ranges or a window they need not wait for the length
+    s.t_pages = p.ranges > 0 || p.window > 0 ? len : p.max_len;
+    return s;
+  };
+
+  // Q as the B operand; query heads past the last repeat the first (never stored).
+  f16x8 qf[NS];
+  const auto load_q = [&](int b) {
+    const uint16_t* qp = p.q + (int64_t)b * p.ldq + (int64_t)(h0 + (row < rows ? row : 0)) * p.d;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const int e = KV8 ? 64 * (s / 2) + 16 * qd + 8 * (s % 2) : 32 * s + 8 * qd;
+      qf[s] = f16x8{};
+      if (FULL || e < p.d) qf[s] = *reinterpret_cast<const f16x8*>(qp + e);
     }
+  };
 
-    // Q as the B operand; query heads past the last repeat the first (never stored).
-    f16x8 qf[NS];
-    {
-      const uint16_t* qp = p.q + (int64_t)b * p.ldq + (int64_t)(h0 + (row < rows ? row : 0)) * p.d;
-#pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        const int e = KV8 ? 64 * (s / 2) + 16 * qd + 8 * (s % 2) : 32 * s + 8 * qd;
-        qf[s] = f16x8{};
-        if (FULL || e < p.d) qf[s] = *reinterpret_cast<const f16x8*>(qp + e);
-      }
+  const uint8_t* kbase = p.k + kvh * p.head_stride * (KV8 ? 1 : 2);
+  const uint8_t* vbase = p.v + kvh * p.head_stride * (KV8 ? 1 : 2);
+
+  // A vector that lies past the head's end is read from its start and not used; an E4M3
+  // vector that passes the end half way (head_dim % 16 == 8) is read 8 bytes earlier and
+  // shifted.
+  const auto vec_at = [&](int e) {
+    return FULL || e + CE <= p.d ? e : (e < p.d ? p.d - CE : 0);
+  };
+  const auto vec_fix = [&](u32x4 w, int e) {
+    if (FULL) return w;
+    if (KV8 && e < p.d && e + CE > p.d) w = u32x4{w[2], w[3], 0u, 0u};
+    return e < p.d ? w : u32x4{0u, 0u, 0u, 0u};
+  };
+
+  // Page numbers (and keep bytes) of the tile at t, one position per lane and half-wave.
+  int page_next = -1, pos_next = 0, slot_next = 0;
+  uint8_t keep_next = 1;
+  const auto read_pages = [&](int b, int t_pages, int t) {
+    const int pos = t + (lane & (TILE - 1));
+    const int at = (int)(__umulhi(2u * (unsigned)pos, p.page_mul) >> p.page_shift);
+    pos_next = pos;
+    slot_next = pos - at * p.page_size;
+    page_next = -1;
+    if (pos < t_pages) {
+      page_next = p.table[(int64_t)b * p.table_stride + at];
+      if (p.keep != nullptr) keep_next = p.keep[(int64_t)b * p.keep_stride + pos];
     }
-
-    const uint8_t* kbase = p.k + kvh * p.head_stride * (KV8 ? 1 : 2);
-    const uint8_t* vbase = p.v + kvh * p.head_stride * (KV8 ? 1 : 2);
-    const int32_t* table = p.table + (int64_t)b * p.table_stride;
-    const uint8_t* keep = p.keep != nullptr ? p.keep + (int64_t)b * p.keep_stride : nullptr;
-
-    // A vector that lies past the head's end is read from its start and not used; an E4M3
-    // vector that passes the end half way (head_dim % 16 == 8) is read 8 bytes earlier and
-    // shifted.
-    const auto vec_at = [&](int e) {
-      return FULL || e + CE <= p.d ? e : (e < p.d ? p.d - CE : 0);
-    };
-    const auto vec_fix = [&](u32x4 w, int e) {
-      if (FULL) return w;
-      if (KV8 && e < p.d && e + CE > p.d) w = u32x4{w[2], w[3], 0u, 0u};
-      return e < p.d ? w : u32x4{0u, 0u, 0u, 0u};
-    };
-
-    // Page numbers (and keep bytes) of the tile at t, one position per lane and half-wave.
-    int page_next = -1, pos_next = 0, slot_next = 0;
-    uint8_t keep_next = 1;
-    const auto read_pages = [&](int t) {
-      const int pos = t + (lane & (TILE - 1));
-      const int at = (int)(__umulhi(2u * (unsigned)pos, p.page_mul) >> p.page_shift);
-      pos_next = pos;
-      slot_next = pos - at * p.page_size;
-      page_next = -1;
-      if (pos < t_pages) {
-        page_next = table[at];
-        if (keep != nullptr) keep_next = keep[pos];
-      }
-    };
-    // Cache offsets of the tile whose pages were read; returns the mask of live positions.  A
-    // position that is not live reads the cache's first slot, and is not used.
-    const auto place = [&]() -> uint64_t {
-      const bool live = (unsigned)page_next < (unsigned)p.num_pages && keep_next != 0 &&
-                        pos_next >= lo && pos_next < t1;
-      off_lds[wave][lane & (TILE - 1)] =
-          live ? page_next * p.page_stride + slot_next * p.slot_stride : 0;
-      return __ballot(live);
-    };
-    u32x4 kr[NT][NK], vr[NV];
-    const auto load_k = [&] {
+  };
+  // Cache offsets of the tile whose pages were read; returns the mask of live positions.  A
+  // position that is not live reads the cache's first slot, and is not used.
+  const auto place = [&](int lo, int t1) -> uint64_t {
+    const bool live = (unsigned)page_next < (unsigned)p.num_pages && keep_next != 0 &&
+                      pos_next >= lo && pos_next < t1;
+    off_lds[wave][lane & (TILE - 1)] =
+        live ? page_next * p.page_stride + slot_next * p.slot_stride : 0;
+    return __ballot(live);
+  };
+  u32x4 kr[NT][NK], vr[NV];
+  const auto load_k = [&] {
 #pragma unroll
-      for (int blk = 0; blk < NT; ++blk) {
-        const uint8_t* kp = kbase + off_lds[wave][16 * blk + row] * (KV8 ? 1 : 2);
+    for (int blk = 0; blk < NT; ++blk) {
+      const uint8_t* kp = kbase + off_lds[wave][16 * blk + row] * (KV8 ? 1 : 2);
 #pragma unroll
-        for (int s = 0; s < NK; ++s)
-          kr[blk][s] = *reinterpret_cast<const u32x4*>(
-              kp + vec_at(4 * CE * s + CE * qd) * (KV8 ? 1 : 2));
-      }
-    };
-    // V is read once and by whole rows, so it need not stay in the caches (16 sequences of up to
-    // 4096: 34.1 us, 30.0 so; 64 of 8192, 373 and 337).  A 64-byte piece
-    // of K's rows is followed by the rest of its line, which has to be there still (one sequence
-    // of 131072 slot-major positions: 99.0 us, V read so 91.0, both 100.8).
-    const auto load_v = [&] {
+      for (int s = 0; s < NK; ++s)
+        kr[blk][s] = *reinterpret_cast<const u32x4*>(
+            kp + vec_at(4 * CE * s + CE * qd) * (KV8 ? 1 : 2));
+    }
+  };
+  // V is read once and by whole rows, so it need not stay in the caches (16 sequences of up to
+  // 4096: 34.1 us, 30.0 so; 64 of 8192, 373 and 337).  A 64-byte piece of K's rows is followed by
+  // the rest of its line, which has to be there still (one sequence of 131072 slot-major
+  // positions: 99.0 us, V read so 91.0, both 100.8).
+  const auto load_v = [&] {
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        vr[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(
-            vbase + (off_lds[wave][(64 * j + lane) / CPR] + vec_at(CE * ((64 * j + lane) % CPR))) *
-                        (KV8 ? 1 : 2)));
-    };
+    for (int j = 0; j < NV; ++j)
+      vr[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(
+          vbase + (off_lds[wave][(64 * j + lane) / CPR] + vec_at(CE * ((64 * j + lane) % CPR))) *
+                      (KV8 ? 1 : 2)));
+  };
 
-    uint16_t* const v_lds = reinterpret_cast<uint16_t*>(lds) + wave * TILE * VS;
-    const float kscale = KV8 && p.k_scale != nullptr ? p.k_scale[kvh] : 1.f;
-    const float sc = p.scale * kscale;
-    const float sc2 = p.softcap > 0.f ? kLog2e : sc * kLog2e;
-    const float cap = sc / p.softcap;
+  uint16_t* const v_lds = reinterpret_cast<uint16_t*>(lds) + wave * TILE * VS;
+  const float kscale = KV8 && p.k_scale != nullptr ? p.k_scale[kvh] : 1.f;
+  const float sc = p.scale * kscale;
+  const float sc2 = p.softcap > 0.f ? kLog2e : sc * kLog2e;
+  const float cap = sc / p.softcap;
+  uint64_t live = 0;
+  bool ready = false;  // this part's first tile is requested, and the next one's pages are read
+  Part cur = part_of(rg.b, rg.first, rg.left);
+  load_q(cur.b);
+
+  for (;;) {
+    rg.left -= cur.count;
+    const bool more = p.ranges > 0 && rg.left > 0;
+    Part nxt{};  // (no pages, nothing live)
+    if (more) {
+      int b = cur.b;
+      do {  // (granules are left, so a sequence with some follows)
+        ++b;
+      } while (granules_of<TILE>(p, max(0, min(p.lens[b], p.max_len))) == 0);
+      nxt = part_of(b, 0, rg.left);
+    }
+    const int b = cur.b;
     float m = -INFINITY, l = 0.f;
     f32x4 o[NB];
 #pragma unroll
     for (int i = 0; i < NB; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    int t = t0 + wave * TILE;
-    read_pages(t);  // (a wave without a tile reads the cache's first slot, and ends)
-    wave_lds_fence();
-    uint64_t live = place();
-    wave_lds_fence();
-    read_pages(t + kStep);
-    load_k();
-    load_v();
-    for (; t < t1; t += kStep) {
+    // A wave's tiles follow each other from one part to the next: a part's last tiles request the
+    // next one's first, so that it is in flight while the waves are joined (64 sequences of up to
+    // 8192, E4M3, masked: 87.2 us without, 85.0 so; 100 of up to 1500 65.9, 63.4; a single part
+    // pays 1% for the choices).  Only a wave with less than two tiles here may have none
+    // requested.
+    int t = cur.t0 + wave * TILE;
+    const int next_t = nxt.t0 + wave * TILE, tiles = t >= cur.t1 ? 0 : t + kStep >= cur.t1 ? 1 : 2;
+    if (!ready) {
+      read_pages(cur.b, cur.t_pages, t);  // (without a tile: the cache's first slot)
+      wave_lds_fence();
+      live = place(cur.lo, cur.t1);
+      wave_lds_fence();
+      const bool here = tiles != 1;
+      read_pages(here ? cur.b : nxt.b, here ? cur.t_pages : nxt.t_pages,
+                 here ? t + kStep : next_t);
+      load_k();
+      load_v();
+    }
+    for (; t < cur.t1; t += kStep) {
       // scores
       f32x4 s[NT];
 #pragma unroll
@@ -366,10 +397,13 @@ __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
       }
       const uint64_t now = live;
       // the next tile's K (positions past the range are not live and read the first slot)
+      const bool last = t + kStep >= cur.t1;
       wave_lds_fence();
-      live = place();
+      live = place(last ? nxt.lo : cur.lo, last ? nxt.t1 : cur.t1);
       wave_lds_fence();
-      read_pages(t + 2 * kStep);
+      const bool here = t + 2 * kStep < cur.t1;
+      read_pages(here ? cur.b : nxt.b, here ? cur.t_pages : nxt.t_pages,
+                 here ? t + 2 * kStep : next_t + (last ? kStep : 0));
       load_k();
 
       // running maximum and sum, in base 2
@@ -459,6 +493,9 @@ __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
       wave_lds_fence();
     }
 
+    ready = more && tiles > (ready ? 1 : 0);
+    if (more) load_q(nxt.b);
+
     // Join the waves, in wave order.
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
@@ -491,10 +528,10 @@ __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
         for (int c = 0; c < 4; ++c) acc[c] = __builtin_fmaf(x[c], f, acc[c]);
       }
       const int64_t h = (int64_t)b * p.q_heads + h0 + r;
-      if (count < granules) {
+      if (cur.count < cur.granules) {
         // a sequence that began in an earlier range leaves the range's first partial, one that
         // goes on in the next its second
-        const int64_t part = 2 * index + (rg.first == 0);
+        const int64_t part = 2 * index + (cur.first == 0);
         const int64_t at = (part * p.units + unit) * p.part_rows + r;
         *reinterpret_cast<f32x4*>(p.part_o + at * p.d + e) = acc;
         if (e == 0) {
@@ -511,12 +548,8 @@ __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
           p.lse[h] = sum == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
       }
     }
-    rg.left -= count;
-    if (rg.left <= 0) return;
-    rg.first = 0;
-    do {  // (granules are left, so a sequence with some follows)
-      ++rg.b;
-    } while (granules_of<TILE>(p, max(0, min(p.lens[rg.b], p.max_len))) == 0);
+    if (!more) return;
+    cur = nxt;
     __syncthreads();  // the joined outputs are no longer read
   }
 }

@@ -28,10 +28,10 @@
 // flight.  Page numbers are read a tile further ahead.
 //
 // Measured as a graph, and in a kernel trace, 8 KV heads of 128: one sequence of 131072 positions,
-// bf16, 91 us, 5.9 TB/s (88.6 us and the join's 4.7; the matrix units are busy 6% of the time);
-// 16 sequences of up to 4096, 30 us, 4.5 TB/s (27.3, and 4.4); 64 of up to 8192, E4M3,
-// 70% of the positions kept, 87 us, 4.3 TB/s of the kept rows (81.3, and 5.9; matrix units 15%,
-// dropped rows and conversions between); one sequence of 128: 5.5 us, the launch and the trips to
+// bf16, 92 us, 5.8 TB/s (89.1 us and the join's 4.7; the matrix units are busy 6% of the time);
+// 16 sequences of up to 4096, 30 us, 4.5 TB/s (26.9, and 4.5); 64 of up to 8192, E4M3,
+// 70% of the positions kept, 85 us, 4.4 TB/s of the kept rows (78.7, and 5.8; matrix units 15%,
+// dropped rows and conversions between); one sequence of 128: 5.7 us, the launch and the trips to
 // memory for the page, K and V.  No byte is fetched twice: the counters show the kept rows' bytes
 // and the table's.
 #include <algorithm>

@@ -552,9 +552,9 @@ int wq_moe_layer_workspace_bytes(int tokens, int n_expert, int top_k, int hidden
  *   p = softmax(x router^T); the top_k largest (equal ones: lowest expert first);
  *   w = routed_scale * p (divided by the chosen ones' sum with `renormalize`);
  *   y = residual + sum over the chosen e of w_e * down_e(silu(x gate_e) * (x up_e)).
- * Sums are fp32 (the router's fp64); the activation between the two products is rounded to
- * the element type, y once.  A NaN logit, or a largest one
- * that is infinite, makes its token's weights, and so its row, NaN.
+ * Sums are fp32 (the router's fp64); the activation between the two products keeps fp32's range
+ * and 16 bits for either element type, so that y's one rounding is the one that shows.  A NaN
+ * logit, or a largest one that is infinite, makes its token's weights, and so its row, NaN.
  */
 int wq_moe_layer(const wq_moe_args* args);
 

@@ -604,6 +604,33 @@ def test_moe_an_expert_s_values_reach_only_its_own_tokens(dev, inter, kind):
     assert torch.equal(y[~hit], clean[~hit]) and not bool(y[hit].isfinite().any())
 
 
+@pytest.mark.parametrize("kind", ["u4b8", "u4", "e4m3"])
+@pytest.mark.parametrize("inter", [384, 896])  # few launches, and more
+def test_moe_activations_past_fp16(dev, kind, inter):
+    """Activations beyond 65504 under a small routing scale: the layer's output is finite."""
+    c = moe_case(dev, 5, 6, 2, 512, inter, F16, kind)
+    c["x"] *= 1000 if kind == "e4m3" else 300
+    layer, y = moe_check(c, scale=2.0 ** -8)
+    e = int(layer.ids[0, 0])
+    g, u = (np64(c["x"][0]) @ dequant(b, kind, c["group"])[e] for b in c["raw"][:2])
+    assert (np.maximum(g, 0) * u).max() > 65504 and bool(y.isfinite().all())
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("kind,group", [("u4b8", 128), ("u4", 16), ("e4m3", 128)])
+@pytest.mark.parametrize("tokens,inter", [(3, 256), (16, 256), (3, 1280), (16, 1280)])
+def test_moe_rounds_its_output_only(dev, dtype, kind, group, tokens, inter):
+    """The error of y (2-norm) is that of its one rounding: the activation's 16 bits add a part of
+    2^-16 a term, against y's half step of 2^-11 or more; a tenth is left for fp32 sums and
+    for the number of elements."""
+    c = moe_case(dev, tokens, 6, 2, 512, inter, dtype, kind, group)
+    _, y = moe_check(c)
+    w = [dequant(b, kind, group) for b in c["raw"]]
+    want = ref.moe_layer(np64(c["x"]), np64(c["router"]), *w, 2, True, 1.0, None, 2.0 ** -16)[0]
+    rounded = np64(torch.from_numpy(want).to(dtype))
+    assert np.linalg.norm(np64(y) - want) <= 1.1 * np.linalg.norm(rounded - want)
+
+
 # ---- streams and graphs -----------------------------------------------------------------------
 
 def test_a_decode_step_on_another_stream_and_in_a_graph(dev):

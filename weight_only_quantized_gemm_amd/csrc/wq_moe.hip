@@ -17,14 +17,19 @@
 //     (no atomics), and the residual.
 // Where there are few weights down_all_kernel does 4 and 5 in one launch.
 // Products are 16x16x32 MFMAs on codes dequantized in registers (wq_device.h); each scale
-// unit's partial is scaled in fp32.  The activation is rounded to the element type between the
-// two products, whose matrix units take it so; that is the layer's one rounding beside y's.
+// unit's partial is scaled in fp32.  The activation goes from one product to the next as two
+// bf16 values, high + low, for either element type: fp32's range, and 16 bits of it, so that
+// y's rounding is the only one that shows (rounded to the element type instead, y was off by 1.4
+// times as much, and an fp16 activation past 65504 was infinite).  Codes and E4M3 values are
+// exact in bf16.
 //
 // Measured as a graph, 128-row groups, K x N of an expert 4096 x 2 * 14336 and 14336 x 4096: one
 // token of two experts, fp16, 43 us, 4.2 TB/s (products 23.5 us at 5.2 TB/s and 13.5 at 4.5 in a
 // kernel trace, routing 4.6, combine 3.4); four tokens of five to six experts, bf16 with zero
 // points, 95 us, 5.2 TB/s (56.4 us at 6.0, 33.9 at 5.0).  16 tokens over 56 of 64 experts of
 // 2048 x 2 * 1024, 64-row groups, 47 us, 4.0 TB/s (24.1 us at 5.2, 14.4 at 4.5).
+#include <type_traits>
+
 #include "wq_decode.h"
 #include "wq_device.h"
 
@@ -331,12 +336,20 @@ __device__ __forceinline__ void wave_lds_fence() {
 template <bool BF16, bool W8>
 constexpr bool kBiased = BF16 && !W8;
 
+// 16 rows of a 128-row chunk as the A operands of its four 32-row steps, in PARTS parts that are
+// added: one, or the activation's two.
+template <int PARTS>
+struct Rows {
+  f16x8 v[PARTS][4];
+};
+
 // The sums of a 128-row chunk of activations over each scale unit, as the products lay them.
 template <bool BF16, bool W8, int GPC>
 struct RowSums {
   f32x4 v[kBiased<BF16, W8> ? GPC : 1];
 
-  __device__ __forceinline__ void form(const f16x8* a, int lane) {
+  template <int PARTS>
+  __device__ __forceinline__ void form(const Rows<PARTS>& a, int lane) {
     if constexpr (kBiased<BF16, W8>) {
       using A = Act<true>;
       const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
@@ -347,14 +360,20 @@ struct RowSums {
         for (int u = 0; u < GPC; ++u) {
           v[u] = zero;
 #pragma unroll
-          for (int j = 4 / GPC * u; j < 4 / GPC * (u + 1); ++j) v[u] = A::mfma16(a[j], ones, v[u]);
+          for (int j = 4 / GPC * u; j < 4 / GPC * (u + 1); ++j)
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) v[u] = A::mfma16(a.v[i][j], ones, v[u]);
         }
       } else {
         const bool second = lane >= 32;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          v[2 * j] = A::mfma16(a[j], second ? none : ones, zero);
-          v[2 * j + 1] = A::mfma16(a[j], second ? ones : none, zero);
+          v[2 * j] = v[2 * j + 1] = zero;
+#pragma unroll
+          for (int i = 0; i < PARTS; ++i) {
+            v[2 * j] = A::mfma16(a.v[i][j], second ? none : ones, v[2 * j]);
+            v[2 * j + 1] = A::mfma16(a.v[i][j], second ? ones : none, v[2 * j + 1]);
+          }
         }
       }
     }
@@ -362,10 +381,11 @@ struct RowSums {
 };
 
 // One 128-row chunk of a 16-column block as its wave holds it: codes, scales, zero points.
-template <bool BF16, bool W8, bool ZP, int GPC>
+// BF16: of the scales; OPS: of the products' operands.
+template <bool BF16, bool OPS, bool W8, bool ZP, int GPC>
 struct Chunk {
-  using A = Act<BF16>;
-  using Sums = RowSums<BF16, W8, GPC>;
+  using A = Act<OPS>;
+  using Sums = RowSums<OPS, W8, GPC>;
   u32x4 w[W8 ? 2 : 1];
   uint16_t s[GPC];
   uint32_t z[ZP ? GPC : 1];  // the lane's half of the unit's codes
@@ -384,16 +404,22 @@ struct Chunk {
     }
   }
 
-  // acc += (16 rows of A, four 32-row steps) x chunk
-  __device__ __forceinline__ void multiply(const f16x8* a, const Sums& sums, int lane,
+  // acc += a x chunk
+  template <int PARTS>
+  __device__ __forceinline__ void multiply(const Rows<PARTS>& a, const Sums& sums, int lane,
                                            f32x4& acc) const {
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+    const auto step = [&](int j, typename A::W8 w, f32x4 part) {
+#pragma unroll
+      for (int i = 0; i < PARTS; ++i) part = A::mfma16(a.v[i][j], w, part);
+      return part;
+    };
     const auto code = [&](int u) {
       return ZP ? (int)((z[ZP ? u : 0] >> (4 * (lane & 7))) & 0xFu) : 8;
     };
     const auto add = [&](int u, f32x4 part) {
-      const float f = A::value(s[u]);
-      if constexpr (kBiased<BF16, W8>) {
+      const float f = Act<BF16>::value(s[u]);
+      if constexpr (kBiased<OPS, W8>) {
         const float excess = (float)(128 + code(u));
 #pragma unroll
         for (int e = 0; e < 4; ++e) part[e] = __builtin_fmaf(-excess, sums.v[u][e], part[e]);
@@ -405,12 +431,12 @@ struct Chunk {
       f32x4 p = zero;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        p = A::mfma16(a[j], A::fp8(w[j / 2][2 * (j % 2)], w[j / 2][2 * (j % 2) + 1]), p);
+        p = step(j, A::fp8(w[j / 2][2 * (j % 2)], w[j / 2][2 * (j % 2) + 1]), p);
       add(0, p);
     } else {
       // the weights of step j, as unit u's zero point makes them
       const auto weights = [&](int j, int u) -> typename A::W8 {
-        if constexpr (BF16)
+        if constexpr (OPS)
           return dequant8_bf_biased(w[0][j], magic_reg_bf128());
         else
           return A::dequant(w[0][j], A::zero(code(u)), A::magic());
@@ -420,8 +446,7 @@ struct Chunk {
         for (int u = 0; u < GPC; ++u) {
           f32x4 p = zero;
 #pragma unroll
-          for (int j = 4 / GPC * u; j < 4 / GPC * (u + 1); ++j)
-            p = A::mfma16(a[j], weights(j, u), p);
+          for (int j = 4 / GPC * u; j < 4 / GPC * (u + 1); ++j) p = step(j, weights(j, u), p);
           add(u, p);
         }
       } else {
@@ -432,8 +457,8 @@ struct Chunk {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const typename A::W8 q0 = weights(j, 2 * j), q1 = weights(j, 2 * j + 1);
-          add(2 * j, A::mfma16(a[j], second ? none : q0, zero));
-          add(2 * j + 1, A::mfma16(a[j], second ? q1 : none, zero));
+          add(2 * j, step(j, second ? none : q0, zero));
+          add(2 * j + 1, step(j, second ? q1 : none, zero));
         }
       }
     }
@@ -444,7 +469,7 @@ struct ProductArgs {
   const uint16_t* a;  // x, rows by token; or the activation, rows by pair
   Bank bank;
   const Route* route;
-  uint16_t* h;   // GATE_UP: the activation [pair][inter]
+  uint16_t* h;   // GATE_UP: the activation [pair][high, low][inter]
   float* part;   // else: fp32 rows [pair][hidden]
   long lda;
   int groups, n;  // n: columns of a row of the output
@@ -452,11 +477,12 @@ struct ProductArgs {
 
 // Two neighbouring 16-column blocks of a slot's expert.  Each wave takes a run of 128-row
 // groups, GW at a time, with all of their weights requested at once.  A lane's activations
-// serve both blocks; of up to kStagedRows rows (a load a lane for each group in flight) the wave
-// first brings its run into LDS, in whole rows: 16 rows read as MFMA operands are as many loads
+// serve both blocks; up to kStagedLines lines (a load a lane for each group in flight) the wave
+// first brings into LDS, in whole lines: 16 rows read as MFMA operands are as many loads
 // as the weights of both blocks, and operands held in registers leave none for weights in flight
-// (the three layers above without staging 46.0, 117 and 57.8 us, with it 44.1, 103 and 51.1).
-constexpr int kStagedRows = 4;
+// (the three layers above without staging 46.0, 117 and 57.8 us, with it 44.1, 103 and 51.1;
+// twice the lines of the activation staged: 43.1, 101 and 49.7 us against 42.7, 98.0 and 49.6).
+constexpr int kStagedLines = 4;
 
 // Groups in flight, by the registers of a chunk: codes, scales, zero points.  (Layers of 1 token,
 // two and four groups, us: 5 registers 44.9 and 43.3, 8 48.5 and 47.8, 12 with zero points 55.1 and
@@ -466,11 +492,11 @@ constexpr int kInFlight = (W8 ? 8 : 4) + GPC * (ZP ? 2 : 1) <= 9 ? 4 : 2;
 
 template <bool GATE_UP, bool BF16, bool W8, bool ZP, int GPC, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void product_kernel(ProductArgs p) {
-  using A = Act<BF16>;
-  using C = Chunk<BF16, W8, ZP, GPC>;
+  constexpr int PARTS = GATE_UP ? 1 : 2;  // lines of a row: the activation has two
+  using C = Chunk<BF16, BF16 || !GATE_UP, W8, ZP, GPC>;
   constexpr int GW = kInFlight<W8, ZP, GPC>;
-  constexpr int LR = GW * 16 + 1;  // granules of a staged row, one of padding
-  constexpr int kStage = WAVES * kStagedRows * LR * 16, kRed = 2 * WAVES * 64 * 16;
+  constexpr int LR = GW * 16 + 1;  // granules of a staged line, one of padding
+  constexpr int kStage = WAVES * kStagedLines * LR * 16, kRed = 2 * WAVES * 64 * 16;
   __shared__ __align__(16) uint8_t lds[kStage > kRed ? kStage : kRed];
   const RouteSlot& slot = p.route->slot[blockIdx.y];
   const int expert = slot.expert, rows = slot.rows;
@@ -484,29 +510,35 @@ __global__ __launch_bounds__(WAVES * 64) void product_kernel(ProductArgs p) {
   const uint32_t first_pair = (uint32_t)__builtin_amdgcn_readfirstlane((int)row_pair);
   const uint32_t pair = row < rows ? row_pair : first_pair;
   const auto row_at = [&](uint32_t pr) {
-    return p.a + (long)(GATE_UP ? pr >> 16 : pr & 0xffffu) * p.lda;
+    return p.a + (long)(GATE_UP ? pr >> 16 : pr & 0xffffu) * PARTS * p.lda;
   };
   const u32x4* b = p.bank.b + expert * p.bank.b_stride;
   const uint16_t* s = p.bank.s + expert * p.bank.s_stride;
   const uint32_t* z = ZP ? p.bank.z + expert * p.bank.z_stride : nullptr;
 
+  // Up to eight rows of two lines are the 16 rows of one product, which are added in pairs at the
+  // end; more rows take a product for each line (rows of two products 45.0, 107 and 51.1 us for
+  // the three layers above).
+  const bool paired = PARTS == 2 && rows <= 8;
   const long block0 = 2L * blockIdx.x * p.groups, block1 = block0 + p.groups;
   f32x4 acc0 = {0.f, 0.f, 0.f, 0.f}, acc1 = acc0;
   const int last = p.groups * (wave + 1) / WAVES;
   int g0 = p.groups * wave / WAVES;
-  if (rows <= kStagedRows) {
-    u32x4* const own = reinterpret_cast<u32x4*>(lds) + wave * kStagedRows * LR;
-    const u32x4* ap = own + (row < rows ? row : 0) * LR + qd;
+  const int lines = rows * PARTS;
+  if (lines <= kStagedLines) {
+    u32x4* const own = reinterpret_cast<u32x4*>(lds) + wave * kStagedLines * LR;
+    const u32x4* ap = own + (row < lines ? row : 0) * LR + qd;
     for (; g0 < last; g0 += GW) {
       const int n = min(GW, last - g0);
       u32x4 stage[GW];
 #pragma unroll
-      for (int u = 0; u < GW; ++u) {  // 64 granules of the rows' GW * 16 each
-        if (u * 64 < rows * GW * 16) {
-          const int i = u * 64 + lane, r = i / (GW * 16), c = i % (GW * 16);
-          const uint32_t pr = __shfl(pair, min(r, rows - 1));
-          stage[u] = reinterpret_cast<const u32x4*>(row_at(pr) + (long)g0 * kGroup)[
-              min(c, n * 16 - 1)];
+      for (int u = 0; u < GW; ++u) {  // 64 granules of the lines' GW * 16 each
+        if (u * 64 < lines * GW * 16) {
+          const int i = u * 64 + lane, c = i % (GW * 16);
+          const int line = min(i / (GW * 16), lines - 1);
+          const uint32_t pr = __shfl(pair, line / PARTS);
+          stage[u] = reinterpret_cast<const u32x4*>(row_at(pr) + line % PARTS * p.lda +
+                                                    (long)g0 * kGroup)[min(c, n * 16 - 1)];
         }
       }
       __builtin_amdgcn_sched_barrier(0);  // the rows are requested before any weight
@@ -520,7 +552,7 @@ __global__ __launch_bounds__(WAVES * 64) void product_kernel(ProductArgs p) {
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int u = 0; u < GW; ++u) {
-        if (u * 64 < rows * GW * 16) {
+        if (u * 64 < lines * GW * 16) {
           const int i = u * 64 + lane;
           own[i / (GW * 16) * LR + i % (GW * 16)] = stage[u];
         }
@@ -529,9 +561,9 @@ __global__ __launch_bounds__(WAVES * 64) void product_kernel(ProductArgs p) {
 #pragma unroll
       for (int i = 0; i < GW; ++i) {
         if (i >= n) continue;
-        f16x8 a[4];
+        Rows<1> a;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) a[j] = __builtin_bit_cast(f16x8, ap[16 * i + 4 * j]);
+        for (int j = 0; j < 4; ++j) a.v[0][j] = __builtin_bit_cast(f16x8, ap[16 * i + 4 * j]);
         typename C::Sums sums;
         sums.form(a, lane);
         c0[i].multiply(a, sums, lane, acc0);
@@ -541,33 +573,53 @@ __global__ __launch_bounds__(WAVES * 64) void product_kernel(ProductArgs p) {
     }
   } else {
     constexpr int U = GW >= 2 ? 2 : 1;
-    const uint16_t* ap = row_at(pair) + 8 * qd;
-    for (; g0 < last; g0 += U) {
-      C c0[U], c1[U];
-      f16x8 a[U][4];
+    const auto direct = [&](auto parts, const uint16_t* ap) {
+      constexpr int P = decltype(parts)::value;
+      for (; g0 < last; g0 += U) {
+        C c0[U], c1[U];
+        Rows<P> a[U];
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int g = min(g0 + i, last - 1);
-        c0[i].load(b, s, z, block0 + g, lane);
-        c1[i].load(b, s, z, block1 + g, lane);
+        for (int i = 0; i < U; ++i) {
+          const int g = min(g0 + i, last - 1);
+          c0[i].load(b, s, z, block0 + g, lane);
+          c1[i].load(b, s, z, block1 + g, lane);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          a[i][j] = *reinterpret_cast<const f16x8*>(ap + (long)g * kGroup + 32 * j);
+          for (int k = 0; k < P; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              a[i].v[k][j] =
+                  *reinterpret_cast<const f16x8*>(ap + k * p.lda + (long)g * kGroup + 32 * j);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          if (g0 + i >= last) continue;
+          typename C::Sums sums;
+          sums.form(a[i], lane);
+          c0[i].multiply(a[i], sums, lane, acc0);
+          c1[i].multiply(a[i], sums, lane, acc1);
+        }
       }
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        if (g0 + i >= last) continue;
-        typename C::Sums sums;
-        sums.form(a[i], lane);
-        c0[i].multiply(a[i], sums, lane, acc0);
-        c1[i].multiply(a[i], sums, lane, acc1);
-      }
-    }
+    };
+    if (paired)
+      direct(std::integral_constant<int, 1>(),
+             row_at(__shfl(pair, row / 2)) + row % 2 * p.lda + 8 * qd);
+    else
+      direct(std::integral_constant<int, PARTS>(), row_at(pair) + 8 * qd);
   }
   __syncthreads();  // the staged rows are no longer read
   f32x4(*const red)[WAVES][64] = reinterpret_cast<f32x4(*)[WAVES][64]>(lds);
-  red[0][wave][lane] = acc0;
-  red[1][wave][lane] = acc1;
+  if (paired) {  // lines 2 r and 2 r + 1 lie in neighbouring elements of a lane
+    const int at = qd / 2 * 16 + row, e = 2 * (qd % 2);
+    float* const r0 = reinterpret_cast<float*>(&red[0][wave][at]) + e;
+    float* const r1 = reinterpret_cast<float*>(&red[1][wave][at]) + e;
+    r0[0] = acc0[0] + acc0[1];
+    r0[1] = acc0[2] + acc0[3];
+    r1[0] = acc1[0] + acc1[1];
+    r1[1] = acc1[2] + acc1[3];
+  } else {
+    red[0][wave][lane] = acc0;
+    red[1][wave][lane] = acc1;
+  }
   __syncthreads();
   // the lane's four elements of the two blocks are summed by different waves, in wave order
 #pragma unroll
@@ -582,7 +634,12 @@ __global__ __launch_bounds__(WAVES * 64) void product_kernel(ProductArgs p) {
     const long out = (long)(__shfl(pair, r) & 0xffffu) * p.n;
     if (r < rows) {
       if constexpr (GATE_UP) {
-        p.h[out + 16 * blockIdx.x + row] = A::round(silu_times(s0, s1));
+        const float v = silu_times(s0, s1);
+        const uint16_t high = Act<true>::round(v);
+        const float left = v - Act<true>::value(high);  // exact
+        uint16_t* const h = p.h + 2 * out + 16 * blockIdx.x + row;
+        h[0] = high;
+        h[p.n] = left - left == 0.f ? Act<true>::round(left) : 0;  // none beside inf or NaN
       } else {
         p.part[out + 32 * blockIdx.x + row] = s0;
         p.part[out + 32 * blockIdx.x + 16 + row] = s1;
@@ -592,7 +649,7 @@ __global__ __launch_bounds__(WAVES * 64) void product_kernel(ProductArgs p) {
 }
 
 struct DownArgs {
-  const uint16_t* h;  // the activation [pair][inter]
+  const uint16_t* h;  // the activation [pair][high, low][inter]
   Bank bank;
   const Route* route;
   const uint16_t* residual;
@@ -611,7 +668,7 @@ constexpr int kDownWaves = 16;
 template <bool BF16, bool W8, bool ZP, int GPC>
 __global__ __launch_bounds__(kDownWaves * 64) void down_all_kernel(DownArgs p) {
   using A = Act<BF16>;
-  using C = Chunk<BF16, W8, ZP, GPC>;
+  using C = Chunk<BF16, true, W8, ZP, GPC>;
   __shared__ f32x4 red[kDownWaves][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -628,13 +685,15 @@ __global__ __launch_bounds__(kDownWaves * 64) void down_all_kernel(DownArgs p) {
     c.load(p.bank.b + e * p.bank.b_stride, p.bank.s + e * p.bank.s_stride,
            ZP ? p.bank.z + e * p.bank.z_stride : nullptr, block + g, lane);
     const int pair = slot.token_pair[row];
-    const uint16_t* ap = p.h + (long)max(pair, 0) * p.inter + (long)g * kGroup + 8 * qd;
-    f16x8 a[4];
+    const uint16_t* ap = p.h + 2L * max(pair, 0) * p.inter + (long)g * kGroup + 8 * qd;
+    Rows<2> a;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      a[j] = *reinterpret_cast<const f16x8*>(ap + 32 * j);
-      if (pair < 0) a[j] = f16x8{};
-    }
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        a.v[k][j] = *reinterpret_cast<const f16x8*>(ap + k * p.inter + 32 * j);
+        if (pair < 0) a.v[k][j] = f16x8{};
+      }
     int member[4];
     float w[4];
 #pragma unroll
@@ -723,7 +782,7 @@ struct MoeScratch {
 MoeScratch scratch_of(void* base, int tokens, int n_expert, int top_k, int hidden, int inter) {
   const size_t logits = round256((size_t)tokens * n_expert * sizeof(float));
   const size_t route = round256(sizeof(Route));
-  const size_t h = round256((size_t)tokens * top_k * inter * 2);
+  const size_t h = round256((size_t)tokens * top_k * inter * 4);
   char* p = static_cast<char*>(base);
   return MoeScratch{reinterpret_cast<float*>(p), reinterpret_cast<Route*>(p + logits),
                     reinterpret_cast<uint16_t*>(p + logits + route),

@@ -3,6 +3,8 @@ own checks, and pins of the 64-bit forms the GPU tests compare with."""
 
 import ctypes
 import math
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -138,6 +140,49 @@ def test_attention_workspace():
     for bad in ((0, 8, 2, 64, 1), (1, 7, 2, 64, 1), (1, 8, 0, 64, 1), (1, 8, 2, 20, 1)):
         with pytest.raises(wq.WQError):
             f(*bad)
+
+
+def test_attention_ranges_of_a_rounded_up_grid(tmp_path):
+    """Every (row, unit) is one work-group's, those of the rounded-up grid past the last row have
+    none, and a range's first granule is right (against 64 bits) up to 2^30 granules."""
+    csrc = os.path.join(os.path.dirname(wq.__file__), "csrc")
+    source, program = tmp_path / "ranges.cc", tmp_path / "ranges"
+    source.write_text(r"""
+        #include <cstdio>
+        #include <vector>
+        #include "wq_ranges.h"
+        int main() {
+          for (int near = 0; near < 2; ++near)
+            for (int rows : {1, 2, 7, 8, 9, 64, 100})
+              for (int units : {1, 3, 513}) {
+                std::vector<int> hits(rows * units);
+                const int grid = (near ? (rows + 7) / 8 * 8 : rows) * units;
+                for (int block = 0, row, unit; block < grid; ++block) {
+                  const bool in = wq::place_of_block(block, units, near, rows, row, unit);
+                  if (in != (row < rows) || row < 0 || unit < 0 || unit >= units)
+                    return std::printf("block %d of %d x %d: %d %d", block, rows, units, row, unit);
+                  if (in) ++hits[row * units + unit];
+                }
+                for (int n : hits)
+                  if (n != 1) return std::printf("%d x %d: %d hits", rows, units, n);
+              }
+          for (long long total : {0ll, 1ll, 129ll, 306783379ll, (1ll << 29) + 1, 1ll << 30})
+            for (int ranges : {1, 2, 3, 42, 256, 768}) {
+              long long length = (total + ranges - 1) / ranges, left = total;
+              if (length < 1) length = 1;
+              for (int row = 0; row < ranges; ++row) {
+                const long long first = row * length, got = wq::range_first(row, total, ranges);
+                if (got != (first < total ? first : -1))
+                  return std::printf("range %d of %d, %lld: %lld", row, ranges, total, got);
+                if (got >= 0) left -= total - first < length ? total - first : length;
+              }
+              if (left) return std::printf("%d ranges of %lld leave %lld", ranges, total, left);
+            }
+        }""")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-I", csrc, str(source), "-o", str(program)],
+                   check=True)
+    done = subprocess.run([str(program)], capture_output=True, text=True, timeout=60)
+    assert done.returncode == 0, done.stdout
 
 
 def bank_args(k, n):

@@ -39,6 +39,7 @@
 
 #include "wq_decode.h"
 #include "wq_device.h"
+#include "wq_ranges.h"
 
 namespace wq {
 namespace {
@@ -133,8 +134,8 @@ struct Range {
   int b, first, left;
 };
 
-// The index-th range; false past the last.  All sequences' granules, one sequence after the
-// other, are cut into `ranges` equal ranges.  The lengths are known only here, so every wave
+// The index-th range; false where it is empty.  All sequences' granules, one sequence after the
+// other, are cut into `ranges` ranges of one length, the last ones shorter or empty.  The lengths are known only here, so every wave
 // counts them, each lane a run of sequences.  (64 sequences of up to 8192 positions, E4M3: cut
 // by the host by the longest length 135 us, in equal splits of each sequence 93.7, as here
 // 88.8; unmasked 121.7 in equal splits, 112.5 here.)
@@ -150,7 +151,7 @@ __device__ __forceinline__ bool find_range(const AttnArgs& p, int index, bool pu
   for (int b = b0; b < b1; ++b) mine += granules(b);
   const int end = wave_scan(mine);
   const int total = __builtin_amdgcn_readlane(end, 63);
-  const int chunk = max(1, (total + p.ranges - 1) / p.ranges);
+  const int chunk = range_length(total, p.ranges);
   if (publish) {  // where the join finds each sequence's parts
     int at = end - mine;
     for (int b = b0; b < b1; ++b) {
@@ -160,8 +161,8 @@ __device__ __forceinline__ bool find_range(const AttnArgs& p, int index, bool pu
       at += n;
     }
   }
-  const int g0 = index * chunk;
-  if (g0 >= total) return false;
+  const int g0 = range_first(index, total, p.ranges);
+  if (g0 < 0) return false;
   const int owner = __builtin_ctzll(__ballot(g0 < end));
   int at = __builtin_amdgcn_readlane(end - mine, owner);
   int b = owner * run;
@@ -224,13 +225,10 @@ __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row = lane & 15, qd = lane >> 4;
-  int index = blockIdx.x / p.units, unit = blockIdx.x - index * p.units;
-  if (p.near_units) {  // eight ranges side by side, so that all units of one have the same L2
-    const int eight = blockIdx.x / (8 * p.units);
-    index = 8 * eight + blockIdx.x % 8;
-    unit = blockIdx.x / 8 - eight * p.units;
-    if (p.ranges == 0 && index >= p.batch) return;
-  }
+  int index, unit;
+  if (!place_of_block(blockIdx.x, p.units, p.near_units != 0, p.ranges > 0 ? p.ranges : p.batch,
+                      index, unit))
+    return;
   Range rg{index, 0, 0};
   if (p.ranges > 0 && !find_range<TILE>(p, index, blockIdx.x == 0 && wave == 0, lane, rg)) return;
   const int kvh = unit / p.head_blocks, hb = unit - kvh * p.head_blocks;

@@ -58,7 +58,8 @@ def paged_attention(q, k_cache, v_cache, table, lens, scale, window=0, softcap=0
             s_err = s_err + np.abs(s) * 8 * E32
             if softcap:
                 s = softcap * np.tanh(s / softcap)
-                s_err = s_err + softcap * 8 * E32
+                # tanh is right to its own size, and its last product to the cap's
+                s_err = s_err + np.minimum(np.abs(s) * 12, softcap * 8) * E32
             s_err = s_err.max() + np.abs(s).max() * 8 * E32  # to base 2 and back
             p = np.exp(s - s.max())
             total = p.sum()

@@ -386,6 +386,23 @@ def test_attention_lens_are_taken_into_range(dev):
     assert lse[1].tolist() == [-math.inf] * 2
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("kind", ["same", "e4m3"])
+@pytest.mark.parametrize("cap", [0.3, 30.0, 1e3, 1e4, 1e6, 1e30])
+def test_attention_caps(dev, dtype, kind, cap):
+    """From caps that flatten every score to caps that leave them as they are."""
+    c = attn_case(dev, [700, 33, 1], 4, 2, 64, 16, dtype, kind, softcap=cap)
+    c["q"] *= 4
+    for cut in (False, True):
+        out, lse = attn_run(c, cut)
+        attn_check(c, out, lse, f"cut {cut}")
+        if cap > 1e7:  # s / c is past the last bit: the same scores
+            plain, plain_lse = attn_run(dict(c, softcap=0.0), cut)
+            assert torch.allclose(lse, plain_lse, rtol=2.0 ** -20, atol=2.0 ** -20)
+            # three roundings of a score of 20 at most, twice, of V up to 5; and an output step
+            assert torch.allclose(out, plain, rtol=2 * torch.finfo(dtype).eps, atol=2.0 ** -12)
+
+
 def test_attention_extreme_scores(dev):
     """Equal huge scores, one dominating score, and scores that fp16 p could not hold."""
     c = attn_case(dev, [400], 2, 1, 64, 16, F16, poison=False)

@@ -91,9 +91,19 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// 1 - 2 / (e^2x + 1): off by some 2^-23, which is all that a capped score needs.
-__device__ __forceinline__ float fast_tanh(float x) {
-  return 1.f - 2.f * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(2.f * kLog2e * x) + 1.f);
+// c tanh(s / c) for x = s / c, within 10 2^-24 of its own value.  1 - 2 / (e^2x + 1) is off by
+// some 2^-23 for any x, which is too much beside a small tanh (with a large c it is the score
+// itself that is left); below 1/2 tanh(x) / x is a polynomial in x^2, fitted to 2^-26, times s.
+// (64 E4M3 sequences of up to 8192, capped: 88.0 us by the exponential alone, 91.6 so; 89.6 to 96.4
+// with a branch that spares tiles of small scores the exponential.)
+__device__ __forceinline__ float capped(float s, float x, float c) {
+  const float z = x * x;
+  float t = __builtin_fmaf(z, 0.017256992f, -0.053052951f);
+  t = __builtin_fmaf(z, t, 0.13325988f);
+  t = __builtin_fmaf(z, t, -0.33333150f);
+  t = __builtin_fmaf(z, t, 1.f);
+  const float e = __builtin_amdgcn_exp2f(2.f * kLog2e * x);
+  return fabsf(x) < 0.5f ? s * t : c * (1.f - 2.f * __builtin_amdgcn_rcpf(e + 1.f));
 }
 
 template <bool BF16>
@@ -410,7 +420,8 @@ __global__ __launch_bounds__(kWaves * 64) void attn_kernel(AttnArgs p) {
 #pragma unroll
         for (int blk = 0; blk < NT; ++blk)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[blk][e] = p.softcap * fast_tanh(s[blk][e] * cap);
+          for (int e = 0; e < 4; ++e)
+            s[blk][e] = capped(s[blk][e] * sc, s[blk][e] * cap, p.softcap);
       }
 #pragma unroll
       for (int blk = 0; blk < NT; ++blk)

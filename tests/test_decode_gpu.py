@@ -590,6 +590,40 @@ def test_moe_ties_take_the_lowest_expert(dev, experts):
         assert layer.ids[t].tolist() == (equal + [0, 1] if up else [0, 1, 2, 4, 5])
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("tokens,experts,hidden", [(1, 8, 512), (1, 16, 2048), (1, 17, 512),
+                                                   (4, 8, 512), (16, 8, 512), (16, 40, 512),
+                                                   (3, 70, 512)])
+@pytest.mark.parametrize("top_k", [1, 3])
+def test_moe_logits_closer_than_an_fp32_step(dev, dtype, tokens, experts, hidden, top_k):
+    """Two experts lead by far and differ by 2^-26 of logits near 16, the higher one ahead: the
+    router's products, sums and order keep fp64 on every route (one token, a few, many; counted
+    or in rounds)."""
+    c = moe_case(dev, tokens, experts, top_k, hidden, 128, dtype)
+    low, high = 1, experts - 2
+    x, r = c["x"], c["router"]
+    x[:, 0], x[:, 7], x[:, 8], x[:, 300] = 1, 2.0 ** -13, 64, 64
+    r[high] = r[low]
+    r[:, [8, 300]] = 0
+    r[[low, high], 0], r[low, 7], r[high, 7] = 16, 0, 2.0 ** -13
+    want = [high, low][:top_k]
+    for cancelling in (0, 64):  # the lower one's products 4096 and -4096
+        r[low, 8], r[low, 300] = cancelling, -cancelling
+        layer, _ = moe_check(c)
+        assert all(layer.ids[t].tolist()[:2] == want for t in range(tokens))
+
+
+def test_moe_logits_past_fp32(dev):
+    """bf16 products and logits beyond fp32's range are ordered, and their weights those of fp64."""
+    c = moe_case(dev, 3, 8, 2, 512, 128, BF16)
+    c["x"][:, 4] = 2.0 ** 60
+    c["router"][:, 4] = 0
+    c["router"][5, 4], c["router"][2, 4] = 2.0 ** 80, 2.0 ** 79
+    layer = decode.MoELayer(*c["banks"], c["router"], 2)
+    layer(c["x"])
+    assert layer.ids[:3].tolist() == [[5, 2]] * 3 and layer.weights[:3].tolist() == [[1, 0]] * 3
+
+
 def test_moe_strides_aliases_and_nan_rows(dev):
     c = moe_case(dev, 6, 8, 2, 512, 256, BF16)
     _, want = moe_check(c, residual=c["x"])

@@ -7,7 +7,8 @@
 //  1. router_kernel: the logits x router^T.
 //  2. route_kernel, one work-group: the tokens' top-k, and for each expert that any token
 //     chose (a "slot") its rows.  (Taken in every work-group of the next kernel instead, the
-//     routing cost 4 to 30 us more than this launch.)  It forms a small router's logits too.
+//     routing cost 4 to 30 us more than this launch.)  It forms one token's logits of a
+//     small router too.
 //  3. product_kernel on the gate/up bank: a work-group per slot and pair of 16-column blocks,
 //     a gate and an up block, ends in the activation silu(g) * u.  The grid has room for the
 //     most slots there can be; work-groups past the last one end at once.
@@ -69,14 +70,19 @@ constexpr int kRouterThreads = 256;
 
 // Products of one expert's router row with T = 1 or 4 tokens (past the last: the last one), over
 // k0, k0 + step, ... of the hidden size, 8 elements each; lanes 64 / T * j, ... of the wave return
-// token t0 + j's sum over the wave.  Eight products at a time are summed in fp32, the sums in
-// fp64 and rounded once: the order of nearly equal logits decides which experts run.
+// token t0 + j's sum over the wave.  Sums and logits are fp64 up to the choice: the order of nearly
+// equal logits decides which experts run.  Products are exact, of fp16 values in fp32 (one
+// conversion less), of bf16 ones in fp64, whose range they need.
 template <bool BF16, int T, int UNROLL>
 __device__ __forceinline__ double wave_logits(const uint16_t* x, int ldx, const uint16_t* rp,
                                               int tokens, int t0, int k0, int step, int end,
                                               int lane) {
   using A = Act<BF16>;
-  double acc[T] = {};
+  const auto value = [](u32x4 w, int i) {
+    return A::value((uint16_t)(w[i / 2] >> (16 * (i % 2))));
+  };
+  constexpr int N = 4 / T;  // sums of a token, so that four are on their way
+  double sums[T][N] = {};
 #pragma unroll UNROLL
   for (int k = k0; k < end; k += step) {
     const u32x4 r = *reinterpret_cast<const u32x4*>(rp + k);
@@ -85,14 +91,19 @@ __device__ __forceinline__ double wave_logits(const uint16_t* x, int ldx, const 
     for (int j = 0; j < T; ++j)
       xv[j] = *reinterpret_cast<const u32x4*>(x + (long)min(t0 + j, tokens - 1) * ldx + k);
 #pragma unroll
-    for (int j = 0; j < T; ++j) {
-      float sum = 0.f;
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        sum = __builtin_fmaf(A::value((uint16_t)(r[i / 2] >> (16 * (i % 2)))),
-                             A::value((uint16_t)(xv[j][i / 2] >> (16 * (i % 2)))), sum);
-      acc[j] += (double)sum;
-    }
+      for (int j = 0; j < T; ++j)
+        sums[j][i % N] = BF16 ? __builtin_fma((double)value(r, i), (double)value(xv[j], i),
+                                              sums[j][i % N])
+                              : sums[j][i % N] + (double)(value(r, i) * value(xv[j], i));
+  }
+  double acc[T];
+#pragma unroll
+  for (int j = 0; j < T; ++j) {
+    acc[j] = sums[j][0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) acc[j] += sums[j][i];
   }
   double v = acc[0];
   if constexpr (T == 4) {
@@ -113,7 +124,7 @@ __device__ __forceinline__ double wave_logits(const uint16_t* x, int ldx, const 
 template <bool BF16>
 __global__ __launch_bounds__(kRouterThreads) void router_kernel(
     const uint16_t* __restrict__ x, int ldx, const uint16_t* __restrict__ router, int tokens,
-    int n_expert, int hidden, float* __restrict__ logits) {
+    int n_expert, int hidden, double* __restrict__ logits) {
   __shared__ double red[kRouterThreads / 64][4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int e = blockIdx.x;
@@ -126,7 +137,7 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(
     double sum = red[0][tid];
 #pragma unroll
     for (int w = 1; w < kRouterThreads / 64; ++w) sum += red[w][tid];
-    logits[(t0 + tid) * n_expert + e] = (float)sum;
+    logits[(t0 + tid) * n_expert + e] = sum;
   }
 }
 
@@ -147,27 +158,35 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
   return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
 }
 
+__device__ __forceinline__ uint64_t read_lane(uint64_t x, int lane) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), lane) << 32 |
+         (uint32_t)__builtin_amdgcn_readlane((int)x, lane);
+}
+
 // One token's top-k by its wave: lane j ends with the j-th best expert and its weight.  Equal
 // logits go to the lower expert, NaN below everything; PER experts a lane.
 template <int PER>
-__device__ __forceinline__ void token_top_k(const float* logits, int n_expert, int top_k,
+__device__ __forceinline__ void token_top_k(const double* logits, int n_expert, int top_k,
                                             bool renormalize, float routed_scale, int lane,
                                             int& my_id, float& my_w) {
-  float l[PER];
-  uint32_t key[PER];  // ordered as the logits are; 0 is below every expert's
+  double l[PER];
+  uint64_t key[PER];  // ordered as the logits are; 0 is below every expert's
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = lane + 64 * i;
     l[i] = e < n_expert ? logits[e] : -INFINITY;
     bad |= l[i] != l[i] || l[i] == INFINITY;
-    const uint32_t bits = __builtin_bit_cast(uint32_t, l[i] + 0.f);  // -0 and 0 are equal
-    key[i] = (bits >> 31) ? ~bits : bits | 0x80000000u;
-    if (l[i] != l[i]) key[i] = 1u;
-    if (e >= n_expert) key[i] = 0u;
+    const uint64_t bits = __builtin_bit_cast(uint64_t, l[i] + 0.);  // -0 and 0 are equal
+    key[i] = (bits >> 63) ? ~bits : bits | 1ull << 63;
+    if (l[i] != l[i]) key[i] = 1;
+    if (e >= n_expert) key[i] = 0;
   }
   const bool nan_row = __ballot(bad) != 0;
-  uint32_t my_key = 0, top_key = 0;
+  // The upper halves of the keys decide, unless two are equal.
+  const auto upper = [&](int i) { return (uint32_t)(key[i] >> 32); };
+  uint64_t my_key = 0;
+  bool done = false;
   if (PER == 1 && n_expert < 4 * top_k) {
     // An expert's place is the number of experts before it: larger keys, and equal ones of
     // lower number.  No round waits for the one before, but there are as many steps as experts,
@@ -175,53 +194,73 @@ __device__ __forceinline__ void token_top_k(const float* logits, int n_expert, i
     // rounds: 8 of 8 experts 13.4, 14.5; 4 of 16 14.2, 14.2; 8 of 64 19.0, 18.2; 1 of 64 15.6,
     // 13.4).
     int place = 0;
-    const uint64_t full = (uint64_t)key[0] << 32 | (uint32_t)(63 - lane);
+    const uint64_t full = (uint64_t)upper(0) << 32 | (uint32_t)(63 - lane);
     for (int e0 = 0; e0 < n_expert; e0 += 8) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int e = e0 + k;  // past n_expert the keys are 0
-        const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)key[0], e);
+        const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)upper(0), e);
         place += ((uint64_t)other << 32 | (uint32_t)(63 - e)) > full;
       }
     }
-    // lane j fetches the key and number of the expert in place j
-    const bool in = lane < n_expert && place < top_k;
-    const int dest = in ? place : 63;
-    my_key = (uint32_t)__builtin_amdgcn_ds_permute(4 * dest, (int)(in ? key[0] : 0u));
-    my_id = __builtin_amdgcn_ds_permute(4 * dest, in ? lane : 0);
-    top_key = (uint32_t)__builtin_amdgcn_readlane((int)my_key, 0);
-  } else {
+    // lane j fetches the key and number of the expert in place j (lanes past the last expert
+    // have the places past its, in their order)
+    const uint32_t high = __builtin_amdgcn_ds_permute(4 * place, (int)upper(0));
+    const uint32_t low = __builtin_amdgcn_ds_permute(4 * place, (int)key[0]);
+    my_id = __builtin_amdgcn_ds_permute(4 * place, lane);
+    my_key = (uint64_t)high << 32 | low;
+    const uint32_t before = __shfl_up(high, 1);
+    done = __ballot(lane > 0 && lane <= top_k && high == before) == 0;
+  }
+  if (!done) {
     for (int j = 0; j < top_k; ++j) {
-      uint32_t best = key[0];
+      uint32_t best = upper(0);
 #pragma unroll
-      for (int i = 1; i < PER; ++i) best = max(best, key[i]);
+      for (int i = 1; i < PER; ++i) best = max(best, upper(i));
       best = wave_max(best);
-      int id = -1;  // lowest expert with this key
+      unsigned long long has[PER];
+      int equal = 0;
 #pragma unroll
-      for (int i = PER - 1; i >= 0; --i) {
-        const unsigned long long has = __ballot(key[i] == best);
-        if (has) id = 64 * i + __builtin_ctzll(has);
+      for (int i = 0; i < PER; ++i) {
+        has[i] = __ballot(upper(i) == best);
+        equal += __popcll(has[i]);
+      }
+      if (equal > 1) {
+        uint32_t low = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) low = max(low, upper(i) == best ? (uint32_t)key[i] : 0u);
+        low = wave_max(low);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) has[i] = __ballot(upper(i) == best && (uint32_t)key[i] == low);
+      }
+      int id = 0;  // lowest expert with this key
+#pragma unroll
+      for (int i = PER - 1; i >= 0; --i)
+        if (has[i]) id = 64 * i + __builtin_ctzll(has[i]);
+      uint64_t chosen = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (id / 64 == i) chosen = read_lane(key[i], id % 64);
+      if (lane == j) {
+        my_key = chosen;
+        my_id = id;
       }
 #pragma unroll
       for (int i = 0; i < PER; ++i)
-        if (id == lane + 64 * i) key[i] = 0u;
-      if (j == 0) top_key = best;
-      if (lane == j) {
-        my_key = best;
-        my_id = id;
-      }
+        if (id == lane + 64 * i) key[i] = 0;
     }
   }
-  const auto value = [](uint32_t k) {
-    return __builtin_bit_cast(float, (k >> 31) ? k & 0x7fffffffu : ~k);
+  const auto value = [](uint64_t k) {
+    return __builtin_bit_cast(double, (k >> 63) ? k & ~(1ull << 63) : ~k);
   };
-  const float top = value(top_key);
-  const float mine = lane < top_k ? expf(value(my_key) - top) : 0.f;
+  // (differences are taken in fp64, so that large logits keep small ones)
+  const double top = value(read_lane(my_key, 0));
+  const float mine = lane < top_k ? expf((float)(value(my_key) - top)) : 0.f;
   float sum = mine;
   if (!renormalize) {
     sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) sum += expf(l[i] - top);
+    for (int i = 0; i < PER; ++i) sum += expf((float)(l[i] - top));
   }
 #pragma unroll
   for (int d = 32; d >= 1; d /= 2) sum += __shfl_xor(sum, d);
@@ -230,7 +269,7 @@ __device__ __forceinline__ void token_top_k(const float* logits, int n_expert, i
 }
 
 struct RouteArgs {
-  const float* logits;
+  const double* logits;
   Route* route;
   int32_t* ids;
   float* weights;
@@ -244,33 +283,30 @@ struct RouteArgs {
 
 // One work-group, a wave per token; 2.4 us for one token of 8 experts (4.6 with the logits of
 // 4096 elements), 4.1 for 16 of 64: a chain of trips to memory and LDS.  PER: 64 experts for each
-// lane of a wave, 1 or 4.  ROUTER: 16 waves form the logits here too, first (1: fp16, 2: bf16): an
-// expert and T tokens for each, or with fewer of these a part of the hidden size.
-template <int PER, int ROUTER, int T>
+// lane of a wave, 1 or 4.  ROUTER: 16 waves form one token's logits here too, first (1: fp16, 2:
+// bf16): an expert for each, or with fewer of these a part of the hidden size.
+template <int PER, int ROUTER>
 __global__ __launch_bounds__(kMaxT * 64) void route_kernel(RouteArgs p) {
   __shared__ uint32_t mask_lds[kMaxE];
   __shared__ uint8_t slot_of[kMaxE];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   for (int i = tid; i < kMaxE; i += blockDim.x) mask_lds[i] = 0;
-  const float* logits = p.logits;
+  const double* logits = p.logits;
   if constexpr (ROUTER != 0) {
-    __shared__ double part_lds[kMaxT][T];
-    __shared__ float logit_lds[kMaxT * T];
-    const int parts = (p.tokens + T - 1) / T, items = p.n_expert * parts, segs = kMaxT / items;
-    if (wave < items * segs) {
-      const int item = wave / segs, e = item / parts, t0 = T * (item - e * parts);
-      const int k0 = (wave - item * segs) * 512 + lane * 8;
-      const double v = wave_logits<ROUTER == 2, T, 4>(p.x, p.ldx, p.router + (long)e * p.hidden,
-                                                      p.tokens, t0, k0, segs * 512, p.hidden, lane);
-      if (lane % (64 / T) == 0) part_lds[wave][lane / (64 / T)] = v;
+    __shared__ double part_lds[kMaxT], logit_lds[kMaxT];
+    const int segs = kMaxT / p.n_expert;
+    if (wave < p.n_expert * segs) {
+      const int e = wave / segs, k0 = (wave - e * segs) * 512 + lane * 8;
+      const double v = wave_logits<ROUTER == 2, 1, 4>(p.x, p.ldx, p.router + (long)e * p.hidden, 1,
+                                                      0, k0, segs * 512, p.hidden, lane);
+      if (lane == 0) part_lds[wave] = v;
     }
     __syncthreads();
-    if (tid < T * items) {
-      const int item = tid / T, e = item / parts, t = T * (item - e * parts) + tid % T;
+    if (tid < p.n_expert) {
       double sum = 0.;
-      for (int k = 0; k < segs; ++k) sum += part_lds[item * segs + k][tid % T];
-      if (t < p.tokens) logit_lds[t * p.n_expert + e] = (float)sum;
+      for (int k = 0; k < segs; ++k) sum += part_lds[tid * segs + k];
+      logit_lds[tid] = sum;
     }
     logits = logit_lds;
   }
@@ -772,7 +808,7 @@ Bank bank_of(const wq_expert_bank& b) {
 }
 
 struct MoeScratch {
-  float* logits;
+  double* logits;
   Route* route;
   uint16_t* h;
   float* part;
@@ -780,11 +816,11 @@ struct MoeScratch {
 };
 
 MoeScratch scratch_of(void* base, int tokens, int n_expert, int top_k, int hidden, int inter) {
-  const size_t logits = round256((size_t)tokens * n_expert * sizeof(float));
+  const size_t logits = round256((size_t)tokens * n_expert * sizeof(double));
   const size_t route = round256(sizeof(Route));
   const size_t h = round256((size_t)tokens * top_k * inter * 4);
   char* p = static_cast<char*>(base);
-  return MoeScratch{reinterpret_cast<float*>(p), reinterpret_cast<Route*>(p + logits),
+  return MoeScratch{reinterpret_cast<double*>(p), reinterpret_cast<Route*>(p + logits),
                     reinterpret_cast<uint16_t*>(p + logits + route),
                     reinterpret_cast<float*>(p + logits + route + h),
                     logits + route + h + (size_t)tokens * top_k * hidden * sizeof(float)};
@@ -886,17 +922,13 @@ hipError_t launch_route(const wq_moe_args& a, const MoeScratch& m, bool by_token
   p.router = static_cast<const uint16_t*>(a.router);
   p.ldx = a.ldx;
   p.hidden = a.hidden;
-  // The routing's one work-group forms the logits of a small router as well, one item of work a
-  // wave: a launch less (us for the layer: 4096 products of a router element and four tokens
-  // 14.9 -> 13.3, 8192 15.8 -> 15.0; 10240 14.4 -> 14.6, 65536 16.6 -> 20.0; of one token 8192
-  // 11.7 -> 10.9, 32768 43.0 -> 42.2, 65536 14.6 -> 14.3 or 15.1, 131072 18.3 -> 19.7).
-  const int items = a.n_expert * ((a.tokens + 3) / 4);
-  if (items <= kMaxT && items * a.hidden <= (a.tokens == 1 ? 32768 : 8192)) {
-    constexpr int R = BF16 ? 2 : 1;
-    if (a.tokens == 1)
-      hipLaunchKernelGGL((route_kernel<1, R, 1>), dim3(1), dim3(kMaxT * 64), 0, stream, p);
-    else
-      hipLaunchKernelGGL((route_kernel<1, R, 4>), dim3(1), dim3(kMaxT * 64), 0, stream, p);
+  // The routing's one work-group forms one token's logits of a small router as well, a launch less
+  // (us for the layer, two launches and one, by the router's elements: 8192 11.55, 10.75; 16384
+  // 12.1, 11.5; 32768 14.5, 14.1; more, with sums of eight products in fp32, 65536 14.6, 14.3 or
+  // 15.1; 131072 18.3, 19.7).  Of several tokens fp64 sums keep one CU for as long as the launch
+  // takes (4096 elements and four tokens 11.8, 12.0; 8192 12.2, 12.2).
+  if (a.tokens == 1 && a.n_expert <= kMaxT && a.n_expert * a.hidden <= 32768) {
+    hipLaunchKernelGGL((route_kernel<1, BF16 ? 2 : 1>), dim3(1), dim3(kMaxT * 64), 0, stream, p);
     return hipGetLastError();
   }
   hipLaunchKernelGGL((router_kernel<BF16>), dim3(a.n_expert, (a.tokens + 3) / 4),
@@ -906,9 +938,9 @@ hipError_t launch_route(const wq_moe_args& a, const MoeScratch& m, bool by_token
   if (e != hipSuccess) return e;
   const dim3 block(64 * a.tokens);
   if (a.n_expert <= 64)
-    hipLaunchKernelGGL((route_kernel<1, 0, 1>), dim3(1), block, 0, stream, p);
+    hipLaunchKernelGGL((route_kernel<1, 0>), dim3(1), block, 0, stream, p);
   else
-    hipLaunchKernelGGL((route_kernel<kMaxE / 64, 0, 1>), dim3(1), block, 0, stream, p);
+    hipLaunchKernelGGL((route_kernel<kMaxE / 64, 0>), dim3(1), block, 0, stream, p);
   return hipGetLastError();
 }
 

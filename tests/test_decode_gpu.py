@@ -98,6 +98,20 @@ def test_add_rms_norm_extremes(dev):
     assert bool(y[3].isfinite().all())
 
 
+@pytest.mark.parametrize("delta", [False, True])
+def test_add_rms_norm_of_squares_past_fp32_and_below_it(dev, delta):
+    """Squares past fp32 give 0; squares below it leave eps alone under the root."""
+    x = torch.full((2, 520), 3e38, dtype=BF16, device=dev)
+    x[1] = 1e-30
+    x[:, 1::2] *= -1
+    d = torch.zeros_like(x) if delta else None
+    w = torch.linspace(0.5, 2, 520, device=dev).to(BF16)
+    y, s = decode.add_rms_norm(x, w, 1e-6, delta=d)
+    assert bool((y[0] == 0).all()) and torch.equal(s, x)
+    want = np64(x[1]) * np64(w) / math.sqrt(float(np.float32(1e-6)))
+    assert (np.abs(np64(y[1]) - want) <= np.abs(want) * (half_step(BF16) + 8 * ref.E32)).all()
+
+
 # ---- rotary positions and the cache write -----------------------------------------------------
 
 def paged(dev, pages, page, heads, d, dtype, order, scales=None, g=None):
@@ -182,6 +196,24 @@ def test_rope_append_in_place_and_special_values(dev):
     assert got is q and torch.equal(got, want)
     head = cache.v[0, 0, 0, :4].float()
     assert bool(head[0].isnan()) and head[1:].tolist() == [448.0, -448.0, 448.0]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("rot", [64, 40])
+def test_rope_append_interleaved_in_place(dev, dtype, rot):
+    g = rng_of(dev, 4)
+    wide = normal(g, (37, 9 * 64), dtype)
+    q = wide[:, 64:320].unflatten(1, (4, 64))
+    k = normal(g, (37, 1, 64), dtype)
+    cache = paged(dev, 5, 8, 1, 64, dtype, "nhd")
+    args = k, k, cache, torch.arange(37, device=dev)
+    kw = dict(positions=torch.arange(37, device=dev, dtype=torch.int32) * 999, interleaved=True,
+              inv_freq=torch.rand(rot // 2, generator=g, device=dev))
+    rest = wide[:, 320:].clone()
+    want = decode.rope_append(q, *args, **kw)
+    assert not torch.equal(want, q)
+    got = decode.rope_append(q, *args, q_out=q, **kw)
+    assert torch.equal(got, want) and torch.equal(wide[:, 320:], rest)
 
 
 # ---- attention ------------------------------------------------------------------------------
@@ -326,6 +358,30 @@ def test_attention_live_infinities_and_nan(dev):
         assert bool(out[0, :, 7].isinf().all()) and int(out[0].isinf().sum()) == 2
         assert bool(out[1].isnan().all()) and bool(lse[1].isnan().all())
         assert bool(out[2].isfinite().all()) and bool(lse[0].isfinite().all())
+
+
+@pytest.mark.parametrize("kind,dtype", [("same", F16), ("e4m3", F16), ("e4m3", BF16)])
+def test_attention_live_infinities_and_nan_of_other_types(dev, kind, dtype):
+    """fp16's parts of p are cut at another place than bf16's; an E4M3 cache holds NaN only."""
+    c = attn_case(dev, [300, 300, 300, 300], 2, 1, 64, 16, dtype, kind)
+    k, v = c["cache"].k, c["cache"].v
+    page = [c["table"][i, 5].long() for i in range(4)]
+    if kind == "same":
+        v[page[0], 3, 0, 7], v[page[1], 3, 0, 9] = float("inf"), float("-inf")
+        k[page[2], 3, 0, 0] = float("nan")
+    else:
+        v.view(torch.uint8)[page[0], 3, 0, 7] = v.view(torch.uint8)[page[1], 3, 0, 9] = 0x7F
+        k.view(torch.uint8)[page[2], 3, 0, 0] = 0xFF
+    for cut in (False, True):
+        out, lse = attn_run(c, cut)
+        hit = [out[0, :, 7], out[1, :, 9]]
+        if kind == "same":
+            assert bool((hit[0] == math.inf).all()) and bool((hit[1] == -math.inf).all())
+        else:
+            assert all(bool(x.isnan().all()) for x in hit)
+        assert [int((~out[i].isfinite()).sum()) for i in range(4)] == [2, 2, 128, 0]
+        assert bool(out[2].isnan().all()) and bool(lse[2].isnan().all())
+        assert bool(lse[[0, 1, 3]].isfinite().all())
 
 
 def test_attention_scores_of_minus_infinity(dev):
@@ -639,6 +695,49 @@ def test_moe_strides_aliases_and_nan_rows(dev):
     rest = [0, 1, 3, 4, 5]
     assert torch.equal(y[rest], want[rest]) and bool(y[2].isnan().all())
     assert bool(layer.weights[2].isnan().all())
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_moe_over_its_residual_or_input(dev, dtype):
+    """The launches of a larger layer: an output over the residual, and over the input."""
+    c = moe_case(dev, 6, 8, 2, 512, 1280, dtype)
+    res = normal(c["g"], (6, 512), dtype)
+    layer, want = moe_check(c, residual=res)
+    x = c["x"].clone()
+    over = torch.cat([x, res], dim=1)
+    got = layer(over[:, :512], residual=over[:, 512:], out=over[:, 512:])
+    assert torch.equal(got, want) and torch.equal(over[:, :512], x)
+    got = layer(x, residual=res, out=x)
+    assert got is x and torch.equal(x, want)
+    both = c["x"].clone()
+    want = layer(c["x"], residual=c["x"])
+    assert torch.equal(layer(both, residual=both, out=both), want)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("tokens,experts,top_k,inter", [
+    (1, 8, 3, 128), (1, 8, 2, 128), (1, 40, 2, 128), (4, 8, 3, 128), (4, 8, 3, 1280),
+    (4, 40, 2, 128), (4, 70, 3, 128)])
+@pytest.mark.parametrize("some", [False, True])
+def test_moe_infinite_logits(dev, dtype, tokens, experts, top_k, inter, some):
+    """A row whose logits are infinite (one +inf before -inf, or -inf alone) is NaN, its experts
+    are in order, and the other rows are what they are without it."""
+    c = moe_case(dev, tokens, experts, top_k, 512, inter, dtype)
+    c["router"][:, 3] = -1
+    if some:
+        c["router"][experts - 3, 3] = 1
+    c["x"][0, 3] = math.inf
+    layer = decode.MoELayer(*c["banks"], c["router"], top_k)
+    y = layer(c["x"])
+    want = ([experts - 3, 0, 1] if some else [0, 1, 2])[:top_k]
+    assert layer.ids[0].tolist() == want
+    assert bool(layer.weights[0].isnan().all()) and bool(y[0].isnan().all())
+    if tokens > 1:
+        w = [dequant(b, c["kind"], c["group"]) for b in c["raw"]]
+        want, ids, weights, err = ref.moe_layer(np64(c["x"][1:]), np64(c["router"]), *w, top_k, True,
+                                                1.0, None, 2.0 ** -16)
+        assert np.array_equal(layer.ids[1:tokens].cpu().numpy(), ids)
+        check(y[1:], want, err * (1 + 64 * ref.E32) + np.abs(want) * 64 * ref.E32, "y")
 
 
 @pytest.mark.parametrize("inter", [256, 1280])

@@ -647,6 +647,19 @@ def test_moe_ties_take_the_lowest_expert(dev, experts):
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("kind,group", [("u4b8", 128), ("u4b8", 64), ("u4b8", 32), ("u4b8", 16),
+                                        ("u4b8", -1), ("u4", 128), ("u4", 64), ("u4", 32),
+                                        ("u4", 16), ("e4m3", 128), ("e4m3", -1)])
+@pytest.mark.parametrize("tokens,experts,inter", [(1, 8, 1024), (16, 5, 384), (16, 17, 128),
+                                                  (3, 4, 512), (8, 1, 2048), (9, 2, 2176)])
+def test_moe_weights_of_small_layers(dev, dtype, kind, group, tokens, experts, inter):
+    """On both sides of the border of the down projections in one launch, 16 groups of K: whole and
+    half rows of work, one expert's rows up to all tokens."""
+    c = moe_case(dev, tokens, experts, min(2, experts), 512, inter, dtype, kind, group)
+    moe_check(c, residual=normal(c["g"], (tokens, 512), dtype))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("tokens,experts,hidden", [(1, 8, 512), (1, 16, 2048), (1, 17, 512),
                                                    (4, 8, 512), (16, 8, 512), (16, 40, 512),
                                                    (3, 70, 512)])
@@ -755,7 +768,7 @@ def test_moe_an_expert_s_values_reach_only_its_own_tokens(dev, inter, kind):
 
 
 @pytest.mark.parametrize("kind", ["u4b8", "u4", "e4m3"])
-@pytest.mark.parametrize("inter", [384, 896])  # few launches, and more
+@pytest.mark.parametrize("inter", [256, 384, 896])  # few launches, and more
 def test_moe_activations_past_fp16(dev, kind, inter):
     """Activations beyond 65504 under a small routing scale: the layer's output is finite."""
     c = moe_case(dev, 5, 6, 2, 512, inter, F16, kind)

@@ -231,7 +231,8 @@ __device__ __forceinline__ void token_top_k(const double* logits, int n_expert, 
         for (int i = 0; i < PER; ++i) low = max(low, upper(i) == best ? (uint32_t)key[i] : 0u);
         low = wave_max(low);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) has[i] = __ballot(upper(i) == best && (uint32_t)key[i] == low);
+        for (int i = 0; i < PER; ++i)
+          has[i] = __ballot(upper(i) == best && (uint32_t)key[i] == low);
       }
       int id = 0;  // lowest expert with this key
 #pragma unroll
@@ -949,10 +950,10 @@ hipError_t launch_moe_type(const wq_moe_args& a, int gate_up_gpc, int down_gpc,
                            hipStream_t stream) {
   const MoeScratch m =
       scratch_of(a.workspace, a.tokens, a.n_expert, a.top_k, a.hidden, a.inter);
-  // A work-group takes all slots' groups of a column block while that is two for each wave: two
-  // launches become one (us, product and combine / down_all: 16 groups 14.6, 14.0; 30 19.6, 18.9;
-  // 48 14.9, 16.6; 64 16.5, 20.6).
-  const bool down_all = max_slots(a.tokens, a.n_expert, a.top_k) * (a.inter / kGroup) <= 32;
+  // A work-group takes all slots' groups of a column block while that is one for each wave: two
+  // launches become one (us, product and combine / down_all: 8 groups 13.0, 12.0; 16 13.6, 13.1;
+  // 24 18.9, 19.7; 32 15.9, 16.9 and 18.3, 20.7; 48 17.2, 20.1).
+  const bool down_all = max_slots(a.tokens, a.n_expert, a.top_k) * (a.inter / kGroup) <= 16;
   hipError_t e = launch_route<BF16>(a, m, down_all, stream);
   if (e != hipSuccess) return e;
   e = launch_bank_type<true, false, BF16>(gate_up_gpc, a, m, stream);

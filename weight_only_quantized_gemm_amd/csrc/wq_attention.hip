@@ -1,12 +1,12 @@
 // Attention of one new token per sequence over a paged KV cache (wq_paged_attention).
 //
 // Each live K and V element is read once and takes part in 2 * (query heads per KV head)
-// products, so the kernel is bound by the cache reads.  The batch's positions are cut into
-// equal ranges (a range a sequence where these are short); a work-group takes a range for one KV
+// products, so the kernel is bound by the cache reads.  The batch's positions are cut into ranges
+// of one length (a range a sequence where these are short); a work-group takes a range for one KV
 // head and up to 16 of its query heads.  Its waves take tiles of 32 or 64 positions in turn and
-// keep their own running maximum, sum and output, joined at the end of each sequence through
-// LDS.  Sequences that lie in several ranges leave fp32 partials that attn_join_kernel adds in
-// their order.
+// keep their own running maximum, sum and output, joined at the end of each sequence through LDS.
+// Sequences that lie in several ranges leave fp32 partials that attn_join_kernel adds in their
+// order.
 //
 // Both products run on 16x16x32 MFMAs with the positions as rows:
 //  - S^T = K Q^T: the A operand is K straight from memory (a lane holds 8 consecutive
@@ -24,16 +24,19 @@
 // a million positions at 2^-26 of the maximum still count.
 //
 // One register set serves the loads: K of the next tile is requested when this tile's scores
-// are formed, V when this tile's V has gone to LDS, so each wave keeps about a tile in
-// flight.  Page numbers are read a tile further ahead.
+// are formed, V when this tile's V has gone to LDS, and page numbers are read a tile further
+// ahead.  As compiled, a tile's first score waits for its V and the next pages as well as for its
+// K (on one path into the loop Q is the newest load), so nothing is in flight while scores are
+// formed.
 //
 // Measured as a graph, and in a kernel trace, 8 KV heads of 128: one sequence of 131072 positions,
-// bf16, 92 us, 5.8 TB/s (89.1 us and the join's 4.7; the matrix units are busy 6% of the time);
-// 16 sequences of up to 4096, 30 us, 4.5 TB/s (26.9, and 4.5); 64 of up to 8192, E4M3,
-// 70% of the positions kept, 85 us, 4.4 TB/s of the kept rows (78.7, and 5.8; matrix units 15%,
-// dropped rows and conversions between); one sequence of 128: 5.7 us, the launch and the trips to
-// memory for the page, K and V.  No byte is fetched twice: the counters show the kept rows' bytes
-// and the table's.
+// bf16, 92 us, 5.8 TB/s, or 97, by where in memory the cache lies (89.8 us and the join's 4.8; the
+// matrix units are busy 6% of the time); 16 sequences of up to 4096, 30 us, 4.8 TB/s (27.6, and
+// 4.3); 64 of up to 8192, E4M3, 70% of the positions kept, 85 us, 4.4 TB/s of the kept rows (79.0,
+// and 5.9; matrix units 15%, dropped rows and conversions between); one sequence of 128: 5.8 us,
+// the launch and two trips to memory, for the page and for K and V.  No byte is fetched twice: the
+// counters show 153.1 MB for the 152.6 of the live rows of 16 sequences, 375.0 for 370.7 kept
+// ones of 64, and 21.1 for the 20.8 inside the windows of seven of up to 3001.
 #include <algorithm>
 #include <type_traits>
 
@@ -148,10 +151,10 @@ struct Range {
 };
 
 // The index-th range; false where it is empty.  All sequences' granules, one sequence after the
-// other, are cut into `ranges` ranges of one length, the last ones shorter or empty.  The lengths are known only here, so every wave
-// counts them, each lane a run of sequences.  (64 sequences of up to 8192 positions, E4M3: cut
-// by the host by the longest length 135 us, in equal splits of each sequence 93.7, as here
-// 88.8; unmasked 121.7 in equal splits, 112.5 here.)
+// other, are cut into `ranges` ranges of one length, the last ones shorter or empty.  The lengths
+// are known only here, so every wave counts them, each lane a run of sequences.  (64 sequences of
+// up to 8192 positions, E4M3: cut by the host by the longest length 135 us, in equal splits of
+// each sequence 93.7, as here 88.8; unmasked 121.7 in equal splits, 112.5 here.)
 template <int TILE>
 __device__ __forceinline__ bool find_range(const AttnArgs& p, int index, bool publish, int lane,
                                            Range& out) {

@@ -25,10 +25,11 @@
 // exact in bf16.
 //
 // Measured as a graph, 128-row groups, K x N of an expert 4096 x 2 * 14336 and 14336 x 4096: one
-// token of two experts, fp16, 43 us, 4.2 TB/s (products 23.5 us at 5.2 TB/s and 13.5 at 4.5 in a
-// kernel trace, routing 4.6, combine 3.4); four tokens of five to six experts, bf16 with zero
-// points, 95 us, 5.2 TB/s (56.4 us at 6.0, 33.9 at 5.0).  16 tokens over 56 of 64 experts of
-// 2048 x 2 * 1024, 64-row groups, 47 us, 4.0 TB/s (24.1 us at 5.2, 14.4 at 4.5).
+// token of two experts, fp16, 44 us, 4.1 TB/s (products 24.1 us at 5.0 TB/s and 13.5 at 4.5 in a
+// kernel trace, routing 5.2, combine 3.8), with E4M3 weights 68 us, 5.3 TB/s (38.5 at 6.2, 21.0 at
+// 5.7); four tokens of five to six experts, bf16 with zero points, 99 us, 5.2 TB/s (57.5 us at 6.0,
+// 36.8 at 4.7).  16 tokens over 56 of 64 experts of 2048 x 2 * 1024, 64-row groups, 50 us, 3.8 TB/s
+// (24.4 us at 5.2, 15.9 at 3.9).
 #include <type_traits>
 
 #include "wq_decode.h"
@@ -118,9 +119,9 @@ __device__ __forceinline__ double wave_logits(const uint16_t* x, int ldx, const 
   return v;
 }
 
-// Logits of one expert and four tokens per work-group, whose threads share the hidden size: 2 us,
-// a launch and a trip to memory, where one CU reading a router of 64 KiB takes 2 us longer and one
-// of 256 KiB 10 us.
+// Logits of one expert and four tokens per work-group, whose threads share the hidden size: 2.1 to
+// 4.8 us, a launch and a trip to memory, where one CU reading a router of 64 KiB takes 2 us longer
+// and one of 256 KiB 10 us.
 template <bool BF16>
 __global__ __launch_bounds__(kRouterThreads) void router_kernel(
     const uint16_t* __restrict__ x, int ldx, const uint16_t* __restrict__ router, int tokens,
@@ -282,8 +283,8 @@ struct RouteArgs {
   int ldx, hidden;
 };
 
-// One work-group, a wave per token; 2.4 us for one token of 8 experts (4.6 with the logits of
-// 4096 elements), 4.1 for 16 of 64: a chain of trips to memory and LDS.  PER: 64 experts for each
+// One work-group, a wave per token; 5.2 us for one token of 8 experts with the logits of 4096
+// elements, 4.6 for 16 of 64 without: a chain of trips to memory and LDS.  PER: 64 experts for each
 // lane of a wave, 1 or 4.  ROUTER: 16 waves form one token's logits here too, first (1: fp16, 2:
 // bf16): an expert for each, or with fewer of these a part of the hidden size.
 template <int PER, int ROUTER>
@@ -761,7 +762,7 @@ __global__ __launch_bounds__(kDownWaves * 64) void down_all_kernel(DownArgs p) {
 }
 
 // y[t] = residual[t] + sum over the token's choices j of w_j part[t][j], 4 columns a thread.
-// Bound by its launch and a trip to memory: 2.3 us for one token of 4096, 3.8 for 16 of 2048.
+// Bound by its launch and a trip to memory: 3.8 us for one token of 4096, 4.3 for 16 of 2048.
 template <bool BF16>
 __global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ part,
                                                       const Route* __restrict__ route, int top_k,

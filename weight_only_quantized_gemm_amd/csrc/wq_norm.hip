@@ -1,7 +1,7 @@
 // RMS norm with the residual add: s = x + delta, y = s / sqrt(mean(s^2) + eps) * w.
 //
 // Two rows read, two written, a few operations per element: bound by memory for many rows
-// (bf16, 8192 rows of 8192: 92 us, 5.8 TB/s of the four rows) and by its launch and one trip to
+// (bf16, 8192 rows of 8192: 94 us, 5.7 TB/s of the four rows) and by its launch and one trip to
 // memory for few (fp16, one row of 4096: 2.7 us).  A row stays in registers as fp32 between its
 // one read and its two writes, so nothing is read twice and the norm sees the unrounded sum.
 #include "wq_decode.h"

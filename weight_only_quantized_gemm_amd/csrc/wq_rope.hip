@@ -7,7 +7,7 @@
 // its threads then each move one unit of 8 elements at a time.
 //
 // Every element is read once and written once, so many tokens are bound by memory (2048 tokens of
-// 32 + 2 x 8 heads of 128 into an E4M3 cache: 11.2 us, 4.1 TB/s) and few by the launch and the
+// 32 + 2 x 8 heads of 128 into an E4M3 cache: 11.4 us, 4.0 TB/s) and few by the launch and the
 // trips to memory for the position and the rows (one token: 3.1 us).
 #include <algorithm>
 

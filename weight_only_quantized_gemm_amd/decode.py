@@ -325,7 +325,8 @@ class PagedAttention:
                 lp = _dense(lse, "lse", torch.float32, dev, (b, heads))
         _attn_call(_ATTN.pack(WQ_ABI_VERSION, _ATTN.size, cache.packed, q.data_ptr(),
                               out.data_ptr(), lp, table, n, kp, *self._space,
-                              self._memory.stream(dev), b, heads, self.max_len, pages, keep_stride, ldq, ldo, *self._last))
+                              self._memory.stream(dev), b, heads, self.max_len, pages,
+                              keep_stride, ldq, ldo, *self._last))
         return out if lse is False else (out, lse)
 
 
@@ -392,5 +393,6 @@ class MoELayer:
         router, gate_up, down = self._banks
         _moe_call(_MOE.pack(WQ_ABI_VERSION, _MOE.size, x.data_ptr(), router, gate_up, down, rp,
                             out.data_ptr(), *self._space, self._memory.stream(dev), tokens,
-                            self.n_expert, self.top_k, hidden, self.inter, ldx, ldr, ldy, *self._last))
+                            self.n_expert, self.top_k, hidden, self.inter, ldx, ldr, ldy,
+                            *self._last))
         return out

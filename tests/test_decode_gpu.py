@@ -328,6 +328,17 @@ def test_attention_many_sequences(dev, batch, longest, hq, hkv):
             attn_check(c, *attn_run(c, cut), f"cut {cut}")
 
 
+@pytest.mark.parametrize("hq,hkv,d,order", [(96, 96, 64, "hnd"), (520, 520, 136, "hnd"),
+                                            (600, 600, 72, "nhd"), (780, 20, 72, "nhd")])
+@pytest.mark.parametrize("kind", ["same", "e4m3"])
+def test_attention_of_many_units(dev, hq, hkv, d, order, kind):
+    """Few ranges, or one, because a range has nearly as many work-groups as a launch, or more; with
+    and without the grid that is rounded up to eight ranges."""
+    c = attn_case(dev, [300, 0, 41], hq, hkv, d, 16, BF16, kind, order)
+    for cut in (False, True):
+        attn_check(c, *attn_run(c, cut), f"cut {cut}")
+
+
 @pytest.mark.parametrize("kw", [{}, dict(kind="e4m3"), dict(keep=True)])
 def test_attention_several_short_sequences_in_a_range(dev, kw):
     """Waves with no, one, two and more tiles of a sequence, in every order."""

@@ -404,7 +404,8 @@ typedef struct wq_norm_args {
 /*
  * RMS norm with the residual add: s = x + delta (x alone without delta), and for each row
  * y = s / sqrt(mean(s^2) + eps) * weight.  The sum and its squares stay in fp32 for the norm: y
- * and sum_out are each rounded once, and a row whose squares pass fp32 gives 0.
+ * and sum_out are each rounded once, a row whose squares pass fp32 gives 0, and squares below
+ * fp32 count as 0 (with an eps of 0 such a row is not finite).
  */
 int wq_add_rms_norm(const wq_norm_args* args);
 

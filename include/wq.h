@@ -559,6 +559,82 @@ int wq_moe_layer_workspace_bytes(int tokens, int n_expert, int top_k, int hidden
  */
 int wq_moe_layer(const wq_moe_args* args);
 
+/* Decode-step calls only: the cache holds 4-bit codes (wq_kv_cache with wq_kv_pairs). */
+#define WQ_FLAG_KV4         (1u << 10)
+
+/* What the codes of a 4-bit cache stand for.  The cache's own wq_kv_cache then describes the
+ * codes: k and v hold two to a byte (element 2i in the low half of byte i of a head), strides
+ * count elements as ever, and it has no k_scale or v_scale.  Each run of group_size elements of a
+ * head has a pair, scale and offset, of the call's element type: pair (page, slot, head, g) at
+ * page*page_stride + slot*slot_stride + head*head_stride + g, and its codes c read as
+ * offset + scale * c. */
+typedef struct wq_kv_pairs {
+  void* k;                  /* device, 4-byte aligned: scale in the low half of a dword    */
+  void* v;
+  int64_t page_stride, slot_stride, head_stride; /* in pairs, >= 0                       */
+  int32_t group_size;       /* head_dim, or 32, 64 or 128 where it divides head_dim        */
+  int32_t reserved;
+} wq_kv_pairs;
+
+typedef struct wq_norm_rope_args {
+  uint32_t abi_version;     /* WQ_ABI_VERSION                                          */
+  uint32_t struct_size;     /* sizeof(wq_norm_rope_args)                               */
+  wq_kv_cache cache;
+  wq_kv_pairs pairs;        /* with WQ_FLAG_KV4; else all zero                          */
+  const void* q;            /* q to sections, and interleaved: as in wq_rope_args         */
+  const void* k;
+  const void* v;
+  void* q_out;
+  const void* q_norm;       /* device [head_dim], 16-byte aligned: the weight of the norm of
+                               every q head; NULL: not normed                          */
+  const void* k_norm;       /* likewise of every k head                                */
+  const int64_t* slots;
+  const int32_t* positions;
+  const float* inv_freq;
+  void* stream;
+  int32_t tokens, q_heads;
+  int32_t ldq, ldk, ldv, ldqo;
+  int32_t rot_dim;
+  int32_t axes;
+  int32_t sections[WQ_MAX_ROPE_AXES];
+  int32_t interleaved;
+  float eps;                /* >= 0                                                    */
+  uint32_t flags;           /* WQ_FLAG_BF16: q, k, v, norms, pairs; WQ_FLAG_FP8 or
+                               WQ_FLAG_KV4: the cache                                   */
+  int32_t reserved;
+} wq_norm_rope_args;
+
+/*
+ * wq_rope_append with norms before the rotation, x / sqrt(mean(x^2) + eps) * weight for each q
+ * and k head by itself, and for 4-bit caches.  A head stays in fp32 from its read to the one
+ * rounding of its write.  A group of a 4-bit cache gets offset = its smallest value and scale =
+ * its range / 15, both rounded to the type, and each element the code nearest to
+ * (x - offset) / scale (ties: the even one; 0 where the scale is 0).  A group whose offset or
+ * scale is not finite (it holds a NaN or an infinity, or passes the type) reads as NaN.  As in
+ * wq_add_rms_norm, a head whose squares pass fp32 is normed to 0.
+ */
+int wq_norm_rope_append(const wq_norm_rope_args* args);
+
+typedef struct wq_cache4_read_args {
+  uint32_t abi_version;     /* WQ_ABI_VERSION                                          */
+  uint32_t struct_size;     /* sizeof(wq_cache4_read_args)                             */
+  wq_kv_cache cache;
+  wq_kv_pairs pairs;
+  const int64_t* slots;     /* device [tokens]: page * page_size + slot, in any order and
+                               as often as wanted; one outside the cache reads as 0       */
+  void* k_out;              /* device [tokens][ldk], heads contiguous in a row; may be NULL */
+  void* v_out;              /* device [tokens][ldv], likewise                           */
+  void* stream;
+  int32_t tokens;           /* 1 to 2^24 - 1                                           */
+  int32_t ldk, ldv;         /* row strides, multiples of 8, >= kv_heads * head_dim (0 if
+                               unused)                                                 */
+  uint32_t flags;           /* WQ_FLAG_BF16                                            */
+  int32_t reserved;
+} wq_cache4_read_args;
+
+/* The values of some slots of a 4-bit cache: offset + scale * code, rounded to the type. */
+int wq_cache4_read(const wq_cache4_read_args* args);
+
 #ifdef __cplusplus
 }
 #endif

@@ -99,3 +99,56 @@ def moe_layer(x, router, gate, up, down, top_k, renormalize, scale, residual, ha
             y[t] += w[t, j] * (h @ down[i])
             err[t] += w[t, j] * ((dh + np.abs(h) * (k2 + 16) * E32) @ np.abs(down[i]))
     return y, ids, w, err
+
+
+def head_norm(x, weight, eps):
+    """x [tokens][heads][d] with each head normed, and the bound of each element."""
+    d = x.shape[-1]
+    y = x / np.sqrt((x * x).sum(axis=-1, keepdims=True) / d + eps) * weight
+    # half of the mean's relative error, a root, a quotient and three products
+    return y, np.abs(y) * ((d + 8) / 2 + 8) * E32
+
+
+def spread(err, half, interleaved):
+    """What a rotation makes of its input's bounds."""
+    out = err.copy()
+    for i in range(half):
+        a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+        out[..., a] = out[..., b] = err[..., a] + err[..., b]
+    return out
+
+
+def unpack4(codes):
+    """[...][d] codes from bytes [...][d / 2], the even element in the low half."""
+    return np.stack([codes & 15, codes >> 4], axis=-1).reshape(*codes.shape[:-1], -1)
+
+
+def values4(codes, pairs):
+    """What bytes [...][d / 2] and pairs [...][groups][2] stand for, in 64 bits."""
+    c = unpack4(codes).astype(np.float64)
+    c = c.reshape(*c.shape[:-1], pairs.shape[-2], -1)
+    with np.errstate(invalid="ignore"):
+        return (pairs[..., 1:] + pairs[..., :1] * c).reshape(*codes.shape[:-1], -1)
+
+
+def check_quantized4(x, err, codes, pairs, half_step, tiny):
+    """Whether bytes and pairs are what x [...][d], known to err, may be stored as: the offset its
+    group's smallest value and the scale a fifteenth of its range, each within a rounding, and
+    every code the nearest one by the pair that is stored.  half_step, tiny: of the pairs' type."""
+    groups = pairs.shape[-2]
+    x = x.reshape(*x.shape[:-1], groups, -1)
+    err = np.broadcast_to(err, codes.shape[:-1] + (codes.shape[-1] * 2,)).reshape(x.shape)
+    code = unpack4(codes).reshape(x.shape).astype(np.float64)
+    scale, offset = pairs[..., :1], pairs[..., 1:]
+    low, high, e = (f(v, axis=-1, keepdims=True) for f, v in ((np.min, x), (np.max, x),
+                                                              (np.max, err)))
+    e = e + tiny
+    assert (np.abs(offset - low) <= np.abs(low) * half_step * 1.01 + e).all()
+    span = (high - low) / 15
+    # the quotient's own rounding, and both ends' errors
+    assert (np.abs(scale - span) <= span * (half_step * 1.01 + 4 * E32) + e).all()
+    off = x - (offset + scale * code)
+    # half a step, the errors of x, its difference and quotient (a code of up to 16 in fp32)
+    room = scale * (0.5 + 64 * E32) + err + (np.abs(x) + np.abs(offset)) * 2 * E32
+    fine = (np.abs(off) <= room) | ((code == 0) & (off < 0)) | ((code == 15) & (off > 0))
+    assert (fine | (scale == 0)).all() and (code[np.broadcast_to(scale == 0, code.shape)] == 0).all()

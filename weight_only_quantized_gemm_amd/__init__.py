@@ -26,6 +26,7 @@ WQ_FLAG_MUL_TOPK_WEIGHTS = 1 << 6
 WQ_FLAG_SWIGLU = 1 << 7
 WQ_FLAG_BF16 = 1 << 8
 WQ_FLAG_FP8 = 1 << 9
+WQ_FLAG_KV4 = 1 << 10
 
 WQ_STAGE_ARGS, WQ_STAGE_SHAPE, WQ_STAGE_DEVICE = 1, 2, 3
 WQ_STAGE_LAUNCH_CONFIG, WQ_STAGE_FUNC_ATTR, WQ_STAGE_LAUNCH = 4, 5, 6
@@ -40,7 +41,7 @@ EXPORTED = (
     "wq_repack_fp8_rows", "wq_fp8_block_scales", "wq_mfma_rate", "wq_gemm_plan",
     "wq_gemm_noalloc", "wq_add_rms_norm", "wq_rope_append",
     "wq_paged_attention_workspace_bytes", "wq_paged_attention",
-    "wq_moe_layer_workspace_bytes", "wq_moe_layer",
+    "wq_moe_layer_workspace_bytes", "wq_moe_layer", "wq_norm_rope_append", "wq_cache4_read",
 )
 WQ_NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -125,6 +126,39 @@ class wq_rope_args(ctypes.Structure):
         ("ldq", ctypes.c_int32), ("ldk", ctypes.c_int32), ("ldv", ctypes.c_int32),
         ("ldqo", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("axes", ctypes.c_int32),
         ("sections", ctypes.c_int32 * WQ_MAX_ROPE_AXES), ("interleaved", ctypes.c_int32),
+        ("flags", ctypes.c_uint32), ("reserved", ctypes.c_int32),
+    ]
+
+
+class wq_kv_pairs(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+        ("slot_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+        ("group_size", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
+
+
+class wq_norm_rope_args(ctypes.Structure):
+    _fields_ = [
+        ("abi_version", ctypes.c_uint32), ("struct_size", ctypes.c_uint32),
+        ("cache", wq_kv_cache), ("pairs", wq_kv_pairs), ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+        ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
+        ("stream", ctypes.c_void_p), ("tokens", ctypes.c_int32), ("q_heads", ctypes.c_int32),
+        ("ldq", ctypes.c_int32), ("ldk", ctypes.c_int32), ("ldv", ctypes.c_int32),
+        ("ldqo", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("axes", ctypes.c_int32),
+        ("sections", ctypes.c_int32 * WQ_MAX_ROPE_AXES), ("interleaved", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("flags", ctypes.c_uint32), ("reserved", ctypes.c_int32),
+    ]
+
+
+class wq_cache4_read_args(ctypes.Structure):
+    _fields_ = [
+        ("abi_version", ctypes.c_uint32), ("struct_size", ctypes.c_uint32),
+        ("cache", wq_kv_cache), ("pairs", wq_kv_pairs), ("slots", ctypes.c_void_p),
+        ("k_out", ctypes.c_void_p), ("v_out", ctypes.c_void_p), ("stream", ctypes.c_void_p),
+        ("tokens", ctypes.c_int32), ("ldk", ctypes.c_int32), ("ldv", ctypes.c_int32),
         ("flags", ctypes.c_uint32), ("reserved", ctypes.c_int32),
     ]
 
@@ -214,6 +248,8 @@ def lib() -> ctypes.CDLL:
             "wq_moe_layer_workspace_bytes": (ctypes.c_int, [i32, i32, i32, i32, i32,
                                                             ctypes.POINTER(sz)]),
             "wq_moe_layer": (ctypes.c_int, [vp]),
+            "wq_norm_rope_append": (ctypes.c_int, [vp]),
+            "wq_cache4_read": (ctypes.c_int, [vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -438,6 +474,14 @@ def wq_add_rms_norm(args: wq_norm_args) -> None:
 
 def wq_rope_append(args: wq_rope_args) -> None:
     _check(lib().wq_rope_append(ctypes.byref(args)))
+
+
+def wq_norm_rope_append(args: wq_norm_rope_args) -> None:
+    _check(lib().wq_norm_rope_append(ctypes.byref(args)))
+
+
+def wq_cache4_read(args: wq_cache4_read_args) -> None:
+    _check(lib().wq_cache4_read(ctypes.byref(args)))
 
 
 def wq_paged_attention_workspace_bytes(batch: int, q_heads: int, kv_heads: int, head_dim: int,

@@ -14,6 +14,9 @@ hipError_t launch_add_rms_norm(const wq_norm_args& a, hipStream_t stream);
 
 hipError_t launch_rope_append(const wq_rope_args& a, hipStream_t stream);
 
+hipError_t launch_norm_rope_append(const wq_norm_rope_args& a, hipStream_t stream);
+hipError_t launch_cache4_read(const wq_cache4_read_args& a, hipStream_t stream);
+
 // How a call's positions are cut: at most `ranges` ranges of equal length over all sequences
 // (0: one range for each sequence), each taken by `units` work-groups, one per KV head and
 // block of 16 of its query heads.  Sequences that no range holds whole leave fp32 partials

@@ -65,6 +65,65 @@ int check_cache(const wq_kv_cache& c, uint32_t flags) {
   return 0;
 }
 
+bool group_ok(int group, int head_dim) {
+  return group == head_dim || ((group == 32 || group == 64 || group == 128) && head_dim % group == 0);
+}
+
+// The pairs of a 4-bit cache that passed check_cache.
+int check_pairs(const wq_kv_cache& c, const wq_kv_pairs& x) {
+  if (x.reserved != 0) return fail(WQ_STAGE_ARGS, WQ_ERR_ABI);
+  if (!group_ok(x.group_size, c.head_dim)) return shape_error();
+  const int64_t strides[3] = {x.page_stride, x.slot_stride, x.head_stride};
+  const int64_t counts[3] = {c.num_pages, c.page_size, c.kv_heads};
+  const int64_t groups = c.head_dim / x.group_size;
+  int64_t extent = groups;
+  for (int i = 0; i < 3; ++i) {
+    if (strides[i] < 0 || (counts[i] > 1 && strides[i] < groups)) return shape_error();
+    if (counts[i] > 1 && strides[i] > (std::numeric_limits<int64_t>::max() / 8) / counts[i])
+      return fail(WQ_STAGE_SHAPE, WQ_ERR_OVERFLOW);
+    extent += strides[i] * (counts[i] - 1);
+    if (extent > std::numeric_limits<int64_t>::max() / 8)
+      return fail(WQ_STAGE_SHAPE, WQ_ERR_OVERFLOW);
+  }
+  int st;
+  if ((st = check_ptr(x.k, 4)) || (st = check_ptr(x.v, 4))) return st;
+  return 0;
+}
+
+bool no_pairs(const wq_kv_pairs& x) {
+  return x.k == nullptr && x.v == nullptr && x.page_stride == 0 && x.slot_stride == 0 &&
+         x.head_stride == 0 && x.group_size == 0 && x.reserved == 0;
+}
+
+// What wq_rope_append and wq_norm_rope_append ask of the arguments that they share.
+template <class Args>
+int check_rope(const Args& a) {
+  if (a.interleaved != 0 && a.interleaved != 1) return flags_error();
+  int st;
+  if ((st = check_cache(a.cache, a.flags))) return st;
+  const int64_t d = a.cache.head_dim;
+  if (a.tokens < 1 || a.tokens > kMaxTokens || a.q_heads < 0 || a.q_heads > kMaxHeads ||
+      a.rot_dim < 0 || a.rot_dim > d || a.rot_dim % 8 != 0 || a.axes < 1 ||
+      a.axes > WQ_MAX_ROPE_AXES)
+    return shape_error();
+  if (!row_stride_ok(a.ldk, a.cache.kv_heads * d) || !row_stride_ok(a.ldv, a.cache.kv_heads * d) ||
+      (a.q_heads > 0 &&
+       (!row_stride_ok(a.ldq, a.q_heads * d) || !row_stride_ok(a.ldqo, a.q_heads * d))))
+    return shape_error();
+  int64_t pairs = 0;
+  for (int i = 0; i < a.axes; ++i) {
+    if (a.sections[i] < 0) return shape_error();
+    pairs += a.sections[i];
+  }
+  if (pairs != a.rot_dim / 2) return shape_error();
+  if ((st = check_ptr(a.k, 16)) || (st = check_ptr(a.v, 16)) || (st = check_ptr(a.slots, 8)))
+    return st;
+  if (a.q_heads > 0 && ((st = check_ptr(a.q, 16)) || (st = check_ptr(a.q_out, 16)))) return st;
+  if (a.rot_dim > 0 && ((st = check_ptr(a.positions, 4)) || (st = check_ptr(a.inv_freq, 4))))
+    return st;
+  return 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -92,29 +151,38 @@ int wq_rope_append(const wq_rope_args* args) {
   if (st) return st;
   const wq_rope_args& a = *args;
   if (a.flags & ~(uint32_t)(WQ_FLAG_BF16 | WQ_FLAG_FP8)) return flags_error();
-  if (a.interleaved != 0 && a.interleaved != 1) return flags_error();
-  if ((st = check_cache(a.cache, a.flags))) return st;
-  const int64_t d = a.cache.head_dim;
-  if (a.tokens < 1 || a.tokens > kMaxTokens || a.q_heads < 0 || a.q_heads > kMaxHeads ||
-      a.rot_dim < 0 || a.rot_dim > d || a.rot_dim % 8 != 0 || a.axes < 1 ||
-      a.axes > WQ_MAX_ROPE_AXES)
-    return shape_error();
-  if (!row_stride_ok(a.ldk, a.cache.kv_heads * d) || !row_stride_ok(a.ldv, a.cache.kv_heads * d) ||
-      (a.q_heads > 0 &&
-       (!row_stride_ok(a.ldq, a.q_heads * d) || !row_stride_ok(a.ldqo, a.q_heads * d))))
-    return shape_error();
-  int64_t pairs = 0;
-  for (int i = 0; i < a.axes; ++i) {
-    if (a.sections[i] < 0) return shape_error();
-    pairs += a.sections[i];
-  }
-  if (pairs != a.rot_dim / 2) return shape_error();
-  if ((st = check_ptr(a.k, 16)) || (st = check_ptr(a.v, 16)) || (st = check_ptr(a.slots, 8)))
-    return st;
-  if (a.q_heads > 0 && ((st = check_ptr(a.q, 16)) || (st = check_ptr(a.q_out, 16)))) return st;
-  if (a.rot_dim > 0 && ((st = check_ptr(a.positions, 4)) || (st = check_ptr(a.inv_freq, 4))))
-    return st;
+  if ((st = check_rope(a))) return st;
   return launched(wq::launch_rope_append(a, as_stream(a.stream)));
+}
+
+int wq_norm_rope_append(const wq_norm_rope_args* args) {
+  int st = check_abi(args);
+  if (st) return st;
+  const wq_norm_rope_args& a = *args;
+  if (a.flags & ~(uint32_t)(WQ_FLAG_BF16 | WQ_FLAG_FP8 | WQ_FLAG_KV4)) return flags_error();
+  if ((a.flags & WQ_FLAG_FP8) && (a.flags & WQ_FLAG_KV4)) return flags_error();
+  if (!(a.flags & WQ_FLAG_KV4) && !no_pairs(a.pairs)) return flags_error();
+  if ((st = check_rope(a))) return st;
+  if ((a.flags & WQ_FLAG_KV4) && (st = check_pairs(a.cache, a.pairs))) return st;
+  if (!(a.eps >= 0.f)) return shape_error();
+  if ((st = check_optional(a.q_norm, 16)) || (st = check_optional(a.k_norm, 16))) return st;
+  return launched(wq::launch_norm_rope_append(a, as_stream(a.stream)));
+}
+
+int wq_cache4_read(const wq_cache4_read_args* args) {
+  int st = check_abi(args);
+  if (st) return st;
+  const wq_cache4_read_args& a = *args;
+  if (a.flags & ~(uint32_t)WQ_FLAG_BF16) return flags_error();
+  if ((st = check_cache(a.cache, a.flags)) || (st = check_pairs(a.cache, a.pairs))) return st;
+  const int64_t row = (int64_t)a.cache.kv_heads * a.cache.head_dim;
+  if (a.tokens < 1 || a.tokens > kMaxTokens || (a.k_out != nullptr && !row_stride_ok(a.ldk, row)) ||
+      (a.v_out != nullptr && !row_stride_ok(a.ldv, row)))
+    return shape_error();
+  if ((st = check_ptr(a.slots, 8)) || (st = check_optional(a.k_out, 16)) ||
+      (st = check_optional(a.v_out, 16)))
+    return st;
+  return launched(wq::launch_cache4_read(a, as_stream(a.stream)));
 }
 
 int wq_paged_attention_workspace_bytes(int batch, int q_heads, int kv_heads, int head_dim,

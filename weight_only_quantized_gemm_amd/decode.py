@@ -1,7 +1,8 @@
 """The decode step around the quantized products, on PyTorch tensors.
 
-RMS norm with the residual add, rotary positions with the paged cache write, attention of one
-new token over that cache, and the mixture-of-experts layer of a few tokens.  PyTorch only
+RMS norm with the residual add, rotary positions (and norms of the query and key heads) with the
+write to a paged cache of 16, 8 or 4 bits, attention of one new token over that cache, and the
+mixture-of-experts layer of a few tokens.  PyTorch only
 allocates device buffers and supplies the stream; every operation is a libwq kernel.
 
 Calls run on the current stream of their tensors' device, enqueue and return; none
@@ -23,9 +24,10 @@ import struct
 
 import torch
 
-from . import (WQ_ABI_VERSION, WQ_FLAG_BF16, WQ_FLAG_FP8, WQ_FLAG_HAS_ZP, WQ_MAX_ROPE_AXES,
-               WQ_MOE_MAX_TOKENS, _check, lib, wq_attn_args, wq_expert_bank, wq_kv_cache,
-               wq_moe_args, wq_moe_layer_workspace_bytes, wq_norm_args,
+from . import (WQ_ABI_VERSION, WQ_FLAG_BF16, WQ_FLAG_FP8, WQ_FLAG_HAS_ZP, WQ_FLAG_KV4,
+               WQ_MAX_ROPE_AXES, WQ_MOE_MAX_TOKENS, _check, lib, wq_attn_args,
+               wq_cache4_read_args, wq_expert_bank, wq_kv_cache, wq_kv_pairs, wq_moe_args,
+               wq_moe_layer_workspace_bytes, wq_norm_args, wq_norm_rope_args,
                wq_paged_attention_workspace_bytes, wq_rope_args)
 
 _TYPE_FLAGS = {torch.float16: 0, torch.bfloat16: WQ_FLAG_BF16}
@@ -44,6 +46,11 @@ _CACHE = f"{ctypes.sizeof(wq_kv_cache)}s"
 _BANK = f"{ctypes.sizeof(wq_expert_bank)}s"
 _NORM = _layout(wq_norm_args, "6P6ifIi")
 _ROPE = _layout(wq_rope_args, _CACHE + "8P8i" + f"{WQ_MAX_ROPE_AXES}iiIi")
+_PAIRS = f"{ctypes.sizeof(wq_kv_pairs)}s"
+_NO_PAIRS = bytes(ctypes.sizeof(wq_kv_pairs))
+_NORM_ROPE = _layout(wq_norm_rope_args,
+                     _CACHE + _PAIRS + "10P8i" + f"{WQ_MAX_ROPE_AXES}iifIi")
+_READ4 = _layout(wq_cache4_read_args, _CACHE + _PAIRS + "4P3iIi")
 _ATTN = _layout(wq_attn_args, _CACHE + "7PNP7iffiIi")
 _MOE = _layout(wq_moe_args, "2P" + 2 * _BANK + "5PNP8ifiIi")
 
@@ -88,6 +95,7 @@ class _Call:
 
 
 _norm_call, _rope_call = _Call("wq_add_rms_norm"), _Call("wq_rope_append")
+_norm_rope_call, _read4_call = _Call("wq_norm_rope_append"), _Call("wq_cache4_read")
 _attn_call, _moe_call = _Call("wq_paged_attention"), _Call("wq_moe_layer")
 
 
@@ -222,15 +230,101 @@ class PagedCache:
         return _type_flag(dtype)
 
 
-def rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: PagedCache,
-                slots: torch.Tensor, *, positions: torch.Tensor | None = None,
-                inv_freq: torch.Tensor | None = None, sections=None, interleaved: bool = False,
+class PagedCache4:
+    """A paged KV cache of 4-bit codes over two uint8 tensors seen as
+    [page][slot][kv_head][head_dim / 2] (two elements to a byte, the even one in its low half) and
+    two fp16 or bf16 tensors [page][slot][kv_head][group][2] of the scale and the offset of each
+    group: a code c reads as offset + scale * c.  A group is the whole head, or 32, 64 or 128
+    elements of it.  Any page, slot and head strides, the same for K and V."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_pairs: torch.Tensor,
+                 v_pairs: torch.Tensor):
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
+            raise ValueError("K and V: two [page][slot][kv_head][head_dim / 2] tensors of the same "
+                             "shape and strides expected")
+        if k_pairs.dim() != 5 or k_pairs.shape != v_pairs.shape or \
+                k_pairs.stride() != v_pairs.stride() or k_pairs.shape[:3] != k.shape[:3] or \
+                k_pairs.shape[4] != 2:
+            raise ValueError("pairs of K and V: two [page][slot][kv_head][group][2] tensors of the "
+                             "same shape and strides expected, pages, slots and heads as the codes'")
+        if k.dtype is not torch.uint8 or v.dtype is not torch.uint8:
+            raise TypeError("codes: uint8 expected")
+        if k_pairs.dtype != v_pairs.dtype or \
+                len({t.device for t in (k, v, k_pairs, v_pairs)}) != 1:
+            raise TypeError("K and V, codes or pairs, differ in type or device")
+        self.dtype, self.device, self.dev = k_pairs.dtype, k.device, k.get_device()
+        self._flags = _type_flag(self.dtype) | WQ_FLAG_KV4
+        self.num_pages, self.page_size, self.kv_heads, half = k.shape
+        self.head_dim, groups = 2 * half, k_pairs.shape[3]
+        if groups < 1 or self.head_dim % groups:
+            raise ValueError(f"{groups} groups of a head of {self.head_dim}")
+        self.group = self.head_dim // groups
+        if k.stride(3) != 1 or k_pairs.stride(4) != 1 or (groups > 1 and k_pairs.stride(3) != 2):
+            raise ValueError("the codes and the pairs of a head must be contiguous")
+        self.k, self.v, self.k_pairs, self.v_pairs = k, v, k_pairs, v_pairs
+        strides, steps = ([t.stride(i) if k.shape[i] > 1 else 0 for i in range(3)]
+                          for t in (k, k_pairs))
+        if any(n % 2 for n in steps) or k_pairs.data_ptr() % 4 or v_pairs.data_ptr() % 4:
+            raise ValueError("pairs: the strides of pages, slots and heads must be whole pairs")
+        self.packed = bytes(wq_kv_cache(
+            k=k.data_ptr(), v=v.data_ptr(), page_stride=2 * strides[0], slot_stride=2 * strides[1],
+            head_stride=2 * strides[2], num_pages=self.num_pages, page_size=self.page_size,
+            kv_heads=self.kv_heads, head_dim=self.head_dim))
+        self.packed_pairs = bytes(wq_kv_pairs(
+            k=k_pairs.data_ptr(), v=v_pairs.data_ptr(), page_stride=steps[0] // 2,
+            slot_stride=steps[1] // 2, head_stride=steps[2] // 2, group_size=self.group))
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, kv_heads: int, head_dim: int,
+              dtype: torch.dtype, device="cuda", group: int | None = None) -> "PagedCache4":
+        """A new cache, pages stored head-major, for calls of this type: 64 elements to a group
+        where that divides the head, else the whole head."""
+        if group is None:
+            group = 64 if head_dim % 64 == 0 else head_dim
+        shape = (num_pages, kv_heads, page_size)
+        return cls(*(torch.zeros((*shape, head_dim // 2), dtype=torch.uint8,
+                                 device=device).transpose(1, 2) for _ in range(2)),
+                   *(torch.zeros((*shape, head_dim // group, 2), dtype=dtype,
+                                 device=device).transpose(1, 2) for _ in range(2)))
+
+    def flags(self, dtype: torch.dtype) -> int:
+        """The flags of a call whose q (or k and v) have this type."""
+        if dtype is not self.dtype:
+            raise TypeError(f"the cache holds pairs of {self.dtype}, the call's tensors are {dtype}")
+        return self._flags
+
+    def read(self, slots: torch.Tensor, k_out: torch.Tensor | None = None,
+             v_out: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+        """(k, v) [tokens][kv_heads][head_dim]: what the codes of these slots stand for (int64
+        page * page_size + slot; a slot outside the cache reads as 0)."""
+        tokens, heads, d = slots.shape[0], self.kv_heads, self.head_dim
+        sl = _dense(slots, "slots", torch.int64, self.dev, (tokens,))
+        outs, ld = [k_out, v_out], [heads * d] * 2
+        for i, name in enumerate(("k_out", "v_out")):
+            if outs[i] is None:
+                outs[i] = torch.empty((tokens, heads, d), dtype=self.dtype, device=self.device)
+            else:
+                ld[i] = _heads(outs[i], name, self.dtype, self.dev, tokens, heads, d)
+        if tokens:
+            _read4_call(_READ4.pack(WQ_ABI_VERSION, _READ4.size, self.packed, self.packed_pairs, sl,
+                                    outs[0].data_ptr(), outs[1].data_ptr(), _stream(self.dev),
+                                    tokens, *ld, self._flags & WQ_FLAG_BF16, 0))
+        return outs[0], outs[1]
+
+
+def rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
+                cache: PagedCache | PagedCache4, slots: torch.Tensor, *,
+                positions: torch.Tensor | None = None, inv_freq: torch.Tensor | None = None,
+                sections=None, interleaved: bool = False, q_norm: torch.Tensor | None = None,
+                k_norm: torch.Tensor | None = None, eps: float = 1e-6,
                 q_out: torch.Tensor | None = None) -> torch.Tensor | None:
     """Rotates q [tokens][q_heads][d] and k [tokens][kv_heads][d] and writes k and v to their
     cache slots (int64 page * page_size + slot; -1 writes nothing).  Pair i turns by
     positions[axis(i)][token] * inv_freq[i]: positions int32 [axes][tokens] (or [tokens]),
     inv_freq fp32 [rot / 2] (None or empty: no rotation), sections the number of pairs of each
-    axis.  Returns the rotated q (q_out, which may be q; a new tensor by default)."""
+    axis.  With q_norm or k_norm [d] each head of q or k is normed before it turns:
+    x / sqrt(mean(x^2) + eps) * weight.  Returns the rotated q (q_out, which may be q; a new tensor
+    by default)."""
     dtype, dev, d, kv_heads = k.dtype, cache.dev, cache.head_dim, cache.kv_heads
     flags = cache.flags(dtype)
     tokens = k.shape[0]
@@ -247,8 +341,8 @@ def rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache:
         else:
             ldqo = _heads(q_out, "q_out", dtype, dev, tokens, heads, d)
         qp, qo = q.data_ptr(), q_out.data_ptr()
-    elif q_out is not None:
-        raise ValueError("q_out needs q")
+    elif q_out is not None or q_norm is not None:
+        raise ValueError("q_out and q_norm need q")
     half = pp = fp = 0
     axes, pairs = 1, [0, 0, 0, 0]
     if inv_freq is not None:
@@ -268,7 +362,17 @@ def rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache:
         fp = _dense(inv_freq, "inv_freq", torch.float32, dev, (half,))
         pp = _dense(positions, "positions", torch.int32, dev,
                     (tokens,) if len(shape) == 1 else (axes, tokens))
-    if tokens:
+    four = flags & WQ_FLAG_KV4
+    if four or q_norm is not None or k_norm is not None:
+        qn = 0 if q_norm is None else _dense(q_norm, "q_norm", dtype, dev, (d,))
+        kn = 0 if k_norm is None else _dense(k_norm, "k_norm", dtype, dev, (d,))
+        if tokens:
+            _norm_rope_call(_NORM_ROPE.pack(
+                WQ_ABI_VERSION, _NORM_ROPE.size, cache.packed,
+                cache.packed_pairs if four else _NO_PAIRS, qp, k.data_ptr(), v.data_ptr(), qo, qn,
+                kn, sl, pp, fp, _stream(dev), tokens, heads, ldq, ldk, ldv, ldqo, 2 * half, axes,
+                *pairs, interleaved, eps, flags, 0))
+    elif tokens:
         _rope_call(_ROPE.pack(WQ_ABI_VERSION, _ROPE.size, cache.packed, qp, k.data_ptr(),
                               v.data_ptr(), qo, sl, pp, fp, _stream(dev), tokens, heads, ldq, ldk,
                               ldv, ldqo, 2 * half, axes, *pairs, interleaved, flags, 0))

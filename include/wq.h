@@ -635,6 +635,44 @@ typedef struct wq_cache4_read_args {
 /* The values of some slots of a 4-bit cache: offset + scale * code, rounded to the type. */
 int wq_cache4_read(const wq_cache4_read_args* args);
 
+typedef struct wq_attn4_args {
+  uint32_t abi_version;     /* WQ_ABI_VERSION                                          */
+  uint32_t struct_size;     /* sizeof(wq_attn4_args)                                   */
+  wq_kv_cache cache;
+  wq_kv_pairs pairs;
+  const void* q;            /* q to window: as in wq_attn_args                           */
+  void* out;
+  float* lse;
+  const int32_t* block_table;
+  const int32_t* lens;
+  const uint8_t* keep;
+  void* workspace;          /* device, 16-byte aligned; wq_paged_attention4_workspace_bytes */
+  size_t workspace_bytes;
+  void* stream;
+  int32_t batch, q_heads;
+  int32_t max_len;
+  int32_t table_stride, keep_stride;
+  int32_t ldq, ldo;
+  float scale;
+  float softcap;
+  int32_t window;
+  uint32_t flags;           /* WQ_FLAG_BF16: q, out and pairs                            */
+  int32_t reserved;
+} wq_attn4_args;
+
+/* Workspace bytes of wq_paged_attention4 (0 where no sequence is split).  Contents need no
+ * initialization; calls that share one must not run concurrently. */
+int wq_paged_attention4_workspace_bytes(int batch, int q_heads, int kv_heads, int head_dim,
+                                        int group_size, int max_len, int window,
+                                        size_t* bytes_out);
+
+/*
+ * wq_paged_attention over a 4-bit cache: k_j and v_j are offset + scale * code, which is not
+ * rounded to the type.  A live group that reads as NaN makes the scores of its position NaN (K) or
+ * its elements of the output (V).  Query elements have to be finite.
+ */
+int wq_paged_attention4(const wq_attn4_args* args);
+
 #ifdef __cplusplus
 }
 #endif

@@ -33,9 +33,12 @@ def rotate(x, positions, inv_freq, sections, interleaved):
 
 
 def paged_attention(q, k_cache, v_cache, table, lens, scale, window=0, softcap=0.0, keep=None,
-                    bad=None):
+                    bad=None, k_terms=None, v_terms=None):
     """q [batch][q_heads][d]; caches [page][slot][kv_head][d] (scales applied).  Returns out,
-    lse and the bounds of both before the output's rounding."""
+    lse and the bounds of both before the output's rounding.  k_terms, v_terms: the sum of the sizes
+    of the terms that make up each element (its own size where it is one term)."""
+    k_terms = np.abs(k_cache) if k_terms is None else k_terms
+    v_terms = np.abs(v_cache) if v_terms is None else v_terms
     batch, q_heads, d = q.shape
     pages, page_size, kv_heads = k_cache.shape[:3]
     per = q_heads // kv_heads
@@ -51,10 +54,11 @@ def paged_attention(q, k_cache, v_cache, table, lens, scale, window=0, softcap=0
             continue
         at = tuple(np.array(live).T)
         k, v = k_cache[at], v_cache[at]  # [n][kv_heads][d]
+        k_size, v_size = k_terms[at], v_terms[at]
         for h in range(q_heads):
             kh, vh = k[:, h // per], v[:, h // per]
             s = kh @ q[b, h] * scale
-            s_err = (np.abs(kh) @ np.abs(q[b, h])) * abs(scale) * (d + 8) * E32
+            s_err = (k_size[:, h // per] @ np.abs(q[b, h])) * abs(scale) * (d + 8) * E32
             s_err = s_err + np.abs(s) * 8 * E32
             if softcap:
                 s = softcap * np.tanh(s / softcap)
@@ -68,7 +72,7 @@ def paged_attention(q, k_cache, v_cache, table, lens, scale, window=0, softcap=0
             out[b, h] = p @ vh / total
             # p is off by its score's error and keeps 16 bits
             rel = 2 * s_err + 2.0 ** -16 + (len(live) + 8) * E32
-            out_err[b, h] = rel * (p @ np.abs(vh)) / total
+            out_err[b, h] = rel * (p @ v_size[:, h // per]) / total
     return out, lse, out_err, lse_err
 
 
@@ -129,6 +133,15 @@ def values4(codes, pairs):
     c = c.reshape(*c.shape[:-1], pairs.shape[-2], -1)
     with np.errstate(invalid="ignore"):
         return (pairs[..., 1:] + pairs[..., :1] * c).reshape(*codes.shape[:-1], -1)
+
+
+def terms4(codes, pairs):
+    """The sizes of the terms of values4's elements as the attention adds them: the code is taken
+    16 larger, and 16 scales off again."""
+    c = unpack4(codes).astype(np.float64)
+    c = c.reshape(*c.shape[:-1], pairs.shape[-2], -1)
+    p = np.abs(pairs)
+    return (p[..., 1:] + p[..., :1] * (c + 32)).reshape(*codes.shape[:-1], -1)
 
 
 def check_quantized4(x, err, codes, pairs, half_step, tiny):

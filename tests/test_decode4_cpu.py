@@ -9,7 +9,7 @@ import pytest
 
 import weight_only_quantized_gemm_amd as wq
 from oracle import decode as ref
-from test_decode_cpu import ABI, ALIGN, BAD, CACHE_REFUSALS, FLAGS, NULL, OVER, P, cache_args, refused
+from test_decode_cpu import ABI, ALIGN, BAD, CACHE_REFUSALS, FLAGS, NULL, OVER, P, SPACE, cache_args, refused
 
 torch = pytest.importorskip("torch")
 from weight_only_quantized_gemm_amd import decode  # noqa: E402
@@ -77,10 +77,49 @@ def test_read_refusals(changes, want):
     refused(wq.wq_cache4_read, read_args(), changes, want)
 
 
+def attn4_args():
+    return wq.versioned(wq.wq_attn4_args, cache=cache_args(), pairs=pairs_args(), q=3 * P, out=4 * P,
+                        block_table=5 * P, lens=6 * P, workspace=7 * P, workspace_bytes=1 << 30,
+                        batch=2, q_heads=4, max_len=40000, table_stride=2500, ldq=256, ldo=256,
+                        scale=0.1)
+
+
+@pytest.mark.parametrize("changes,want", PAIR_REFUSALS + [
+    (dict(batch=0), BAD), (dict(batch=65536), BAD), (dict(q_heads=3), BAD), (dict(q_heads=0), BAD),
+    (dict(max_len=0), BAD), (dict(max_len=(1 << 30) + 1), BAD), (dict(table_stride=2499), BAD),
+    (dict(keep=P, keep_stride=39999), BAD), (dict(ldq=128), BAD), (dict(ldo=260), BAD),
+    (dict(window=-1), BAD), (dict(scale=math.inf), BAD), (dict(scale=math.nan), BAD),
+    (dict(softcap=-1.0), BAD), (dict(softcap=math.inf), BAD), (dict(q=None), NULL),
+    (dict(out=P + 8), ALIGN), (dict(lse=P + 2), ALIGN), (dict(block_table=None), NULL),
+    (dict(lens=P + 1), ALIGN), (dict(workspace=None), SPACE), (dict(workspace_bytes=64), SPACE),
+    (dict(workspace=P + 8), ALIGN), (dict(flags=KV4), FLAGS), (dict(flags=FP8), FLAGS),
+    (dict(abi_version=2), ABI), (dict(struct_size=8), ABI), (dict(reserved=1), ABI),
+])
+def test_attention4_refusals(changes, want):
+    refused(wq.wq_paged_attention4, attn4_args(), changes, want)
+
+
+def test_attention4_workspace():
+    f = wq.wq_paged_attention4_workspace_bytes
+    assert f(1, 8, 2, 64, 32, 1) == 0 == f(1, 8, 2, 64, 64, 256)  # no sequence is split
+    assert f(3, 8, 2, 64, 32, 1 << 20) > 0 == f(1, 8, 2, 64, 32, 1 << 20, 700)
+    with pytest.raises(wq.WQError) as e:
+        f(65535, 512, 512, 64, 64, 128)                           # work-groups of one launch
+    assert e.value.code == wq.WQ_ERR_OVERFLOW
+    with pytest.raises(wq.WQError) as e:
+        f(65535, 8, 2, 64, 64, 1 << 30)                           # steps of all sequences
+    assert e.value.code == wq.WQ_ERR_OVERFLOW
+    for bad in ((0, 8, 2, 64, 32, 1), (1, 7, 2, 64, 32, 1), (1, 8, 0, 64, 32, 1), (1, 8, 2, 20, 20, 1),
+                (1, 8, 2, 64, 16, 1), (1, 8, 2, 80, 32, 1), (1, 8, 2, 64, 128, 1)):
+        with pytest.raises(wq.WQError):
+            f(*bad)
+
+
 def test_null_structs_and_sizes():
     L = wq.lib()
     for name, cls in (("wq_norm_rope_append", wq.wq_norm_rope_args),
-                      ("wq_cache4_read", wq.wq_cache4_read_args)):
+                      ("wq_cache4_read", wq.wq_cache4_read_args),
+                      ("wq_paged_attention4", wq.wq_attn4_args)):
         assert getattr(L, name)(None) == (wq.WQ_STAGE_ARGS << 16) | wq.WQ_ERR_NULL
         with pytest.raises(wq.WQError) as e:  # the binding's size passes, later checks fail
             getattr(wq, name)(wq.versioned(cls))
@@ -133,6 +172,12 @@ def test_binding_refuses_before_the_library():
         cache.read(slots, k_out=k[:4])
     with pytest.raises(TypeError):
         cache.read(slots, v_out=k.float())
+    plan = decode.PagedAttention(cache, 5, 4, 48, dtype=f16)
+    with pytest.raises(TypeError):
+        decode.PagedAttention(cache, 5, 4, 48, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        plan(torch.zeros((4, 4, 64), dtype=f16), torch.zeros((5, 3), dtype=torch.int32),
+             torch.zeros(5, dtype=torch.int32))
 
 
 # ---- pins of the 64-bit forms --------------------------------------------------------------------

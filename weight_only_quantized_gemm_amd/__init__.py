@@ -42,6 +42,7 @@ EXPORTED = (
     "wq_gemm_noalloc", "wq_add_rms_norm", "wq_rope_append",
     "wq_paged_attention_workspace_bytes", "wq_paged_attention",
     "wq_moe_layer_workspace_bytes", "wq_moe_layer", "wq_norm_rope_append", "wq_cache4_read",
+    "wq_paged_attention4_workspace_bytes", "wq_paged_attention4",
 )
 WQ_NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -178,6 +179,21 @@ class wq_attn_args(ctypes.Structure):
     ]
 
 
+class wq_attn4_args(ctypes.Structure):
+    _fields_ = [
+        ("abi_version", ctypes.c_uint32), ("struct_size", ctypes.c_uint32),
+        ("cache", wq_kv_cache), ("pairs", wq_kv_pairs), ("q", ctypes.c_void_p),
+        ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+        ("keep", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t), ("stream", ctypes.c_void_p),
+        ("batch", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("max_len", ctypes.c_int32),
+        ("table_stride", ctypes.c_int32), ("keep_stride", ctypes.c_int32),
+        ("ldq", ctypes.c_int32), ("ldo", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("flags", ctypes.c_uint32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
 class wq_expert_bank(ctypes.Structure):
     _fields_ = [
         ("b", ctypes.c_void_p), ("s", ctypes.c_void_p), ("zp", ctypes.c_void_p),
@@ -250,6 +266,8 @@ def lib() -> ctypes.CDLL:
             "wq_moe_layer": (ctypes.c_int, [vp]),
             "wq_norm_rope_append": (ctypes.c_int, [vp]),
             "wq_cache4_read": (ctypes.c_int, [vp]),
+            "wq_paged_attention4_workspace_bytes": (ctypes.c_int, [i32] * 7 + [ctypes.POINTER(sz)]),
+            "wq_paged_attention4": (ctypes.c_int, [vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -494,6 +512,18 @@ def wq_paged_attention_workspace_bytes(batch: int, q_heads: int, kv_heads: int, 
 
 def wq_paged_attention(args: wq_attn_args) -> None:
     _check(lib().wq_paged_attention(ctypes.byref(args)))
+
+
+def wq_paged_attention4_workspace_bytes(batch: int, q_heads: int, kv_heads: int, head_dim: int,
+                                        group_size: int, max_len: int, window: int = 0) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().wq_paged_attention4_workspace_bytes(batch, q_heads, kv_heads, head_dim, group_size,
+                                                     max_len, window, ctypes.byref(out)))
+    return int(out.value)
+
+
+def wq_paged_attention4(args: wq_attn4_args) -> None:
+    _check(lib().wq_paged_attention4(ctypes.byref(args)))
 
 
 def wq_moe_layer_workspace_bytes(tokens: int, n_expert: int, top_k: int, hidden: int,

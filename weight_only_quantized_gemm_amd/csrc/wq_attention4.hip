@@ -1,0 +1,563 @@
+// Attention of one new token per sequence over a paged cache of 4-bit codes (wq_paged_attention4).
+//
+// As in the 16-bit kernel, a work-group takes a range of the batch's positions for one KV head, its
+// waves take tiles of positions in turn with a running maximum, sum and output of their own, and
+// both products run on 16x16x32 MFMAs with the positions as rows, S^T = K Q^T and O^T = V^T P^T.
+// What differs is that a row is codes c and, for each group g of the head, a scale and an offset:
+//
+//   k_j[i] = o_jg + s_jg c_ji:   q . k_j = sum_g s_jg (q . c_j)_g + o_jg (sum of q over g)
+//   sum_j p_j v_j[i]            = sum_j (p_j s_jg) c_ji + sum_j p_j o_jg
+//
+// so codes go into the products as they are, and what belongs to a (position, group) is applied to
+// the scores and to p, in fp32.  The sixteen columns of a product are query heads times groups:
+// column (h, g) holds head h's query with all but g's elements zero, its scores' lanes add up over g,
+// and its p is multiplied by g's scale alone.  A column then costs what it would without groups,
+// and an output column holds all of the head's elements, of which those in g are used.
+//
+// A code becomes a 16-bit operand in half an instruction and a shift: c in the upper bits of a bf16
+// mantissa below the exponent of 16 is 16 + c.  For K the 16 is in the accumulator that a product
+// starts from (-16 times the sum of q over g), for V in the offset (o - 16 s).  The operands are bf16
+// for both element types: q of fp16 is cut into two (exactly), p s into two that keep 16 bits.
+//
+// V's codes need the positions along the register: the transposing read of 4-bit elements gives a
+// lane 16 positions of one element, which serve two products.
+#include <type_traits>
+
+#include "wq_attention.h"
+
+namespace wq {
+namespace {
+
+constexpr int kTile = 64, kStep = kWaves * kTile;  // positions of a wave's step, and of all four's
+
+struct Attn4Args : AttnArgs {
+  const uint32_t *k_pairs, *v_pairs;
+  int64_t pair_page, pair_slot, pair_head;
+  int group_size, groups;
+};
+
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
+
+// Eight codes as 16 + c, nibbles in the order 0, 4, 1, 5, 2, 6, 3, 7.
+__device__ __forceinline__ bf16x8 from_codes(uint32_t w, uint32_t pattern) {
+  const uint32_t mask = 0x00780078u;
+  u32x4 x;
+  x[0] = ((w << 3) & mask) | pattern;
+  x[1] = ((w >> 1) & mask) | pattern;
+  x[2] = ((w >> 5) & mask) | pattern;
+  x[3] = ((w >> 9) & mask) | pattern;
+  return __builtin_bit_cast(bf16x8, x);
+}
+
+__device__ __forceinline__ f32x4 mfma_bf(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// Sum over the groups' lanes of a head (GP neighbours).
+template <int GP>
+__device__ __forceinline__ float group_sum(float x) {
+  const auto add = [&](int y) { x += __builtin_bit_cast(float, y); };
+  if constexpr (GP >= 2)  // quad_perm 1 0 3 2
+    add(__builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0xB1, 0xf, 0xf, false));
+  if constexpr (GP >= 4)  // quad_perm 2 3 0 1
+    add(__builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x4E, 0xf, 0xf, false));
+  if constexpr (GP >= 8)  // row_half_mirror: the other four of eight lanes, whose sums are equal
+    add(__builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x141, 0xf, 0xf, false));
+  return x;
+}
+
+// W: dwords of a row that a lane holds of K, head_dim rounded up over 32.  GP: groups of a head,
+// rounded up to a power of two.  FULL: head_dim is 32 W.
+template <bool BF16, int W, int GP, bool FULL>
+__global__ __launch_bounds__(kWaves * 64) void attn4_kernel(Attn4Args p) {
+  using A = Act<BF16>;
+  constexpr int DP = 32 * W;
+  constexpr int NT = kTile / 16;   // 16-position blocks of a tile
+  constexpr int NB = DP / 16;      // 16-element blocks of the output
+  constexpr int HB = 16 / GP;      // query heads of a work-group
+  constexpr int SD = W % 2 == 0 ? 4 * W + 4 : 4 * W + 8;  // dwords of an LDS row of V: 4 mod 8
+  constexpr int OS = DP + 4;       // LDS row of the joined outputs
+  constexpr int kVDwords = kTile * SD + 2;
+  constexpr int kVBytes = kWaves * kVDwords * 4, kOBytes = kWaves * HB * OS * 4;
+  __shared__ __align__(16) uint8_t lds[kVBytes > kOBytes ? kVBytes : kOBytes];
+  __shared__ __align__(16) uint32_t pair_lds[kWaves][2][GP][kTile];
+  __shared__ int64_t off_lds[kWaves][kTile];
+  __shared__ float ml_lds[kWaves][HB][2];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row = lane & 15, qd = lane >> 4;
+  int index, unit;
+  if (!place_of_block(blockIdx.x, p.units, p.near_units != 0, p.ranges > 0 ? p.ranges : p.batch,
+                      index, unit))
+    return;
+  Range rg{index, 0, 0};
+  if (p.ranges > 0 && !find_range<kTile>(p, index, blockIdx.x == 0 && wave == 0, lane, rg)) return;
+  const int kvh = unit / p.head_blocks, hb = unit - kvh * p.head_blocks;
+  const int h0 = kvh * p.group + HB * hb;         // first query head
+  const int rows = min(HB, p.group - HB * hb);
+  const int my_head = row / GP, my_group = row % GP;  // this lane's column
+
+  // Part of a sequence that this range holds.
+  struct Part {
+    int b, lo, t0, t1;           // sequence, first live position, positions [t0, t1)
+    int t_pages;                 // page numbers are read for positions below it
+    int first, count, granules;  // granules of the sequence: first one here, how many, in all
+  };
+  const auto part_of = [&](int b, int first, int left) {
+    Part s;
+    const int len = max(0, min(p.lens[b], p.max_len));
+    s.b = b;
+    s.lo = p.window > 0 ? max(0, len - p.window) : 0;
+    s.first = first;
+    s.granules = granules_of<kTile>(p, len);
+    s.count = p.ranges > 0 ? min(s.granules - first, left) : s.granules;
+    const int start = window_start<kTile>(p, len);
+    s.t0 = start + first * kStep;
+    s.t1 = p.ranges > 0 ? min(len, start + (first + s.count) * kStep) : len;
+    s.t_pages = p.ranges > 0 || p.window > 0 ? len : p.max_len;
+    return s;
+  };
+
+  const int nd = FULL ? 4 * W : p.d / 8;  // dwords of a row
+  // The dword of a row that a lane holds in its w-th register: 16 or 8 bytes side by side.
+  const auto dword_of = [&](int w) {
+    if (W == 2) return 2 * qd + w;
+    if (W == 3) return w < 2 ? 2 * qd + w : 8 + qd;
+    if (W == 6) return w < 4 ? 4 * qd + w : 16 + 2 * qd + (w - 4);
+    return 16 * (w / 4) + 4 * qd + w % 4;
+  };
+
+  // Q as the B operand: this column's head, its group's elements, in the codes' order.
+  uint32_t pattern;
+  asm volatile("v_mov_b32 %0, 0x41804180" : "=v"(pattern));
+  bf16x8 qh[W], ql[BF16 ? 1 : W];
+  float q_sum = 0.f;
+  const auto load_q = [&](int b) {
+    const uint16_t* qp =
+        p.q + (int64_t)b * p.ldq + (int64_t)(h0 + (my_head < rows ? my_head : 0)) * p.d;
+    q_sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const int dw = dword_of(w);
+      u32x4 raw = {0u, 0u, 0u, 0u};
+      if ((FULL || dw < nd) && my_head < rows && 8 * dw / p.group_size == my_group)
+        raw = *reinterpret_cast<const u32x4*>(qp + 8 * dw);
+      uint16_t x[8];
+      __builtin_memcpy(x, &raw, 16);
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        const uint16_t bits = x[t / 2 + 4 * (t % 2)];
+        const float f = A::value(bits);
+        q_sum += f;
+        if constexpr (BF16) {
+          qh[w][t] = __builtin_bit_cast(bf16, bits);
+        } else {
+          const bf16 high = (bf16)f;
+          qh[w][t] = high;
+          ql[w][t] = (bf16)(f - (float)high);  // at most 4 bits are left: exact
+        }
+      }
+    }
+    q_sum += __shfl_xor(q_sum, 16);
+    q_sum += __shfl_xor(q_sum, 32);
+  };
+
+  const uint8_t* kbase = p.k + kvh * p.head_stride / 2;
+  const uint8_t* vbase = p.v + kvh * p.head_stride / 2;
+  const uint32_t* k_pairs = p.k_pairs + kvh * p.pair_head;
+  const uint32_t* v_pairs = p.v_pairs + kvh * p.pair_head;
+
+  // Page numbers (and keep bytes) of the tile at t, one position per lane.
+  int page_next = -1, pos_next = 0, slot_next = 0;
+  uint8_t keep_next = 1;
+  const auto read_pages = [&](int b, int t_pages, int t) {
+    const int pos = t + lane;
+    const int at = (int)(__umulhi(2u * (unsigned)pos, p.page_mul) >> p.page_shift);
+    pos_next = pos;
+    slot_next = pos - at * p.page_size;
+    page_next = -1;
+    if (pos < t_pages) {
+      page_next = p.table[(int64_t)b * p.table_stride + at];
+      if (p.keep != nullptr) keep_next = p.keep[(int64_t)b * p.keep_stride + pos];
+    }
+  };
+  // Cache offsets of the tile whose pages were read; returns the mask of live positions.  A
+  // position that is not live reads the cache's first slot, and is not used.
+  int64_t pair_off = 0;
+  const auto place = [&](int lo, int t1) -> uint64_t {
+    const bool live = (unsigned)page_next < (unsigned)p.num_pages && keep_next != 0 &&
+                      pos_next >= lo && pos_next < t1;
+    off_lds[wave][lane] = live ? (page_next * p.page_stride + slot_next * p.slot_stride) / 2 : 0;
+    pair_off = live ? page_next * p.pair_page + slot_next * p.pair_slot : 0;
+    return __ballot(live);
+  };
+  uint32_t kr[NT][W], kp[GP], vp[GP];
+  u32x4 vr[W];
+  const auto load_pairs = [&](const uint32_t* base, uint32_t* x) {
+    if (p.groups == GP) {
+#pragma unroll
+      for (int g = 0; g < GP; ++g) x[g] = base[g];
+    } else {  // (the last column's groups are no groups: any pair will do)
+#pragma unroll
+      for (int g = 0; g < GP; ++g) x[g] = base[min(g, p.groups - 1)];
+    }
+  };
+  const auto load_k = [&] {
+    load_pairs(k_pairs + pair_off, kp);
+#pragma unroll
+    for (int blk = 0; blk < NT; ++blk) {
+      const uint8_t* at = kbase + off_lds[wave][16 * blk + row];
+      if constexpr (FULL) {
+        constexpr int kPiece = W == 2 || W == 3 ? 2 : 4;
+#pragma unroll
+        for (int w = 0; w < W; w += kPiece) {
+          const uint32_t* src = reinterpret_cast<const uint32_t*>(at) + dword_of(w);
+#pragma unroll
+          for (int i = w; i < (w + kPiece < W ? w + kPiece : W); ++i) kr[blk][i] = src[i - w];
+        }
+      } else {  // a dword past the head's end meets a zero of Q: the first one is read instead
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const int dw = dword_of(w);
+          kr[blk][w] = reinterpret_cast<const uint32_t*>(at)[dw < nd ? dw : 0];
+        }
+      }
+    }
+  };
+  // V by whole rows, 16 bytes a lane: read once, so it need not stay in the caches.
+  const auto load_v = [&] {
+    load_pairs(v_pairs + pair_off, vp);
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const int piece = 64 * j + lane, c = 4 * (piece % W);
+      const uint32_t* at =
+          reinterpret_cast<const uint32_t*>(vbase + off_lds[wave][piece / W]);
+      if constexpr (FULL) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vr[j][i] = __builtin_nontemporal_load(at + c + i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vr[j][i] = at[c + i < nd ? c + i : 0];
+      }
+    }
+  };
+  // Dword offset of V's row r in LDS: rows 4 qd + e of four blocks, 8 bytes each, that a transposing
+  // read takes together, lie in different banks but for two blocks each.
+  const auto v_row = [](int r) { return r * SD + 2 * (r >> 4 & 1); };
+  // Pairs of the tile in LDS by group; zero where a position is not live, whatever lies there.
+  const auto put_pairs = [&](int which, const uint32_t* x, uint64_t now) {
+    const bool mine = (now >> lane) & 1;
+#pragma unroll
+    for (int g = 0; g < GP; ++g) pair_lds[wave][which][g][lane] = mine ? x[g] : 0u;
+  };
+  const auto pairs_of = [&](int which, int blk) {
+    return *reinterpret_cast<const u32x4*>(&pair_lds[wave][which][my_group][16 * blk + 4 * qd]);
+  };
+
+  uint32_t* const v_lds = reinterpret_cast<uint32_t*>(lds) + wave * kVDwords;
+  const float sc = p.scale;
+  const float sc2 = p.softcap > 0.f ? kLog2e : sc * kLog2e;
+  const float cap = sc / p.softcap;
+  uint64_t live = 0;
+  bool ready = false;  // this part's first tile is requested, and the next one's pages are read
+  Part cur = part_of(rg.b, rg.first, rg.left);
+  load_q(cur.b);
+
+  for (;;) {
+    rg.left -= cur.count;
+    const bool more = p.ranges > 0 && rg.left > 0;
+    Part nxt{};  // (no pages, nothing live)
+    if (more) {
+      int b = cur.b;
+      do {  // (granules are left, so a sequence with some follows)
+        ++b;
+      } while (granules_of<kTile>(p, max(0, min(p.lens[b], p.max_len))) == 0);
+      nxt = part_of(b, 0, rg.left);
+    }
+    const int b = cur.b;
+    float m = -INFINITY, l = 0.f, low_sum = 0.f;
+    f32x4 o[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    // A wave's tiles follow each other from one part to the next, so that the next part's first is
+    // in flight while the waves are joined.
+    int t = cur.t0 + wave * kTile;
+    const int next_t = nxt.t0 + wave * kTile, tiles = t >= cur.t1 ? 0 : t + kStep >= cur.t1 ? 1 : 2;
+    if (!ready) {
+      read_pages(cur.b, cur.t_pages, t);  // (without a tile: the cache's first slot)
+      wave_lds_fence();
+      live = place(cur.lo, cur.t1);
+      wave_lds_fence();
+      const bool here = tiles != 1;
+      read_pages(here ? cur.b : nxt.b, here ? cur.t_pages : nxt.t_pages, here ? t + kStep : next_t);
+      load_k();
+      load_v();
+    }
+    for (; t < cur.t1; t += kStep) {
+      // the codes' products, without the 16 in each operand
+      f32x4 s[NT];
+      const float start = -16.f * q_sum;
+#pragma unroll
+      for (int blk = 0; blk < NT; ++blk) {
+        s[blk] = f32x4{start, start, start, start};
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const bf16x8 c = from_codes(kr[blk][w], pattern);
+          s[blk] = mfma_bf(c, qh[w], s[blk]);
+          if constexpr (!BF16) s[blk] = mfma_bf(c, ql[w], s[blk]);
+        }
+      }
+      const uint64_t now = live;
+      put_pairs(0, kp, now);
+      put_pairs(1, vp, now);
+      // the next tile's K (positions past the range are not live and read the first slot)
+      const bool last = t + kStep >= cur.t1;
+      wave_lds_fence();
+      live = place(last ? nxt.lo : cur.lo, last ? nxt.t1 : cur.t1);
+      wave_lds_fence();
+      const bool here = t + 2 * kStep < cur.t1;
+      read_pages(here ? cur.b : nxt.b, here ? cur.t_pages : nxt.t_pages,
+                 here ? t + 2 * kStep : next_t + (last ? kStep : 0));
+      load_k();
+
+      // scores: this column's group, then all of the head's
+#pragma unroll
+      for (int blk = 0; blk < NT; ++blk) {
+        const u32x4 pr = pairs_of(0, blk);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float scale = A::value((uint16_t)pr[e]), offset = A::value((uint16_t)(pr[e] >> 16));
+          s[blk][e] = group_sum<GP>(__builtin_fmaf(scale, s[blk][e], offset * q_sum));
+        }
+      }
+
+      // running maximum and sum, in base 2
+      float mx = -INFINITY;
+      if (p.softcap > 0.f) {
+#pragma unroll
+        for (int blk = 0; blk < NT; ++blk)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            s[blk][e] = capped(s[blk][e] * sc, s[blk][e] * cap, p.softcap);
+      }
+#pragma unroll
+      for (int blk = 0; blk < NT; ++blk)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[blk][e] *= sc2;
+      if (now != ~0ull) {
+#pragma unroll
+        for (int blk = 0; blk < NT; ++blk)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            s[blk][e] = (now >> (16 * blk + 4 * qd + e)) & 1 ? s[blk][e] : -INFINITY;
+      }
+#pragma unroll
+      for (int blk = 0; blk < NT; ++blk)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx = fmaxf(mx, s[blk][e]);
+      mx = fmaxf(mx, __shfl_xor(mx, 16));
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      const float m_new = fmaxf(m, mx);
+      const float top = m_new == -INFINITY ? 0.f : m_new;  // nothing live so far
+      const float alpha = __builtin_amdgcn_exp2f(m - top);
+      if (__ballot(m_new > m)) {  // some head's maximum moved
+        l *= alpha;
+        low_sum *= alpha;
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][e] *= alpha;
+      }
+      m = m_new;
+
+      // p times the scale of this column's group as two bf16 parts, cut off and rounded; element
+      // 2 e + i of a product's eight is position e of block 2 k + i, as V's codes come
+      bf16x8 ph[NT / 2], pl[NT / 2];
+#pragma unroll
+      for (int k = 0; k < NT / 2; ++k) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const u32x4 pr = pairs_of(1, 2 * k + i);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float scale = A::value((uint16_t)pr[e]);
+            const float offset = A::value((uint16_t)(pr[e] >> 16));
+            const float x = __builtin_amdgcn_exp2f(s[2 * k + i][e] - top);
+            l += x;
+            low_sum = __builtin_fmaf(x, __builtin_fmaf(-16.f, scale, offset), low_sum);
+            const float y = x * scale;
+            const uint32_t high = __builtin_bit_cast(uint32_t, y) & 0xffff0000u;
+            ph[k][2 * e + i] = __builtin_bit_cast(bf16, (uint16_t)(high >> 16));
+            pl[k][2 * e + i] = (bf16)(y - __builtin_bit_cast(float, high));
+          }
+        }
+      }
+
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        const int piece = 64 * j + lane;
+        uint32_t* at = v_lds + v_row(piece / W) + 4 * (piece % W);
+        *reinterpret_cast<u32x2*>(at) = u32x2{vr[j][0], vr[j][1]};
+        *reinterpret_cast<u32x2*>(at + 2) = u32x2{vr[j][2], vr[j][3]};
+      }
+      wave_lds_fence();
+      load_v();
+
+      const uint32_t* src = v_lds + v_row(16 * (row >> 2) + 4 * qd + (row & 3));
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const i32x2 c =
+            __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_i32x2*)(src + 2 * i));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const bf16x8 v = from_codes((uint32_t)c[k], pattern);
+          o[i] = mfma_bf(v, ph[k], o[i]);
+          o[i] = mfma_bf(v, pl[k], o[i]);
+        }
+      }
+      wave_lds_fence();
+    }
+
+    ready = more && tiles > (ready ? 1 : 0);
+    if (more) load_q(nxt.b);
+
+    // Join the waves, in wave order.
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    low_sum += __shfl_xor(low_sum, 16);
+    low_sum += __shfl_xor(low_sum, 32);
+    __syncthreads();  // every wave is done with its V rows
+    float* const o_lds = reinterpret_cast<float*>(lds);
+    if (qd == 0 && my_group == 0) {
+      ml_lds[wave][my_head][0] = m;
+      ml_lds[wave][my_head][1] = l;
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+      if (16 * i / p.group_size == my_group)
+        *reinterpret_cast<f32x4*>(o_lds + (wave * HB + my_head) * OS + 16 * i + 4 * qd) =
+            f32x4{o[i][0] + low_sum, o[i][1] + low_sum, o[i][2] + low_sum, o[i][3] + low_sum};
+    __syncthreads();
+    const int per_row = p.d / 4;
+    for (int i = threadIdx.x; i < rows * per_row; i += kWaves * 64) {
+      const int r = i / per_row, e = 4 * (i - r * per_row);
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) top = fmaxf(top, ml_lds[w][r][0]);
+      const float ref = top == -INFINITY ? 0.f : top;
+      float sum = 0.f;
+      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float f = __builtin_amdgcn_exp2f(ml_lds[w][r][0] - ref);
+        sum = __builtin_fmaf(ml_lds[w][r][1], f, sum);
+        const f32x4 x = *reinterpret_cast<const f32x4*>(o_lds + (w * HB + r) * OS + e);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[c] = __builtin_fmaf(x[c], f, acc[c]);
+      }
+      const int64_t h = (int64_t)b * p.q_heads + h0 + r;
+      if (cur.count < cur.granules) {
+        // a sequence that began in an earlier range leaves the range's first partial, one that
+        // goes on in the next its second
+        const int64_t part = 2 * index + (cur.first == 0);
+        const int64_t at = (part * p.units + unit) * p.part_rows + r;
+        *reinterpret_cast<f32x4*>(p.part_o + at * p.d + e) = acc;
+        if (e == 0) {
+          p.part_ml[at * 2] = top;
+          p.part_ml[at * 2 + 1] = sum;
+        }
+      } else {
+        const float f = sum == 0.f ? 0.f : 1.f / sum;
+        uint16_t* dst = p.out + (int64_t)b * p.ldo + (int64_t)(h0 + r) * p.d + e;
+        *reinterpret_cast<u32x2*>(dst) =
+            u32x2{(uint32_t)A::round(acc[0] * f) | ((uint32_t)A::round(acc[1] * f) << 16),
+                  (uint32_t)A::round(acc[2] * f) | ((uint32_t)A::round(acc[3] * f) << 16)};
+        if (e == 0 && p.lse != nullptr)
+          p.lse[h] = sum == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+      }
+    }
+    if (!more) return;
+    cur = nxt;
+    __syncthreads();  // the joined outputs are no longer read
+  }
+}
+
+template <bool BF16, int W, int GP>
+void launch_attn4_w(const Attn4Args& p, dim3 grid, hipStream_t stream) {
+  const dim3 block(kWaves * 64);
+  if (p.d == 32 * W)
+    hipLaunchKernelGGL((attn4_kernel<BF16, W, GP, true>), grid, block, 0, stream, p);
+  else
+    hipLaunchKernelGGL((attn4_kernel<BF16, W, GP, false>), grid, block, 0, stream, p);
+}
+
+template <bool BF16, int W>
+void launch_attn4_g(const Attn4Args& p, dim3 grid, hipStream_t stream) {
+  if (p.groups == 1) return launch_attn4_w<BF16, W, 1>(p, grid, stream);
+  if (p.groups == 2) return launch_attn4_w<BF16, W, 2>(p, grid, stream);
+  if constexpr (W > 2) {
+    if (p.groups <= 4) return launch_attn4_w<BF16, W, 4>(p, grid, stream);
+  }
+  if constexpr (W > 4) launch_attn4_w<BF16, W, 8>(p, grid, stream);
+}
+
+// The instance for a head_dim: rounded up to 64, 96, 128, 192 and 256.
+template <bool BF16>
+void launch_attn4(const Attn4Args& p, dim3 grid, hipStream_t stream) {
+  if (p.d <= 64) return launch_attn4_g<BF16, 2>(p, grid, stream);
+  if (p.d <= 96) return launch_attn4_g<BF16, 3>(p, grid, stream);
+  if (p.d <= 128) return launch_attn4_g<BF16, 4>(p, grid, stream);
+  if (p.d <= 192) return launch_attn4_g<BF16, 6>(p, grid, stream);
+  launch_attn4_g<BF16, 8>(p, grid, stream);
+}
+
+}  // namespace
+
+AttnPlan attn4_plan(int batch, int q_heads, int kv_heads, int head_dim, int group_size, int max_len,
+                    int window) {
+  AttnPlan plan{};
+  const int groups = head_dim / group_size;
+  plan.block_shift = groups == 1 ? 4 : groups == 2 ? 3 : groups <= 4 ? 2 : 1;
+  const int heads = 1 << plan.block_shift;
+  plan.head_blocks = (q_heads / kv_heads + heads - 1) / heads;
+  plan.units = kv_heads * plan.head_blocks;
+  // positions a sequence may need, from the tile that holds the window's first
+  const long span = window > 0 && window < max_len - kTile ? window + kTile - 1 : max_len;
+  const long keys = span * (head_dim / 2 + 4 * groups);
+  const long whole = std::min(256l, std::max(96l, (long)batch * plan.units)) * 512;
+  if (span > kStep && keys > whole) {
+    const int work_groups = head_dim <= 128 ? 512 : 256;
+    plan.ranges = std::max(1, work_groups / plan.units);
+  }
+  return plan;
+}
+
+hipError_t launch_paged_attention4(const wq_attn4_args& a, const AttnPlan& plan,
+                                   hipStream_t stream) {
+  Attn4Args p{};
+  static_cast<AttnArgs&>(p) = attn_args(a, plan);
+  p.k_pairs = static_cast<const uint32_t*>(a.pairs.k);
+  p.v_pairs = static_cast<const uint32_t*>(a.pairs.v);
+  p.pair_page = a.pairs.page_stride;
+  p.pair_slot = a.pairs.slot_stride;
+  p.pair_head = a.pairs.head_stride;
+  p.group_size = a.pairs.group_size;
+  p.groups = p.d / p.group_size;
+  const bool bf16 = (a.flags & WQ_FLAG_BF16) != 0;
+  // units that read the same rows or share lines, as in the 16-bit kernel
+  p.near_units = plan.head_blocks > 1 ||
+                 (p.kv_heads > 1 && p.head_stride < p.slot_stride && p.head_stride / 2 % 128 != 0);
+  const dim3 grid = attn_grid(p);
+  if (bf16)
+    launch_attn4<true>(p, grid, stream);
+  else
+    launch_attn4<false>(p, grid, stream);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || plan.ranges == 0) return e;
+  return launch_attn_join(p, bf16, stream);
+}
+
+}  // namespace wq

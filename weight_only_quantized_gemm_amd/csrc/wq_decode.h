@@ -19,12 +19,13 @@ hipError_t launch_cache4_read(const wq_cache4_read_args& a, hipStream_t stream);
 
 // How a call's positions are cut: at most `ranges` ranges of equal length over all sequences
 // (0: one range for each sequence), each taken by `units` work-groups, one per KV head and
-// block of 16 of its query heads.  Sequences that no range holds whole leave fp32 partials
+// block of 2^block_shift of its query heads.  Sequences that no range holds whole leave fp32 partials
 // that a second kernel joins.
 struct AttnPlan {
   int ranges;
   int units;
-  int head_blocks;  // blocks of 16 query heads per KV head
+  int head_blocks;  // blocks of query heads per KV head
+  int block_shift;  // 2^block_shift query heads to a block
 };
 AttnPlan attn_plan(int batch, int q_heads, int kv_heads, int head_dim, int max_len, int window,
                    bool kv8);
@@ -32,6 +33,12 @@ size_t attn_workspace_bytes(const AttnPlan& plan, int batch, int q_heads, int kv
                             int head_dim);
 hipError_t launch_paged_attention(const wq_attn_args& a, const AttnPlan& plan,
                                   hipStream_t stream);
+
+
+AttnPlan attn4_plan(int batch, int q_heads, int kv_heads, int head_dim, int group_size, int max_len,
+                    int window);
+hipError_t launch_paged_attention4(const wq_attn4_args& a, const AttnPlan& plan,
+                                   hipStream_t stream);
 
 size_t moe_workspace_bytes(int tokens, int n_expert, int top_k, int hidden, int inter);
 // gpc: scale units per 128 rows of K of each bank (1, 2, 4 or 8).

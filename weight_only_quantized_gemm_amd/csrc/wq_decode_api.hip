@@ -124,6 +124,43 @@ int check_rope(const Args& a) {
   return 0;
 }
 
+bool attention_shape_ok(int batch, int q_heads, int kv_heads, int head_dim, int max_len,
+                        int window) {
+  return batch >= 1 && batch <= kMaxHeads && kv_heads >= 1 && q_heads >= kv_heads &&
+         q_heads <= kMaxHeads && q_heads % kv_heads == 0 && head_dim >= 16 && head_dim <= 256 &&
+         head_dim % 8 == 0 && max_len >= 1 && max_len <= (1 << 30) && window >= 0;
+}
+
+// Work-groups of one launch; steps of 128 positions over all sequences, counted in 32 bits.
+bool attention_too_large(const wq::AttnPlan& plan, int batch, int max_len, int window) {
+  const int64_t steps = (window > 0 ? std::min(window, max_len) : max_len) / 128 + 2;
+  return (int64_t)(plan.ranges > 0 ? plan.ranges : batch) * plan.units > (1 << 23) ||
+         batch * steps > (1 << 30);
+}
+
+// What the attention calls ask of the arguments that they share, the cache and shape checked.
+template <class Args>
+int check_attention(const Args& a, size_t need) {
+  const int64_t row = (int64_t)a.q_heads * a.cache.head_dim;
+  if (!row_stride_ok(a.ldq, row) || !row_stride_ok(a.ldo, row) || a.table_stride < 1 ||
+      (int64_t)a.table_stride * a.cache.page_size < a.max_len ||
+      (a.keep != nullptr && a.keep_stride < a.max_len))
+    return shape_error();
+  // a scale or cap that is no number would make every output one
+  if (!(a.scale - a.scale == 0.f) || !(a.softcap >= 0.f && a.softcap - a.softcap == 0.f))
+    return shape_error();
+  int st;
+  if ((st = check_ptr(a.q, 16)) || (st = check_ptr(a.out, 16)) || (st = check_optional(a.lse, 4)) ||
+      (st = check_ptr(a.block_table, 4)) || (st = check_ptr(a.lens, 4)))
+    return st;
+  if (need > 0) {
+    if (a.workspace == nullptr || a.workspace_bytes < need)
+      return fail(WQ_STAGE_ARGS, WQ_ERR_WORKSPACE);
+    if (!aligned(a.workspace, 16)) return fail(WQ_STAGE_ARGS, WQ_ERR_ALIGN);
+  }
+  return 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -190,17 +227,11 @@ int wq_paged_attention_workspace_bytes(int batch, int q_heads, int kv_heads, int
                                        size_t* bytes_out) {
   if (bytes_out == nullptr) return fail(WQ_STAGE_ARGS, WQ_ERR_NULL);
   if (flags & ~(uint32_t)(WQ_FLAG_BF16 | WQ_FLAG_FP8)) return flags_error();
-  if (batch < 1 || batch > kMaxHeads || kv_heads < 1 || q_heads < kv_heads ||
-      q_heads > kMaxHeads || q_heads % kv_heads != 0 || head_dim < 16 || head_dim > 256 ||
-      head_dim % 8 != 0 || max_len < 1 || max_len > (1 << 30) || window < 0)
+  if (!attention_shape_ok(batch, q_heads, kv_heads, head_dim, max_len, window))
     return shape_error();
   const wq::AttnPlan plan = wq::attn_plan(batch, q_heads, kv_heads, head_dim, max_len, window,
                                           (flags & WQ_FLAG_FP8) != 0);
-  // work-groups of one launch; steps of 128 positions over all sequences, counted in 32 bits
-  const int64_t steps = (window > 0 ? std::min(window, max_len) : max_len) / 128 + 2;
-  if ((int64_t)(plan.ranges > 0 ? plan.ranges : batch) * plan.units > (1 << 23) ||
-      batch * steps > (1 << 30))
-    return fail(WQ_STAGE_SHAPE, WQ_ERR_OVERFLOW);
+  if (attention_too_large(plan, batch, max_len, window)) return fail(WQ_STAGE_SHAPE, WQ_ERR_OVERFLOW);
   *bytes_out = wq::attn_workspace_bytes(plan, batch, q_heads, kv_heads, head_dim);
   return 0;
 }
@@ -214,27 +245,43 @@ int wq_paged_attention(const wq_attn_args* args) {
   size_t need = 0;
   if ((st = wq_paged_attention_workspace_bytes(a.batch, a.q_heads, a.cache.kv_heads,
                                                a.cache.head_dim, a.max_len, a.window, a.flags,
-                                               &need)))
+                                               &need)) ||
+      (st = check_attention(a, need)))
     return st;
-  const int64_t row = (int64_t)a.q_heads * a.cache.head_dim;
-  if (!row_stride_ok(a.ldq, row) || !row_stride_ok(a.ldo, row) || a.table_stride < 1 ||
-      (int64_t)a.table_stride * a.cache.page_size < a.max_len ||
-      (a.keep != nullptr && a.keep_stride < a.max_len))
-    return shape_error();
-  // a scale or cap that is no number would make every output one
-  if (!(a.scale - a.scale == 0.f) || !(a.softcap >= 0.f && a.softcap - a.softcap == 0.f))
-    return shape_error();
-  if ((st = check_ptr(a.q, 16)) || (st = check_ptr(a.out, 16)) || (st = check_optional(a.lse, 4)) ||
-      (st = check_ptr(a.block_table, 4)) || (st = check_ptr(a.lens, 4)))
-    return st;
-  if (need > 0) {
-    if (a.workspace == nullptr || a.workspace_bytes < need)
-      return fail(WQ_STAGE_ARGS, WQ_ERR_WORKSPACE);
-    if (!aligned(a.workspace, 16)) return fail(WQ_STAGE_ARGS, WQ_ERR_ALIGN);
-  }
   const wq::AttnPlan plan = wq::attn_plan(a.batch, a.q_heads, a.cache.kv_heads, a.cache.head_dim,
                                           a.max_len, a.window, (a.flags & WQ_FLAG_FP8) != 0);
   return launched(wq::launch_paged_attention(a, plan, as_stream(a.stream)));
+}
+
+int wq_paged_attention4_workspace_bytes(int batch, int q_heads, int kv_heads, int head_dim,
+                                        int group_size, int max_len, int window,
+                                        size_t* bytes_out) {
+  if (bytes_out == nullptr) return fail(WQ_STAGE_ARGS, WQ_ERR_NULL);
+  if (!attention_shape_ok(batch, q_heads, kv_heads, head_dim, max_len, window) ||
+      !group_ok(group_size, head_dim))
+    return shape_error();
+  const wq::AttnPlan plan =
+      wq::attn4_plan(batch, q_heads, kv_heads, head_dim, group_size, max_len, window);
+  if (attention_too_large(plan, batch, max_len, window)) return fail(WQ_STAGE_SHAPE, WQ_ERR_OVERFLOW);
+  *bytes_out = wq::attn_workspace_bytes(plan, batch, q_heads, kv_heads, head_dim);
+  return 0;
+}
+
+int wq_paged_attention4(const wq_attn4_args* args) {
+  int st = check_abi(args);
+  if (st) return st;
+  const wq_attn4_args& a = *args;
+  if (a.flags & ~(uint32_t)WQ_FLAG_BF16) return flags_error();
+  if ((st = check_cache(a.cache, a.flags)) || (st = check_pairs(a.cache, a.pairs))) return st;
+  size_t need = 0;
+  if ((st = wq_paged_attention4_workspace_bytes(a.batch, a.q_heads, a.cache.kv_heads,
+                                                a.cache.head_dim, a.pairs.group_size, a.max_len,
+                                                a.window, &need)) ||
+      (st = check_attention(a, need)))
+    return st;
+  const wq::AttnPlan plan = wq::attn4_plan(a.batch, a.q_heads, a.cache.kv_heads, a.cache.head_dim,
+                                           a.pairs.group_size, a.max_len, a.window);
+  return launched(wq::launch_paged_attention4(a, plan, as_stream(a.stream)));
 }
 
 int wq_moe_layer_workspace_bytes(int tokens, int n_expert, int top_k, int hidden, int inter,

@@ -25,10 +25,11 @@ import struct
 import torch
 
 from . import (WQ_ABI_VERSION, WQ_FLAG_BF16, WQ_FLAG_FP8, WQ_FLAG_HAS_ZP, WQ_FLAG_KV4,
-               WQ_MAX_ROPE_AXES, WQ_MOE_MAX_TOKENS, _check, lib, wq_attn_args,
-               wq_cache4_read_args, wq_expert_bank, wq_kv_cache, wq_kv_pairs, wq_moe_args,
+               WQ_MAX_ROPE_AXES, WQ_MOE_MAX_TOKENS, _check, lib, wq_attn4_args,
+               wq_attn_args, wq_cache4_read_args, wq_expert_bank, wq_kv_cache, wq_kv_pairs, wq_moe_args,
                wq_moe_layer_workspace_bytes, wq_norm_args, wq_norm_rope_args,
-               wq_paged_attention_workspace_bytes, wq_rope_args)
+               wq_paged_attention4_workspace_bytes, wq_paged_attention_workspace_bytes,
+               wq_rope_args)
 
 _TYPE_FLAGS = {torch.float16: 0, torch.bfloat16: WQ_FLAG_BF16}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -52,6 +53,7 @@ _NORM_ROPE = _layout(wq_norm_rope_args,
                      _CACHE + _PAIRS + "10P8i" + f"{WQ_MAX_ROPE_AXES}iifIi")
 _READ4 = _layout(wq_cache4_read_args, _CACHE + _PAIRS + "4P3iIi")
 _ATTN = _layout(wq_attn_args, _CACHE + "7PNP7iffiIi")
+_ATTN4 = _layout(wq_attn4_args, _CACHE + _PAIRS + "7PNP7iffiIi")
 _MOE = _layout(wq_moe_args, "2P" + 2 * _BANK + "5PNP8ifiIi")
 
 
@@ -96,7 +98,8 @@ class _Call:
 
 _norm_call, _rope_call = _Call("wq_add_rms_norm"), _Call("wq_rope_append")
 _norm_rope_call, _read4_call = _Call("wq_norm_rope_append"), _Call("wq_cache4_read")
-_attn_call, _moe_call = _Call("wq_paged_attention"), _Call("wq_moe_layer")
+_attn_call, _attn4_call = _Call("wq_paged_attention"), _Call("wq_paged_attention4")
+_moe_call = _Call("wq_moe_layer")
 
 
 def _type_flag(dtype: torch.dtype) -> int:
@@ -381,24 +384,33 @@ def rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
 
 class PagedAttention:
     """Attention of one new token for `batch` sequences of up to `max_len` positions over a
-    paged cache: the plan of a call and its workspace.  window: only the last that many
+    paged cache of any kind: the plan of a call and its workspace.  window: only the last that many
     positions; softcap: scores become softcap * tanh(score / softcap); scale: 1/sqrt(head_dim)
     by default.  One of its calls must not overlap another on a different stream."""
 
-    def __init__(self, cache: PagedCache, batch: int, q_heads: int, max_len: int, *,
+    def __init__(self, cache: PagedCache | PagedCache4, batch: int, q_heads: int, max_len: int, *,
                  dtype: torch.dtype, scale: float | None = None, window: int = 0,
                  softcap: float = 0.0):
         self.cache, self.batch, self.q_heads, self.max_len = cache, batch, q_heads, max_len
         self.dtype, self.device = dtype, cache.device
-        nbytes = wq_paged_attention_workspace_bytes(batch, q_heads, cache.kv_heads,
-                                                    cache.head_dim, max_len, window,
-                                                    cache.flags(dtype))
+        flags = cache.flags(dtype)
+        if flags & WQ_FLAG_KV4:
+            nbytes = wq_paged_attention4_workspace_bytes(batch, q_heads, cache.kv_heads,
+                                                         cache.head_dim, cache.group, max_len,
+                                                         window)
+            self._call, self._layout = _attn4_call, _ATTN4
+            self._cache = (cache.packed, cache.packed_pairs)
+            flags &= WQ_FLAG_BF16
+        else:
+            nbytes = wq_paged_attention_workspace_bytes(batch, q_heads, cache.kv_heads,
+                                                        cache.head_dim, max_len, window, flags)
+            self._call, self._layout, self._cache = _attn_call, _ATTN, (cache.packed,)
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         self._space = (self.workspace.data_ptr(), nbytes)
         self._lse = torch.empty((batch, q_heads), dtype=torch.float32, device=self.device)
         self._memory = _PlanMemory(cache.dev, self.workspace)
         scale = 1.0 / math.sqrt(cache.head_dim) if scale is None else scale
-        self._last = (scale, softcap, window, cache.flags(dtype), 0)
+        self._last = (scale, softcap, window, flags, 0)
 
     def __call__(self, q: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor, *,
                  keep: torch.Tensor | None = None, out: torch.Tensor | None = None,
@@ -427,10 +439,11 @@ class PagedAttention:
                 lp = lse.data_ptr()
             else:
                 lp = _dense(lse, "lse", torch.float32, dev, (b, heads))
-        _attn_call(_ATTN.pack(WQ_ABI_VERSION, _ATTN.size, cache.packed, q.data_ptr(),
-                              out.data_ptr(), lp, table, n, kp, *self._space,
-                              self._memory.stream(dev), b, heads, self.max_len, pages,
-                              keep_stride, ldq, ldo, *self._last))
+        layout = self._layout
+        self._call(layout.pack(WQ_ABI_VERSION, layout.size, *self._cache, q.data_ptr(),
+                               out.data_ptr(), lp, table, n, kp, *self._space,
+                               self._memory.stream(dev), b, heads, self.max_len, pages,
+                               keep_stride, ldq, ldo, *self._last))
         return out if lse is False else (out, lse)
 
 

@@ -673,6 +673,50 @@ int wq_paged_attention4_workspace_bytes(int batch, int q_heads, int kv_heads, in
  */
 int wq_paged_attention4(const wq_attn4_args* args);
 
+/* wq_sample only: fp32 logits. */
+#define WQ_FLAG_FP32        (1u << 11)
+
+#define WQ_SAMPLE_MAX_VOCAB (1 << 19)
+typedef struct wq_sample_args {
+  uint32_t abi_version;     /* WQ_ABI_VERSION                                          */
+  uint32_t struct_size;     /* sizeof(wq_sample_args)                                  */
+  const void* logits;       /* device [rows][ld], aligned to its type                    */
+  const float* u;           /* device [rows]: a random number in [0, 1) for each row      */
+  const float* temperature; /* device [rows], or NULL: 1; 0 (and whatever is not above 0):
+                               the largest logit                                       */
+  const int32_t* top_k;     /* device [rows], or NULL; below 1: all                      */
+  const float* top_p;       /* device [rows], or NULL; 1 and more, and NaN: all            */
+  const float* min_p;       /* device [rows], or NULL; 0 and less, and NaN: all            */
+  int32_t* ids;             /* device [rows]: the chosen tokens                          */
+  float* logprob;           /* device [rows], or NULL                                    */
+  void* workspace;          /* device, 16-byte aligned; wq_sample_workspace_bytes         */
+  size_t workspace_bytes;
+  void* stream;
+  int32_t rows, vocab;      /* rows 1 to 65535; vocab 1 to WQ_SAMPLE_MAX_VOCAB            */
+  int64_t ld;               /* row stride in elements, >= vocab                         */
+  uint32_t flags;           /* WQ_FLAG_BF16 or WQ_FLAG_FP32; 0: fp16                     */
+  int32_t reserved;
+} wq_sample_args;
+
+/* Workspace bytes of wq_sample (0 where it needs none).  Contents need no initialization; calls
+ * that share one must not run concurrently. */
+int wq_sample_workspace_bytes(int rows, int vocab, uint32_t flags, size_t* bytes_out);
+
+/*
+ * The next token of each row by its logits z, settings and random number.  With tokens in order of
+ * their logits (equal ones: lowest first) and p_i = exp((z_i - max z) / temperature):
+ *   - top_k leaves the first k tokens;
+ *   - top_p, of these, the shortest run from the first whose p sum to at least top_p of their sum;
+ *   - min_p, of these, the ones with p_i >= min_p, and the first one in any case.
+ * The id is the first token (by number) at which the sum of p over the kept ones up to it passes
+ * u times the sum over all of them; logprob is the log of its share of that sum.  Sums are those of
+ * p in steps of 2^-44, so results do not depend on an order of addition.  Rows without a
+ * temperature above 0 give their largest logit (the lowest token among equals) and logprob 0.  A
+ * row that holds a NaN, or nothing above -inf, gives -1 and NaN; beside a logit of +inf others
+ * count for nothing.  u is taken into [0, 1).
+ */
+int wq_sample(const wq_sample_args* args);
+
 #ifdef __cplusplus
 }
 #endif

@@ -165,3 +165,41 @@ def check_quantized4(x, err, codes, pairs, half_step, tiny):
     room = scale * (0.5 + 64 * E32) + err + (np.abs(x) + np.abs(offset)) * 2 * E32
     fine = (np.abs(off) <= room) | ((code == 0) & (off < 0)) | ((code == 15) & (off > 0))
     assert (fine | (scale == 0)).all() and (code[np.broadcast_to(scale == 0, code.shape)] == 0).all()
+
+
+def sample(z, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """The token of one row of logits (64 bits), the log of its share, whether the token is certain,
+    and how far the share may be off, relative to itself.
+
+    n values of p, each off by half a step of 2^-44, make sums that are off by n 2^-45 of the largest p
+    at worst, which the whole holds at least once; a share of the whole is off by twice that, and
+    2^-40 is left for p's own error and that of the sums here."""
+    n = len(z)
+    eps = n * 2.0 ** -44 + 2.0 ** -40
+    if np.isnan(z).any() or z.max() == -np.inf:
+        return -1, np.nan, True, 0.0
+    order = np.lexsort((np.arange(n), -z))
+    if not temperature > 0:
+        return int(order[0]), 0.0, True, 0.0
+    with np.errstate(invalid="ignore", over="ignore"):
+        x = np.where(z == z.max(), 0.0, (z - z.max()) / temperature)
+    x[z == -np.inf] = -np.inf
+    p = np.exp(x)
+    keep, slack = order, 8 * eps * p.sum()
+    if 0 < top_k < n:
+        keep = keep[:top_k]
+    if top_p < 1:
+        upto = np.cumsum(p[keep])
+        want, off = max(top_p, 0.0) * upto[-1], eps * upto[-1] if top_p > 0 else 0.0
+        low, count, high = (min(int(np.searchsorted(upto, w)) + 1, len(keep))
+                            for w in (want - off, want, want + off))
+        slack += upto[high - 1] - upto[low - 1]  # tokens that may stay or not
+        keep = keep[:count]
+    if min_p > 0:
+        keep = keep[(p[keep] >= min_p) | (z[keep] == z.max())]
+    keep = np.sort(keep[p[keep] > 0])
+    upto = np.cumsum(p[keep])
+    want = min(max(u, 0.0), 1 - 2.0 ** -53) * upto[-1]
+    i = min(int(np.searchsorted(upto, want, side="right")), len(keep) - 1)
+    certain = len(keep) == 1 or np.abs(upto[:-1] - want).min() > slack
+    return int(keep[i]), float(x[keep[i]] - np.log(upto[-1])), bool(certain), slack / upto[-1]

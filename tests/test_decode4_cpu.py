@@ -115,11 +115,52 @@ def test_attention4_workspace():
             f(*bad)
 
 
+def sample_args():
+    return wq.versioned(wq.wq_sample_args, logits=P, u=2 * P, temperature=3 * P, top_k=4 * P,
+                        top_p=5 * P, min_p=6 * P, ids=7 * P, logprob=8 * P, workspace=9 * P,
+                        workspace_bytes=1 << 40, rows=3, vocab=50001, ld=50001)
+
+
+@pytest.mark.parametrize("changes,want", [
+    (dict(rows=0), BAD), (dict(rows=65536), BAD), (dict(vocab=0), BAD),
+    (dict(vocab=(1 << 19) + 1, ld=1 << 20), BAD), (dict(ld=50000), BAD), (dict(ld=-1), BAD),
+    (dict(ld=1 << 60), OVER), (dict(logits=None), NULL), (dict(u=None), NULL), (dict(ids=None), NULL),
+    (dict(logits=P + 1), ALIGN), (dict(logits=P + 2, flags=wq.WQ_FLAG_FP32), ALIGN),
+    (dict(u=P + 2), ALIGN), (dict(temperature=P + 1), ALIGN), (dict(top_k=P + 2), ALIGN),
+    (dict(top_p=P + 2), ALIGN), (dict(min_p=P + 1), ALIGN), (dict(ids=P + 2), ALIGN),
+    (dict(logprob=P + 2), ALIGN), (dict(flags=FP8), FLAGS),
+    (dict(flags=wq.WQ_FLAG_FP32 | wq.WQ_FLAG_BF16), FLAGS), (dict(abi_version=2), ABI),
+    (dict(struct_size=8), ABI), (dict(reserved=1), ABI),
+])
+def test_sample_refusals(changes, want):
+    refused(wq.wq_sample, sample_args(), changes, want)
+
+
+def test_sampler_refuses_before_the_library():
+    plan = decode.Sampler(4, 100, dtype=torch.float16, device="cpu")
+    z, u = torch.zeros((4, 100), dtype=torch.float16), torch.zeros(4)
+    with pytest.raises(TypeError):
+        decode.Sampler(4, 100, dtype=torch.float64, device="cpu")
+    with pytest.raises(wq.WQError):
+        decode.Sampler(4, (1 << 19) + 1, device="cpu")
+    for args, kw in (((z[:, :99], u), {}), ((torch.cat([z, z]), u), {}), ((z[:0], u[:0]), {}),
+                     ((z, u[:3]), {}), ((z, u), dict(top_p=u[:2])),
+                     ((torch.zeros((4, 200), dtype=torch.float16)[:, ::2], u), {})):
+        with pytest.raises(ValueError):
+            plan(*args, **kw)
+    for args, kw in (((z.float(), u), {}), ((z, u.double()), {}), ((z, u), dict(top_k=u)),
+                     ((z, u), dict(temperature=u.half())), ((z, u), dict(ids=u.long())),
+                     ((z, u), dict(logprob=u.half()))):
+        with pytest.raises(TypeError):
+            plan(*args, **kw)
+
+
 def test_null_structs_and_sizes():
     L = wq.lib()
     for name, cls in (("wq_norm_rope_append", wq.wq_norm_rope_args),
                       ("wq_cache4_read", wq.wq_cache4_read_args),
-                      ("wq_paged_attention4", wq.wq_attn4_args)):
+                      ("wq_paged_attention4", wq.wq_attn4_args),
+                      ("wq_sample", wq.wq_sample_args)):
         assert getattr(L, name)(None) == (wq.WQ_STAGE_ARGS << 16) | wq.WQ_ERR_NULL
         with pytest.raises(wq.WQError) as e:  # the binding's size passes, later checks fail
             getattr(wq, name)(wq.versioned(cls))
@@ -202,3 +243,27 @@ def test_reference_codes_and_their_check():
         with pytest.raises(AssertionError):
             ref.check_quantized4(x, 0.0, np.array(codes, dtype=np.uint8), np.array(pair),
                                  2.0 ** -11, 0.0)
+
+
+def test_reference_sampling_against_its_steps():
+    g = np.random.default_rng(4)
+    z = g.normal(size=40) * 2
+    p = np.exp(z - z.max())
+    order = np.argsort(-z)
+    for u in g.random(20):
+        full = np.cumsum(p / p.sum())
+        assert ref.sample(z, u)[0] == int((full <= u).sum())
+        top = np.sort(order[:5])
+        share = np.cumsum(p[top] / p[top].sum())
+        got, logp, _, _ = ref.sample(z, u, top_k=5)
+        assert got == top[int((share <= u).sum())] and np.isclose(logp, np.log(p[got] / p[top].sum()))
+    # the shortest run that holds half
+    run = 1 + int((np.cumsum(p[order]) < 0.5 * p.sum()).sum())
+    seen = {ref.sample(z, u, top_p=0.5)[0] for u in np.linspace(0, 0.9999, 4000)}
+    assert seen == set(order[:run].tolist())
+    seen = {ref.sample(z, u, min_p=0.2, temperature=2.0)[0] for u in np.linspace(0, 0.9999, 4000)}
+    assert seen == set(np.flatnonzero(np.exp((z - z.max()) / 2) >= 0.2).tolist())
+    assert ref.sample(z, 0.7, temperature=0.0)[:2] == (order[0], 0.0)
+    assert ref.sample(np.array([0.0, np.nan]), 0.5)[0] == -1
+    assert ref.sample(np.full(3, -np.inf), 0.5)[0] == -1
+    assert ref.sample(np.array([1.0, np.inf, 2.0]), 0.99)[0] == 1

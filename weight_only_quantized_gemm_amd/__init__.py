@@ -27,6 +27,7 @@ WQ_FLAG_SWIGLU = 1 << 7
 WQ_FLAG_BF16 = 1 << 8
 WQ_FLAG_FP8 = 1 << 9
 WQ_FLAG_KV4 = 1 << 10
+WQ_FLAG_FP32 = 1 << 11
 
 WQ_STAGE_ARGS, WQ_STAGE_SHAPE, WQ_STAGE_DEVICE = 1, 2, 3
 WQ_STAGE_LAUNCH_CONFIG, WQ_STAGE_FUNC_ATTR, WQ_STAGE_LAUNCH = 4, 5, 6
@@ -43,10 +44,12 @@ EXPORTED = (
     "wq_paged_attention_workspace_bytes", "wq_paged_attention",
     "wq_moe_layer_workspace_bytes", "wq_moe_layer", "wq_norm_rope_append", "wq_cache4_read",
     "wq_paged_attention4_workspace_bytes", "wq_paged_attention4",
+    "wq_sample_workspace_bytes", "wq_sample",
 )
 WQ_NOALLOC_SCRATCH_BYTES = 32 << 20
 
 WQ_MAX_ROPE_AXES = 4
+WQ_SAMPLE_MAX_VOCAB = 1 << 19
 WQ_MOE_MAX_TOKENS, WQ_MOE_MAX_EXPERTS, WQ_MOE_MAX_TOPK = 16, 256, 16
 
 WQ_KERNEL_SMALL_M, WQ_KERNEL_TILE_256, WQ_KERNEL_TILE_128 = 1, 2, 3
@@ -194,6 +197,18 @@ class wq_attn4_args(ctypes.Structure):
     ]
 
 
+class wq_sample_args(ctypes.Structure):
+    _fields_ = [
+        ("abi_version", ctypes.c_uint32), ("struct_size", ctypes.c_uint32),
+        ("logits", ctypes.c_void_p), ("u", ctypes.c_void_p), ("temperature", ctypes.c_void_p),
+        ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p), ("min_p", ctypes.c_void_p),
+        ("ids", ctypes.c_void_p), ("logprob", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t), ("stream", ctypes.c_void_p),
+        ("rows", ctypes.c_int32), ("vocab", ctypes.c_int32), ("ld", ctypes.c_int64),
+        ("flags", ctypes.c_uint32), ("reserved", ctypes.c_int32),
+    ]
+
+
 class wq_expert_bank(ctypes.Structure):
     _fields_ = [
         ("b", ctypes.c_void_p), ("s", ctypes.c_void_p), ("zp", ctypes.c_void_p),
@@ -268,6 +283,8 @@ def lib() -> ctypes.CDLL:
             "wq_cache4_read": (ctypes.c_int, [vp]),
             "wq_paged_attention4_workspace_bytes": (ctypes.c_int, [i32] * 7 + [ctypes.POINTER(sz)]),
             "wq_paged_attention4": (ctypes.c_int, [vp]),
+            "wq_sample_workspace_bytes": (ctypes.c_int, [i32, i32, u32, ctypes.POINTER(sz)]),
+            "wq_sample": (ctypes.c_int, [vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -524,6 +541,16 @@ def wq_paged_attention4_workspace_bytes(batch: int, q_heads: int, kv_heads: int,
 
 def wq_paged_attention4(args: wq_attn4_args) -> None:
     _check(lib().wq_paged_attention4(ctypes.byref(args)))
+
+
+def wq_sample_workspace_bytes(rows: int, vocab: int, flags: int = 0) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().wq_sample_workspace_bytes(rows, vocab, flags, ctypes.byref(out)))
+    return int(out.value)
+
+
+def wq_sample(args: wq_sample_args) -> None:
+    _check(lib().wq_sample(ctypes.byref(args)))
 
 
 def wq_moe_layer_workspace_bytes(tokens: int, n_expert: int, top_k: int, hidden: int,

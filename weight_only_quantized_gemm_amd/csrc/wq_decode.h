@@ -40,6 +40,9 @@ AttnPlan attn4_plan(int batch, int q_heads, int kv_heads, int head_dim, int grou
 hipError_t launch_paged_attention4(const wq_attn4_args& a, const AttnPlan& plan,
                                    hipStream_t stream);
 
+size_t sample_workspace_bytes(int rows, int vocab, uint32_t flags);
+hipError_t launch_sample(const wq_sample_args& a, hipStream_t stream);
+
 size_t moe_workspace_bytes(int tokens, int n_expert, int top_k, int hidden, int inter);
 // gpc: scale units per 128 rows of K of each bank (1, 2, 4 or 8).
 hipError_t launch_moe_layer(const wq_moe_args& a, int gate_up_gpc, int down_gpc,

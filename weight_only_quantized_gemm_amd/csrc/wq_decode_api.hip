@@ -284,6 +284,36 @@ int wq_paged_attention4(const wq_attn4_args* args) {
   return launched(wq::launch_paged_attention4(a, plan, as_stream(a.stream)));
 }
 
+int wq_sample_workspace_bytes(int rows, int vocab, uint32_t flags, size_t* bytes_out) {
+  if (bytes_out == nullptr) return fail(WQ_STAGE_ARGS, WQ_ERR_NULL);
+  if (flags != 0 && flags != WQ_FLAG_BF16 && flags != WQ_FLAG_FP32) return flags_error();
+  if (rows < 1 || rows > kMaxHeads || vocab < 1 || vocab > WQ_SAMPLE_MAX_VOCAB) return shape_error();
+  *bytes_out = wq::sample_workspace_bytes(rows, vocab, flags);
+  return 0;
+}
+
+int wq_sample(const wq_sample_args* args) {
+  int st = check_abi(args);
+  if (st) return st;
+  const wq_sample_args& a = *args;
+  size_t need = 0;
+  if ((st = wq_sample_workspace_bytes(a.rows, a.vocab, a.flags, &need))) return st;
+  if (a.ld < a.vocab) return shape_error();
+  if (a.ld > std::numeric_limits<int64_t>::max() / 8 / a.rows)
+    return fail(WQ_STAGE_SHAPE, WQ_ERR_OVERFLOW);
+  if ((st = check_ptr(a.logits, (a.flags & WQ_FLAG_FP32) ? 4 : 2)) || (st = check_ptr(a.u, 4)) ||
+      (st = check_ptr(a.ids, 4)) || (st = check_optional(a.temperature, 4)) ||
+      (st = check_optional(a.top_k, 4)) || (st = check_optional(a.top_p, 4)) ||
+      (st = check_optional(a.min_p, 4)) || (st = check_optional(a.logprob, 4)))
+    return st;
+  if (need > 0) {
+    if (a.workspace == nullptr || a.workspace_bytes < need)
+      return fail(WQ_STAGE_ARGS, WQ_ERR_WORKSPACE);
+    if (!aligned(a.workspace, 16)) return fail(WQ_STAGE_ARGS, WQ_ERR_ALIGN);
+  }
+  return launched(wq::launch_sample(a, as_stream(a.stream)));
+}
+
 int wq_moe_layer_workspace_bytes(int tokens, int n_expert, int top_k, int hidden, int inter,
                                  size_t* bytes_out) {
   if (bytes_out == nullptr) return fail(WQ_STAGE_ARGS, WQ_ERR_NULL);

@@ -1,12 +1,12 @@
 """The decode step around the quantized products, on PyTorch tensors.
 
 RMS norm with the residual add, rotary positions (and norms of the query and key heads) with the
-write to a paged cache of 16, 8 or 4 bits, attention of one new token over that cache, and the
-mixture-of-experts layer of a few tokens.  PyTorch only
+write to a paged cache of 16, 8 or 4 bits, attention of one new token over that cache, the
+mixture-of-experts layer of a few tokens, and the choice of the next token.  PyTorch only
 allocates device buffers and supplies the stream; every operation is a libwq kernel.
 
 Calls run on the current stream of their tensors' device, enqueue and return; none
-synchronizes, so all of them may be captured into a graph.  A plan (PagedAttention, MoELayer)
+synchronizes, so all of them may be captured into a graph.  A plan (PagedAttention, MoELayer, Sampler)
 owns a workspace: its calls must not overlap on different streams.  Tensors that a call is given
 follow PyTorch's rules for streams other than their own; a plan's own memory is not reused before
 the calls made on any stream are done.
@@ -24,12 +24,12 @@ import struct
 
 import torch
 
-from . import (WQ_ABI_VERSION, WQ_FLAG_BF16, WQ_FLAG_FP8, WQ_FLAG_HAS_ZP, WQ_FLAG_KV4,
-               WQ_MAX_ROPE_AXES, WQ_MOE_MAX_TOKENS, _check, lib, wq_attn4_args,
+from . import (WQ_ABI_VERSION, WQ_FLAG_BF16, WQ_FLAG_FP8, WQ_FLAG_FP32, WQ_FLAG_HAS_ZP,
+               WQ_FLAG_KV4, WQ_MAX_ROPE_AXES, WQ_MOE_MAX_TOKENS, _check, lib, wq_attn4_args,
                wq_attn_args, wq_cache4_read_args, wq_expert_bank, wq_kv_cache, wq_kv_pairs, wq_moe_args,
                wq_moe_layer_workspace_bytes, wq_norm_args, wq_norm_rope_args,
                wq_paged_attention4_workspace_bytes, wq_paged_attention_workspace_bytes,
-               wq_rope_args)
+               wq_rope_args, wq_sample_args, wq_sample_workspace_bytes)
 
 _TYPE_FLAGS = {torch.float16: 0, torch.bfloat16: WQ_FLAG_BF16}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -54,6 +54,7 @@ _NORM_ROPE = _layout(wq_norm_rope_args,
 _READ4 = _layout(wq_cache4_read_args, _CACHE + _PAIRS + "4P3iIi")
 _ATTN = _layout(wq_attn_args, _CACHE + "7PNP7iffiIi")
 _ATTN4 = _layout(wq_attn4_args, _CACHE + _PAIRS + "7PNP7iffiIi")
+_SAMPLE = _layout(wq_sample_args, "9PNP2iqIi")
 _MOE = _layout(wq_moe_args, "2P" + 2 * _BANK + "5PNP8ifiIi")
 
 
@@ -99,7 +100,7 @@ class _Call:
 _norm_call, _rope_call = _Call("wq_add_rms_norm"), _Call("wq_rope_append")
 _norm_rope_call, _read4_call = _Call("wq_norm_rope_append"), _Call("wq_cache4_read")
 _attn_call, _attn4_call = _Call("wq_paged_attention"), _Call("wq_paged_attention4")
-_moe_call = _Call("wq_moe_layer")
+_moe_call, _sample_call = _Call("wq_moe_layer"), _Call("wq_sample")
 
 
 def _type_flag(dtype: torch.dtype) -> int:
@@ -513,3 +514,54 @@ class MoELayer:
                             self.n_expert, self.top_k, hidden, self.inter, ldx, ldr, ldy,
                             *self._last))
         return out
+
+
+class Sampler:
+    """The choice of the next token from logits of up to `rows` rows over `vocab` tokens (fp16,
+    bf16 or fp32): the plan of a call and its workspace.  One of its calls must not overlap another
+    on a different stream."""
+
+    def __init__(self, rows: int, vocab: int, *, dtype: torch.dtype = torch.float32,
+                 device="cuda"):
+        self.rows, self.vocab, self.dtype = rows, vocab, dtype
+        self.flags = WQ_FLAG_FP32 if dtype is torch.float32 else _type_flag(dtype)
+        nbytes = wq_sample_workspace_bytes(rows, vocab, self.flags)
+        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.device, self.dev = self.workspace.device, self.workspace.get_device()
+        self._space = (self.workspace.data_ptr(), nbytes)
+        self._memory = _PlanMemory(self.dev, self.workspace)
+
+    def __call__(self, logits: torch.Tensor, u: torch.Tensor, *,
+                 temperature: torch.Tensor | None = None, top_k: torch.Tensor | None = None,
+                 top_p: torch.Tensor | None = None, min_p: torch.Tensor | None = None,
+                 ids: torch.Tensor | None = None, logprob: bool | torch.Tensor = False):
+        """The int32 token of each row of logits [rows][vocab] by the random numbers u [rows] in
+        [0, 1).  Each setting is a tensor [rows] (fp32; top_k int32): probabilities are those of
+        logits / temperature (0: the largest logit); top_k keeps the k largest (0: all), top_p of
+        these the fewest that hold that share (1: all), min_p of these the ones that have that share
+        of the largest (0: all); equal logits count in order of their tokens.  The token is the
+        first at which the kept probabilities' sum, in order of tokens, passes u.  Returns ids, or
+        (ids, log of the kept share) when logprob is True or a fp32 [rows] tensor to write.  A row
+        that holds NaN, or -inf alone, gives -1."""
+        dev, dtype, vocab = self.dev, self.dtype, self.vocab
+        rows = logits.shape[0]
+        if not 0 < rows <= self.rows:
+            raise ValueError(f"logits: 1 to {self.rows} rows expected, got {rows}")
+        ld = _rows(logits, "logits", dtype, dev, (rows, vocab))
+        up = _dense(u, "u", torch.float32, dev, (rows,))
+        settings = [0 if t is None else _dense(t, name, kind, dev, (rows,))
+                    for t, name, kind in ((temperature, "temperature", torch.float32),
+                                          (top_k, "top_k", torch.int32),
+                                          (top_p, "top_p", torch.float32),
+                                          (min_p, "min_p", torch.float32))]
+        if ids is None:
+            ids = torch.empty(rows, dtype=torch.int32, device=self.device)
+        idp, lp = _dense(ids, "ids", torch.int32, dev, (rows,)), 0
+        if logprob is not False:
+            if logprob is True:
+                logprob = torch.empty(rows, dtype=torch.float32, device=self.device)
+            lp = _dense(logprob, "logprob", torch.float32, dev, (rows,))
+        _sample_call(_SAMPLE.pack(WQ_ABI_VERSION, _SAMPLE.size, logits.data_ptr(), up, *settings,
+                                  idp, lp, *self._space, self._memory.stream(dev), rows, vocab, ld,
+                                  self.flags, 0))
+        return ids if logprob is False else (ids, logprob)

@@ -5,18 +5,38 @@
 // The cut is a pair (key, index), the key a logit's bits made to ascend with its value.  The token
 // is then where the sum of what stays, in order of numbers, passes u times the whole.
 //
-// Borders decide, so p is formed in fp64 (of the logits' exact difference, to some 1e-14) and
+// Borders decide, so p is formed in fp64 (of the logits' exact difference, to some 4e-14) and
 // summed as integers, in steps of 2^-44: the sums are the same in any order.
+//
+// A row is read three times, by as many work-groups as fill the chip:
+//   sample_max     the largest logit of each slice of a row;
+//   sample_bins    tokens, and sums of p, by how far a logit lies below the largest, in 2025 bins of
+//                  1/45 of a power of two: the cut lies in one of them (top_k and top_p: in one each);
+//   sample_gather  the sums of p over what lies above the cut's bin, for each 1 KiB of the row, and a
+//                  list of what lies in it;
+//   sample_pick    a work-group a row: the list in order, the cut, and the token.
+// A bin that holds more tokens than the list is sought again by the bytes of the keys, in passes over
+// the row by sample_pick's work-group.
+#include <algorithm>
+#include <type_traits>
+
 #include "wq_decode.h"
 #include "wq_device.h"
 
 namespace wq {
 namespace {
 
-constexpr int kThreads = 1024, kWaves = kThreads / 64;
 typedef unsigned long long u64;
 
 enum LogitType { kFp16, kBf16, kFp32 };
+
+constexpr int kThreads = 512, kWaves = kThreads / 64;            // of the kernels on slices
+constexpr int kPickThreads = 1024, kPickWaves = kPickThreads / 64;
+constexpr int kMaxSlices = 64;
+constexpr int kBins = 2048;  // the last one: p is 0 in steps of 2^-44
+constexpr double kBinsPerPower = 45.;
+constexpr int kList = 4096;
+constexpr int kMaxChunks = WQ_SAMPLE_MAX_VOCAB / 256 + 1;
 
 struct SampleArgs {
   const void* logits;
@@ -25,7 +45,14 @@ struct SampleArgs {
   int32_t* ids;
   float* logprob;
   int64_t ld;
-  int vocab;
+  int vocab, slices, max_chunks;
+  // workspace, for each row: [slices], [kBins], [kBins], [max_chunks], [kList], one
+  u64* best;        // a slice's largest key and, below it, the first of its tokens, negated
+  u64* bin_mass;
+  uint32_t* bin_count;
+  u64* chunk_mass;
+  u64* list;        // keys and negated tokens
+  uint32_t* listed;
 };
 
 // Ascends with the value; -0 is 0.
@@ -37,28 +64,25 @@ __device__ __forceinline__ float value_of(uint32_t key) {
   return __builtin_bit_cast(float, key >> 31 ? key & 0x7fffffffu : ~key);
 }
 
-// 2^t for t <= 0, to 2^-52 of its value: the power series of 2^r about 0 up to its twelfth power,
-// whose next term is below 2^-53 for |r| <= 1/2.
+// 2^t for t <= 0, to 3.7e-14 of its value: 1 + r q(r) for the remainder |r| <= 1/2 of t, q of degree
+// 8 through the Chebyshev points.
 __device__ __forceinline__ double exp2_neg(double t) {
   if (!(t > -1000.)) return 0.;
   const double n = rint(t), r = t - n;
-  double x = 2.5678435993488196e-11;   // ln(2)^12 / 12!
-  x = fma(x, r, 4.44553827187081e-10);
-  x = fma(x, r, 7.054911620801121e-09);
-  x = fma(x, r, 1.0178086009239696e-07);
-  x = fma(x, r, 1.3215486790144305e-06);
-  x = fma(x, r, 1.5252733804059838e-05);
-  x = fma(x, r, 0.00015403530393381606);
-  x = fma(x, r, 0.0013333558146428441);
-  x = fma(x, r, 0.009618129107628477);
-  x = fma(x, r, 0.055504108664821576);
-  x = fma(x, r, 0.2402265069591007);
-  x = fma(x, r, 0.6931471805599453);
+  double x = 1.0203121171282166e-07;
+  x = fma(x, r, 1.3255224873639605e-06);
+  x = fma(x, r, 1.5252686845725586e-05);
+  x = fma(x, r, 1.5403455852474373e-04);
+  x = fma(x, r, 1.333355817904396e-03);
+  x = fma(x, r, 9.618129159402536e-03);
+  x = fma(x, r, 5.550410866476042e-02);
+  x = fma(x, r, 2.402265069581299e-01);
+  x = fma(x, r, 6.931471805599453e-01);
   x = fma(x, r, 1.);
   return __builtin_ldexp(x, (int)n);
 }
 
-// The row's probabilities: exponent of p in base 2, p, and p in steps of 2^-44.
+// The row's probabilities: exponent of p in base 2, p, p in steps of 2^-44, and the bin.
 struct Weights {
   double top, rate;  // the largest logit; log2(e) / T
   __device__ double exponent(float z) const {
@@ -68,6 +92,40 @@ struct Weights {
   __device__ static u64 steps(double p) {
     // the integer nearest to 2^44 p lies in the low bits of its sum with 2^52
     return __builtin_bit_cast(u64, fma(p, 0x1p44, 0x1p52)) & ((1ull << 52) - 1);
+  }
+  // Never falls as z does.  Below 2^-45 there are no steps.
+  __device__ static int bin(double exponent) {
+    return exponent > -45. ? (int)(-exponent * kBinsPerPower) : kBins - 1;
+  }
+  // A logit below which no exponent is above this one.
+  __device__ float logit_below(double exponent) const {
+    if (top == INFINITY) return INFINITY;
+    const double z = top + (exponent - 0x1p-20) / rate;
+    return (float)(z - fabs(z) * 0x1p-20) - 1e-30f;
+  }
+};
+
+// What a row asks for.
+struct Setting {
+  float t, min_p;
+  double top_p;
+  int k;
+  bool greedy, cut_k, cut_p;
+
+  __device__ Setting(const SampleArgs& p, int row) {
+    t = p.temperature != nullptr ? p.temperature[row] : 1.f;
+    k = p.top_k != nullptr ? p.top_k[row] : 0;
+    const float share = p.top_p != nullptr ? p.top_p[row] : 1.f;
+    min_p = p.min_p != nullptr ? p.min_p[row] : 0.f;
+    greedy = !(t > 0.f);
+    cut_k = k > 0 && k < p.vocab;
+    cut_p = share < 1.f;
+    top_p = share > 0.f ? share : 0.;
+  }
+  // The least sum that is not below top_p of the total, and that the first token has at least.
+  __device__ u64 share_of(u64 total) const {
+    const double want = ceil(top_p * (double)total);
+    return want < 1. ? 1 : (u64)want;
   }
 };
 
@@ -124,23 +182,277 @@ __device__ __forceinline__ u64 wave_sum(u64 x) {
   return x;
 }
 
-// The last token that stays: those of a larger key stay, and those of this key up to the index.
+// The slice's chunks.
+template <int TYPE>
+__device__ __forceinline__ void slice_of(const SampleArgs& p, const Row<TYPE>& row, int slice,
+                                         int& from, int& to) {
+  from = (int)((int64_t)row.chunks * slice / p.slices);
+  to = (int)((int64_t)row.chunks * (slice + 1) / p.slices);
+}
+
+constexpr u64 kNan = ~0ull;  // in a slice's best: it holds a NaN
+
+// A token's place in the order: larger keys first, equal ones by number.
+__device__ __forceinline__ u64 place_of(uint32_t key, int at) {
+  return (u64)key << 32 | (uint32_t)~at;
+}
+__device__ __forceinline__ uint32_t key_at(u64 place) { return (uint32_t)(place >> 32); }
+__device__ __forceinline__ int token_at(u64 place) { return (int)~(uint32_t)place; }
+
+template <int TYPE>
+__global__ __launch_bounds__(kThreads) void sample_max(SampleArgs p) {
+  __shared__ u64 best_lds[kWaves];
+  const int slice = blockIdx.x, r = blockIdx.y;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const Row<TYPE> row(p, r);
+  constexpr int kLen = Row<TYPE>::kLen;
+  int from, to;
+  slice_of(p, row, slice, from, to);
+  uint32_t key = 0;
+  int at = 0;
+  bool nan = false;
+#pragma unroll 4
+  for (int c = from + wave; c < to; c += kWaves) {
+    float z[kLen];
+    row.load(c, lane, z);
+    const int first = row.first(c, lane);
+#pragma unroll
+    for (int i = 0; i < kLen; ++i) {
+      const bool in = row.has(first + i);
+      nan |= in && z[i] != z[i];
+      const uint32_t k = in ? key_of(z[i]) : 0u;
+      if (k > key) {
+        key = k;
+        at = first + i;
+      }
+    }
+  }
+  u64 best = nan ? kNan : place_of(key, at);
+#pragma unroll
+  for (int d = 32; d >= 1; d /= 2) best = max(best, (u64)__shfl_xor(best, d));
+  if (lane == 0) best_lds[wave] = best;
+  // the row's bins and list start empty
+  for (int i = slice * kThreads + tid; i < kBins; i += p.slices * kThreads) {
+    p.bin_mass[(int64_t)r * kBins + i] = 0;
+    p.bin_count[(int64_t)r * kBins + i] = 0;
+  }
+  if (slice == 0 && tid == 0) p.listed[r] = 0;
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < kWaves; ++w) best = max(best, best_lds[w]);
+    p.best[(int64_t)r * p.slices + slice] = best;
+  }
+}
+
+// The row's largest logit, as a place, by each wave.
+__device__ __forceinline__ u64 row_best(const SampleArgs& p, int r, int lane) {
+  u64 best = lane < p.slices ? p.best[(int64_t)r * p.slices + lane] : 0;
+#pragma unroll
+  for (int d = 32; d >= 1; d /= 2) best = max(best, (u64)__shfl_xor(best, d));
+  return best;
+}
+__device__ __forceinline__ bool row_is_bad(u64 best) {
+  return best == kNan || value_of(key_at(best)) == -INFINITY;
+}
+
+template <int TYPE>
+__global__ __launch_bounds__(kThreads) void sample_bins(SampleArgs p) {
+  __shared__ u64 mass[kBins];
+  __shared__ uint32_t count[kBins];
+  const int slice = blockIdx.x, r = blockIdx.y;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const Setting set(p, r);
+  if (set.greedy || !(set.cut_k || set.cut_p)) return;
+  const u64 best = row_best(p, r, lane);
+  if (row_is_bad(best)) return;
+  for (int i = tid; i < kBins; i += kThreads) {
+    mass[i] = 0;
+    count[i] = 0;
+  }
+  __syncthreads();
+  const Row<TYPE> row(p, r);
+  constexpr int kLen = Row<TYPE>::kLen;
+  const Weights weights{(double)value_of(key_at(best)), 1.4426950408889634 / (double)set.t};
+  const float least = weights.logit_below(-45.);
+  int from, to;
+  slice_of(p, row, slice, from, to);
+  for (int c = from + wave; c < to; c += kWaves) {
+    float z[kLen];
+    row.load(c, lane, z);
+    const int first = row.first(c, lane);
+#pragma unroll
+    for (int i = 0; i < kLen; ++i) {
+      if (!row.has(first + i) || !(z[i] >= least)) continue;  // (tokens without a step count not)
+      const double e = weights.exponent(z[i]);
+      const int b = Weights::bin(e);
+      if (set.cut_k) atomicAdd(&count[b], 1u);
+      if (set.cut_p) atomicAdd(&mass[b], Weights::steps(exp2_neg(e)));
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < kBins - 1; i += kThreads) {
+    if (count[i]) atomicAdd(&p.bin_count[(int64_t)r * kBins + i], count[i]);
+    if (mass[i]) atomicAdd(&p.bin_mass[(int64_t)r * kBins + i], mass[i]);
+  }
+}
+
+// Where the cuts lie: the bins of the list, and what is above them.
+struct Bins {
+  int k, p_low, p_high;  // bin of the k-th token; bins that may hold the token at top_p; -1: no cut
+  uint32_t above_k;      // tokens above bin k
+  u64 mass_above_k, mass_above_p;  // sums of p above bins k and p_low
+  u64 all;                         // and over all of them
+  __device__ int first() const { return p_low >= 0 ? p_low : k >= 0 ? k : kBins; }
+  __device__ bool lists(int bin) const {
+    return bin == k || (bin >= p_low && bin <= p_high && p_low >= 0);
+  }
+};
+
+// Exclusive prefixes of the row's bins by THREADS threads, in sums; and the bins that are sought.
+template <int THREADS>
+__device__ Bins find_bins(const SampleArgs& p, const Setting& set, int r, u64* mass_lds,
+                          uint32_t* count_lds, Bins& out) {
+  constexpr int kEach = kBins / THREADS, kWaves = THREADS / 64;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  u64 m[kEach], mass = 0;
+  uint32_t n[kEach], count = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    m[i] = p.bin_mass[(int64_t)r * kBins + kEach * tid + i];
+    n[i] = p.bin_count[(int64_t)r * kBins + kEach * tid + i];
+    mass += m[i];
+    count += n[i];
+  }
+  u64 mass_to = mass;
+  uint32_t count_to = count;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const u64 om = __shfl_up(mass_to, d);
+    const uint32_t on = __shfl_up(count_to, d);
+    if (lane >= d) {
+      mass_to += om;
+      count_to += on;
+    }
+  }
+  if (lane == 63) {
+    mass_lds[wave] = mass_to;
+    count_lds[wave] = count_to;
+  }
+  if (tid == 0) out = Bins{-1, -1, -1, 0, 0, 0, 0};
+  __syncthreads();
+  u64 all = 0;
+  mass_to -= mass;
+  count_to -= count;
+  for (int w = 0; w < kWaves; ++w) {
+    if (w < wave) {
+      mass_to += mass_lds[w];
+      count_to += count_lds[w];
+    }
+    all += mass_lds[w];
+  }
+  if (tid == 0) out.all = all;
+  // the k-th token's bin; among tokens without a step there is nothing to cut
+  if (set.cut_k) {
+    uint32_t upto = count_to;
+    u64 above = mass_to;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      if (upto < (uint32_t)set.k && (uint32_t)set.k <= upto + n[i]) {
+        out.k = kEach * tid + i;
+        out.above_k = upto;
+        out.mass_above_k = above;
+        mass_lds[kWaves] = above;
+        mass_lds[kWaves + 1] = above + m[i];
+      }
+      upto += n[i];
+      above += m[i];
+    }
+  }
+  __syncthreads();
+  if (set.cut_p) {
+    // top_p of at least what lies above the k-th token's bin, and at most that and all of the bin
+    const bool k_cuts = out.k >= 0;
+    const u64 low = set.share_of(k_cuts ? mass_lds[kWaves] : all);
+    const u64 high = set.share_of(k_cuts ? mass_lds[kWaves + 1] : all);
+    u64 above = mass_to;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      if (above < low && low <= above + m[i]) {
+        out.p_low = kEach * tid + i;
+        out.mass_above_p = above;
+      }
+      if (above < high && high <= above + m[i]) out.p_high = kEach * tid + i;
+      above += m[i];
+    }
+  }
+  __syncthreads();
+  return out;
+}
+
+template <int TYPE>
+__global__ __launch_bounds__(kThreads) void sample_gather(SampleArgs p) {
+  __shared__ u64 mass_lds[kWaves + 2];
+  __shared__ uint32_t count_lds[kWaves];
+  __shared__ Bins bins_lds;
+  const int slice = blockIdx.x, r = blockIdx.y;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const Setting set(p, r);
+  if (set.greedy) return;
+  const u64 best = row_best(p, r, lane);
+  if (row_is_bad(best)) return;
+  Bins bins{-1, -1, -1, 0, 0, 0, 0};
+  if (set.cut_k || set.cut_p)
+    bins = find_bins<kThreads>(p, set, r, mass_lds, count_lds, bins_lds);
+  const Row<TYPE> row(p, r);
+  constexpr int kLen = Row<TYPE>::kLen;
+  const Weights weights{(double)value_of(key_at(best)), 1.4426950408889634 / (double)set.t};
+  const int first_bin = bins.first();
+  const int last_bin = max(bins.k, bins.p_high);
+  // nothing below the last bin of the list is looked at
+  const float least =
+      weights.logit_below(last_bin >= 0 ? (last_bin + 1) * (-1. / kBinsPerPower) : -45.);
+  int from, to;
+  slice_of(p, row, slice, from, to);
+  for (int c = from + wave; c < to; c += kWaves) {
+    float z[kLen];
+    row.load(c, lane, z);
+    const int first = row.first(c, lane);
+    u64 sum = 0;
+#pragma unroll
+    for (int i = 0; i < kLen; ++i) {
+      if (!row.has(first + i) || !(z[i] >= least)) continue;
+      const double e = weights.exponent(z[i]);
+      const int b = Weights::bin(e);
+      if (b < first_bin) {
+        const double x = exp2_neg(e);
+        sum += key_of(z[i]) == key_at(best) || !(x < (double)set.min_p) ? Weights::steps(x) : 0;
+      } else if (bins.lists(b)) {
+        const uint32_t n = atomicAdd(&p.listed[r], 1u);
+        if (n < kList) p.list[(int64_t)r * kList + n] = place_of(key_of(z[i]), first + i);
+      }
+    }
+    sum = wave_sum(sum);
+    if (lane == 0) p.chunk_mass[(int64_t)r * p.max_chunks + c] = sum;
+  }
+}
+
+// The last token that stays, by its place.
 struct Cut {
   uint32_t key;
   int index;
   __device__ bool keeps(uint32_t k, int at) const { return k > key || (k == key && at <= index); }
 };
 
-constexpr int kMaxChunks = WQ_SAMPLE_MAX_VOCAB / 256 + 1;
-
 struct Shared {
   u64 mass[kMaxChunks];   // of chunks; and of keys' bytes while a cut is sought
   uint32_t count[kMaxChunks];
-  uint32_t best_key[kWaves];
-  int best_at[kWaves], nan[kWaves];
+  u64 list[kList], list_mass[kList + 1];  // places in order; sums of p before each
+  u64 wave_mass[kPickWaves + 2];
+  uint32_t wave_count[kPickWaves];
+  Bins bins;
   // found by one thread for all
   uint32_t key;
-  int chunk, index;
+  int index, first_k;
   u64 above, total;
   uint32_t above_count;
 };
@@ -163,70 +475,27 @@ __device__ T wave_prefix(T* x, int n, int lane) {
   return sum;
 }
 
-// One work-group a row.
+// A work-group a row.
 template <int TYPE>
-__global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs p) {
+__global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
   __shared__ Shared sh;
   const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const Row<TYPE> row(p, r);
-  constexpr int kLen = Row<TYPE>::kLen;
-  float z[kLen];
-
-  // the largest logit, its first token, and whether there is a NaN
-  uint32_t key = 0;
-  int at = 0, nan = 0;
-  for (int c = wave; c < row.chunks; c += kWaves) {
-    row.load(c, lane, z);
-    const int first = row.first(c, lane);
-#pragma unroll
-    for (int i = 0; i < kLen; ++i) {
-      if (!row.has(first + i)) continue;
-      nan |= z[i] != z[i];
-      const uint32_t k = key_of(z[i]);
-      if (k > key) {
-        key = k;
-        at = first + i;
-      }
-    }
-  }
-#pragma unroll
-  for (int d = 32; d >= 1; d /= 2) {
-    const uint32_t k = __shfl_xor(key, d);
-    const int a = __shfl_xor(at, d);
-    nan |= __shfl_xor(nan, d);
-    if (k > key || (k == key && a < at)) {
-      key = k;
-      at = a;
-    }
-  }
-  if (lane == 0) {
-    sh.best_key[wave] = key;
-    sh.best_at[wave] = at;
-    sh.nan[wave] = nan;
-  }
-  __syncthreads();
-  nan = 0;
-  key = 0;
-  at = 0;
-  for (int w = 0; w < kWaves; ++w) {
-    nan |= sh.nan[w];
-    if (sh.best_key[w] > key || (sh.best_key[w] == key && sh.best_at[w] < at)) {
-      key = sh.best_key[w];
-      at = sh.best_at[w];
-    }
-  }
-  const float top = value_of(key);
-  const float t = p.temperature != nullptr ? p.temperature[r] : 1.f;
-  const bool greedy = !(t > 0.f);
-  if (nan || top == -INFINITY || greedy) {
+  constexpr int kThreads = kPickThreads, kWaves = kPickWaves;
+  const Setting set(p, r);
+  const u64 best = row_best(p, r, lane);
+  if (row_is_bad(best) || set.greedy) {
     if (tid == 0) {
-      const bool bad = nan || top == -INFINITY;
-      p.ids[r] = bad ? -1 : at;
+      const bool bad = row_is_bad(best);
+      p.ids[r] = bad ? -1 : token_at(best);
       if (p.logprob != nullptr) p.logprob[r] = bad ? __builtin_nanf("") : 0.f;
     }
     return;
   }
-  const Weights weights{(double)top, 1.4426950408889634 / (double)t};
+  const Row<TYPE> row(p, r);
+  constexpr int kLen = Row<TYPE>::kLen;
+  float z[kLen];
+  const uint32_t key = key_at(best);
+  const Weights weights{(double)value_of(key), 1.4426950408889634 / (double)set.t};
 
   // The cut at which the count of tokens, or the sum of their p, reaches a target: by the bytes of
   // the key from the top, then by number among the tokens of that key.  Leaves in sh.above the sum
@@ -319,15 +588,11 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs p) {
   };
 
   Cut cut{0, row.vocab};
-  const int k = p.top_k != nullptr ? p.top_k[r] : 0;
-  const float top_p = p.top_p != nullptr ? p.top_p[r] : 1.f;
-  const float min_p = p.min_p != nullptr ? p.min_p[r] : 0.f;
-  const bool cut_k = k > 0 && k < row.vocab, cut_p = top_p < 1.f;
   const auto kept = [&](float v, int i) -> double {  // p where the token stays, else 0
     const uint32_t kk = key_of(v);
     if (!row.has(i) || !cut.keeps(kk, i)) return 0.;
     const double x = weights.p(v);
-    return kk == key || !(x < (double)min_p) ? x : 0.;
+    return kk == key || !(x < (double)set.min_p) ? x : 0.;
   };
   const auto chunk_sums = [&](bool all) {
     __syncthreads();
@@ -344,29 +609,95 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs p) {
       if (lane == 0) sh.mass[c] = sum;
     }
     __syncthreads();
-    if (wave == 0) {
-      const u64 total = wave_prefix(sh.mass, row.chunks, lane);
-      if (lane == 0) sh.total = total;
+  };
+
+  const uint32_t listed = set.cut_k || set.cut_p ? p.listed[r] : 0u;
+  if (listed > (uint32_t)kList) {
+    u64 total = 0;
+    if (set.cut_k) {
+      cut = find_cut(true, (u64)set.k);
+      total = sh.above;
+    } else {
+      chunk_sums(true);
+      if (wave == 0) {
+        const u64 sum = wave_prefix(sh.mass, row.chunks, lane);
+        if (lane == 0) sh.total = sum;
+      }
+      __syncthreads();
+      total = sh.total;
+    }
+    if (set.cut_p) cut = find_cut(false, set.share_of(total));
+    chunk_sums(false);
+  } else {
+    for (int c = tid; c < row.chunks; c += kThreads)
+      sh.mass[c] = p.chunk_mass[(int64_t)r * p.max_chunks + c];
+    if (set.cut_k || set.cut_p) {
+      const Bins bins =
+          find_bins<kPickThreads>(p, set, r, sh.wave_mass, sh.wave_count, sh.bins);
+      // the list in order (bitonic)
+      int n2 = 1;
+      while (n2 < (int)listed) n2 *= 2;
+      for (int i = tid; i < n2; i += kThreads)
+        sh.list[i] = i < (int)listed ? p.list[(int64_t)r * kList + i] : 0;
+      for (int size = 2; size <= n2; size *= 2)
+        for (int gap = size / 2; gap > 0; gap /= 2) {
+          __syncthreads();
+          for (int i = tid; i < n2 / 2; i += kThreads) {
+            const int a = 2 * i - (i & (gap - 1)), b = a + gap;
+            const u64 x = sh.list[a], y = sh.list[b];
+            if ((x < y) == ((a & size) == 0)) {
+              sh.list[a] = y;
+              sh.list[b] = x;
+            }
+          }
+        }
+      __syncthreads();
+      if (tid == 0) sh.index = sh.first_k = -1;
+      __syncthreads();
+      const auto bin_at = [&](int i) {
+        return Weights::bin(weights.exponent(value_of(key_at(sh.list[i]))));
+      };
+      for (int i = tid; i < (int)listed; i += kThreads) {
+        sh.list_mass[i] = Weights::steps(weights.p(value_of(key_at(sh.list[i]))));
+        if (bin_at(i) == bins.k && (i == 0 || bin_at(i - 1) != bins.k)) sh.first_k = i;
+      }
+      __syncthreads();
+      if (wave == 0) {
+        const u64 sum = wave_prefix(sh.list_mass, (int)listed, lane);
+        if (lane == 0) sh.list_mass[listed] = sum;
+      }
+      __syncthreads();
+      u64 total = bins.all;
+      int last = -1;  // entry of the cut
+      if (bins.k >= 0) {
+        last = sh.first_k + set.k - (int)bins.above_k - 1;
+        total = bins.mass_above_k + sh.list_mass[last + 1] - sh.list_mass[sh.first_k];
+      }
+      if (set.cut_p) {
+        const u64 want = set.share_of(total);
+        for (int i = tid; i < (int)listed; i += kThreads)
+          if (bins.mass_above_p + sh.list_mass[i] < want &&
+              want <= bins.mass_above_p + sh.list_mass[i + 1])
+            sh.index = i;
+      } else if (tid == 0) {
+        sh.index = last;
+      }
+      __syncthreads();
+      if (sh.index >= 0) {
+        cut = Cut{key_at(sh.list[sh.index]), token_at(sh.list[sh.index])};
+        // what stays of the list joins its chunks
+        for (int i = tid; i <= sh.index; i += kThreads) {
+          const float v = value_of(key_at(sh.list[i]));
+          const int at = token_at(sh.list[i]);
+          atomicAdd(&sh.mass[(at + row.skew) / Row<TYPE>::kChunk], Weights::steps(kept(v, at)));
+        }
+      }
     }
     __syncthreads();
-  };
-  u64 total = 0;
-  if (cut_k) {
-    cut = find_cut(true, (u64)k);
-    total = sh.above;
-  } else if (cut_p) {
-    chunk_sums(true);
-    total = sh.total;
   }
-  if (cut_p) {
-    // the least sum that is not below top_p of the total, and that the first token has at least
-    const double want = ceil((double)fmaxf(top_p, 0.f) * (double)total);
-    cut = find_cut(false, want < 1. ? 1 : (u64)want);
-  }
-  chunk_sums(false);
-  total = sh.total;
 
   if (wave == 0) {
+    const u64 total = wave_prefix(sh.mass, row.chunks, lane);
     const float u = p.u[r];
     const double want = u > 0.f ? (double)u * (double)total : 0.;
     const u64 pass = want < (double)total ? min((u64)want, total - 1) : total - 1;
@@ -406,7 +737,20 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs p) {
 
 }  // namespace
 
-size_t sample_workspace_bytes(int, int, uint32_t) { return 0; }
+// Work-groups to a row: two of 512 threads on each CU in all, and a chunk at least for each wave.
+static int slices_of(int rows, int chunks) {
+  return std::max(1, std::min({kMaxSlices, chunks / kWaves, 1024 / rows}));
+}
+
+static int chunks_of(int vocab, uint32_t flags) {
+  const int chunk = (flags & WQ_FLAG_FP32) ? 256 : 512;
+  return vocab / chunk + 2;  // (a row may begin and end inside one)
+}
+
+size_t sample_workspace_bytes(int rows, int vocab, uint32_t flags) {
+  const size_t chunks = chunks_of(vocab, flags);
+  return rows * (8 * (kMaxSlices + kBins + chunks + kList) + 4 * (kBins + 4));
+}
 
 hipError_t launch_sample(const wq_sample_args& a, hipStream_t stream) {
   SampleArgs p{};
@@ -420,14 +764,29 @@ hipError_t launch_sample(const wq_sample_args& a, hipStream_t stream) {
   p.logprob = a.logprob;
   p.ld = a.ld;
   p.vocab = a.vocab;
-  const dim3 grid((unsigned)a.rows), block(kThreads);
-  if (a.flags & WQ_FLAG_FP32)
-    hipLaunchKernelGGL((sample_kernel<kFp32>), grid, block, 0, stream, p);
-  else if (a.flags & WQ_FLAG_BF16)
-    hipLaunchKernelGGL((sample_kernel<kBf16>), grid, block, 0, stream, p);
-  else
-    hipLaunchKernelGGL((sample_kernel<kFp16>), grid, block, 0, stream, p);
-  return hipGetLastError();
+  p.max_chunks = chunks_of(a.vocab, a.flags);
+  p.slices = slices_of(a.rows, p.max_chunks);
+  const size_t rows = a.rows;
+  p.best = static_cast<u64*>(a.workspace);
+  p.bin_mass = p.best + rows * kMaxSlices;
+  p.chunk_mass = p.bin_mass + rows * kBins;
+  p.list = p.chunk_mass + rows * p.max_chunks;
+  p.bin_count = reinterpret_cast<uint32_t*>(p.list + rows * kList);
+  p.listed = p.bin_count + rows * kBins;
+  const dim3 grid((unsigned)p.slices, (unsigned)a.rows), block(kThreads);
+  const dim3 pick((unsigned)a.rows), pick_block(kPickThreads);
+  const bool cuts = a.top_k != nullptr || a.top_p != nullptr;
+  const auto run = [&](auto type) {
+    constexpr int TYPE = decltype(type)::value;
+    hipLaunchKernelGGL((sample_max<TYPE>), grid, block, 0, stream, p);
+    if (cuts) hipLaunchKernelGGL((sample_bins<TYPE>), grid, block, 0, stream, p);
+    hipLaunchKernelGGL((sample_gather<TYPE>), grid, block, 0, stream, p);
+    hipLaunchKernelGGL((sample_pick<TYPE>), pick, pick_block, 0, stream, p);
+    return hipGetLastError();
+  };
+  if (a.flags & WQ_FLAG_FP32) return run(std::integral_constant<int, kFp32>());
+  if (a.flags & WQ_FLAG_BF16) return run(std::integral_constant<int, kBf16>());
+  return run(std::integral_constant<int, kFp16>());
 }
 
 }  // namespace wq

@@ -27,16 +27,29 @@ namespace wq {
 namespace {
 
 typedef unsigned long long u64;
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 enum LogitType { kFp16, kBf16, kFp32 };
 
 constexpr int kThreads = 512, kWaves = kThreads / 64;            // of the kernels on slices
-constexpr int kPickThreads = 1024, kPickWaves = kPickThreads / 64;
+constexpr int kPickThreads = 256, kPickWaves = kPickThreads / 64;
 constexpr int kMaxSlices = 64;
 constexpr int kBins = 2048;  // the last one: p is 0 in steps of 2^-44
 constexpr double kBinsPerPower = 45.;
-constexpr int kList = 4096;
+constexpr int kList = 4096, kSliceList = 2048;
 constexpr int kMaxChunks = WQ_SAMPLE_MAX_VOCAB / 256 + 1;
+
+// Where the cuts lie: the bins of the list, and what is above them.
+struct Bins {
+  int k, p_low, p_high;  // bin of the k-th token; bins that may hold the token at top_p; -1: no cut
+  uint32_t above_k;      // tokens above bin k
+  u64 mass_above_k, mass_above_p;  // sums of p above bins k and p_low
+  u64 all;                         // and over all of them
+  __device__ int first() const { return p_low >= 0 ? p_low : k >= 0 ? k : kBins; }
+  __device__ bool lists(int bin) const {
+    return bin == k || (bin >= p_low && bin <= p_high && p_low >= 0);
+  }
+};
 
 struct SampleArgs {
   const void* logits;
@@ -52,6 +65,7 @@ struct SampleArgs {
   uint32_t* bin_count;
   u64* chunk_mass;
   u64* list;        // keys and negated tokens
+  Bins* bins;
   uint32_t* listed;
 };
 
@@ -85,10 +99,11 @@ __device__ __forceinline__ double exp2_neg(double t) {
 // The row's probabilities: exponent of p in base 2, p, p in steps of 2^-44, and the bin.
 struct Weights {
   double top, rate;  // the largest logit; log2(e) / T
-  __device__ double exponent(float z) const {
-    return (double)z == top ? 0. : ((double)z - top) * rate;
-  }
-  __device__ double p(float z) const { return z == -INFINITY ? 0. : exp2_neg(exponent(z)); }
+  __device__ Weights(float largest, float t)
+      // an infinite logit is above all others by more than any T brings back
+      : top(largest == INFINITY ? 1e300 : (double)largest), rate(1.4426950408889634 / (double)t) {}
+  __device__ double exponent(float z) const { return (fmin((double)z, top) - top) * rate; }
+  __device__ double p(float z) const { return exp2_neg(exponent(z)); }
   __device__ static u64 steps(double p) {
     // the integer nearest to 2^44 p lies in the low bits of its sum with 2^52
     return __builtin_bit_cast(u64, fma(p, 0x1p44, 0x1p52)) & ((1ull << 52) - 1);
@@ -99,7 +114,6 @@ struct Weights {
   }
   // A logit below which no exponent is above this one.
   __device__ float logit_below(double exponent) const {
-    if (top == INFINITY) return INFINITY;
     const double z = top + (exponent - 0x1p-20) / rate;
     return (float)(z - fabs(z) * 0x1p-20) - 1e-30f;
   }
@@ -135,6 +149,8 @@ template <int TYPE>
 struct Row {
   static constexpr int kLen = TYPE == kFp32 ? 4 : 8;
   static constexpr int kChunk = 64 * kLen;  // elements that a wave takes at a time
+  static constexpr uint32_t kLowest =
+      TYPE == kFp32 ? 0xff800000u : TYPE == kBf16 ? 0xff80ff80u : 0xfc00fc00u;  // -inf
   const char* base;
   int vocab, skew, chunks;
 
@@ -148,22 +164,32 @@ struct Row {
   }
   // The number of a lane's first element of a chunk.
   __device__ int first(int chunk, int lane) const { return (chunk * 64 + lane) * kLen - skew; }
-  __device__ void load(int chunk, int lane, float* z) const {
-    const int at = first(chunk, lane);
+  // A lane's vector of a chunk; -inf outside the row.
+  __device__ u32x4 raw(int chunk, int lane) const {
     const char* src = base + ((int64_t)chunk * 64 + lane) * 16;
-    u32x4 w = {0u, 0u, 0u, 0u};
+    const int from = first(chunk, 0);
+    if (from >= 0 && from + kChunk <= vocab)  // (a condition of the wave's)
+      return *reinterpret_cast<const u32x4*>(src);
+    const int at = first(chunk, lane);
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = kLowest;
     if (at >= 0 && at + kLen <= vocab) {
       w = *reinterpret_cast<const u32x4*>(src);
     } else if constexpr (TYPE == kFp32) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (at + i >= 0 && at + i < vocab) w[i] = reinterpret_cast<const uint32_t*>(src)[i];
+        if (has(at + i)) w[i] = reinterpret_cast<const uint32_t*>(src)[i];
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (at + i >= 0 && at + i < vocab)
-          w[i / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(src)[i] << (16 * (i % 2));
+        if (has(at + i))
+          w[i / 2] = (w[i / 2] & (i % 2 ? 0xffffu : 0xffff0000u)) |
+                     (uint32_t) reinterpret_cast<const uint16_t*>(src)[i] << (16 * (i % 2));
     }
+    return w;
+  }
+  __device__ static void values(u32x4 w, float* z) {
 #pragma unroll
     for (int i = 0; i < kLen; ++i) {
       const uint32_t bits = w[TYPE == kFp32 ? i : i / 2];
@@ -173,8 +199,26 @@ struct Row {
         z[i] = Act<TYPE == kBf16>::value((uint16_t)(bits >> (16 * (i % 2))));
     }
   }
+  __device__ void load(int chunk, int lane, float* z) const { values(raw(chunk, lane), z); }
   __device__ bool has(int at) const { return at >= 0 && at < vocab; }
 };
+
+// Chunks from + wave, from + wave + waves, ... before `to`, the next one's vector in flight while
+// f(chunk, values) runs.
+template <int TYPE, class F>
+__device__ __forceinline__ void each_chunk(const Row<TYPE>& row, int from, int to, int wave,
+                                           int waves, int lane, F f) {
+  int c = from + wave;
+  if (c >= to) return;
+  u32x4 next = row.raw(c, lane);
+  for (; c < to; c += waves) {
+    const u32x4 w = next;
+    if (c + waves < to) next = row.raw(c + waves, lane);
+    float z[Row<TYPE>::kLen];
+    Row<TYPE>::values(w, z);
+    f(c, z);
+  }
+}
 
 __device__ __forceinline__ u64 wave_sum(u64 x) {
 #pragma unroll
@@ -208,26 +252,65 @@ __global__ __launch_bounds__(kThreads) void sample_max(SampleArgs p) {
   constexpr int kLen = Row<TYPE>::kLen;
   int from, to;
   slice_of(p, row, slice, from, to);
-  uint32_t key = 0;
-  int at = 0;
-  bool nan = false;
-#pragma unroll 4
-  for (int c = from + wave; c < to; c += kWaves) {
+  // The largest value of a lane and the first chunk that has it; the largest bits without signs,
+  // by which a NaN shows.
+  float top = -INFINITY;
+  int top_chunk = from + wave;
+  u32x4 sizes = {0u, 0u, 0u, 0u};
+  const auto look = [&](int c, u32x4 w) {
     float z[kLen];
-    row.load(c, lane, z);
-    const int first = row.first(c, lane);
+    Row<TYPE>::values(w, z);
+    float m = fmaxf(z[0], z[1]);
 #pragma unroll
-    for (int i = 0; i < kLen; ++i) {
-      const bool in = row.has(first + i);
-      nan |= in && z[i] != z[i];
-      const uint32_t k = in ? key_of(z[i]) : 0u;
-      if (k > key) {
-        key = k;
-        at = first + i;
+    for (int i = 2; i < kLen; ++i) m = fmaxf(m, z[i]);
+    if (m > top) {
+      top = m;
+      top_chunk = c;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (TYPE == kFp32) {
+        sizes[i] = max(sizes[i], w[i] & 0x7fffffffu);
+      } else {
+        const uint32_t a = sizes[i], b = w[i] & 0x7fff7fffu;
+        sizes[i] = __builtin_bit_cast(
+            uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
+                                                __builtin_bit_cast(u16x2, b)));
       }
     }
+  };
+  int c = from + wave;
+  for (; c + 3 * kWaves < to; c += 4 * kWaves) {
+    u32x4 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = row.raw(c + i * kWaves, lane);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) look(c + i * kWaves, w[i]);
   }
-  u64 best = nan ? kNan : place_of(key, at);
+  for (; c < to; c += kWaves) look(c, row.raw(c, lane));
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = sizes[i];
+    if constexpr (TYPE == kFp32)
+      nan |= x > 0x7f800000u;
+    else
+      nan |= (x & 0xffffu) > (Row<TYPE>::kLowest & 0x7fffu) ||
+             (x >> 16) > (Row<TYPE>::kLowest & 0x7fffu);
+  }
+  // the first token of the wave's largest value, in one of the lanes that have it
+  uint32_t key = key_of(top), wave_key = key;
+#pragma unroll
+  for (int d = 32; d >= 1; d /= 2) wave_key = max(wave_key, (uint32_t)__shfl_xor(wave_key, d));
+  u64 best = 0;
+  if (from + wave < to && key == wave_key) {
+    float z[kLen];
+    row.load(top_chunk, lane, z);
+#pragma unroll
+    for (int i = kLen - 1; i >= 0; --i)
+      if (z[i] == top) best = place_of(key, row.first(top_chunk, lane) + i);
+  }
+  if (nan) best = kNan;
 #pragma unroll
   for (int d = 32; d >= 1; d /= 2) best = max(best, (u64)__shfl_xor(best, d));
   if (lane == 0) best_lds[wave] = best;
@@ -272,23 +355,20 @@ __global__ __launch_bounds__(kThreads) void sample_bins(SampleArgs p) {
   __syncthreads();
   const Row<TYPE> row(p, r);
   constexpr int kLen = Row<TYPE>::kLen;
-  const Weights weights{(double)value_of(key_at(best)), 1.4426950408889634 / (double)set.t};
+  const Weights weights(value_of(key_at(best)), set.t);
   const float least = weights.logit_below(-45.);
   int from, to;
   slice_of(p, row, slice, from, to);
-  for (int c = from + wave; c < to; c += kWaves) {
-    float z[kLen];
-    row.load(c, lane, z);
-    const int first = row.first(c, lane);
+  each_chunk(row, from, to, wave, kWaves, lane, [&](int, const float* z) {
 #pragma unroll
     for (int i = 0; i < kLen; ++i) {
-      if (!row.has(first + i) || !(z[i] >= least)) continue;  // (tokens without a step count not)
+      if (!(z[i] >= least)) continue;  // (tokens without a step are not counted)
       const double e = weights.exponent(z[i]);
       const int b = Weights::bin(e);
       if (set.cut_k) atomicAdd(&count[b], 1u);
       if (set.cut_p) atomicAdd(&mass[b], Weights::steps(exp2_neg(e)));
     }
-  }
+  });
   __syncthreads();
   for (int i = tid; i < kBins - 1; i += kThreads) {
     if (count[i]) atomicAdd(&p.bin_count[(int64_t)r * kBins + i], count[i]);
@@ -296,30 +376,17 @@ __global__ __launch_bounds__(kThreads) void sample_bins(SampleArgs p) {
   }
 }
 
-// Where the cuts lie: the bins of the list, and what is above them.
-struct Bins {
-  int k, p_low, p_high;  // bin of the k-th token; bins that may hold the token at top_p; -1: no cut
-  uint32_t above_k;      // tokens above bin k
-  u64 mass_above_k, mass_above_p;  // sums of p above bins k and p_low
-  u64 all;                         // and over all of them
-  __device__ int first() const { return p_low >= 0 ? p_low : k >= 0 ? k : kBins; }
-  __device__ bool lists(int bin) const {
-    return bin == k || (bin >= p_low && bin <= p_high && p_low >= 0);
-  }
-};
-
-// Exclusive prefixes of the row's bins by THREADS threads, in sums; and the bins that are sought.
-template <int THREADS>
+// The bins that are sought, by the whole work-group.
 __device__ Bins find_bins(const SampleArgs& p, const Setting& set, int r, u64* mass_lds,
                           uint32_t* count_lds, Bins& out) {
-  constexpr int kEach = kBins / THREADS, kWaves = THREADS / 64;
+  constexpr int kEach = kBins / kThreads;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   u64 m[kEach], mass = 0;
   uint32_t n[kEach], count = 0;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    m[i] = p.bin_mass[(int64_t)r * kBins + kEach * tid + i];
-    n[i] = p.bin_count[(int64_t)r * kBins + kEach * tid + i];
+    m[i] = set.cut_p ? p.bin_mass[(int64_t)r * kBins + kEach * tid + i] : 0;
+    n[i] = set.cut_k ? p.bin_count[(int64_t)r * kBins + kEach * tid + i] : 0;
     mass += m[i];
     count += n[i];
   }
@@ -391,8 +458,8 @@ __device__ Bins find_bins(const SampleArgs& p, const Setting& set, int r, u64* m
 
 template <int TYPE>
 __global__ __launch_bounds__(kThreads) void sample_gather(SampleArgs p) {
-  __shared__ u64 mass_lds[kWaves + 2];
-  __shared__ uint32_t count_lds[kWaves];
+  __shared__ u64 mass_lds[kWaves + 2], list[kSliceList];
+  __shared__ uint32_t count_lds[kWaves], listed, at_lds;
   __shared__ Bins bins_lds;
   const int slice = blockIdx.x, r = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -400,40 +467,50 @@ __global__ __launch_bounds__(kThreads) void sample_gather(SampleArgs p) {
   if (set.greedy) return;
   const u64 best = row_best(p, r, lane);
   if (row_is_bad(best)) return;
+  if (tid == 0) listed = 0;
+  __syncthreads();
   Bins bins{-1, -1, -1, 0, 0, 0, 0};
   if (set.cut_k || set.cut_p)
-    bins = find_bins<kThreads>(p, set, r, mass_lds, count_lds, bins_lds);
+    bins = find_bins(p, set, r, mass_lds, count_lds, bins_lds);
   const Row<TYPE> row(p, r);
   constexpr int kLen = Row<TYPE>::kLen;
-  const Weights weights{(double)value_of(key_at(best)), 1.4426950408889634 / (double)set.t};
+  const Weights weights(value_of(key_at(best)), set.t);
   const int first_bin = bins.first();
   const int last_bin = max(bins.k, bins.p_high);
   // nothing below the last bin of the list is looked at
   const float least =
       weights.logit_below(last_bin >= 0 ? (last_bin + 1) * (-1. / kBinsPerPower) : -45.);
+  if (slice == 0 && tid == 0) p.bins[r] = bins;
   int from, to;
   slice_of(p, row, slice, from, to);
-  for (int c = from + wave; c < to; c += kWaves) {
-    float z[kLen];
-    row.load(c, lane, z);
+  each_chunk(row, from, to, wave, kWaves, lane, [&](int c, const float* z) {
     const int first = row.first(c, lane);
     u64 sum = 0;
 #pragma unroll
     for (int i = 0; i < kLen; ++i) {
-      if (!row.has(first + i) || !(z[i] >= least)) continue;
+      if (!(z[i] >= least)) continue;
       const double e = weights.exponent(z[i]);
       const int b = Weights::bin(e);
       if (b < first_bin) {
         const double x = exp2_neg(e);
         sum += key_of(z[i]) == key_at(best) || !(x < (double)set.min_p) ? Weights::steps(x) : 0;
       } else if (bins.lists(b)) {
-        const uint32_t n = atomicAdd(&p.listed[r], 1u);
-        if (n < kList) p.list[(int64_t)r * kList + n] = place_of(key_of(z[i]), first + i);
+        const uint32_t n = atomicAdd(&listed, 1u);
+        if (n < kSliceList) list[n] = place_of(key_of(z[i]), first + i);
       }
     }
-    sum = wave_sum(sum);
+    if (__ballot(sum != 0)) sum = wave_sum(sum);
     if (lane == 0) p.chunk_mass[(int64_t)r * p.max_chunks + c] = sum;
-  }
+  });
+  // the slice's list to the row's; one that is too long makes the row's too long
+  __syncthreads();
+  const uint32_t mine = listed;
+  if (tid == 0 && mine)
+    at_lds = atomicAdd(&p.listed[r], mine <= kSliceList ? mine : (uint32_t)kList + 1);
+  __syncthreads();
+  if (mine <= kSliceList)
+    for (uint32_t i = tid; i < mine; i += kThreads)
+      if (at_lds + i < kList) p.list[(int64_t)r * kList + at_lds + i] = list[i];
 }
 
 // The last token that stays, by its place.
@@ -447,9 +524,6 @@ struct Shared {
   u64 mass[kMaxChunks];   // of chunks; and of keys' bytes while a cut is sought
   uint32_t count[kMaxChunks];
   u64 list[kList], list_mass[kList + 1];  // places in order; sums of p before each
-  u64 wave_mass[kPickWaves + 2];
-  uint32_t wave_count[kPickWaves];
-  Bins bins;
   // found by one thread for all
   uint32_t key;
   int index, first_k;
@@ -495,7 +569,7 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
   constexpr int kLen = Row<TYPE>::kLen;
   float z[kLen];
   const uint32_t key = key_at(best);
-  const Weights weights{(double)value_of(key), 1.4426950408889634 / (double)set.t};
+  const Weights weights(value_of(key), set.t);
 
   // The cut at which the count of tokens, or the sum of their p, reaches a target: by the bytes of
   // the key from the top, then by number among the tokens of that key.  Leaves in sh.above the sum
@@ -632,8 +706,7 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
     for (int c = tid; c < row.chunks; c += kThreads)
       sh.mass[c] = p.chunk_mass[(int64_t)r * p.max_chunks + c];
     if (set.cut_k || set.cut_p) {
-      const Bins bins =
-          find_bins<kPickThreads>(p, set, r, sh.wave_mass, sh.wave_count, sh.bins);
+      const Bins bins = p.bins[r];
       // the list in order (bitonic)
       int n2 = 1;
       while (n2 < (int)listed) n2 *= 2;
@@ -749,7 +822,7 @@ static int chunks_of(int vocab, uint32_t flags) {
 
 size_t sample_workspace_bytes(int rows, int vocab, uint32_t flags) {
   const size_t chunks = chunks_of(vocab, flags);
-  return rows * (8 * (kMaxSlices + kBins + chunks + kList) + 4 * (kBins + 4));
+  return rows * (8 * (kMaxSlices + kBins + chunks + kList) + sizeof(Bins) + 4 * (kBins + 1));
 }
 
 hipError_t launch_sample(const wq_sample_args& a, hipStream_t stream) {
@@ -771,7 +844,8 @@ hipError_t launch_sample(const wq_sample_args& a, hipStream_t stream) {
   p.bin_mass = p.best + rows * kMaxSlices;
   p.chunk_mass = p.bin_mass + rows * kBins;
   p.list = p.chunk_mass + rows * p.max_chunks;
-  p.bin_count = reinterpret_cast<uint32_t*>(p.list + rows * kList);
+  p.bins = reinterpret_cast<Bins*>(p.list + rows * kList);
+  p.bin_count = reinterpret_cast<uint32_t*>(p.bins + rows);
   p.listed = p.bin_count + rows * kBins;
   const dim3 grid((unsigned)p.slices, (unsigned)a.rows), block(kThreads);
   const dim3 pick((unsigned)a.rows), pick_block(kPickThreads);

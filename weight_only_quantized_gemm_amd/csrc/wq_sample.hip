@@ -32,7 +32,7 @@ typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 enum LogitType { kFp16, kBf16, kFp32 };
 
 constexpr int kThreads = 512, kWaves = kThreads / 64;            // of the kernels on slices
-constexpr int kPickThreads = 256, kPickWaves = kPickThreads / 64;
+constexpr int kPickThreads = 512, kPickWaves = kPickThreads / 64;
 constexpr int kMaxSlices = 64;
 constexpr int kBins = 2048;  // the last one: p is 0 in steps of 2^-44
 constexpr double kBinsPerPower = 45.;
@@ -80,18 +80,25 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 
 // 2^t for t <= 0, to 3.7e-14 of its value: 1 + r q(r) for the remainder |r| <= 1/2 of t, q of degree
 // 8 through the Chebyshev points.
+// a * b + c with c in scalar registers: the compiler's own form copies a constant c to vector
+// registers each time, because it writes the sum over it.
+__device__ __forceinline__ double fma_s(double a, double b, double c) {
+  double d;
+  asm("v_fma_f64 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "s"(c));
+  return d;
+}
+
 __device__ __forceinline__ double exp2_neg(double t) {
-  if (!(t > -1000.)) return 0.;
+  t = fmax(t, -1100.);  // (no number too, as -inf less -inf: 0)
   const double n = rint(t), r = t - n;
-  double x = 1.0203121171282166e-07;
-  x = fma(x, r, 1.3255224873639605e-06);
-  x = fma(x, r, 1.5252686845725586e-05);
-  x = fma(x, r, 1.5403455852474373e-04);
-  x = fma(x, r, 1.333355817904396e-03);
-  x = fma(x, r, 9.618129159402536e-03);
-  x = fma(x, r, 5.550410866476042e-02);
-  x = fma(x, r, 2.402265069581299e-01);
-  x = fma(x, r, 6.931471805599453e-01);
+  double x = fma_s(1.0203121171282166e-07, r, 1.3255224873639605e-06);
+  x = fma_s(x, r, 1.5252686845725586e-05);
+  x = fma_s(x, r, 1.5403455852474373e-04);
+  x = fma_s(x, r, 1.333355817904396e-03);
+  x = fma_s(x, r, 9.618129159402536e-03);
+  x = fma_s(x, r, 5.550410866476042e-02);
+  x = fma_s(x, r, 2.402265069581299e-01);
+  x = fma_s(x, r, 6.931471805599453e-01);
   x = fma(x, r, 1.);
   return __builtin_ldexp(x, (int)n);
 }
@@ -111,6 +118,10 @@ struct Weights {
   // Never falls as z does.  Below 2^-45 there are no steps.
   __device__ static int bin(double exponent) {
     return exponent > -45. ? (int)(-exponent * kBinsPerPower) : kBins - 1;
+  }
+  // A logit below which no token has a step, and, with min_p, none stays.
+  __device__ float least(float min_p) const {
+    return logit_below(min_p > 0.f ? fmin(fmax(-45., log2((double)min_p) - 0x1p-10), 0.) : -45.);
   }
   // A logit below which no exponent is above this one.
   __device__ float logit_below(double exponent) const {
@@ -204,14 +215,16 @@ struct Row {
 };
 
 // Chunks from + wave, from + wave + waves, ... before `to`, the next one's vector in flight while
-// f(chunk, values) runs.
+// f(chunk, values) runs; `next`: the first one's, requested by first_vector.
+template <int TYPE>
+__device__ __forceinline__ u32x4 first_vector(const Row<TYPE>& row, int from, int to, int wave,
+                                              int lane) {
+  return from + wave < to ? row.raw(from + wave, lane) : u32x4{0u, 0u, 0u, 0u};
+}
 template <int TYPE, class F>
 __device__ __forceinline__ void each_chunk(const Row<TYPE>& row, int from, int to, int wave,
-                                           int waves, int lane, F f) {
-  int c = from + wave;
-  if (c >= to) return;
-  u32x4 next = row.raw(c, lane);
-  for (; c < to; c += waves) {
+                                           int waves, int lane, u32x4 next, F f) {
+  for (int c = from + wave; c < to; c += waves) {
     const u32x4 w = next;
     if (c + waves < to) next = row.raw(c + waves, lane);
     float z[Row<TYPE>::kLen];
@@ -338,35 +351,78 @@ __device__ __forceinline__ bool row_is_bad(u64 best) {
   return best == kNan || value_of(key_at(best)) == -INFINITY;
 }
 
+// The steps of p of a lane's values, kMin: those that min_p lets stay.
+template <int LEN, bool MIN>
+__device__ __forceinline__ u64 kept_steps(const Weights& weights, const float* z, uint32_t top_key,
+                                          float min_p) {
+  u64 sum = 0;
+#pragma unroll
+  for (int i = 0; i < LEN; ++i) {
+    const double x = weights.p(z[i]);
+    if constexpr (MIN)
+      sum += key_of(z[i]) == top_key || !(x < (double)min_p) ? Weights::steps(x) : 0;
+    else
+      sum += Weights::steps(x);
+  }
+  return sum;
+}
+
+// Rows that are cut: tokens and sums of p by bins.  Others: the sums of their chunks.
 template <int TYPE>
 __global__ __launch_bounds__(kThreads) void sample_bins(SampleArgs p) {
   __shared__ u64 mass[kBins];
   __shared__ uint32_t count[kBins];
   const int slice = blockIdx.x, r = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const Row<TYPE> row(p, r);
+  constexpr int kLen = Row<TYPE>::kLen;
+  int from, to;
+  slice_of(p, row, slice, from, to);
+  const u32x4 first = first_vector(row, from, to, wave, lane);
   const Setting set(p, r);
-  if (set.greedy || !(set.cut_k || set.cut_p)) return;
   const u64 best = row_best(p, r, lane);
-  if (row_is_bad(best)) return;
+  if (set.greedy || row_is_bad(best)) return;
+  const Weights weights(value_of(key_at(best)), set.t);
+  if (!(set.cut_k || set.cut_p)) {
+    const float least = weights.least(set.min_p);
+    each_chunk(row, from, to, wave, kWaves, lane, first, [&](int c, const float* z) {
+      bool any = false;
+#pragma unroll
+      for (int i = 0; i < kLen; ++i) any |= z[i] >= least;
+      u64 sum = 0;
+      if (__ballot(any)) {
+        sum = set.min_p > 0.f ? kept_steps<kLen, true>(weights, z, key_at(best), set.min_p)
+                              : kept_steps<kLen, false>(weights, z, 0, 0.f);
+        sum = wave_sum(sum);
+      }
+      if (lane == 0) p.chunk_mass[(int64_t)r * p.max_chunks + c] = sum;
+    });
+    return;
+  }
   for (int i = tid; i < kBins; i += kThreads) {
     mass[i] = 0;
     count[i] = 0;
   }
   __syncthreads();
-  const Row<TYPE> row(p, r);
-  constexpr int kLen = Row<TYPE>::kLen;
-  const Weights weights(value_of(key_at(best)), set.t);
-  const float least = weights.logit_below(-45.);
-  int from, to;
-  slice_of(p, row, slice, from, to);
-  each_chunk(row, from, to, wave, kWaves, lane, [&](int, const float* z) {
+  const float least = weights.least(0.f);
+  each_chunk(row, from, to, wave, kWaves, lane, first, [&](int, const float* z) {
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < kLen; ++i) any |= z[i] >= least;
+    if (!__ballot(any)) return;
+    int b[kLen];
+    u64 steps[kLen];
 #pragma unroll
     for (int i = 0; i < kLen; ++i) {
-      if (!(z[i] >= least)) continue;  // (tokens without a step are not counted)
       const double e = weights.exponent(z[i]);
-      const int b = Weights::bin(e);
-      if (set.cut_k) atomicAdd(&count[b], 1u);
-      if (set.cut_p) atomicAdd(&mass[b], Weights::steps(exp2_neg(e)));
+      b[i] = Weights::bin(e);
+      if (set.cut_p) steps[i] = Weights::steps(exp2_neg(e));
+    }
+#pragma unroll
+    for (int i = 0; i < kLen; ++i) {
+      if (b[i] == kBins - 1) continue;  // (tokens without a step are not counted)
+      if (set.cut_k) atomicAdd(&count[b[i]], 1u);
+      if (set.cut_p) atomicAdd(&mass[b[i]], steps[i]);
     }
   });
   __syncthreads();
@@ -463,28 +519,24 @@ __global__ __launch_bounds__(kThreads) void sample_gather(SampleArgs p) {
   __shared__ Bins bins_lds;
   const int slice = blockIdx.x, r = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const Setting set(p, r);
-  if (set.greedy) return;
-  const u64 best = row_best(p, r, lane);
-  if (row_is_bad(best)) return;
-  if (tid == 0) listed = 0;
-  __syncthreads();
-  Bins bins{-1, -1, -1, 0, 0, 0, 0};
-  if (set.cut_k || set.cut_p)
-    bins = find_bins(p, set, r, mass_lds, count_lds, bins_lds);
   const Row<TYPE> row(p, r);
   constexpr int kLen = Row<TYPE>::kLen;
-  const Weights weights(value_of(key_at(best)), set.t);
-  const int first_bin = bins.first();
-  const int last_bin = max(bins.k, bins.p_high);
-  // nothing below the last bin of the list is looked at
-  const float least =
-      weights.logit_below(last_bin >= 0 ? (last_bin + 1) * (-1. / kBinsPerPower) : -45.);
-  if (slice == 0 && tid == 0) p.bins[r] = bins;
   int from, to;
   slice_of(p, row, slice, from, to);
-  each_chunk(row, from, to, wave, kWaves, lane, [&](int c, const float* z) {
-    const int first = row.first(c, lane);
+  const u32x4 first = first_vector(row, from, to, wave, lane);
+  const Setting set(p, r);
+  const u64 best = row_best(p, r, lane);
+  if (set.greedy || row_is_bad(best) || !(set.cut_k || set.cut_p)) return;
+  if (tid == 0) listed = 0;
+  const Bins bins = find_bins(p, set, r, mass_lds, count_lds, bins_lds);
+  const Weights weights(value_of(key_at(best)), set.t);
+  const int first_bin = bins.first(), last_bin = max(bins.k, bins.p_high);
+  // nothing below the last bin of the list is looked at
+  const float least = last_bin >= 0 ? weights.logit_below((last_bin + 1) * (-1. / kBinsPerPower))
+                                    : weights.least(set.min_p);
+  if (slice == 0 && tid == 0) p.bins[r] = bins;
+  each_chunk(row, from, to, wave, kWaves, lane, first, [&](int c, const float* z) {
+    const int at = row.first(c, lane);
     u64 sum = 0;
 #pragma unroll
     for (int i = 0; i < kLen; ++i) {
@@ -496,7 +548,7 @@ __global__ __launch_bounds__(kThreads) void sample_gather(SampleArgs p) {
         sum += key_of(z[i]) == key_at(best) || !(x < (double)set.min_p) ? Weights::steps(x) : 0;
       } else if (bins.lists(b)) {
         const uint32_t n = atomicAdd(&listed, 1u);
-        if (n < kSliceList) list[n] = place_of(key_of(z[i]), first + i);
+        if (n < kSliceList) list[n] = place_of(key_of(z[i]), at + i);
       }
     }
     if (__ballot(sum != 0)) sum = wave_sum(sum);
@@ -523,7 +575,8 @@ struct Cut {
 struct Shared {
   u64 mass[kMaxChunks];   // of chunks; and of keys' bytes while a cut is sought
   uint32_t count[kMaxChunks];
-  u64 list[kList], list_mass[kList + 1];  // places in order; sums of p before each
+  u64 list[kList];        // places in order
+  u64 wave_mass[kPickWaves + 1];
   // found by one thread for all
   uint32_t key;
   int index, first_k;
@@ -549,6 +602,72 @@ __device__ T wave_prefix(T* x, int n, int lane) {
   return sum;
 }
 
+// The sum over the threads before this one; that over all of them in sums[kPickWaves].
+__device__ __forceinline__ u64 block_prefix(u64 mine, u64* sums, int tid) {
+  const int lane = tid & 63, wave = tid >> 6;
+  u64 upto = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const u64 other = __shfl_up(upto, d);
+    if (lane >= d) upto += other;
+  }
+  __syncthreads();  // (the last call's sums are read)
+  if (lane == 63) sums[wave] = upto;
+  __syncthreads();
+  u64 all = 0;
+  upto -= mine;
+#pragma unroll
+  for (int w = 0; w < kPickWaves; ++w) {
+    if (w < wave) upto += sums[w];
+    all += sums[w];
+  }
+  if (tid == 0) sums[kPickWaves] = all;
+  __syncthreads();
+  return upto;
+}
+
+// n places in descending order to `list`, by a bitonic network over the next power of two, which is
+// returned: of one place a thread, whose exchanges within a wave need no LDS, as far as it goes.
+__device__ __forceinline__ int sort_list(u64* list, const u64* from, int n, int tid) {
+  int n2 = 64;
+  while (n2 < n) n2 *= 2;
+  if (n2 <= kPickThreads) {
+    u64 x = tid < n ? from[tid] : 0;
+    for (int size = 2; size <= n2; size *= 2)
+      for (int gap = size / 2; gap > 0; gap /= 2) {
+        u64 y;
+        if (gap >= 64) {
+          __syncthreads();
+          list[tid] = x;
+          __syncthreads();
+          y = list[tid ^ gap];
+        } else {
+          y = __shfl_xor(x, gap);
+        }
+        // the first of a pair takes the larger one where the run descends
+        x = ((tid & gap) == 0) == ((tid & size) == 0) ? max(x, y) : min(x, y);
+      }
+    __syncthreads();
+    list[tid] = x;
+  } else {
+    for (int i = tid; i < n2; i += kPickThreads) list[i] = i < n ? from[i] : 0;
+    for (int size = 2; size <= n2; size *= 2)
+      for (int gap = size / 2; gap > 0; gap /= 2) {
+        __syncthreads();
+        for (int i = tid; i < n2 / 2; i += kPickThreads) {
+          const int a = 2 * i - (i & (gap - 1)), b = a + gap;
+          const u64 x = list[a], y = list[b];
+          if ((x < y) == ((a & size) == 0)) {
+            list[a] = y;
+            list[b] = x;
+          }
+        }
+      }
+  }
+  __syncthreads();
+  return n2;
+}
+
 // A work-group a row.
 template <int TYPE>
 __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
@@ -556,6 +675,10 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
   const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   constexpr int kThreads = kPickThreads, kWaves = kPickWaves;
   const Setting set(p, r);
+  const bool cuts = set.cut_k || set.cut_p;
+  const uint32_t listed = p.listed[r];
+  const float u = p.u[r];
+  const Bins bins = p.bins[r];  // (of no meaning where nothing is cut)
   const u64 best = row_best(p, r, lane);
   if (row_is_bad(best) || set.greedy) {
     if (tid == 0) {
@@ -668,92 +791,73 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
     const double x = weights.p(v);
     return kk == key || !(x < (double)set.min_p) ? x : 0.;
   };
-  const auto chunk_sums = [&](bool all) {
+  const auto chunk_sums = [&] {
     __syncthreads();
     for (int c = wave; c < row.chunks; c += kWaves) {
       row.load(c, lane, z);
       const int first = row.first(c, lane);
       u64 sum = 0;
 #pragma unroll
-      for (int i = 0; i < kLen; ++i)
-        sum += Weights::steps(!all              ? kept(z[i], first + i)
-                              : row.has(first + i) ? weights.p(z[i])
-                                                   : 0.);
+      for (int i = 0; i < kLen; ++i) sum += Weights::steps(kept(z[i], first + i));
       sum = wave_sum(sum);
       if (lane == 0) sh.mass[c] = sum;
     }
     __syncthreads();
   };
 
-  const uint32_t listed = set.cut_k || set.cut_p ? p.listed[r] : 0u;
-  if (listed > (uint32_t)kList) {
+  if (cuts && listed > (uint32_t)kList) {
     u64 total = 0;
     if (set.cut_k) {
       cut = find_cut(true, (u64)set.k);
       total = sh.above;
     } else {
-      chunk_sums(true);
-      if (wave == 0) {
-        const u64 sum = wave_prefix(sh.mass, row.chunks, lane);
-        if (lane == 0) sh.total = sum;
-      }
-      __syncthreads();
-      total = sh.total;
+      total = bins.all;
     }
     if (set.cut_p) cut = find_cut(false, set.share_of(total));
-    chunk_sums(false);
+    chunk_sums();
   } else {
     for (int c = tid; c < row.chunks; c += kThreads)
       sh.mass[c] = p.chunk_mass[(int64_t)r * p.max_chunks + c];
-    if (set.cut_k || set.cut_p) {
-      const Bins bins = p.bins[r];
-      // the list in order (bitonic)
-      int n2 = 1;
-      while (n2 < (int)listed) n2 *= 2;
-      for (int i = tid; i < n2; i += kThreads)
-        sh.list[i] = i < (int)listed ? p.list[(int64_t)r * kList + i] : 0;
-      for (int size = 2; size <= n2; size *= 2)
-        for (int gap = size / 2; gap > 0; gap /= 2) {
-          __syncthreads();
-          for (int i = tid; i < n2 / 2; i += kThreads) {
-            const int a = 2 * i - (i & (gap - 1)), b = a + gap;
-            const u64 x = sh.list[a], y = sh.list[b];
-            if ((x < y) == ((a & size) == 0)) {
-              sh.list[a] = y;
-              sh.list[b] = x;
-            }
-          }
-        }
-      __syncthreads();
-      if (tid == 0) sh.index = sh.first_k = -1;
-      __syncthreads();
-      const auto bin_at = [&](int i) {
-        return Weights::bin(weights.exponent(value_of(key_at(sh.list[i]))));
+    if (cuts && listed > 0) {
+      const int n = (int)listed;
+      const auto steps_of = [&](u64 place) {
+        return Weights::steps(weights.p(value_of(key_at(place))));
       };
-      for (int i = tid; i < (int)listed; i += kThreads) {
-        sh.list_mass[i] = Weights::steps(weights.p(value_of(key_at(sh.list[i]))));
-        if (bin_at(i) == bins.k && (i == 0 || bin_at(i - 1) != bins.k)) sh.first_k = i;
+      const auto bin_of = [&](u64 place) {
+        return Weights::bin(weights.exponent(value_of(key_at(place))));
+      };
+      if (tid == 0) sh.index = sh.first_k = -1;
+      const int n2 = sort_list(sh.list, p.list + (int64_t)r * kList, n, tid);
+      // each thread's entries: the sum of p before them
+      const int each = (n2 + kThreads - 1) / kThreads, begin = tid * each;
+      u64 mine = 0;
+      for (int i = begin; i < min(begin + each, n); ++i) {
+        mine += steps_of(sh.list[i]);
+        if (bin_of(sh.list[i]) == bins.k && (i == 0 || bin_of(sh.list[i - 1]) != bins.k))
+          sh.first_k = i;
       }
-      __syncthreads();
-      if (wave == 0) {
-        const u64 sum = wave_prefix(sh.list_mass, (int)listed, lane);
-        if (lane == 0) sh.list_mass[listed] = sum;
-      }
-      __syncthreads();
-      u64 total = bins.all;
-      int last = -1;  // entry of the cut
+      u64 before = block_prefix(mine, sh.wave_mass, tid), total = bins.all;
       if (bins.k >= 0) {
-        last = sh.first_k + set.k - (int)bins.above_k - 1;
-        total = bins.mass_above_k + sh.list_mass[last + 1] - sh.list_mass[sh.first_k];
+        // the entry of the k-th token, and the sum of p up to it
+        const int last = sh.first_k + set.k - (int)bins.above_k - 1;
+        u64 sum = before;
+        for (int i = begin; i < min(begin + each, n); ++i) {
+          if (i == sh.first_k) sh.above = sum;
+          sum += steps_of(sh.list[i]);
+          if (i == last) sh.total = sum;
+        }
+        if (tid == 0) sh.index = last;
+        __syncthreads();
+        total = bins.mass_above_k + sh.total - sh.above;
       }
       if (set.cut_p) {
         const u64 want = set.share_of(total);
-        for (int i = tid; i < (int)listed; i += kThreads)
-          if (bins.mass_above_p + sh.list_mass[i] < want &&
-              want <= bins.mass_above_p + sh.list_mass[i + 1])
-            sh.index = i;
-      } else if (tid == 0) {
-        sh.index = last;
+        u64 sum = bins.mass_above_p + before;
+        for (int i = begin; i < min(begin + each, n); ++i) {
+          const u64 next = sum + steps_of(sh.list[i]);
+          if (sum < want && want <= next) sh.index = i;
+          sum = next;
+        }
       }
       __syncthreads();
       if (sh.index >= 0) {
@@ -769,41 +873,50 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
     __syncthreads();
   }
 
+  // the chunk in which the sum passes u of the whole
+  const int each = (row.chunks + kThreads - 1) / kThreads, begin = tid * each;
+  u64 mine = 0;
+  for (int c = begin; c < min(begin + each, row.chunks); ++c) mine += sh.mass[c];
+  u64 sum = block_prefix(mine, sh.wave_mass, tid);
+  const u64 total = sh.wave_mass[kWaves];
+  const double want = u > 0.f ? (double)u * (double)total : 0.;
+  const u64 pass = want < (double)total ? min((u64)want, total - 1) : total - 1;
+  if (sum <= pass && pass < sum + mine)
+    for (int c = begin;; ++c) {
+      if (pass < sum + sh.mass[c]) {
+        sh.index = c;
+        sh.above = sum;
+        break;
+      }
+      sum += sh.mass[c];
+    }
+  __syncthreads();
   if (wave == 0) {
-    const u64 total = wave_prefix(sh.mass, row.chunks, lane);
-    const float u = p.u[r];
-    const double want = u > 0.f ? (double)u * (double)total : 0.;
-    const u64 pass = want < (double)total ? min((u64)want, total - 1) : total - 1;
-    int chunk = 0;
-    for (int c = lane; c < row.chunks; c += 64)
-      if (sh.mass[c] <= pass) chunk = c;
-#pragma unroll
-    for (int d = 32; d >= 1; d /= 2) chunk = max(chunk, __shfl_xor(chunk, d));
-    row.load(chunk, lane, z);
-    const int first = row.first(chunk, lane);
-    u64 m[kLen], mine = 0;
+    row.load(sh.index, lane, z);
+    const int first = row.first(sh.index, lane);
+    u64 m[kLen], all = 0;
 #pragma unroll
     for (int i = 0; i < kLen; ++i) {
       m[i] = Weights::steps(kept(z[i], first + i));
-      mine += m[i];
+      all += m[i];
     }
-    u64 upto = mine;
+    u64 upto = all;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
       const u64 other = __shfl_up(upto, d);
       if (lane >= d) upto += other;
     }
-    u64 sum = sh.mass[chunk] + upto - mine;
+    u64 at = sh.above + upto - all;
 #pragma unroll
     for (int i = 0; i < kLen; ++i) {
-      const u64 next = sum + m[i];
-      if (sum <= pass && pass < next) {
+      const u64 next = at + m[i];
+      if (at <= pass && pass < next) {
         p.ids[r] = first + i;
         if (p.logprob != nullptr)
           p.logprob[r] = (float)(weights.exponent(z[i]) * 0.6931471805599453 -
                                  log((double)total * 0x1p-44));
       }
-      sum = next;
+      at = next;
     }
   }
 }
@@ -853,8 +966,8 @@ hipError_t launch_sample(const wq_sample_args& a, hipStream_t stream) {
   const auto run = [&](auto type) {
     constexpr int TYPE = decltype(type)::value;
     hipLaunchKernelGGL((sample_max<TYPE>), grid, block, 0, stream, p);
-    if (cuts) hipLaunchKernelGGL((sample_bins<TYPE>), grid, block, 0, stream, p);
-    hipLaunchKernelGGL((sample_gather<TYPE>), grid, block, 0, stream, p);
+    hipLaunchKernelGGL((sample_bins<TYPE>), grid, block, 0, stream, p);
+    if (cuts) hipLaunchKernelGGL((sample_gather<TYPE>), grid, block, 0, stream, p);
     hipLaunchKernelGGL((sample_pick<TYPE>), pick, pick_block, 0, stream, p);
     return hipGetLastError();
   };

@@ -32,7 +32,7 @@ typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 enum LogitType { kFp16, kBf16, kFp32 };
 
 constexpr int kThreads = 512, kWaves = kThreads / 64;            // of the kernels on slices
-constexpr int kPickThreads = 512, kPickWaves = kPickThreads / 64;
+constexpr int kPickThreads = 1024, kPickWaves = kPickThreads / 64;
 constexpr int kMaxSlices = 64;
 constexpr int kBins = 2048;  // the last one: p is 0 in steps of 2^-44
 constexpr double kBinsPerPower = 45.;
@@ -380,6 +380,10 @@ __global__ __launch_bounds__(kThreads) void sample_bins(SampleArgs p) {
   slice_of(p, row, slice, from, to);
   const u32x4 first = first_vector(row, from, to, wave, lane);
   const Setting set(p, r);
+  for (int i = tid; i < kBins; i += kThreads) {
+    mass[i] = 0;
+    count[i] = 0;
+  }
   const u64 best = row_best(p, r, lane);
   if (set.greedy || row_is_bad(best)) return;
   const Weights weights(value_of(key_at(best)), set.t);
@@ -398,10 +402,6 @@ __global__ __launch_bounds__(kThreads) void sample_bins(SampleArgs p) {
       if (lane == 0) p.chunk_mass[(int64_t)r * p.max_chunks + c] = sum;
     });
     return;
-  }
-  for (int i = tid; i < kBins; i += kThreads) {
-    mass[i] = 0;
-    count[i] = 0;
   }
   __syncthreads();
   const float least = weights.least(0.f);
@@ -432,17 +432,31 @@ __global__ __launch_bounds__(kThreads) void sample_bins(SampleArgs p) {
   }
 }
 
+// A thread's bins of the row, requested before they are known to be needed.
+struct MyBins {
+  static constexpr int kEach = kBins / kThreads;
+  u64 m[kEach];
+  uint32_t n[kEach];
+  __device__ MyBins(const SampleArgs& p, int r, int tid) {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      m[i] = p.bin_mass[(int64_t)r * kBins + kEach * tid + i];
+      n[i] = p.bin_count[(int64_t)r * kBins + kEach * tid + i];
+    }
+  }
+};
+
 // The bins that are sought, by the whole work-group.
-__device__ Bins find_bins(const SampleArgs& p, const Setting& set, int r, u64* mass_lds,
-                          uint32_t* count_lds, Bins& out) {
-  constexpr int kEach = kBins / kThreads;
+__device__ __forceinline__ Bins find_bins(const MyBins& my, const Setting& set, u64* mass_lds,
+                                          uint32_t* count_lds, Bins& out) {
+  constexpr int kEach = MyBins::kEach;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  u64 m[kEach], mass = 0;
-  uint32_t n[kEach], count = 0;
+  const u64* m = my.m;
+  const uint32_t* n = my.n;
+  u64 mass = 0;
+  uint32_t count = 0;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    m[i] = set.cut_p ? p.bin_mass[(int64_t)r * kBins + kEach * tid + i] : 0;
-    n[i] = set.cut_k ? p.bin_count[(int64_t)r * kBins + kEach * tid + i] : 0;
     mass += m[i];
     count += n[i];
   }
@@ -524,11 +538,12 @@ __global__ __launch_bounds__(kThreads) void sample_gather(SampleArgs p) {
   int from, to;
   slice_of(p, row, slice, from, to);
   const u32x4 first = first_vector(row, from, to, wave, lane);
+  const MyBins my(p, r, tid);
   const Setting set(p, r);
   const u64 best = row_best(p, r, lane);
   if (set.greedy || row_is_bad(best) || !(set.cut_k || set.cut_p)) return;
   if (tid == 0) listed = 0;
-  const Bins bins = find_bins(p, set, r, mass_lds, count_lds, bins_lds);
+  const Bins bins = find_bins(my, set, mass_lds, count_lds, bins_lds);
   const Weights weights(value_of(key_at(best)), set.t);
   const int first_bin = bins.first(), last_bin = max(bins.k, bins.p_high);
   // nothing below the last bin of the list is looked at
@@ -538,17 +553,38 @@ __global__ __launch_bounds__(kThreads) void sample_gather(SampleArgs p) {
   each_chunk(row, from, to, wave, kWaves, lane, first, [&](int c, const float* z) {
     const int at = row.first(c, lane);
     u64 sum = 0;
+    const auto put = [&](int i) {
+      const uint32_t n = atomicAdd(&listed, 1u);
+      if (n < kSliceList) list[n] = place_of(key_of(z[i]), at + i);
+    };
+    int busy = 0;  // elements that some lane has to look at
 #pragma unroll
-    for (int i = 0; i < kLen; ++i) {
-      if (!(z[i] >= least)) continue;
-      const double e = weights.exponent(z[i]);
-      const int b = Weights::bin(e);
-      if (b < first_bin) {
-        const double x = exp2_neg(e);
-        sum += key_of(z[i]) == key_at(best) || !(x < (double)set.min_p) ? Weights::steps(x) : 0;
-      } else if (bins.lists(b)) {
-        const uint32_t n = atomicAdd(&listed, 1u);
-        if (n < kSliceList) list[n] = place_of(key_of(z[i]), at + i);
+    for (int i = 0; i < kLen; ++i) busy += __ballot(z[i] >= least) != 0;
+    if (busy > kLen / 2) {  // all of them side by side, without branches
+      bool in_list[kLen];
+#pragma unroll
+      for (int i = 0; i < kLen; ++i) {
+        const double e = weights.exponent(z[i]), x = exp2_neg(e);
+        const int b = Weights::bin(e);
+        in_list[i] = b >= first_bin && bins.lists(b);
+        const bool stays = key_of(z[i]) == key_at(best) || !(x < (double)set.min_p);
+        sum += b < first_bin && stays ? Weights::steps(x) : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < kLen; ++i)
+        if (in_list[i]) put(i);
+    } else if (busy > 0) {
+#pragma unroll
+      for (int i = 0; i < kLen; ++i) {
+        if (!(z[i] >= least)) continue;
+        const double e = weights.exponent(z[i]);
+        const int b = Weights::bin(e);
+        if (b < first_bin) {
+          const double x = exp2_neg(e);
+          sum += key_of(z[i]) == key_at(best) || !(x < (double)set.min_p) ? Weights::steps(x) : 0;
+        } else if (bins.lists(b)) {
+          put(i);
+        }
       }
     }
     if (__ballot(sum != 0)) sum = wave_sum(sum);
@@ -627,12 +663,12 @@ __device__ __forceinline__ u64 block_prefix(u64 mine, u64* sums, int tid) {
 }
 
 // n places in descending order to `list`, by a bitonic network over the next power of two, which is
-// returned: of one place a thread, whose exchanges within a wave need no LDS, as far as it goes.
-__device__ __forceinline__ int sort_list(u64* list, const u64* from, int n, int tid) {
-  int n2 = 64;
+// returned: of one place a thread (`mine`), whose exchanges within a wave need no LDS, as far as it goes.
+__device__ __forceinline__ int sort_list(u64* list, u64 mine, const u64* from, int n, int tid) {
+  int n2 = 1;
   while (n2 < n) n2 *= 2;
   if (n2 <= kPickThreads) {
-    u64 x = tid < n ? from[tid] : 0;
+    u64 x = tid < n ? mine : 0;
     for (int size = 2; size <= n2; size *= 2)
       for (int gap = size / 2; gap > 0; gap /= 2) {
         u64 y;
@@ -675,10 +711,15 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
   const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   constexpr int kThreads = kPickThreads, kWaves = kPickWaves;
   const Setting set(p, r);
+  const Row<TYPE> row(p, r);
+  for (int c = tid; c < row.chunks; c += kThreads)
+    sh.mass[c] = p.chunk_mass[(int64_t)r * p.max_chunks + c];
   const bool cuts = set.cut_k || set.cut_p;
   const uint32_t listed = p.listed[r];
   const float u = p.u[r];
-  const Bins bins = p.bins[r];  // (of no meaning where nothing is cut)
+  // (what no kernel has written for this row is not used)
+  const Bins bins = p.bins[r];
+  const u64 first_listed = tid < kList ? p.list[(int64_t)r * kList + tid] : 0;
   const u64 best = row_best(p, r, lane);
   if (row_is_bad(best) || set.greedy) {
     if (tid == 0) {
@@ -688,7 +729,6 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
     }
     return;
   }
-  const Row<TYPE> row(p, r);
   constexpr int kLen = Row<TYPE>::kLen;
   float z[kLen];
   const uint32_t key = key_at(best);
@@ -816,8 +856,6 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
     if (set.cut_p) cut = find_cut(false, set.share_of(total));
     chunk_sums();
   } else {
-    for (int c = tid; c < row.chunks; c += kThreads)
-      sh.mass[c] = p.chunk_mass[(int64_t)r * p.max_chunks + c];
     if (cuts && listed > 0) {
       const int n = (int)listed;
       const auto steps_of = [&](u64 place) {
@@ -827,7 +865,7 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
         return Weights::bin(weights.exponent(value_of(key_at(place))));
       };
       if (tid == 0) sh.index = sh.first_k = -1;
-      const int n2 = sort_list(sh.list, p.list + (int64_t)r * kList, n, tid);
+      const int n2 = sort_list(sh.list, first_listed, p.list + (int64_t)r * kList, n, tid);
       // each thread's entries: the sum of p before them
       const int each = (n2 + kThreads - 1) / kThreads, begin = tid * each;
       u64 mine = 0;
@@ -892,7 +930,9 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
     }
   __syncthreads();
   if (wave == 0) {
-    row.load(sh.index, lane, z);
+    const u32x4 w = row.raw(sh.index, lane);
+    const double whole = log((double)total * 0x1p-44);  // (while the vector is in flight)
+    Row<TYPE>::values(w, z);
     const int first = row.first(sh.index, lane);
     u64 m[kLen], all = 0;
 #pragma unroll
@@ -913,8 +953,7 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
       if (at <= pass && pass < next) {
         p.ids[r] = first + i;
         if (p.logprob != nullptr)
-          p.logprob[r] = (float)(weights.exponent(z[i]) * 0.6931471805599453 -
-                                 log((double)total * 0x1p-44));
+          p.logprob[r] = (float)(weights.exponent(z[i]) * 0.6931471805599453 - whole);
       }
       at = next;
     }

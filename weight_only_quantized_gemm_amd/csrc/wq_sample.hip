@@ -32,11 +32,11 @@ typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 enum LogitType { kFp16, kBf16, kFp32 };
 
 constexpr int kThreads = 512, kWaves = kThreads / 64;            // of the kernels on slices
-constexpr int kPickThreads = 1024, kPickWaves = kPickThreads / 64;
+constexpr int kPickThreads = 256, kPickWaves = kPickThreads / 64;
 constexpr int kMaxSlices = 64;
 constexpr int kBins = 2048;  // the last one: p is 0 in steps of 2^-44
 constexpr double kBinsPerPower = 45.;
-constexpr int kList = 4096, kSliceList = 2048;
+constexpr int kList = 16 * kPickThreads, kSliceList = 2048;
 constexpr int kMaxChunks = WQ_SAMPLE_MAX_VOCAB / 256 + 1;
 
 // Where the cuts lie: the bins of the list, and what is above them.
@@ -233,10 +233,46 @@ __device__ __forceinline__ void each_chunk(const Row<TYPE>& row, int from, int t
   }
 }
 
-__device__ __forceinline__ u64 wave_sum(u64 x) {
-#pragma unroll
-  for (int d = 32; d >= 1; d /= 2) x += __shfl_xor(x, d);
+// A step of a scan over the wave's lanes: what lies CTRL before a lane, 0 where nothing does or the
+// lane's row is not in ROWS.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t lanes_before(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xf, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ u64 lanes_before(u64 x) {
+  return lanes_before<CTRL, ROWS>((uint32_t)x) |
+         (u64)lanes_before<CTRL, ROWS>((uint32_t)(x >> 32)) << 32;
+}
+// Inclusive scan: row_shr 1, 2, 4 and 8 within rows of 16 lanes, then a row's last lane to the next
+// row, and the first half's last to the second.
+template <class T, class F>
+__device__ __forceinline__ T wave_scan(T x, F f) {
+  x = f(x, lanes_before<0x111, 0xf>(x));
+  x = f(x, lanes_before<0x112, 0xf>(x));
+  x = f(x, lanes_before<0x114, 0xf>(x));
+  x = f(x, lanes_before<0x118, 0xf>(x));
+  x = f(x, lanes_before<0x142, 0xa>(x));
+  x = f(x, lanes_before<0x143, 0xc>(x));
   return x;
+}
+template <class T>
+__device__ __forceinline__ T wave_upto(T x) {
+  return wave_scan(x, [](T a, T b) { return a + b; });
+}
+__device__ __forceinline__ uint32_t last_lane(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+}
+__device__ __forceinline__ u64 last_lane(u64 x) {
+  return last_lane((uint32_t)x) | (u64)last_lane((uint32_t)(x >> 32)) << 32;
+}
+template <class T>
+__device__ __forceinline__ T wave_sum(T x) {
+  return last_lane(wave_upto(x));
+}
+template <class T>
+__device__ __forceinline__ T wave_max(T x) {
+  return last_lane(wave_scan(x, [](T a, T b) { return a > b ? a : b; }));
 }
 
 // The slice's chunks.
@@ -312,9 +348,7 @@ __global__ __launch_bounds__(kThreads) void sample_max(SampleArgs p) {
              (x >> 16) > (Row<TYPE>::kLowest & 0x7fffu);
   }
   // the first token of the wave's largest value, in one of the lanes that have it
-  uint32_t key = key_of(top), wave_key = key;
-#pragma unroll
-  for (int d = 32; d >= 1; d /= 2) wave_key = max(wave_key, (uint32_t)__shfl_xor(wave_key, d));
+  const uint32_t key = key_of(top), wave_key = wave_max(key);
   u64 best = 0;
   if (from + wave < to && key == wave_key) {
     float z[kLen];
@@ -324,8 +358,7 @@ __global__ __launch_bounds__(kThreads) void sample_max(SampleArgs p) {
       if (z[i] == top) best = place_of(key, row.first(top_chunk, lane) + i);
   }
   if (nan) best = kNan;
-#pragma unroll
-  for (int d = 32; d >= 1; d /= 2) best = max(best, (u64)__shfl_xor(best, d));
+  best = wave_max(best);
   if (lane == 0) best_lds[wave] = best;
   // the row's bins and list start empty
   for (int i = slice * kThreads + tid; i < kBins; i += p.slices * kThreads) {
@@ -342,10 +375,7 @@ __global__ __launch_bounds__(kThreads) void sample_max(SampleArgs p) {
 
 // The row's largest logit, as a place, by each wave.
 __device__ __forceinline__ u64 row_best(const SampleArgs& p, int r, int lane) {
-  u64 best = lane < p.slices ? p.best[(int64_t)r * p.slices + lane] : 0;
-#pragma unroll
-  for (int d = 32; d >= 1; d /= 2) best = max(best, (u64)__shfl_xor(best, d));
-  return best;
+  return wave_max(lane < p.slices ? p.best[(int64_t)r * p.slices + lane] : 0);
 }
 __device__ __forceinline__ bool row_is_bad(u64 best) {
   return best == kNan || value_of(key_at(best)) == -INFINITY;
@@ -460,17 +490,8 @@ __device__ __forceinline__ Bins find_bins(const MyBins& my, const Setting& set, 
     mass += m[i];
     count += n[i];
   }
-  u64 mass_to = mass;
-  uint32_t count_to = count;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const u64 om = __shfl_up(mass_to, d);
-    const uint32_t on = __shfl_up(count_to, d);
-    if (lane >= d) {
-      mass_to += om;
-      count_to += on;
-    }
-  }
+  u64 mass_to = wave_upto(mass);
+  uint32_t count_to = wave_upto(count);
   if (lane == 63) {
     mass_lds[wave] = mass_to;
     count_lds[wave] = count_to;
@@ -626,14 +647,9 @@ __device__ T wave_prefix(T* x, int n, int lane) {
   T sum = 0;
   for (int i = 0; i < n; i += 64) {
     const T mine = i + lane < n ? x[i + lane] : 0;
-    T upto = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const T other = __shfl_up(upto, d);
-      if (lane >= d) upto += other;
-    }
+    const T upto = wave_upto(mine);
     if (i + lane < n) x[i + lane] = sum + upto - mine;
-    sum += __shfl(upto, 63);
+    sum += last_lane(upto);
   }
   return sum;
 }
@@ -641,12 +657,7 @@ __device__ T wave_prefix(T* x, int n, int lane) {
 // The sum over the threads before this one; that over all of them in sums[kPickWaves].
 __device__ __forceinline__ u64 block_prefix(u64 mine, u64* sums, int tid) {
   const int lane = tid & 63, wave = tid >> 6;
-  u64 upto = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const u64 other = __shfl_up(upto, d);
-    if (lane >= d) upto += other;
-  }
+  u64 upto = wave_upto(mine);
   __syncthreads();  // (the last call's sums are read)
   if (lane == 63) sums[wave] = upto;
   __syncthreads();
@@ -662,46 +673,62 @@ __device__ __forceinline__ u64 block_prefix(u64 mine, u64* sums, int tid) {
   return upto;
 }
 
-// n places in descending order to `list`, by a bitonic network over the next power of two, which is
-// returned: of one place a thread (`mine`), whose exchanges within a wave need no LDS, as far as it goes.
-__device__ __forceinline__ int sort_list(u64* list, u64 mine, const u64* from, int n, int tid) {
-  int n2 = 1;
-  while (n2 < n) n2 *= 2;
-  if (n2 <= kPickThreads) {
-    u64 x = tid < n ? mine : 0;
-    for (int size = 2; size <= n2; size *= 2)
-      for (int gap = size / 2; gap > 0; gap /= 2) {
-        u64 y;
-        if (gap >= 64) {
-          __syncthreads();
-          list[tid] = x;
-          __syncthreads();
-          y = list[tid ^ gap];
-        } else {
-          y = __shfl_xor(x, gap);
-        }
-        // the first of a pair takes the larger one where the run descends
-        x = ((tid & gap) == 0) == ((tid & size) == 0) ? max(x, y) : min(x, y);
-      }
-    __syncthreads();
-    list[tid] = x;
-  } else {
-    for (int i = tid; i < n2; i += kPickThreads) list[i] = i < n ? from[i] : 0;
-    for (int size = 2; size <= n2; size *= 2)
-      for (int gap = size / 2; gap > 0; gap /= 2) {
-        __syncthreads();
-        for (int i = tid; i < n2 / 2; i += kPickThreads) {
-          const int a = 2 * i - (i & (gap - 1)), b = a + gap;
-          const u64 x = list[a], y = list[b];
-          if ((x < y) == ((a & size) == 0)) {
-            list[a] = y;
-            list[b] = x;
+// n2 places, EACH of a thread's (place j * threads + tid in its j-th), in descending order to `list`, by
+// a bitonic network: exchanges within a thread and a wave need no LDS.
+template <int EACH>
+__device__ __forceinline__ void sort_places(u64* list, u64* x, int n2, int tid) {
+  for (int size = 2; size <= n2; size *= 2) {
+    for (int gap = size / 2; gap > 0; gap /= 2) {
+      // the first of a pair takes the larger one where the run descends
+      if (gap >= kPickThreads) {
+#pragma unroll
+        for (int j = 0; j < EACH; ++j) {
+#pragma unroll
+          for (int half = 1; half < EACH; half *= 2) {
+            if (gap != half * kPickThreads || (j & half)) continue;
+            const u64 a = x[j], b = x[j | half];
+            const bool down = ((j * kPickThreads + tid) & size) == 0;
+            x[j] = down == (a > b) ? a : b;
+            x[j | half] = down == (a > b) ? b : a;
           }
         }
+        continue;
       }
+      u64 y[EACH];
+      if (gap >= 64) {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < EACH; ++j) list[j * kPickThreads + tid] = x[j];
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < EACH; ++j) y[j] = list[j * kPickThreads + (tid ^ gap)];
+      } else {
+#pragma unroll
+        for (int j = 0; j < EACH; ++j) y[j] = __shfl_xor(x[j], gap);
+      }
+#pragma unroll
+      for (int j = 0; j < EACH; ++j) {
+        const bool down = ((j * kPickThreads + tid) & size) == 0;
+        x[j] = ((tid & gap) == 0) == down ? max(x[j], y[j]) : min(x[j], y[j]);
+      }
+    }
   }
   __syncthreads();
-  return n2;
+#pragma unroll
+  for (int j = 0; j < EACH; ++j) list[j * kPickThreads + tid] = x[j];
+  __syncthreads();
+}
+
+template <int EACH>
+__device__ __forceinline__ void sort_list(u64* list, u64 mine, const u64* from, int n, int n2,
+                                          int tid) {
+  u64 x[EACH];
+#pragma unroll
+  for (int j = 0; j < EACH; ++j) {
+    const int i = j * kPickThreads + tid;
+    x[j] = i < n ? (j == 0 ? mine : from[i]) : 0;
+  }
+  sort_places<EACH>(list, x, n2, tid);
 }
 
 // A work-group a row.
@@ -784,11 +811,10 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
     for (int c = wave; c < row.chunks; c += kWaves) {
       row.load(c, lane, z);
       const int first = row.first(c, lane);
-      int n = 0;
+      uint32_t n = 0;
 #pragma unroll
       for (int i = 0; i < kLen; ++i) n += row.has(first + i) && key_of(z[i]) == prefix;
-#pragma unroll
-      for (int d = 32; d >= 1; d /= 2) n += __shfl_xor(n, d);
+      n = wave_sum(n);
       if (lane == 0) sh.count[c] = n;
     }
     __syncthreads();
@@ -799,22 +825,16 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
         sh.index = row.vocab - 1;
       }
       // the chunk in which the left-th of them lies, and it there
-      int chunk = 0;
+      uint32_t last = 0;
       for (int c = lane; c < row.chunks; c += 64)
-        if (sh.count[c] < left) chunk = c;
-#pragma unroll
-      for (int d = 32; d >= 1; d /= 2) chunk = max(chunk, __shfl_xor(chunk, d));
+        if (sh.count[c] < left) last = c;
+      const int chunk = (int)wave_max(last);
       row.load(chunk, lane, z);
       const int first = row.first(chunk, lane);
       uint32_t mine = 0;
 #pragma unroll
       for (int i = 0; i < kLen; ++i) mine += row.has(first + i) && key_of(z[i]) == prefix;
-      uint32_t upto = mine;
-#pragma unroll
-      for (int d = 1; d < 64; d *= 2) {
-        const uint32_t other = __shfl_up(upto, d);
-        if (lane >= d) upto += other;
-      }
+      const uint32_t upto = wave_upto(mine);
       u64 n = sh.count[chunk] + upto - mine;
 #pragma unroll
       for (int i = 0; i < kLen; ++i)
@@ -865,7 +885,15 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
         return Weights::bin(weights.exponent(value_of(key_at(place))));
       };
       if (tid == 0) sh.index = sh.first_k = -1;
-      const int n2 = sort_list(sh.list, first_listed, p.list + (int64_t)r * kList, n, tid);
+      const u64* places = p.list + (int64_t)r * kList;
+      int n2 = 1;
+      while (n2 < n) n2 *= 2;
+      if (n2 <= kPickThreads)
+        sort_list<1>(sh.list, first_listed, places, n, n2, tid);
+      else if (n2 <= 4 * kPickThreads)
+        sort_list<4>(sh.list, first_listed, places, n, n2, tid);
+      else
+        sort_list<16>(sh.list, first_listed, places, n, n2, tid);
       // each thread's entries: the sum of p before them
       const int each = (n2 + kThreads - 1) / kThreads, begin = tid * each;
       u64 mine = 0;
@@ -940,12 +968,7 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
       m[i] = Weights::steps(kept(z[i], first + i));
       all += m[i];
     }
-    u64 upto = all;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const u64 other = __shfl_up(upto, d);
-      if (lane >= d) upto += other;
-    }
+    const u64 upto = wave_upto(all);
     u64 at = sh.above + upto - all;
 #pragma unroll
     for (int i = 0; i < kLen; ++i) {

@@ -32,11 +32,11 @@ typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 enum LogitType { kFp16, kBf16, kFp32 };
 
 constexpr int kThreads = 512, kWaves = kThreads / 64;            // of the kernels on slices
-constexpr int kPickThreads = 256, kPickWaves = kPickThreads / 64;
+constexpr int kPickThreads = 256, kPickWaves = kPickThreads / 64;  // (a thread a byte value)
 constexpr int kMaxSlices = 64;
 constexpr int kBins = 2048;  // the last one: p is 0 in steps of 2^-44
 constexpr double kBinsPerPower = 45.;
-constexpr int kList = 16 * kPickThreads, kSliceList = 2048;
+constexpr int kList = 2048;
 constexpr int kMaxChunks = WQ_SAMPLE_MAX_VOCAB / 256 + 1;
 
 // Where the cuts lie: the bins of the list, and what is above them.
@@ -265,6 +265,10 @@ __device__ __forceinline__ uint32_t last_lane(uint32_t x) {
 }
 __device__ __forceinline__ u64 last_lane(u64 x) {
   return last_lane((uint32_t)x) | (u64)last_lane((uint32_t)(x >> 32)) << 32;
+}
+__device__ __forceinline__ u64 lane_at(u64 x, int lane) {
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, lane) |
+         (u64)(uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), lane) << 32;
 }
 template <class T>
 __device__ __forceinline__ T wave_sum(T x) {
@@ -549,7 +553,7 @@ __device__ __forceinline__ Bins find_bins(const MyBins& my, const Setting& set, 
 
 template <int TYPE>
 __global__ __launch_bounds__(kThreads) void sample_gather(SampleArgs p) {
-  __shared__ u64 mass_lds[kWaves + 2], list[kSliceList];
+  __shared__ u64 mass_lds[kWaves + 2], list[kList];
   __shared__ uint32_t count_lds[kWaves], listed, at_lds;
   __shared__ Bins bins_lds;
   const int slice = blockIdx.x, r = blockIdx.y;
@@ -576,7 +580,7 @@ __global__ __launch_bounds__(kThreads) void sample_gather(SampleArgs p) {
     u64 sum = 0;
     const auto put = [&](int i) {
       const uint32_t n = atomicAdd(&listed, 1u);
-      if (n < kSliceList) list[n] = place_of(key_of(z[i]), at + i);
+      if (n < kList) list[n] = place_of(key_of(z[i]), at + i);
     };
     int busy = 0;  // elements that some lane has to look at
 #pragma unroll
@@ -615,9 +619,9 @@ __global__ __launch_bounds__(kThreads) void sample_gather(SampleArgs p) {
   __syncthreads();
   const uint32_t mine = listed;
   if (tid == 0 && mine)
-    at_lds = atomicAdd(&p.listed[r], mine <= kSliceList ? mine : (uint32_t)kList + 1);
+    at_lds = atomicAdd(&p.listed[r], mine <= kList ? mine : (uint32_t)kList + 1);
   __syncthreads();
-  if (mine <= kSliceList)
+  if (mine <= kList)
     for (uint32_t i = tid; i < mine; i += kThreads)
       if (at_lds + i < kList) p.list[(int64_t)r * kList + at_lds + i] = list[i];
 }
@@ -632,12 +636,13 @@ struct Cut {
 struct Shared {
   u64 mass[kMaxChunks];   // of chunks; and of keys' bytes while a cut is sought
   uint32_t count[kMaxChunks];
-  u64 list[kList];        // places in order
-  u64 wave_mass[kPickWaves + 1];
+  u64 list[kList], list_mass[kList];  // places, and their steps of p
+  u64 byte_mass[kPickThreads], wave_mass[kPickWaves + 1];
+  uint32_t byte_count[kPickThreads];
   // found by one thread for all
   uint32_t key;
-  int index, first_k;
-  u64 above, total;
+  int index;
+  u64 above, total, place;
   uint32_t above_count;
 };
 
@@ -673,64 +678,6 @@ __device__ __forceinline__ u64 block_prefix(u64 mine, u64* sums, int tid) {
   return upto;
 }
 
-// n2 places, EACH of a thread's (place j * threads + tid in its j-th), in descending order to `list`, by
-// a bitonic network: exchanges within a thread and a wave need no LDS.
-template <int EACH>
-__device__ __forceinline__ void sort_places(u64* list, u64* x, int n2, int tid) {
-  for (int size = 2; size <= n2; size *= 2) {
-    for (int gap = size / 2; gap > 0; gap /= 2) {
-      // the first of a pair takes the larger one where the run descends
-      if (gap >= kPickThreads) {
-#pragma unroll
-        for (int j = 0; j < EACH; ++j) {
-#pragma unroll
-          for (int half = 1; half < EACH; half *= 2) {
-            if (gap != half * kPickThreads || (j & half)) continue;
-            const u64 a = x[j], b = x[j | half];
-            const bool down = ((j * kPickThreads + tid) & size) == 0;
-            x[j] = down == (a > b) ? a : b;
-            x[j | half] = down == (a > b) ? b : a;
-          }
-        }
-        continue;
-      }
-      u64 y[EACH];
-      if (gap >= 64) {
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < EACH; ++j) list[j * kPickThreads + tid] = x[j];
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < EACH; ++j) y[j] = list[j * kPickThreads + (tid ^ gap)];
-      } else {
-#pragma unroll
-        for (int j = 0; j < EACH; ++j) y[j] = __shfl_xor(x[j], gap);
-      }
-#pragma unroll
-      for (int j = 0; j < EACH; ++j) {
-        const bool down = ((j * kPickThreads + tid) & size) == 0;
-        x[j] = ((tid & gap) == 0) == down ? max(x[j], y[j]) : min(x[j], y[j]);
-      }
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < EACH; ++j) list[j * kPickThreads + tid] = x[j];
-  __syncthreads();
-}
-
-template <int EACH>
-__device__ __forceinline__ void sort_list(u64* list, u64 mine, const u64* from, int n, int n2,
-                                          int tid) {
-  u64 x[EACH];
-#pragma unroll
-  for (int j = 0; j < EACH; ++j) {
-    const int i = j * kPickThreads + tid;
-    x[j] = i < n ? (j == 0 ? mine : from[i]) : 0;
-  }
-  sort_places<EACH>(list, x, n2, tid);
-}
-
 // A work-group a row.
 template <int TYPE>
 __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
@@ -746,7 +693,7 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
   const float u = p.u[r];
   // (what no kernel has written for this row is not used)
   const Bins bins = p.bins[r];
-  const u64 first_listed = tid < kList ? p.list[(int64_t)r * kList + tid] : 0;
+  const u64 first_listed = p.list[(int64_t)r * kList + lane];
   const u64 best = row_best(p, r, lane);
   if (row_is_bad(best) || set.greedy) {
     if (tid == 0) {
@@ -884,55 +831,108 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
       const auto bin_of = [&](u64 place) {
         return Weights::bin(weights.exponent(value_of(key_at(place))));
       };
-      if (tid == 0) sh.index = sh.first_k = -1;
       const u64* places = p.list + (int64_t)r * kList;
-      int n2 = 1;
-      while (n2 < n) n2 *= 2;
-      if (n2 <= kPickThreads)
-        sort_list<1>(sh.list, first_listed, places, n, n2, tid);
-      else if (n2 <= 4 * kPickThreads)
-        sort_list<4>(sh.list, first_listed, places, n, n2, tid);
-      else
-        sort_list<16>(sh.list, first_listed, places, n, n2, tid);
-      // each thread's entries: the sum of p before them
-      const int each = (n2 + kThreads - 1) / kThreads, begin = tid * each;
-      u64 mine = 0;
-      for (int i = begin; i < min(begin + each, n); ++i) {
-        mine += steps_of(sh.list[i]);
-        if (bin_of(sh.list[i]) == bins.k && (i == 0 || bin_of(sh.list[i - 1]) != bins.k))
-          sh.first_k = i;
-      }
-      u64 before = block_prefix(mine, sh.wave_mass, tid), total = bins.all;
-      if (bins.k >= 0) {
-        // the entry of the k-th token, and the sum of p up to it
-        const int last = sh.first_k + set.k - (int)bins.above_k - 1;
-        u64 sum = before;
-        for (int i = begin; i < min(begin + each, n); ++i) {
-          if (i == sh.first_k) sh.above = sum;
-          sum += steps_of(sh.list[i]);
-          if (i == last) sh.total = sum;
+      u64 place = 0;  // of the cut; 0: there is none
+      if (n <= 64) {
+        // every wave by itself: a lane an entry, which counts what is before it
+        const bool in = lane < n, in_k = in && bin_of(first_listed) == bins.k;
+        const u64 x = in ? first_listed : 0, m = in ? steps_of(x) : 0;
+        const u64 k_lanes = __ballot(in_k);
+        u64 before = 0, before_k = 0;
+        int rank_k = 0;
+        for (int j = 0; j < n; ++j) {
+          const u64 y = lane_at(x, j), mass = lane_at(m, j);
+          const bool above = y > x, of_k = (k_lanes >> j) & 1;
+          before += above ? mass : 0;
+          before_k += above && of_k ? mass : 0;
+          rank_k += above && of_k;
         }
-        if (tid == 0) sh.index = last;
+        u64 total = bins.all;
+        if (bins.k >= 0) {
+          const u64 hit = __ballot(in_k && rank_k == set.k - (int)bins.above_k - 1);
+          const int at = __builtin_ctzll(hit);
+          place = lane_at(x, at);
+          total = bins.mass_above_k + lane_at(before_k + m, at);
+        }
+        if (set.cut_p) {
+          const u64 want = set.share_of(total), sum = bins.mass_above_p + before;
+          const u64 hit = __ballot(in && sum < want && want <= sum + m);
+          if (hit) place = lane_at(x, __builtin_ctzll(hit));
+        }
+        if (wave == 0 && in) sh.list[lane] = x;
+      } else {
+        u64 vary = 0;
+        for (int i = tid; i < n; i += kThreads) {
+          const u64 x = places[i];
+          sh.list[i] = x;
+          sh.list_mass[i] = steps_of(x);
+          vary |= x ^ first_listed;
+        }
+        // (first_listed is another entry for each lane: the bits in which any two differ are among
+        // these or in which those do)
+        vary |= first_listed ^ lane_at(first_listed, 0);
+        vary = wave_scan(vary, [](u64 a, u64 b) { return a | b; });
+        if (lane == 63) sh.wave_mass[wave] = vary;
         __syncthreads();
-        total = bins.mass_above_k + sh.total - sh.above;
-      }
-      if (set.cut_p) {
-        const u64 want = set.share_of(total);
-        u64 sum = bins.mass_above_p + before;
-        for (int i = begin; i < min(begin + each, n); ++i) {
-          const u64 next = sum + steps_of(sh.list[i]);
-          if (sum < want && want <= next) sh.index = i;
-          sum = next;
+        vary = 0;
+        for (int w = 0; w < kWaves; ++w) vary |= sh.wave_mass[w];
+        // The place at which the count or the sums of p of the entries, those of bin k alone or all,
+        // pass a target; by the bytes in which entries differ, from the top.  `sum`: of p up to it.
+        const auto find_place = [&](bool of_k, u64 target, u64& sum) -> u64 {
+          u64 prefix = 0, above = 0;
+          sum = 0;
+          for (int shift = 56; shift >= 0; shift -= 8) {
+            if (((vary >> shift) & 255) == 0) {
+              prefix |= sh.list[0] & (255ull << shift);
+              continue;
+            }
+            __syncthreads();
+            sh.byte_mass[tid] = 0;
+            sh.byte_count[tid] = 0;
+            __syncthreads();
+            for (int i = tid; i < n; i += kThreads) {
+              const u64 x = sh.list[i];
+              if (((x ^ prefix) & (~255ull << shift)) != 0 ||
+                  (of_k && bin_of(x) != bins.k))
+                continue;
+              const int d = 255 - (int)(x >> shift & 255);
+              atomicAdd(&sh.byte_count[d], 1u);
+              atomicAdd(&sh.byte_mass[d], sh.list_mass[i]);
+            }
+            __syncthreads();
+            const u64 mine = sh.byte_mass[tid], n_mine = sh.byte_count[tid];
+            const u64 mass_before = block_prefix(mine, sh.wave_mass, tid);
+            const u64 before = of_k ? block_prefix(n_mine, sh.wave_mass, tid) : mass_before;
+            const u64 size = of_k ? n_mine : mine;
+            if (above + before < target && target <= above + before + size) {
+              sh.place = (u64)(255 - tid) << shift;
+              sh.above = above + before;
+              sh.total = sum + mass_before;
+            }
+            __syncthreads();
+            prefix |= sh.place;
+            above = sh.above;
+            sum = sh.total;
+          }
+          return prefix;
+        };
+        u64 total = bins.all, sum;
+        if (bins.k >= 0) {
+          place = find_place(true, (u64)(set.k - (int)bins.above_k), sum);
+          total = bins.mass_above_k + sum + steps_of(place);
         }
+        if (set.cut_p) place = find_place(false, set.share_of(total) - bins.mass_above_p, sum);
       }
-      __syncthreads();
-      if (sh.index >= 0) {
-        cut = Cut{key_at(sh.list[sh.index]), token_at(sh.list[sh.index])};
+      if (place != 0) {
+        cut = Cut{key_at(place), token_at(place)};
+        __syncthreads();
         // what stays of the list joins its chunks
-        for (int i = tid; i <= sh.index; i += kThreads) {
-          const float v = value_of(key_at(sh.list[i]));
-          const int at = token_at(sh.list[i]);
-          atomicAdd(&sh.mass[(at + row.skew) / Row<TYPE>::kChunk], Weights::steps(kept(v, at)));
+        for (int i = tid; i < n; i += kThreads) {
+          const u64 x = sh.list[i];
+          if (x < place) continue;
+          const int at = token_at(x);
+          atomicAdd(&sh.mass[(at + row.skew) / Row<TYPE>::kChunk],
+                    Weights::steps(kept(value_of(key_at(x)), at)));
         }
       }
     }

@@ -88,7 +88,7 @@ __device__ __forceinline__ double fma_s(double a, double b, double c) {
   return d;
 }
 
-__device__ __forceinline__ double exp2_neg(double t) {
+__device__ __forceinline__ double exp2_neg(double t, int more = 0) {
   t = fmax(t, -1100.);  // (no number too, as -inf less -inf: 0)
   const double n = rint(t), r = t - n;
   double x = fma_s(1.0203121171282166e-07, r, 1.3255224873639605e-06);
@@ -100,28 +100,31 @@ __device__ __forceinline__ double exp2_neg(double t) {
   x = fma_s(x, r, 2.402265069581299e-01);
   x = fma_s(x, r, 6.931471805599453e-01);
   x = fma(x, r, 1.);
-  return __builtin_ldexp(x, (int)n);
+  return __builtin_ldexp(x, (int)n + more);
 }
 
 // The row's probabilities: exponent of p in base 2, p, p in steps of 2^-44, and the bin.
 struct Weights {
   double top, rate;  // the largest logit; log2(e) / T
-  __device__ Weights(float largest, float t)
-      // an infinite logit is above all others by more than any T brings back
-      : top(largest == INFINITY ? 1e300 : (double)largest), rate(1.4426950408889634 / (double)t) {}
-  __device__ double exponent(float z) const { return (fmin((double)z, top) - top) * rate; }
+  __device__ Weights(float largest, float t) : top(largest), rate(1.4426950408889634 / (double)t) {}
+  __device__ double exponent(float z) const { return ((double)z - top) * rate; }
   __device__ double p(float z) const { return exp2_neg(exponent(z)); }
-  __device__ static u64 steps(double p) {
-    // the integer nearest to 2^44 p lies in the low bits of its sum with 2^52
-    return __builtin_bit_cast(u64, fma(p, 0x1p44, 0x1p52)) & ((1ull << 52) - 1);
+  // Steps as a whole number in fp64; of up to 512 tokens they add exactly.
+  __device__ static double steps_at(double exponent) { return rint(exp2_neg(exponent, 44)); }
+  __device__ static u64 whole(double steps) {
+    // the low bits of its sum with 2^52, which rounds what is no whole number
+    return __builtin_bit_cast(u64, steps + 0x1p52) & ((1ull << 52) - 1);
   }
+  __device__ u64 steps(float z) const { return whole(exp2_neg(exponent(z), 44)); }
   // Never falls as z does.  Below 2^-45 there are no steps.
   __device__ static int bin(double exponent) {
-    return exponent > -45. ? (int)(-exponent * kBinsPerPower) : kBins - 1;
+    return (int)min((uint32_t)(int)(-exponent * kBinsPerPower), (uint32_t)kBins - 1u);
   }
-  // A logit below which no token has a step, and, with min_p, none stays.
+  // A logit below which no token is in a bin before the last, and, with min_p, none stays.
   __device__ float least(float min_p) const {
-    return logit_below(min_p > 0.f ? fmin(fmax(-45., log2((double)min_p) - 0x1p-10), 0.) : -45.);
+    constexpr double kDeepest = (kBins - 1) / -kBinsPerPower;
+    return logit_below(min_p > 0.f ? fmin(fmax(kDeepest, log2((double)min_p) - 0x1p-10), 0.)
+                                   : kDeepest);
   }
   // A logit below which no exponent is above this one.
   __device__ float logit_below(double exponent) const {
@@ -129,6 +132,10 @@ struct Weights {
     return (float)(z - fabs(z) * 0x1p-20) - 1e-30f;
   }
 };
+
+__device__ __forceinline__ float scalar(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
+}
 
 // What a row asks for.
 struct Setting {
@@ -140,8 +147,12 @@ struct Setting {
   __device__ Setting(const SampleArgs& p, int row) {
     t = p.temperature != nullptr ? p.temperature[row] : 1.f;
     k = p.top_k != nullptr ? p.top_k[row] : 0;
-    const float share = p.top_p != nullptr ? p.top_p[row] : 1.f;
+    float share = p.top_p != nullptr ? p.top_p[row] : 1.f;
     min_p = p.min_p != nullptr ? p.min_p[row] : 0.f;
+    t = scalar(t);  // what depends on them is then a branch of the wave
+    k = __builtin_amdgcn_readfirstlane(k);
+    share = scalar(share);
+    min_p = scalar(min_p);
     greedy = !(t > 0.f);
     cut_k = k > 0 && k < p.vocab;
     cut_p = share < 1.f;
@@ -164,6 +175,7 @@ struct Row {
       TYPE == kFp32 ? 0xff800000u : TYPE == kBf16 ? 0xff80ff80u : 0xfc00fc00u;  // -inf
   const char* base;
   int vocab, skew, chunks;
+  bool infinite = false;  // +inf reads as 0, all others as -inf: they count for nothing beside it
 
   __device__ Row(const SampleArgs& p, int row) {
     constexpr int kSize = 16 / kLen;
@@ -210,7 +222,14 @@ struct Row {
         z[i] = Act<TYPE == kBf16>::value((uint16_t)(bits >> (16 * (i % 2))));
     }
   }
-  __device__ void load(int chunk, int lane, float* z) const { values(raw(chunk, lane), z); }
+  __device__ void take(u32x4 w, float* z) const {
+    values(w, z);
+    if (infinite) {
+#pragma unroll
+      for (int i = 0; i < kLen; ++i) z[i] = z[i] == INFINITY ? 0.f : -INFINITY;
+    }
+  }
+  __device__ void load(int chunk, int lane, float* z) const { take(raw(chunk, lane), z); }
   __device__ bool has(int at) const { return at >= 0 && at < vocab; }
 };
 
@@ -228,7 +247,7 @@ __device__ __forceinline__ void each_chunk(const Row<TYPE>& row, int from, int t
     const u32x4 w = next;
     if (c + waves < to) next = row.raw(c + waves, lane);
     float z[Row<TYPE>::kLen];
-    Row<TYPE>::values(w, z);
+    row.take(w, z);
     f(c, z);
   }
 }
@@ -384,21 +403,27 @@ __device__ __forceinline__ u64 row_best(const SampleArgs& p, int r, int lane) {
 __device__ __forceinline__ bool row_is_bad(u64 best) {
   return best == kNan || value_of(key_at(best)) == -INFINITY;
 }
+// The row's largest logit as Row::take gives it.
+template <int TYPE>
+__device__ __forceinline__ float row_top(Row<TYPE>& row, u64 best) {
+  const float top = value_of(key_at(best));
+  row.infinite = top == INFINITY;
+  return row.infinite ? 0.f : top;
+}
 
-// The steps of p of a lane's values, kMin: those that min_p lets stay.
-template <int LEN, bool MIN>
-__device__ __forceinline__ u64 kept_steps(const Weights& weights, const float* z, uint32_t top_key,
-                                          float min_p) {
-  u64 sum = 0;
+// The largest of a lane's values.
+template <int LEN>
+__device__ __forceinline__ float largest(const float* z) {
+  float m = z[0];
 #pragma unroll
-  for (int i = 0; i < LEN; ++i) {
-    const double x = weights.p(z[i]);
-    if constexpr (MIN)
-      sum += key_of(z[i]) == top_key || !(x < (double)min_p) ? Weights::steps(x) : 0;
-    else
-      sum += Weights::steps(x);
-  }
-  return sum;
+  for (int i = 1; i < LEN; ++i) m = fmaxf(m, z[i]);
+  return m;
+}
+
+// Whether min_p lets a token stay that has this exponent and key.
+__device__ __forceinline__ bool min_keeps(double exponent, uint32_t key, uint32_t top_key,
+                                          float min_p) {
+  return key == top_key || !(exp2_neg(exponent) < (double)min_p);
 }
 
 // Rows that are cut: tokens and sums of p by bins.  Others: the sums of their chunks.
@@ -408,7 +433,7 @@ __global__ __launch_bounds__(kThreads) void sample_bins(SampleArgs p) {
   __shared__ uint32_t count[kBins];
   const int slice = blockIdx.x, r = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const Row<TYPE> row(p, r);
+  Row<TYPE> row(p, r);
   constexpr int kLen = Row<TYPE>::kLen;
   int from, to;
   slice_of(p, row, slice, from, to);
@@ -420,41 +445,46 @@ __global__ __launch_bounds__(kThreads) void sample_bins(SampleArgs p) {
   }
   const u64 best = row_best(p, r, lane);
   if (set.greedy || row_is_bad(best)) return;
-  const Weights weights(value_of(key_at(best)), set.t);
+  const float top = row_top(row, best);
+  const uint32_t top_key = key_of(top);
+  const Weights weights(top, set.t);
   if (!(set.cut_k || set.cut_p)) {
     const float least = weights.least(set.min_p);
     each_chunk(row, from, to, wave, kWaves, lane, first, [&](int c, const float* z) {
-      bool any = false;
+      double sum = 0.;
+      u64 all = 0;
+      if (__ballot(largest<kLen>(z) >= least)) {
+        if (set.min_p > 0.f) {
 #pragma unroll
-      for (int i = 0; i < kLen; ++i) any |= z[i] >= least;
-      u64 sum = 0;
-      if (__ballot(any)) {
-        sum = set.min_p > 0.f ? kept_steps<kLen, true>(weights, z, key_at(best), set.min_p)
-                              : kept_steps<kLen, false>(weights, z, 0, 0.f);
-        sum = wave_sum(sum);
+          for (int i = 0; i < kLen; ++i) {
+            const double e = weights.exponent(z[i]);
+            if (min_keeps(e, key_of(z[i]), top_key, set.min_p)) sum += Weights::steps_at(e);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kLen; ++i) sum += Weights::steps_at(weights.exponent(z[i]));
+        }
+        all = wave_sum(Weights::whole(sum));
       }
-      if (lane == 0) p.chunk_mass[(int64_t)r * p.max_chunks + c] = sum;
+      if (lane == 0) p.chunk_mass[(int64_t)r * p.max_chunks + c] = all;
     });
     return;
   }
   __syncthreads();
   const float least = weights.least(0.f);
   each_chunk(row, from, to, wave, kWaves, lane, first, [&](int, const float* z) {
-    bool any = false;
-#pragma unroll
-    for (int i = 0; i < kLen; ++i) any |= z[i] >= least;
-    if (!__ballot(any)) return;
+    if (!__ballot(largest<kLen>(z) >= least)) return;
     int b[kLen];
     u64 steps[kLen];
 #pragma unroll
     for (int i = 0; i < kLen; ++i) {
       const double e = weights.exponent(z[i]);
       b[i] = Weights::bin(e);
-      if (set.cut_p) steps[i] = Weights::steps(exp2_neg(e));
+      if (set.cut_p) steps[i] = Weights::whole(exp2_neg(e, 44));
     }
 #pragma unroll
     for (int i = 0; i < kLen; ++i) {
-      if (b[i] == kBins - 1) continue;  // (tokens without a step are not counted)
+      if (b[i] == kBins - 1) continue;
       if (set.cut_k) atomicAdd(&count[b[i]], 1u);
       if (set.cut_p) atomicAdd(&mass[b[i]], steps[i]);
     }
@@ -558,7 +588,7 @@ __global__ __launch_bounds__(kThreads) void sample_gather(SampleArgs p) {
   __shared__ Bins bins_lds;
   const int slice = blockIdx.x, r = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const Row<TYPE> row(p, r);
+  Row<TYPE> row(p, r);
   constexpr int kLen = Row<TYPE>::kLen;
   int from, to;
   slice_of(p, row, slice, from, to);
@@ -569,7 +599,9 @@ __global__ __launch_bounds__(kThreads) void sample_gather(SampleArgs p) {
   if (set.greedy || row_is_bad(best) || !(set.cut_k || set.cut_p)) return;
   if (tid == 0) listed = 0;
   const Bins bins = find_bins(my, set, mass_lds, count_lds, bins_lds);
-  const Weights weights(value_of(key_at(best)), set.t);
+  const float top = row_top(row, best);
+  const uint32_t top_key = key_of(top);
+  const Weights weights(top, set.t);
   const int first_bin = bins.first(), last_bin = max(bins.k, bins.p_high);
   // nothing below the last bin of the list is looked at
   const float least = last_bin >= 0 ? weights.logit_below((last_bin + 1) * (-1. / kBinsPerPower))
@@ -577,23 +609,27 @@ __global__ __launch_bounds__(kThreads) void sample_gather(SampleArgs p) {
   if (slice == 0 && tid == 0) p.bins[r] = bins;
   each_chunk(row, from, to, wave, kWaves, lane, first, [&](int c, const float* z) {
     const int at = row.first(c, lane);
-    u64 sum = 0;
+    double sum = 0.;
+    u64 all = 0;
     const auto put = [&](int i) {
       const uint32_t n = atomicAdd(&listed, 1u);
       if (n < kList) list[n] = place_of(key_of(z[i]), at + i);
     };
     int busy = 0;  // elements that some lane has to look at
+    if (__ballot(largest<kLen>(z) >= least))
 #pragma unroll
-    for (int i = 0; i < kLen; ++i) busy += __ballot(z[i] >= least) != 0;
+      for (int i = 0; i < kLen; ++i) busy += __ballot(z[i] >= least) != 0;
     if (busy > kLen / 2) {  // all of them side by side, without branches
       bool in_list[kLen];
 #pragma unroll
       for (int i = 0; i < kLen; ++i) {
-        const double e = weights.exponent(z[i]), x = exp2_neg(e);
+        const double e = weights.exponent(z[i]);
         const int b = Weights::bin(e);
         in_list[i] = b >= first_bin && bins.lists(b);
-        const bool stays = key_of(z[i]) == key_at(best) || !(x < (double)set.min_p);
-        sum += b < first_bin && stays ? Weights::steps(x) : 0;
+        bool stays = b < first_bin;
+        if (set.min_p > 0.f) stays &= min_keeps(e, key_of(z[i]), top_key, set.min_p);
+        const double steps = Weights::steps_at(e);
+        sum += stays ? steps : 0.;
       }
 #pragma unroll
       for (int i = 0; i < kLen; ++i)
@@ -605,15 +641,15 @@ __global__ __launch_bounds__(kThreads) void sample_gather(SampleArgs p) {
         const double e = weights.exponent(z[i]);
         const int b = Weights::bin(e);
         if (b < first_bin) {
-          const double x = exp2_neg(e);
-          sum += key_of(z[i]) == key_at(best) || !(x < (double)set.min_p) ? Weights::steps(x) : 0;
+          if (!(set.min_p > 0.f) || min_keeps(e, key_of(z[i]), top_key, set.min_p))
+            sum += Weights::steps_at(e);
         } else if (bins.lists(b)) {
           put(i);
         }
       }
     }
-    if (__ballot(sum != 0)) sum = wave_sum(sum);
-    if (lane == 0) p.chunk_mass[(int64_t)r * p.max_chunks + c] = sum;
+    if (busy > 0) all = wave_sum(Weights::whole(sum));
+    if (lane == 0) p.chunk_mass[(int64_t)r * p.max_chunks + c] = all;
   });
   // the slice's list to the row's; one that is too long makes the row's too long
   __syncthreads();
@@ -685,7 +721,7 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
   const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   constexpr int kThreads = kPickThreads, kWaves = kPickWaves;
   const Setting set(p, r);
-  const Row<TYPE> row(p, r);
+  Row<TYPE> row(p, r);
   for (int c = tid; c < row.chunks; c += kThreads)
     sh.mass[c] = p.chunk_mass[(int64_t)r * p.max_chunks + c];
   const bool cuts = set.cut_k || set.cut_p;
@@ -705,8 +741,9 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
   }
   constexpr int kLen = Row<TYPE>::kLen;
   float z[kLen];
-  const uint32_t key = key_at(best);
-  const Weights weights(value_of(key), set.t);
+  const float top = row_top(row, best);
+  const uint32_t key = key_of(top);
+  const Weights weights(top, set.t);
 
   // The cut at which the count of tokens, or the sum of their p, reaches a target: by the bytes of
   // the key from the top, then by number among the tokens of that key.  Leaves in sh.above the sum
@@ -730,7 +767,7 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
           const uint32_t k = key_of(z[i]);
           if (!row.has(first + i) || (shift < 24 && (k ^ prefix) >> (shift + 8))) continue;
           atomicAdd(&sh.count[255 - (k >> shift & 255)], 1u);
-          atomicAdd(&sh.mass[255 - (k >> shift & 255)], Weights::steps(weights.p(z[i])));
+          atomicAdd(&sh.mass[255 - (k >> shift & 255)], weights.steps(z[i]));
         }
       }
       __syncthreads();
@@ -751,7 +788,7 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
       above_count = sh.above_count;
     }
     // how many of this key stay
-    const u64 each = Weights::steps(weights.p(value_of(prefix)));
+    const u64 each = weights.steps(value_of(prefix));
     const u64 left = by_count ? target - above_count
                               : (each == 0 ? 1 : (target - above + each - 1) / each);
     __syncthreads();
@@ -792,11 +829,11 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
   };
 
   Cut cut{0, row.vocab};
-  const auto kept = [&](float v, int i) -> double {  // p where the token stays, else 0
+  const auto kept = [&](float v, int i) -> u64 {  // the steps of p where the token stays, else 0
     const uint32_t kk = key_of(v);
-    if (!row.has(i) || !cut.keeps(kk, i)) return 0.;
-    const double x = weights.p(v);
-    return kk == key || !(x < (double)set.min_p) ? x : 0.;
+    const bool stays = row.has(i) && cut.keeps(kk, i) &&
+                       (!(set.min_p > 0.f) || min_keeps(weights.exponent(v), kk, key, set.min_p));
+    return stays ? weights.steps(v) : 0;
   };
   const auto chunk_sums = [&] {
     __syncthreads();
@@ -805,7 +842,7 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
       const int first = row.first(c, lane);
       u64 sum = 0;
 #pragma unroll
-      for (int i = 0; i < kLen; ++i) sum += Weights::steps(kept(z[i], first + i));
+      for (int i = 0; i < kLen; ++i) sum += kept(z[i], first + i);
       sum = wave_sum(sum);
       if (lane == 0) sh.mass[c] = sum;
     }
@@ -826,7 +863,7 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
     if (cuts && listed > 0) {
       const int n = (int)listed;
       const auto steps_of = [&](u64 place) {
-        return Weights::steps(weights.p(value_of(key_at(place))));
+        return weights.steps(value_of(key_at(place)));
       };
       const auto bin_of = [&](u64 place) {
         return Weights::bin(weights.exponent(value_of(key_at(place))));
@@ -932,7 +969,7 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
           if (x < place) continue;
           const int at = token_at(x);
           atomicAdd(&sh.mass[(at + row.skew) / Row<TYPE>::kChunk],
-                    Weights::steps(kept(value_of(key_at(x)), at)));
+                    kept(value_of(key_at(x)), at));
         }
       }
     }
@@ -960,12 +997,12 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
   if (wave == 0) {
     const u32x4 w = row.raw(sh.index, lane);
     const double whole = log((double)total * 0x1p-44);  // (while the vector is in flight)
-    Row<TYPE>::values(w, z);
+    row.take(w, z);
     const int first = row.first(sh.index, lane);
     u64 m[kLen], all = 0;
 #pragma unroll
     for (int i = 0; i < kLen; ++i) {
-      m[i] = Weights::steps(kept(z[i], first + i));
+      m[i] = kept(z[i], first + i);
       all += m[i];
     }
     const u64 upto = wave_upto(all);

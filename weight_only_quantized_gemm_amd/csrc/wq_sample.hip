@@ -615,26 +615,7 @@ __global__ __launch_bounds__(kThreads) void sample_gather(SampleArgs p) {
       const uint32_t n = atomicAdd(&listed, 1u);
       if (n < kList) list[n] = place_of(key_of(z[i]), at + i);
     };
-    int busy = 0;  // elements that some lane has to look at
-    if (__ballot(largest<kLen>(z) >= least))
-#pragma unroll
-      for (int i = 0; i < kLen; ++i) busy += __ballot(z[i] >= least) != 0;
-    if (busy > kLen / 2) {  // all of them side by side, without branches
-      bool in_list[kLen];
-#pragma unroll
-      for (int i = 0; i < kLen; ++i) {
-        const double e = weights.exponent(z[i]);
-        const int b = Weights::bin(e);
-        in_list[i] = b >= first_bin && bins.lists(b);
-        bool stays = b < first_bin;
-        if (set.min_p > 0.f) stays &= min_keeps(e, key_of(z[i]), top_key, set.min_p);
-        const double steps = Weights::steps_at(e);
-        sum += stays ? steps : 0.;
-      }
-#pragma unroll
-      for (int i = 0; i < kLen; ++i)
-        if (in_list[i]) put(i);
-    } else if (busy > 0) {
+    if (__ballot(largest<kLen>(z) >= least)) {
 #pragma unroll
       for (int i = 0; i < kLen; ++i) {
         if (!(z[i] >= least)) continue;
@@ -647,8 +628,8 @@ __global__ __launch_bounds__(kThreads) void sample_gather(SampleArgs p) {
           put(i);
         }
       }
+      all = wave_sum(Weights::whole(sum));
     }
-    if (busy > 0) all = wave_sum(Weights::whole(sum));
     if (lane == 0) p.chunk_mass[(int64_t)r * p.max_chunks + c] = all;
   });
   // the slice's list to the row's; one that is too long makes the row's too long

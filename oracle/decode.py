@@ -33,10 +33,11 @@ def rotate(x, positions, inv_freq, sections, interleaved):
 
 
 def paged_attention(q, k_cache, v_cache, table, lens, scale, window=0, softcap=0.0, keep=None,
-                    bad=None, k_terms=None, v_terms=None):
+                    bad=None, k_terms=None, v_terms=None, q_step=0.0):
     """q [batch][q_heads][d]; caches [page][slot][kv_head][d] (scales applied).  Returns out,
     lse and the bounds of both before the output's rounding.  k_terms, v_terms: the sum of the sizes
-    of the terms that make up each element (its own size where it is one term)."""
+    of the terms that make up each element (its own size where it is one term).  q_step: how far each
+    element of q may be off, relative to its head's largest."""
     k_terms = np.abs(k_cache) if k_terms is None else k_terms
     v_terms = np.abs(v_cache) if v_terms is None else v_terms
     batch, q_heads, d = q.shape
@@ -60,6 +61,7 @@ def paged_attention(q, k_cache, v_cache, table, lens, scale, window=0, softcap=0
             s = kh @ q[b, h] * scale
             s_err = (k_size[:, h // per] @ np.abs(q[b, h])) * abs(scale) * (d + 8) * E32
             s_err = s_err + np.abs(s) * 8 * E32
+            s_err = s_err + q_step * np.abs(q[b, h]).max() * k_size[:, h // per].sum(1) * abs(scale)
             if softcap:
                 s = softcap * np.tanh(s / softcap)
                 # tanh is right to its own size, and its last product to the cap's

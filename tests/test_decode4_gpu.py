@@ -291,6 +291,12 @@ def attn_run(c, cut=False, **kw):
     return plan(c["q"], c["table"], c["lens"], keep=c["keep"], lse=True, **kw)
 
 
+# q is cut into two E4M3 pieces (fp16: three) of 2^-9 and 2^-13 (and 2^-17) at their finest, below 2^8
+# times a power of two that the largest element of a group is at least half of: half a step of 2^-13
+# (2^-17) against 2^7.
+Q_STEP = {BF16: 2.0 ** -21, F16: 2.0 ** -25}
+
+
 def attn_check(c, out, lse, label=""):
     cache = c["cache"]
     parts = [(x.cpu().numpy(), np64(y)) for x, y in ((cache.k, cache.k_pairs), (cache.v, cache.v_pairs))]
@@ -298,7 +304,7 @@ def attn_check(c, out, lse, label=""):
         np64(c["q"]), *(ref.values4(*x) for x in parts), c["table"].cpu().numpy(),
         c["lens"].cpu().numpy(), c["scale"], c["window"], c["softcap"],
         None if c["keep"] is None else c["keep"].cpu().numpy(), None,
-        *(ref.terms4(*x) for x in parts))
+        *(ref.terms4(*x) for x in parts), Q_STEP[c["dtype"]])
     check(out, want, err, label + " out")
     check(lse, want_lse, lse_err, label + " lse")
 

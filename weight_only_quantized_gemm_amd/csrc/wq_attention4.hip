@@ -14,10 +14,12 @@
 // and its p is multiplied by g's scale alone.  A column then costs what it would without groups,
 // and an output column holds all of the head's elements, of which those in g are used.
 //
-// A code becomes a 16-bit operand in half an instruction and a shift: c in the upper bits of a bf16
-// mantissa below the exponent of 16 is 16 + c.  For K the 16 is in the accumulator that a product
-// starts from (-16 times the sum of q over g), for V in the offset (o - 16 s).  The operands are bf16
-// for both element types: q of fp16 is cut into two (exactly), p s into two that keep 16 bits.
+// K's codes become bytes (two instructions and a half for eight): 0 to 15 are, as E4M3 values, 2^-9 to
+// 15 2^-9, which an MFMA of 8-bit operands takes with a block scale of 2^9.  Its other operand is q in
+// two E4M3 pieces (fp16: three) of four bits each, below a power of two of its column.  V's codes
+// meet p, whose range no 8-bit type has: they become bf16 values of 16 + c, an instruction and a shift
+// for two, and the offsets o - 16 s take the 16 off again; p s is cut into two bf16 parts, which keep
+// 16 bits.
 //
 // V's codes need the positions along the register: the transposing read of 4-bit elements gives a
 // lane 16 positions of one element, which serve two products.
@@ -33,10 +35,12 @@ constexpr int kTile = 64, kStep = kWaves * kTile;  // positions of a wave's step
 struct Attn4Args : AttnArgs {
   const uint32_t *k_pairs, *v_pairs;
   int64_t pair_page, pair_slot, pair_head;
-  int group_size, groups;
+  int group_size;
+  int short_strides;  // strides of pages and slots, and slots times strides, are below 2^32
 };
 
 typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
 
 // Eight codes as 16 + c, nibbles in the order 0, 4, 1, 5, 2, 6, 3, 7.
@@ -54,34 +58,61 @@ __device__ __forceinline__ f32x4 mfma_bf(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
+__device__ __forceinline__ float add_bits(float x, int y) {
+  return x + __builtin_bit_cast(float, y);
+}
 // Sum over the groups' lanes of a head (GP neighbours).
 template <int GP>
 __device__ __forceinline__ float group_sum(float x) {
-  const auto add = [&](int y) { x += __builtin_bit_cast(float, y); };
   if constexpr (GP >= 2)  // quad_perm 1 0 3 2
-    add(__builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0xB1, 0xf, 0xf, false));
+    x = add_bits(x, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0xB1, 0xf, 0xf, false));
   if constexpr (GP >= 4)  // quad_perm 2 3 0 1
-    add(__builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x4E, 0xf, 0xf, false));
+    x = add_bits(x, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x4E, 0xf, 0xf, false));
   if constexpr (GP >= 8)  // row_half_mirror: the other four of eight lanes, whose sums are equal
-    add(__builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x141, 0xf, 0xf, false));
+    x = add_bits(x, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x141, 0xf, 0xf, false));
   return x;
 }
 
-// W: dwords of a row that a lane holds of K, head_dim rounded up over 32.  GP: groups of a head,
-// rounded up to a power of two.  FULL: head_dim is 32 W.
-template <bool BF16, int W, int GP, bool FULL>
-__global__ __launch_bounds__(kWaves * 64) void attn4_kernel(Attn4Args p) {
+// f over the four lanes of a column (16 apart): rows of 16 lanes change places in pairs.
+template <class F>
+__device__ __forceinline__ float over_column(float x, F f) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, x),
+                                                  __builtin_bit_cast(uint32_t, x), false, false);
+  x = f(__builtin_bit_cast(float, (uint32_t)a[0]), __builtin_bit_cast(float, (uint32_t)a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x),
+                                                  __builtin_bit_cast(uint32_t, x), false, false);
+  return f(__builtin_bit_cast(float, (uint32_t)b[0]), __builtin_bit_cast(float, (uint32_t)b[1]));
+}
+__device__ __forceinline__ float column_max(float x) {
+  return over_column(x, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float column_sum(float x) {
+  return over_column(x, [](float a, float b) { return a + b; });
+}
+
+constexpr int pow2_from(int x) { return x <= 1 ? 1 : x <= 2 ? 2 : x <= 4 ? 4 : 8; }
+
+// W: dwords of a row that a lane holds of K, head_dim rounded up over 32.  G: groups of a head.  NC:
+// sets of sixteen columns that a work-group takes, which share K's and V's operands.  FULL: head_dim is
+// 32 W.
+template <bool BF16, int W, int G, int NC, bool FULL>
+__global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
   using A = Act<BF16>;
   constexpr int DP = 32 * W;
-  constexpr int NT = kTile / 16;   // 16-position blocks of a tile
-  constexpr int NB = DP / 16;      // 16-element blocks of the output
-  constexpr int HB = 16 / GP;      // query heads of a work-group
+  constexpr int GP = pow2_from(G);
+  constexpr int NT = kTile / 16;       // 16-position blocks of a tile
+  constexpr int NB = DP / 16;          // 16-element blocks of the output
+  constexpr int NM = (2 * W + 7) / 8;  // 128-element steps of K
+  constexpr int NP = BF16 ? 2 : 3;     // pieces of q
+  constexpr int HS = 16 / GP;          // query heads of a set
+  constexpr int HB = NC * HS;          // and of a work-group
   constexpr int SD = W % 2 == 0 ? 4 * W + 4 : 4 * W + 8;  // dwords of an LDS row of V: 4 mod 8
-  constexpr int OS = DP + 4;       // LDS row of the joined outputs
+  constexpr int OS = DP + 4;           // LDS row of the joined outputs
   constexpr int kVDwords = kTile * SD + 2;
   constexpr int kVBytes = kWaves * kVDwords * 4, kOBytes = kWaves * HB * OS * 4;
   __shared__ __align__(16) uint8_t lds[kVBytes > kOBytes ? kVBytes : kOBytes];
-  __shared__ __align__(16) uint32_t pair_lds[kWaves][2][GP][kTile];
+  // scales and offsets of K, scales and offsets less 16 scales of V
+  __shared__ __align__(16) float pair_lds[kWaves][4][G][kTile];
   __shared__ int64_t off_lds[kWaves][kTile];
   __shared__ float ml_lds[kWaves][HB][2];
 
@@ -97,7 +128,8 @@ __global__ __launch_bounds__(kWaves * 64) void attn4_kernel(Attn4Args p) {
   const int kvh = unit / p.head_blocks, hb = unit - kvh * p.head_blocks;
   const int h0 = kvh * p.group + HB * hb;         // first query head
   const int rows = min(HB, p.group - HB * hb);
-  const int my_head = row / GP, my_group = row % GP;  // this lane's column
+  const int my_head = row / GP, my_group = row % GP;  // this lane's column in a set
+  const int my_pair = GP == G ? my_group : min(my_group, G - 1);  // (no group: any pair will do)
 
   // Part of a sequence that this range holds.
   struct Part {
@@ -129,39 +161,63 @@ __global__ __launch_bounds__(kWaves * 64) void attn4_kernel(Attn4Args p) {
     return 16 * (w / 4) + 4 * qd + w % 4;
   };
 
-  // Q as the B operand: this column's head, its group's elements, in the codes' order.
+  // q as the B operand: this column's head, its group's elements, as pieces below 2^8 times the power
+  // of two in q_scale; elements 0, 2, 4, 6 of a dword's eight, then the others, as K's bytes come.  A
+  // negative scale of the scores is q's sign, and one of 0 its value.
   uint32_t pattern;
   asm volatile("v_mov_b32 %0, 0x41804180" : "=v"(pattern));
-  bf16x8 qh[W], ql[BF16 ? 1 : W];
-  float q_sum = 0.f;
+  const float sign = p.scale > 0.f ? 1.f : p.scale < 0.f ? -1.f : 0.f;
+  const float sc = p.scale == 0.f ? 1.f : fabsf(p.scale);
+  i32x8 qp[NC][NP][NM];
+  int q_scale[NC];
+  float q_sum[NC];
   const auto load_q = [&](int b) {
-    const uint16_t* qp =
-        p.q + (int64_t)b * p.ldq + (int64_t)(h0 + (my_head < rows ? my_head : 0)) * p.d;
-    q_sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const int dw = dword_of(w);
-      u32x4 raw = {0u, 0u, 0u, 0u};
-      if ((FULL || dw < nd) && my_head < rows && 8 * dw / p.group_size == my_group)
-        raw = *reinterpret_cast<const u32x4*>(qp + 8 * dw);
-      uint16_t x[8];
-      __builtin_memcpy(x, &raw, 16);
+    for (int n = 0; n < NC; ++n) {
+      const int head = n * HS + my_head;
+      const uint16_t* src = p.q + (int64_t)b * p.ldq + (int64_t)(h0 + (head < rows ? head : 0)) * p.d;
+      float x[W][8], most = 0.f, sum = 0.f;
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        const uint16_t bits = x[t / 2 + 4 * (t % 2)];
-        const float f = A::value(bits);
-        q_sum += f;
-        if constexpr (BF16) {
-          qh[w][t] = __builtin_bit_cast(bf16, bits);
-        } else {
-          const bf16 high = (bf16)f;
-          qh[w][t] = high;
-          ql[w][t] = (bf16)(f - (float)high);  // at most 4 bits are left: exact
+      for (int w = 0; w < W; ++w) {
+        const int dw = dword_of(w);
+        u32x4 raw = {0u, 0u, 0u, 0u};
+        if ((FULL || dw < nd) && head < rows && 8 * dw / p.group_size == my_group)
+          raw = *reinterpret_cast<const u32x4*>(src + 8 * dw);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          x[w][t] = sign * A::value((uint16_t)(raw[t / 2] >> (16 * (t % 2))));
+          sum += x[w][t];
+          most = fmaxf(most, fabsf(x[w][t]));
         }
       }
+      q_sum[n] = column_sum(sum);
+      // the largest element's exponent, seven below which is the pieces' (within what scales hold)
+      const int top = (int)(__builtin_bit_cast(uint32_t, column_max(most)) >> 23) - 127 - 7;
+      const int e = min(max(top, -110), 120);
+      q_scale[n] = 127 + e;
+      const float down = __builtin_ldexpf(1.f, -e);
+#pragma unroll
+      for (int m = 0; m < NM; ++m)
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const int w = (8 * m + r) / 2, odd = r % 2;  // elements odd, odd + 2, ... of dword w
+          float y[4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) y[t] = w < W ? x[w < W ? w : 0][2 * t + odd] * down : 0.f;
+#pragma unroll
+          for (int piece = 0; piece < NP; ++piece) {
+            int bytes = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+            bytes = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], bytes, true);
+            qp[n][piece][m][r] = bytes;
+            const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(bytes, false);
+            const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(bytes, true);
+            y[0] = (y[0] - lo[0]) * 16.f;  // exact: what a piece leaves, four bits down
+            y[1] = (y[1] - lo[1]) * 16.f;
+            y[2] = (y[2] - hi[0]) * 16.f;
+            y[3] = (y[3] - hi[1]) * 16.f;
+          }
+        }
     }
-    q_sum += __shfl_xor(q_sum, 16);
-    q_sum += __shfl_xor(q_sum, 32);
   };
 
   const uint8_t* kbase = p.k + kvh * p.head_stride / 2;
@@ -189,23 +245,24 @@ __global__ __launch_bounds__(kWaves * 64) void attn4_kernel(Attn4Args p) {
   const auto place = [&](int lo, int t1) -> uint64_t {
     const bool live = (unsigned)page_next < (unsigned)p.num_pages && keep_next != 0 &&
                       pos_next >= lo && pos_next < t1;
-    off_lds[wave][lane] = live ? (page_next * p.page_stride + slot_next * p.slot_stride) / 2 : 0;
-    pair_off = live ? page_next * p.pair_page + slot_next * p.pair_slot : 0;
+    const int page = live ? page_next : 0, slot = live ? slot_next : 0;
+    if (p.short_strides) {
+      off_lds[wave][lane] = (int64_t)(((uint64_t)(uint32_t)page * (uint32_t)p.page_stride +
+                                       (uint32_t)slot * (uint32_t)p.slot_stride) /
+                                      2);
+      pair_off = (int64_t)((uint64_t)(uint32_t)page * (uint32_t)p.pair_page +
+                           (uint32_t)slot * (uint32_t)p.pair_slot);
+    } else {
+      off_lds[wave][lane] = (page * p.page_stride + slot * p.slot_stride) / 2;
+      pair_off = page * p.pair_page + slot * p.pair_slot;
+    }
     return __ballot(live);
   };
-  uint32_t kr[NT][W], kp[GP], vp[GP];
+  uint32_t kr[NT][W], kp[G], vp[G];
   u32x4 vr[W];
-  const auto load_pairs = [&](const uint32_t* base, uint32_t* x) {
-    if (p.groups == GP) {
-#pragma unroll
-      for (int g = 0; g < GP; ++g) x[g] = base[g];
-    } else {  // (the last column's groups are no groups: any pair will do)
-#pragma unroll
-      for (int g = 0; g < GP; ++g) x[g] = base[min(g, p.groups - 1)];
-    }
-  };
   const auto load_k = [&] {
-    load_pairs(k_pairs + pair_off, kp);
+#pragma unroll
+    for (int g = 0; g < G; ++g) kp[g] = k_pairs[pair_off + g];
 #pragma unroll
     for (int blk = 0; blk < NT; ++blk) {
       const uint8_t* at = kbase + off_lds[wave][16 * blk + row];
@@ -217,7 +274,7 @@ __global__ __launch_bounds__(kWaves * 64) void attn4_kernel(Attn4Args p) {
 #pragma unroll
           for (int i = w; i < (w + kPiece < W ? w + kPiece : W); ++i) kr[blk][i] = src[i - w];
         }
-      } else {  // a dword past the head's end meets a zero of Q: the first one is read instead
+      } else {  // a dword past the head's end meets a zero of q: the first one is read instead
 #pragma unroll
         for (int w = 0; w < W; ++w) {
           const int dw = dword_of(w);
@@ -228,7 +285,8 @@ __global__ __launch_bounds__(kWaves * 64) void attn4_kernel(Attn4Args p) {
   };
   // V by whole rows, 16 bytes a lane: read once, so it need not stay in the caches.
   const auto load_v = [&] {
-    load_pairs(v_pairs + pair_off, vp);
+#pragma unroll
+    for (int g = 0; g < G; ++g) vp[g] = v_pairs[pair_off + g];
 #pragma unroll
     for (int j = 0; j < W; ++j) {
       const int piece = 64 * j + lane, c = 4 * (piece % W);
@@ -247,18 +305,24 @@ __global__ __launch_bounds__(kWaves * 64) void attn4_kernel(Attn4Args p) {
   // read takes together, lie in different banks but for two blocks each.
   const auto v_row = [](int r) { return r * SD + 2 * (r >> 4 & 1); };
   // Pairs of the tile in LDS by group; zero where a position is not live, whatever lies there.
-  const auto put_pairs = [&](int which, const uint32_t* x, uint64_t now) {
+  const auto put_pairs = [&](uint64_t now) {
     const bool mine = (now >> lane) & 1;
 #pragma unroll
-    for (int g = 0; g < GP; ++g) pair_lds[wave][which][g][lane] = mine ? x[g] : 0u;
+    for (int g = 0; g < G; ++g) {
+      const uint32_t k = mine ? kp[g] : 0u, v = mine ? vp[g] : 0u;
+      const float scale = A::value((uint16_t)v);
+      pair_lds[wave][0][g][lane] = A::value((uint16_t)k);
+      pair_lds[wave][1][g][lane] = A::value((uint16_t)(k >> 16));
+      pair_lds[wave][2][g][lane] = scale;
+      pair_lds[wave][3][g][lane] = __builtin_fmaf(-16.f, scale, A::value((uint16_t)(v >> 16)));
+    }
   };
   const auto pairs_of = [&](int which, int blk) {
-    return *reinterpret_cast<const u32x4*>(&pair_lds[wave][which][my_group][16 * blk + 4 * qd]);
+    return *reinterpret_cast<const f32x4*>(&pair_lds[wave][which][my_pair][16 * blk + 4 * qd]);
   };
 
   uint32_t* const v_lds = reinterpret_cast<uint32_t*>(lds) + wave * kVDwords;
-  const float sc = p.scale;
-  const float sc2 = p.softcap > 0.f ? kLog2e : sc * kLog2e;
+  const float sc2 = p.softcap > 0.f ? kLog2e : sc * kLog2e;  // scores to base 2
   const float cap = sc / p.softcap;
   uint64_t live = 0;
   bool ready = false;  // this part's first tile is requested, and the next one's pages are read
@@ -277,10 +341,15 @@ __global__ __launch_bounds__(kWaves * 64) void attn4_kernel(Attn4Args p) {
       nxt = part_of(b, 0, rg.left);
     }
     const int b = cur.b;
-    float m = -INFINITY, l = 0.f, low_sum = 0.f;
-    f32x4 o[NB];
+    float m[NC], l[NC], low_sum[NC];  // m: of the scores before they are taken to base 2
+    f32x4 o[NC][NB];
 #pragma unroll
-    for (int i = 0; i < NB; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int n = 0; n < NC; ++n) {
+      m[n] = -INFINITY;
+      l[n] = low_sum[n] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) o[n][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
 
     // A wave's tiles follow each other from one part to the next, so that the next part's first is
     // in flight while the waves are joined.
@@ -297,22 +366,30 @@ __global__ __launch_bounds__(kWaves * 64) void attn4_kernel(Attn4Args p) {
       load_v();
     }
     for (; t < cur.t1; t += kStep) {
-      // the codes' products, without the 16 in each operand
-      f32x4 s[NT];
-      const float start = -16.f * q_sum;
+      // the codes' products: what is not there of a row's last 128 elements meets zeros of q
+      f32x4 s[NC][NT];
 #pragma unroll
       for (int blk = 0; blk < NT; ++blk) {
-        s[blk] = f32x4{start, start, start, start};
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-          const bf16x8 c = from_codes(kr[blk][w], pattern);
-          s[blk] = mfma_bf(c, qh[w], s[blk]);
-          if constexpr (!BF16) s[blk] = mfma_bf(c, ql[w], s[blk]);
+        for (int n = 0; n < NC; ++n) s[n][blk] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < NM; ++j) {
+          i32x8 c;
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            const int w = (8 * j + r) / 2;
+            c[r] = (int)(kr[blk][w < W ? w : 0] >> (r % 2 ? 4 : 0) & 0x0f0f0f0fu);
+          }
+#pragma unroll
+          for (int n = 0; n < NC; ++n)
+#pragma unroll
+            for (int piece = 0; piece < NP; ++piece)
+              s[n][blk] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                  c, qp[n][piece][j], s[n][blk], 0, 0, 0, 127 + 9, 0, q_scale[n] - 4 * piece);
         }
       }
       const uint64_t now = live;
-      put_pairs(0, kp, now);
-      put_pairs(1, vp, now);
+      put_pairs(now);
       // the next tile's K (positions past the range are not live and read the first slot)
       const bool last = t + kStep >= cur.t1;
       wave_lds_fence();
@@ -326,73 +403,96 @@ __global__ __launch_bounds__(kWaves * 64) void attn4_kernel(Attn4Args p) {
       // scores: this column's group, then all of the head's
 #pragma unroll
       for (int blk = 0; blk < NT; ++blk) {
-        const u32x4 pr = pairs_of(0, blk);
+        const f32x4 scale = pairs_of(0, blk), offset = pairs_of(1, blk);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float scale = A::value((uint16_t)pr[e]), offset = A::value((uint16_t)(pr[e] >> 16));
-          s[blk][e] = group_sum<GP>(__builtin_fmaf(scale, s[blk][e], offset * q_sum));
-        }
+        for (int n = 0; n < NC; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            s[n][blk][e] = group_sum<GP>(__builtin_fmaf(scale[e], s[n][blk][e], offset[e] * q_sum[n]));
       }
-
-      // running maximum and sum, in base 2
-      float mx = -INFINITY;
       if (p.softcap > 0.f) {
 #pragma unroll
-        for (int blk = 0; blk < NT; ++blk)
+        for (int n = 0; n < NC; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            s[blk][e] = capped(s[blk][e] * sc, s[blk][e] * cap, p.softcap);
+          for (int blk = 0; blk < NT; ++blk)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              s[n][blk][e] = capped(s[n][blk][e] * sc, s[n][blk][e] * cap, p.softcap);
       }
-#pragma unroll
-      for (int blk = 0; blk < NT; ++blk)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[blk][e] *= sc2;
       if (now != ~0ull) {
+        const uint32_t lo = (uint32_t)now >> (4 * qd), hi = (uint32_t)(now >> 32) >> (4 * qd);
 #pragma unroll
         for (int blk = 0; blk < NT; ++blk)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            s[blk][e] = (now >> (16 * blk + 4 * qd + e)) & 1 ? s[blk][e] : -INFINITY;
+          for (int e = 0; e < 4; ++e) {
+            // all ones where the position is live
+            const uint32_t mine =
+                (uint32_t)__builtin_amdgcn_sbfe((int)(blk < 2 ? lo : hi), 16 * (blk % 2) + e, 1);
+#pragma unroll
+            for (int n = 0; n < NC; ++n) {
+              const float x = s[n][blk][e];
+              const uint32_t bits =
+                  (__builtin_bit_cast(uint32_t, x) & mine) | (0xff800000u & ~mine);
+              s[n][blk][e] = __builtin_bit_cast(float, bits);
+            }
+          }
       }
+
+      // running maximum and sum
+      float base[NC];
 #pragma unroll
-      for (int blk = 0; blk < NT; ++blk)
+      for (int n = 0; n < NC; ++n) {
+        float mx = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mx = fmaxf(mx, s[blk][e]);
-      mx = fmaxf(mx, __shfl_xor(mx, 16));
-      mx = fmaxf(mx, __shfl_xor(mx, 32));
-      const float m_new = fmaxf(m, mx);
-      const float top = m_new == -INFINITY ? 0.f : m_new;  // nothing live so far
-      const float alpha = __builtin_amdgcn_exp2f(m - top);
-      if (__ballot(m_new > m)) {  // some head's maximum moved
-        l *= alpha;
-        low_sum *= alpha;
+        for (int blk = 0; blk < NT; ++blk)
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
+          for (int e = 0; e < 4; ++e) mx = fmaxf(mx, s[n][blk][e]);
+        const float m_new = fmaxf(m[n], column_max(mx));
+        const float top = m_new == -INFINITY ? 0.f : m_new;  // nothing live so far
+        if (__ballot(m_new > m[n])) {  // some head's maximum moved
+          const float alpha = __builtin_amdgcn_exp2f((m[n] - top) * sc2);
+          l[n] *= alpha;
+          low_sum[n] *= alpha;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[i][e] *= alpha;
+          for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[n][i][e] *= alpha;
+        }
+        m[n] = m_new;
+        base[n] = -top * sc2;
       }
-      m = m_new;
 
       // p times the scale of this column's group as two bf16 parts, cut off and rounded; element
       // 2 e + i of a product's eight is position e of block 2 k + i, as V's codes come
-      bf16x8 ph[NT / 2], pl[NT / 2];
+      bf16x8 ph[NC][NT / 2], pl[NC][NT / 2];
 #pragma unroll
       for (int k = 0; k < NT / 2; ++k) {
+        f32x4 scale[2], low[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const u32x4 pr = pairs_of(1, 2 * k + i);
+          scale[i] = pairs_of(2, 2 * k + i);
+          low[i] = pairs_of(3, 2 * k + i);
+        }
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+          u32x4 high;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float scale = A::value((uint16_t)pr[e]);
-            const float offset = A::value((uint16_t)(pr[e] >> 16));
-            const float x = __builtin_amdgcn_exp2f(s[2 * k + i][e] - top);
-            l += x;
-            low_sum = __builtin_fmaf(x, __builtin_fmaf(-16.f, scale, offset), low_sum);
-            const float y = x * scale;
-            const uint32_t high = __builtin_bit_cast(uint32_t, y) & 0xffff0000u;
-            ph[k][2 * e + i] = __builtin_bit_cast(bf16, (uint16_t)(high >> 16));
-            pl[k][2 * e + i] = (bf16)(y - __builtin_bit_cast(float, high));
+            float y[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float x =
+                  __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][2 * k + i][e], sc2, base[n]));
+              l[n] += x;
+              low_sum[n] = __builtin_fmaf(x, low[i][e], low_sum[n]);
+              y[i] = x * scale[i][e];
+              const uint32_t bits = __builtin_bit_cast(uint32_t, y[i]) & 0xffff0000u;
+              pl[n][k][2 * e + i] = (bf16)(y[i] - __builtin_bit_cast(float, bits));
+            }
+            high[e] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, y[1]),
+                                            __builtin_bit_cast(uint32_t, y[0]), 0x07060302u);
           }
+          ph[n][k] = __builtin_bit_cast(bf16x8, high);
         }
       }
 
@@ -414,8 +514,11 @@ __global__ __launch_bounds__(kWaves * 64) void attn4_kernel(Attn4Args p) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const bf16x8 v = from_codes((uint32_t)c[k], pattern);
-          o[i] = mfma_bf(v, ph[k], o[i]);
-          o[i] = mfma_bf(v, pl[k], o[i]);
+#pragma unroll
+          for (int n = 0; n < NC; ++n) {
+            o[n][i] = mfma_bf(v, ph[n][k], o[n][i]);
+            o[n][i] = mfma_bf(v, pl[n][k], o[n][i]);
+          }
         }
       }
       wave_lds_fence();
@@ -425,21 +528,22 @@ __global__ __launch_bounds__(kWaves * 64) void attn4_kernel(Attn4Args p) {
     if (more) load_q(nxt.b);
 
     // Join the waves, in wave order.
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
-    low_sum += __shfl_xor(low_sum, 16);
-    low_sum += __shfl_xor(low_sum, 32);
     __syncthreads();  // every wave is done with its V rows
     float* const o_lds = reinterpret_cast<float*>(lds);
-    if (qd == 0 && my_group == 0) {
-      ml_lds[wave][my_head][0] = m;
-      ml_lds[wave][my_head][1] = l;
-    }
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
-      if (16 * i / p.group_size == my_group)
-        *reinterpret_cast<f32x4*>(o_lds + (wave * HB + my_head) * OS + 16 * i + 4 * qd) =
-            f32x4{o[i][0] + low_sum, o[i][1] + low_sum, o[i][2] + low_sum, o[i][3] + low_sum};
+    for (int n = 0; n < NC; ++n) {
+      const float sum = column_sum(l[n]), low = column_sum(low_sum[n]);
+      const int head = n * HS + my_head;
+      if (qd == 0 && my_group == 0) {
+        ml_lds[wave][head][0] = m[n] * sc2;
+        ml_lds[wave][head][1] = sum;
+      }
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+        if (16 * i / p.group_size == my_group)
+          *reinterpret_cast<f32x4*>(o_lds + (wave * HB + head) * OS + 16 * i + 4 * qd) =
+              f32x4{o[n][i][0] + low, o[n][i][1] + low, o[n][i][2] + low, o[n][i][3] + low};
+    }
     __syncthreads();
     const int per_row = p.d / 4;
     for (int i = threadIdx.x; i < rows * per_row; i += kWaves * 64) {
@@ -485,33 +589,59 @@ __global__ __launch_bounds__(kWaves * 64) void attn4_kernel(Attn4Args p) {
   }
 }
 
-template <bool BF16, int W, int GP>
-void launch_attn4_w(const Attn4Args& p, dim3 grid, hipStream_t stream) {
+// Sets of columns of a work-group: two where one does not hold a KV head's query heads (they share
+// the conversions, the reads and the addresses), as far as the registers go.
+int column_sets(int group, int groups, int head_dim) {
+  return head_dim <= 128 && group * pow2_from(groups) > 16 ? 2 : 1;
+}
+
+template <bool BF16, int W, int G, bool FULL>
+void launch_attn4_n(const Attn4Args& p, dim3 grid, hipStream_t stream) {
   const dim3 block(kWaves * 64);
-  if (p.d == 32 * W)
-    hipLaunchKernelGGL((attn4_kernel<BF16, W, GP, true>), grid, block, 0, stream, p);
-  else
-    hipLaunchKernelGGL((attn4_kernel<BF16, W, GP, false>), grid, block, 0, stream, p);
-}
-
-template <bool BF16, int W>
-void launch_attn4_g(const Attn4Args& p, dim3 grid, hipStream_t stream) {
-  if (p.groups == 1) return launch_attn4_w<BF16, W, 1>(p, grid, stream);
-  if (p.groups == 2) return launch_attn4_w<BF16, W, 2>(p, grid, stream);
-  if constexpr (W > 2) {
-    if (p.groups <= 4) return launch_attn4_w<BF16, W, 4>(p, grid, stream);
+  if constexpr (W <= 4) {
+    if (column_sets(p.group, G, p.d) == 2) {
+      hipLaunchKernelGGL((attn4_kernel<BF16, W, G, 2, FULL>), grid, block, 0, stream, p);
+      return;
+    }
   }
-  if constexpr (W > 4) launch_attn4_w<BF16, W, 8>(p, grid, stream);
+  hipLaunchKernelGGL((attn4_kernel<BF16, W, G, 1, FULL>), grid, block, 0, stream, p);
 }
 
-// The instance for a head_dim: rounded up to 64, 96, 128, 192 and 256.
+// The instance for a head_dim: rounded up to 64, 96, 128, 192 and 256.  A head that is no multiple of 32
+// is one group, but for 160 and 224.
+template <bool BF16, int W>
+void launch_attn4_w(const Attn4Args& p, dim3 grid, hipStream_t stream) {
+  const int groups = p.d / p.group_size;
+  if (p.d != 32 * W) {
+    if constexpr (W == 6) {
+      if (groups == 5) return launch_attn4_n<BF16, W, 5, false>(p, grid, stream);
+    }
+    if constexpr (W == 8) {
+      if (groups == 7) return launch_attn4_n<BF16, W, 7, false>(p, grid, stream);
+    }
+    return launch_attn4_n<BF16, W, 1, false>(p, grid, stream);
+  }
+  if (groups == 1) return launch_attn4_n<BF16, W, 1, true>(p, grid, stream);
+  if constexpr (W == 2 || W == 4 || W == 8) {
+    if (groups == 2) return launch_attn4_n<BF16, W, 2, true>(p, grid, stream);
+  }
+  if constexpr (W == 4 || W == 8) {
+    if (groups == 4) return launch_attn4_n<BF16, W, 4, true>(p, grid, stream);
+  }
+  if constexpr (W == 8) launch_attn4_n<BF16, W, 8, true>(p, grid, stream);
+  if constexpr (W == 3 || W == 6) {
+    if (groups == 3) return launch_attn4_n<BF16, W, 3, true>(p, grid, stream);
+  }
+  if constexpr (W == 6) launch_attn4_n<BF16, W, 6, true>(p, grid, stream);
+}
+
 template <bool BF16>
 void launch_attn4(const Attn4Args& p, dim3 grid, hipStream_t stream) {
-  if (p.d <= 64) return launch_attn4_g<BF16, 2>(p, grid, stream);
-  if (p.d <= 96) return launch_attn4_g<BF16, 3>(p, grid, stream);
-  if (p.d <= 128) return launch_attn4_g<BF16, 4>(p, grid, stream);
-  if (p.d <= 192) return launch_attn4_g<BF16, 6>(p, grid, stream);
-  launch_attn4_g<BF16, 8>(p, grid, stream);
+  if (p.d <= 64) return launch_attn4_w<BF16, 2>(p, grid, stream);
+  if (p.d <= 96) return launch_attn4_w<BF16, 3>(p, grid, stream);
+  if (p.d <= 128) return launch_attn4_w<BF16, 4>(p, grid, stream);
+  if (p.d <= 192) return launch_attn4_w<BF16, 6>(p, grid, stream);
+  launch_attn4_w<BF16, 8>(p, grid, stream);
 }
 
 }  // namespace
@@ -520,7 +650,8 @@ AttnPlan attn4_plan(int batch, int q_heads, int kv_heads, int head_dim, int grou
                     int window) {
   AttnPlan plan{};
   const int groups = head_dim / group_size;
-  plan.block_shift = groups == 1 ? 4 : groups == 2 ? 3 : groups <= 4 ? 2 : 1;
+  const int in_set = groups == 1 ? 4 : groups == 2 ? 3 : groups <= 4 ? 2 : 1;
+  plan.block_shift = in_set + (column_sets(q_heads / kv_heads, groups, head_dim) == 2);
   const int heads = 1 << plan.block_shift;
   plan.head_blocks = (q_heads / kv_heads + heads - 1) / heads;
   plan.units = kv_heads * plan.head_blocks;
@@ -545,7 +676,9 @@ hipError_t launch_paged_attention4(const wq_attn4_args& a, const AttnPlan& plan,
   p.pair_slot = a.pairs.slot_stride;
   p.pair_head = a.pairs.head_stride;
   p.group_size = a.pairs.group_size;
-  p.groups = p.d / p.group_size;
+  const int64_t limit = int64_t(1) << 32;
+  p.short_strides = p.page_stride < limit && p.page_size * p.slot_stride < limit &&
+                    p.pair_page < limit && p.page_size * p.pair_slot < limit;
   const bool bf16 = (a.flags & WQ_FLAG_BF16) != 0;
   // units that read the same rows or share lines, as in the 16-bit kernel
   p.near_units = plan.head_blocks > 1 ||

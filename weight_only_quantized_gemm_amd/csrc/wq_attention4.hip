@@ -152,13 +152,17 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
     return s;
   };
 
+  // A lane holds K's rows in pieces of four or two dwords, of which the four lanes of a row make a run.
+  // Where the head ends inside one, a piece is read from as far before its place as it takes, and
+  // what is there twice meets zeros of q the second time.
+  constexpr int kPiece = W == 2 || W == 3 ? 2 : 4;
+  constexpr auto kLength = [](int w) {  // of the piece that register w begins
+    return W == 3 && w == 2 ? 1 : W == 6 && w == 4 ? 2 : kPiece;
+  };
   const int nd = FULL ? 4 * W : p.d / 8;  // dwords of a row
-  // The dword of a row that a lane holds in its w-th register: 16 or 8 bytes side by side.
-  const auto dword_of = [&](int w) {
-    if (W == 2) return 2 * qd + w;
-    if (W == 3) return w < 2 ? 2 * qd + w : 8 + qd;
-    if (W == 6) return w < 4 ? 4 * qd + w : 16 + 2 * qd + (w - 4);
-    return 16 * (w / 4) + 4 * qd + w % 4;
+  const auto place_of_piece = [&](int w) { return 4 * w + kLength(w) * qd; };
+  const auto piece_at = [&](int w) {
+    return FULL ? place_of_piece(w) : min(place_of_piece(w), nd - kLength(w));
   };
 
   // q as the B operand: this column's head, its group's elements, as pieces below 2^8 times the power
@@ -179,9 +183,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
       float x[W][8], most = 0.f, sum = 0.f;
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        const int dw = dword_of(w);
+        const int first = w / kPiece * kPiece;
+        const int dw = piece_at(first) + w - first;
         u32x4 raw = {0u, 0u, 0u, 0u};
-        if ((FULL || dw < nd) && head < rows && 8 * dw / p.group_size == my_group)
+        if ((FULL || dw >= place_of_piece(first)) && head < rows && 8 * dw / p.group_size == my_group)
           raw = *reinterpret_cast<const u32x4*>(src + 8 * dw);
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
@@ -266,20 +271,11 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
 #pragma unroll
     for (int blk = 0; blk < NT; ++blk) {
       const uint8_t* at = kbase + off_lds[wave][16 * blk + row];
-      if constexpr (FULL) {
-        constexpr int kPiece = W == 2 || W == 3 ? 2 : 4;
 #pragma unroll
-        for (int w = 0; w < W; w += kPiece) {
-          const uint32_t* src = reinterpret_cast<const uint32_t*>(at) + dword_of(w);
+      for (int w = 0; w < W; w += kPiece) {
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(at) + piece_at(w);
 #pragma unroll
-          for (int i = w; i < (w + kPiece < W ? w + kPiece : W); ++i) kr[blk][i] = src[i - w];
-        }
-      } else {  // a dword past the head's end meets a zero of q: the first one is read instead
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-          const int dw = dword_of(w);
-          kr[blk][w] = reinterpret_cast<const uint32_t*>(at)[dw < nd ? dw : 0];
-        }
+        for (int i = 0; i < kLength(w); ++i) kr[blk][w + i] = src[i];
       }
     }
   };
@@ -292,12 +288,12 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
       const int piece = 64 * j + lane, c = 4 * (piece % W);
       const uint32_t* at =
           reinterpret_cast<const uint32_t*>(vbase + off_lds[wave][piece / W]);
-      if constexpr (FULL) {
+      if (FULL || nd >= 4) {  // (the last piece of a row ends where the head does)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) vr[j][i] = __builtin_nontemporal_load(at + c + i);
+        for (int i = 0; i < 4; ++i) vr[j][i] = __builtin_nontemporal_load(at + min(c, nd - 4) + i);
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) vr[j][i] = at[c + i < nd ? c + i : 0];
+        for (int i = 0; i < 4; ++i) vr[j][i] = at[min(c + i, nd - 1)];
       }
     }
   };
@@ -326,8 +322,8 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
   const float cap = sc / p.softcap;
   uint64_t live = 0;
   bool ready = false;  // this part's first tile is requested, and the next one's pages are read
+  bool first_part = true;
   Part cur = part_of(rg.b, rg.first, rg.left);
-  load_q(cur.b);
 
   for (;;) {
     rg.left -= cur.count;
@@ -365,6 +361,8 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
       load_k();
       load_v();
     }
+    if (first_part) load_q(cur.b);  // (behind the requests of the first tile)
+    first_part = false;
     for (; t < cur.t1; t += kStep) {
       // the codes' products: what is not there of a row's last 128 elements meets zeros of q
       f32x4 s[NC][NT];
@@ -499,9 +497,16 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
 #pragma unroll
       for (int j = 0; j < W; ++j) {
         const int piece = 64 * j + lane;
-        uint32_t* at = v_lds + v_row(piece / W) + 4 * (piece % W);
-        *reinterpret_cast<u32x2*>(at) = u32x2{vr[j][0], vr[j][1]};
-        *reinterpret_cast<u32x2*>(at + 2) = u32x2{vr[j][2], vr[j][3]};
+        uint32_t* at = v_lds + v_row(piece / W);
+        if constexpr (FULL) {
+          at += 4 * (piece % W);
+          *reinterpret_cast<u32x2*>(at) = u32x2{vr[j][0], vr[j][1]};
+          *reinterpret_cast<u32x2*>(at + 2) = u32x2{vr[j][2], vr[j][3]};
+        } else {  // (where it was read; of a head of less than 32 elements the first piece holds all)
+          at += nd >= 4 ? min(4 * (piece % W), nd - 4) : 4 * (piece % W);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) at[i] = vr[j][i];
+        }
       }
       wave_lds_fence();
       load_v();

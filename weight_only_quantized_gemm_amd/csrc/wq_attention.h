@@ -202,9 +202,10 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs p) {
     p.lse[h] = sum == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
-// The arguments that every kind of cache has, from the call's (wq_attn_args or wq_attn4_args).
+// The arguments that every kind of cache has, from the call's (wq_attn_args or wq_attn4_args).  group:
+// query heads that count as a KV head's.
 template <class Args>
-AttnArgs attn_args(const Args& a, const AttnPlan& plan) {
+AttnArgs attn_args(const Args& a, const AttnPlan& plan, int group) {
   AttnArgs p{};
   p.q = static_cast<const uint16_t*>(a.q);
   p.out = static_cast<uint16_t*>(a.out);
@@ -224,7 +225,7 @@ AttnArgs attn_args(const Args& a, const AttnPlan& plan) {
   p.kv_heads = a.cache.kv_heads;
   p.q_heads = a.q_heads;
   p.d = a.cache.head_dim;
-  p.group = a.q_heads / a.cache.kv_heads;
+  p.group = group;
   p.head_blocks = plan.head_blocks;
   p.max_len = a.max_len;
   p.table_stride = a.table_stride;

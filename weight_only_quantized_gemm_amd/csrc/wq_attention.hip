@@ -514,7 +514,7 @@ size_t attn_workspace_bytes(const AttnPlan& plan, int batch, int q_heads, int kv
 
 hipError_t launch_paged_attention(const wq_attn_args& a, const AttnPlan& plan,
                                   hipStream_t stream) {
-  AttnArgs p = attn_args(a, plan);
+  AttnArgs p = attn_args(a, plan, a.q_heads / a.cache.kv_heads);
   const bool bf16 = (a.flags & WQ_FLAG_BF16) != 0, kv8 = (a.flags & WQ_FLAG_FP8) != 0;
   // Work-groups go to the eight XCDs in turn.  Where several blocks of query heads read the same
   // rows, or the heads of a slot lie side by side in rows that do not end with a line, the units of

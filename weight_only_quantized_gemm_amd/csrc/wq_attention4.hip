@@ -30,12 +30,14 @@
 namespace wq {
 namespace {
 
-constexpr int kTile = 64, kStep = kWaves * kTile;  // positions of a wave's step, and of all four's
+// Positions of a wave's step: 64 rows of K and V, of one KV head or of two.
+constexpr int tile_of(int nk) { return 64 / nk; }
 
 struct Attn4Args : AttnArgs {
   const uint32_t *k_pairs, *v_pairs;
   int64_t pair_page, pair_slot, pair_head;
   int group_size;
+  int kv_group;       // query heads of a KV head (`group`: those of a work-group's NK)
   int short_strides;  // strides of pages and slots, and slots times strides, are below 2^32
 };
 
@@ -93,14 +95,18 @@ __device__ __forceinline__ float column_sum(float x) {
 constexpr int pow2_from(int x) { return x <= 1 ? 1 : x <= 2 ? 2 : x <= 4 ? 4 : 8; }
 
 // W: dwords of a row that a lane holds of K, head_dim rounded up over 32.  G: groups of a head.  NC:
-// sets of sixteen columns that a work-group takes, which share K's and V's operands.  FULL: head_dim is
-// 32 W.
-template <bool BF16, int W, int G, int NC, bool FULL>
+// sets of sixteen columns that a work-group takes, which share K's and V's operands.  NK: KV heads that
+// share a set: the first half of a tile's rows is one's, the second the other's, and a column looks at
+// its own.  FULL: head_dim is 32 W.
+template <bool BF16, int W, int G, int NC, int NK, bool FULL>
 __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
   using A = Act<BF16>;
+  static_assert(NK == 1 || NC == 1, "two KV heads take one set of columns");
   constexpr int DP = 32 * W;
   constexpr int GP = pow2_from(G);
-  constexpr int NT = kTile / 16;       // 16-position blocks of a tile
+  constexpr int kTile = tile_of(NK), kStep = kWaves * kTile;
+  constexpr int NT = 4;                // 16-row blocks of a tile
+  constexpr int NL = NT / NK;          // blocks that a column looks at
   constexpr int NB = DP / 16;          // 16-element blocks of the output
   constexpr int NM = (2 * W + 7) / 8;  // 128-element steps of K
   constexpr int NP = BF16 ? 2 : 3;     // pieces of q
@@ -108,11 +114,11 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
   constexpr int HB = NC * HS;          // and of a work-group
   constexpr int SD = W % 2 == 0 ? 4 * W + 4 : 4 * W + 8;  // dwords of an LDS row of V: 4 mod 8
   constexpr int OS = DP + 4;           // LDS row of the joined outputs
-  constexpr int kVDwords = kTile * SD + 2;
+  constexpr int kVDwords = 64 * SD + 2;
   constexpr int kVBytes = kWaves * kVDwords * 4, kOBytes = kWaves * HB * OS * 4;
   __shared__ __align__(16) uint8_t lds[kVBytes > kOBytes ? kVBytes : kOBytes];
   // scales and offsets of K, scales and offsets less 16 scales of V
-  __shared__ __align__(16) float pair_lds[kWaves][4][G][kTile];
+  __shared__ __align__(16) float pair_lds[kWaves][4][G][64];
   __shared__ int64_t off_lds[kWaves][kTile];
   __shared__ float ml_lds[kWaves][HB][2];
 
@@ -127,8 +133,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
   if (p.ranges > 0 && !find_range<kTile>(p, index, blockIdx.x == 0 && wave == 0, lane, rg)) return;
   const int kvh = unit / p.head_blocks, hb = unit - kvh * p.head_blocks;
   const int h0 = kvh * p.group + HB * hb;         // first query head
-  const int rows = min(HB, p.group - HB * hb);
+  const int rows = min(min(HB, p.group - HB * hb), p.q_heads - h0);
   const int my_head = row / GP, my_group = row % GP;  // this lane's column in a set
+  const int my_kv = NK == 1 ? 0 : (int)(my_head >= p.kv_group);  // its KV head of the work-group's
   const int my_pair = GP == G ? my_group : min(my_group, G - 1);  // (no group: any pair will do)
 
   // Part of a sequence that this range holds.
@@ -225,16 +232,20 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
     }
   };
 
-  const uint8_t* kbase = p.k + kvh * p.head_stride / 2;
-  const uint8_t* vbase = p.v + kvh * p.head_stride / 2;
-  const uint32_t* k_pairs = p.k_pairs + kvh * p.pair_head;
-  const uint32_t* v_pairs = p.v_pairs + kvh * p.pair_head;
+  // the second KV head's rows; of an odd number of heads the last again, for columns without heads
+  const int64_t second = NK == 2 && NK * kvh + 1 < p.kv_heads ? 1 : 0;
+  const uint8_t* kbase = p.k + NK * kvh * p.head_stride / 2;
+  const uint8_t* vbase = p.v + NK * kvh * p.head_stride / 2;
+  const int64_t row_step = second * p.head_stride / 2;
+  const int64_t pair_step = NK == 2 && lane >= 32 ? second * p.pair_head : 0;
+  const uint32_t* k_pairs = p.k_pairs + NK * kvh * p.pair_head + pair_step;
+  const uint32_t* v_pairs = p.v_pairs + NK * kvh * p.pair_head + pair_step;
 
-  // Page numbers (and keep bytes) of the tile at t, one position per lane.
+  // Page numbers (and keep bytes) of the tile at t, one position per lane (NK 2: and half-wave).
   int page_next = -1, pos_next = 0, slot_next = 0;
   uint8_t keep_next = 1;
   const auto read_pages = [&](int b, int t_pages, int t) {
-    const int pos = t + lane;
+    const int pos = t + (lane & (kTile - 1));
     const int at = (int)(__umulhi(2u * (unsigned)pos, p.page_mul) >> p.page_shift);
     pos_next = pos;
     slot_next = pos - at * p.page_size;
@@ -252,13 +263,13 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
                       pos_next >= lo && pos_next < t1;
     const int page = live ? page_next : 0, slot = live ? slot_next : 0;
     if (p.short_strides) {
-      off_lds[wave][lane] = (int64_t)(((uint64_t)(uint32_t)page * (uint32_t)p.page_stride +
+      off_lds[wave][lane & (kTile - 1)] = (int64_t)(((uint64_t)(uint32_t)page * (uint32_t)p.page_stride +
                                        (uint32_t)slot * (uint32_t)p.slot_stride) /
                                       2);
       pair_off = (int64_t)((uint64_t)(uint32_t)page * (uint32_t)p.pair_page +
                            (uint32_t)slot * (uint32_t)p.pair_slot);
     } else {
-      off_lds[wave][lane] = (page * p.page_stride + slot * p.slot_stride) / 2;
+      off_lds[wave][lane & (kTile - 1)] = (page * p.page_stride + slot * p.slot_stride) / 2;
       pair_off = page * p.pair_page + slot * p.pair_slot;
     }
     return __ballot(live);
@@ -270,7 +281,8 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
     for (int g = 0; g < G; ++g) kp[g] = k_pairs[pair_off + g];
 #pragma unroll
     for (int blk = 0; blk < NT; ++blk) {
-      const uint8_t* at = kbase + off_lds[wave][16 * blk + row];
+      const uint8_t* at = kbase + off_lds[wave][(16 * blk + row) & (kTile - 1)];
+      if (NK == 2 && blk >= NL) at += row_step;
 #pragma unroll
       for (int w = 0; w < W; w += kPiece) {
         const uint32_t* src = reinterpret_cast<const uint32_t*>(at) + piece_at(w);
@@ -285,9 +297,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
     for (int g = 0; g < G; ++g) vp[g] = v_pairs[pair_off + g];
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-      const int piece = 64 * j + lane, c = 4 * (piece % W);
-      const uint32_t* at =
-          reinterpret_cast<const uint32_t*>(vbase + off_lds[wave][piece / W]);
+      const int piece = 64 * j + lane, r = piece / W, c = 4 * (piece % W);
+      const uint32_t* at = reinterpret_cast<const uint32_t*>(
+          vbase + off_lds[wave][r & (kTile - 1)] + (NK == 2 && r >= kTile ? row_step : 0));
       if (FULL || nd >= 4) {  // (the last piece of a row ends where the head does)
 #pragma unroll
         for (int i = 0; i < 4; ++i) vr[j][i] = __builtin_nontemporal_load(at + min(c, nd - 4) + i);
@@ -313,8 +325,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
       pair_lds[wave][3][g][lane] = __builtin_fmaf(-16.f, scale, A::value((uint16_t)(v >> 16)));
     }
   };
-  const auto pairs_of = [&](int which, int blk) {
-    return *reinterpret_cast<const f32x4*>(&pair_lds[wave][which][my_pair][16 * blk + 4 * qd]);
+  const auto pairs_of = [&](int which, int blk) {  // (blk: of those that this column looks at)
+    return *reinterpret_cast<const f32x4*>(
+        &pair_lds[wave][which][my_pair][kTile * my_kv + 16 * blk + 4 * qd]);
   };
 
   uint32_t* const v_lds = reinterpret_cast<uint32_t*>(lds) + wave * kVDwords;
@@ -365,11 +378,11 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
     first_part = false;
     for (; t < cur.t1; t += kStep) {
       // the codes' products: what is not there of a row's last 128 elements meets zeros of q
-      f32x4 s[NC][NT];
+      f32x4 all[NC][NT];
 #pragma unroll
       for (int blk = 0; blk < NT; ++blk) {
 #pragma unroll
-        for (int n = 0; n < NC; ++n) s[n][blk] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int n = 0; n < NC; ++n) all[n][blk] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < NM; ++j) {
           i32x8 c;
@@ -382,10 +395,21 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
           for (int n = 0; n < NC; ++n)
 #pragma unroll
             for (int piece = 0; piece < NP; ++piece)
-              s[n][blk] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                  c, qp[n][piece][j], s[n][blk], 0, 0, 0, 127 + 9, 0, q_scale[n] - 4 * piece);
+              all[n][blk] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                  c, qp[n][piece][j], all[n][blk], 0, 0, 0, 127 + 9, 0, q_scale[n] - 4 * piece);
         }
       }
+      f32x4 s[NC][NL];
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int blk = 0; blk < NL; ++blk) {
+          s[n][blk] = all[n][blk];
+          if constexpr (NK == 2) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[n][blk][e] = my_kv ? all[n][blk + NL][e] : all[n][blk][e];
+          }
+        }
       const uint64_t now = live;
       put_pairs(now);
       // the next tile's K (positions past the range are not live and read the first slot)
@@ -400,7 +424,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
 
       // scores: this column's group, then all of the head's
 #pragma unroll
-      for (int blk = 0; blk < NT; ++blk) {
+      for (int blk = 0; blk < NL; ++blk) {
         const f32x4 scale = pairs_of(0, blk), offset = pairs_of(1, blk);
 #pragma unroll
         for (int n = 0; n < NC; ++n)
@@ -412,15 +436,16 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
 #pragma unroll
         for (int n = 0; n < NC; ++n)
 #pragma unroll
-          for (int blk = 0; blk < NT; ++blk)
+          for (int blk = 0; blk < NL; ++blk)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               s[n][blk][e] = capped(s[n][blk][e] * sc, s[n][blk][e] * cap, p.softcap);
       }
       if (now != ~0ull) {
-        const uint32_t lo = (uint32_t)now >> (4 * qd), hi = (uint32_t)(now >> 32) >> (4 * qd);
+        uint32_t lo = (uint32_t)now >> (4 * qd), hi = (uint32_t)(now >> 32) >> (4 * qd);
+        if (NK == 2) hi = lo;  // (both KV heads' positions are the same)
 #pragma unroll
-        for (int blk = 0; blk < NT; ++blk)
+        for (int blk = 0; blk < NL; ++blk)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             // all ones where the position is live
@@ -442,7 +467,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
       for (int n = 0; n < NC; ++n) {
         float mx = -INFINITY;
 #pragma unroll
-        for (int blk = 0; blk < NT; ++blk)
+        for (int blk = 0; blk < NL; ++blk)
 #pragma unroll
           for (int e = 0; e < 4; ++e) mx = fmaxf(mx, s[n][blk][e]);
         const float m_new = fmaxf(m[n], column_max(mx));
@@ -462,9 +487,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
 
       // p times the scale of this column's group as two bf16 parts, cut off and rounded; element
       // 2 e + i of a product's eight is position e of block 2 k + i, as V's codes come
-      bf16x8 ph[NC][NT / 2], pl[NC][NT / 2];
+      bf16x8 ph[NC][2], pl[NC][2];
 #pragma unroll
-      for (int k = 0; k < NT / 2; ++k) {
+      for (int k = 0; k < NL / 2; ++k) {
         f32x4 scale[2], low[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -492,6 +517,13 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
           }
           ph[n][k] = __builtin_bit_cast(bf16x8, high);
         }
+      }
+      if constexpr (NK == 2) {  // a column's own KV head's rows alone
+        const bf16x8 none = {};
+        ph[0][1] = my_kv ? ph[0][0] : none;
+        pl[0][1] = my_kv ? pl[0][0] : none;
+        ph[0][0] = my_kv ? none : ph[0][0];
+        pl[0][0] = my_kv ? none : pl[0][0];
       }
 
 #pragma unroll
@@ -594,87 +626,123 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
   }
 }
 
-// Sets of columns of a work-group: two where one does not hold a KV head's query heads (they share
-// the conversions, the reads and the addresses), as far as the registers go.
-int column_sets(int group, int groups, int head_dim) {
-  return head_dim <= 128 && group * pow2_from(groups) > 16 ? 2 : 1;
+// How a KV head's query heads lie in columns.  Two KV heads share a set where both fit (`pairs`): a
+// column then works on half of the rows, a position's rows of two heads, which may share lines, are
+// read together, and positions are cut more finely.  Two sets where one does not hold the heads of
+// one (they share the conversions, the reads and the addresses), as far as the registers go.
+struct Columns {
+  int kv_heads, sets;
+  int heads_log2;  // query heads of a work-group, at most
+};
+Columns columns_of(int group, int kv_heads, int groups, int head_dim, bool pairs) {
+  const int padded = pow2_from(groups);
+  Columns c{1, 1, padded == 1 ? 4 : padded == 2 ? 3 : padded == 4 ? 2 : 1};
+  if (pairs && kv_heads > 1 && 2 * group * padded <= 16) {
+    c.kv_heads = 2;
+  } else if (head_dim <= 128 && group * padded > 16) {
+    c.sets = 2;
+    ++c.heads_log2;
+  }
+  return c;
 }
 
 template <bool BF16, int W, int G, bool FULL>
-void launch_attn4_n(const Attn4Args& p, dim3 grid, hipStream_t stream) {
+void launch_attn4_n(const Attn4Args& p, const Columns& c, dim3 grid, hipStream_t stream) {
   const dim3 block(kWaves * 64);
+  if (c.kv_heads == 2) {
+    if constexpr (G < 8)  // (eight groups leave no room)
+      hipLaunchKernelGGL((attn4_kernel<BF16, W, G, 1, 2, FULL>), grid, block, 0, stream, p);
+    return;
+  }
   if constexpr (W <= 4) {
-    if (column_sets(p.group, G, p.d) == 2) {
-      hipLaunchKernelGGL((attn4_kernel<BF16, W, G, 2, FULL>), grid, block, 0, stream, p);
+    if (c.sets == 2) {
+      hipLaunchKernelGGL((attn4_kernel<BF16, W, G, 2, 1, FULL>), grid, block, 0, stream, p);
       return;
     }
   }
-  hipLaunchKernelGGL((attn4_kernel<BF16, W, G, 1, FULL>), grid, block, 0, stream, p);
+  hipLaunchKernelGGL((attn4_kernel<BF16, W, G, 1, 1, FULL>), grid, block, 0, stream, p);
 }
 
 // The instance for a head_dim: rounded up to 64, 96, 128, 192 and 256.  A head that is no multiple of 32
 // is one group, but for 160 and 224.
 template <bool BF16, int W>
-void launch_attn4_w(const Attn4Args& p, dim3 grid, hipStream_t stream) {
+void launch_attn4_w(const Attn4Args& p, const Columns& c, dim3 grid, hipStream_t stream) {
   const int groups = p.d / p.group_size;
   if (p.d != 32 * W) {
     if constexpr (W == 6) {
-      if (groups == 5) return launch_attn4_n<BF16, W, 5, false>(p, grid, stream);
+      if (groups == 5) return launch_attn4_n<BF16, W, 5, false>(p, c, grid, stream);
     }
     if constexpr (W == 8) {
-      if (groups == 7) return launch_attn4_n<BF16, W, 7, false>(p, grid, stream);
+      if (groups == 7) return launch_attn4_n<BF16, W, 7, false>(p, c, grid, stream);
     }
-    return launch_attn4_n<BF16, W, 1, false>(p, grid, stream);
+    return launch_attn4_n<BF16, W, 1, false>(p, c, grid, stream);
   }
-  if (groups == 1) return launch_attn4_n<BF16, W, 1, true>(p, grid, stream);
+  if (groups == 1) return launch_attn4_n<BF16, W, 1, true>(p, c, grid, stream);
   if constexpr (W == 2 || W == 4 || W == 8) {
-    if (groups == 2) return launch_attn4_n<BF16, W, 2, true>(p, grid, stream);
+    if (groups == 2) return launch_attn4_n<BF16, W, 2, true>(p, c, grid, stream);
   }
   if constexpr (W == 4 || W == 8) {
-    if (groups == 4) return launch_attn4_n<BF16, W, 4, true>(p, grid, stream);
+    if (groups == 4) return launch_attn4_n<BF16, W, 4, true>(p, c, grid, stream);
   }
-  if constexpr (W == 8) launch_attn4_n<BF16, W, 8, true>(p, grid, stream);
+  if constexpr (W == 8) launch_attn4_n<BF16, W, 8, true>(p, c, grid, stream);
   if constexpr (W == 3 || W == 6) {
-    if (groups == 3) return launch_attn4_n<BF16, W, 3, true>(p, grid, stream);
+    if (groups == 3) return launch_attn4_n<BF16, W, 3, true>(p, c, grid, stream);
   }
-  if constexpr (W == 6) launch_attn4_n<BF16, W, 6, true>(p, grid, stream);
+  if constexpr (W == 6) launch_attn4_n<BF16, W, 6, true>(p, c, grid, stream);
 }
 
 template <bool BF16>
-void launch_attn4(const Attn4Args& p, dim3 grid, hipStream_t stream) {
-  if (p.d <= 64) return launch_attn4_w<BF16, 2>(p, grid, stream);
-  if (p.d <= 96) return launch_attn4_w<BF16, 3>(p, grid, stream);
-  if (p.d <= 128) return launch_attn4_w<BF16, 4>(p, grid, stream);
-  if (p.d <= 192) return launch_attn4_w<BF16, 6>(p, grid, stream);
-  launch_attn4_w<BF16, 8>(p, grid, stream);
+void launch_attn4(const Attn4Args& p, const Columns& c, dim3 grid, hipStream_t stream) {
+  if (p.d <= 64) return launch_attn4_w<BF16, 2>(p, c, grid, stream);
+  if (p.d <= 96) return launch_attn4_w<BF16, 3>(p, c, grid, stream);
+  if (p.d <= 128) return launch_attn4_w<BF16, 4>(p, c, grid, stream);
+  if (p.d <= 192) return launch_attn4_w<BF16, 6>(p, c, grid, stream);
+  launch_attn4_w<BF16, 8>(p, c, grid, stream);
 }
 
 }  // namespace
 
 AttnPlan attn4_plan(int batch, int q_heads, int kv_heads, int head_dim, int group_size, int max_len,
                     int window) {
-  AttnPlan plan{};
-  const int groups = head_dim / group_size;
-  const int in_set = groups == 1 ? 4 : groups == 2 ? 3 : groups <= 4 ? 2 : 1;
-  plan.block_shift = in_set + (column_sets(q_heads / kv_heads, groups, head_dim) == 2);
-  const int heads = 1 << plan.block_shift;
-  plan.head_blocks = (q_heads / kv_heads + heads - 1) / heads;
-  plan.units = kv_heads * plan.head_blocks;
-  // positions a sequence may need, from the tile that holds the window's first
-  const long span = window > 0 && window < max_len - kTile ? window + kTile - 1 : max_len;
-  const long keys = span * (head_dim / 2 + 4 * groups);
-  const long whole = std::min(256l, std::max(96l, (long)batch * plan.units)) * 512;
-  if (span > kStep && keys > whole) {
-    const int work_groups = head_dim <= 128 ? 512 : 256;
-    plan.ranges = std::max(1, work_groups / plan.units);
-  }
+  const int groups = head_dim / group_size, group = q_heads / kv_heads;
+  Columns c;
+  const auto plan_of = [&](bool pairs) {
+    c = columns_of(group, kv_heads, groups, head_dim, pairs);
+    const int heads = 1 << c.heads_log2;
+    AttnPlan plan{};
+    plan.block_shift = c.heads_log2;
+    plan.head_blocks = (c.kv_heads * group + heads - 1) / heads;
+    plan.units = (kv_heads + c.kv_heads - 1) / c.kv_heads * plan.head_blocks;
+    return plan;
+  };
+  // Positions a sequence may need, from the tile that holds the window's first.  Short sequences stay
+  // whole, by single KV heads, which makes more work-groups.
+  AttnPlan plan = plan_of(false);
+  const long span = window > 0 && window < max_len - 64 ? window + 63 : max_len;
+  const long whole = 7 * std::min(256l, std::max(96l, (long)batch * plan.units));
+  if (span <= kWaves * 64 || span <= whole) return plan;
+  plan = plan_of(true);
+  const int work_groups = head_dim <= 128 ? 512 : 256;
+  plan.ranges = std::max(1, work_groups / plan.units);
   return plan;
+}
+
+size_t attn4_workspace_bytes(const AttnPlan& plan, int batch, int q_heads, int kv_heads,
+                             int head_dim, int group_size) {
+  const Columns c = columns_of(q_heads / kv_heads, kv_heads, head_dim / group_size, head_dim,
+                               plan.ranges > 0);
+  // (as many rows to a partial as a work-group has heads)
+  return attn_workspace_bytes(plan, batch, c.kv_heads * (q_heads / kv_heads), 1, head_dim);
 }
 
 hipError_t launch_paged_attention4(const wq_attn4_args& a, const AttnPlan& plan,
                                    hipStream_t stream) {
+  const int group = a.q_heads / a.cache.kv_heads, groups = a.cache.head_dim / a.pairs.group_size;
+  const Columns c = columns_of(group, a.cache.kv_heads, groups, a.cache.head_dim, plan.ranges > 0);
   Attn4Args p{};
-  static_cast<AttnArgs&>(p) = attn_args(a, plan);
+  // the query heads of a work-group's KV heads count as one's
+  static_cast<AttnArgs&>(p) = attn_args(a, plan, c.kv_heads * group);
+  p.kv_group = group;
   p.k_pairs = static_cast<const uint32_t*>(a.pairs.k);
   p.v_pairs = static_cast<const uint32_t*>(a.pairs.v);
   p.pair_page = a.pairs.page_stride;
@@ -685,14 +753,17 @@ hipError_t launch_paged_attention4(const wq_attn4_args& a, const AttnPlan& plan,
   p.short_strides = p.page_stride < limit && p.page_size * p.slot_stride < limit &&
                     p.pair_page < limit && p.page_size * p.pair_slot < limit;
   const bool bf16 = (a.flags & WQ_FLAG_BF16) != 0;
-  // units that read the same rows or share lines, as in the 16-bit kernel
-  p.near_units = plan.head_blocks > 1 ||
-                 (p.kv_heads > 1 && p.head_stride < p.slot_stride && p.head_stride / 2 % 128 != 0);
+  // units that read the same rows or share lines, of codes or of pairs, as in the 16-bit kernel
+  const auto shares = [&](int64_t head, int64_t slot) { return head < slot && head % 128 != 0; };
+  p.near_units =
+      plan.head_blocks > 1 ||
+      (plan.units > 1 && (shares(c.kv_heads * p.head_stride / 2, p.slot_stride / 2) ||
+                          shares(c.kv_heads * p.pair_head * 4, p.pair_slot * 4)));
   const dim3 grid = attn_grid(p);
   if (bf16)
-    launch_attn4<true>(p, grid, stream);
+    launch_attn4<true>(p, c, grid, stream);
   else
-    launch_attn4<false>(p, grid, stream);
+    launch_attn4<false>(p, c, grid, stream);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || plan.ranges == 0) return e;
   return launch_attn_join(p, bf16, stream);

@@ -37,6 +37,8 @@ hipError_t launch_paged_attention(const wq_attn_args& a, const AttnPlan& plan,
 
 AttnPlan attn4_plan(int batch, int q_heads, int kv_heads, int head_dim, int group_size, int max_len,
                     int window);
+size_t attn4_workspace_bytes(const AttnPlan& plan, int batch, int q_heads, int kv_heads,
+                             int head_dim, int group_size);
 hipError_t launch_paged_attention4(const wq_attn4_args& a, const AttnPlan& plan,
                                    hipStream_t stream);
 

@@ -263,7 +263,7 @@ int wq_paged_attention4_workspace_bytes(int batch, int q_heads, int kv_heads, in
   const wq::AttnPlan plan =
       wq::attn4_plan(batch, q_heads, kv_heads, head_dim, group_size, max_len, window);
   if (attention_too_large(plan, batch, max_len, window)) return fail(WQ_STAGE_SHAPE, WQ_ERR_OVERFLOW);
-  *bytes_out = wq::attn_workspace_bytes(plan, batch, q_heads, kv_heads, head_dim);
+  *bytes_out = wq::attn4_workspace_bytes(plan, batch, q_heads, kv_heads, head_dim, group_size);
   return 0;
 }
 

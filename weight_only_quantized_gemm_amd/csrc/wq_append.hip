@@ -11,6 +11,7 @@
 // Sines and cosines are formed once per work-group and token, the angle in fp64 (a position of
 // 10^6 times an fp32 frequency loses the phase in fp32).
 #include <algorithm>
+#include <type_traits>
 
 #include "wq_decode.h"
 #include "wq_device.h"
@@ -40,7 +41,7 @@ struct AppendArgs {
   int end[WQ_MAX_ROPE_AXES];  // first pair past each axis
   int axes;
   int lanes_log2;             // lanes of a head
-  float eps;
+  float eps, inv_d;
 };
 
 template <bool BF16>
@@ -72,23 +73,56 @@ __device__ __forceinline__ uint32_t pack4_e4m3(const float* f, float scale) {
   return (uint32_t)w;
 }
 
+// (a 64-bit division costs as much as a head's norm)
+__device__ __forceinline__ int64_t page_of(int64_t slot, int page_size, int64_t total) {
+  return total <= 0xffffffffll ? (int64_t)((uint32_t)slot / (uint32_t)page_size) : slot / page_size;
+}
+
+// f over `width` neighbouring lanes, a power of two up to 32: what a step has made equal in a group
+// may come from any lane of the neighbouring group, so mirrors serve where no exchange does.
+template <class F>
+__device__ __forceinline__ float over_lanes(float x, int width, F f) {
+  const auto dpp = [&](auto ctrl) {
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(ctrl)::value, 0xf,
+                                           0xf, false));
+  };
+  if (width > 1) x = f(x, dpp(std::integral_constant<int, 0xB1>()));   // quad_perm 1 0 3 2
+  if (width > 2) x = f(x, dpp(std::integral_constant<int, 0x4E>()));   // quad_perm 2 3 0 1
+  if (width > 4) x = f(x, dpp(std::integral_constant<int, 0x141>()));  // row_half_mirror
+  if (width > 8) x = f(x, dpp(std::integral_constant<int, 0x140>()));  // row_mirror
+  if (width > 16) {
+    const auto rows = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, x),
+                                                       __builtin_bit_cast(uint32_t, x), false, false);
+    x = f(__builtin_bit_cast(float, (uint32_t)rows[0]), __builtin_bit_cast(float, (uint32_t)rows[1]));
+  }
+  return x;
+}
+__device__ __forceinline__ float lanes_sum(float x, int width) {
+  return over_lanes(x, width, [](float a, float b) { return a + b; });
+}
+
 // Eight elements of a group whose lanes are `width` wide: their codes, and the group's pair.  A
-// lane past the head's end takes part with `in` false.
+// lane past the head's end takes part with zeros and `in` false.
+//
+// A quotient is the product q = t / scale by the reciprocal instruction, two steps off at most, plus
+// its remainder times the reciprocal.  The scale has 11 bits or fewer, so the remainder t - q scale is
+// exact, the sum is off the quotient by 2^-20 of a step before it is rounded, and a quotient of 24
+// bits by 11 is nearer than 2^-12 of a step to no border of rounding: the codes are those of a
+// division, ties among them, for a third of its instructions.
 template <bool BF16>
 __device__ __forceinline__ uint32_t quantize8(const float* x, bool in, int width, uint32_t& pair) {
   using A = Act<BF16>;
-  float low = INFINITY, high = -INFINITY, bad = 0.f;
+  float low = x[0], high = x[0], bad = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    low = fminf(low, in ? x[i] : INFINITY);
-    high = fmaxf(high, in ? x[i] : -INFINITY);
-    bad += in ? x[i] * 0.f : 0.f;  // NaN for a NaN or an infinity
+    low = fminf(low, x[i]);
+    high = fmaxf(high, x[i]);
+    bad = __builtin_fmaf(x[i], 0x1p-9f, bad);  // not finite for a NaN or an infinity alone
   }
-  for (int w = 1; w < width; w *= 2) {
-    low = fminf(low, __shfl_xor(low, w));
-    high = fmaxf(high, __shfl_xor(high, w));
-    bad += __shfl_xor(bad, w);
-  }
+  low = over_lanes(in ? low : INFINITY, width, [](float a, float b) { return fminf(a, b); });
+  high = over_lanes(in ? high : -INFINITY, width, [](float a, float b) { return fmaxf(a, b); });
+  bad = lanes_sum(bad * 0.f, width);
   uint32_t sbits = A::round((high - low) / 15.f), obits = A::round(low);
   float scale = A::value((uint16_t)sbits);
   const float offset = A::value((uint16_t)obits);
@@ -97,15 +131,24 @@ __device__ __forceinline__ uint32_t quantize8(const float* x, bool in, int width
     scale = 0.f;
   }
   pair = sbits | obits << 16;
-  uint32_t codes = 0;
-  if (scale > 0.f) {
+  const float inverse = __builtin_amdgcn_rcpf(scale);
+  const bool far = scale < 0x1p-90f || scale > 0x1p120f;  // the remainder or t may leave fp32's range
+  float c[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float c = fminf(fmaxf(rintf((x[i] - offset) / scale), 0.f), 15.f);
-      codes |= (uint32_t)c << (4 * i);
-    }
+  for (int i = 0; i < 8; ++i) {
+    const float t = x[i] - offset, q = t * inverse;
+    c[i] = __builtin_fmaf(__builtin_fmaf(-q, scale, t), inverse, q);
   }
-  return codes;
+  if (__ballot(far && scale > 0.f)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = far ? (x[i] - offset) / scale : c[i];
+  }
+  float half[2] = {0.f, 0.f};  // four codes each, as a number
+#pragma unroll
+  for (int i = 7; i >= 0; --i)
+    half[i / 4] = __builtin_fmaf(half[i / 4], 16.f, rintf(__builtin_amdgcn_fmed3f(c[i], 0.f, 15.f)));
+  const uint32_t codes = (uint32_t)half[0] | (uint32_t)half[1] << 16;
+  return scale > 0.f ? codes : 0u;
 }
 
 template <bool BF16, int CACHE, bool INTERLEAVED>
@@ -114,6 +157,49 @@ __global__ __launch_bounds__(kThreads) void norm_rope_append_kernel(AppendArgs p
   __shared__ __align__(16) float rows[CACHE == kCache4 ? kWaves : 1][64 * 8];
   const int token = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lanes = 1 << p.lanes_log2, per_wave = 64 >> p.lanes_log2;
+  const int e = lane & (lanes - 1);
+  const int per_head = p.d / 8, turned = p.half / 4;  // units of eight elements; turned ones
+  const int heads = p.q_heads + 2 * p.kv_heads;
+  const int first = (blockIdx.y * kWaves + wave) * per_wave, step = gridDim.y * kWaves * per_wave;
+
+  // A lane's unit of the heads at h0: its head's kind, the element offsets of the unit's two runs of
+  // four, and what is read.  A unit's elements are in flight while the one before it is done, and the
+  // first one's while the sines are formed.
+  struct Unit {
+    int head, kvh, e0, e1;
+    bool is_q, is_v, turn;
+    u32x2 x0, x1;
+  };
+  const uint16_t* const q_row = p.q + (int64_t)token * p.ldq;
+  const uint16_t* const k_row = p.k + (int64_t)token * p.ldk;
+  const uint16_t* const v_row = p.v + (int64_t)token * p.ldv;
+  uint16_t* const q_out = p.q_out + (int64_t)token * p.ldqo;
+  const auto unit_of = [&](int h0, const uint16_t* q_row, const uint16_t* k_row, const uint16_t* v_row) {
+    Unit u;
+    u.head = h0 + (lane >> p.lanes_log2);
+    u.is_q = u.head < p.q_heads;
+    u.is_v = u.head >= p.q_heads + p.kv_heads;
+    u.kvh = u.is_v ? u.head - p.q_heads - p.kv_heads : u.head - p.q_heads;
+    u.turn = !u.is_v && e < turned;
+    u.e0 = 8 * e;
+    u.e1 = 8 * e + 4;
+    if (u.turn && !INTERLEAVED) {
+      u.e0 = 4 * e;
+      u.e1 = p.half + 4 * e;
+    }
+    u.x0 = u.x1 = u32x2{0u, 0u};
+    if (u.head < heads && e < per_head) {
+      const uint16_t* src = (u.is_v ? v_row : u.is_q ? q_row : k_row) +
+                            __mul24(u.is_q ? u.head : u.kvh, p.d);
+      u.x0 = *reinterpret_cast<const u32x2*>(src + u.e0);
+      u.x1 = *reinterpret_cast<const u32x2*>(src + u.e1);
+    }
+    return u;
+  };
+  Unit next = unit_of(first, q_row, k_row, v_row);
+  const int64_t slot = p.slots[token];
+
   if (tid < p.half) {
     int axis = 0;
     while (axis + 1 < p.axes && tid >= p.end[axis]) ++axis;
@@ -122,54 +208,35 @@ __global__ __launch_bounds__(kThreads) void norm_rope_append_kernel(AppendArgs p
     const double turns = angle * 0.15915494309189533577;  // 1 / (2 pi)
     sincospif(2.f * (float)(turns - rint(turns)), &sn[tid], &cs[tid]);
   }
-  const int64_t slot = p.slots[token];
   const bool real = slot >= 0 && slot < p.total_slots;
-  const int64_t page = real ? slot / p.page_size : 0;
+  const int64_t page = real ? page_of(slot, p.page_size, p.total_slots) : 0;
   const int64_t in_page = real ? slot - page * p.page_size : 0;
   const int64_t cache_at = page * p.page_stride + in_page * p.slot_stride;
   const int64_t pair_at = page * p.pair_page + in_page * p.pair_slot;
   __syncthreads();
 
-  const int lanes = 1 << p.lanes_log2, per_wave = 64 >> p.lanes_log2;
-  const int e = lane & (lanes - 1);
-  const int per_head = p.d / 8, turned = p.half / 4;  // units of eight elements; turned ones
-  const int heads = p.q_heads + 2 * p.kv_heads;
-  const int first = (blockIdx.y * kWaves + wave) * per_wave, step = gridDim.y * kWaves * per_wave;
   for (int h0 = first; h0 < heads; h0 += step) {
-    const int head = h0 + (lane >> p.lanes_log2);
-    const bool is_q = head < p.q_heads, is_v = head >= p.q_heads + p.kv_heads;
+    const Unit u = next;
+    if (h0 + step < heads) next = unit_of(h0 + step, q_row, k_row, v_row);
+    const int head = u.head, kvh = u.kvh, e0 = u.e0, e1 = u.e1;
+    const bool is_q = u.is_q, is_v = u.is_v, turn = u.turn;
     const bool in = head < heads && e < per_head && (is_q || real);
-    const int kvh = is_v ? head - p.q_heads - p.kv_heads : head - p.q_heads;
-    // element offsets of the unit's two runs of four
-    const bool turn = !is_v && e < turned;
-    int e0 = 8 * e, e1 = 8 * e + 4;
-    if (turn && !INTERLEAVED) {
-      e0 = 4 * e;
-      e1 = p.half + 4 * e;
-    }
-    float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
     const uint16_t* weight = is_q ? p.q_norm : is_v ? nullptr : p.k_norm;
     u32x2 w0 = {0u, 0u}, w1 = {0u, 0u};
-    if (in) {
-      const uint16_t* src = is_v   ? p.v + (int64_t)token * p.ldv + (int64_t)kvh * p.d
-                            : is_q ? p.q + (int64_t)token * p.ldq + (int64_t)head * p.d
-                                   : p.k + (int64_t)token * p.ldk + (int64_t)kvh * p.d;
-      const u32x2 x0 = *reinterpret_cast<const u32x2*>(src + e0);
-      const u32x2 x1 = *reinterpret_cast<const u32x2*>(src + e1);
-      if (weight != nullptr) {
-        w0 = *reinterpret_cast<const u32x2*>(weight + e0);
-        w1 = *reinterpret_cast<const u32x2*>(weight + e1);
-      }
-      unpack4<BF16>(x0, a);
-      unpack4<BF16>(x1, b);
+    if (in && weight != nullptr) {
+      w0 = *reinterpret_cast<const u32x2*>(weight + e0);
+      w1 = *reinterpret_cast<const u32x2*>(weight + e1);
     }
+    float a[4], b[4];
+    unpack4<BF16>(u.x0, a);
+    unpack4<BF16>(u.x1, b);
     if (p.q_norm != nullptr || p.k_norm != nullptr) {
       float ss = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) ss = __builtin_fmaf(a[i], a[i], __builtin_fmaf(b[i], b[i], ss));
-      for (int w = 1; w < lanes; w *= 2) ss += __shfl_xor(ss, w);
+      ss = lanes_sum(ss, lanes);
       if (weight != nullptr) {
-        const float r = 1.f / sqrtf(ss / (float)p.d + p.eps);
+        const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, p.inv_d, p.eps));
         float wa[4], wb[4];
         unpack4<BF16>(w0, wa);
         unpack4<BF16>(w1, wb);
@@ -202,7 +269,7 @@ __global__ __launch_bounds__(kThreads) void norm_rope_append_kernel(AppendArgs p
       }
     }
     if (in && is_q) {
-      uint16_t* dst = p.q_out + (int64_t)token * p.ldqo + (int64_t)head * p.d;
+      uint16_t* dst = q_out + __mul24(head, p.d);
       *reinterpret_cast<u32x2*>(dst + e0) = pack4<BF16>(a);
       *reinterpret_cast<u32x2*>(dst + e1) = pack4<BF16>(b);
     }
@@ -263,7 +330,7 @@ __global__ __launch_bounds__(kThreads) void cache4_read_kernel(ReadArgs p) {
   using A = Act<BF16>;
   const int64_t token = blockIdx.x, slot = p.slots[token];
   const bool real = slot >= 0 && slot < p.total_slots;
-  const int64_t page = real ? slot / p.page_size : 0;
+  const int64_t page = real ? page_of(slot, p.page_size, p.total_slots) : 0;
   const int64_t in_page = real ? slot - page * p.page_size : 0;
   const int per_head = p.d / 8, units = p.kv_heads * per_head;
   for (int u = threadIdx.x; u < 2 * units; u += kThreads) {
@@ -330,6 +397,7 @@ hipError_t launch_norm_rope_append(const wq_norm_rope_args& a, hipStream_t strea
   p.ldqo = a.ldqo;
   p.axes = a.axes;
   p.eps = a.eps;
+  p.inv_d = 1.f / (float)p.d;
   int end = 0;
   for (int i = 0; i < a.axes; ++i) p.end[i] = end += a.sections[i];
   while (8 << p.lanes_log2 < p.d) ++p.lanes_log2;

@@ -895,7 +895,8 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
         vary = 0;
         for (int w = 0; w < kWaves; ++w) vary |= sh.wave_mass[w];
         // The place at which the count or the sums of p of the entries, those of bin k alone or all,
-        // pass a target; by the bytes in which entries differ, from the top.  `sum`: of p up to it.
+        // pass a target; by the bytes in which entries differ, from the top, until one is left.  `sum`:
+        // of p up to it.
         const auto find_place = [&](bool of_k, u64 target, u64& sum) -> u64 {
           u64 prefix = 0, above = 0;
           sum = 0;
@@ -926,11 +927,22 @@ __global__ __launch_bounds__(kPickThreads) void sample_pick(SampleArgs p) {
               sh.place = (u64)(255 - tid) << shift;
               sh.above = above + before;
               sh.total = sum + mass_before;
+              sh.above_count = (uint32_t)n_mine;
             }
             __syncthreads();
             prefix |= sh.place;
             above = sh.above;
             sum = sh.total;
+            if (sh.above_count == 1) {
+              __syncthreads();  // (the byte is read)
+              for (int i = tid; i < n; i += kThreads) {
+                const u64 x = sh.list[i];
+                if (((x ^ prefix) & (~0ull << shift)) == 0 && !(of_k && bin_of(x) != bins.k))
+                  sh.place = x;
+              }
+              __syncthreads();
+              return sh.place;
+            }
           }
           return prefix;
         };

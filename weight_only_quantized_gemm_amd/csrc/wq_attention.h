@@ -9,11 +9,6 @@
 #include "wq_ranges.h"
 
 namespace wq {
-namespace {
-
-constexpr int kWaves = 4;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 struct AttnArgs {
   const uint16_t* q;
@@ -39,6 +34,12 @@ struct AttnArgs {
   int page_shift;
   float scale, softcap;
 };
+
+namespace {
+
+constexpr int kWaves = 4;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 // Orders a wave's own LDS accesses (they execute in order; this keeps the compiler to it).
 __device__ __forceinline__ void wave_lds_fence() {

@@ -1,0 +1,10 @@
+// The 4-bit cache's attention for fp16 tensors.
+#include "wq_attention4_kernel.h"
+
+namespace wq {
+
+void launch_attn4_fp16(const Attn4Args& p, const Columns& c, dim3 grid, hipStream_t stream) {
+  launch_attn4<false>(p, c, grid, stream);
+}
+
+}  // namespace wq

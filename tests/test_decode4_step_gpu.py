@@ -15,7 +15,7 @@ wq = pytest.importorskip("weight_only_quantized_gemm_amd")
 from weight_only_quantized_gemm_amd import decode  # noqa: E402
 
 from test_decode_gpu import BF16, F16, normal, np64, rng_of  # noqa: E402
-from test_decode4_gpu import paged4  # noqa: E402
+from test_decode4_gpu import attn_case, attn_run, paged4  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -201,6 +201,34 @@ def test_pages_far_apart(dev):
         slots = torch.tensor([5, 47, 5, 20], device=dev)
         for a, b in zip(far.read(slots), near.read(slots)):
             assert torch.equal(a, b), slot_bytes
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d,group,hq,hkv", [(64, 32, 4, 4), (80, 80, 6, 3), (128, 64, 8, 2),
+                                            (128, 32, 32, 2), (256, 32, 5, 1)])
+def test_query_heads_of_infinities_and_nan(dev, dtype, d, group, hq, hkv):
+    """They give NaN, of a sequence with live positions, and leave all others as they are."""
+    for cut in (False, True):
+        c = attn_case(dev, [300, 64, 0, 1], hq, hkv, d, group, 16, dtype)
+        clean, clean_lse = attn_run(c, cut)
+        hit = torch.zeros((4, hq), dtype=torch.bool, device=dev)
+        hit[0, 1] = hit[3, 2] = True
+        for bad in (math.nan, math.inf, -math.inf):
+            q = c["q"].clone()
+            q[0, 1, 5] = q[3, 2, d - 1] = q[2, 0, 0] = bad
+            out, lse = attn_run(dict(c, q=q), cut)
+            assert bool(out[hit].isnan().all()) and bool(lse[hit].isnan().all()), (cut, bad)
+            assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
+
+
+def test_head_norms_below_normal_squares(dev):
+    """Squares among fp32's smallest numbers count: with an eps of 0 a head is of size one."""
+    k = torch.full((2, 1, 64), 2.0 ** -70, dtype=BF16, device=dev)
+    k[1] = 2.0 ** -66
+    cache = decode.PagedCache.empty(1, 16, 1, 64, BF16, dev)
+    decode.rope_append(None, k, k, cache, torch.arange(2, device=dev), k_norm=torch.ones_like(k[0, 0]),
+                       eps=0.0)
+    assert bool((cache.k[0, :2] == 1).all())
 
 
 def test_a_slot_read_twice(dev):

@@ -236,7 +236,7 @@ __global__ __launch_bounds__(kThreads) void norm_rope_append_kernel(AppendArgs p
       for (int i = 0; i < 4; ++i) ss = __builtin_fmaf(a[i], a[i], __builtin_fmaf(b[i], b[i], ss));
       ss = lanes_sum(ss, lanes);
       if (weight != nullptr) {
-        const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, p.inv_d, p.eps));
+        const float r = rsqrtf(__builtin_fmaf(ss, p.inv_d, p.eps));
         float wa[4], wb[4];
         unpack4<BF16>(w0, wa);
         unpack4<BF16>(w1, wb);

@@ -43,8 +43,11 @@ constexpr int pow2_from(int x) { return x <= 1 ? 1 : x <= 2 ? 2 : x <= 4 ? 4 : 8
 
 // How a KV head's query heads lie in columns.  Two KV heads share a set where both fit (`pairs`): a
 // column then works on half of the rows, a position's rows of two heads, which may share lines, are
-// read together, and positions are cut more finely.  Two sets where one does not hold the heads of
-// one (they share the conversions, the reads and the addresses), as far as the registers go.
+// read together, and positions are cut more finely (131072 positions of 8 KV heads of 128: 40.7 us,
+// 43.2 by single heads, slots stored before heads; 36.3 and 35.3, heads before slots.  Seven windows
+// of 1000 over 12 heads of 80: 15.7 and 17.0).  Two sets where one does not hold the heads of one
+// (they share the conversions, the reads and the addresses), as far as the registers go (64
+// sequences of up to 8192, 64 heads over 8, groups of 32: 96 us, 113 by single sets).
 struct Columns {
   int kv_heads, sets;
   int heads_log2;  // query heads of a work-group, at most

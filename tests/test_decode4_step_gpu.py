@@ -15,7 +15,7 @@ wq = pytest.importorskip("weight_only_quantized_gemm_amd")
 from weight_only_quantized_gemm_amd import decode  # noqa: E402
 
 from test_decode_gpu import BF16, F16, normal, np64, rng_of  # noqa: E402
-from test_decode4_gpu import attn_case, attn_run, paged4  # noqa: E402
+from test_decode4_gpu import attn_case, attn_check, attn_run, paged4  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -219,6 +219,20 @@ def test_query_heads_of_infinities_and_nan(dev, dtype, d, group, hq, hkv):
             out, lse = attn_run(dict(c, q=q), cut)
             assert bool(out[hit].isnan().all()) and bool(lse[hit].isnan().all()), (cut, bad)
             assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d,group", [(64, 32), (80, 80), (128, 128), (128, 64), (256, 32)])
+def test_query_heads_with_a_large_element(dev, dtype, d, group):
+    """A few large elements (some just below a power of two) beside small ones, which still count."""
+    c = attn_case(dev, [300, 64, 1, 700], 6, 2, d, group, 16, dtype)
+    q = c["q"] * 0.25
+    for i, x in enumerate((40.0, 31.9, 63.75, 500.0, 128.0, 3.98)):
+        q[:, i, (7 * i) % d] = x
+        q[0, i, (11 * i + 20) % d] = -x
+    c["q"] = q
+    for cut in (False, True):
+        attn_check(c, *attn_run(c, cut), f"cut {cut}")
 
 
 def test_head_norms_below_normal_squares(dev):

@@ -202,41 +202,53 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
   };
 
   // q as the B operand: this column's head, its group's elements, as pieces below 2^8 times the power
-  // of two in q_scale; elements 0, 2, 4, 6 of a dword's eight, then the others, as K's bytes come.  A
-  // negative scale of the scores is q's sign, and one of 0 its value.
+  // of two in q_scale; elements 0, 2, 4, 6 of a dword's eight, then the others, as K's bytes come.
+  // The products of an 8-bit MFMA lose what lies more than ten bits below the largest operand's
+  // exponent (measured: beside 128 a piece of 2^-4 counts for nothing), so a piece is a multiple of
+  // 2^-3, whose products are whole, and what it leaves is the next one's, four bits down.  Two pieces
+  // hold q to 2^-8 beside 2^7, and what they leave meets the mean code, 7.5, in mean_left, where the
+  // products begin: without it the scores' sums are off by 1e-5, in place of 1e-6 and less.  fp16's third
+  // holds q to 2^-12.  (64 sequences of 64 heads of up to 8192, groups of 32: 97 us without mean_left, 103
+  // with it, 106 with a third piece for bf16 in its place.)  A negative scale of the scores is q's sign,
+  // and one of 0 its value.
   uint32_t pattern;
   asm volatile("v_mov_b32 %0, 0x41804180" : "=v"(pattern));
   const float sign = p.scale > 0.f ? 1.f : p.scale < 0.f ? -1.f : 0.f;
   const float sc = p.scale == 0.f ? 1.f : fabsf(p.scale);
   i32x8 qp[NC][NP][NM];
   int q_scale[NC];
-  float q_sum[NC];
+  float q_sum[NC], mean_left[NC] = {};
+  const auto element = [](u32x4 w, int t) { return A::value((uint16_t)(w[t / 2] >> (16 * (t % 2)))); };
   const auto load_q = [&](int b) {
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
       const int head = n * HS + my_head;
       const uint16_t* src = p.q + (int64_t)b * p.ldq + (int64_t)(h0 + (head < rows ? head : 0)) * p.d;
-      float x[W][8], most = 0.f, sum = 0.f;
+      u32x4 raw[W];
+      float most = 0.f, sum = 0.f;
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         const int first = w / kPiece * kPiece;
         const int dw = piece_at(first) + w - first;
-        u32x4 raw = {0u, 0u, 0u, 0u};
+        raw[w] = u32x4{0u, 0u, 0u, 0u};
         if ((FULL || dw >= place_of_piece(first)) && head < rows && 8 * dw / p.group_size == my_group)
-          raw = *reinterpret_cast<const u32x4*>(src + 8 * dw);
+          raw[w] = *reinterpret_cast<const u32x4*>(src + 8 * dw);
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
-          x[w][t] = sign * A::value((uint16_t)(raw[t / 2] >> (16 * (t % 2))));
-          sum += x[w][t];
-          most = fmaxf(most, fabsf(x[w][t]));
+          const float x = element(raw[w], t);
+          sum += x;
+          most = fmaxf(most, fabsf(x));
         }
       }
-      q_sum[n] = column_sum(sum);
-      // the largest element's exponent, seven below which is the pieces' (within what scales hold)
-      const int top = (int)(__builtin_bit_cast(uint32_t, column_max(most)) >> 23) - 127 - 7;
+      q_sum[n] = sign * column_sum(sum);
+      // the largest element's exponent, seven below which is the pieces' (within what scales hold);
+      // one more where its first piece would round up to 2^8
+      const float largest = column_max(most) * (256.f / 248.f);
+      const int top = (int)(__builtin_bit_cast(uint32_t, largest) >> 23) - 127 - 7;
       const int e = min(max(top, -110), 120);
       q_scale[n] = 127 + e;
-      const float down = __builtin_ldexpf(1.f, -e);
+      const float down = __builtin_ldexpf(sign, -e);
+      float left = 0.f;
 #pragma unroll
       for (int m = 0; m < NM; ++m)
 #pragma unroll
@@ -244,11 +256,14 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
           const int w = (8 * m + r) / 2, odd = r % 2;  // elements odd, odd + 2, ... of dword w
           float y[4];
 #pragma unroll
-          for (int t = 0; t < 4; ++t) y[t] = w < W ? x[w < W ? w : 0][2 * t + odd] * down : 0.f;
+          for (int t = 0; t < 4; ++t) y[t] = w < W ? element(raw[w < W ? w : 0], 2 * t + odd) * down : 0.f;
 #pragma unroll
           for (int piece = 0; piece < NP; ++piece) {
-            int bytes = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
-            bytes = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], bytes, true);
+            float whole[4];  // of 2^-3
+#pragma unroll
+            for (int t = 0; t < 4; ++t) whole[t] = (y[t] + 0x1.8p20f) - 0x1.8p20f;
+            int bytes = __builtin_amdgcn_cvt_pk_fp8_f32(whole[0], whole[1], 0, false);
+            bytes = __builtin_amdgcn_cvt_pk_fp8_f32(whole[2], whole[3], bytes, true);
             qp[n][piece][m][r] = bytes;
             const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(bytes, false);
             const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(bytes, true);
@@ -257,7 +272,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
             y[2] = (y[2] - hi[0]) * 16.f;
             y[3] = (y[3] - hi[1]) * 16.f;
           }
+          left += (y[0] + y[1]) + (y[2] + y[3]);
         }
+      if constexpr (BF16) mean_left[n] = column_sum(left) * __builtin_ldexpf(7.5f, e - 4 * NP);
     }
   };
 
@@ -411,7 +428,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
 #pragma unroll
       for (int blk = 0; blk < NT; ++blk) {
 #pragma unroll
-        for (int n = 0; n < NC; ++n) all[n][blk] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int n = 0; n < NC; ++n) {
+          const float x = BF16 ? mean_left[n] : 0.f;
+          all[n][blk] = f32x4{x, x, x, x};
+        }
 #pragma unroll
         for (int j = 0; j < NM; ++j) {
           i32x8 c;

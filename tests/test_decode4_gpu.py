@@ -291,7 +291,7 @@ def attn_run(c, cut=False, **kw):
     return plan(c["q"], c["table"], c["lens"], keep=c["keep"], lse=True, **kw)
 
 
-# q is cut into two E4M3 pieces (fp16: three) below 2^8 times a power of two, multiples of 2^-3 and 2^-7
+# q is cut into two E4M3 pieces at least (fp16: three) below 2^8 times a power of two, multiples of 2^-3 and 2^-7
 # (and 2^-11) that meet K's codes without loss; what they leave is half of the last at most, beside a
 # largest element of 124 at least (half of 248, past which a piece would round up to 2^8): 2^-8 / 124 <
 # 2^-14.95 (2^-12 / 124 < 2^-18.95).

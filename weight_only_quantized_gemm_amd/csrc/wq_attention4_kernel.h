@@ -16,13 +16,17 @@
 //
 // K's codes become bytes (two instructions and a half for eight): 0 to 15 are, as E4M3 values, 2^-9 to
 // 15 2^-9, which an MFMA of 8-bit operands takes with a block scale of 2^9.  Its other operand is q in
-// two E4M3 pieces (fp16: three) of four bits each, below a power of two of its column.  V's codes
-// meet p, whose range no 8-bit type has: they become bf16 values of 16 + c, an instruction and a shift
+// two or three E4M3 pieces of four bits each, below a power of two of its column.  V's codes meet p, whose range no 8-bit type has: they become bf16 values of 16 + c, an instruction and a shift
 // for two, and the offsets o - 16 s take the 16 off again; p s is cut into two bf16 parts, which keep
 // 16 bits.
 //
 // V's codes need the positions along the register: the transposing read of 4-bit elements gives a
 // lane 16 positions of one element, which serve two products.
+//
+// Long sequences of one set of columns are bound by memory (131072 positions of 8 KV heads of 128, groups
+// of 64: 33 us in the kernel, 4.6 TB/s, slots before heads; 5.2 heads before slots), two sets by
+// instructions, some 750 vector ones and 80 MFMAs a tile (64 sequences of up to 8192, 64 heads, groups of
+// 32: 103 us, 2.3 TB/s), short ones by latency (128 positions: 7.1 us).
 #pragma once
 
 #include <type_traits>
@@ -138,7 +142,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
   constexpr int NL = NT / NK;          // blocks that a column looks at
   constexpr int NB = DP / 16;          // 16-element blocks of the output
   constexpr int NM = (2 * W + 7) / 8;  // 128-element steps of K
-  constexpr int NP = BF16 ? 2 : 3;     // pieces of q
+  constexpr int NP = BF16 && (NC == 2 || W > 4) ? 2 : 3;  // pieces of q
   constexpr int HS = 16 / GP;          // query heads of a set
   constexpr int HB = NC * HS;          // and of a work-group
   constexpr int SD = W % 2 == 0 ? 4 * W + 4 : 4 * W + 8;  // dwords of an LDS row of V: 4 mod 8
@@ -205,12 +209,13 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
   // of two in q_scale; elements 0, 2, 4, 6 of a dword's eight, then the others, as K's bytes come.
   // The products of an 8-bit MFMA lose what lies more than ten bits below the largest operand's
   // exponent (measured: beside 128 a piece of 2^-4 counts for nothing), so a piece is a multiple of
-  // 2^-3, whose products are whole, and what it leaves is the next one's, four bits down.  Two pieces
-  // hold q to 2^-8 beside 2^7, and what they leave meets the mean code, 7.5, in mean_left, where the
-  // products begin: without it the scores' sums are off by 1e-5, in place of 1e-6 and less.  fp16's third
-  // holds q to 2^-12.  (64 sequences of 64 heads of up to 8192, groups of 32: 97 us without mean_left, 103
-  // with it, 106 with a third piece for bf16 in its place.)  A negative scale of the scores is q's sign,
-  // and one of 0 its value.
+  // 2^-3, whose products are whole, and what it leaves is the next one's, four bits down.  Three pieces
+  // hold q to 2^-12 beside 2^7.  bf16, whose bits there are 2^-1 wide, has two where registers are
+  // short: they hold it to 2^-8, and what they leave meets the mean code, 7.5, in mean_left, where the
+  // products begin; without it the scores' sums were off by 1e-5, in place of 1e-6 and less.  (64
+  // sequences of 64 heads of up to 8192, groups of 32: 97 us without mean_left, 103 with it, 106 with a
+  // third piece; 16 of 32 heads of up to 4096 22.5, 23.1, 23.4.)  A negative scale of the scores is q's
+  // sign, and one of 0 its value.
   uint32_t pattern;
   asm volatile("v_mov_b32 %0, 0x41804180" : "=v"(pattern));
   const float sign = p.scale > 0.f ? 1.f : p.scale < 0.f ? -1.f : 0.f;
@@ -274,7 +279,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
           }
           left += (y[0] + y[1]) + (y[2] + y[3]);
         }
-      if constexpr (BF16) mean_left[n] = column_sum(left) * __builtin_ldexpf(7.5f, e - 4 * NP);
+      if constexpr (NP == 2) mean_left[n] = column_sum(left) * __builtin_ldexpf(7.5f, e - 4 * NP);
     }
   };
 
@@ -429,7 +434,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
       for (int blk = 0; blk < NT; ++blk) {
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
-          const float x = BF16 ? mean_left[n] : 0.f;
+          const float x = NP == 2 ? mean_left[n] : 0.f;
           all[n][blk] = f32x4{x, x, x, x};
         }
 #pragma unroll

@@ -67,8 +67,7 @@ hipError_t launch_paged_attention4(const wq_attn4_args& a, const AttnPlan& plan,
       (plan.units > 1 && (shares(c.kv_heads * p.head_stride / 2, p.slot_stride / 2) ||
                           shares(c.kv_heads * p.pair_head * 4, p.pair_slot * 4)));
   const dim3 grid = attn_grid(p);
-  (bf16 ? launch_attn4_bf16 : launch_attn4_fp16)(p, c, grid, stream);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = (bf16 ? launch_attn4_bf16 : launch_attn4_fp16)(p, c, grid, stream);
   if (e != hipSuccess || plan.ranges == 0) return e;
   return launch_attn_join(p, bf16, stream);
 }

@@ -3,8 +3,8 @@
 
 namespace wq {
 
-void launch_attn4_fp16(const Attn4Args& p, const Columns& c, dim3 grid, hipStream_t stream) {
-  launch_attn4<false>(p, c, grid, stream);
+hipError_t launch_attn4_fp16(const Attn4Args& p, const Columns& c, dim3 grid, hipStream_t stream) {
+  return launch_attn4<false>(p, c, grid, stream);
 }
 
 }  // namespace wq

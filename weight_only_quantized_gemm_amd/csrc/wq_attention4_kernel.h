@@ -49,7 +49,8 @@ constexpr int pow2_from(int x) { return x <= 1 ? 1 : x <= 2 ? 2 : x <= 4 ? 4 : 8
 // column then works on half of the rows, a position's rows of two heads, which may share lines, are
 // read together, and positions are cut more finely (131072 positions of 8 KV heads of 128: 40.7 us,
 // 43.2 by single heads, slots stored before heads; 36.3 and 35.3, heads before slots.  Seven windows
-// of 1000 over 12 heads of 80: 15.7 and 17.0).  Two sets where one does not hold the heads of one
+// of 1000 over 12 heads of 80: 15.7 and 17.0); eight groups have no such
+// instance.  Two sets where one does not hold the heads of one
 // (they share the conversions, the reads and the addresses), as far as the registers go (64
 // sequences of up to 8192, 64 heads over 8, groups of 32: 96 us, 113 by single sets).
 struct Columns {
@@ -59,7 +60,7 @@ struct Columns {
 inline Columns columns_of(int group, int kv_heads, int groups, int head_dim, bool pairs) {
   const int padded = pow2_from(groups);
   Columns c{1, 1, padded == 1 ? 4 : padded == 2 ? 3 : padded == 4 ? 2 : 1};
-  if (pairs && kv_heads > 1 && 2 * group * padded <= 16) {
+  if (pairs && kv_heads > 1 && groups < 8 && 2 * group * padded <= 16) {
     c.kv_heads = 2;
   } else if (head_dim <= 128 && group * padded > 16) {
     c.sets = 2;
@@ -68,8 +69,9 @@ inline Columns columns_of(int group, int kv_heads, int groups, int head_dim, boo
   return c;
 }
 
-void launch_attn4_fp16(const Attn4Args& p, const Columns& c, dim3 grid, hipStream_t stream);
-void launch_attn4_bf16(const Attn4Args& p, const Columns& c, dim3 grid, hipStream_t stream);
+// hipErrorNotSupported, and no launch, where there is no instance.
+hipError_t launch_attn4_fp16(const Attn4Args& p, const Columns& c, dim3 grid, hipStream_t stream);
+hipError_t launch_attn4_bf16(const Attn4Args& p, const Columns& c, dim3 grid, hipStream_t stream);
 
 namespace {
 
@@ -681,35 +683,41 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
 }
 
 template <bool BF16, int W, int G, bool FULL>
-void launch_attn4_n(const Attn4Args& p, const Columns& c, dim3 grid, hipStream_t stream) {
+hipError_t launch_attn4_n(const Attn4Args& p, const Columns& c, dim3 grid, hipStream_t stream) {
   const dim3 block(kWaves * 64);
-  if (c.kv_heads == 2) {
-    if constexpr (G < 8)  // (eight groups leave no room)
-      hipLaunchKernelGGL((attn4_kernel<BF16, W, G, 1, 2, FULL>), grid, block, 0, stream, p);
-    return;
+  if (c.kv_heads == 1 && c.sets == 1) {
+    hipLaunchKernelGGL((attn4_kernel<BF16, W, G, 1, 1, FULL>), grid, block, 0, stream, p);
+    return hipGetLastError();
   }
-  if constexpr (W <= 4) {
-    if (c.sets == 2) {
-      hipLaunchKernelGGL((attn4_kernel<BF16, W, G, 2, 1, FULL>), grid, block, 0, stream, p);
-      return;
+  if constexpr (G < 8) {
+    if (c.kv_heads == 2 && c.sets == 1) {
+      hipLaunchKernelGGL((attn4_kernel<BF16, W, G, 1, 2, FULL>), grid, block, 0, stream, p);
+      return hipGetLastError();
     }
   }
-  hipLaunchKernelGGL((attn4_kernel<BF16, W, G, 1, 1, FULL>), grid, block, 0, stream, p);
+  if constexpr (W <= 4) {
+    if (c.kv_heads == 1 && c.sets == 2) {
+      hipLaunchKernelGGL((attn4_kernel<BF16, W, G, 2, 1, FULL>), grid, block, 0, stream, p);
+      return hipGetLastError();
+    }
+  }
+  return hipErrorNotSupported;
 }
 
 // The instance for a head_dim: rounded up to 64, 96, 128, 192 and 256.  A head that is no multiple of 32
 // is one group, but for 160 and 224.
 template <bool BF16, int W>
-void launch_attn4_w(const Attn4Args& p, const Columns& c, dim3 grid, hipStream_t stream) {
+hipError_t launch_attn4_w(const Attn4Args& p, const Columns& c, dim3 grid, hipStream_t stream) {
   const int groups = p.d / p.group_size;
   if (p.d != 32 * W) {
+    if (groups == 1) return launch_attn4_n<BF16, W, 1, false>(p, c, grid, stream);
     if constexpr (W == 6) {
       if (groups == 5) return launch_attn4_n<BF16, W, 5, false>(p, c, grid, stream);
     }
     if constexpr (W == 8) {
       if (groups == 7) return launch_attn4_n<BF16, W, 7, false>(p, c, grid, stream);
     }
-    return launch_attn4_n<BF16, W, 1, false>(p, c, grid, stream);
+    return hipErrorNotSupported;
   }
   if (groups == 1) return launch_attn4_n<BF16, W, 1, true>(p, c, grid, stream);
   if constexpr (W == 2 || W == 4 || W == 8) {
@@ -718,20 +726,25 @@ void launch_attn4_w(const Attn4Args& p, const Columns& c, dim3 grid, hipStream_t
   if constexpr (W == 4 || W == 8) {
     if (groups == 4) return launch_attn4_n<BF16, W, 4, true>(p, c, grid, stream);
   }
-  if constexpr (W == 8) launch_attn4_n<BF16, W, 8, true>(p, c, grid, stream);
+  if constexpr (W == 8) {
+    if (groups == 8) return launch_attn4_n<BF16, W, 8, true>(p, c, grid, stream);
+  }
   if constexpr (W == 3 || W == 6) {
     if (groups == 3) return launch_attn4_n<BF16, W, 3, true>(p, c, grid, stream);
   }
-  if constexpr (W == 6) launch_attn4_n<BF16, W, 6, true>(p, c, grid, stream);
+  if constexpr (W == 6) {
+    if (groups == 6) return launch_attn4_n<BF16, W, 6, true>(p, c, grid, stream);
+  }
+  return hipErrorNotSupported;
 }
 
 template <bool BF16>
-void launch_attn4(const Attn4Args& p, const Columns& c, dim3 grid, hipStream_t stream) {
+hipError_t launch_attn4(const Attn4Args& p, const Columns& c, dim3 grid, hipStream_t stream) {
   if (p.d <= 64) return launch_attn4_w<BF16, 2>(p, c, grid, stream);
   if (p.d <= 96) return launch_attn4_w<BF16, 3>(p, c, grid, stream);
   if (p.d <= 128) return launch_attn4_w<BF16, 4>(p, c, grid, stream);
   if (p.d <= 192) return launch_attn4_w<BF16, 6>(p, c, grid, stream);
-  launch_attn4_w<BF16, 8>(p, c, grid, stream);
+  return launch_attn4_w<BF16, 8>(p, c, grid, stream);
 }
 
 }  // namespace

@@ -198,7 +198,7 @@ def sample(z, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
         slack += upto[high - 1] - upto[low - 1]  # tokens that may stay or not
         keep = keep[:count]
     if min_p > 0:
-        keep = keep[(p[keep] >= min_p) | (z[keep] == z.max())]
+        keep = keep[(p[keep] >= min_p) | (np.arange(len(keep)) == 0)]  # the first in any case
     keep = np.sort(keep[p[keep] > 0])
     upto = np.cumsum(p[keep])
     want = min(max(u, 0.0), 1 - 2.0 ** -53) * upto[-1]

@@ -157,7 +157,7 @@ struct Setting {
     k = __builtin_amdgcn_readfirstlane(k);
     share = scalar(share);
     min_p = scalar(min_p);
-    greedy = !(t > 0.f);
+    greedy = !(t > 0.f) || min_p > 1.f;  // (no p is above 1: the first token alone is left)
     cut_k = k > 0 && k < p.vocab;
     cut_p = share < 1.f;
     top_p = share > 0.f ? share : 0.;

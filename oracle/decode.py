@@ -137,13 +137,82 @@ def values4(codes, pairs):
         return (pairs[..., 1:] + pairs[..., :1] * c).reshape(*codes.shape[:-1], -1)
 
 
-def terms4(codes, pairs):
-    """The sizes of the terms of values4's elements as the attention adds them: the code is taken
-    16 larger, and 16 scales off again."""
+def terms4(codes, pairs, shift=16):
+    """The sizes of the terms of values4's elements as the attention adds them: V's code is taken
+    16 larger, and 16 scales off again; K's as it is, with a shift of 0."""
     c = unpack4(codes).astype(np.float64)
     c = c.reshape(*c.shape[:-1], pairs.shape[-2], -1)
     p = np.abs(pairs)
-    return (p[..., 1:] + p[..., :1] * (c + 32)).reshape(*codes.shape[:-1], -1)
+    return (p[..., 1:] + p[..., :1] * (c + 2 * shift)).reshape(*codes.shape[:-1], -1)
+
+
+def e4m3(x):
+    """The nearest numbers with four significant bits, ties to even, of multiples of 2^-9 up to 448."""
+    step = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(x), 2.0 ** -6))) - 3)
+    return np.rint(x / step) * step
+
+
+def held4(q, pieces):
+    """What the 4-bit attention's products take of the elements q [...][n] of a query head's group, in
+    so many pieces of four bits, and the sum of what the pieces leave [...]."""
+    top = np.abs(q).max(axis=-1, keepdims=True) * (256 / 248)
+    unit = 2.0 ** np.maximum(np.floor(np.log2(np.maximum(top, 2.0 ** -140))) - 7, -110)
+    held, left = np.zeros_like(q), q / unit
+    for i in range(pieces):
+        piece = e4m3(np.rint(left * 8) / 8)
+        held, left = held + piece * 16.0 ** -i, (left - piece) * 16
+    return held * unit, (left * unit).sum(axis=-1) * 16.0 ** -pieces
+
+
+def paged_attention4(q, k, v, table, lens, scale, pieces, window=0, softcap=0.0, keep=None,
+                     mean_code=7.5):
+    """paged_attention over a 4-bit cache, k and v pairs of (codes, pairs): the formula's out and lse
+    for the q that the products take (held4), the bounds of fp32 arithmetic on both, and the code that
+    what the pieces leave of q meets on average (of two pieces; 0: it is lost)."""
+    (kc, kp), (vc, vp) = ((unpack4(c).astype(np.float64), p) for c, p in (k, v))
+    groups = kp.shape[-2]
+    k_size, v_size = terms4(*k, shift=0), terms4(*v)
+    values = values4(*v)
+    batch, q_heads, d = q.shape
+    pages, page_size, kv_heads = kc.shape[:3]
+    per = q_heads // kv_heads
+    out, out_err = np.zeros_like(q), np.zeros_like(q)
+    lse, lse_err = np.full((batch, q_heads), -np.inf), np.zeros((batch, q_heads))
+    for b in range(batch):
+        j = np.arange(max(0, lens[b] - window) if window else 0, lens[b])
+        if keep is not None:
+            j = j[keep[b][j] != 0]
+        page = table[b][j // page_size]
+        at = page[(page >= 0) & (page < pages)], (j % page_size)[(page >= 0) & (page < pages)]
+        n = len(at[0])
+        if n == 0:
+            continue
+        for h in range(q_heads):
+            kh = h // per
+            parts = q[b, h].reshape(groups, -1)
+            held, left = held4(parts, pieces)
+            dots = np.einsum("jge,ge->jg", kc[at][:, kh].reshape(n, groups, -1), held)
+            if pieces == 2:
+                dots = dots + left * mean_code
+            pair = kp[at][:, kh]
+            s = (pair[..., 0] * dots + pair[..., 1] * parts.sum(axis=1)).sum(axis=1) * scale
+            # The codes' products are whole; a lane adds a quarter of a head's q in turn.
+            s_err = (k_size[at][:, kh] @ np.abs(q[b, h])) * abs(scale) * (d / 4 + 12) * E32
+            s_err = s_err + np.abs(s) * 8 * E32
+            if softcap:
+                s = softcap * np.tanh(s / softcap)
+                s_err = s_err + np.minimum(np.abs(s) * 12, softcap * 8) * E32
+            s_err = s_err.max() + np.abs(s).max() * 8 * E32  # to base 2 and back
+            p = np.exp(s - s.max())
+            total = p.sum()
+            lse[b, h] = np.log(total) + s.max()
+            lse_err[b, h] = s_err + (n / 32 + 16) * E32 * (1 + abs(lse[b, h]))
+            out[b, h] = p @ values[at][:, kh] / total
+            # p is off by its score's error; p times the scale keeps 16 bits where it meets 16 + code
+            cut = (vp[at][:, kh][..., :1] * (vc[at][:, kh].reshape(n, groups, -1) + 16)).reshape(n, d)
+            out_err[b, h] = ((2 * s_err + (n + 8) * E32) * (p @ v_size[at][:, kh])
+                             + 2.0 ** -16 * (p @ np.abs(cut))) / total
+    return out, lse, out_err, lse_err
 
 
 def check_quantized4(x, err, codes, pairs, half_step, tiny):

@@ -1,0 +1,98 @@
+"""How near the 4-bit attention comes to its formula, on the GPU: against the 64-bit form for the q
+that its products take (oracle/decode.py: held4), so that only fp32 arithmetic and the output's
+rounding are left to the bounds.  These are held against the outputs' own size: a bound that would
+let a wrong output pass fails its test."""
+
+import numpy as np
+import pytest
+
+from oracle import decode as ref
+
+torch = pytest.importorskip("torch")
+wq = pytest.importorskip("weight_only_quantized_gemm_amd")
+
+from test_decode_gpu import BF16, F16, check, half_step, np64  # noqa: E402
+from test_decode4_gpu import attn_case, attn_run  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+# d, group, q heads, KV heads, order: each head size with its groups, in one and two sets of columns
+# and with two KV heads to a set
+SHAPES = [
+    (16, 16, 2, 1, "hnd"), (24, 24, 40, 2, "nhd"), (64, 32, 4, 4, "nhd"), (64, 64, 20, 1, "hnd"),
+    (64, 32, 18, 2, "hnd"), (72, 72, 6, 2, "hnd"), (80, 80, 3, 3, "nhd"), (96, 32, 10, 2, "hnd"),
+    (96, 96, 34, 2, "nhd"), (120, 120, 4, 2, "hnd"), (128, 32, 16, 2, "hnd"), (128, 32, 2, 2, "nhd"),
+    (128, 64, 8, 2, "nhd"), (128, 64, 18, 2, "hnd"), (128, 128, 40, 2, "nhd"), (136, 136, 2, 1, "hnd"),
+    (160, 32, 4, 2, "hnd"), (184, 184, 2, 1, "nhd"), (192, 32, 6, 2, "nhd"), (192, 64, 3, 3, "hnd"),
+    (192, 192, 8, 2, "nhd"), (224, 32, 5, 1, "hnd"), (256, 32, 4, 4, "hnd"), (256, 32, 6, 2, "nhd"),
+    (256, 64, 4, 4, "nhd"), (256, 128, 17, 1, "hnd"), (256, 256, 8, 2, "nhd")]
+
+
+@pytest.fixture(scope="module")
+def dev():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    return torch.device("cuda:0")
+
+
+def pieces_of(dtype, d, group, per):
+    """How many pieces q is cut into: bf16's two where registers are short, past a head of 128 and
+    where a KV head's columns, its query heads times their groups, take a second set."""
+    padded = 1 << (d // group - 1).bit_length()
+    return 2 if dtype is BF16 and (d > 128 or per * padded > 16) else 3
+
+
+def exact(c, pieces, **kw):
+    cache = c["cache"]
+    k, v = ((x.cpu().numpy(), np64(y))
+            for x, y in ((cache.k, cache.k_pairs), (cache.v, cache.v_pairs)))
+    return ref.paged_attention4(np64(c["q"]), k, v, c["table"].cpu().numpy(), c["lens"].cpu().numpy(),
+                                c["scale"], pieces, c["window"], c["softcap"],
+                                None if c["keep"] is None else c["keep"].cpu().numpy(), **kw)
+
+
+def near(c, pieces, cuts=(False, True)):
+    want, want_lse, err, lse_err = exact(c, pieces)
+    long = (c["lens"] >= 300).cpu().numpy()
+    size, room, n = (np.linalg.norm(want[long], axis=-1), np.linalg.norm(err[long], axis=-1),
+                     c["lens"].cpu().numpy()[long][:, None])
+    assert (room <= 0.15 * size).all(), float((room / size).max())
+    for cut in cuts:
+        out, lse = attn_run(c, cut)
+        check(out, want, err, f"out, cut {cut}")
+        check(lse, want_lse, lse_err, f"lse, cut {cut}")
+        # the positions' errors have signs of their own: of n, the bound's 1 / sqrt(n), four times
+        off = np.linalg.norm((np64(out) - want)[long], axis=-1)
+        assert (off <= half_step(c["dtype"]) * size + 4 * room / np.sqrt(n)).all(), cut
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d,group,hq,hkv,order", SHAPES)
+def test_attention_comes_near_its_formula(dev, dtype, d, group, hq, hkv, order):
+    c = attn_case(dev, [0, 1, 33, 64, 129, 300, 600], hq, hkv, d, group, 16, dtype, order)
+    near(c, pieces_of(dtype, d, group, hq // hkv))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("kw", [dict(window=310), dict(softcap=5.0), dict(window=400, softcap=30.0)])
+@pytest.mark.parametrize("d,group,hq,hkv", [(64, 32, 18, 2), (128, 64, 8, 2), (256, 32, 4, 2)])
+def test_attention_of_windows_and_caps_comes_near_its_formula(dev, dtype, kw, d, group, hq, hkv):
+    c = attn_case(dev, [700, 33, 1, 320], hq, hkv, d, group, 16, dtype, **kw)
+    near(c, pieces_of(dtype, d, group, hq // hkv))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d,group,hq,hkv,order", SHAPES)
+def test_what_lies_far_below_a_groups_largest_element_counts(dev, dtype, d, group, hq, hkv, order):
+    """All elements of q but one of each group at 2^-16 of it: three pieces hold them in the last, two
+    leave them to the mean code.  Without either the log of the sum is another."""
+    c = attn_case(dev, [600, 300, 64], hq, hkv, d, group, 16, dtype, order)
+    c["q"].fill_(2.0 ** -16)
+    c["q"][:, :, group // 3::group] = 1.0
+    pieces = pieces_of(dtype, d, group, hq // hkv)
+    _, want_lse, _, lse_err = exact(c, pieces)
+    _, lost_lse, _, _ = exact(c, 2, mean_code=0.0)
+    for cut in (False, True):
+        _, lse = attn_run(c, cut)
+        check(lse, want_lse, lse_err, f"lse, cut {cut}")
+        off = np.abs(np64(lse) - lost_lse)
+        assert (off > 2 * (lse_err + np.abs(want_lse) * 2.0 ** -24)).all(), float(off.min())

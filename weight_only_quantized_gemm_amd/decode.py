@@ -285,6 +285,8 @@ class PagedCache4:
         where that divides the head, else the whole head."""
         if group is None:
             group = 64 if head_dim % 64 == 0 else head_dim
+        if head_dim % 2 or group != head_dim and (group not in (32, 64, 128) or head_dim % group):
+            raise ValueError(f"groups of {group} of a head of {head_dim}")
         shape = (num_pages, kv_heads, page_size)
         return cls(*(torch.zeros((*shape, head_dim // 2), dtype=torch.uint8,
                                  device=device).transpose(1, 2) for _ in range(2)),

@@ -8,7 +8,7 @@ import pytest
 torch = pytest.importorskip("torch")
 wq = pytest.importorskip("weight_only_quantized_gemm_amd")
 
-from test_sample_gpu import BF16, F16, F32, run, sample_check  # noqa: E402
+from test_sample_gpu import BF16, F16, F32, logits_of, run, sample_check  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +37,17 @@ def test_min_p_past_one_leaves_the_first_token(dev, dtype, vocab, cuts):
     again, shares = run(z, u, min_p=[1.0] * 8, top_k=[3] * 8)
     assert again.tolist() == [2, 2, 2, 1, 5, vocab - 1, -1, vocab - 1]
     assert math.isclose(float(shares[0]), -math.log(3), rel_tol=2.0 ** -23)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("cuts", [dict(top_k=[1, 3, 600, 50, 4990, 4999, 5, 2]), dict(top_p=[0.5, 0.9, 0.1, 0.999] * 2),
+                                  dict(top_k=[700] * 8, top_p=[0.8] * 8, min_p=[0.0, 0.1] * 4)])
+def test_cuts_at_temperatures_of_any_size(dev, dtype, cuts):
+    """Exponents from none to past every bin: those of a tiny temperature pass 32 bits, and -inf over
+    an infinite one is no number."""
+    g = np.random.default_rng(21)
+    z = logits_of(g, 8, 5000, dtype)
+    z[:, 7::9] = -math.inf
+    u = g.random(8).astype(np.float32)
+    # (of some hundreds of tokens that are all alike, a border may be where u falls)
+    sample_check(z, u, most=1, temperature=[1e-44, 1e-30, 1e-7, 1e-3, 1e4, 1e30, 3e38, math.inf], **cuts)

@@ -82,8 +82,6 @@ __device__ __forceinline__ float value_of(uint32_t key) {
   return __builtin_bit_cast(float, key >> 31 ? key & 0x7fffffffu : ~key);
 }
 
-// 2^t for t <= 0, to 3.7e-14 of its value: 1 + r q(r) for the remainder |r| <= 1/2 of t, q of degree
-// 8 through the Chebyshev points.
 // a * b + c with c in scalar registers: the compiler's own form copies a constant c to vector
 // registers each time, because it writes the sum over it.
 __device__ __forceinline__ double fma_s(double a, double b, double c) {
@@ -92,6 +90,16 @@ __device__ __forceinline__ double fma_s(double a, double b, double c) {
   return d;
 }
 
+// x without its fraction, the nearest number of 32 bits where it is none (as the instruction has it,
+// and the language does not: infinities are the last, no number and what is below 0 are 0).
+__device__ __forceinline__ uint32_t whole_of(double x) {
+  uint32_t n;
+  asm("v_cvt_u32_f64 %0, %1" : "=v"(n) : "v"(x));
+  return n;
+}
+
+// 2^t for t <= 0, to 3.7e-14 of its value: 1 + r q(r) for the remainder |r| <= 1/2 of t, q of degree
+// 8 through the Chebyshev points.
 __device__ __forceinline__ double exp2_neg(double t, int more = 0) {
   t = fmax(t, -1100.);  // (no number too, as -inf less -inf: 0)
   const double n = rint(t), r = t - n;
@@ -122,7 +130,7 @@ struct Weights {
   __device__ u64 steps(float z) const { return whole(exp2_neg(exponent(z), 44)); }
   // Never falls as z does.  Below 2^-45 there are no steps.
   __device__ static int bin(double exponent) {
-    return (int)min((uint32_t)(int)(-exponent * kBinsPerPower), (uint32_t)kBins - 1u);
+    return (int)min(whole_of(-exponent * kBinsPerPower), (uint32_t)kBins - 1u);
   }
   // A logit below which no token is in a bin before the last, and, with min_p, none stays.
   __device__ float least(float min_p) const {

@@ -125,7 +125,8 @@ def test_every_accepted_shape_of_the_4_bit_attention_has_its_kernel(recorder):
         assert grid % units == 0 and threads == 256, (c, launches)
         assert need or grid in (c["batch"] * units, -(-c["batch"] // 8) * 8 * units), (c, launches)
         if need:
-            assert f"attn_join_kernelILb{bf16}E" in launches[1], (c, launches)
+            shift = heads.bit_length() - 1
+            assert f"attn_join_kernelILb{bf16}ELi{shift}E" in launches[1], (c, launches)
             assert launches[1].split()[1:3] == [str(c["hq"]), str(c["batch"])]
         seen.add(at.group(0))
     assert len(seen) > 80  # most instances that there are

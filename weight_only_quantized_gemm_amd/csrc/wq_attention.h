@@ -26,8 +26,7 @@ struct AttnArgs {
   int num_pages, page_size, kv_heads, q_heads, d, group, head_blocks, max_len;
   int table_stride, keep_stride, ldq, ldo, window, batch;
   int units;       // work-groups of a range: KV heads times head blocks
-  int block_shift; // a work-group takes up to 2^block_shift query heads
-  int part_rows;   // query heads of a partial: 2^block_shift, or the group where it is smaller
+  int part_rows;   // query heads of a partial: a work-group's most, or the group where it is smaller
   int ranges;      // most ranges that the batch is cut into; 0: one for each sequence
   int near_units;  // the units of a range share lines: they run on the same XCD
   uint32_t page_mul;  // position / page_size = umulhi(2 * position, page_mul) >> page_shift
@@ -139,10 +138,11 @@ __device__ __forceinline__ bool find_range(const AttnArgs& p, int index, bool pu
 // Joins the parts of one query head: groups of threads, each d / 4 wide, take parts in turn
 // and are added in group order.  Sequences of one part are done; empty ones become 0.  Bound by
 // its launch and two trips to memory, the part numbers and the parts: 4.5 us for 16 sequences of
-// 32 heads.
+// 32 heads.  SHIFT: a work-group of the attention took up to 2^SHIFT query heads (as an argument
+// of the kernel it cost the seven sequences above 0.25 us of 16.85: one more load before the others).
 constexpr int kJoinThreads = 256;
 
-template <bool BF16>
+template <bool BF16, int SHIFT>
 __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs p) {
   using A = Act<BF16>;
   __shared__ f32x4 acc_lds[kJoinThreads];
@@ -155,8 +155,8 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs p) {
   const int groups = kJoinThreads / per_row;
   const int g = tid / per_row, e = 4 * (tid - g * per_row);
   const int kvh = head / p.group, in_group = head - kvh * p.group;
-  const int unit = kvh * p.head_blocks + (in_group >> p.block_shift);
-  const int64_t at = unit * p.part_rows + (in_group & ((1 << p.block_shift) - 1));
+  const int unit = kvh * p.head_blocks + (in_group >> SHIFT);
+  const int64_t at = unit * p.part_rows + (in_group & ((1 << SHIFT) - 1));
 
   // each group of threads keeps its own maximum, so that no load waits for another split
   float top = -INFINITY, sum = 0.f;
@@ -236,7 +236,6 @@ AttnArgs attn_args(const Args& a, const AttnPlan& plan, int group) {
   p.window = a.window;
   p.batch = a.batch;
   p.units = plan.units;
-  p.block_shift = plan.block_shift;
   p.part_rows = std::min(p.group, 1 << plan.block_shift);
   p.ranges = plan.ranges;
   p.scale = a.scale;
@@ -261,13 +260,14 @@ inline dim3 attn_grid(const AttnArgs& p) {
   return dim3((unsigned)(rows * p.units));
 }
 
-// The second kernel of a call whose sequences are cut.
-inline hipError_t launch_attn_join(const AttnArgs& p, bool bf16, hipStream_t stream) {
+// The second kernel of a call whose sequences are cut.  SHIFT: the plan's block_shift.
+template <int SHIFT>
+hipError_t launch_attn_join(const AttnArgs& p, bool bf16, hipStream_t stream) {
   const dim3 join((unsigned)p.q_heads, (unsigned)p.batch);
   if (bf16)
-    hipLaunchKernelGGL((attn_join_kernel<true>), join, dim3(kJoinThreads), 0, stream, p);
+    hipLaunchKernelGGL((attn_join_kernel<true, SHIFT>), join, dim3(kJoinThreads), 0, stream, p);
   else
-    hipLaunchKernelGGL((attn_join_kernel<false>), join, dim3(kJoinThreads), 0, stream, p);
+    hipLaunchKernelGGL((attn_join_kernel<false, SHIFT>), join, dim3(kJoinThreads), 0, stream, p);
   return hipGetLastError();
 }
 

@@ -45,6 +45,8 @@
 namespace wq {
 namespace {
 
+constexpr int kBlockShift = 4;  // 16 query heads to a work-group
+
 // Positions of a wave's step (dp: head_dim rounded up to 64, 128 or more).  64 rows of an E4M3
 // head of 128 keep 16 KiB requested, as 32 of a 16-bit one do (16 sequences of 4096 positions:
 // 36.4 us with 32, 34.7 with 64; one of 65536: 35.3 and 32.7).  16-bit heads of 64 are faster
@@ -483,7 +485,7 @@ int attn_groups(int batch, int head_dim, bool kv8) {
 AttnPlan attn_plan(int batch, int q_heads, int kv_heads, int head_dim, int max_len, int window,
                    bool kv8) {
   AttnPlan plan{};
-  plan.block_shift = 4;
+  plan.block_shift = kBlockShift;
   plan.head_blocks = (q_heads / kv_heads + 15) / 16;
   plan.units = kv_heads * plan.head_blocks;
   // positions a sequence may need, from the tile that holds the window's first
@@ -531,7 +533,7 @@ hipError_t launch_paged_attention(const wq_attn_args& a, const AttnPlan& plan,
     kv8 ? launch_attn<false, true>(p, grid, stream) : launch_attn<false, false>(p, grid, stream);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || plan.ranges == 0) return e;
-  return launch_attn_join(p, bf16, stream);
+  return launch_attn_join<kBlockShift>(p, bf16, stream);
 }
 
 }  // namespace wq

@@ -69,7 +69,14 @@ hipError_t launch_paged_attention4(const wq_attn4_args& a, const AttnPlan& plan,
   const dim3 grid = attn_grid(p);
   const hipError_t e = (bf16 ? launch_attn4_bf16 : launch_attn4_fp16)(p, c, grid, stream);
   if (e != hipSuccess || plan.ranges == 0) return e;
-  return launch_attn_join(p, bf16, stream);
+  switch (plan.block_shift) {
+    case 1: return launch_attn_join<1>(p, bf16, stream);
+    case 2: return launch_attn_join<2>(p, bf16, stream);
+    case 3: return launch_attn_join<3>(p, bf16, stream);
+    case 4: return launch_attn_join<4>(p, bf16, stream);
+    case 5: return launch_attn_join<5>(p, bf16, stream);
+  }
+  return hipErrorNotSupported;
 }
 
 }  // namespace wq

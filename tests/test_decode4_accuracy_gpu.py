@@ -3,6 +3,8 @@ that its products take (oracle/decode.py: held4), so that only fp32 arithmetic a
 rounding are left to the bounds.  These are held against the outputs' own size: a bound that would
 let a wrong output pass fails its test."""
 
+import math
+
 import numpy as np
 import pytest
 
@@ -55,7 +57,10 @@ def near(c, pieces, cuts=(False, True)):
     long = (c["lens"] >= 300).cpu().numpy()
     size, room, n = (np.linalg.norm(want[long], axis=-1), np.linalg.norm(err[long], axis=-1),
                      c["lens"].cpu().numpy()[long][:, None])
-    assert (room <= 0.15 * size).all(), float((room / size).max())
+    # (scores of 1 / sqrt(d) of q's and K's products; a bound grows with theirs)
+    q = np64(c["q"])
+    scores = max(1.0, abs(c["scale"]) * math.sqrt(np.square(q).mean() * q.shape[-1]))
+    assert (room <= 0.15 * scores * size).all(), float((room / size).max())
     for cut in cuts:
         out, lse = attn_run(c, cut)
         check(out, want, err, f"out, cut {cut}")
@@ -96,3 +101,32 @@ def test_what_lies_far_below_a_groups_largest_element_counts(dev, dtype, d, grou
         check(lse, want_lse, lse_err, f"lse, cut {cut}")
         off = np.abs(np64(lse) - lost_lse)
         assert (off > 2 * (lse_err + np.abs(want_lse) * 2.0 ** -24)).all(), float(off.min())
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("scale,softcap", [(-0.09, 0.0), (0.0, 0.0), (-0.2, 4.0), (2.0 ** -140, 0.0), (1e-3, 0.5)])
+@pytest.mark.parametrize("d,group,hq,hkv", [(64, 32, 18, 2), (128, 64, 8, 2), (256, 32, 4, 2)])
+def test_attention_of_scales_of_any_sign(dev, dtype, scale, softcap, d, group, hq, hkv):
+    """A negative scale turns the order of the scores, one of 0 makes them alike."""
+    c = attn_case(dev, [700, 33, 1, 320], hq, hkv, d, group, 16, dtype, softcap=softcap)
+    c["scale"] = scale
+    near(c, pieces_of(dtype, d, group, hq // hkv))
+
+
+@pytest.mark.parametrize("power", [-95, -60, 60, 110])
+@pytest.mark.parametrize("d,group,hq,hkv", [(64, 32, 18, 2), (128, 64, 8, 2), (256, 32, 4, 2)])
+def test_attention_of_queries_of_any_size(dev, power, d, group, hq, hkv):
+    """Queries far from 1, which the scale takes back."""
+    c = attn_case(dev, [700, 33, 1, 320], hq, hkv, d, group, 16, BF16)
+    c["q"] *= 2.0 ** power
+    c["scale"] *= 2.0 ** -power
+    near(c, pieces_of(BF16, d, group, hq // hkv))
+
+
+@pytest.mark.parametrize("power", [-100, 100, 112])
+@pytest.mark.parametrize("d,group,hq,hkv", [(64, 32, 18, 2), (128, 64, 8, 2), (256, 32, 4, 2)])
+def test_attention_of_values_of_any_size(dev, power, d, group, hq, hkv):
+    """V's pairs far from 1: scales of up to 2^111.4, 31 of which 700 positions add up below 2^126."""
+    c = attn_case(dev, [700, 33, 1, 320], hq, hkv, d, group, 16, BF16, poison=False)
+    c["cache"].v_pairs.mul_(2.0 ** power)
+    near(c, pieces_of(BF16, d, group, hq // hkv))

@@ -19,17 +19,17 @@ AttnPlan attn4_plan(int batch, int q_heads, int kv_heads, int head_dim, int grou
   // Positions a sequence may need, from the tile that holds the window's first.  Short sequences stay
   // whole, by single KV heads, which makes more work-groups and leaves out the join; the longer ones
   // may be, the more work-groups they make (us of 32 heads over 8 of 128, whole and cut: one of 1000
-  // 12.9 and 11.4; 16 of up to 500 9.7 and 12.6, up to 1500 16.4 and 15.5; 32 up to 2000 20.8 and 22.7,
-  // up to 2500 24.3 and 24.2; 64 up to 2000 26.9 and 30.6, up to 4000 43.9 and 41.9; 128 up to 2000
-  // 47.7 and 46.0).
+  // 12.9 and 11.4; 16 of up to 500 10.2 and 12.8, up to 1500 17.7 and 15.9; 32 up to 2000 22.5 and 23.3,
+  // up to 2500 26.2 and 24.9; 64 up to 2000 28.7 and 31.5, up to 4000 46.6 and 43.5; 128 up to 2000
+  // 50.8 and 47.9).
   AttnPlan plan = plan_of(false);
   const long span = window > 0 && window < max_len - 64 ? window + 63 : max_len;
   const long whole = std::max(672l, 9 * std::min(256l, (long)batch * plan.units));
   if (span <= whole) return plan;
   plan = plan_of(true);
-  // Two work-groups a CU (us with 256, 512 and 768: 16 sequences of up to 4096 23.4, 22.7, 24.6; 64 of
-  // 64 heads of up to 8192, groups of 32, 128, 96, 113; heads of 256, 38.8 with 256 and 35.3 with
-  // 512).
+  // Two work-groups a CU (us with 256, 512 and 768: 16 sequences of up to 4096 23.9, 23.0, 25.0; 64 of
+  // 64 heads of up to 8192, groups of 32, 135, 103, 123; 16 of up to 4096, heads of 256, 41.7, 39.5,
+  // 42.2).
   plan.ranges = std::max(1, 512 / plan.units);
   return plan;
 }

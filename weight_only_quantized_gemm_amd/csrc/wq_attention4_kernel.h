@@ -24,9 +24,13 @@
 // lane 16 positions of one element, which serve two products.
 //
 // Long sequences of one set of columns are bound by memory (131072 positions of 8 KV heads of 128, groups
-// of 64: 33 us in the kernel, 4.6 TB/s, slots before heads; 5.2 heads before slots), two sets by
-// instructions, some 750 vector ones and 80 MFMAs a tile (64 sequences of up to 8192, 64 heads, groups of
-// 32: 103 us, 2.3 TB/s), short ones by latency (128 positions: 7.1 us).
+// of 64, slots before heads: 33.4 us in the kernel, 4.5 TB/s; with the join 40.8, and 38.1 heads before
+// slots), two sets by instructions, some 750 vector ones and 80 MFMAs a tile (64 sequences of up to 8192,
+// 64 heads, groups of 32: 103 us, 2.3 TB/s), short ones by latency (128 positions: 7.1 us).  Heads past 128
+// and two sets are short of registers: 47 of the 106 instances keep some in scratch memory, most where the
+// head is no multiple of 32 (up to 105) and heads of 256 in eight groups (46, bf16 18); the 64 sequences'
+// instance 9 (fp16 23).  16 sequences of up to 4096, 32 heads of 256 over 8: 55.6 us in groups of 32, 38.2
+// of 64 (fp16 64.4 and 42.9).
 #pragma once
 
 #include <type_traits>
@@ -47,12 +51,12 @@ constexpr int pow2_from(int x) { return x <= 1 ? 1 : x <= 2 ? 2 : x <= 4 ? 4 : 8
 
 // How a KV head's query heads lie in columns.  Two KV heads share a set where both fit (`pairs`): a
 // column then works on half of the rows, a position's rows of two heads, which may share lines, are
-// read together, and positions are cut more finely (131072 positions of 8 KV heads of 128: 40.7 us,
-// 43.2 by single heads, slots stored before heads; 36.3 and 35.3, heads before slots.  Seven windows
-// of 1000 over 12 heads of 80: 15.7 and 17.0); eight groups have no such
-// instance.  Two sets where one does not hold the heads of one
-// (they share the conversions, the reads and the addresses), as far as the registers go (64
-// sequences of up to 8192, 64 heads over 8, groups of 32: 96 us, 113 by single sets).
+// read together, and positions are cut more finely (131072 positions of 8 KV heads of 128: 40.8 us,
+// 43.7 by single heads, slots stored before heads; 38.1 either way, heads before slots.  Seven windows
+// of 1000 over 12 heads of 80: 15.6 and 17.1).  Eight groups have no such instance.  Two sets where one
+// does not hold the heads of one (they share the conversions, the reads and the addresses), as far as
+// the registers go (64 sequences of up to 8192, 64 heads over 8, groups of 32: 103 us, 118 by single
+// sets).
 struct Columns {
   int kv_heads, sets;
   int heads_log2;  // query heads of a work-group, at most

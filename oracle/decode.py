@@ -154,21 +154,19 @@ def e4m3(x):
 
 def held4(q, pieces):
     """What the 4-bit attention's products take of the elements q [...][n] of a query head's group, in
-    so many pieces of four bits, and the sum of what the pieces leave [...]."""
+    so many pieces of four bits."""
     top = np.abs(q).max(axis=-1, keepdims=True) * (256 / 248)
     unit = 2.0 ** np.maximum(np.floor(np.log2(np.maximum(top, 2.0 ** -140))) - 7, -110)
     held, left = np.zeros_like(q), q / unit
     for i in range(pieces):
         piece = e4m3(np.rint(left * 8) / 8)
         held, left = held + piece * 16.0 ** -i, (left - piece) * 16
-    return held * unit, (left * unit).sum(axis=-1) * 16.0 ** -pieces
+    return held * unit
 
 
-def paged_attention4(q, k, v, table, lens, scale, pieces, window=0, softcap=0.0, keep=None,
-                     mean_code=7.5):
+def paged_attention4(q, k, v, table, lens, scale, window=0, softcap=0.0, keep=None, pieces=3):
     """paged_attention over a 4-bit cache, k and v pairs of (codes, pairs): the formula's out and lse
-    for the q that the products take (held4), the bounds of fp32 arithmetic on both, and the code that
-    what the pieces leave of q meets on average (of two pieces; 0: it is lost)."""
+    for the q that the products take (held4), and the bounds of fp32 arithmetic on both."""
     (kc, kp), (vc, vp) = ((unpack4(c).astype(np.float64), p) for c, p in (k, v))
     groups = kp.shape[-2]
     k_size, v_size = terms4(*k, shift=0), terms4(*v)
@@ -190,10 +188,7 @@ def paged_attention4(q, k, v, table, lens, scale, pieces, window=0, softcap=0.0,
         for h in range(q_heads):
             kh = h // per
             parts = q[b, h].reshape(groups, -1)
-            held, left = held4(parts, pieces)
-            dots = np.einsum("jge,ge->jg", kc[at][:, kh].reshape(n, groups, -1), held)
-            if pieces == 2:
-                dots = dots + left * mean_code
+            dots = np.einsum("jge,ge->jg", kc[at][:, kh].reshape(n, groups, -1), held4(parts, pieces))
             pair = kp[at][:, kh]
             s = (pair[..., 0] * dots + pair[..., 1] * parts.sum(axis=1)).sum(axis=1) * scale
             # The codes' products are whole; a lane adds a quarter of a head's q in turn.

@@ -36,24 +36,17 @@ def dev():
     return torch.device("cuda:0")
 
 
-def pieces_of(dtype, d, group, per):
-    """How many pieces q is cut into: bf16's two where registers are short, past a head of 128 and
-    where a KV head's columns, its query heads times their groups, take a second set."""
-    padded = 1 << (d // group - 1).bit_length()
-    return 2 if dtype is BF16 and (d > 128 or per * padded > 16) else 3
-
-
-def exact(c, pieces, **kw):
+def exact(c, **kw):
     cache = c["cache"]
     k, v = ((x.cpu().numpy(), np64(y))
             for x, y in ((cache.k, cache.k_pairs), (cache.v, cache.v_pairs)))
     return ref.paged_attention4(np64(c["q"]), k, v, c["table"].cpu().numpy(), c["lens"].cpu().numpy(),
-                                c["scale"], pieces, c["window"], c["softcap"],
+                                c["scale"], c["window"], c["softcap"],
                                 None if c["keep"] is None else c["keep"].cpu().numpy(), **kw)
 
 
-def near(c, pieces, cuts=(False, True)):
-    want, want_lse, err, lse_err = exact(c, pieces)
+def near(c):
+    want, want_lse, err, lse_err = exact(c)
     long = (c["lens"] >= 300).cpu().numpy()
     size, room, n = (np.linalg.norm(want[long], axis=-1), np.linalg.norm(err[long], axis=-1),
                      c["lens"].cpu().numpy()[long][:, None])
@@ -61,7 +54,7 @@ def near(c, pieces, cuts=(False, True)):
     q = np64(c["q"])
     scores = max(1.0, abs(c["scale"]) * math.sqrt(np.square(q).mean() * q.shape[-1]))
     assert (room <= 0.15 * scores * size).all(), float((room / size).max())
-    for cut in cuts:
+    for cut in (False, True):
         out, lse = attn_run(c, cut)
         check(out, want, err, f"out, cut {cut}")
         check(lse, want_lse, lse_err, f"lse, cut {cut}")
@@ -74,7 +67,7 @@ def near(c, pieces, cuts=(False, True)):
 @pytest.mark.parametrize("d,group,hq,hkv,order", SHAPES)
 def test_attention_comes_near_its_formula(dev, dtype, d, group, hq, hkv, order):
     c = attn_case(dev, [0, 1, 33, 64, 129, 300, 600], hq, hkv, d, group, 16, dtype, order)
-    near(c, pieces_of(dtype, d, group, hq // hkv))
+    near(c)
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
@@ -82,20 +75,19 @@ def test_attention_comes_near_its_formula(dev, dtype, d, group, hq, hkv, order):
 @pytest.mark.parametrize("d,group,hq,hkv", [(64, 32, 18, 2), (128, 64, 8, 2), (256, 32, 4, 2)])
 def test_attention_of_windows_and_caps_comes_near_its_formula(dev, dtype, kw, d, group, hq, hkv):
     c = attn_case(dev, [700, 33, 1, 320], hq, hkv, d, group, 16, dtype, **kw)
-    near(c, pieces_of(dtype, d, group, hq // hkv))
+    near(c)
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("d,group,hq,hkv,order", SHAPES)
 def test_what_lies_far_below_a_groups_largest_element_counts(dev, dtype, d, group, hq, hkv, order):
-    """All elements of q but one of each group at 2^-16 of it: three pieces hold them in the last, two
-    leave them to the mean code.  Without either the log of the sum is another."""
+    """All elements of q but one of each group at 2^-16 of it: the last of three pieces holds them.  With
+    two the log of the sum is another."""
     c = attn_case(dev, [600, 300, 64], hq, hkv, d, group, 16, dtype, order)
     c["q"].fill_(2.0 ** -16)
     c["q"][:, :, group // 3::group] = 1.0
-    pieces = pieces_of(dtype, d, group, hq // hkv)
-    _, want_lse, _, lse_err = exact(c, pieces)
-    _, lost_lse, _, _ = exact(c, 2, mean_code=0.0)
+    _, want_lse, _, lse_err = exact(c)
+    _, lost_lse, _, _ = exact(c, pieces=2)
     for cut in (False, True):
         _, lse = attn_run(c, cut)
         check(lse, want_lse, lse_err, f"lse, cut {cut}")
@@ -110,7 +102,7 @@ def test_attention_of_scales_of_any_sign(dev, dtype, scale, softcap, d, group, h
     """A negative scale turns the order of the scores, one of 0 makes them alike."""
     c = attn_case(dev, [700, 33, 1, 320], hq, hkv, d, group, 16, dtype, softcap=softcap)
     c["scale"] = scale
-    near(c, pieces_of(dtype, d, group, hq // hkv))
+    near(c)
 
 
 @pytest.mark.parametrize("power", [-95, -60, 60, 110])
@@ -120,7 +112,7 @@ def test_attention_of_queries_of_any_size(dev, power, d, group, hq, hkv):
     c = attn_case(dev, [700, 33, 1, 320], hq, hkv, d, group, 16, BF16)
     c["q"] *= 2.0 ** power
     c["scale"] *= 2.0 ** -power
-    near(c, pieces_of(BF16, d, group, hq // hkv))
+    near(c)
 
 
 @pytest.mark.parametrize("power", [-100, 100, 112])
@@ -129,4 +121,28 @@ def test_attention_of_values_of_any_size(dev, power, d, group, hq, hkv):
     """V's pairs far from 1: scales of up to 2^111.4, 31 of which 700 positions add up below 2^126."""
     c = attn_case(dev, [700, 33, 1, 320], hq, hkv, d, group, 16, BF16, poison=False)
     c["cache"].v_pairs.mul_(2.0 ** power)
-    near(c, pieces_of(BF16, d, group, hq // hkv))
+    near(c)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d,group,hq,hkv,order", SHAPES)
+def test_the_log_of_one_positions_sum_is_its_score(dev, dtype, d, group, hq, hkv, order):
+    """Of a single position, to fp32's arithmetic (2-norm over all heads): a group's code part and its
+    offset's part are each rounded to 2^-24 of themselves, the former with each of three pieces, the
+    latter with its sum of q; four such steps are allowed.  Queries of two pieces miss it by far."""
+    c = attn_case(dev, [1] * 40, hq, hkv, d, group, 16, dtype, order)
+    codes, pairs = c["cache"].k.cpu().numpy(), np64(c["cache"].k_pairs)
+    at = c["table"][:, 0].cpu().numpy(), np.zeros(40, dtype=int)
+    q = np64(c["q"]).reshape(40, hq, d // group, group)
+    code, pair = (np.repeat(x[at].reshape(40, hkv, d // group, -1), hq // hkv, axis=1)
+                  for x in (ref.unpack4(codes), pairs))
+    parts = np.abs(pair[..., 0] * (code * q).sum(-1)) + np.abs(pair[..., 1] * q.sum(-1))
+    sizes = parts.sum(-1) * c["scale"]
+    _, want, _, _ = exact(c)
+    _, lost, _, _ = exact(c, pieces=2)
+    most = 4 * 2.0 ** -24 * np.linalg.norm(sizes)
+    for cut in (False, True):
+        _, lse = attn_run(c, cut)
+        assert np.linalg.norm(np64(lse) - want) <= most, cut
+    if dtype is F16:
+        assert np.linalg.norm(np64(lse) - lost) > most

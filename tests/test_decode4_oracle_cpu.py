@@ -21,17 +21,16 @@ def test_reference_pieces_hold_a_query(pieces):
     2^-8; fp16's eleven are three pieces', which leave 2^-12.  Whole numbers below 2^7 are held."""
     g = np.random.default_rng(pieces)
     q = g.normal(size=(50, 64)) * 2.0 ** g.integers(-40, 40, (50, 1))
-    held, left = ref.held4(q, pieces)
+    held = ref.held4(q, pieces)
     most = np.abs(q).max(axis=1, keepdims=True)
     assert (np.abs(held - q) <= most * 2.0 ** (7 - 4 * pieces) / 124).all()
     bits = 8 if pieces == 2 else 11
     step = 2.0 ** (np.floor(np.log2(np.abs(q))) - bits + 1)
     typed = np.rint(q / step) * step
     top = np.abs(typed).max(axis=1, keepdims=True)
-    assert (np.abs(ref.held4(typed, pieces)[0] - typed) <= top * 2.0 ** (-4 * pieces) / 124).all()
-    assert np.allclose((q - held).sum(axis=1), left, rtol=1e-6, atol=1e-9 * most[:, 0])
+    assert (np.abs(ref.held4(typed, pieces) - typed) <= top * 2.0 ** (-4 * pieces) / 124).all()
     whole = np.arange(-127.0, 128.0)[None]
-    assert np.array_equal(ref.held4(whole, 3)[0], whole) and ref.held4(whole * 0, 2)[1] == 0
+    assert np.array_equal(ref.held4(whole, 3), whole) and not ref.held4(whole * 0, 2).any()
 
 
 def cache(g, pages, page, heads, d, group):
@@ -52,10 +51,10 @@ def test_reference_attention_of_codes(kw):
     lens = [448, 300, 0]
     kw = dict(kw, keep=g.integers(0, 4, (3, 448)) if kw.get("keep") else None)
     want, lse, _, _ = ref.paged_attention(q, ref.values4(*k), ref.values4(*v), table, lens, 0.125, **kw)
-    same, same_lse, err, lse_err = ref.paged_attention4(q, k, v, table, lens, 0.125, 9, **kw)
+    same, same_lse, err, lse_err = ref.paged_attention4(q, k, v, table, lens, 0.125, pieces=9, **kw)
     assert np.allclose(same, want, atol=1e-9) and np.allclose(same_lse[:2], lse[:2], atol=1e-9)
     assert (same_lse[2] == -np.inf).all() and (same[2] == 0).all()
-    two, _, _, _ = ref.paged_attention4(q, k, v, table, lens, 0.125, 2, **kw)
+    two, _, _, _ = ref.paged_attention4(q, k, v, table, lens, 0.125, pieces=2, **kw)
     # an element of q off by 2^-1 / 124 of the largest, 64 of them with codes within 7.5 of their mean
     # and scales of 0.4, shifts a score by so much at most, and p by e to it
     shift = np.abs(q).max() / 248 * 64 * 7.5 * 0.4 * 0.125
@@ -65,7 +64,7 @@ def test_reference_attention_of_codes(kw):
     assert (err <= (2 * lse_err.max() + 1e-3) * 40).all()
     wrong = [np.zeros_like(want)]
     for codes, pairs in ((v[0], v[1][..., ::-1, :]), (v[0] >> 4 | v[0] << 4, v[1])):
-        wrong.append(ref.paged_attention4(q, k, (codes, pairs), table, lens, 0.125, 2, **kw)[0])
+        wrong.append(ref.paged_attention4(q, k, (codes, pairs), table, lens, 0.125, pieces=2, **kw)[0])
     for x in wrong:
         passed = np.abs(x - want)[:2] <= err[:2] + np.abs(want[:2]) * 2.0 ** -8
         assert passed.mean() < 0.2

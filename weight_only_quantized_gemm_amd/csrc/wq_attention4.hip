@@ -28,7 +28,7 @@ AttnPlan attn4_plan(int batch, int q_heads, int kv_heads, int head_dim, int grou
   if (span <= whole) return plan;
   plan = plan_of(true);
   // Two work-groups a CU (us with 256, 512 and 768: 16 sequences of up to 4096 23.9, 23.0, 25.0; 64 of
-  // 64 heads of up to 8192, groups of 32, 135, 103, 123; 16 of up to 4096, heads of 256, 41.7, 39.5,
+  // 64 heads of up to 8192, groups of 32, 135, 102, 123; 16 of up to 4096, heads of 256, 41.7, 39.5,
   // 42.2).
   plan.ranges = std::max(1, 512 / plan.units);
   return plan;

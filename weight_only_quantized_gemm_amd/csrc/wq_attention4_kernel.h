@@ -16,21 +16,20 @@
 //
 // K's codes become bytes (two instructions and a half for eight): 0 to 15 are, as E4M3 values, 2^-9 to
 // 15 2^-9, which an MFMA of 8-bit operands takes with a block scale of 2^9.  Its other operand is q in
-// two or three E4M3 pieces of four bits each, below a power of two of its column.  V's codes meet p, whose range no 8-bit type has: they become bf16 values of 16 + c, an instruction and a shift
-// for two, and the offsets o - 16 s take the 16 off again; p s is cut into two bf16 parts, which keep
-// 16 bits.
+// three E4M3 pieces of four bits each, below a power of two of its column.  V's codes meet p, whose range no
+// 8-bit type has: they become bf16 values of 16 + c, an instruction and a shift for two, and the offsets
+// o - 16 s take the 16 off again; p s is cut into two bf16 parts, which keep 16 bits.
 //
 // V's codes need the positions along the register: the transposing read of 4-bit elements gives a
 // lane 16 positions of one element, which serve two products.
 //
 // Long sequences of one set of columns are bound by memory (131072 positions of 8 KV heads of 128, groups
 // of 64, slots before heads: 33.4 us in the kernel, 4.5 TB/s; with the join 40.8, and 38.1 heads before
-// slots), two sets by instructions, some 750 vector ones and 80 MFMAs a tile (64 sequences of up to 8192,
-// 64 heads, groups of 32: 103 us, 2.3 TB/s), short ones by latency (128 positions: 7.1 us).  Heads past 128
-// and two sets are short of registers: 47 of the 106 instances keep some in scratch memory, most where the
-// head is no multiple of 32 (up to 105) and heads of 256 in eight groups (46, bf16 18); the 64 sequences'
-// instance 9 (fp16 23).  16 sequences of up to 4096, 32 heads of 256 over 8: 55.6 us in groups of 32, 38.2
-// of 64 (fp16 64.4 and 42.9).
+// slots), two sets by instructions, some 760 vector ones and 88 MFMAs a tile (64 sequences of up to 8192,
+// 64 heads, groups of 32: 103 us, 2.3 TB/s; fp16 104), short ones by latency (128 positions: 7.1 us).  Heads
+// past 128, and one group in two sets, are short of registers: 40 of the 102 instances keep some in scratch
+// memory, most where the head is no multiple of 32 (up to 105), those of 256 6 to 27.  16 sequences of up to
+// 4096, 32 heads of 256 over 8: 57.8 us in groups of 32, 38.1 of 64 (fp16 60.7 and 42.4).
 #pragma once
 
 #include <type_traits>
@@ -55,7 +54,7 @@ constexpr int pow2_from(int x) { return x <= 1 ? 1 : x <= 2 ? 2 : x <= 4 ? 4 : 8
 // 43.7 by single heads, slots stored before heads; 38.1 either way, heads before slots.  Seven windows
 // of 1000 over 12 heads of 80: 15.6 and 17.1).  Eight groups have no such instance.  Two sets where one
 // does not hold the heads of one (they share the conversions, the reads and the addresses), as far as
-// the registers go (64 sequences of up to 8192, 64 heads over 8, groups of 32: 103 us, 118 by single
+// the registers go (64 sequences of up to 8192, 64 heads over 8, groups of 32: 102 us, 118 by single
 // sets).
 struct Columns {
   int kv_heads, sets;
@@ -148,7 +147,14 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
   constexpr int NL = NT / NK;          // blocks that a column looks at
   constexpr int NB = DP / 16;          // 16-element blocks of the output
   constexpr int NM = (2 * W + 7) / 8;  // 128-element steps of K
-  constexpr int NP = BF16 && (NC == 2 || W > 4) ? 2 : 3;  // pieces of q
+  constexpr int NP = 3;                // pieces of q
+  // Pieces in registers.  Where these are short the last ones lie in LDS and are read for each tile (us
+  // with all in registers and so: 64 fp16 sequences of 64 heads of up to 8192, groups of 32, 125 and 104; 16
+  // of up to 4096, heads of 256 in groups of 32 66.6 and 63.2, bf16 in one group 42.9 and 39.5; heads of 224
+  // 87.7 and 71.5).  Not of one group in two sets (32 heads to a KV head, bf16: 38.6 and 43.2), nor of fp16
+  // heads in one (of 200 46.8 and 50.1).
+  constexpr int NR = NC == 2 && G > 1 ? 1 : W > 4 && (BF16 || G > 1) ? 2 : NP;
+  constexpr int NA = NP - NR;
   constexpr int HS = 16 / GP;          // query heads of a set
   constexpr int HB = NC * HS;          // and of a work-group
   constexpr int SD = W % 2 == 0 ? 4 * W + 4 : 4 * W + 8;  // dwords of an LDS row of V: 4 mod 8
@@ -160,6 +166,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
   __shared__ __align__(16) float pair_lds[kWaves][4][G][64];
   __shared__ int64_t off_lds[kWaves][kTile];
   __shared__ float ml_lds[kWaves][HB][2];
+  // q's last pieces: every wave writes the same, and a lane reads what it wrote.  Parts take turns,
+  // because a wave that is done with one writes the next one's while others are still at it.
+  __shared__ u32x4 last_lds[NA > 0 ? 2 : 1][NC][NM][NA > 0 ? NA : 1][2][64];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -216,21 +225,22 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
   // The products of an 8-bit MFMA lose what lies more than ten bits below the largest operand's
   // exponent (measured: beside 128 a piece of 2^-4 counts for nothing), so a piece is a multiple of
   // 2^-3, whose products are whole, and what it leaves is the next one's, four bits down.  Three pieces
-  // hold q to 2^-12 beside 2^7.  bf16, whose bits there are 2^-1 wide, has two where registers are
-  // short: they hold it to 2^-8, and what they leave meets the mean code, 7.5, in mean_left, where the
-  // products begin; without it the scores' sums were off by 1e-5, in place of 1e-6 and less.  (64
-  // sequences of 64 heads of up to 8192, groups of 32: 97 us without mean_left, 103 with it, 106 with a
-  // third piece; 16 of 32 heads of up to 4096 22.5, 23.1, 23.4.)  A negative scale of the scores is q's
-  // sign, and one of 0 its value.
+  // hold q to 2^-12 beside 2^7, two of bf16's to 2^-8, which showed in the log of the sum, by 1e-5.  (bf16
+  // heads past 128 are faster with two, and what they leave met by the mean code: 16 sequences of up to
+  // 4096, heads of 256 in groups of 32 56.9 us, 59.3 with three, of 64 39.3 and 38.6, in one group 35.3
+  // and 39.6; heads of 192 28.6 and 29.6.)  A negative scale of the scores is q's sign, and one of 0 its
+  // value.
   uint32_t pattern;
   asm volatile("v_mov_b32 %0, 0x41804180" : "=v"(pattern));
   const float sign = p.scale > 0.f ? 1.f : p.scale < 0.f ? -1.f : 0.f;
   const float sc = p.scale == 0.f ? 1.f : fabsf(p.scale);
-  i32x8 qp[NC][NP][NM];
+  i32x8 qp[NC][NR][NM];
+  int turn = 0;
   int q_scale[NC];
-  float q_sum[NC], mean_left[NC] = {};
+  float q_sum[NC];
   const auto element = [](u32x4 w, int t) { return A::value((uint16_t)(w[t / 2] >> (16 * (t % 2)))); };
   const auto load_q = [&](int b) {
+    turn ^= 1;
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
       const int head = n * HS + my_head;
@@ -259,9 +269,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
       const int e = min(max(top, -110), 120);
       q_scale[n] = 127 + e;
       const float down = __builtin_ldexpf(sign, -e);
-      float left = 0.f;
 #pragma unroll
-      for (int m = 0; m < NM; ++m)
+      for (int m = 0; m < NM; ++m) {
+        i32x8 last[NA > 0 ? NA : 1];
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
           const int w = (8 * m + r) / 2, odd = r % 2;  // elements odd, odd + 2, ... of dword w
@@ -275,7 +285,11 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
             for (int t = 0; t < 4; ++t) whole[t] = (y[t] + 0x1.8p20f) - 0x1.8p20f;
             int bytes = __builtin_amdgcn_cvt_pk_fp8_f32(whole[0], whole[1], 0, false);
             bytes = __builtin_amdgcn_cvt_pk_fp8_f32(whole[2], whole[3], bytes, true);
-            qp[n][piece][m][r] = bytes;
+            if (piece < NR) {
+              qp[n][piece < NR ? piece : 0][m][r] = bytes;
+            } else {
+              last[piece < NR ? 0 : piece - NR][r] = bytes;
+            }
             const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(bytes, false);
             const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(bytes, true);
             y[0] = (y[0] - lo[0]) * 16.f;  // exact: what a piece leaves, four bits down
@@ -283,9 +297,15 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
             y[2] = (y[2] - hi[0]) * 16.f;
             y[3] = (y[3] - hi[1]) * 16.f;
           }
-          left += (y[0] + y[1]) + (y[2] + y[3]);
         }
-      if constexpr (NP == 2) mean_left[n] = column_sum(left) * __builtin_ldexpf(7.5f, e - 4 * NP);
+#pragma unroll
+        for (int k = 0; k < NA; ++k)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            last_lds[turn][n][m][k][i][lane] =
+                u32x4{(uint32_t)last[k][4 * i], (uint32_t)last[k][4 * i + 1],
+                      (uint32_t)last[k][4 * i + 2], (uint32_t)last[k][4 * i + 3]};
+      }
     }
   };
 
@@ -431,18 +451,27 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
       load_k();
       load_v();
     }
-    if (first_part) load_q(cur.b);  // (behind the requests of the first tile)
+    if (first_part) {  // (behind the requests of the first tile)
+      load_q(cur.b);
+    }
     first_part = false;
     for (; t < cur.t1; t += kStep) {
       // the codes' products: what is not there of a row's last 128 elements meets zeros of q
+      i32x8 last[NC][NM][NA > 0 ? NA : 1];
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int j = 0; j < NM; ++j)
+#pragma unroll
+          for (int k = 0; k < NA; ++k)
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+              last[n][j][k][r] = (int)last_lds[turn][n][j][k][r / 4][lane][r % 4];
       f32x4 all[NC][NT];
 #pragma unroll
       for (int blk = 0; blk < NT; ++blk) {
 #pragma unroll
-        for (int n = 0; n < NC; ++n) {
-          const float x = NP == 2 ? mean_left[n] : 0.f;
-          all[n][blk] = f32x4{x, x, x, x};
-        }
+        for (int n = 0; n < NC; ++n) all[n][blk] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < NM; ++j) {
           i32x8 c;
@@ -456,7 +485,8 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
 #pragma unroll
             for (int piece = 0; piece < NP; ++piece)
               all[n][blk] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                  c, qp[n][piece][j], all[n][blk], 0, 0, 0, 127 + 9, 0, q_scale[n] - 4 * piece);
+                  c, piece < NR ? qp[n][piece < NR ? piece : 0][j] : last[n][j][piece < NR ? 0 : piece - NR],
+                  all[n][blk], 0, 0, 0, 127 + 9, 0, q_scale[n] - 4 * piece);
         }
       }
       f32x4 s[NC][NL];
@@ -473,13 +503,13 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
       const uint64_t now = live;
       put_pairs(now);
       // the next tile's K (positions past the range are not live and read the first slot)
-      const bool last = t + kStep >= cur.t1;
+      const bool ends = t + kStep >= cur.t1;
       wave_lds_fence();
-      live = place(last ? nxt.lo : cur.lo, last ? nxt.t1 : cur.t1);
+      live = place(ends ? nxt.lo : cur.lo, ends ? nxt.t1 : cur.t1);
       wave_lds_fence();
       const bool here = t + 2 * kStep < cur.t1;
       read_pages(here ? cur.b : nxt.b, here ? cur.t_pages : nxt.t_pages,
-                 here ? t + 2 * kStep : next_t + (last ? kStep : 0));
+                 here ? t + 2 * kStep : next_t + (ends ? kStep : 0));
       load_k();
 
       // scores: this column's group, then all of the head's
@@ -682,7 +712,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
     }
     if (!more) return;
     cur = nxt;
-    __syncthreads();  // the joined outputs are no longer read
+    __syncthreads();  // the joined outputs are no longer read, nor this part's q
   }
 }
 

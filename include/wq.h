@@ -669,11 +669,10 @@ int wq_paged_attention4_workspace_bytes(int batch, int q_heads, int kv_heads, in
 /*
  * wq_paged_attention over a 4-bit cache: k_j and v_j are offset + scale * code, which is not
  * rounded to the type.  Scores are of each query head to 2^-18.9 of its largest element (heads whose
- * largest is below 2^-103: to 2^-122).  V's terms are
- * added as scale * (16 + code) in fp32: bf16 scales whose 31 times, over a sequence's positions,
- * pass 2^128 may give no number.  A live group that reads as NaN makes the scores of its position
- * NaN (K) or its elements of the output (V); a NaN or an infinity in a query head makes its output
- * and lse NaN, unless it has no live position.
+ * largest is below 2^-103: to 2^-122).  V's terms are added as scale * (16 + code) in fp32: bf16
+ * scales whose 31 times, over a sequence's positions, pass 2^128 may give no number.  A live group
+ * that reads as NaN makes the scores of its position NaN (K) or its elements of the output (V); a NaN
+ * or an infinity in a query head makes its output and lse NaN, unless it has no live position.
  */
 int wq_paged_attention4(const wq_attn4_args* args);
 

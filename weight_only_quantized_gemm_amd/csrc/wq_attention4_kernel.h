@@ -451,9 +451,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn4_kernel(Attn4Args p) {
       load_k();
       load_v();
     }
-    if (first_part) {  // (behind the requests of the first tile)
-      load_q(cur.b);
-    }
+    if (first_part) load_q(cur.b);  // (behind the requests of the first tile)
     first_part = false;
     for (; t < cur.t1; t += kStep) {
       // the codes' products: what is not there of a row's last 128 elements meets zeros of q
